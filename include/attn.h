@@ -338,6 +338,80 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const float *
                       float *delta_ws, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
                       float scale, void *stream);
 
+/*
+ * Attention with a sliding window and sinks: attn_fwd under a causal mask whose
+ * reach is bounded.  Query row i stands at position p = i + Sk - Sq (bottom-right
+ * aligned, as attn_fwd's causal mask) and sees key j iff
+ *     j <= p  and  (j > p - window  or  j < sinks),
+ * that is the last `window` keys up to its own and the first `sinks` of the
+ * sequence.  window >= Sk is attn_fwd's causal mask.  Key tiles that no row of a
+ * query tile sees are neither read nor computed, so the work grows with
+ * Sq * (window + sinks).  The pages the other entry points cite have no
+ * counterpart; the formula is the standard one, with the mask above.
+ *
+ *   q [B,Hq,Sq,D], k, v [B,Hkv,Sk,D] bf16
+ *   o [B,Hq,Sq,D] bf16 (each fp32 result rounded to nearest even once)
+ *   lse [B,Hq,Sq] fp32
+ *   window >= 1, sinks >= 0 (else ATTN_ERR_INVALID_ARG); both may exceed Sk.
+ *   D 64 or 128 (else ATTN_ERR_UNSUPPORTED).  Sizes, alignment, other errors and
+ *   rows that see no key (O = 0, LSE = -inf) as attn_fwd.
+ *   K and V have to be finite in every 128-key tile (keys [128n, 128n + 128)) that
+ *   holds a key some row sees: a masked key has weight 0 in its tile, and 0 times
+ *   a V that is not finite is NaN.  (As in attn_fwd; the decode form has no such
+ *   condition.)
+ */
+ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+                             int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                             float scale, void *stream);
+
+/*
+ * Gradients of sum(dO * O) for attn_window_fwd: attn_bwd's formulas under its mask.
+ *   q, k, v, o, dout bf16 and lse fp32, o and lse as written by attn_window_fwd
+ *   dq [B,Hq,Sq,D], dk, dv [B,Hkv,Sk,D]   bf16 outputs, summed in fp32 (dK and dV
+ *      over the query heads of the KV head too) and rounded once; keys that no row
+ *      sees, and rows that see no key, get 0
+ *   delta_ws [B,Hq,Sq] fp32               caller-owned workspace
+ *   Same arguments and errors as attn_window_fwd; all pointers 16-byte aligned.
+ */
+ATTN_API int attn_window_bwd(const void *q, const void *k, const void *v, const void *o,
+                             const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                             float *delta_ws, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                             int window, int sinks, float scale, void *stream);
+
+/*
+ * Decode with a sliding window and sinks, in one launch: the query of sequence b
+ * stands at its last key (position seqlens[b] - 1, or Sk - 1 without seqlens), so
+ * it sees keys [max(len - window, 0), len) and [0, min(sinks, len)).  Only the
+ * 32-key blocks that hold such a key are read.  Of a block that is seen in part
+ * the other keys' K and V may be anything (NaN, unwritten).
+ *
+ *   q [B,Hq,1,D], k, v [B,Hkv,Sk,D] bf16; seqlens device int32 [B] or NULL
+ *   o [B,Hq,D] bf16 (rounded once from fp32), lse [B,Hq] fp32, 16-byte aligned
+ *   num_splits: the seen blocks are shared out evenly, ceil(blocks / num_splits)
+ *      each.  With num_splits = 1, o_part, lse_part and counters may be NULL and
+ *      are not touched; otherwise they are as attn_decode_fused (partials
+ *      [num_splits,B,Hq,D] and [num_splits,B,Hq], zeroed counters).
+ *      attn_decode_num_splits(B, Hq, Hkv, min(Sk, window + sinks), D) is a good count.
+ *   window, sinks as attn_window_fwd; D in {64, 128, 256}; other arguments and
+ *   errors as attn_decode_fused.  A sequence of length 0 gives O = 0, LSE = -inf.
+ */
+ATTN_API int attn_decode_window(const void *q, const void *k, const void *v, const int *seqlens,
+                                void *o, float *lse, float *o_part, float *lse_part, int *counters,
+                                int B, int Hq, int Hkv, int Sk, int D, int window, int sinks,
+                                int num_splits, float scale, void *stream);
+
+/*
+ * attn_decode_window over a paged cache (layout, block_table and seqlens as
+ * attn_decode_splitkv_paged).  Table entries of pages that hold no seen key are
+ * not read and may be anything (attn_pages_free sets them to -1).
+ */
+ATTN_API int attn_decode_window_paged(const void *q, const void *k_cache, const void *v_cache,
+                                      const int *block_table, const int *seqlens, void *o,
+                                      float *lse, float *o_part, float *lse_part, int *counters,
+                                      int B, int Hq, int Hkv, int num_pages, int page_size,
+                                      int max_pages, int D, int window, int sinks, int num_splits,
+                                      float scale, void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 ATTN_API const char *attn_status_string(int status);
 

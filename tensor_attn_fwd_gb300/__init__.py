@@ -19,10 +19,15 @@ Names follow the C ABI:
     attn_bwd(q, k, v, o, lse, dout, causal, scale) -> (dq, dk, dv)
     attn_rope_table(max_pos, D, base)           -> (cos, sin) table
     attn_qkv_rope(x, w, table, Hq, Hkv)         -> (q, k, v) bf16, RoPE applied
+    attn_window_fwd(q, k, v, window, sinks)     -> (o bf16, lse)   sliding window + sinks
+    attn_window_bwd(q, k, v, o, lse, dout, window, sinks) -> (dq, dk, dv) bf16
+    decode_window(q, k, v, window, sinks)       -> (o bf16, lse)   one new token
+    decode_window_paged(q, k_cache, v_cache, block_table, seqlens, window, sinks)
 Layouts: Q [B,Hq,Sq,D], K/V [B,Hkv,Sk,D] bf16; O [B,Hq,Sq,D], LSE [B,Hq,Sq] fp32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,7 +40,8 @@ __all__ = ["AttnError", "attn_fwd", "attn_fwd_bf16o", "attn_decode_splitkv", "at
            "attn_rope_table", "attn_qkv_rope", "attn_decode_num_splits",
            "attn_status_string", "attn_debug_status", "library_path", "load_library",
            "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_MISALIGNED",
-           "ATTN_ERR_CUDA", "ATTN_ERR_TIMEOUT", "ATTN_ERR_BOUNDS", "attn_wait_selftest", "attn_fwd_splitkv", "attn_fwd_num_splits"]
+           "ATTN_ERR_CUDA", "ATTN_ERR_TIMEOUT", "ATTN_ERR_BOUNDS", "attn_wait_selftest", "attn_fwd_splitkv", "attn_fwd_num_splits",
+           "attn_window_fwd", "attn_window_bwd", "decode_window", "decode_window_paged"]
 
 ATTN_OK = 0
 ATTN_ERR_INVALID_ARG = 1
@@ -75,6 +81,10 @@ _SIGNATURES = {
     "attn_decode_num_splits": ([_int, _int, _int, _int, _int, ctypes.POINTER(_int)], _int),
     "attn_qkv_rope": ([_vp] * 7 + [_int] * 8 + [_vp], _int),
     "attn_bwd": ([_vp] * 10 + [_int] * 7 + [_flt, _vp], _int),
+    "attn_window_fwd": ([_vp] * 5 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_window_bwd": ([_vp] * 10 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_decode_window": ([_vp] * 9 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_decode_window_paged": ([_vp] * 10 + [_int] * 10 + [_flt, _vp], _int),
     "attn_status_string": ([_int], ctypes.c_char_p),
     "attn_debug_status": ([_vp], _int),
     "attn_wait_selftest": ([ctypes.c_ulonglong, _vp, _vp], _int),
@@ -667,3 +677,199 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                           float(scale), _stream_handle(stream))
     _raise_if(st, "attn_bwd")
     return dq, dk, dv
+
+
+@contextlib.contextmanager
+def _call_scope(device: torch.device, stream):
+    """The device and stream of one call; yields the stream's handle.  What the call
+    allocates belongs to that stream, so freeing it cannot race with the kernels."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield torch.cuda.current_stream().cuda_stream
+    else:
+        handle = _stream_handle(stream)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+            yield handle
+
+
+def _reach(window, sinks):
+    """window and sinks as C ints; what exceeds every sequence means all keys."""
+    window, sinks = int(window), int(sinks)
+    _check(window >= 1, "window must be at least 1")
+    _check(sinks >= 0, "sinks must not be negative")
+    return min(window, 1 << 30), min(sinks, 1 << 30)
+
+
+def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int,
+                    sinks: int = 0, scale: float | None = None, o: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, stream=None):
+    """Attention under a sliding window with sinks; returns (o bf16 [B,Hq,Sq,D], lse fp32).
+
+    q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64 or 128.  Row i stands
+    at p = i + Sk - Sq and sees key j when j <= p and (j > p - window or j < sinks).
+    """
+    _check_bf16("q", q, 4)
+    _check_bf16("k", k, 4)
+    _check_bf16("v", v, 4)
+    B, Hq, Sq, D = q.shape
+    Bk, Hkv, Sk, Dk = k.shape
+    _check(Bk == B and Dk == D and tuple(v.shape) == tuple(k.shape), "q/k/v shape mismatch")
+    _check(k.device == q.device and v.device == q.device, "q/k/v must share a device")
+    window, sinks = _reach(window, sinks)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    lib = load_library()
+    with _call_scope(q.device, stream) as handle:
+        o = _out_bf16(o, (B, Hq, Sq, D), q.device, "o")
+        lse = _out(lse, (B, Hq, Sq), q.device, "lse")
+        st = lib.attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                 lse.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window, sinks,
+                                 float(scale), handle)
+    _raise_if(st, "attn_window_fwd")
+    return o, lse
+
+
+def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                    lse: torch.Tensor, dout: torch.Tensor, window: int, sinks: int = 0,
+                    scale: float | None = None, dq: torch.Tensor | None = None,
+                    dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                    delta_ws: torch.Tensor | None = None, stream=None):
+    """Gradients of sum(dout * O) for O = attn_window_fwd(q, k, v, window, sinks):
+    returns (dq, dk, dv) bf16, summed in fp32 and rounded once.
+
+    o (bf16) and lse (fp32) are attn_window_fwd's results; dout is bf16 like q.
+    """
+    for name, t in (("q", q), ("k", k), ("v", v), ("o", o), ("dout", dout)):
+        _check_bf16(name, t, 4)
+        _check(t.device == q.device, f"{name} must be on {q.device}")
+    B, Hq, Sq, D = q.shape
+    Bk, Hkv, Sk, Dk = k.shape
+    _check(Bk == B and Dk == D and tuple(v.shape) == tuple(k.shape), "q/k/v shape mismatch")
+    _check(tuple(dout.shape) == tuple(q.shape), "dout must match q")
+    _check(tuple(o.shape) == tuple(q.shape), "o must match q")
+    _check(isinstance(lse, torch.Tensor), "lse must be a torch.Tensor")
+    lse = _out(lse, (B, Hq, Sq), q.device, "lse")
+    window, sinks = _reach(window, sinks)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    lib = load_library()
+    with _call_scope(q.device, stream) as handle:
+        dq = _out_bf16(dq, (B, Hq, Sq, D), q.device, "dq")
+        dk = _out_bf16(dk, (B, Hkv, Sk, D), q.device, "dk")
+        dv = _out_bf16(dv, (B, Hkv, Sk, D), q.device, "dv")
+        delta_ws = _out(delta_ws, (B, Hq, Sq), q.device, "delta_ws")
+        st = lib.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                 lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                 dv.data_ptr(), delta_ws.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
+                                 sinks, float(scale), handle)
+    _raise_if(st, "attn_window_bwd")
+    return dq, dk, dv
+
+
+def _decode_window(what, q, k, v, table, seqlens, Sk, window, sinks, num_splits, scale, workspace,
+                   o, lse, counters, stream):
+    """The two windowed decodes: ``table`` is None for a contiguous cache."""
+    B, Hq, _, D = q.shape
+    Hkv = k.shape[1]
+    if seqlens is not None:
+        _check(isinstance(seqlens, torch.Tensor) and seqlens.is_cuda
+               and seqlens.dtype == torch.int32 and seqlens.is_contiguous()
+               and tuple(seqlens.shape) == (B,) and seqlens.device == q.device,
+               "seqlens must be a contiguous int32 CUDA tensor of shape [B] on q's device")
+    window, sinks = _reach(window, sinks)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    lib = load_library()
+    n = _int(0)
+    with _call_scope(q.device, stream) as handle:
+        if num_splits is None:
+            _raise_if(lib.attn_decode_num_splits(B, Hq, Hkv, max(1, min(Sk, window + sinks)), D,
+                                                 ctypes.byref(n)), "attn_decode_num_splits")
+            num_splits = n.value
+        ns = int(num_splits)
+        o = _out_bf16(o, (B, Hq, D), q.device, "o")
+        lse = _out(lse, (B, Hq), q.device, "lse")
+        part = lse_part = count = None
+        if ns != 1:
+            part, lse_part = (None, None) if workspace is None else workspace
+            part = _out(part, (ns, B, Hq, D), q.device, "o_part")
+            lse_part = _out(lse_part, (ns, B, Hq), q.device, "lse_part")
+            _raise_if(lib.attn_decode_fused_counters(B, Hq, Hkv, ctypes.byref(n)),
+                      "attn_decode_fused_counters")
+            if counters is None:
+                # A captured call zeroes counters of its own on every replay: graphs that
+                # run at the same time must not share the stream's array.
+                counters = (torch.zeros(n.value, dtype=torch.int32, device=q.device)
+                            if torch.cuda.is_current_stream_capturing()
+                            else _stream_counters(q.device, handle, n.value))
+            _check(isinstance(counters, torch.Tensor) and counters.is_cuda
+                   and counters.dtype == torch.int32 and counters.is_contiguous()
+                   and counters.numel() >= n.value and counters.device == q.device,
+                   f"counters must be a contiguous int32 CUDA tensor with >= {n.value} entries")
+            count = counters.data_ptr()
+        outs = (o.data_ptr(), lse.data_ptr(), part if part is None else part.data_ptr(),
+                lse_part if lse_part is None else lse_part.data_ptr(), count)
+        seq = None if seqlens is None else seqlens.data_ptr()
+        if table is None:
+            st = lib.attn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), seq, *outs, B,
+                                        Hq, Hkv, Sk, D, window, sinks, ns, float(scale), handle)
+        else:
+            st = lib.attn_decode_window_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                              table.data_ptr(), seq, *outs, B, Hq, Hkv, k.shape[0],
+                                              k.shape[2], table.shape[1], D, window, sinks, ns,
+                                              float(scale), handle)
+    _raise_if(st, what)
+    return o, lse
+
+
+def decode_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+                  seqlens: torch.Tensor | None = None, num_splits: int | None = None,
+                  scale: float | None = None, workspace=None, o=None, lse=None,
+                  counters: torch.Tensor | None = None, stream=None):
+    """Decode one token under a sliding window with sinks, in one launch; returns
+    (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
+
+    q [B,Hq,1,D], k/v [B,Hkv,Sk,D] (bf16), D 64, 128 or 256.  The query stands at
+    its sequence's last key (Sk keys, or its first seqlens[b]) and sees the last
+    ``window`` keys and the first ``sinks``.  ``num_splits=None`` picks
+    attn_decode_num_splits for the keys seen; ``workspace`` and ``counters`` as
+    attn_decode_fused (not used with one split).
+    """
+    _check_bf16("q", q, 4)
+    _check_bf16("k", k, 4)
+    _check_bf16("v", v, 4)
+    B, Hq, Sq, D = q.shape
+    _check(Sq == 1, "decode takes one query row per head (q.shape[2] == 1)")
+    Bk, Hkv, Sk, Dk = k.shape
+    _check(Bk == B and Dk == D and tuple(v.shape) == tuple(k.shape), "q/k/v shape mismatch")
+    _check(k.device == q.device and v.device == q.device, "q/k/v must share a device")
+    return _decode_window("attn_decode_window", q, k, v, None, seqlens, Sk, window, sinks,
+                          num_splits, scale, workspace, o, lse, counters, stream)
+
+
+def decode_window_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        block_table: torch.Tensor, seqlens: torch.Tensor, window: int,
+                        sinks: int = 0, num_splits: int | None = None, scale: float | None = None,
+                        workspace=None, o=None, lse=None, counters: torch.Tensor | None = None,
+                        stream=None):
+    """decode_window over a paged cache (k_cache/v_cache [num_pages,Hkv,page_size,D],
+    block_table int32 [B,max_pages], seqlens int32 [B], as decode_paged).  Entries of
+    pages that hold no seen key are not read (attn_pages_free makes them -1)."""
+    _check_bf16("q", q, 4)
+    _check_bf16("k_cache", k_cache, 4)
+    _check_bf16("v_cache", v_cache, 4)
+    B, Hq, Sq, D = q.shape
+    _check(Sq == 1, "decode takes one query row per head (q.shape[2] == 1)")
+    num_pages, Hkv, page_size, Dk = k_cache.shape
+    _check(Dk == D and tuple(v_cache.shape) == tuple(k_cache.shape), "q/cache shape mismatch")
+    _check(isinstance(block_table, torch.Tensor) and block_table.is_cuda
+           and block_table.dtype == torch.int32 and block_table.is_contiguous()
+           and block_table.device == q.device and block_table.dim() == 2
+           and block_table.shape[0] == B,
+           "block_table must be a contiguous int32 tensor [B, max_pages] on q's device")
+    _check(seqlens is not None, "a paged cache needs seqlens")
+    _check(k_cache.device == q.device and v_cache.device == q.device,
+           "q and caches must share a device")
+    return _decode_window("attn_decode_window_paged", q, k_cache, v_cache, block_table, seqlens,
+                          block_table.shape[1] * page_size, window, sinks, num_splits, scale,
+                          workspace, o, lse, counters, stream)

@@ -152,9 +152,9 @@ int attn_version(void) { return (1 << 16) | 0; }
 
 namespace {
 
-int fwd_common(const void* q, const void* k, const void* v, void* o, int o_bf16, float* lse,
-               int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
-               void* stream) {
+// The argument checks of the prefill entry points; ATTN_OK or the status to return.
+int fwd_check_args(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                   int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale) {
   if (!q || !k || !v || !o || !lse) return ATTN_ERR_INVALID_ARG;
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
   if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
@@ -169,6 +169,14 @@ int fwd_common(const void* q, const void* k, const void* v, void* o, int o_bf16,
   if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+int fwd_common(const void* q, const void* k, const void* v, void* o, int o_bf16, float* lse,
+               int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
+               void* stream) {
+  const int chk = fwd_check_args(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, causal, scale);
+  if (chk != ATTN_OK) return chk;
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
   const cudaError_t e = launch_attn_fwd(q, k, v, o, o_bf16, lse, B, Hq, Hkv, Sq, Sk, D, causal,
@@ -215,6 +223,23 @@ int attn_fwd_splitkv(const void* q, const void* k, const void* v, float* o_part,
   const cudaError_t e =
       launch_attn_fwd_splitkv(q, k, v, o_part, lse_part, B, Hq, Hkv, Sq, Sk, D, causal,
                               num_splits, scale, static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                    int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                    void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  const int chk = fwd_check_args(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, 1, scale);
+  if (chk != ATTN_OK) return chk;
+  if (D == 256) return ATTN_ERR_UNSUPPORTED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  // A window or sinks past the last key mean all keys; clamped, the kernels' sums fit int.
+  const cudaError_t e =
+      launch_attn_window_fwd(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
+                             sinks < Sk ? sinks : Sk, scale, static_cast<cudaStream_t>(stream),
+                             status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -394,6 +419,58 @@ int attn_decode_fused_paged(const void* q, const void* k_cache, const void* v_ca
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+namespace {
+
+// Sk: the cache's capacity; paged: its layout, or nullptr (contiguous, [B,Hkv,Sk,D]).
+int decode_window_common(const void* q, const void* k, const void* v, const int* seqlens,
+                         const PagedKV* paged, void* o, float* lse, float* o_part,
+                         float* lse_part, int* counters, int B, int Hq, int Hkv, int Sk, int D,
+                         int window, int sinks, int num_splits, float scale, void* stream) {
+  if (!o || !lse || window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  // One split writes the result itself: no partials, no counters.
+  if (num_splits != 1 && (!o_part || !lse_part || !counters)) return ATTN_ERR_INVALID_ARG;
+  const int chk =
+      decode_check_args(q, k, v, B, Hq, Hkv, Sk, D, num_splits, scale, paged != nullptr);
+  if (chk != ATTN_OK) return chk;
+  if (!aligned16(o_part) || !aligned16(lse_part) || !aligned16(o) || !aligned16(lse))
+    return ATTN_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(counters) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(seqlens) & 3u) != 0)
+    return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const FusedCombine out{o, lse, counters};
+  const cudaError_t e = launch_decode_window(
+      q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk, D, window < Sk ? window : Sk,
+      sinks < Sk ? sinks : Sk, num_splits, scale, static_cast<cudaStream_t>(stream), status, out);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int attn_decode_window(const void* q, const void* k, const void* v, const int* seqlens, void* o,
+                       float* lse, float* o_part, float* lse_part, int* counters, int B, int Hq,
+                       int Hkv, int Sk, int D, int window, int sinks, int num_splits, float scale,
+                       void* stream) {
+  return decode_window_common(q, k, v, seqlens, nullptr, o, lse, o_part, lse_part, counters, B,
+                              Hq, Hkv, Sk, D, window, sinks, num_splits, scale, stream);
+}
+
+int attn_decode_window_paged(const void* q, const void* k_cache, const void* v_cache,
+                             const int* block_table, const int* seqlens, void* o, float* lse,
+                             float* o_part, float* lse_part, int* counters, int B, int Hq,
+                             int Hkv, int num_pages, int page_size, int max_pages, int D,
+                             int window, int sinks, int num_splits, float scale, void* stream) {
+  PagedKV paged;
+  int capacity = 0;
+  const int pchk = paged_check_args(block_table, seqlens, Hkv, num_pages, page_size, max_pages,
+                                    D, B, &paged, &capacity);
+  if (pchk != ATTN_OK) return pchk;
+  return decode_window_common(q, k_cache, v_cache, seqlens, &paged, o, lse, o_part, lse_part,
+                              counters, B, Hq, Hkv, capacity, D, window, sinks, num_splits, scale,
+                              stream);
+}
+
 int attn_decode_splitkv_paged(const void* q, const void* k_cache, const void* v_cache,
                               const int* block_table, const int* seqlens, float* o_part,
                               float* lse_part, int B, int Hq, int Hkv, int num_pages,
@@ -410,9 +487,13 @@ int attn_decode_splitkv_paged(const void* q, const void* k_cache, const void* v_
                        num_splits, scale, stream, &paged);
 }
 
-int attn_bwd(const void* q, const void* k, const void* v, const float* o, const float* lse,
-             const void* dout, float* dq, float* dk, float* dv, float* delta_ws, int B, int Hq,
-             int Hkv, int Sq, int Sk, int D, int causal, float scale, void* stream) {
+namespace {
+
+// The argument checks of the backward entry points; ATTN_OK or the status to return.
+int bwd_check_args(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                   const void* dout, const void* dq, const void* dk, const void* dv,
+                   const float* delta_ws, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                   int causal, float scale) {
   if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !delta_ws)
     return ATTN_ERR_INVALID_ARG;
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
@@ -433,11 +514,38 @@ int attn_bwd(const void* q, const void* k, const void* v, const float* o, const 
       !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
       !aligned16(delta_ws))
     return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int attn_bwd(const void* q, const void* k, const void* v, const float* o, const float* lse,
+             const void* dout, float* dq, float* dk, float* dv, float* delta_ws, int B, int Hq,
+             int Hkv, int Sq, int Sk, int D, int causal, float scale, void* stream) {
+  const int chk = bwd_check_args(q, k, v, o, lse, dout, dq, dk, dv, delta_ws, B, Hq, Hkv, Sq, Sk,
+                                 D, causal, scale);
+  if (chk != ATTN_OK) return chk;
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
   const cudaError_t e =
       launch_attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, delta_ws, B, Hq, Hkv, Sq, Sk, D, causal,
                       scale, static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                    const void* dout, void* dq, void* dk, void* dv, float* delta_ws, int B, int Hq,
+                    int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                    void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  const int chk = bwd_check_args(q, k, v, o, lse, dout, dq, dk, dv, delta_ws, B, Hq, Hkv, Sq, Sk,
+                                 D, 1, scale);
+  if (chk != ATTN_OK) return chk;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e = launch_attn_window_bwd(
+      q, k, v, o, lse, dout, dq, dk, dv, delta_ws, B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
+      sinks < Sk ? sinks : Sk, scale, static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

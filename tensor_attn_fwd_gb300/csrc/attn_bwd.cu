@@ -44,9 +44,11 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace attn {
 namespace {
@@ -108,6 +110,9 @@ struct BwdParams {
   int* status;
   int B, Hq, Hkv, Sq, Sk, causal;
   float scale, scale_log2;
+  // Windowed kernels: the visibility of window.cuh, and bf16 gradients (out0, out1
+  // point at bf16).
+  int window, sinks;
 };
 
 // Read-only global load issued where it stands in the program.
@@ -170,19 +175,22 @@ __device__ __forceinline__ int kv_tiles_for(const BwdParams& p, int m) {
 }
 
 // ------------------------------------------------------------------ Delta
-template <int D>
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <int D, typename TO>
 __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16* __restrict__ dout,
-                                                        const float* __restrict__ o,
+                                                        const TO* __restrict__ o,
                                                         float* __restrict__ delta, int rows) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   constexpr int DPL = D / 32;
   const __nv_bfloat16* dr = dout + static_cast<size_t>(row) * D + lane * DPL;
-  const float* orow = o + static_cast<size_t>(row) * D + lane * DPL;
+  const TO* orow = o + static_cast<size_t>(row) * D + lane * DPL;
   float acc = 0.f;
 #pragma unroll
-  for (int e = 0; e < DPL; ++e) acc = fmaf(__bfloat162float(dr[e]), orow[e], acc);
+  for (int e = 0; e < DPL; ++e) acc = fmaf(__bfloat162float(dr[e]), to_f32(orow[e]), acc);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (lane == 0) delta[row] = acc;
@@ -271,8 +279,37 @@ __device__ __forceinline__ void store_acc_row(uint32_t taddr, float* dst, float 
   }
 }
 
-// ------------------------------------------------------------------ dK / dV
+// The same for a bf16 gradient (each fp32 sum rounded to nearest even once); the
+// lanes of a pair write 32 contiguous bytes each.
 template <int D>
+__device__ __forceinline__ void store_acc_row16(uint32_t taddr, __nv_bfloat16* dst, float mul,
+                                                bool valid, int c_begin, int c_end, int lane,
+                                                const void* base, size_t bytes, int* status) {
+  const int pb = lane & 1;
+  const bool partner_valid = __shfl_xor_sync(0xffffffffu, valid, 1);
+  const bool even_valid = pb ? partner_valid : valid, odd_valid = pb ? valid : partner_valid;
+  __nv_bfloat16* even_row = dst - pb * D;
+  const bool v8 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+#pragma unroll 1
+  for (int c = c_begin; c < c_end; c += 32) {
+    uint32_t w[16];
+    {
+      uint32_t a[32];
+      tmem_ld32(taddr + c, a);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(a[2 * i]) * mul, __uint_as_float(a[2 * i + 1]) * mul);
+    }
+    pair_transpose8(w, lane);
+    __nv_bfloat16* e = even_row + c + 16 * pb;
+    __nv_bfloat16* o = even_row + D + c + 16 * pb;
+    if (even_valid && store_in_bounds(e, 32, base, bytes, status)) st_global_8w(e, &w[0], v8);
+    if (odd_valid && store_in_bounds(o, 32, base, bytes, status)) st_global_8w(o, &w[8], v8);
+  }
+}
+
+// ------------------------------------------------------------------ dK / dV
+template <int D, bool WIN = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -296,8 +333,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int b = bg / p.Hkv, g = bg % p.Hkv;
   const int group = p.Hq / p.Hkv;
   const int mtiles = (p.Sq + 127) / 128;
-  const int m0 = min(first_q_tile(p, n), mtiles);
-  const int per_head = mtiles - m0;
+  int m0 = min(first_q_tile(p, n), mtiles);
+  int per_head = mtiles - m0;
+  if constexpr (WIN) {
+    const QTileRange qr = window_q_tiles(p.Sq, p.Sk, p.window, p.sinks, n);
+    m0 = qr.m0;
+    per_head = max(qr.m1 - qr.m0, 0);
+  }
   const int nsteps = group * per_head;
 
   if (threadIdx.x == 0) {
@@ -448,9 +490,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (s + 1 < nsteps) fetch(s + 1);
       // Visible columns (query rows 128m + col) of this key: [c_lo, c_hi) --
       // row >= key - (Sk - Sq) under the causal mask, row < Sq.
-      const int row_lo = p.causal ? key - (p.Sk - p.Sq) : -0x40000000;
+      const int row_lo = WIN || p.causal ? key - (p.Sk - p.Sq) : -0x40000000;
       const int c_lo = max(row_lo - 128 * m, 0);
-      const int c_hi = key_valid ? min(p.Sq - 128 * m, 128) : 0;
+      int c_hi = key_valid ? min(p.Sq - 128 * m, 128) : 0;
+      // Windowed: rows up to the last whose window reaches the key, sinks to the end.
+      if (WIN && key >= p.sinks) c_hi = min(c_hi, row_lo + p.window - 128 * m);
       const bool need_mask = __any_sync(0xffffffffu, c_lo > 64 * half || c_hi < 64 * half + 64);
       ok = __all_sync(0xffffffffu, bwd_wait(&bars->s_full, s & 1, bars));
       if (!ok) break;
@@ -524,10 +568,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_arrive_warp(&bars->ds_full);
     }
     if (ok) {
-      float* dk_row = p.out0 + (static_cast<size_t>(bg) * p.Sk + key) * D;
-      float* dv_row = p.out1 + (static_cast<size_t>(bg) * p.Sk + key) * D;
-      const size_t kv_bytes = static_cast<size_t>(p.B) * p.Hkv * p.Sk * D * sizeof(float);
-      if (nsteps == 0) {
+      const size_t kv_row = (static_cast<size_t>(bg) * p.Sk + key) * D;
+      float* dk_row = p.out0 + kv_row;
+      float* dv_row = p.out1 + kv_row;
+      const size_t kv_bytes =
+          static_cast<size_t>(p.B) * p.Hkv * p.Sk * D * (WIN ? sizeof(__nv_bfloat16) : sizeof(float));
+      if constexpr (WIN) {
+        __nv_bfloat16* dk16 = reinterpret_cast<__nv_bfloat16*>(p.out0) + kv_row;
+        __nv_bfloat16* dv16 = reinterpret_cast<__nv_bfloat16*>(p.out1) + kv_row;
+        if (nsteps == 0) {
+          if (key_valid && store_in_bounds(dk16, D * 2, p.out0, kv_bytes, p.status) &&
+              store_in_bounds(dv16, D * 2, p.out1, kv_bytes, p.status)) {
+            for (int c = half * D / 2; c < (half + 1) * D / 2; c += 8) {
+              *reinterpret_cast<uint4*>(dk16 + c) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(dv16 + c) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        } else {
+          ok = __all_sync(0xffffffffu, bwd_wait(&bars->acc_full, 0, bars));
+          if (ok) {
+            tc_fence_after();
+            store_acc_row16<D>(tmem + lane_addr + C::kColA0, dk16, p.scale, key_valid,
+                               half * D / 2, (half + 1) * D / 2, lane, p.out0, kv_bytes, p.status);
+            store_acc_row16<D>(tmem + lane_addr + C::kColA1, dv16, 1.f, key_valid, half * D / 2,
+                               (half + 1) * D / 2, lane, p.out1, kv_bytes, p.status);
+          }
+        }
+      } else if (nsteps == 0) {
         // No query row sees these keys: their gradients are zero.
         if (key_valid && store_in_bounds(dk_row, D * 4, p.out0, kv_bytes, p.status) &&
             store_in_bounds(dv_row, D * 4, p.out1, kv_bytes, p.status)) {
@@ -571,7 +638,28 @@ __device__ __forceinline__ int dq_tile_index(int round, int cta, int grid) {
   return round * grid + ((round & 1) ? (grid - 1 - cta) : cta);
 }
 
-template <int D>
+// The KV tiles of query tile m: step s reads tile kv_tile(s), s < nsteps.
+template <bool WIN>
+struct DqTiles {
+  int nsteps;
+  TileRange r;
+  __device__ __forceinline__ DqTiles(const BwdParams& p, int m) {
+    if constexpr (WIN) {
+      r = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, 128 * m);
+      nsteps = r.count();
+    } else {
+      nsteps = kv_tiles_for(p, m);
+    }
+  }
+  __device__ __forceinline__ int kv_tile(int s) const {
+    if constexpr (WIN)
+      return r.tile(s);
+    else
+      return s;
+  }
+};
+
+template <int D, bool WIN = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV,
@@ -634,7 +722,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
       const int m = mtiles - 1 - idx / BH, bh = idx % BH;
-      const int nsteps = kv_tiles_for(p, m);
+      const DqTiles<WIN> tiles(p, m);
+      const int nsteps = tiles.nsteps;
       if (nsteps == 0) continue;
       const int bkv = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / group;
       // Q and dO of this tile once the previous tile's last S and dP are done.
@@ -656,14 +745,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           good = bwd_wait(&bars->empty[sk], ((g / kKStages) - 1) & 1, bars);
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars->full[sk], C::kTile);
-          load_tile<D>(sK + sk * C::kTile, &tmK, &bars->full[sk], 128 * s, bkv);
+          load_tile<D>(sK + sk * C::kTile, &tmK, &bars->full[sk], 128 * tiles.kv_tile(s), bkv);
         }
         __syncwarp();
         if (g >= uint32_t(kVStages))
           good &= bwd_wait(&bars->empty_v[sv], ((g / kVStages) - 1) & 1, bars);
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars->full_v[sv], C::kTile);
-          load_tile<D>(sV + sv * C::kTile, &tmV, &bars->full_v[sv], 128 * s, bkv);
+          load_tile<D>(sV + sv * C::kTile, &tmV, &bars->full_v[sv], 128 * tiles.kv_tile(s), bkv);
         }
         __syncwarp();
         gl = g + 1;
@@ -703,7 +792,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
-      const int nsteps = kv_tiles_for(p, mtiles - 1 - idx / BH);
+      const int nsteps = DqTiles<WIN>(p, mtiles - 1 - idx / BH).nsteps;
       if (nsteps == 0) continue;
       const int buf = kt & 1;
       const uint32_t acc_col = buf ? C::kColA1 : C::kColA0;
@@ -753,19 +842,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int r = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
-    const size_t q_bytes = static_cast<size_t>(p.B) * p.Hq * p.Sq * D * sizeof(float);
+    const size_t q_bytes =
+        static_cast<size_t>(p.B) * p.Hq * p.Sq * D * (WIN ? sizeof(__nv_bfloat16) : sizeof(float));
     uint32_t G = 0;  // first global step of the current tile
     int kt = 0;      // tiles with work so far
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
       const int m = mtiles - 1 - idx / BH, bh = idx % BH;
-      const int nsteps = kv_tiles_for(p, m);
+      const DqTiles<WIN> tiles(p, m);
+      const int nsteps = tiles.nsteps;
       const int row = 128 * m + r;
       const bool row_valid = row < p.Sq;
       float* dq_row = p.out0 + (static_cast<size_t>(bh) * p.Sq + row) * D;
+      __nv_bfloat16* dq16 =
+          reinterpret_cast<__nv_bfloat16*>(p.out0) + (static_cast<size_t>(bh) * p.Sq + row) * D;
       if (nsteps == 0) {
         // No key is visible to these rows: their gradient is zero.
+        if constexpr (WIN) {
+          if (row_valid && store_in_bounds(dq16, D * 2, p.out0, q_bytes, p.status))
+            for (int c = half * D / 2; c < (half + 1) * D / 2; c += 8)
+              *reinterpret_cast<uint4*>(dq16 + c) = make_uint4(0u, 0u, 0u, 0u);
+          continue;
+        }
         if (row_valid && store_in_bounds(dq_row, D * 4, p.out0, q_bytes, p.status))
           for (int c = half * D / 2; c < (half + 1) * D / 2; c += 4)
             *reinterpret_cast<float4*>(dq_row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -776,7 +875,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float dlt = row_valid ? __ldg(p.delta + static_cast<size_t>(bh) * p.Sq + row) : 0.f;
       const uint64_t nl2 = f2_pack(-lse2, -lse2);
       const uint64_t ndl = f2_pack(-dlt, -dlt);
-      const int key_hi = p.causal ? min(p.Sk - 1, row + p.Sk - p.Sq) : p.Sk - 1;
+      const int key_hi = WIN || p.causal ? min(p.Sk - 1, row + p.Sk - p.Sq) : p.Sk - 1;
+      const int win_lo = row + p.Sk - p.Sq - p.window + 1;  // windowed: the window's first key
       for (int s = 0; s < nsteps && ok; ++s) {
         const uint32_t g = G + s;
         ok = __all_sync(0xffffffffu, bwd_wait(&bars->s_full, g & 1, bars));
@@ -790,8 +890,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         mbar_arrive_warp(&bars->p_ready);
         // Keys 128s + 64*half + e are visible for e < n_vis (causal limit, Sk).
-        const int n_vis = row_valid ? min(max(key_hi - (128 * s + 64 * half) + 1, 0), 64) : 0;
-        const bool need_mask = __any_sync(0xffffffffu, n_vis < 64);
+        const int key0 = 128 * tiles.kv_tile(s) + 64 * half;
+        const int n_vis = row_valid ? min(max(key_hi - key0 + 1, 0), 64) : 0;
+        // Windowed: of those, only e < n_sink or e >= n_skip.
+        const int n_sink = p.sinks - key0, n_skip = win_lo - key0;
+        const bool need_mask =
+            __any_sync(0xffffffffu, n_vis < 64 || (WIN && n_skip > 0 && n_sink < 64));
         float pv[64];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
@@ -800,8 +904,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     x0, x1);
           float p0 = ex2(x0), p1 = ex2(x1);
           if (need_mask) {
-            p0 = e < n_vis ? p0 : 0.f;
-            p1 = e + 1 < n_vis ? p1 : 0.f;
+            p0 = e < n_vis && (!WIN || e < n_sink || e >= n_skip) ? p0 : 0.f;
+            p1 = e + 1 < n_vis && (!WIN || e + 1 < n_sink || e + 1 >= n_skip) ? p1 : 0.f;
           }
           pv[e] = p0;
           pv[e + 1] = p1;
@@ -836,9 +940,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ok = __all_sync(0xffffffffu, bwd_wait(&bars->acc_full2[buf], (kt >> 1) & 1, bars));
       if (!ok) break;
       tc_fence_after();
-      store_acc_row<D>(tmem + lane_addr + (buf ? C::kColA1 : C::kColA0), dq_row, p.scale,
-                       row_valid, half * D / 2, (half + 1) * D / 2, lane, p.out0, q_bytes,
-                       p.status);
+      const uint32_t acc = tmem + lane_addr + (buf ? C::kColA1 : C::kColA0);
+      if constexpr (WIN)
+        store_acc_row16<D>(acc, dq16, p.scale, row_valid, half * D / 2, (half + 1) * D / 2, lane,
+                           p.out0, q_bytes, p.status);
+      else
+        store_acc_row<D>(acc, dq_row, p.scale, row_valid, half * D / 2, (half + 1) * D / 2, lane,
+                         p.out0, q_bytes, p.status);
       tc_fence_before();
       mbar_arrive_warp(&bars->acc_free[buf]);
       G += nsteps;
@@ -856,15 +964,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
-template <int D>
-cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const float* o,
-                            const float* lse, const void* dout, float* dq, float* dk, float* dv,
+// o, dq, dk and dv are fp32, or bf16 in the windowed form (window > 0).
+template <int D, bool WIN>
+cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const void* o,
+                            const float* lse, const void* dout, void* dq, void* dk, void* dv,
                             float* delta, int B, int Hq, int Hkv, int Sq, int Sk, int causal,
-                            float scale, cudaStream_t stream, int* status) {
+                            int window, int sinks, float scale, cudaStream_t stream, int* status) {
   using C = BwdCfg<D>;
+  using TO = std::conditional_t<WIN, __nv_bfloat16, float>;
   const int rows = B * Hq * Sq;
-  bwd_delta_kernel<D><<<(rows + 7) / 8, 256, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(dout), o, delta, rows);
+  bwd_delta_kernel<D, TO><<<(rows + 7) / 8, 256, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(dout), static_cast<const TO*>(o), delta, rows);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   CUtensorMap tmQ, tmK, tmV, tmDO;
@@ -873,10 +983,10 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const f
       !encode_bf16_map(&tmV, v, D, Sk, B * Hkv, 128) ||
       !encode_bf16_map(&tmDO, dout, D, Sq, B * Hq, 128))
     return cudaErrorInvalidValue;
-  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(bwd_dkdv_kernel<D>),
+  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(bwd_dkdv_kernel<D, WIN>),
                             static_cast<int>(C::kSmem))) != cudaSuccess)
     return e;
-  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(bwd_dq_kernel<D>),
+  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(bwd_dq_kernel<D, WIN>),
                             static_cast<int>(C::kSmemDq))) != cudaSuccess)
     return e;
   BwdParams p;
@@ -891,16 +1001,18 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const f
   p.causal = causal;
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
-  p.out0 = dk;
-  p.out1 = dv;
+  p.window = window;
+  p.sinks = sinks;
+  p.out0 = static_cast<float*>(dk);
+  p.out1 = static_cast<float*>(dv);
   const int kv_ctas = B * Hkv * ((Sk + 127) / 128);
-  bwd_dkdv_kernel<D><<<kv_ctas, kBwdThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, tmDO, p);
+  bwd_dkdv_kernel<D, WIN><<<kv_ctas, kBwdThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, tmDO, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  p.out0 = dq;
+  p.out0 = static_cast<float*>(dq);
   p.out1 = nullptr;
   const int q_tiles = B * Hq * ((Sq + 127) / 128);
   const int q_ctas = q_tiles < sm_count() ? q_tiles : sm_count();
-  bwd_dq_kernel<D><<<q_ctas, kBwdThreads, C::kSmemDq, stream>>>(tmQ, tmK, tmV, tmDO, p);
+  bwd_dq_kernel<D, WIN><<<q_ctas, kBwdThreads, C::kSmemDq, stream>>>(tmQ, tmK, tmV, tmDO, p);
   return cudaGetLastError();
 }
 
@@ -911,10 +1023,22 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const f
                             float* delta, int B, int Hq, int Hkv, int Sq, int Sk, int D,
                             int causal, float scale, cudaStream_t stream, int* status) {
   if (D == 128)
-    return launch_bwd_impl<128>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
-                                causal, scale, stream, status);
-  return launch_bwd_impl<64>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk, causal,
-                             scale, stream, status);
+    return launch_bwd_impl<128, false>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq,
+                                       Sk, causal, 0, 0, scale, stream, status);
+  return launch_bwd_impl<64, false>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
+                                    causal, 0, 0, scale, stream, status);
+}
+
+cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, const void* o,
+                                   const float* lse, const void* dout, void* dq, void* dk,
+                                   void* dv, float* delta, int B, int Hq, int Hkv, int Sq, int Sk,
+                                   int D, int window, int sinks, float scale, cudaStream_t stream,
+                                   int* status) {
+  if (D == 128)
+    return launch_bwd_impl<128, true>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq,
+                                      Sk, 1, window, sinks, scale, stream, status);
+  return launch_bwd_impl<64, true>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
+                                   1, window, sinks, scale, stream, status);
 }
 
 }  // namespace attn

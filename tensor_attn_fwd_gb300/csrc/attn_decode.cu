@@ -91,7 +91,23 @@ __device__ __forceinline__ uint32_t swz(uint32_t base, int key, int cidx) {
   return base + (cidx >> 3) * (kBlk * 128) + key * 128 + ((((cidx & 7) ^ (key & 7))) << 4);
 }
 
-template <int D>
+// The 32-key blocks that a windowed sequence of `len` keys attends to: blocks
+// [0, s) with its sinks and [w, w + n - s) with its window, n in all (s <= w; sink
+// blocks that meet the window are counted to it).  Its query stands at len - 1.
+struct WindowBlocks {
+  int lo;  // first key of the window
+  int s, w, n;
+  __device__ __forceinline__ WindowBlocks(int len, int window, int sinks) {
+    lo = max(len - window, 0);
+    w = lo / kBlk;
+    s = min((min(sinks, len) + kBlk - 1) / kBlk, w);
+    n = len > 0 ? s + (len + kBlk - 1) / kBlk - w : 0;
+  }
+  __device__ __forceinline__ int key0(int i) const { return (i < s ? i : i - s + w) * kBlk; }
+};
+
+// WIN: the windowed form (window, sinks), whose fused result O is bf16.
+template <int D, bool WIN = false>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     decode_splitkv_kernel(const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,
@@ -100,8 +116,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                           const int* __restrict__ block_table, int page_size, int max_pages,
                           int num_pages, int B, int Hq, int Hkv, int Sk, int num_splits,
                           int head_slices, float scale_log2, int* status,
-                          float* __restrict__ o_final, float* __restrict__ lse_final,
-                          int* __restrict__ counters) {
+                          void* __restrict__ o_final, float* __restrict__ lse_final,
+                          int* __restrict__ counters, int window, int sinks) {
   using C = DecCfg<D>;
   constexpr int KS = D / 16;  // k-steps of S = Q K^T
   constexpr int NT = D / 8;   // n-tiles of O += P V
@@ -139,7 +155,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int key_begin = kb64 < len ? static_cast<int>(kb64) : len;
   const int key_end = min(key_begin + chunk, len);
   const int nkeys = key_end - key_begin;
-  const int nblk = (nkeys + kBlk - 1) / kBlk;
+  // Windowed: whole 32-key blocks of the ones the sequence sees, evenly over the
+  // splits (blocks start at multiples of 32 keys: none straddles two pages).
+  const WindowBlocks wb(WIN ? len : 0, WIN ? window : 1, WIN ? sinks : 0);
+  const int wchunk = (wb.n + num_splits - 1) / num_splits;
+  const int wb0 = min(split * wchunk, wb.n);
+  const int nblk = WIN ? min(wchunk, wb.n - wb0) : (nkeys + kBlk - 1) / kBlk;
+  // First key of this split's block i.
+  auto block_key = [&](int i) { return WIN ? wb.key0(wb0 + i) : key_begin + i * kBlk; };
   const int my_nblk = warp < nblk ? (nblk - warp + kWarps - 1) / kWarps : 0;
   const int nloads = 2 * my_nblk;
   const int bkv = b * Hkv + g;
@@ -165,12 +188,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // The warp looks up its first kPidBlocks page ids at once (a lane each), so
   // the issuing lane does not wait on a table load in front of every copy.
   if (block_table != nullptr && lane < my_nblk)
-    my_pids[lane] = page_of(key_begin + (warp + lane * kWarps) * kBlk);
+    my_pids[lane] = page_of(block_key(warp + lane * kWarps));
   __syncwarp();
 
   // Load number li of this warp: even = K block, odd = V block of its (li/2)-th block.
   auto issue = [&](int li) {
-    const int key0 = key_begin + (warp + (li >> 1) * kWarps) * kBlk;
+    const int key0 = block_key(warp + (li >> 1) * kWarps);
     const int slot = li % kSlots;
     uint8_t* dst = my_ring + slot * C::kSlotBytes;
     int plane = bkv, row = key0;
@@ -218,8 +241,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   bool ok = true;
   int consumed = 0;
   for (int i = 0; i < my_nblk && ok; ++i) {
-    const int key0 = key_begin + (warp + i * kWarps) * kBlk;
-    const int nvalid = min(kBlk, key_end - key0);
+    const int key0 = block_key(warp + i * kWarps);
+    const int nvalid = min(kBlk, (WIN ? len : key_end) - key0);
+    // Windowed: of those keys, only key < n_sink or key >= n_skip.
+    const int n_sink = sinks - key0, n_skip = wb.lo - key0;
+    const bool partial = nvalid < kBlk || (WIN && n_skip > 0 && n_sink < kBlk);
+    auto visible = [&](int key) {
+      return key < nvalid && (!WIN || key < n_sink || key >= n_skip);
+    };
 
     // ---------------- K block: S = Q K^T for 32 keys (4 n-tiles of 8 keys)
     float s[4][4];
@@ -259,7 +288,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = 8 * nt + 2 * tq + (e & 1);
-          const float x = key < nvalid ? s[nt][e] * scale_log2 : -INFINITY;
+          const float x = visible(key) ? s[nt][e] * scale_log2 : -INFINITY;
           s[nt][e] = x;
           mx[e >> 1] = fmaxf(mx[e >> 1], x);
         }
@@ -270,6 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
         alpha[r] = 1.f;
+        // (Every block has a visible key: the maximum is finite from the first on.)
         if (m_run[r] == -INFINITY || mx[r] > m_run[r] + kLazyRescale) {
           alpha[r] = ex2(m_run[r] - mx[r]);  // 0 on the first block
           m_run[r] = mx[r];
@@ -311,13 +341,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if (!ok) break;
       consumed = li + 1;
       const uint32_t vb = smem_u32(my_ring + slot * C::kSlotBytes);
-      if (nvalid < kBlk) {
-        // Rows past the block's last key are real keys of another split, zero
+      if (partial) {
+        // Rows outside the window, and rows past the block's last key are real keys of another split, zero
         // fill past Sk, or (with per-sequence lengths) unwritten cache memory
         // that may hold NaN/Inf: zero them so that p = 0 contributes nothing.
         uint8_t* vrow = my_ring + slot * C::kSlotBytes;
-        for (int idx = lane; idx < (kBlk - nvalid) * 8 * C::kSub; idx += 32) {
-          const int r = nvalid + idx / (8 * C::kSub);
+        const int r0 = WIN ? 0 : nvalid;
+        for (int idx = lane; idx < (kBlk - r0) * 8 * C::kSub; idx += 32) {
+          const int r = r0 + idx / (8 * C::kSub);
+          if (WIN && visible(r)) continue;
           const int c = idx % (8 * C::kSub);  // 16-byte chunk across the sub-tiles
           *reinterpret_cast<uint4*>(vrow + (c >> 3) * C::kSubBytes + r * 128 + (c & 7) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
@@ -414,6 +446,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       }
       const size_t row = (static_cast<size_t>(split) * B + b) * Hq + hq;
       const size_t rows = static_cast<size_t>(num_splits) * B * Hq;  // debug bounds checks
+      if (WIN && num_splits == 1) {
+        // The only split is the result: no partials.
+        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(o_final) + row * D + part * DPT;
+        if (store_in_bounds(dst16, DPT * 2, o_final, rows * D * 2, status)) {
+#pragma unroll
+          for (int e = 0; e < DPT; e += 8)
+            *reinterpret_cast<uint4*>(dst16 + e) =
+                make_uint4(pack_bf16x2(out[e], out[e + 1]), pack_bf16x2(out[e + 2], out[e + 3]),
+                           pack_bf16x2(out[e + 4], out[e + 5]), pack_bf16x2(out[e + 6], out[e + 7]));
+        }
+        if (part == 0 &&
+            store_in_bounds(lse_final + row, 4, lse_final, rows * sizeof(float), status))
+          lse_final[row] = lse;
+        return;
+      }
       float* dst = o_part + row * D + part * DPT;
       if (store_in_bounds(dst, DPT * 4, o_part, rows * D * sizeof(float), status)) {
 #pragma unroll
@@ -433,7 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // barrier), the acquire in the last CTA makes every other CTA's visible.
   // The merge is combine_kernel's, warp by warp over the rows (lanes over the
   // splits), so both paths give the same bits; it reads through L2 (ld.cg).
-  if (counters != nullptr) {
+  if (counters != nullptr && !(WIN && num_splits == 1)) {
     __shared__ int s_last;
     __syncthreads();
     int* counter = counters + blockIdx.z * gridDim.y + blockIdx.y;
@@ -520,7 +567,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           for (int e = 0; e < DPL; ++e) out[i][e] *= inv;
           L = M[i] + logf(W[i]);
         }
-        float* dst = o_final + row0[i] * D + lane * DPL;
+        if constexpr (WIN) {
+          // bf16 O, rounded once (P is rounded to bf16 for the second product).
+          __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(o_final) + row0[i] * D + lane * DPL;
+          if (store_in_bounds(dst16, DPL * 2, o_final, split_rows * D * 2, status)) {
+            uint32_t pk[DPL / 2];
+#pragma unroll
+            for (int e = 0; e < DPL / 2; ++e) pk[e] = pack_bf16x2(out[i][2 * e], out[i][2 * e + 1]);
+            if constexpr (DPL == 8)
+              *reinterpret_cast<uint4*>(dst16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            else if constexpr (DPL == 4)
+              *reinterpret_cast<uint2*>(dst16) = make_uint2(pk[0], pk[1]);
+            else
+              *reinterpret_cast<uint32_t*>(dst16) = pk[0];
+          }
+          if (lane == 0 && store_in_bounds(lse_final + row0[i], 4, lse_final,
+                                           split_rows * sizeof(float), status))
+            lse_final[row0[i]] = L;
+          continue;
+        }
+        float* dst = static_cast<float*>(o_final) + row0[i] * D + lane * DPL;
         if (store_in_bounds(dst, DPL * 4, o_final, split_rows * D * sizeof(float), status)) {
           if constexpr (DPL >= 4) {
 #pragma unroll
@@ -618,11 +684,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   if (lane == 0) lse[row] = L;
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_decode_impl(const void* q, const void* k, const void* v, const int* seqlens,
                                const PagedKV* paged, float* o_part, float* lse_part, int B,
                                int Hq, int Hkv, int Sk, int num_splits, float scale,
-                               cudaStream_t stream, int* status, const FusedCombine* fused) {
+                               cudaStream_t stream, int* status, const FusedCombine* fused,
+                               int window, int sinks) {
   using C = DecCfg<D>;
   const int G = Hq / Hkv;
   const int head_slices = (G + kRows - 1) / kRows;
@@ -634,18 +701,19 @@ cudaError_t launch_decode_impl(const void* q, const void* k, const void* v, cons
   if (!encode_bf16_map(&tmK, k, D, rows, planes, kBlk) ||
       !encode_bf16_map(&tmV, v, D, rows, planes, kBlk))
     return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(decode_splitkv_kernel<D>),
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(decode_splitkv_kernel<D, WIN>),
                                    static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;
   const dim3 grid(num_splits, Hkv * head_slices, B);
   const float scale_log2 = scale * 1.4426950408889634f;
   return launch_programmatic(
-      decode_splitkv_kernel<D>, grid, dim3(kWarps * 32), C::kSmemBytes, stream, tmK, tmV,
+      decode_splitkv_kernel<D, WIN>, grid, dim3(kWarps * 32), C::kSmemBytes, stream, tmK, tmV,
       static_cast<const __nv_bfloat16*>(q), o_part, lse_part, seqlens,
       paged != nullptr ? paged->block_table : nullptr, paged != nullptr ? paged->page_size : 0,
       paged != nullptr ? paged->max_pages : 0, paged != nullptr ? paged->num_pages : 0, B, Hq, Hkv,
       Sk, num_splits, head_slices, scale_log2, status, fused != nullptr ? fused->o : nullptr,
-      fused != nullptr ? fused->lse : nullptr, fused != nullptr ? fused->counters : nullptr);
+      fused != nullptr ? fused->lse : nullptr, fused != nullptr ? fused->counters : nullptr, window,
+      sinks);
 }
 
 }  // namespace
@@ -656,13 +724,28 @@ cudaError_t launch_decode_splitkv(const void* q, const void* k, const void* v, f
                                   const int* seqlens, const PagedKV* paged,
                                   const FusedCombine* fused) {
   if (D == 256)
-    return launch_decode_impl<256>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
-                                   num_splits, scale, stream, status, fused);
+    return launch_decode_impl<256, false>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv,
+                                          Sk, num_splits, scale, stream, status, fused, 0, 0);
   if (D == 128)
-    return launch_decode_impl<128>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
-                                   num_splits, scale, stream, status, fused);
-  return launch_decode_impl<64>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
-                                num_splits, scale, stream, status, fused);
+    return launch_decode_impl<128, false>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv,
+                                          Sk, num_splits, scale, stream, status, fused, 0, 0);
+  return launch_decode_impl<64, false>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
+                                       num_splits, scale, stream, status, fused, 0, 0);
+}
+
+cudaError_t launch_decode_window(const void* q, const void* k, const void* v, const int* seqlens,
+                                 const PagedKV* paged, float* o_part, float* lse_part, int B,
+                                 int Hq, int Hkv, int Sk, int D, int window, int sinks,
+                                 int num_splits, float scale, cudaStream_t stream, int* status,
+                                 const FusedCombine& out) {
+  if (D == 256)
+    return launch_decode_impl<256, true>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
+                                         num_splits, scale, stream, status, &out, window, sinks);
+  if (D == 128)
+    return launch_decode_impl<128, true>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
+                                         num_splits, scale, stream, status, &out, window, sinks);
+  return launch_decode_impl<64, true>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
+                                      num_splits, scale, stream, status, &out, window, sinks);
 }
 
 cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o, float* lse,

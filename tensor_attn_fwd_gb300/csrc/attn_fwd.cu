@@ -45,6 +45,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace attn {
 namespace {
@@ -106,6 +107,7 @@ struct FwdParams {
   int split_tiles;   // KV tiles per split
   size_t split_stride_o, split_stride_lse;
   int total_items;   // B * Hq * num_pairs * num_splits (B * Hq / 2 * num_splits in pairs)
+  int window, sinks;  // windowed kernels: row at position p sees (p - window, p] and [0, sinks)
 };
 
 // A work item is two 128-row query tiles that stream the same K/V: rows
@@ -119,7 +121,53 @@ struct Item {
   int j0;      // first KV tile of the split
   int n[2];    // end (exclusive) of query tile 0 / 1's KV tiles in the split;
                // n[t] <= j0: nothing to compute for tile t
+  // Windowed kernels: each query tile's KV tiles and their union, which the item
+  // streams; j0 is the union's first tile and n[t] = r[t].e.
+  TileRange r[2], u;
 };
+
+// The KV tile after j in an item's stream.
+template <bool WIN>
+__device__ __forceinline__ int next_tile(const Item& it, int j) {
+  if constexpr (WIN)
+    return it.u.next(j);
+  else
+    return j + 1;
+}
+
+// Windowed items, KV head by KV head (their query heads, then row tiles side by
+// side, so that the items in flight share K/V in L2).  With an even number of
+// query heads per KV head an item is one 128-row tile of two heads: both tiles
+// then need the same KV tiles.  Otherwise it is 256 rows of one head, whose tiles
+// differ by one KV tile at either end.
+__device__ __forceinline__ Item get_window_item(const FwdParams& p, int idx) {
+  const int group = p.Hq / p.Hkv;
+  const int per_group = p.head_pairs ? group / 2 : group;
+  const int rest = idx / per_group;
+  const int bg = rest / p.num_pairs;  // b * Hkv + KV head
+  const int tile = p.num_pairs - 1 - rest % p.num_pairs;
+  Item it;
+  it.split = 0;
+  it.bh = (bg / p.Hkv) * p.Hq + (bg % p.Hkv) * group +
+          (idx % per_group) * (p.head_pairs ? 2 : 1);
+  it.q_row0 = tile * (p.head_pairs ? 128 : kRowsPerItem);
+  it.r[0] = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0);
+  it.r[1] = p.head_pairs ? it.r[0]
+                         : window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0 + 128);
+  it.n[0] = it.r[0].e;
+  it.n[1] = it.r[1].e;
+  // Tile 1's rows come later: its tiles start and end no earlier, unless it (or
+  // tile 0, whose rows may all stand before the first key) is empty.
+  it.u = it.r[1];
+  if (it.r[1].e == 0) {
+    it.u = it.r[0];
+  } else if (it.r[0].e > 0) {
+    it.u.w = it.r[0].w;
+    it.u.s = min(max(it.r[0].s, it.r[1].s), it.u.w);
+  }
+  it.j0 = it.u.first();
+  return it;
+}
 
 // Number of leading keys that query tile t of an item needs, in KV tiles.
 __device__ __forceinline__ int tile_kv_count(const FwdParams& p, int row_first) {
@@ -164,8 +212,9 @@ __device__ __forceinline__ int tile_bh(const FwdParams& p, const Item& it, int t
 //            1.5-2.5 % slower.  Under the causal mask, chunking the KV heads so
 //            that the heads in flight stay in L2 (the D = 256 kernel's ORDER 2)
 //            measured -3 to +3 % here, so causal launches keep ORDER 0.
-template <int ORDER>
+template <int ORDER, bool WIN>
 __device__ __forceinline__ Item get_item(const FwdParams& p, int idx) {
+  if constexpr (WIN) return get_window_item(p, idx);
   const int BH = p.B * p.Hq;
   Item it;
   if (p.head_pairs) {
@@ -230,7 +279,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* 
 // elect.sync, so the warp reconverges by itself.
 
 // ------------------------------------------------------------------ producer
-template <int D, int ORDER>
+template <int D, int ORDER, bool WIN>
 __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
                           const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* bars) {
   using C = Cfg<D>;
@@ -245,7 +294,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
   for (int r = 0; ok; ++r) {
     const int idx = item_index(r, blockIdx.x, gridDim.x);
     if (idx >= p.total_items) break;
-    const Item it = get_item<ORDER>(p, idx);
+    const Item it = get_item<ORDER, WIN>(p, idx);
     const int n = max(it.n[0], it.n[1]);  // end of the item's KV tiles
     if (n <= it.j0) continue;
     const int b = it.bh / p.Hq, h = it.bh % p.Hq;  // both tiles' KV head
@@ -288,9 +337,10 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
       __syncwarp();
       ok = __all_sync(0xffffffffu, g);
     }
-    for (int j = it.j0; j < n && ok; ++j) {
+    for (int j = it.j0, jn; j < n && ok; j = jn) {
       uint32_t sv, sk = 0;
-      const bool pair = j + 1 < n;
+      jn = next_tile<WIN>(it, j);
+      const bool pair = jn < n;
       bool good = take_stage(sv);
       if (pair) good &= take_stage(sk);
       if (elect_one()) {
@@ -303,7 +353,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
 #pragma unroll
           for (int s = 0; s < C::kSub; ++s)
             tma_load_3d_hint(sKV + sk * C::kTileBytes + s * kSubBytes, tmK, &bars->kv_full[sv],
-                             s * 64, (j + 1) * 128, bkv, pol_kv);
+                             s * 64, jn * 128, bkv, pol_kv);
           mbar_arrive(&bars->kv_full[sk]);
         }
       }
@@ -326,7 +376,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
 }
 
 // ------------------------------------------------------------------ MMA issuer
-template <int D, int ORDER>
+template <int D, int ORDER, bool WIN>
 __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* bars,
                          uint32_t tmem) {
   using C = Cfg<D>;
@@ -389,14 +439,15 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
   for (int r = 0; ok; ++r) {
     const int idx = item_index(r, blockIdx.x, gridDim.x);
     if (idx >= p.total_items) break;
-    const Item it = get_item<ORDER>(p, idx);
+    const Item it = get_item<ORDER, WIN>(p, idx);
     const int n = max(it.n[0], it.n[1]);  // end of the item's KV tiles
     if (n <= it.j0) continue;
     if (!(ok = wait_warp(&bars->q_full, q_ctr & 1, bars))) break;
     ++q_ctr;
 
     // Q may be overwritten once the item's last S MMA has completed.
-    int s_left = max(it.n[0] - it.j0, 0) + max(it.n[1] - it.j0, 0);
+    int s_left = WIN ? it.r[0].count() + it.r[1].count()
+                     : max(it.n[0] - it.j0, 0) + max(it.n[1] - it.j0, 0);
     auto issue_s_counted = [&](int t, uint32_t st) {
       issue_s(t, st);
       tc_commit_w(&bars->s_full[t]);
@@ -407,7 +458,7 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
     tc_fence_after();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (it.n[t] > it.j0) issue_s_counted(t, kst);
+      if (WIN ? it.r[t].has(it.j0) : it.n[t] > it.j0) issue_s_counted(t, kst);
     }
     tc_commit_w(&bars->kv_empty[kst]);
 
@@ -415,11 +466,12 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
     // later wait of the item give up after a few polls, and the MMAs keep
     // in-bounds operands, so the item runs out quickly and the vote ends it.
     bool good = true;
-    for (int j = it.j0; j < n; ++j) {
+    for (int j = it.j0, jn; j < n; j = jn) {
       // Both operand tiles of this step are acquired before any P wait, so
       // their (usually already satisfied) waits overlap queued MMAs.
       uint32_t vst, nkst = 0;
-      const bool has_next = j + 1 < n;
+      jn = next_tile<WIN>(it, j);
+      const bool has_next = jn < n;
       good &= acquire_kv(vst);
       if (has_next) {  // landed with V_j: counted on V_j's barrier
         nkst = kv_ctr % C::kStages;
@@ -427,19 +479,28 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (j >= it.n[t]) continue;
+        if constexpr (WIN) {
+          // A tile of the union that this query tile does not need: only its
+          // next scores, if the stream's next tile is one it needs.
+          if (!it.r[t].has(j)) {
+            if (has_next && it.r[t].has(jn)) issue_s_counted(t, nkst);
+            continue;
+          }
+        } else {
+          if (j >= it.n[t]) continue;
+        }
         // P arrives in two halves (keys 0-63, 64-127): start on the first
         // while the softmax warps are still producing the second.
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           good &= wait_or_abort(&bars->p_full[t][half], p_phase[t], bars);
           tc_fence_after();
-          issue_pv_half(t, vst, half, j == it.j0);
+          issue_pv_half(t, vst, half, j == (WIN ? it.r[t].first() : it.j0));
         }
         p_phase[t] ^= 1;
         if (j == it.n[t] - 1)
           tc_commit_w(&bars->o_full[t]);
-        else
+        else if (!WIN || it.r[t].has(jn))
           issue_s_counted(t, nkst);
       }
       tc_commit_w(&bars->kv_empty[vst]);
@@ -455,7 +516,7 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
 }
 
 // ------------------------------------------------------------------ softmax
-template <int D, int ORDER>
+template <int D, int ORDER, bool WIN>
 __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int warp, int lane) {
   using C = Cfg<D>;
   const int t = warp >> 2;
@@ -471,10 +532,12 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
   for (int r = 0; ok; ++r) {
     const int idx = item_index(r, blockIdx.x, gridDim.x);
     if (idx >= p.total_items) break;
-    const Item it = get_item<ORDER>(p, idx);
+    const Item it = get_item<ORDER, WIN>(p, idx);
     // This warpgroup's tile (t is a runtime value: select, do not index, so the
     // item stays in registers).
     const int nt = t ? it.n[1] : it.n[0];  // end of this tile's KV tiles in the split
+    const TileRange tr = t ? it.r[1] : it.r[0];  // windowed: this tile's KV tiles
+    const int j_first = WIN ? tr.first() : it.j0;
     const int bh = tile_bh(p, it, t);
     const int row = tile_row0(p, it, t) + quad * 32 + lane;
     const bool row_valid = row < p.Sq;
@@ -484,14 +547,14 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
     __nv_bfloat16* o_row16 = static_cast<__nv_bfloat16*>(p.o) + o_off;
     float* lse_ptr = p.lse + static_cast<size_t>(bh) * p.Sq + row +
                      static_cast<size_t>(it.split) * p.split_stride_lse;
-    if (nt <= it.j0) {
+    if (nt <= j_first) {
       // No key of the split visible to any row of this tile (or the tile is
       // past Sq): O = 0, LSE = -inf (a split a combine weighs with 0).
       if (row_valid &&
-          store_in_bounds(p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
-                          D * (p.o_bf16 ? 2 : 4), p.o, p.o_bytes, p.status) &&
+          store_in_bounds(WIN || p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
+                          D * (WIN || p.o_bf16 ? 2 : 4), p.o, p.o_bytes, p.status) &&
           store_in_bounds(lse_ptr, 4, p.lse, p.lse_bytes, p.status)) {
-        if (p.o_bf16) {
+        if (WIN || p.o_bf16) {
 #pragma unroll 4
           for (int c = 0; c < D; c += 8)
             *reinterpret_cast<uint4*>(o_row16 + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -505,11 +568,13 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
       continue;
     }
     // Largest key index this row may see.
-    const int limit = p.causal ? min(row + p.Sk - p.Sq, p.Sk - 1) : p.Sk - 1;
+    const int limit = WIN || p.causal ? min(row + p.Sk - p.Sq, p.Sk - 1) : p.Sk - 1;
+    // Windowed: first key of the row's window; earlier keys are seen below `sinks`.
+    const int win_lo = row + p.Sk - p.Sq - p.window + 1;
     float m = -INFINITY;  // reference maximum (log2 domain)
     float l = 0.f;
 
-    for (int j = it.j0; j < nt; ++j) {
+    for (int j = j_first; j < nt; j = WIN ? tr.next(j) : j + 1) {
       ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[t], s_phase, bars));
       if (!ok) break;
       s_phase ^= 1;
@@ -521,11 +586,13 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
       tmem_ld64(tS, sa);
       tmem_ld64_nowait(tS + 64, sb);
       const int key0 = j * 128;
-      const bool need_mask = __any_sync(0xffffffffu, key0 + 127 > limit);
+      const bool need_mask = __any_sync(
+          0xffffffffu, key0 + 127 > limit || (WIN && key0 < win_lo && key0 + 127 >= p.sinks));
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-          if (key0 + c > limit) sa[c] = __float_as_uint(-INFINITY);
+          if (key0 + c > limit || (WIN && key0 + c < win_lo && key0 + c >= p.sinks))
+            sa[c] = __float_as_uint(-INFINITY);
       }
       // Row maximum: 4 independent chains of 3-input max.
       float ch[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -538,7 +605,8 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-          if (key0 + 64 + c > limit) sb[c] = __float_as_uint(-INFINITY);
+          if (key0 + 64 + c > limit || (WIN && key0 + 64 + c < win_lo && key0 + 64 + c >= p.sinks))
+            sb[c] = __float_as_uint(-INFINITY);
       }
 #pragma unroll
       for (int c = 0; c < 64; c += 8)
@@ -549,7 +617,7 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
 
       bool rescale = false;
       float alpha = 1.f;
-      if (j == it.j0) {
+      if (j == j_first) {
         m = m_tile;
       } else if (m_tile - m > kRescaleThreshold) {  // false when both are -inf
         alpha = ex2(m - m_tile);
@@ -627,7 +695,7 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
     // 32, halving the L1 wavefronts that the per-row layout of TMEM costs.
     const int pb = lane & 1;
     const bool even_valid = row - pb < p.Sq, odd_valid = row - pb + 1 < p.Sq;
-    if (p.o_bf16) {
+    if (WIN || p.o_bf16) {
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t w[16];
@@ -673,7 +741,7 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, int ORDER>
+template <int D, int ORDER, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -729,13 +797,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // launch allocation of 384 threads x 168 registers (checked at build time).
   if (warp < 8) {
     setmaxnreg_inc<kRegsSoftmax>();
-    softmax_role<D, ORDER>(p, bars, tmem, warp, lane);
+    softmax_role<D, ORDER, WIN>(p, bars, tmem, warp, lane);
   } else {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kMmaWarp) {
-      mma_role<D, ORDER>(p, sQ, sKV, bars, tmem);
+      mma_role<D, ORDER, WIN>(p, sQ, sKV, bars, tmem);
     } else if (warp == kLoadWarp) {
-      load_role<D, ORDER>(&tmQ, &tmK, &tmV, p, sQ, sKV, bars);
+      load_role<D, ORDER, WIN>(&tmQ, &tmK, &tmV, p, sQ, sKV, bars);
     }
   }
 
@@ -792,7 +860,60 @@ cudaError_t launch_fwd_impl(const void* q, const void* k, const void* v, void* o
                              tmK, tmV, p);
 }
 
+// Windowed forward: one split, bf16 O (P is rounded to bf16 for the second
+// product, so an fp32 O would hold no more).
+template <int D>
+cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void* o, float* lse,
+                               int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks,
+                               float scale, cudaStream_t stream, int* status) {
+  using C = Cfg<D>;
+  CUtensorMap tmQ, tmK, tmV;
+  if (!encode_bf16_map(&tmQ, q, D, Sq, B * Hq, 128) || !encode_bf16_map(&tmK, k, D, Sk, B * Hkv, 128) ||
+      !encode_bf16_map(&tmV, v, D, Sk, B * Hkv, 128))
+    return cudaErrorInvalidValue;
+  auto kernel = attn_fwd_kernel<D, 0, true>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel),
+                                         static_cast<int>(C::kSmemBytes));
+  if (e != cudaSuccess) return e;
+  FwdParams p = {};
+  p.o = o;
+  p.o_bf16 = 1;
+  p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  p.o_bytes = static_cast<size_t>(B) * Hq * Sq * D * 2;
+  p.lse_bytes = static_cast<size_t>(B) * Hq * Sq * sizeof(float);
+  p.lse = lse;
+  p.status = status;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Sq = Sq;
+  p.Sk = Sk;
+  p.causal = 1;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.head_pairs = (Hq / Hkv) % 2 == 0;
+  const int rows = p.head_pairs ? 128 : kRowsPerItem;
+  p.num_pairs = (Sq + rows - 1) / rows;
+  p.num_splits = 1;
+  p.window = window;
+  p.sinks = sinks;
+  p.total_items = (p.head_pairs ? B * Hq / 2 : B * Hq) * p.num_pairs;
+  const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
+  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,
+                             tmK, tmV, p);
+}
+
 }  // namespace
+
+cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, void* o,
+                                   float* lse, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                   int window, int sinks, float scale, cudaStream_t stream,
+                                   int* status) {
+  if (D == 128)
+    return launch_window_impl<128>(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, window, sinks, scale,
+                                   stream, status);
+  return launch_window_impl<64>(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, window, sinks, scale, stream,
+                                status);
+}
 
 cudaError_t launch_attn_fwd(const void* q, const void* k, const void* v, void* o, int o_bf16,
                             float* lse, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,

@@ -128,7 +128,7 @@ int decode_check_args(const void* q, const void* k, const void* v, int B, int Hq
 // 16-head slice) group last also combines the group's partials into o / lse
 // (counters: int32 [B * Hkv * ceil((Hq/Hkv)/16)], zero on entry, zero again after).
 struct FusedCombine {
-  float* o;
+  void* o;  // fp32; bf16 for launch_decode_window
   float* lse;
   int* counters;
 };
@@ -137,6 +137,27 @@ cudaError_t launch_decode_splitkv(const void* q, const void* k, const void* v, f
                                   int num_splits, float scale, cudaStream_t stream, int* status,
                                   const int* seqlens = nullptr, const PagedKV* paged = nullptr,
                                   const FusedCombine* fused = nullptr);
+
+// The windowed form (always fused): sequence b's query stands at its last key and
+// sees the last `window` keys and the first `sinks` (1 <= window <= Sk, 0 <= sinks
+// <= Sk).  Splits share out the 32-key blocks that hold a visible key.
+cudaError_t launch_decode_window(const void* q, const void* k, const void* v, const int* seqlens,
+                                 const PagedKV* paged, float* o_part, float* lse_part, int B,
+                                 int Hq, int Hkv, int Sk, int D, int window, int sinks,
+                                 int num_splits, float scale, cudaStream_t stream, int* status,
+                                 const FusedCombine& out);
+
+// Sliding-window prefill and backward (bf16 O and gradients, D 64 or 128); window
+// and sinks clamped as above.
+cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, void* o,
+                                   float* lse, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                   int window, int sinks, float scale, cudaStream_t stream,
+                                   int* status);
+cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, const void* o,
+                                   const float* lse, const void* dout, void* dq, void* dk,
+                                   void* dv, float* delta, int B, int Hq, int Hkv, int Sq, int Sk,
+                                   int D, int window, int sinks, float scale, cudaStream_t stream,
+                                   int* status);
 
 // Backward: Delta into `delta` ([B,Hq,Sq]), then dK/dV and dQ kernels.
 cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const float* o,

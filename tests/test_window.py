@@ -1,0 +1,466 @@
+"""Attention with a sliding window and sinks: attn_window_fwd, attn_window_bwd,
+decode_window and decode_window_paged against the formula in 64 bits.
+
+Bounds, element by element, from the roundings that the kernels make (u = 2^-8,
+half a bf16 step relative to the value; fp32 sums of the products add less than
+w = 2^-12 relative to the sum of magnitudes at these sizes):
+  O     P is rounded to bf16 for the second product, O once at the end:
+        u |O| + (u + w) sum_j P |V|
+  LSE   scores are fp32 sums of D products, each within 2^-24 of the running sum of
+        magnitudes: (D + 8) 2^-24 max_j scale sum_d |q k| + 2^-18
+  dV    u |dV| + (u + w) sum_i P |dO|
+  dS    dS is rounded to bf16; Delta reads the rounded O:
+        e_dS = (u + w) |dS| + P (sum_d |dO| e_O + w sum_d |dO| |V|)
+  dQ    u |dQ| + scale sum_j e_dS |K| + w scale sum_j |dS| |K|; dK alike
+"""
+import itertools
+import math
+
+import pytest
+import torch
+
+import tensor_attn_fwd_gb300 as attn
+
+U, W = 2.0 ** -8, 2.0 ** -12
+NEG = float("-inf")
+
+
+def visible(Sq, Sk, window, sinks):
+    p = torch.arange(Sq)[:, None] + Sk - Sq
+    j = torch.arange(Sk)[None, :]
+    return (j <= p) & ((j > p - window) | (j < sinks))
+
+
+def reference(q, k, v, window, sinks, scale, do=None):
+    """The outputs in 64 bits and their bounds: dicts of tensors."""
+    q, k, v = (t.double().cpu() for t in (q, k, v))
+    B, Hq, Sq, D = q.shape
+    Hkv, Sk = k.shape[1:3]
+    n = Hq // Hkv
+    kx, vx = (t.repeat_interleave(n, 1) for t in (k, v))
+    seen = visible(Sq, Sk, window, sinks)
+    x = (q @ kx.transpose(-1, -2)) * scale
+    x = x.masked_fill(~seen, NEG)
+    lse = torch.logsumexp(x, -1)
+    p = torch.exp(x - lse.masked_fill(lse == NEG, 0.0)[..., None]).masked_fill(~seen, 0.0)
+    o = p @ vx
+    mag = (q.abs() @ kx.abs().transpose(-1, -2)).masked_fill(~seen, 0.0).amax(-1) * scale
+    ref = {"o": o, "lse": lse}
+    tol = {"o": U * o.abs() + (U + W) * (p @ vx.abs()), "lse": (D + 8) * 2.0 ** -24 * mag + 2.0 ** -18}
+    if do is not None:
+        do = do.double().cpu()
+
+        def shared(t):  # the sum over the query heads of a KV head
+            return t.view(B, Hkv, n, Sk, D).sum(2)
+
+        pt = p.transpose(-1, -2)
+        ds = p * (do @ vx.transpose(-1, -2) - (do * o).sum(-1, keepdim=True))
+        e_ds = (U + W) * ds.abs() + p * ((do.abs() * tol["o"]).sum(-1, keepdim=True)
+                                         + W * (do.abs() @ vx.abs().transpose(-1, -2)))
+        both = e_ds + W * ds.abs()
+        ref["dv"] = shared(pt @ do)
+        ref["dq"] = scale * (ds @ kx)
+        ref["dk"] = scale * shared(ds.transpose(-1, -2) @ q)
+        tol["dv"] = U * ref["dv"].abs() + (U + W) * shared(pt @ do.abs())
+        tol["dq"] = U * ref["dq"].abs() + scale * (both @ kx.abs())
+        tol["dk"] = U * ref["dk"].abs() + scale * shared(both.transpose(-1, -2) @ q.abs())
+    return ref, tol
+
+
+def check(name, got, ref, tol):
+    got = got.double().cpu()
+    assert got.shape == ref.shape, name
+    empty = ref == NEG
+    assert torch.equal(got == NEG, empty), f"{name}: rows without keys"
+    err = torch.where(empty, 0.0, got - ref.masked_fill(empty, 0.0)).abs()
+    assert bool(torch.isfinite(err).all()), f"{name}: not finite"
+    over = (err - tol - 1e-30).max().item()
+    assert over <= 0, f"{name}: {over:.3e} over the bound (worst error {err.max().item():.3e})"
+
+
+def inputs(B, Hq, Hkv, Sq, Sk, D, seed, grad=False):
+    g = torch.Generator().manual_seed(seed)
+    shapes = [(B, Hq, Sq, D), (B, Hkv, Sk, D), (B, Hkv, Sk, D)] + ([(B, Hq, Sq, D)] if grad else [])
+    return [torch.randn(s, generator=g).to(torch.bfloat16).cuda() for s in shapes]
+
+
+# B, Hq, Hkv, Sq, Sk, D, window, sinks
+SHAPES = [
+    (1, 1, 1, 1, 1, 64, 1, 0),              # one row, one key
+    (1, 2, 1, 1, 1, 128, 5, 3),             # a window and sinks longer than the sequence
+    (1, 2, 1, 1, 1000, 128, 999, 0),        # one row of a long cache
+    (2, 4, 2, 129, 129, 64, 1, 0),          # a row sees itself alone
+    (1, 4, 4, 128, 128, 64, 32, 1),         # one tile
+    (1, 2, 2, 300, 300, 128, 128, 0),       # row pairs, window of one tile
+    (1, 4, 1, 257, 257, 64, 100, 130),      # sinks past the first tile
+    (1, 3, 1, 500, 500, 128, 70, 4),        # an odd group: row pairs
+    (1, 2, 1, 700, 700, 64, 129, 200),
+    (1, 1, 1, 900, 900, 64, 130, 129),      # a gap in the tiles of a row pair
+    (1, 5, 1, 1030, 1030, 128, 1, 1),       # far apart: one sink, one key
+    (2, 2, 2, 100, 700, 64, 300, 7),        # a chunk against a longer cache
+    (1, 4, 2, 300, 129, 128, 40, 3),        # rows before the first key
+    (1, 2, 2, 300, 100, 64, 10, 0),         # whole tiles of such rows, row pairs
+    (1, 2, 2, 200, 200, 64, 10000, 0),      # the window covers everything
+    (1, 2, 2, 200, 200, 64, 2, 10000),      # the sinks do
+    (1, 2, 2, 640, 640, 64, 128, 128),      # everything on tile borders
+    (1, 6, 2, 1100, 1100, 128, 257, 513),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward_and_backward_match_the_formula(shape):
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, 11 * Sq + Sk + window, grad=True)
+    scale = 1.0 / math.sqrt(D)
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks)
+    grads = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    ref, tol = reference(q, k, v, window, sinks, scale, do)
+    check("o", o, ref["o"], tol["o"])
+    check("lse", lse, ref["lse"], tol["lse"])
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        check(name, got, ref[name], tol[name])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,D", [(2, 4, 2, 333, 333, 128), (1, 3, 3, 200, 700, 64),
+                                              (1, 2, 1, 300, 129, 64)])
+def test_a_window_over_everything_is_the_causal_forward(B, Hq, Hkv, Sq, Sk, D):
+    q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, 5)
+    want = attn.attn_fwd_bf16o(q, k, v, causal=True)
+    for window, sinks in ((Sk, 0), (2 ** 31 + 5, 0), (1, Sk), (7, 2 ** 40)):
+        got = attn.attn_window_fwd(q, k, v, window, sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_gradients_are_the_differences_of_the_forward():
+    # Directional differences of L = sum(dO O) in 64 bits along random directions.
+    B, Hq, Hkv, S, D, window, sinks = 1, 4, 2, 90, 64, 17, 3
+    q, k, v, do = inputs(B, Hq, Hkv, S, S, D, 3, grad=True)
+    scale = 1.0 / math.sqrt(D)
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks)
+    grads = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+    _, tol = reference(q, k, v, window, sinks, scale, do)
+    h = 1e-4
+    g = torch.Generator().manual_seed(1)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        base = [t.double().cpu() for t in (q, k, v)]
+        d = torch.randn(base[i].shape, generator=g, dtype=torch.float64)
+        loss = []
+        for sign in (1, -1):
+            at = list(base)
+            at[i] = base[i] + sign * h * d
+            loss.append((reference(*at, window, sinks, scale)[0]["o"] * do.double().cpu()).sum())
+        diff = ((loss[0] - loss[1]) / (2 * h)).item()
+        got = (grads[i].double().cpu() * d).sum().item()
+        # The gradient's bound along d, and the difference's own h^2 term.
+        assert abs(got - diff) <= (tol[name] * d.abs()).sum().item() + 1e-4 * abs(diff), name
+
+
+@pytest.mark.gpu
+def test_unseen_keys_may_be_anything_outside_the_tiles_in_use():
+    # Keys that the window has passed, in tiles that no row sees.
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = 1, 4, 2, 70, 1024, 128, 100, 5
+    q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, 8, grad=True)
+    want = attn.attn_window_fwd(q, k, v, window, sinks)
+    gwant = attn.attn_window_bwd(q, k, v, *want, do, window, sinks)
+    k2, v2 = k.clone(), v.clone()
+    first = (Sk - Sq - window + 1) // 128 * 128
+    k2[:, :, 128:first] = float("nan")
+    v2[:, :, 128:first] = float("inf")
+    got = attn.attn_window_fwd(q, k2, v2, window, sinks)
+    ggot = attn.attn_window_bwd(q, k2, v2, *got, do, window, sinks)
+    for a, b in zip(got + ggot, want + gwant):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_outputs_rows_behind_the_tensor_stay():
+    B, Hq, Hkv, S, D, window, sinks = 1, 2, 1, 201, 64, 33, 2
+    q, k, v, do = inputs(B, Hq, Hkv, S, S, D, 9, grad=True)
+
+    def guarded(shape, dtype):
+        n = math.prod(shape)
+        buf = torch.full((n + 4096,), 7.0, dtype=dtype, device="cuda")
+        return buf, buf[:n].view(shape)
+
+    ob, o = guarded(q.shape, torch.bfloat16)
+    lb, lse = guarded(q.shape[:3], torch.float32)
+    attn.attn_window_fwd(q, k, v, window, sinks, o=o, lse=lse)
+    gs = [guarded(t.shape, torch.bfloat16) for t in (q, k, v)]
+    attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks, dq=gs[0][1], dk=gs[1][1], dv=gs[2][1])
+    for buf, view in [(ob, o), (lb, lse)] + gs:
+        assert bool((buf[view.numel():] == 7.0).all())
+
+
+# ------------------------------------------------------------------ decode
+def paged(k, v, page, seed, spare=3):
+    """A paged copy of contiguous caches: (k_cache, v_cache, table), pages shuffled."""
+    B, Hkv, Sk, D = k.shape
+    M = -(-Sk // page)
+    P = B * M + spare
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randperm(P, generator=g)[: B * M].view(B, M)
+    out = []
+    for t in (k, v):
+        pad = torch.zeros(B, Hkv, M * page, D, dtype=t.dtype, device=t.device)
+        pad[:, :, :Sk] = t
+        cache = torch.full((P, Hkv, page, D), float("nan"), dtype=t.dtype, device=t.device)
+        cache[ids.view(-1).cuda()] = (pad.view(B, Hkv, M, page, D).transpose(1, 2)
+                                      .reshape(B * M, Hkv, page, D))
+        out.append(cache)
+    return out[0], out[1], ids.int().cuda().contiguous()
+
+
+def decode_reference(q, k, v, lens, window, sinks, scale):
+    outs, tols = {"o": [], "lse": []}, {"o": [], "lse": []}
+    B, Hq, _, D = q.shape
+    for b, n in enumerate(lens):
+        if n == 0:
+            z = torch.zeros(1, Hq, 1, D, dtype=torch.float64)
+            r, t = {"o": z, "lse": z[..., 0] + NEG}, {"o": z, "lse": z[..., 0]}
+        else:
+            r, t = reference(q[b:b + 1], k[b:b + 1, :, :n], v[b:b + 1, :, :n], window, sinks, scale)
+        for name in outs:
+            outs[name].append(r[name][:, :, 0])
+            tols[name].append(t[name][:, :, 0])
+    return {n: torch.cat(x) for n, x in outs.items()}, {n: torch.cat(x) for n, x in tols.items()}
+
+
+# Hq, Hkv, D, window, sinks, lengths
+DECODES = [
+    (1, 1, 64, 1, 0, [1, 2, 33, 64]),
+    (4, 1, 128, 40, 4, [0, 1, 39, 40, 41, 44, 45, 76, 300]),
+    (8, 2, 64, 100, 33, [5, 32, 33, 132, 133, 134, 517]),
+    (6, 2, 256, 64, 1, [64, 65, 96, 97, 400]),
+    (17, 1, 128, 31, 70, [31, 70, 101, 102, 230]),      # a group wider than one MMA tile
+    (4, 4, 128, 10 ** 6, 0, [1, 100, 333]),             # a window over everything
+    (2, 1, 64, 3, 10 ** 6, [1, 100, 333]),              # sinks over everything
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", DECODES)
+@pytest.mark.parametrize("splits", [1, 3, None])
+def test_decode_matches_the_formula(case, splits):
+    Hq, Hkv, D, window, sinks, lens = case
+    B, Sk = len(lens), max(lens)
+    if splits is not None and splits > Sk:
+        splits = Sk
+    q, k, v = inputs(B, Hq, Hkv, 1, Sk, D, 17 * Hq + D) if B else None
+    scale = 1.0 / math.sqrt(D)
+    seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    # Keys past a sequence's length, and those that its window has passed, are garbage.
+    kg, vg = k.clone(), v.clone()
+    for b, n in enumerate(lens):
+        hidden = torch.ones(Sk, dtype=torch.bool)
+        hidden[:n] = ~visible(1, n, window, sinks)[0] if n else hidden[:0]
+        kg[b, :, hidden.cuda()] = float("nan")
+        vg[b, :, hidden.cuda()] = float("-inf")
+    ref, tol = decode_reference(q, k, v, lens, window, sinks, scale)
+    o, lse = attn.decode_window(q, kg, vg, window, sinks, seqlens=seqlens, num_splits=splits)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    check("o", o, ref["o"], tol["o"])
+    check("lse", lse, ref["lse"], tol["lse"])
+    for page in (32, 96):
+        kc, vc, table = paged(kg, vg, page, seed=page)
+        # Pages without a seen key are not read: their entries are no pages.
+        slot = torch.arange(table.shape[1])
+        for b, n in enumerate(lens):
+            live = (slot * page < n) & (((slot + 1) * page > n - window) | (slot * page < sinks))
+            table[b, ~live.cuda()] = -1
+        op, lp = attn.decode_window_paged(q, kc, vc, table, seqlens, window, sinks,
+                                          num_splits=splits)
+        assert attn.attn_debug_status() == attn.ATTN_OK
+        assert torch.equal(op, o) and torch.equal(lp, lse) or splits is None
+        check("o", op, ref["o"], tol["o"])
+        check("lse", lp, ref["lse"], tol["lse"])
+
+
+@pytest.mark.gpu
+def test_decode_without_lengths_is_the_forward_of_the_last_row():
+    B, Hq, Hkv, Sk, D, window, sinks = 2, 8, 2, 777, 128, 130, 9
+    q, k, v = inputs(B, Hq, Hkv, 1, Sk, D, 4)
+    ref, tol = reference(q, k, v, window, sinks, 1.0 / math.sqrt(D))
+    o, lse = attn.decode_window(q, k, v, window, sinks)
+    check("o", o, ref["o"][:, :, 0], tol["o"][:, :, 0])
+    check("lse", lse, ref["lse"][:, :, 0], tol["lse"][:, :, 0])
+
+
+@pytest.mark.gpu
+def test_decode_reports_a_bad_page_it_reaches():
+    q, k, v = inputs(1, 2, 1, 1, 128, 64, 2)
+    kc, vc, table = paged(k, v, 32, 1, spare=0)
+    seqlens = torch.tensor([128], dtype=torch.int32, device="cuda")
+    table[0, 1] = 99  # passed by the window: never looked at
+    attn.decode_window_paged(q, kc, vc, table, seqlens, 40, 3)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    table[0, 3] = 4
+    attn.decode_window_paged(q, kc, vc, table, seqlens, 40, 3)
+    assert attn.attn_debug_status() == attn.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_streams_and_two_graphs_at_once():
+    Hq, Hkv, D, Sk, window, sinks = 8, 2, 128, 4096, 2000, 4
+    sets = [inputs(1, Hq, Hkv, 1, Sk, D, s) for s in (1, 2)]
+    want = [attn.decode_window(*s, window, sinks, num_splits=8) for s in sets]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    on_side = attn.decode_window(*sets[0], window, sinks, num_splits=8, stream=side)
+    side.synchronize()
+    assert torch.equal(on_side[0], want[0][0]) and torch.equal(on_side[1], want[0][1])
+    graphs, outs = [], []
+    for s in sets:  # both captured on one stream, with no counters of the caller's
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(attn.decode_window(*s, window, sinks, num_splits=8))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+
+
+@pytest.mark.gpu
+def test_training_step_in_a_graph_repeats_its_bits():
+    B, Hq, Hkv, S, D, window, sinks = 1, 4, 2, 400, 64, 100, 4
+    q, k, v, do = inputs(B, Hq, Hkv, S, S, D, 6, grad=True)
+
+    def step():
+        o, lse = attn.attn_window_fwd(q, k, v, window, sinks)
+        return (o, lse) + attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+
+    want = step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ refusals (no GPU)
+A, M = 0x10000000, 0x10000004
+
+
+def _lib():
+    from tensor_attn_fwd_gb300 import build as attn_build
+    attn_build.build()
+    return attn.load_library()
+
+
+def fwd(q=A, k=A, v=A, o=A, lse=A, B=1, Hq=2, Hkv=1, Sq=8, Sk=8, D=64, window=4, sinks=1,
+        scale=0.125):
+    return _lib().attn_window_fwd(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, window, sinks, scale, None)
+
+
+def bwd(q=A, k=A, v=A, o=A, lse=A, do=A, dq=A, dk=A, dv=A, ws=A, B=1, Hq=2, Hkv=1, Sq=8, Sk=8, D=64,
+        window=4, sinks=1, scale=0.125):
+    return _lib().attn_window_bwd(q, k, v, o, lse, do, dq, dk, dv, ws, B, Hq, Hkv, Sq, Sk, D, window,
+                                  sinks, scale, None)
+
+
+COMMON = [
+    (dict(q=None), attn.ATTN_ERR_INVALID_ARG),
+    (dict(lse=None), attn.ATTN_ERR_INVALID_ARG),
+    (dict(window=0), attn.ATTN_ERR_INVALID_ARG),
+    (dict(window=-1), attn.ATTN_ERR_INVALID_ARG),
+    (dict(sinks=-1), attn.ATTN_ERR_INVALID_ARG),
+    (dict(Hq=3, Hkv=2), attn.ATTN_ERR_INVALID_ARG),
+    (dict(Sq=0), attn.ATTN_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), attn.ATTN_ERR_INVALID_ARG),
+    (dict(D=256), attn.ATTN_ERR_UNSUPPORTED),
+    (dict(D=96), attn.ATTN_ERR_UNSUPPORTED),
+    (dict(Sk=(1 << 30) + 1), attn.ATTN_ERR_UNSUPPORTED),
+    (dict(v=M), attn.ATTN_ERR_MISALIGNED),
+    (dict(o=M), attn.ATTN_ERR_MISALIGNED),
+]
+
+
+@pytest.mark.parametrize("call,kw,code", [(f, kw, c) for f in (fwd, bwd) for kw, c in COMMON] + [
+    (bwd, dict(ws=None), attn.ATTN_ERR_INVALID_ARG),
+    (bwd, dict(dk=M), attn.ATTN_ERR_MISALIGNED)])
+def test_prefill_and_backward_reject(call, kw, code):
+    assert call(**kw) == code
+
+
+def dec(q=A, k=A, v=A, sl=A, o=A, lse=A, op=A, lp=A, ct=A, B=1, Hq=4, Hkv=1, Sk=64, D=128, window=8,
+        sinks=1, ns=4, scale=0.1):
+    return _lib().attn_decode_window(q, k, v, sl, o, lse, op, lp, ct, B, Hq, Hkv, Sk, D, window,
+                                     sinks, ns, scale, None)
+
+
+def decp(q=A, k=A, v=A, sl=A, o=A, lse=A, op=A, lp=A, ct=A, B=1, Hq=4, Hkv=1, D=128, window=8,
+         sinks=1, ns=4, scale=0.1, bt=A, num_pages=8, page=64, max_pages=4):
+    return _lib().attn_decode_window_paged(q, k, v, bt, sl, o, lse, op, lp, ct, B, Hq, Hkv,
+                                           num_pages, page, max_pages, D, window, sinks, ns, scale,
+                                           None)
+
+
+@pytest.mark.parametrize("call,kw,code", list(itertools.chain.from_iterable(
+    [(f, kw, c) for kw, c in [
+        (dict(o=None), attn.ATTN_ERR_INVALID_ARG),
+        (dict(lse=None), attn.ATTN_ERR_INVALID_ARG),
+        (dict(op=None), attn.ATTN_ERR_INVALID_ARG),
+        (dict(ct=None), attn.ATTN_ERR_INVALID_ARG),
+        (dict(window=0), attn.ATTN_ERR_INVALID_ARG),
+        (dict(sinks=-3), attn.ATTN_ERR_INVALID_ARG),
+        (dict(ns=0), attn.ATTN_ERR_INVALID_ARG),
+        (dict(ns=10 ** 6), attn.ATTN_ERR_INVALID_ARG),
+        (dict(D=96), attn.ATTN_ERR_UNSUPPORTED),
+        (dict(B=70000), attn.ATTN_ERR_UNSUPPORTED),
+        (dict(k=M), attn.ATTN_ERR_MISALIGNED),
+        (dict(o=M), attn.ATTN_ERR_MISALIGNED),
+        (dict(op=M), attn.ATTN_ERR_MISALIGNED),
+        (dict(ct=A + 2), attn.ATTN_ERR_MISALIGNED),
+        (dict(sl=A + 1), attn.ATTN_ERR_MISALIGNED),
+    ]] for f in (dec, decp))) + [
+        (decp, dict(sl=None), attn.ATTN_ERR_INVALID_ARG),
+        (decp, dict(bt=None), attn.ATTN_ERR_INVALID_ARG),
+        (decp, dict(page=48), attn.ATTN_ERR_UNSUPPORTED),
+        (decp, dict(max_pages=1 << 25), attn.ATTN_ERR_UNSUPPORTED)])
+def test_decode_rejects(call, kw, code):
+    assert call(**kw) == code
+
+
+def test_python_rejects():
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        attn.attn_window_fwd(q, q, q, 4)  # CPU tensors
+    with pytest.raises(ValueError):
+        attn.attn_window_bwd(q, q, q, q, q, q, 4)
+    with pytest.raises(ValueError):
+        attn.decode_window(q[:, :, :1], q, q, 4)
+
+
+@pytest.mark.gpu
+def test_python_rejects_shapes_types_and_reach():
+    q, k, v = inputs(1, 2, 1, 8, 8, 64, 1)
+    o, lse = attn.attn_window_fwd(q, k, v, 4)
+    for bad in (dict(window=0), dict(window=-2), dict(window=4, sinks=-1)):
+        with pytest.raises(ValueError):
+            attn.attn_window_fwd(q, k, v, **bad)
+    with pytest.raises(ValueError):
+        attn.attn_window_fwd(q.float(), k, v, 4)
+    with pytest.raises(ValueError):
+        attn.attn_window_fwd(q.transpose(1, 2), k, v, 4)
+    with pytest.raises(ValueError):
+        attn.attn_window_bwd(q, k, v, o.float(), lse, q, 4)   # o is bf16
+    with pytest.raises(ValueError):
+        attn.attn_window_bwd(q, k, v, o, None, q, 4)
+    with pytest.raises(ValueError):
+        attn.decode_window(q, k, v, 4)                        # eight query rows
+    with pytest.raises(ValueError):
+        attn.decode_window(q[:, :, :1].contiguous(), k, v, 4,
+                           seqlens=torch.tensor([8], device="cuda"))  # int64 lengths
