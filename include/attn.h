@@ -47,8 +47,9 @@ typedef enum {
     ATTN_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned */
     ATTN_ERR_CUDA = 4,         /* the CUDA runtime reported an error */
     ATTN_ERR_TIMEOUT = 5,      /* a kernel's bounded wait expired (device status) */
-    ATTN_ERR_BOUNDS = 6        /* debug builds (-DATTN_DEBUG_BOUNDS): a kernel skipped a
+    ATTN_ERR_BOUNDS = 6,       /* debug builds (-DATTN_DEBUG_BOUNDS): a kernel skipped a
                                   store outside its output buffer (device status) */
+    ATTN_ERR_NO_PAGES = 7      /* attn_pages_fork ran out of free pages (device status) */
 } attn_status;
 
 /*
@@ -411,6 +412,107 @@ ATTN_API int attn_decode_window_paged(const void *q, const void *k_cache, const 
                                       int B, int Hq, int Hkv, int num_pages, int page_size,
                                       int max_pages, int D, int window, int sinks, int num_splits,
                                       float scale, void *stream);
+
+/*
+ * Pages of a KV cache, kept on the device.  A paged cache (attn_decode_splitkv_paged)
+ * leaves its pages to the caller; these four calls keep them without the host
+ * reading anything back.  block_table int32 [rows, max_pages] names the page of
+ * each slot of a row (keys [slot * page_size, (slot + 1) * page_size)), -1: no page.
+ * refs int32 [num_pages] counts the holders of each page: the table's entries that
+ * name it, and whoever else keeps it (a prompt cache adds its own); 0: free.  One
+ * table serves the caches of all layers.  The pages the decode entry points cite
+ * print no bookkeeping; the rules are stated here in full.
+ *
+ * Common rules: all arrays are device int32, 4-byte aligned; no call reads or
+ * writes page contents but attn_pages_copy.  Results depend on the inputs alone
+ * (free pages are taken lowest id first).  An entry that is neither a page nor -1
+ * sets ATTN_ERR_INVALID_ARG in the device status word (attn_debug_status) and
+ * counts as -1.  Limits: rows * max_pages < 2^31, max_pages * page_size <= 2^30,
+ * num_pages <= 2^30 (else ATTN_ERR_UNSUPPORTED).  Outputs may not overlap inputs
+ * unless said otherwise.
+ */
+
+/*
+ * Give up the pages that the next decode cannot read.  Slot s of row b keeps its
+ * page iff seqlens[b] >= 0, s * page_size < seqlens[b] + room, and
+ *     (s + 1) * page_size > seqlens[b] - window  or  s * page_size < sinks:
+ * exactly the pages that attn_decode_window_paged reads at these lengths, and those
+ * reserved for the next `room` keys.  Any other entry becomes -1 and its page's
+ * count falls by one.  seqlens[b] < 0 marks a finished row: all its pages go.  A
+ * window as long as the rows (INT_MAX) gives up only what lies behind them.
+ *   block_table_out [B,max_pages], refs_out [num_pages]; each may be its input.
+ *   window >= 1, sinks >= 0, room >= 0.  A page whose count is not positive sets
+ *   ATTN_ERR_INVALID_ARG in the status word (and is counted down all the same).
+ */
+ATTN_API int attn_pages_free(const int *block_table, const int *refs, const int *seqlens,
+                             int *block_table_out, int *refs_out, int B, int max_pages,
+                             int num_pages, int page_size, int window, int sinks, int room,
+                             void *stream);
+
+/*
+ * Rows of a new table from rows of an old one: reordering beams, n samples of a
+ * prompt, dropping finished rows, and reserving pages for coming keys (parents =
+ * 0, 1, ..., B-1).  New row r continues old row parents[r] (-1: an empty row), has
+ * its length, and holds pages for keys [0, length + room) (as far as max_pages):
+ *   slots below length / page_size, full of keys, are shared: the old entry;
+ *   the others will be written.  An old page in such a slot stays with the lowest
+ *   (r, slot) that has it there, provided that nobody else holds it (no shared
+ *   slot of the new table, no holder outside the old one).  All others get a free
+ *   page (refs = 0 on entry), lowest id first in the order of (r, slot).  Where the
+ *   slot already holds keys (its row's length is no multiple of page_size),
+ *   (src[r], dst[r]) lists the page to copy, for attn_pages_copy on every layer's
+ *   cache, before the new rows are written or read; otherwise both are -1.
+ * The old table's entries no longer count; refs_out is refs less those, plus the
+ * new ones.  Pages that become free are handed out from the next call on.
+ *   parents [R]; block_table_out [R,max_pages], refs_out [num_pages],
+ *   seqlens_out [R], src, dst [R]
+ *   counts [2]: pages needed and pages free.  If the first exceeds the second,
+ *   ATTN_ERR_NO_PAGES is set in the status word, the slots that got none are -1,
+ *   and a row whose keys they were ends before them (seqlens_out[r] a multiple of
+ *   page_size).
+ *   workspace: attn_pages_workspace(num_pages, R) int32, contents undefined
+ *   A parent outside [-1, B) sets ATTN_ERR_INVALID_ARG in the status word and makes
+ *   an empty row.  seqlens are clamped to [0, max_pages * page_size].
+ */
+ATTN_API int attn_pages_fork(const int *block_table, const int *refs, const int *seqlens,
+                             const int *parents, int *block_table_out, int *refs_out,
+                             int *seqlens_out, int *src, int *dst, int *counts, int *workspace,
+                             int B, int R, int max_pages, int num_pages, int page_size, int room,
+                             void *stream);
+
+/*
+ * Move the live pages (refs > 0) to the lowest ids, so that the pool's tail from
+ * num_live on is free.  With n live pages, those below id n stay; the i-th lowest
+ * live page from n on moves to the i-th lowest free id below n.  src and dst
+ * [num_pages / 2] list the moves (then -1), for attn_pages_copy on every layer's
+ * cache before the new table is used; block_table_out [B,max_pages] and refs_out
+ * [num_pages] name the pages by their new ids, num_live [1] is n.
+ *   workspace: attn_pages_workspace(num_pages, 0) int32, contents undefined
+ *   src and dst may be NULL when num_pages = 1.  A table entry of a page with refs
+ *   <= 0 sets ATTN_ERR_INVALID_ARG in the status word and becomes -1.
+ */
+ATTN_API int attn_pages_compact(const int *block_table, const int *refs, int *block_table_out,
+                                int *refs_out, int *src, int *dst, int *num_live, int *workspace,
+                                int B, int max_pages, int num_pages, void *stream);
+
+/* int32 entries of workspace for attn_pages_fork (R rows) and attn_pages_compact (R = 0).
+ * Host-only.  ATTN_ERR_INVALID_ARG for num_pages < 1, R < 0 or a NULL result. */
+ATTN_API int attn_pages_workspace(int num_pages, int R, long long *entries);
+
+/*
+ * Copy pages of one layer's caches: page dst[i] of k_cache and of v_cache becomes
+ * page src[i], for i < n; a pair of -1 is skipped.
+ *   k_cache, v_cache: num_pages contiguous pages of page_bytes each (for the decode
+ *   layout Hkv * page_size * D * 2), 16-byte aligned; page_bytes a multiple of 16
+ *   (else ATTN_ERR_UNSUPPORTED)
+ *   src, dst device int32 [n]; n = 0 does nothing.  The pairs run at the same time:
+ *   a dst may not appear as another pair's dst or src (its contents would be either
+ *   page's; lists by attn_pages_fork and attn_pages_compact never do).  A pair with
+ *   an id outside [0, num_pages) that is not -1, -1 is skipped and sets
+ *   ATTN_ERR_INVALID_ARG in the status word.
+ */
+ATTN_API int attn_pages_copy(void *k_cache, void *v_cache, const int *src, const int *dst, int n,
+                             int num_pages, long long page_bytes, void *stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 ATTN_API const char *attn_status_string(int status);

@@ -23,6 +23,11 @@ Names follow the C ABI:
     attn_window_bwd(q, k, v, o, lse, dout, window, sinks) -> (dq, dk, dv) bf16
     decode_window(q, k, v, window, sinks)       -> (o bf16, lse)   one new token
     decode_window_paged(q, k_cache, v_cache, block_table, seqlens, window, sinks)
+    attn_pages_free(block_table, refs, seqlens, page_size, window, sinks) -> (block_table, refs)
+    attn_pages_fork(block_table, refs, seqlens, parents, page_size, room)
+                            -> (block_table, refs, seqlens, src, dst, counts)
+    attn_pages_compact(block_table, refs) -> (block_table, refs, src, dst, num_live)
+    attn_pages_copy(k_cache, v_cache, src, dst)
 Layouts: Q [B,Hq,Sq,D], K/V [B,Hkv,Sk,D] bf16; O [B,Hq,Sq,D], LSE [B,Hq,Sq] fp32.
 """
 from __future__ import annotations
@@ -41,7 +46,9 @@ __all__ = ["AttnError", "attn_fwd", "attn_fwd_bf16o", "attn_decode_splitkv", "at
            "attn_status_string", "attn_debug_status", "library_path", "load_library",
            "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_MISALIGNED",
            "ATTN_ERR_CUDA", "ATTN_ERR_TIMEOUT", "ATTN_ERR_BOUNDS", "attn_wait_selftest", "attn_fwd_splitkv", "attn_fwd_num_splits",
-           "attn_window_fwd", "attn_window_bwd", "decode_window", "decode_window_paged"]
+           "attn_window_fwd", "attn_window_bwd", "decode_window", "decode_window_paged",
+           "attn_pages_free", "attn_pages_fork", "attn_pages_compact", "attn_pages_copy",
+           "ATTN_ERR_NO_PAGES"]
 
 ATTN_OK = 0
 ATTN_ERR_INVALID_ARG = 1
@@ -50,6 +57,7 @@ ATTN_ERR_MISALIGNED = 3
 ATTN_ERR_CUDA = 4
 ATTN_ERR_TIMEOUT = 5
 ATTN_ERR_BOUNDS = 6
+ATTN_ERR_NO_PAGES = 7
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libattn.so"
@@ -85,6 +93,11 @@ _SIGNATURES = {
     "attn_window_bwd": ([_vp] * 10 + [_int] * 8 + [_flt, _vp], _int),
     "attn_decode_window": ([_vp] * 9 + [_int] * 8 + [_flt, _vp], _int),
     "attn_decode_window_paged": ([_vp] * 10 + [_int] * 10 + [_flt, _vp], _int),
+    "attn_pages_free": ([_vp] * 5 + [_int] * 7 + [_vp], _int),
+    "attn_pages_fork": ([_vp] * 11 + [_int] * 6 + [_vp], _int),
+    "attn_pages_compact": ([_vp] * 8 + [_int] * 3 + [_vp], _int),
+    "attn_pages_workspace": ([_int, _int, ctypes.POINTER(ctypes.c_longlong)], _int),
+    "attn_pages_copy": ([_vp] * 4 + [_int, _int, ctypes.c_longlong, _vp], _int),
     "attn_status_string": ([_int], ctypes.c_char_p),
     "attn_debug_status": ([_vp], _int),
     "attn_wait_selftest": ([ctypes.c_ulonglong, _vp, _vp], _int),
@@ -873,3 +886,137 @@ def decode_window_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     return _decode_window("attn_decode_window_paged", q, k_cache, v_cache, block_table, seqlens,
                           block_table.shape[1] * page_size, window, sinks, num_splits, scale,
                           workspace, o, lse, counters, stream)
+
+
+def _check_int32(name: str, t: torch.Tensor, shape, device=None):
+    """A contiguous int32 CUDA tensor; shape entries of None are free."""
+    _check(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
+           and t.is_contiguous() and (device is None or t.device == device),
+           f"{name} must be a contiguous int32 CUDA tensor on the table's device")
+    _check(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
+           f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _out_int32(t, shape, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _check_int32(name, t, shape, device)
+    return t
+
+
+def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,
+                    page_size: int, window: int | None = None, sinks: int = 0, room: int = 0,
+                    block_table_out: torch.Tensor | None = None,
+                    refs_out: torch.Tensor | None = None, stream=None):
+    """Give up the pages that the next decode cannot read; returns (block_table, refs).
+
+    block_table int32 [B,max_pages] (-1: no page), refs int32 [num_pages] (holders of
+    each page), seqlens int32 [B] (negative: a finished row).  Kept are the pages that
+    decode_window_paged reads at these lengths with this window and sinks
+    (``window=None``: every key), and those reserved for the next ``room`` keys.
+    ``block_table_out`` and ``refs_out`` may be the inputs.
+    """
+    _check_int32("block_table", block_table, (None, None))
+    _check_int32("refs", refs, (None,), block_table.device)
+    B, M = block_table.shape
+    _check_int32("seqlens", seqlens, (B,), block_table.device)
+    window, sinks = _reach(1 << 30 if window is None else window, sinks)
+    _check(int(room) >= 0, "room must not be negative")
+    lib = load_library()
+    with _call_scope(block_table.device, stream) as handle:
+        table = _out_int32(block_table_out, (B, M), block_table.device, "block_table_out")
+        count = _out_int32(refs_out, (refs.shape[0],), block_table.device, "refs_out")
+        st = lib.attn_pages_free(block_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
+                                 table.data_ptr(), count.data_ptr(), B, M, refs.shape[0],
+                                 int(page_size), window, sinks, min(int(room), 1 << 30), handle)
+    _raise_if(st, "attn_pages_free")
+    return table, count
+
+
+def attn_pages_fork(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,
+                    parents: torch.Tensor, page_size: int, room: int = 0, stream=None):
+    """New rows from old ones, with pages for keys [0, length + room); returns
+    (block_table [R,max_pages], refs, seqlens [R], src [R], dst [R], counts [2]).
+
+    parents int32 [R]: the old row that each new row continues (-1: an empty row).
+    Full pages are shared; a page still to be written stays with the lowest row that
+    has it, if nobody else holds it, and the others get free pages, lowest id first.
+    (src, dst) lists the pages to copy (attn_pages_copy, for every layer's cache)
+    before the new rows are used.  counts holds the pages needed and the pages free;
+    if they do not suffice, attn_debug_status reports ATTN_ERR_NO_PAGES.
+    """
+    _check_int32("block_table", block_table, (None, None))
+    device = block_table.device
+    _check_int32("refs", refs, (None,), device)
+    _check_int32("parents", parents, (None,), device)
+    B, M = block_table.shape
+    _check_int32("seqlens", seqlens, (B,), device)
+    _check(int(room) >= 0, "room must not be negative")
+    R, P = parents.shape[0], refs.shape[0]
+    lib = load_library()
+    n = ctypes.c_longlong(0)
+    _raise_if(lib.attn_pages_workspace(P, R, ctypes.byref(n)), "attn_pages_workspace")
+    with _call_scope(device, stream) as handle:
+        table = torch.empty((R, M), dtype=torch.int32, device=device)
+        count = torch.empty(P, dtype=torch.int32, device=device)
+        lens, src, dst = torch.empty((3, R), dtype=torch.int32, device=device).unbind()
+        counts = torch.empty(2, dtype=torch.int32, device=device)
+        workspace = torch.empty(n.value, dtype=torch.int32, device=device)
+        st = lib.attn_pages_fork(block_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
+                                 parents.data_ptr(), table.data_ptr(), count.data_ptr(),
+                                 lens.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                 counts.data_ptr(), workspace.data_ptr(), B, R, M, P,
+                                 int(page_size), min(int(room), 1 << 30), handle)
+    _raise_if(st, "attn_pages_fork")
+    return table, count, lens, src, dst, counts
+
+
+def attn_pages_compact(block_table: torch.Tensor, refs: torch.Tensor, stream=None):
+    """Number the live pages (refs > 0) from 0; returns (block_table, refs,
+    src [num_pages // 2], dst [num_pages // 2], num_live [1]).
+
+    Pages below num_live stay, the others move to the lowest free ids; (src, dst)
+    lists the moves (then -1) for attn_pages_copy, for every layer's cache, before
+    the new table is used.
+    """
+    _check_int32("block_table", block_table, (None, None))
+    device = block_table.device
+    _check_int32("refs", refs, (None,), device)
+    B, M = block_table.shape
+    P = refs.shape[0]
+    lib = load_library()
+    n = ctypes.c_longlong(0)
+    _raise_if(lib.attn_pages_workspace(P, 0, ctypes.byref(n)), "attn_pages_workspace")
+    with _call_scope(device, stream) as handle:
+        table = torch.empty((B, M), dtype=torch.int32, device=device)
+        count = torch.empty(P, dtype=torch.int32, device=device)
+        src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=device).unbind()
+        num_live = torch.empty(1, dtype=torch.int32, device=device)
+        workspace = torch.empty(n.value, dtype=torch.int32, device=device)
+        st = lib.attn_pages_compact(block_table.data_ptr(), refs.data_ptr(), table.data_ptr(),
+                                    count.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                    num_live.data_ptr(), workspace.data_ptr(), B, M, P, handle)
+    _raise_if(st, "attn_pages_compact")
+    return table, count, src, dst, num_live
+
+
+def attn_pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor,
+                    dst: torch.Tensor, stream=None):
+    """Page dst[i] becomes page src[i], in place, in both caches of a layer
+    ([num_pages, ...], contiguous, of any one type); pairs of -1 are skipped.  No dst
+    may appear twice or as a src (the lists of attn_pages_fork and
+    attn_pages_compact never do)."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() >= 2
+               and t.numel() > 0, f"{name} must be a contiguous CUDA tensor [num_pages, ...]")
+    _check(k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
+           and k_cache.device == v_cache.device, "the caches must have one shape, type and device")
+    _check_int32("src", src, (None,), k_cache.device)
+    _check_int32("dst", dst, tuple(src.shape), k_cache.device)
+    lib = load_library()
+    num_pages = k_cache.shape[0]
+    page_bytes = k_cache.numel() // num_pages * k_cache.element_size()
+    with _call_scope(k_cache.device, stream) as handle:
+        st = lib.attn_pages_copy(k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(),
+                                 dst.data_ptr(), src.shape[0], num_pages, page_bytes, handle)
+    _raise_if(st, "attn_pages_copy")

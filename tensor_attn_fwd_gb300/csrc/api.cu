@@ -144,6 +144,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA: CUDA runtime error";
     case ATTN_ERR_TIMEOUT: return "ATTN_ERR_TIMEOUT: a kernel wait expired";
     case ATTN_ERR_BOUNDS: return "ATTN_ERR_BOUNDS: a kernel store fell outside its output (debug build)";
+    case ATTN_ERR_NO_PAGES: return "ATTN_ERR_NO_PAGES: no free pages left";
     default: return "unknown attn status";
   }
 }
@@ -640,6 +641,114 @@ int attn_combine(const float* o_part, const float* lse_part, float* o, float* ls
     return ATTN_ERR_MISALIGNED;
   const cudaError_t e = launch_combine(o_part, lse_part, o, lse, B * Hq, D, num_splits,
                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The checks that the page tables share; ATTN_OK or the status to return.
+int pages_check_args(const int* block_table, const int* refs, const int* block_table_out,
+                     const int* refs_out, int B, int max_pages, int num_pages, int page_size) {
+  if (!block_table || !refs || !block_table_out || !refs_out) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+  // Slots of the table are numbered, and keys counted, with int.
+  if (static_cast<long long>(B) * max_pages > (1ll << 31) - 1 ||
+      static_cast<long long>(max_pages) * page_size > kMaxSeq || num_pages > kMaxSeq)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(block_table) || !aligned4(refs) || !aligned4(block_table_out) ||
+      !aligned4(refs_out))
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int attn_pages_free(const int* block_table, const int* refs, const int* seqlens,
+                    int* block_table_out, int* refs_out, int B, int max_pages, int num_pages,
+                    int page_size, int window, int sinks, int room, void* stream) {
+  if (!seqlens || window < 1 || sinks < 0 || room < 0) return ATTN_ERR_INVALID_ARG;
+  const int chk = pages_check_args(block_table, refs, block_table_out, refs_out, B, max_pages,
+                                   num_pages, page_size);
+  if (chk != ATTN_OK) return chk;
+  if (!aligned4(seqlens)) return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  // Past the rows' capacity a window reaches every key: clamped, the sums fit int.
+  const cudaError_t e = launch_pages_free(
+      block_table, refs, seqlens, block_table_out, refs_out, B, max_pages, num_pages, page_size,
+      window < kMaxSeq ? window : kMaxSeq, sinks, room, static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_pages_fork(const int* block_table, const int* refs, const int* seqlens,
+                    const int* parents, int* block_table_out, int* refs_out, int* seqlens_out,
+                    int* src, int* dst, int* counts, int* workspace, int B, int R, int max_pages,
+                    int num_pages, int page_size, int room, void* stream) {
+  if (!seqlens || !parents || !seqlens_out || !src || !dst || !counts || !workspace)
+    return ATTN_ERR_INVALID_ARG;
+  if (R <= 0 || room < 0) return ATTN_ERR_INVALID_ARG;
+  const int chk = pages_check_args(block_table, refs, block_table_out, refs_out, B, max_pages,
+                                   num_pages, page_size);
+  if (chk != ATTN_OK) return chk;
+  if (static_cast<long long>(R) * max_pages > (1ll << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+  // The phases read their inputs after other CTAs have written outputs.
+  if (block_table_out == block_table || refs_out == refs || seqlens_out == seqlens ||
+      seqlens_out == parents || src == parents || dst == parents || src == dst)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(seqlens) || !aligned4(parents) || !aligned4(seqlens_out) || !aligned4(src) ||
+      !aligned4(dst) || !aligned4(counts) || !aligned4(workspace))
+    return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e = launch_pages_fork(
+      block_table, refs, seqlens, parents, block_table_out, refs_out, seqlens_out, src, dst, counts,
+      workspace, B, R, max_pages, num_pages, page_size, room, static_cast<cudaStream_t>(stream),
+      status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_pages_compact(const int* block_table, const int* refs, int* block_table_out,
+                       int* refs_out, int* src, int* dst, int* num_live, int* workspace, int B,
+                       int max_pages, int num_pages, void* stream) {
+  if (!num_live || !workspace || (num_pages > 1 && (!src || !dst))) return ATTN_ERR_INVALID_ARG;
+  const int chk = pages_check_args(block_table, refs, block_table_out, refs_out, B, max_pages,
+                                   num_pages, 1);
+  if (chk != ATTN_OK) return chk;
+  if (block_table_out == block_table || refs_out == refs || (src != nullptr && src == dst))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(src) || !aligned4(dst) || !aligned4(num_live) || !aligned4(workspace))
+    return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e = launch_pages_compact(
+      block_table, refs, block_table_out, refs_out, src, dst, num_live, workspace, B, max_pages,
+      num_pages, static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_pages_workspace(int num_pages, int R, long long* entries) {
+  if (entries == nullptr || num_pages < 1 || R < 0) return ATTN_ERR_INVALID_ARG;
+  *entries = pages_workspace(num_pages, R);
+  return ATTN_OK;
+}
+
+int attn_pages_copy(void* k_cache, void* v_cache, const int* src, const int* dst, int n,
+                    int num_pages, long long page_bytes, void* stream) {
+  if (!k_cache || !v_cache || n < 0 || num_pages <= 0 || page_bytes <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (n > 0 && (!src || !dst)) return ATTN_ERR_INVALID_ARG;
+  if (page_bytes % 16 != 0 || num_pages > kMaxSeq) return ATTN_ERR_UNSUPPORTED;
+  if (page_bytes > (2ll * kMaxElems) / num_pages) return ATTN_ERR_UNSUPPORTED;
+  if (page_bytes > (1ll << 40)) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(src) || !aligned4(dst))
+    return ATTN_ERR_MISALIGNED;
+  if (n == 0) return ATTN_OK;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e = launch_pages_copy(k_cache, v_cache, src, dst, n, num_pages, page_bytes,
+                                          static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -159,6 +159,26 @@ cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, 
                                    int D, int window, int sinks, float scale, cudaStream_t stream,
                                    int* status);
 
+// Page bookkeeping (pages.cu): P pages, a table of B rows x M slots.  Calls whose
+// largest array has at most kPagesClusterWork elements run as one cluster.
+constexpr int kPagesMaxCtas = 512;
+constexpr long long kPagesClusterWork = 1 << 16;
+// int32 workspace of launch_pages_fork (R new rows) and launch_pages_compact (R = 0).
+inline long long pages_workspace(int P, int R) { return 2ll * P + R + 2 * kPagesMaxCtas; }
+cudaError_t launch_pages_free(const int* table, const int* refs, const int* seqlens,
+                              int* table_out, int* refs_out, int B, int M, int P, int page_size,
+                              int window, int sinks, int room, cudaStream_t stream, int* status);
+cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seqlens,
+                              const int* parents, int* table_out, int* refs_out, int* seqlens_out,
+                              int* src, int* dst, int* counts, int* workspace, int B, int R, int M,
+                              int P, int page_size, int room, cudaStream_t stream, int* status);
+cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_out, int* refs_out,
+                                 int* src, int* dst, int* num_live, int* workspace, int B, int M,
+                                 int P, cudaStream_t stream, int* status);
+cudaError_t launch_pages_copy(void* k, void* v, const int* src, const int* dst, int n,
+                              int num_pages, long long page_bytes, cudaStream_t stream,
+                              int* status);
+
 // Backward: Delta into `delta` ([B,Hq,Sq]), then dK/dV and dQ kernels.
 cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const float* o,
                             const float* lse, const void* dout, float* dq, float* dk, float* dv,

@@ -1,0 +1,499 @@
+// pages.cu -- bookkeeping of a paged KV cache on the device: free, fork, compact,
+// and the page copies that fork and compact list.
+//
+// A block table [rows, max_pages] (int32) names the page of each slot of a row
+// (-1: none); refs[p] counts the holders of page p (0: free).  All results are
+// functions of the inputs alone: pages are handed out lowest id first, in the
+// order of (row, slot), and the atomics below add and take minima of integers, so
+// their order changes nothing.  The host never reads back, so the calls can be
+// captured in a graph between decode steps.
+//
+// Each operation is a few phases with a barrier between them, which every CTA
+// enters:
+//   free     1 copy refs              2 give up the references
+//   fork     1 copy refs, count free  2 count holders, list free pages, copy the
+//            read-only slots          3 count the pages each row needs
+//            4 hand them out
+//   compact  1 count live             2 list holes and movers   3 renumber
+// Bound: the bytes of the tables for large ones, latency for the usual few
+// thousand entries.  A small call is one launch of one cluster of 8 CTAs, whose
+// barrier is the hardware's; a large one launches one grid per phase (phases()).
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kClusterCtas = 8;
+
+__device__ __forceinline__ void record_status(int* status, int code) {
+  if (status != nullptr) atomicCAS(status, 0, code);
+}
+
+// This CTA's part [begin, end) of n things shared out over the grid.
+struct Part {
+  int begin, end;
+  __device__ __forceinline__ explicit Part(int n) {
+    const int chunk = (n + gridDim.x - 1) / gridDim.x;
+    begin = static_cast<int>(min(static_cast<long long>(blockIdx.x) * chunk, static_cast<long long>(n)));
+    end = min(begin + chunk, n);
+  }
+};
+
+// Sum of one value per thread over the CTA (kWarps warps); every thread gets it.
+__device__ __forceinline__ int block_sum(int x, int* smem) {
+  x = __reduce_add_sync(0xffffffffu, x);
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = x;
+  __syncthreads();
+  const int total = __reduce_add_sync(0xffffffffu, smem[threadIdx.x & 31]);
+  __syncthreads();
+  return total;
+}
+
+// Exclusive prefix sum of one value per thread over the CTA; total: their sum.
+__device__ __forceinline__ int block_scan(int x, int* smem, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) smem[warp] = incl;
+  __syncthreads();
+  int w = smem[lane], wincl = w;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, wincl, off);
+    if (lane >= off) wincl += y;
+  }
+  total = __shfl_sync(0xffffffffu, wincl, 31);
+  const int before = __shfl_sync(0xffffffffu, wincl - w, warp);
+  __syncthreads();
+  return before + incl - x;
+}
+
+// Sum of counts[0, n) by the whole CTA.
+__device__ __forceinline__ int sum_counts(const int* counts, int n, int* smem) {
+  int x = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) x += counts[i];
+  return block_sum(x, smem);
+}
+
+// A table entry: a page, or -1 (an entry that is neither is reported and read as -1).
+__device__ __forceinline__ int checked_entry(int e, int num_pages, int* status) {
+  if (e >= num_pages || e < -1) {
+    record_status(status, ATTN_ERR_INVALID_ARG);
+    return -1;
+  }
+  return e;
+}
+
+// The phases [first, last) with the grid's barrier between them: in a cluster
+// launch all of them and the cluster's barrier, else one phase a launch.
+template <typename Op>
+__global__ void __launch_bounds__(kThreads, 1) pages_kernel(const Op op, int first, int last) {
+  __shared__ int smem[32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int ph = first; ph < last; ++ph) {
+    op.run(ph, smem);
+    if (ph + 1 < last) cluster_sync();
+  }
+}
+
+// ------------------------------------------------------------------ free
+struct FreeOp {
+  static constexpr int kPhases = 2;
+  const int *table, *refs, *seqlens;
+  int *table_out, *refs_out;
+  int B, M, P, page_size, window, sinks, room;
+  int* status;
+
+  __device__ void run(int ph, int*) const {
+    const int tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+    if (ph == 0) {
+      if (refs != refs_out)
+        for (int p = tid; p < P; p += n_threads) refs_out[p] = refs[p];
+      return;
+    }
+    const unsigned entries = static_cast<unsigned>(B) * M;  // < 2^31: i cannot wrap
+    for (unsigned i = tid; i < entries; i += n_threads) {
+      const int b = i / static_cast<unsigned>(M), s = i - b * M;
+      const int e = checked_entry(table[i], P, status);
+      const int len = min(seqlens[b], M * page_size);
+      // A slot is kept when the row goes on and the slot holds a key that the next
+      // decode reads (the window of seqlens, the sinks) or that is still to come.
+      const int lo = s * page_size;
+      const bool keep = len >= 0 && lo < static_cast<long long>(len) + room &&
+                        (lo + page_size > len - window || lo < sinks);
+      if (!keep && e >= 0 && atomicSub(refs_out + e, 1) <= 0)
+        record_status(status, ATTN_ERR_INVALID_ARG);  // more holders than were counted
+      table_out[i] = keep ? e : -1;
+    }
+  }
+};
+
+// ------------------------------------------------------------------ fork
+struct ForkOp {
+  static constexpr int kPhases = 4;
+  const int *table, *refs, *seqlens, *parents;
+  int *table_out, *refs_out, *seqlens_out, *src, *dst, *counts;
+  int *lowest, *free_list, *need, *cta_free, *cta_need;  // workspace
+  int B, R, M, P, page_size, room;
+  int* status;
+
+  // New row r: its parent (-1: an empty row), length, and slots to be written [lo, hi).
+  struct Row {
+    int parent, len, lo, hi;
+  };
+  __device__ __forceinline__ Row row(int r) const {
+    Row x;
+    x.parent = parents[r];
+    if (x.parent >= B || x.parent < -1) {
+      record_status(status, ATTN_ERR_INVALID_ARG);
+      x.parent = -1;
+    }
+    x.len = x.parent < 0 ? 0 : min(max(seqlens[x.parent], 0), M * page_size);
+    x.lo = x.len / page_size;
+    const long long end = (static_cast<long long>(x.len) + room + page_size - 1) / page_size;
+    x.hi = x.parent < 0 ? 0 : static_cast<int>(min(end, static_cast<long long>(M)));
+    return x;
+  }
+  // A page of a slot to be written stays with the lowest (row, slot) that has it
+  // there, if nobody else holds it.  refs_out holds the other holders until phase 3,
+  // in which only that (row, slot) changes it.
+  __device__ __forceinline__ bool keeps(int e, int at) const {
+    return e >= 0 && lowest[e] == at && refs_out[e] == 0;
+  }
+
+  __device__ void run(int ph, int* smem) const {
+    const int tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Part pages(P), rows(R);
+    if (ph == 0) {
+      int n = 0;
+      for (int p = pages.begin + threadIdx.x; p < pages.end; p += kThreads) {
+        const int c = refs[p];
+        n += c == 0;
+        refs_out[p] = c;
+        lowest[p] = INT_MAX;
+      }
+      n = block_sum(n, smem);
+      if (threadIdx.x == 0) cta_free[blockIdx.x] = n;
+      for (int r = tid; r < R; r += n_threads) seqlens_out[r] = row(r).len;
+    } else if (ph == 1) {
+      // refs_out: the holders that are no slots of the old table ...
+      const unsigned entries = static_cast<unsigned>(B) * M, new_entries = static_cast<unsigned>(R) * M;
+      for (unsigned i = tid; i < entries; i += n_threads) {
+        const int e = checked_entry(table[i], P, status);
+        if (e >= 0) atomicSub(refs_out + e, 1);
+      }
+      // ... and the read-only slots of the new one.
+      for (unsigned i = tid; i < new_entries; i += n_threads) {
+        const int r = i / static_cast<unsigned>(M), s = i - r * M;
+        const Row x = row(r);
+        int e = -1;
+        if (s < x.hi || s < x.lo) e = checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, status);
+        if (s < x.lo) {
+          if (e >= 0) atomicAdd(refs_out + e, 1);
+        } else if (e >= 0) {
+          atomicMin(lowest + e, static_cast<int>(i));
+          e = -1;
+        }
+        table_out[i] = e;
+      }
+      int at = sum_counts(cta_free, blockIdx.x, smem);
+      for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads) {
+        const int p = p0 + threadIdx.x;
+        const int is_free = p < pages.end && refs[p] == 0;
+        int total;
+        const int k = at + block_scan(is_free, smem, total);
+        if (is_free) free_list[k] = p;
+        at += total;
+      }
+    } else if (ph == 2) {
+      // A warp per row: the pages it needs, then this CTA's rows' offsets.
+      for (int r = rows.begin + warp; r < rows.end; r += kWarps) {
+        const Row x = row(r);
+        int n = 0;
+        for (int s = x.lo + lane; s < x.hi; s += 32) {
+          const int e = checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, nullptr);
+          n += !keeps(e, r * M + s);
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) need[r] = n;
+      }
+      __syncthreads();
+      int at = 0;
+      for (int r0 = rows.begin; r0 < rows.end; r0 += kThreads) {
+        const int r = r0 + threadIdx.x;
+        const int n = r < rows.end ? need[r] : 0;
+        int total;
+        const int k = at + block_scan(n, smem, total);
+        if (r < rows.end) need[r] = k;
+        at += total;
+      }
+      if (threadIdx.x == 0) cta_need[blockIdx.x] = at;
+    } else {
+      const int n_free = sum_counts(cta_free, gridDim.x, smem);
+      const int base = sum_counts(cta_need, blockIdx.x, smem);
+      if (blockIdx.x == gridDim.x - 1) {
+        const int n = base + cta_need[blockIdx.x];
+        if (threadIdx.x == 0) {
+          counts[0] = n;
+          counts[1] = n_free;
+          if (n > n_free) record_status(status, ATTN_ERR_NO_PAGES);
+        }
+      }
+      for (int r = rows.begin + warp; r < rows.end; r += kWarps) {
+        const Row x = row(r);
+        int k = base + need[r];
+        int from = -1, to = -1;  // the row's copy: its first writable slot may hold keys
+        for (int s0 = x.lo; s0 < x.hi; s0 += 32) {
+          const int s = s0 + lane;
+          const bool mine = s < x.hi;
+          const int at = r * M + s;
+          const int e =
+              mine ? checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, nullptr) : -1;
+          const bool keep = mine && keeps(e, at);
+          const unsigned fresh = __ballot_sync(0xffffffffu, mine && !keep);
+          int page = e;
+          if (mine && !keep) {
+            const int mine_k = k + __popc(fresh & ((1u << lane) - 1u));
+            page = mine_k < n_free ? free_list[mine_k] : -1;
+            const bool holds_keys = s * page_size < x.len;
+            if (holds_keys && e >= 0 && page >= 0) {
+              from = e;
+              to = page;
+            }
+            // No page left: the row ends before the slot's keys.
+            if (holds_keys && page < 0) seqlens_out[r] = s * page_size;
+          }
+          if (mine) {
+            if (page >= 0) refs_out[page] = 1;
+            table_out[at] = page;
+          }
+          k += __popc(fresh);
+        }
+        // Only slot lo, lane 0's in the first round, can hold keys.
+        if (lane == 0) {
+          src[r] = from;
+          dst[r] = to;
+        }
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ compact
+struct CompactOp {
+  static constexpr int kPhases = 3;
+  const int *table, *refs;
+  int *table_out, *refs_out, *src, *dst, *num_live;
+  int *rank, *cta_live;  // workspace
+  int B, M, P;
+  int* status;
+
+  // Live pages in [begin, end), by the whole CTA.
+  __device__ __forceinline__ int live_in(int begin, int end, int* smem) const {
+    int n = 0;
+    for (int p = begin + threadIdx.x; p < end; p += kThreads) n += refs[p] > 0;
+    return block_sum(n, smem);
+  }
+  // Live pages below id n_live: those that stay.
+  __device__ __forceinline__ int staying(int n_live, int* smem) const {
+    const int chunk = (P + gridDim.x - 1) / gridDim.x;
+    const int cta = n_live / chunk;  // the CTA part that n_live lies in (or past the last)
+    return sum_counts(cta_live, min(cta, static_cast<int>(gridDim.x)), smem) +
+           live_in(min(cta * chunk, P), n_live, smem);
+  }
+
+  __device__ void run(int ph, int* smem) const {
+    const int tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+    const Part pages(P);
+    if (ph == 0) {
+      const int n = live_in(pages.begin, pages.end, smem);
+      if (threadIdx.x == 0) cta_live[blockIdx.x] = n;
+      return;
+    }
+    const int n_live = sum_counts(cta_live, gridDim.x, smem);
+    const int stay = staying(n_live, smem);
+    const int moves = n_live - stay;  // as many holes below n_live as live pages from it on
+    if (ph == 1) {
+      int before = sum_counts(cta_live, blockIdx.x, smem);
+      for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads) {
+        const int p = p0 + threadIdx.x;
+        const int c = p < pages.end ? refs[p] : 0;
+        int total;
+        const int k = before + block_scan(c > 0, smem, total);  // live pages below p
+        before += total;
+        if (p >= pages.end) continue;
+        if (p < n_live) {
+          if (c > 0)
+            refs_out[p] = c;
+          else
+            dst[p - k] = p;
+        } else {
+          refs_out[p] = 0;
+          if (c > 0) {
+            src[k - stay] = p;
+            rank[p] = k - stay;
+          }
+        }
+      }
+      for (int i = moves + tid; i < P / 2; i += n_threads) src[i] = dst[i] = -1;
+      if (tid == 0) *num_live = n_live;
+    } else {
+      for (int i = tid; i < moves; i += n_threads) refs_out[dst[i]] = refs[src[i]];
+      const unsigned entries = static_cast<unsigned>(B) * M;
+      for (unsigned i = tid; i < entries; i += n_threads) {
+        int e = checked_entry(table[i], P, status);
+        if (e >= 0 && refs[e] <= 0) {  // an entry of a page that counts no holder
+          record_status(status, ATTN_ERR_INVALID_ARG);
+          e = -1;
+        }
+        table_out[i] = e >= n_live ? dst[rank[e]] : e;
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ copies
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 8;  // 16-byte vectors a thread: 32 KB a CTA
+
+__global__ void __launch_bounds__(kCopyThreads)
+    pages_copy_kernel(uint4* k, uint4* v, const int* __restrict__ src, const int* __restrict__ dst,
+                      int num_pages, long long page_vecs, int chunks, int* status) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int pair = blockIdx.y;
+  const int from = __ldg(src + pair), to = __ldg(dst + pair);
+  if (from < 0 && to < 0) return;
+  if (from < 0 || to < 0 || from >= num_pages || to >= num_pages) {
+    if (threadIdx.x == 0) record_status(status, ATTN_ERR_INVALID_ARG);
+    return;
+  }
+  uint4* base = blockIdx.x < chunks ? k : v;
+  const long long c = static_cast<long long>(blockIdx.x % chunks) * (kCopyThreads * kCopyVecs);
+  const uint4* a = base + from * page_vecs;
+  uint4* b = base + to * page_vecs;
+  uint4 x[kCopyVecs];
+#pragma unroll
+  for (int i = 0; i < kCopyVecs; ++i) {
+    const long long at = c + i * kCopyThreads + threadIdx.x;
+    if (at < page_vecs) x[i] = a[at];
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyVecs; ++i) {
+    const long long at = c + i * kCopyThreads + threadIdx.x;
+    if (at < page_vecs) b[at] = x[i];
+  }
+}
+
+// ------------------------------------------------------------------ host side
+template <typename Op>
+cudaError_t launch(const Op& op, long long work, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kClusterCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  if (work <= kPagesClusterWork) {
+    cfg.gridDim = dim3(kClusterCtas, 1, 1);
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_kernel<Op>, op, 0, Op::kPhases);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  const long long ctas = (work + 4 * kThreads - 1) / (4 * kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < kPagesMaxCtas ? ctas : kPagesMaxCtas), 1, 1);
+  cfg.numAttrs = 1;
+  for (int ph = 0; ph < Op::kPhases; ++ph) {
+    cudaError_t e = cudaLaunchKernelEx(&cfg, pages_kernel<Op>, op, ph, ph + 1);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_pages_free(const int* table, const int* refs, const int* seqlens,
+                              int* table_out, int* refs_out, int B, int M, int P, int page_size,
+                              int window, int sinks, int room, cudaStream_t stream, int* status) {
+  const FreeOp op{table, refs, seqlens, table_out, refs_out, B,    M,
+                  P,     page_size, window, sinks, room, status};
+  const long long entries = static_cast<long long>(B) * M;
+  return launch(op, entries > P ? entries : P, stream);
+}
+
+cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seqlens,
+                              const int* parents, int* table_out, int* refs_out, int* seqlens_out,
+                              int* src, int* dst, int* counts, int* workspace, int B, int R, int M,
+                              int P, int page_size, int room, cudaStream_t stream, int* status) {
+  ForkOp op{table, refs, seqlens, parents, table_out, refs_out, seqlens_out, src, dst, counts};
+  op.lowest = workspace;
+  op.free_list = op.lowest + P;
+  op.cta_free = op.free_list + P;
+  op.cta_need = op.cta_free + kPagesMaxCtas;
+  op.need = op.cta_need + kPagesMaxCtas;
+  op.B = B;
+  op.R = R;
+  op.M = M;
+  op.P = P;
+  op.page_size = page_size;
+  op.room = room;
+  op.status = status;
+  const long long entries = static_cast<long long>(B > R ? B : R) * M;
+  return launch(op, entries > P ? entries : P, stream);
+}
+
+cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_out, int* refs_out,
+                                 int* src, int* dst, int* num_live, int* workspace, int B, int M,
+                                 int P, cudaStream_t stream, int* status) {
+  CompactOp op{table, refs, table_out, refs_out, src, dst, num_live};
+  op.rank = workspace;
+  op.cta_live = workspace + P;
+  op.B = B;
+  op.M = M;
+  op.P = P;
+  op.status = status;
+  const long long entries = static_cast<long long>(B) * M;
+  return launch(op, entries > P ? entries : P, stream);
+}
+
+cudaError_t launch_pages_copy(void* k, void* v, const int* src, const int* dst, int n,
+                              int num_pages, long long page_bytes, cudaStream_t stream,
+                              int* status) {
+  const long long vecs = page_bytes / 16;
+  const int chunks =
+      static_cast<int>((vecs + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs));
+  // At most 65535 pairs in the grid's y.
+  for (int at = 0; at < n; at += 65535) {
+    const int m = n - at < 65535 ? n - at : 65535;
+    const cudaError_t e = launch_programmatic(
+        pages_copy_kernel, dim3(2 * chunks, m, 1), dim3(kCopyThreads), 0, stream,
+        static_cast<uint4*>(k), static_cast<uint4*>(v), src + at, dst + at, num_pages, vecs, chunks,
+        status);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace attn
