@@ -32,8 +32,8 @@ Layouts: Q [B,Hq,Sq,D], K/V [B,Hkv,Sk,D] bf16; O [B,Hq,Sq,D], LSE [B,Hq,Sq] fp32
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -692,25 +692,71 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     return dq, dk, dv
 
 
-@contextlib.contextmanager
-def _call_scope(device: torch.device, stream):
-    """The device and stream of one call; yields the stream's handle.  What the call
-    allocates belongs to that stream, so freeing it cannot race with the kernels."""
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream().cuda_stream
-    else:
-        handle = _stream_handle(stream)
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-            yield handle
+# The calls below are often a few microseconds of GPU work: their checks build no
+# message and open no context unless they have to.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+class _Scope:
+    """The device and stream of one call: ``handle`` is the stream's.  What the call
+    allocates inside belongs to that stream, so freeing it cannot race with the
+    kernels.  The usual call, on the current stream of the tensors' own device,
+    changes nothing."""
+
+    __slots__ = ("handle", "_context")
+
+    def __init__(self, device: torch.device, stream):
+        self._context = None
+        if stream is not None:
+            self.handle = _stream_handle(stream)
+            self._context = torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=device))
+        else:
+            if torch.cuda.current_device() != device.index:
+                self._context = torch.cuda.device(device)
+            self.handle = (_raw_stream(device.index) if _raw_stream is not None
+                           else torch.cuda.current_stream(device).cuda_stream)
+
+    def __enter__(self):
+        if self._context is not None:
+            self._context.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self._context is not None:
+            self._context.__exit__(*exc)
+        return False
+
+
+def _check_inputs(device: torch.device, ndim: int, **tensors):
+    """bf16, CUDA, contiguous, ``ndim`` dims, on ``device``; raises ValueError."""
+    for name, t in tensors.items():
+        if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.dim() == ndim
+                and t.device == device and device.type == "cuda" and t.is_contiguous()):
+            _check_bf16(name, t, ndim)
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _device_of(q):
+    return q.device if isinstance(q, torch.Tensor) else None
 
 
 def _reach(window, sinks):
     """window and sinks as C ints; what exceeds every sequence means all keys."""
     window, sinks = int(window), int(sinks)
-    _check(window >= 1, "window must be at least 1")
-    _check(sinks >= 0, "sinks must not be negative")
+    if window < 1:
+        raise ValueError("window must be at least 1")
+    if sinks < 0:
+        raise ValueError("sinks must not be negative")
     return min(window, 1 << 30), min(sinks, 1 << 30)
+
+
+def _sizes(q, k, v):
+    """(B, Hq, Hkv, Sq, Sk, D) of q [B,Hq,Sq,D] and k, v [B,Hkv,Sk,D]."""
+    B, Hq, Sq, D = q.shape
+    Bk, Hkv, Sk, Dk = k.shape
+    if Bk != B or Dk != D or v.shape != k.shape:
+        raise ValueError("q/k/v shape mismatch")
+    return B, Hq, Hkv, Sq, Sk, D
 
 
 def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int,
@@ -721,23 +767,18 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
     q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64 or 128.  Row i stands
     at p = i + Sk - Sq and sees key j when j <= p and (j > p - window or j < sinks).
     """
-    _check_bf16("q", q, 4)
-    _check_bf16("k", k, 4)
-    _check_bf16("v", v, 4)
-    B, Hq, Sq, D = q.shape
-    Bk, Hkv, Sk, Dk = k.shape
-    _check(Bk == B and Dk == D and tuple(v.shape) == tuple(k.shape), "q/k/v shape mismatch")
-    _check(k.device == q.device and v.device == q.device, "q/k/v must share a device")
+    device = _device_of(q)
+    _check_inputs(device, 4, q=q, k=k, v=v)
+    B, Hq, Hkv, Sq, Sk, D = _sizes(q, k, v)
     window, sinks = _reach(window, sinks)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     lib = load_library()
-    with _call_scope(q.device, stream) as handle:
-        o = _out_bf16(o, (B, Hq, Sq, D), q.device, "o")
-        lse = _out(lse, (B, Hq, Sq), q.device, "lse")
+    with _Scope(device, stream) as handle:
+        o = _out_bf16(o, (B, Hq, Sq, D), device, "o")
+        lse = _out(lse, (B, Hq, Sq), device, "lse")
         st = lib.attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                 lse.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window, sinks,
-                                 float(scale), handle)
+                                 lse.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window, sinks, scale,
+                                 handle)
     _raise_if(st, "attn_window_fwd")
     return o, lse
 
@@ -752,85 +793,86 @@ def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
 
     o (bf16) and lse (fp32) are attn_window_fwd's results; dout is bf16 like q.
     """
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o), ("dout", dout)):
-        _check_bf16(name, t, 4)
-        _check(t.device == q.device, f"{name} must be on {q.device}")
-    B, Hq, Sq, D = q.shape
-    Bk, Hkv, Sk, Dk = k.shape
-    _check(Bk == B and Dk == D and tuple(v.shape) == tuple(k.shape), "q/k/v shape mismatch")
-    _check(tuple(dout.shape) == tuple(q.shape), "dout must match q")
-    _check(tuple(o.shape) == tuple(q.shape), "o must match q")
-    _check(isinstance(lse, torch.Tensor), "lse must be a torch.Tensor")
-    lse = _out(lse, (B, Hq, Sq), q.device, "lse")
+    device = _device_of(q)
+    _check_inputs(device, 4, q=q, k=k, v=v, o=o, dout=dout)
+    B, Hq, Hkv, Sq, Sk, D = _sizes(q, k, v)
+    if dout.shape != q.shape or o.shape != q.shape:
+        raise ValueError("dout and o must match q")
+    if not isinstance(lse, torch.Tensor):
+        raise ValueError("lse must be a torch.Tensor")
+    lse = _out(lse, (B, Hq, Sq), device, "lse")
     window, sinks = _reach(window, sinks)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     lib = load_library()
-    with _call_scope(q.device, stream) as handle:
-        dq = _out_bf16(dq, (B, Hq, Sq, D), q.device, "dq")
-        dk = _out_bf16(dk, (B, Hkv, Sk, D), q.device, "dk")
-        dv = _out_bf16(dv, (B, Hkv, Sk, D), q.device, "dv")
-        delta_ws = _out(delta_ws, (B, Hq, Sq), q.device, "delta_ws")
+    with _Scope(device, stream) as handle:
+        dq = _out_bf16(dq, (B, Hq, Sq, D), device, "dq")
+        dk = _out_bf16(dk, (B, Hkv, Sk, D), device, "dk")
+        dv = _out_bf16(dv, (B, Hkv, Sk, D), device, "dv")
+        delta_ws = _out(delta_ws, (B, Hq, Sq), device, "delta_ws")
         st = lib.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                  lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                  dv.data_ptr(), delta_ws.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
-                                 sinks, float(scale), handle)
+                                 sinks, scale, handle)
     _raise_if(st, "attn_window_bwd")
     return dq, dk, dv
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_splits(device_index: int, B: int, Hq: int, Hkv: int, keys: int, D: int) -> int:
+    """attn_decode_num_splits, a rule on the sizes alone, asked once per shape."""
+    return attn_decode_num_splits(B, Hq, Hkv, keys, D, device_index)
 
 
 def _decode_window(what, q, k, v, table, seqlens, Sk, window, sinks, num_splits, scale, workspace,
                    o, lse, counters, stream):
     """The two windowed decodes: ``table`` is None for a contiguous cache."""
-    B, Hq, _, D = q.shape
-    Hkv = k.shape[1]
+    B, Hq, Sq, D = q.shape
+    if Sq != 1:
+        raise ValueError("decode takes one query row per head (q.shape[2] == 1)")
+    device, Hkv = q.device, k.shape[1]
     if seqlens is not None:
-        _check(isinstance(seqlens, torch.Tensor) and seqlens.is_cuda
-               and seqlens.dtype == torch.int32 and seqlens.is_contiguous()
-               and tuple(seqlens.shape) == (B,) and seqlens.device == q.device,
-               "seqlens must be a contiguous int32 CUDA tensor of shape [B] on q's device")
+        _check_int32("seqlens", seqlens, (B,), device)
     window, sinks = _reach(window, sinks)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     lib = load_library()
-    n = _int(0)
-    with _call_scope(q.device, stream) as handle:
-        if num_splits is None:
-            _raise_if(lib.attn_decode_num_splits(B, Hq, Hkv, max(1, min(Sk, window + sinks)), D,
-                                                 ctypes.byref(n)), "attn_decode_num_splits")
-            num_splits = n.value
-        ns = int(num_splits)
-        o = _out_bf16(o, (B, Hq, D), q.device, "o")
-        lse = _out(lse, (B, Hq), q.device, "lse")
+    with _Scope(device, stream) as handle:
+        ns = (_decode_splits(device.index, B, Hq, Hkv, max(1, min(Sk, window + sinks)), D)
+              if num_splits is None else int(num_splits))
+        o = _out_bf16(o, (B, Hq, D), device, "o")
+        lse = _out(lse, (B, Hq), device, "lse")
         part = lse_part = count = None
-        if ns != 1:
-            part, lse_part = (None, None) if workspace is None else workspace
-            part = _out(part, (ns, B, Hq, D), q.device, "o_part")
-            lse_part = _out(lse_part, (ns, B, Hq), q.device, "lse_part")
-            _raise_if(lib.attn_decode_fused_counters(B, Hq, Hkv, ctypes.byref(n)),
-                      "attn_decode_fused_counters")
+        if ns > 1:
+            if workspace is None:
+                # One allocation: the partials, then their LSEs (D a multiple of 64).
+                workspace = torch.empty(ns * B * Hq * (D + 1), dtype=torch.float32, device=device)
+                part = workspace.data_ptr()
+                lse_part = part + 4 * ns * B * Hq * D
+            else:
+                part = _out(workspace[0], (ns, B, Hq, D), device, "o_part").data_ptr()
+                lse_part = _out(workspace[1], (ns, B, Hq), device, "lse_part").data_ptr()
+            n = B * Hkv * -(-Hq // (16 * Hkv)) if Hkv else 0  # attn_decode_fused_counters
             if counters is None:
                 # A captured call zeroes counters of its own on every replay: graphs that
                 # run at the same time must not share the stream's array.
-                counters = (torch.zeros(n.value, dtype=torch.int32, device=q.device)
+                counters = (torch.zeros(n, dtype=torch.int32, device=device)
                             if torch.cuda.is_current_stream_capturing()
-                            else _stream_counters(q.device, handle, n.value))
-            _check(isinstance(counters, torch.Tensor) and counters.is_cuda
-                   and counters.dtype == torch.int32 and counters.is_contiguous()
-                   and counters.numel() >= n.value and counters.device == q.device,
-                   f"counters must be a contiguous int32 CUDA tensor with >= {n.value} entries")
+                            else _stream_counters(device, handle, n))
+            elif not (isinstance(counters, torch.Tensor) and counters.dtype == torch.int32
+                      and counters.device == device and counters.is_contiguous()
+                      and counters.numel() >= n):
+                raise ValueError(f"counters must be a contiguous int32 CUDA tensor with >= {n} "
+                                 "entries on q's device")
             count = counters.data_ptr()
-        outs = (o.data_ptr(), lse.data_ptr(), part if part is None else part.data_ptr(),
-                lse_part if lse_part is None else lse_part.data_ptr(), count)
+        outs = (o.data_ptr(), lse.data_ptr(), part, lse_part, count)
         seq = None if seqlens is None else seqlens.data_ptr()
         if table is None:
             st = lib.attn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), seq, *outs, B,
-                                        Hq, Hkv, Sk, D, window, sinks, ns, float(scale), handle)
+                                        Hq, Hkv, Sk, D, window, sinks, ns, scale, handle)
         else:
             st = lib.attn_decode_window_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                               table.data_ptr(), seq, *outs, B, Hq, Hkv, k.shape[0],
                                               k.shape[2], table.shape[1], D, window, sinks, ns,
-                                              float(scale), handle)
+                                              scale, handle)
     _raise_if(st, what)
     return o, lse
 
@@ -848,14 +890,8 @@ def decode_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int
     attn_decode_num_splits for the keys seen; ``workspace`` and ``counters`` as
     attn_decode_fused (not used with one split).
     """
-    _check_bf16("q", q, 4)
-    _check_bf16("k", k, 4)
-    _check_bf16("v", v, 4)
-    B, Hq, Sq, D = q.shape
-    _check(Sq == 1, "decode takes one query row per head (q.shape[2] == 1)")
-    Bk, Hkv, Sk, Dk = k.shape
-    _check(Bk == B and Dk == D and tuple(v.shape) == tuple(k.shape), "q/k/v shape mismatch")
-    _check(k.device == q.device and v.device == q.device, "q/k/v must share a device")
+    _check_inputs(_device_of(q), 4, q=q, k=k, v=v)
+    Sk = _sizes(q, k, v)[4]
     return _decode_window("attn_decode_window", q, k, v, None, seqlens, Sk, window, sinks,
                           num_splits, scale, workspace, o, lse, counters, stream)
 
@@ -868,33 +904,26 @@ def decode_window_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     """decode_window over a paged cache (k_cache/v_cache [num_pages,Hkv,page_size,D],
     block_table int32 [B,max_pages], seqlens int32 [B], as decode_paged).  Entries of
     pages that hold no seen key are not read (attn_pages_free makes them -1)."""
-    _check_bf16("q", q, 4)
-    _check_bf16("k_cache", k_cache, 4)
-    _check_bf16("v_cache", v_cache, 4)
-    B, Hq, Sq, D = q.shape
-    _check(Sq == 1, "decode takes one query row per head (q.shape[2] == 1)")
-    num_pages, Hkv, page_size, Dk = k_cache.shape
-    _check(Dk == D and tuple(v_cache.shape) == tuple(k_cache.shape), "q/cache shape mismatch")
-    _check(isinstance(block_table, torch.Tensor) and block_table.is_cuda
-           and block_table.dtype == torch.int32 and block_table.is_contiguous()
-           and block_table.device == q.device and block_table.dim() == 2
-           and block_table.shape[0] == B,
-           "block_table must be a contiguous int32 tensor [B, max_pages] on q's device")
-    _check(seqlens is not None, "a paged cache needs seqlens")
-    _check(k_cache.device == q.device and v_cache.device == q.device,
-           "q and caches must share a device")
+    device = _device_of(q)
+    _check_inputs(device, 4, q=q, k_cache=k_cache, v_cache=v_cache)
+    if k_cache.shape[3] != q.shape[3] or v_cache.shape != k_cache.shape:
+        raise ValueError("q/cache shape mismatch")
+    _check_int32("block_table", block_table, (q.shape[0], None), device)
+    if seqlens is None:
+        raise ValueError("a paged cache needs seqlens")
     return _decode_window("attn_decode_window_paged", q, k_cache, v_cache, block_table, seqlens,
-                          block_table.shape[1] * page_size, window, sinks, num_splits, scale,
-                          workspace, o, lse, counters, stream)
+                          block_table.shape[1] * k_cache.shape[2], window, sinks, num_splits,
+                          scale, workspace, o, lse, counters, stream)
 
 
 def _check_int32(name: str, t: torch.Tensor, shape, device=None):
     """A contiguous int32 CUDA tensor; shape entries of None are free."""
-    _check(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
-           and t.is_contiguous() and (device is None or t.device == device),
-           f"{name} must be a contiguous int32 CUDA tensor on the table's device")
-    _check(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
-           f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
+            and t.is_contiguous() and (device is None or t.device == device)):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor"
+                         + (f" on {device}" if device is not None else ""))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _out_int32(t, shape, device, name):
@@ -902,6 +931,20 @@ def _out_int32(t, shape, device, name):
         return torch.empty(shape, dtype=torch.int32, device=device)
     _check_int32(name, t, shape, device)
     return t
+
+
+def _room(room) -> int:
+    room = int(room)
+    if room < 0:
+        raise ValueError("room must not be negative")
+    return min(room, 1 << 30)
+
+
+def _pages_workspace(num_pages: int, rows: int, device) -> torch.Tensor:
+    n = ctypes.c_longlong(0)
+    _raise_if(load_library().attn_pages_workspace(num_pages, rows, ctypes.byref(n)),
+              "attn_pages_workspace")
+    return torch.empty(n.value, dtype=torch.int32, device=device)
 
 
 def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,
@@ -921,14 +964,14 @@ def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     B, M = block_table.shape
     _check_int32("seqlens", seqlens, (B,), block_table.device)
     window, sinks = _reach(1 << 30 if window is None else window, sinks)
-    _check(int(room) >= 0, "room must not be negative")
+    room = _room(room)
     lib = load_library()
-    with _call_scope(block_table.device, stream) as handle:
+    with _Scope(block_table.device, stream) as handle:
         table = _out_int32(block_table_out, (B, M), block_table.device, "block_table_out")
         count = _out_int32(refs_out, (refs.shape[0],), block_table.device, "refs_out")
         st = lib.attn_pages_free(block_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
                                  table.data_ptr(), count.data_ptr(), B, M, refs.shape[0],
-                                 int(page_size), window, sinks, min(int(room), 1 << 30), handle)
+                                 int(page_size), window, sinks, room, handle)
     _raise_if(st, "attn_pages_free")
     return table, count
 
@@ -951,22 +994,21 @@ def attn_pages_fork(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     _check_int32("parents", parents, (None,), device)
     B, M = block_table.shape
     _check_int32("seqlens", seqlens, (B,), device)
-    _check(int(room) >= 0, "room must not be negative")
+    room = _room(room)
     R, P = parents.shape[0], refs.shape[0]
     lib = load_library()
-    n = ctypes.c_longlong(0)
-    _raise_if(lib.attn_pages_workspace(P, R, ctypes.byref(n)), "attn_pages_workspace")
-    with _call_scope(device, stream) as handle:
-        table = torch.empty((R, M), dtype=torch.int32, device=device)
-        count = torch.empty(P, dtype=torch.int32, device=device)
-        lens, src, dst = torch.empty((3, R), dtype=torch.int32, device=device).unbind()
-        counts = torch.empty(2, dtype=torch.int32, device=device)
-        workspace = torch.empty(n.value, dtype=torch.int32, device=device)
+    with _Scope(device, stream) as handle:
+        workspace = _pages_workspace(P, R, device)
+        # The results share one allocation.
+        table, count, lens, src, dst, counts = torch.empty(
+            R * M + P + 3 * R + 2, dtype=torch.int32, device=device).split_with_sizes(
+                (R * M, P, R, R, R, 2))
+        table = table.view(R, M)
         st = lib.attn_pages_fork(block_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
                                  parents.data_ptr(), table.data_ptr(), count.data_ptr(),
                                  lens.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                  counts.data_ptr(), workspace.data_ptr(), B, R, M, P,
-                                 int(page_size), min(int(room), 1 << 30), handle)
+                                 int(page_size), room, handle)
     _raise_if(st, "attn_pages_fork")
     return table, count, lens, src, dst, counts
 
@@ -985,14 +1027,14 @@ def attn_pages_compact(block_table: torch.Tensor, refs: torch.Tensor, stream=Non
     B, M = block_table.shape
     P = refs.shape[0]
     lib = load_library()
-    n = ctypes.c_longlong(0)
-    _raise_if(lib.attn_pages_workspace(P, 0, ctypes.byref(n)), "attn_pages_workspace")
-    with _call_scope(device, stream) as handle:
-        table = torch.empty((B, M), dtype=torch.int32, device=device)
-        count = torch.empty(P, dtype=torch.int32, device=device)
-        src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=device).unbind()
-        num_live = torch.empty(1, dtype=torch.int32, device=device)
-        workspace = torch.empty(n.value, dtype=torch.int32, device=device)
+    half = P // 2
+    with _Scope(device, stream) as handle:
+        workspace = _pages_workspace(P, 0, device)
+        # The results share one allocation.
+        table, count, src, dst, num_live = torch.empty(
+            B * M + P + 2 * half + 1, dtype=torch.int32, device=device).split_with_sizes(
+                (B * M, P, half, half, 1))
+        table = table.view(B, M)
         st = lib.attn_pages_compact(block_table.data_ptr(), refs.data_ptr(), table.data_ptr(),
                                     count.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                     num_live.data_ptr(), workspace.data_ptr(), B, M, P, handle)
@@ -1007,16 +1049,18 @@ def attn_pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Ten
     may appear twice or as a src (the lists of attn_pages_fork and
     attn_pages_compact never do)."""
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() >= 2
-               and t.numel() > 0, f"{name} must be a contiguous CUDA tensor [num_pages, ...]")
-    _check(k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
-           and k_cache.device == v_cache.device, "the caches must have one shape, type and device")
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() >= 2
+                and t.numel() > 0):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [num_pages, ...]")
+    if (k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype
+            or k_cache.device != v_cache.device):
+        raise ValueError("the caches must have one shape, type and device")
     _check_int32("src", src, (None,), k_cache.device)
     _check_int32("dst", dst, tuple(src.shape), k_cache.device)
     lib = load_library()
     num_pages = k_cache.shape[0]
     page_bytes = k_cache.numel() // num_pages * k_cache.element_size()
-    with _call_scope(k_cache.device, stream) as handle:
+    with _Scope(k_cache.device, stream) as handle:
         st = lib.attn_pages_copy(k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(),
                                  dst.data_ptr(), src.shape[0], num_pages, page_bytes, handle)
     _raise_if(st, "attn_pages_copy")

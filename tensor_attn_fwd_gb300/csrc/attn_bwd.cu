@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const int c = 2 * half + cc;
+        const uint32_t bits = WIN ? window_bits(c_lo - 32 * c, c_hi - 32 * c, 0) : 0u;
         uint32_t sr[32];
         tmem_ld32(tmem + lane_addr + C::kColS + 32 * c, sr);
         uint32_t pk[16];
@@ -524,7 +525,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             float pu = ex2(x[u]);
             if (need_mask) {
               const int col = 32 * c + e + u;
-              pu = (col >= c_lo && col < c_hi) ? pu : 0.f;
+              if constexpr (WIN)
+                pu = (bits >> (e + u) & 1u) ? pu : 0.f;
+              else
+                pu = (col >= c_lo && col < c_hi) ? pu : 0.f;
             }
             pv[32 * cc + e + u] = pu;
           }
@@ -896,6 +900,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int n_sink = p.sinks - key0, n_skip = win_lo - key0;
         const bool need_mask =
             __any_sync(0xffffffffu, n_vis < 64 || (WIN && n_skip > 0 && n_sink < 64));
+        uint32_t bits[2] = {0u, 0u};
+        if constexpr (WIN) {
+          bits[0] = window_bits(n_skip, n_vis, n_sink);
+          bits[1] = window_bits(n_skip - 32, n_vis - 32, n_sink - 32);
+        }
         float pv[64];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
@@ -904,8 +913,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     x0, x1);
           float p0 = ex2(x0), p1 = ex2(x1);
           if (need_mask) {
-            p0 = e < n_vis && (!WIN || e < n_sink || e >= n_skip) ? p0 : 0.f;
-            p1 = e + 1 < n_vis && (!WIN || e + 1 < n_sink || e + 1 >= n_skip) ? p1 : 0.f;
+            if constexpr (WIN) {
+              p0 = (bits[e >> 5] >> (e & 31) & 1u) ? p0 : 0.f;
+              p1 = (bits[e >> 5] >> ((e & 31) + 1) & 1u) ? p1 : 0.f;
+            } else {
+              p0 = e < n_vis ? p0 : 0.f;
+              p1 = e + 1 < n_vis ? p1 : 0.f;
+            }
           }
           pv[e] = p0;
           pv[e + 1] = p1;

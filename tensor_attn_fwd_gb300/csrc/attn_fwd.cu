@@ -588,11 +588,28 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
       const int key0 = j * 128;
       const bool need_mask = __any_sync(
           0xffffffffu, key0 + 127 > limit || (WIN && key0 < win_lo && key0 + 127 >= p.sinks));
-      if (need_mask) {
+      // Windowed: columns [64h, 64h + 64) of the step, 32 at a time; those that every
+      // row of the warp sees are left alone.
+      auto mask_half = [&](uint32_t(&x)[64], int h) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (key0 + c > limit || (WIN && key0 + c < win_lo && key0 + c >= p.sinks))
-            sa[c] = __float_as_uint(-INFINITY);
+        for (int g = 0; g < 2; ++g) {
+          const int k0 = key0 + 64 * h + 32 * g;
+          const uint32_t bits = window_bits(win_lo - k0, limit + 1 - k0, p.sinks - k0);
+          if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(bits >> c & 1u)) x[32 * g + c] = __float_as_uint(-INFINITY);
+          }
+        }
+      };
+      if (need_mask) {
+        if constexpr (WIN) {
+          mask_half(sa, 0);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (key0 + c > limit) sa[c] = __float_as_uint(-INFINITY);
+        }
       }
       // Row maximum: 4 independent chains of 3-input max.
       float ch[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -603,10 +620,13 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
           ch[e] = max3(ch[e], __uint_as_float(sa[c + e]), __uint_as_float(sa[c + 4 + e]));
       tmem_ld_wait64(sb);
       if (need_mask) {
+        if constexpr (WIN) {
+          mask_half(sb, 1);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (key0 + 64 + c > limit || (WIN && key0 + 64 + c < win_lo && key0 + 64 + c >= p.sinks))
-            sb[c] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < 64; ++c)
+            if (key0 + 64 + c > limit) sb[c] = __float_as_uint(-INFINITY);
+        }
       }
 #pragma unroll
       for (int c = 0; c < 64; c += 8)

@@ -6,6 +6,8 @@
 // below leaves the range of int (sequences are at most 2^30 long).
 #pragma once
 
+#include <cstdint>
+
 namespace attn {
 
 // KV tiles [0, s) and [w, e) with s <= w < e, or none (e = 0).  The window part of
@@ -30,6 +32,17 @@ __device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window,
   r.w = max(row_first + Sk - Sq - window + 1, 0) / 128;
   r.s = min((min(sinks, hi) + 127) / 128, r.w);
   return r;
+}
+
+// Masks of 32 columns as bits: one test per column, where the comparisons of the
+// visibility rule cost several instructions each (a masked 128-key step of the
+// forward took 3.4 us with them).
+__device__ __forceinline__ uint32_t bits_below(int n) {  // bits [0, n), n clamped to [0, 32]
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+// Bits [lo, hi), and of those below lo the first `sinks`.
+__device__ __forceinline__ uint32_t window_bits(int lo, int hi, int sinks) {
+  return bits_below(hi) & (~bits_below(lo) | bits_below(sinks));
 }
 
 // Query tiles [m0, m1) of 128 rows that see a key of key tile n (m1 <= m0: none):
