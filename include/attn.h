@@ -371,13 +371,20 @@ ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *
  *   dq [B,Hq,Sq,D], dk, dv [B,Hkv,Sk,D]   bf16 outputs, summed in fp32 (dK and dV
  *      over the query heads of the KV head too) and rounded once; keys that no row
  *      sees, and rows that see no key, get 0
- *   delta_ws [B,Hq,Sq] fp32               caller-owned workspace
+ *   workspace: attn_window_bwd_workspace floats, caller-owned, contents undefined
+ *      (Delta, and partial sums of the key tiles that hold sinks: every later row
+ *      sees those, so their work is split and added up in a fixed order)
  *   Same arguments and errors as attn_window_fwd; all pointers 16-byte aligned.
  */
 ATTN_API int attn_window_bwd(const void *q, const void *k, const void *v, const void *o,
                              const float *lse, const void *dout, void *dq, void *dk, void *dv,
-                             float *delta_ws, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                             float *workspace, int B, int Hq, int Hkv, int Sq, int Sk, int D,
                              int window, int sinks, float scale, void *stream);
+
+/* Floats of workspace for attn_window_bwd on the current device.  Host-only.
+ * ATTN_ERR_INVALID_ARG and ATTN_ERR_UNSUPPORTED as attn_window_bwd. */
+ATTN_API int attn_window_bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                                       int sinks, long long *floats);
 
 /*
  * Decode with a sliding window and sinks, in one launch: the query of sequence b

@@ -91,6 +91,7 @@ _SIGNATURES = {
     "attn_bwd": ([_vp] * 10 + [_int] * 7 + [_flt, _vp], _int),
     "attn_window_fwd": ([_vp] * 5 + [_int] * 8 + [_flt, _vp], _int),
     "attn_window_bwd": ([_vp] * 10 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_window_bwd_workspace": ([_int] * 8 + [ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_decode_window": ([_vp] * 9 + [_int] * 8 + [_flt, _vp], _int),
     "attn_decode_window_paged": ([_vp] * 10 + [_int] * 10 + [_flt, _vp], _int),
     "attn_pages_free": ([_vp] * 5 + [_int] * 7 + [_vp], _int),
@@ -787,11 +788,13 @@ def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
                     lse: torch.Tensor, dout: torch.Tensor, window: int, sinks: int = 0,
                     scale: float | None = None, dq: torch.Tensor | None = None,
                     dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
-                    delta_ws: torch.Tensor | None = None, stream=None):
+                    workspace: torch.Tensor | None = None, stream=None):
     """Gradients of sum(dout * O) for O = attn_window_fwd(q, k, v, window, sinks):
     returns (dq, dk, dv) bf16, summed in fp32 and rounded once.
 
     o (bf16) and lse (fp32) are attn_window_fwd's results; dout is bf16 like q.
+    ``workspace`` is an optional fp32 CUDA tensor of at least
+    attn_window_bwd_workspace floats (include/attn.h).
     """
     device = _device_of(q)
     _check_inputs(device, 4, q=q, k=k, v=v, o=o, dout=dout)
@@ -808,10 +811,19 @@ def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
         dq = _out_bf16(dq, (B, Hq, Sq, D), device, "dq")
         dk = _out_bf16(dk, (B, Hkv, Sk, D), device, "dk")
         dv = _out_bf16(dv, (B, Hkv, Sk, D), device, "dv")
-        delta_ws = _out(delta_ws, (B, Hq, Sq), device, "delta_ws")
+        n = ctypes.c_longlong(0)
+        _raise_if(lib.attn_window_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks,
+                                                ctypes.byref(n)), "attn_window_bwd_workspace")
+        if workspace is None:
+            workspace = torch.empty(n.value, dtype=torch.float32, device=device)
+        elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.float32
+                  and workspace.device == device and workspace.is_contiguous()
+                  and workspace.numel() >= n.value):
+            raise ValueError(f"workspace must be a contiguous float32 tensor on {device} with at "
+                             f"least {n.value} entries")
         st = lib.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                  lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                 dv.data_ptr(), delta_ws.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
+                                 dv.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
                                  sinks, scale, handle)
     _raise_if(st, "attn_window_bwd")
     return dq, dk, dv

@@ -535,19 +535,33 @@ int attn_bwd(const void* q, const void* k, const void* v, const float* o, const 
 }
 
 int attn_window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                    const void* dout, void* dq, void* dk, void* dv, float* delta_ws, int B, int Hq,
-                    int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                    const void* dout, void* dq, void* dk, void* dv, float* workspace, int B,
+                    int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
                     void* stream) {
   if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
-  const int chk = bwd_check_args(q, k, v, o, lse, dout, dq, dk, dv, delta_ws, B, Hq, Hkv, Sq, Sk,
+  const int chk = bwd_check_args(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, Sq, Sk,
                                  D, 1, scale);
   if (chk != ATTN_OK) return chk;
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
   const cudaError_t e = launch_attn_window_bwd(
-      q, k, v, o, lse, dout, dq, dk, dv, delta_ws, B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
-      sinks < Sk ? sinks : Sk, scale, static_cast<cudaStream_t>(stream), status);
+      q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, Sq, Sk, D,
+      window < Sk ? window : Sk, sinks < Sk ? sinks : Sk, scale, static_cast<cudaStream_t>(stream),
+      status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_window_bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                              long long* floats) {
+  if (floats == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0 ||
+      window < 1 || sinks < 0 || Hq % Hkv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Sq > kMaxSeq || Sk > kMaxSeq || static_cast<long long>(B) * Hq > (1ll << 30))
+    return ATTN_ERR_UNSUPPORTED;
+  *floats = window_bwd_workspace_floats(B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
+                                        sinks < Sk ? sinks : Sk);
+  return ATTN_OK;
 }
 
 int attn_rope_table(float* table, int max_pos, int D, float base, void* stream) {

@@ -44,7 +44,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -113,6 +112,12 @@ struct BwdParams {
   // Windowed kernels: the visibility of window.cuh, and bf16 gradients (out0, out1
   // point at bf16).
   int window, sinks;
+  // Windowed dK/dV: the first split_tiles key tiles (those with sinks, which every
+  // later row sees) are cut along their steps into `parts` CTAs each.  Part i of
+  // such a tile writes fp32 partials, [part][tile][B * Hkv][128][D], dK's then dV's,
+  // to `partials`; bwd_sum_parts_kernel adds them in order.
+  int split_tiles, parts;
+  float* partials;
 };
 
 // Read-only global load issued where it stands in the program.
@@ -175,25 +180,55 @@ __device__ __forceinline__ int kv_tiles_for(const BwdParams& p, int m) {
 }
 
 // ------------------------------------------------------------------ Delta
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-template <int D, typename TO>
+template <int D>
 __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16* __restrict__ dout,
-                                                        const TO* __restrict__ o,
+                                                        const float* __restrict__ o,
                                                         float* __restrict__ delta, int rows) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   constexpr int DPL = D / 32;
   const __nv_bfloat16* dr = dout + static_cast<size_t>(row) * D + lane * DPL;
-  const TO* orow = o + static_cast<size_t>(row) * D + lane * DPL;
+  const float* orow = o + static_cast<size_t>(row) * D + lane * DPL;
   float acc = 0.f;
 #pragma unroll
-  for (int e = 0; e < DPL; ++e) acc = fmaf(__bfloat162float(dr[e]), to_f32(orow[e]), acc);
+  for (int e = 0; e < DPL; ++e) acc = fmaf(__bfloat162float(dr[e]), orow[e], acc);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (lane == 0) delta[row] = acc;
+}
+
+// Delta for a bf16 O: D / 8 lanes a row, each one 16-byte load of O and of dO for
+// four rows at a time (bound by the two reads).
+constexpr int kDeltaRows = 4;
+template <int D>
+__global__ void __launch_bounds__(256)
+    window_delta_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ o,
+                        float* __restrict__ delta, int rows) {
+  constexpr int L = D / 8;  // lanes a row
+  const int lane = threadIdx.x % L;
+  const int row0 = blockIdx.x * (256 / L) * kDeltaRows + threadIdx.x / L;
+  uint4 a[kDeltaRows], b[kDeltaRows];
+#pragma unroll
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const int row = min(row0 + i * (256 / L), rows - 1);
+    a[i] = __ldg(dout + static_cast<size_t>(row) * L + lane);
+    b[i] = __ldg(o + static_cast<size_t>(row) * L + lane);
+  }
+#pragma unroll
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    float acc = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // a bf16 is the upper half of its float
+      acc = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), acc);
+      acc = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), acc);
+    }
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    const int row = row0 + i * (256 / L);
+    if (lane == 0 && row < rows) delta[row] = acc;
+  }
 }
 
 // ------------------------------------------------------------------ shared pieces
@@ -328,8 +363,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   // Work: key tile n of KV head (b, g); CTAs are numbered n-major so the
   // largest work (low n under a causal mask) is scheduled first.
-  const int n = blockIdx.x / (p.B * p.Hkv);
-  const int bg = blockIdx.x % (p.B * p.Hkv);
+  const int BH = p.B * p.Hkv;
+  int n = blockIdx.x / BH;
+  const int bg = blockIdx.x % BH;
+  int part = -1;  // windowed: this CTA's part of a split tile
+  if constexpr (WIN) {
+    if (n < p.split_tiles * p.parts) {
+      part = n % p.parts;
+      n /= p.parts;
+    } else {
+      n -= p.split_tiles * (p.parts - 1);
+    }
+  }
   const int b = bg / p.Hkv, g = bg % p.Hkv;
   const int group = p.Hq / p.Hkv;
   const int mtiles = (p.Sq + 127) / 128;
@@ -340,7 +385,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     m0 = qr.m0;
     per_head = max(qr.m1 - qr.m0, 0);
   }
-  const int nsteps = group * per_head;
+  int nsteps = group * per_head;
+  int s_base = 0;  // first of the tile's steps that this CTA takes
+  if constexpr (WIN) {
+    if (part >= 0) {
+      const int chunk = (nsteps + p.parts - 1) / p.parts;
+      s_base = min(part * chunk, nsteps);
+      nsteps = min(chunk, nsteps - s_base);
+    }
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->fixed_full, 1);
@@ -379,8 +432,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int st = s % kStages;
         bool good = true;
         if (s >= kStages) good = bwd_wait(&bars->empty[st], ((s / kStages) - 1) & 1, bars);
-        const int h = g * group + s / per_head;
-        const int m = m0 + s % per_head;
+        const int h = g * group + (s_base + s) / per_head;
+        const int m = m0 + (s_base + s) % per_head;
         uint8_t* dst = sRing + st * 2 * C::kTile;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars->full[st], 2 * C::kTile);
@@ -461,8 +514,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // row Sq - 1 (in bounds) and are zeroed when staged.
     float pre_l[2] = {0.f, 0.f}, pre_d[2] = {0.f, 0.f};
     auto fetch = [&](int s) {
-      const int h = g * group + s / per_head;
-      const int m = m0 + s % per_head;
+      const int h = g * group + (s_base + s) / per_head;
+      const int m = m0 + (s_base + s) % per_head;
       const size_t base = static_cast<size_t>(b * p.Hq + h) * p.Sq;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -473,7 +526,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     };
     if (nsteps > 0) fetch(0);
     for (int s = 0; s < nsteps && ok; ++s) {
-      const int m = m0 + s % per_head;
+      const int m = m0 + (s_base + s) % per_head;
       // This step's -LSE (log2 domain) and -Delta for the warpgroup's 64
       // columns, in the warp's own buffer (no cross-warp barrier, so an
       // aborting warp cannot strand others); read back as broadcast float4.
@@ -580,7 +633,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if constexpr (WIN) {
         __nv_bfloat16* dk16 = reinterpret_cast<__nv_bfloat16*>(p.out0) + kv_row;
         __nv_bfloat16* dv16 = reinterpret_cast<__nv_bfloat16*>(p.out1) + kv_row;
-        if (nsteps == 0) {
+        if (part >= 0) {
+          // Partials of every row of the tile (those past Sk are never read).
+          const size_t plane = static_cast<size_t>(p.split_tiles) * BH * 128 * D;
+          const size_t part_bytes = 2 * p.parts * plane * sizeof(float);
+          float* dk_part = p.partials + part * plane +
+                           (static_cast<size_t>(n * BH + bg) * 128 + r) * D;
+          float* dv_part = dk_part + p.parts * plane;
+          if (nsteps == 0) {
+            for (int c = half * D / 2; c < (half + 1) * D / 2; c += 4) {
+              *reinterpret_cast<float4*>(dk_part + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+              *reinterpret_cast<float4*>(dv_part + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          } else {
+            ok = __all_sync(0xffffffffu, bwd_wait(&bars->acc_full, 0, bars));
+            if (ok) {
+              tc_fence_after();
+              store_acc_row<D>(tmem + lane_addr + C::kColA0, dk_part, p.scale, true, half * D / 2,
+                               (half + 1) * D / 2, lane, p.partials, part_bytes, p.status);
+              store_acc_row<D>(tmem + lane_addr + C::kColA1, dv_part, 1.f, true, half * D / 2,
+                               (half + 1) * D / 2, lane, p.partials, part_bytes, p.status);
+            }
+          }
+        } else if (nsteps == 0) {
           if (key_valid && store_in_bounds(dk16, D * 2, p.out0, kv_bytes, p.status) &&
               store_in_bounds(dv16, D * 2, p.out1, kv_bytes, p.status)) {
             for (int c = half * D / 2; c < (half + 1) * D / 2; c += 8) {
@@ -627,6 +702,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// dK and dV of the split key tiles: the sum of their parts, in order, rounded once.
+// A thread per four dims of a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+    bwd_sum_parts_kernel(const float* __restrict__ partials, __nv_bfloat16* __restrict__ dk,
+                         __nv_bfloat16* __restrict__ dv, int split_tiles, int parts, int BH,
+                         int Sk) {
+  const size_t plane = static_cast<size_t>(split_tiles) * BH * 128 * D;
+  const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int row = static_cast<int>(at / D);  // (tile * BH + bg) * 128 + key of the tile
+  const int tile = row / (128 * BH), bg = (row / 128) % BH;
+  const int key = 128 * tile + (row & 127);
+  if (at >= plane || key >= Sk) return;
+  const size_t to = (static_cast<size_t>(bg) * Sk + key) * D + at % D;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float* src = partials + i * parts * plane + at;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < parts; ++q) {
+      const float4 y = *reinterpret_cast<const float4*>(src + q * plane);
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+    *reinterpret_cast<uint2*>((i ? dv : dk) + to) =
+        make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   }
 }
 
@@ -978,17 +1083,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
-// o, dq, dk and dv are fp32, or bf16 in the windowed form (window > 0).
+// The sink tiles' parts (see BwdParams).  A key tile with sinks is seen by every
+// later row, group * ceil(Sq/128) steps, where the others take about group *
+// (window/128 + 2): on one CTA it outlasts all of them (8192 rows, window 1024, 32/8
+// heads: 432 us for dK/dV, of which 0.4 of the CTAs' time was idle).  It is cut into
+// parts of at least a common tile's steps and half an SM's share of all steps, below
+// which finer parts balance no better.  At most 32 (the sum's loop).
+struct SinkSplit {
+  int tiles, parts;
+};
+SinkSplit sink_split(int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks) {
+  const long long mtiles = (Sq + 127) / 128, ntiles = (Sk + 127) / 128;
+  const long long tiles = (sinks + 127) / 128;
+  const long long reach = window / 128 + 2;
+  const long long common = reach < mtiles ? reach : mtiles, group = Hq / Hkv;
+  const long long share =
+      group * B * Hkv * ((ntiles - tiles) * common + tiles * mtiles) / (2 * sm_count());
+  const long long least = group * common > share ? group * common : share;
+  const long long parts = tiles == 0 ? 1 : (group * mtiles + least - 1) / least;
+  if (parts <= 1) return {0, 1};
+  return {static_cast<int>(tiles), static_cast<int>(parts < 32 ? parts : 32)};
+}
+
+// o, dq, dk and dv are fp32, or bf16 in the windowed form (window > 0), whose
+// `delta` is followed by the partials of the split sink tiles.
 template <int D, bool WIN>
 cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const void* o,
                             const float* lse, const void* dout, void* dq, void* dk, void* dv,
                             float* delta, int B, int Hq, int Hkv, int Sq, int Sk, int causal,
                             int window, int sinks, float scale, cudaStream_t stream, int* status) {
   using C = BwdCfg<D>;
-  using TO = std::conditional_t<WIN, __nv_bfloat16, float>;
   const int rows = B * Hq * Sq;
-  bwd_delta_kernel<D, TO><<<(rows + 7) / 8, 256, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(dout), static_cast<const TO*>(o), delta, rows);
+  if constexpr (WIN) {
+    const int per_cta = 256 / (D / 8) * kDeltaRows;
+    window_delta_kernel<D><<<(rows + per_cta - 1) / per_cta, 256, 0, stream>>>(
+        static_cast<const uint4*>(dout), static_cast<const uint4*>(o), delta, rows);
+  } else {
+    bwd_delta_kernel<D><<<(rows + 7) / 8, 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(dout), static_cast<const float*>(o), delta, rows);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   CUtensorMap tmQ, tmK, tmV, tmDO;
@@ -1019,9 +1152,27 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
   p.sinks = sinks;
   p.out0 = static_cast<float*>(dk);
   p.out1 = static_cast<float*>(dv);
-  const int kv_ctas = B * Hkv * ((Sk + 127) / 128);
+  p.split_tiles = 0;
+  p.parts = 1;
+  p.partials = nullptr;
+  if constexpr (WIN) {
+    const SinkSplit split = sink_split(B, Hq, Hkv, Sq, Sk, window, sinks);
+    p.split_tiles = split.tiles;
+    p.parts = split.parts;
+    p.partials = delta + window_bwd_delta_floats(B, Hq, Sq);
+  }
+  const int kv_ctas = B * Hkv * ((Sk + 127) / 128 + p.split_tiles * (p.parts - 1));
   bwd_dkdv_kernel<D, WIN><<<kv_ctas, kBwdThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, tmDO, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if constexpr (WIN) {
+    if (p.split_tiles > 0) {
+      const size_t vecs = static_cast<size_t>(p.split_tiles) * B * Hkv * 128 * (D / 4);
+      bwd_sum_parts_kernel<D><<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(
+          p.partials, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
+          p.split_tiles, p.parts, B * Hkv, Sk);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  }
   p.out0 = static_cast<float*>(dq);
   p.out1 = nullptr;
   const int q_tiles = B * Hq * ((Sq + 127) / 128);
@@ -1041,6 +1192,13 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const f
                                        Sk, causal, 0, 0, scale, stream, status);
   return launch_bwd_impl<64, false>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
                                     causal, 0, 0, scale, stream, status);
+}
+
+long long window_bwd_workspace_floats(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                                      int sinks) {
+  const SinkSplit split = sink_split(B, Hq, Hkv, Sq, Sk, window, sinks);
+  return window_bwd_delta_floats(B, Hq, Sq) +
+         2ll * split.tiles * split.parts * B * Hkv * 128 * D;
 }
 
 cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, const void* o,

@@ -159,6 +159,14 @@ cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, 
                                    int D, int window, int sinks, float scale, cudaStream_t stream,
                                    int* status);
 
+// The backward's workspace in floats: Delta [B,Hq,Sq] rounded up to 32 bytes, then
+// the partial dK and dV of the sink tiles that are split.
+inline long long window_bwd_delta_floats(int B, int Hq, int Sq) {
+  return (static_cast<long long>(B) * Hq * Sq + 7) / 8 * 8;
+}
+long long window_bwd_workspace_floats(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                                      int sinks);
+
 // Page bookkeeping (pages.cu): P pages, a table of B rows x M slots.  Calls whose
 // largest array has at most kPagesClusterWork elements run as one cluster.
 constexpr int kPagesMaxCtas = 512;

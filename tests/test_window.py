@@ -13,6 +13,7 @@ w = 2^-12 relative to the sum of magnitudes at these sizes):
         e_dS = (u + w) |dS| + P (sum_d |dO| e_O + w sum_d |dO| |V|)
   dQ    u |dQ| + scale sum_j e_dS |K| + w scale sum_j |dS| |K|; dK alike
 """
+import ctypes
 import itertools
 import math
 
@@ -157,6 +158,32 @@ def test_gradients_are_the_differences_of_the_forward():
         got = (grads[i].double().cpu() * d).sum().item()
         # The gradient's bound along d, and the difference's own h^2 term.
         assert abs(got - diff) <= (tol[name] * d.abs()).sum().item() + 1e-4 * abs(diff), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 8, 1, 1300, 1300, 128, 60, 5), (2, 2, 1, 900, 1000, 64, 1, 257),
+                                   (1, 4, 4, 2000, 2000, 64, 129, 128)])
+def test_sink_tiles_whose_rows_are_split(shape):
+    # Sequences long against their window: the tiles with sinks are cut into parts.
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, Sq, grad=True)
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks)
+    ref, tol = reference(q, k, v, window, sinks, 1.0 / math.sqrt(D), do)
+    grads = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        check(name, got, ref[name], tol[name])
+    n = ctypes.c_longlong(0)
+    assert _lib().attn_window_bwd_workspace(*shape, ctypes.byref(n)) == attn.ATTN_OK
+    assert n.value > B * Hq * Sq  # Delta, and partial sums
+    # A workspace of the caller's: only its own floats are written, whatever they held.
+    ws = torch.full((n.value + 4096,), float("nan"), device="cuda")
+    again = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks, workspace=ws)
+    assert bool(torch.isnan(ws[n.value:]).all())
+    for a, b in zip(grads, again):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks, workspace=ws[: n.value - 1])
 
 
 @pytest.mark.gpu
@@ -393,6 +420,16 @@ COMMON = [
     (bwd, dict(dk=M), attn.ATTN_ERR_MISALIGNED)])
 def test_prefill_and_backward_reject(call, kw, code):
     assert call(**kw) == code
+
+
+def test_backward_workspace():
+    n = ctypes.c_longlong(0)
+    size = _lib().attn_window_bwd_workspace
+    assert size(1, 2, 1, 8, 8, 64, 4, 1, None) == attn.ATTN_ERR_INVALID_ARG
+    assert size(1, 2, 1, 8, 8, 64, 0, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert size(1, 3, 2, 8, 8, 64, 4, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert size(1, 2, 1, 8, 8, 96, 4, 1, ctypes.byref(n)) == attn.ATTN_ERR_UNSUPPORTED
+    assert size(1, 2, 1, 9, 9, 64, 4, 0, ctypes.byref(n)) == attn.ATTN_OK and n.value >= 2 * 9
 
 
 def dec(q=A, k=A, v=A, sl=A, o=A, lse=A, op=A, lp=A, ct=A, B=1, Hq=4, Hkv=1, Sk=64, D=128, window=8,
