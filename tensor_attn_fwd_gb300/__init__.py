@@ -33,7 +33,6 @@ Layouts: Q [B,Hq,Sq,D], K/V [B,Hkv,Sk,D] bf16; O [B,Hq,Sq,D], LSE [B,Hq,Sq] fp32
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -693,71 +692,37 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     return dq, dk, dv
 
 
-# The calls below are often a few microseconds of GPU work: their checks build no
-# message and open no context unless they have to.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# ---------------------------------------------------------------- bounded caches
+# These calls are often a few microseconds of GPU work, so their arguments are checked
+# and their outputs allocated by a compiled module (csrc/binding.cpp) in place of the
+# code above.  It raises ValueError and AttnError alike, and calls the same C ABI.
+_fast = None
 
 
-class _Scope:
-    """The device and stream of one call: ``handle`` is the stream's.  What the call
-    allocates inside belongs to that stream, so freeing it cannot race with the
-    kernels.  The usual call, on the current stream of the tensors' own device,
-    changes nothing."""
-
-    __slots__ = ("handle", "_context")
-
-    def __init__(self, device: torch.device, stream):
-        self._context = None
-        if stream is not None:
-            self.handle = _stream_handle(stream)
-            self._context = torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=device))
-        else:
-            if torch.cuda.current_device() != device.index:
-                self._context = torch.cuda.device(device)
-            self.handle = (_raw_stream(device.index) if _raw_stream is not None
-                           else torch.cuda.current_stream(device).cuda_stream)
-
-    def __enter__(self):
-        if self._context is not None:
-            self._context.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self._context is not None:
-            self._context.__exit__(*exc)
-        return False
+def _native():
+    """The compiled binding (built by ``tensor_attn_fwd_gb300.build``); raise if absent."""
+    global _fast
+    if _fast is None:
+        load_library()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError(
+                "tensor_attn_fwd_gb300/_binding.so is missing or was built for another PyTorch: "
+                "build it with `python -m tensor_attn_fwd_gb300.build` (or "
+                "__graft_entry__.build()); there is no fallback implementation") from e
+        module.setup(AttnError)
+        _fast = module
+    return _fast
 
 
-def _check_inputs(device: torch.device, ndim: int, **tensors):
-    """bf16, CUDA, contiguous, ``ndim`` dims, on ``device``; raises ValueError."""
-    for name, t in tensors.items():
-        if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.dim() == ndim
-                and t.device == device and device.type == "cuda" and t.is_contiguous()):
-            _check_bf16(name, t, ndim)
-            raise ValueError(f"{name} must be on {device}")
-
-
-def _device_of(q):
-    return q.device if isinstance(q, torch.Tensor) else None
-
-
-def _reach(window, sinks):
-    """window and sinks as C ints; what exceeds every sequence means all keys."""
-    window, sinks = int(window), int(sinks)
-    if window < 1:
-        raise ValueError("window must be at least 1")
-    if sinks < 0:
-        raise ValueError("sinks must not be negative")
-    return min(window, 1 << 30), min(sinks, 1 << 30)
-
-
-def _sizes(q, k, v):
-    """(B, Hq, Hkv, Sq, Sk, D) of q [B,Hq,Sq,D] and k, v [B,Hkv,Sk,D]."""
-    B, Hq, Sq, D = q.shape
-    Bk, Hkv, Sk, Dk = k.shape
-    if Bk != B or Dk != D or v.shape != k.shape:
-        raise ValueError("q/k/v shape mismatch")
-    return B, Hq, Hkv, Sq, Sk, D
+def _on_stream(stream, call, first, *args):
+    """``call`` with ``stream`` current: what it allocates belongs to that stream, so
+    freeing it cannot race with the kernels.  ``first`` is the call's first tensor."""
+    _check(isinstance(first, torch.Tensor) and first.is_cuda, "the tensors must be CUDA tensors")
+    handle = _stream_handle(stream)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=first.device)):
+        return call(first, *args)
 
 
 def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int,
@@ -768,20 +733,10 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
     q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64 or 128.  Row i stands
     at p = i + Sk - Sq and sees key j when j <= p and (j > p - window or j < sinks).
     """
-    device = _device_of(q)
-    _check_inputs(device, 4, q=q, k=k, v=v)
-    B, Hq, Hkv, Sq, Sk, D = _sizes(q, k, v)
-    window, sinks = _reach(window, sinks)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    lib = load_library()
-    with _Scope(device, stream) as handle:
-        o = _out_bf16(o, (B, Hq, Sq, D), device, "o")
-        lse = _out(lse, (B, Hq, Sq), device, "lse")
-        st = lib.attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                 lse.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window, sinks, scale,
-                                 handle)
-    _raise_if(st, "attn_window_fwd")
-    return o, lse
+    call = (_fast or _native()).window_fwd
+    if stream is not None:
+        return _on_stream(stream, call, q, k, v, window, sinks, scale, o, lse)
+    return call(q, k, v, window, sinks, scale, o, lse)
 
 
 def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
@@ -796,103 +751,18 @@ def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     ``workspace`` is an optional fp32 CUDA tensor of at least
     attn_window_bwd_workspace floats (include/attn.h).
     """
-    device = _device_of(q)
-    _check_inputs(device, 4, q=q, k=k, v=v, o=o, dout=dout)
-    B, Hq, Hkv, Sq, Sk, D = _sizes(q, k, v)
-    if dout.shape != q.shape or o.shape != q.shape:
-        raise ValueError("dout and o must match q")
-    if not isinstance(lse, torch.Tensor):
-        raise ValueError("lse must be a torch.Tensor")
-    lse = _out(lse, (B, Hq, Sq), device, "lse")
-    window, sinks = _reach(window, sinks)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    lib = load_library()
-    with _Scope(device, stream) as handle:
-        dq = _out_bf16(dq, (B, Hq, Sq, D), device, "dq")
-        dk = _out_bf16(dk, (B, Hkv, Sk, D), device, "dk")
-        dv = _out_bf16(dv, (B, Hkv, Sk, D), device, "dv")
-        n = ctypes.c_longlong(0)
-        _raise_if(lib.attn_window_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks,
-                                                ctypes.byref(n)), "attn_window_bwd_workspace")
-        if workspace is None:
-            workspace = torch.empty(n.value, dtype=torch.float32, device=device)
-        elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.float32
-                  and workspace.device == device and workspace.is_contiguous()
-                  and workspace.numel() >= n.value):
-            raise ValueError(f"workspace must be a contiguous float32 tensor on {device} with at "
-                             f"least {n.value} entries")
-        st = lib.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                 lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                 dv.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
-                                 sinks, scale, handle)
-    _raise_if(st, "attn_window_bwd")
-    return dq, dk, dv
-
-
-@functools.lru_cache(maxsize=4096)
-def _decode_splits(device_index: int, B: int, Hq: int, Hkv: int, keys: int, D: int) -> int:
-    """attn_decode_num_splits, a rule on the sizes alone, asked once per shape."""
-    return attn_decode_num_splits(B, Hq, Hkv, keys, D, device_index)
-
-
-def _decode_window(what, q, k, v, table, seqlens, Sk, window, sinks, num_splits, scale, workspace,
-                   o, lse, counters, stream):
-    """The two windowed decodes: ``table`` is None for a contiguous cache."""
-    B, Hq, Sq, D = q.shape
-    if Sq != 1:
-        raise ValueError("decode takes one query row per head (q.shape[2] == 1)")
-    device, Hkv = q.device, k.shape[1]
-    if seqlens is not None:
-        _check_int32("seqlens", seqlens, (B,), device)
-    window, sinks = _reach(window, sinks)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    lib = load_library()
-    with _Scope(device, stream) as handle:
-        ns = (_decode_splits(device.index, B, Hq, Hkv, max(1, min(Sk, window + sinks)), D)
-              if num_splits is None else int(num_splits))
-        o = _out_bf16(o, (B, Hq, D), device, "o")
-        lse = _out(lse, (B, Hq), device, "lse")
-        part = lse_part = count = None
-        if ns > 1:
-            if workspace is None:
-                # One allocation: the partials, then their LSEs (D a multiple of 64).
-                workspace = torch.empty(ns * B * Hq * (D + 1), dtype=torch.float32, device=device)
-                part = workspace.data_ptr()
-                lse_part = part + 4 * ns * B * Hq * D
-            else:
-                part = _out(workspace[0], (ns, B, Hq, D), device, "o_part").data_ptr()
-                lse_part = _out(workspace[1], (ns, B, Hq), device, "lse_part").data_ptr()
-            n = B * Hkv * -(-Hq // (16 * Hkv)) if Hkv else 0  # attn_decode_fused_counters
-            if counters is None:
-                # A captured call zeroes counters of its own on every replay: graphs that
-                # run at the same time must not share the stream's array.
-                counters = (torch.zeros(n, dtype=torch.int32, device=device)
-                            if torch.cuda.is_current_stream_capturing()
-                            else _stream_counters(device, handle, n))
-            elif not (isinstance(counters, torch.Tensor) and counters.dtype == torch.int32
-                      and counters.device == device and counters.is_contiguous()
-                      and counters.numel() >= n):
-                raise ValueError(f"counters must be a contiguous int32 CUDA tensor with >= {n} "
-                                 "entries on q's device")
-            count = counters.data_ptr()
-        outs = (o.data_ptr(), lse.data_ptr(), part, lse_part, count)
-        seq = None if seqlens is None else seqlens.data_ptr()
-        if table is None:
-            st = lib.attn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), seq, *outs, B,
-                                        Hq, Hkv, Sk, D, window, sinks, ns, scale, handle)
-        else:
-            st = lib.attn_decode_window_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                              table.data_ptr(), seq, *outs, B, Hq, Hkv, k.shape[0],
-                                              k.shape[2], table.shape[1], D, window, sinks, ns,
-                                              scale, handle)
-    _raise_if(st, what)
-    return o, lse
+    call = (_fast or _native()).window_bwd
+    if stream is not None:
+        return _on_stream(stream, call, q, k, v, o, lse, dout, window, sinks, scale, dq, dk, dv,
+                          workspace)
+    return call(q, k, v, o, lse, dout, window, sinks, scale, dq, dk, dv, workspace)
 
 
 def decode_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
                   seqlens: torch.Tensor | None = None, num_splits: int | None = None,
-                  scale: float | None = None, workspace=None, o=None, lse=None,
-                  counters: torch.Tensor | None = None, stream=None):
+                  scale: float | None = None, workspace=None, o: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, counters: torch.Tensor | None = None,
+                  stream=None):
     """Decode one token under a sliding window with sinks, in one launch; returns
     (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
 
@@ -900,63 +770,34 @@ def decode_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int
     its sequence's last key (Sk keys, or its first seqlens[b]) and sees the last
     ``window`` keys and the first ``sinks``.  ``num_splits=None`` picks
     attn_decode_num_splits for the keys seen; ``workspace`` and ``counters`` as
-    attn_decode_fused (not used with one split).
+    attn_decode_fused (not used with one split).  Without ``counters`` a call captured
+    in a graph has its own.
     """
-    _check_inputs(_device_of(q), 4, q=q, k=k, v=v)
-    Sk = _sizes(q, k, v)[4]
-    return _decode_window("attn_decode_window", q, k, v, None, seqlens, Sk, window, sinks,
-                          num_splits, scale, workspace, o, lse, counters, stream)
+    call = (_fast or _native()).decode_window
+    part, lse_part = (None, None) if workspace is None else workspace
+    if stream is not None:
+        return _on_stream(stream, call, q, k, v, seqlens, window, sinks, num_splits, scale, part,
+                          lse_part, o, lse, counters)
+    return call(q, k, v, seqlens, window, sinks, num_splits, scale, part, lse_part, o, lse,
+                counters)
 
 
 def decode_window_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                         block_table: torch.Tensor, seqlens: torch.Tensor, window: int,
                         sinks: int = 0, num_splits: int | None = None, scale: float | None = None,
-                        workspace=None, o=None, lse=None, counters: torch.Tensor | None = None,
+                        workspace=None, o: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, counters: torch.Tensor | None = None,
                         stream=None):
     """decode_window over a paged cache (k_cache/v_cache [num_pages,Hkv,page_size,D],
     block_table int32 [B,max_pages], seqlens int32 [B], as decode_paged).  Entries of
     pages that hold no seen key are not read (attn_pages_free makes them -1)."""
-    device = _device_of(q)
-    _check_inputs(device, 4, q=q, k_cache=k_cache, v_cache=v_cache)
-    if k_cache.shape[3] != q.shape[3] or v_cache.shape != k_cache.shape:
-        raise ValueError("q/cache shape mismatch")
-    _check_int32("block_table", block_table, (q.shape[0], None), device)
-    if seqlens is None:
-        raise ValueError("a paged cache needs seqlens")
-    return _decode_window("attn_decode_window_paged", q, k_cache, v_cache, block_table, seqlens,
-                          block_table.shape[1] * k_cache.shape[2], window, sinks, num_splits,
-                          scale, workspace, o, lse, counters, stream)
-
-
-def _check_int32(name: str, t: torch.Tensor, shape, device=None):
-    """A contiguous int32 CUDA tensor; shape entries of None are free."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
-            and t.is_contiguous() and (device is None or t.device == device)):
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor"
-                         + (f" on {device}" if device is not None else ""))
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _out_int32(t, shape, device, name):
-    if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
-    _check_int32(name, t, shape, device)
-    return t
-
-
-def _room(room) -> int:
-    room = int(room)
-    if room < 0:
-        raise ValueError("room must not be negative")
-    return min(room, 1 << 30)
-
-
-def _pages_workspace(num_pages: int, rows: int, device) -> torch.Tensor:
-    n = ctypes.c_longlong(0)
-    _raise_if(load_library().attn_pages_workspace(num_pages, rows, ctypes.byref(n)),
-              "attn_pages_workspace")
-    return torch.empty(n.value, dtype=torch.int32, device=device)
+    call = (_fast or _native()).decode_window_paged
+    part, lse_part = (None, None) if workspace is None else workspace
+    if stream is not None:
+        return _on_stream(stream, call, q, k_cache, v_cache, block_table, seqlens, window, sinks,
+                          num_splits, scale, part, lse_part, o, lse, counters)
+    return call(q, k_cache, v_cache, block_table, seqlens, window, sinks, num_splits, scale, part,
+                lse_part, o, lse, counters)
 
 
 def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,
@@ -971,21 +812,12 @@ def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     (``window=None``: every key), and those reserved for the next ``room`` keys.
     ``block_table_out`` and ``refs_out`` may be the inputs.
     """
-    _check_int32("block_table", block_table, (None, None))
-    _check_int32("refs", refs, (None,), block_table.device)
-    B, M = block_table.shape
-    _check_int32("seqlens", seqlens, (B,), block_table.device)
-    window, sinks = _reach(1 << 30 if window is None else window, sinks)
-    room = _room(room)
-    lib = load_library()
-    with _Scope(block_table.device, stream) as handle:
-        table = _out_int32(block_table_out, (B, M), block_table.device, "block_table_out")
-        count = _out_int32(refs_out, (refs.shape[0],), block_table.device, "refs_out")
-        st = lib.attn_pages_free(block_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
-                                 table.data_ptr(), count.data_ptr(), B, M, refs.shape[0],
-                                 int(page_size), window, sinks, room, handle)
-    _raise_if(st, "attn_pages_free")
-    return table, count
+    call = (_fast or _native()).pages_free
+    if stream is not None:
+        return _on_stream(stream, call, block_table, refs, seqlens, page_size, window, sinks, room,
+                          block_table_out, refs_out)
+    return call(block_table, refs, seqlens, page_size, window, sinks, room, block_table_out,
+                refs_out)
 
 
 def attn_pages_fork(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,
@@ -1000,29 +832,10 @@ def attn_pages_fork(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     before the new rows are used.  counts holds the pages needed and the pages free;
     if they do not suffice, attn_debug_status reports ATTN_ERR_NO_PAGES.
     """
-    _check_int32("block_table", block_table, (None, None))
-    device = block_table.device
-    _check_int32("refs", refs, (None,), device)
-    _check_int32("parents", parents, (None,), device)
-    B, M = block_table.shape
-    _check_int32("seqlens", seqlens, (B,), device)
-    room = _room(room)
-    R, P = parents.shape[0], refs.shape[0]
-    lib = load_library()
-    with _Scope(device, stream) as handle:
-        workspace = _pages_workspace(P, R, device)
-        # The results share one allocation.
-        table, count, lens, src, dst, counts = torch.empty(
-            R * M + P + 3 * R + 2, dtype=torch.int32, device=device).split_with_sizes(
-                (R * M, P, R, R, R, 2))
-        table = table.view(R, M)
-        st = lib.attn_pages_fork(block_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
-                                 parents.data_ptr(), table.data_ptr(), count.data_ptr(),
-                                 lens.data_ptr(), src.data_ptr(), dst.data_ptr(),
-                                 counts.data_ptr(), workspace.data_ptr(), B, R, M, P,
-                                 int(page_size), room, handle)
-    _raise_if(st, "attn_pages_fork")
-    return table, count, lens, src, dst, counts
+    call = (_fast or _native()).pages_fork
+    if stream is not None:
+        return _on_stream(stream, call, block_table, refs, seqlens, parents, page_size, room)
+    return call(block_table, refs, seqlens, parents, page_size, room)
 
 
 def attn_pages_compact(block_table: torch.Tensor, refs: torch.Tensor, stream=None):
@@ -1033,25 +846,10 @@ def attn_pages_compact(block_table: torch.Tensor, refs: torch.Tensor, stream=Non
     lists the moves (then -1) for attn_pages_copy, for every layer's cache, before
     the new table is used.
     """
-    _check_int32("block_table", block_table, (None, None))
-    device = block_table.device
-    _check_int32("refs", refs, (None,), device)
-    B, M = block_table.shape
-    P = refs.shape[0]
-    lib = load_library()
-    half = P // 2
-    with _Scope(device, stream) as handle:
-        workspace = _pages_workspace(P, 0, device)
-        # The results share one allocation.
-        table, count, src, dst, num_live = torch.empty(
-            B * M + P + 2 * half + 1, dtype=torch.int32, device=device).split_with_sizes(
-                (B * M, P, half, half, 1))
-        table = table.view(B, M)
-        st = lib.attn_pages_compact(block_table.data_ptr(), refs.data_ptr(), table.data_ptr(),
-                                    count.data_ptr(), src.data_ptr(), dst.data_ptr(),
-                                    num_live.data_ptr(), workspace.data_ptr(), B, M, P, handle)
-    _raise_if(st, "attn_pages_compact")
-    return table, count, src, dst, num_live
+    call = (_fast or _native()).pages_compact
+    if stream is not None:
+        return _on_stream(stream, call, block_table, refs)
+    return call(block_table, refs)
 
 
 def attn_pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor,
@@ -1060,19 +858,7 @@ def attn_pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Ten
     ([num_pages, ...], contiguous, of any one type); pairs of -1 are skipped.  No dst
     may appear twice or as a src (the lists of attn_pages_fork and
     attn_pages_compact never do)."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() >= 2
-                and t.numel() > 0):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor [num_pages, ...]")
-    if (k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype
-            or k_cache.device != v_cache.device):
-        raise ValueError("the caches must have one shape, type and device")
-    _check_int32("src", src, (None,), k_cache.device)
-    _check_int32("dst", dst, tuple(src.shape), k_cache.device)
-    lib = load_library()
-    num_pages = k_cache.shape[0]
-    page_bytes = k_cache.numel() // num_pages * k_cache.element_size()
-    with _Scope(k_cache.device, stream) as handle:
-        st = lib.attn_pages_copy(k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(),
-                                 dst.data_ptr(), src.shape[0], num_pages, page_bytes, handle)
-    _raise_if(st, "attn_pages_copy")
+    call = (_fast or _native()).pages_copy
+    if stream is not None:
+        return _on_stream(stream, call, k_cache, v_cache, src, dst)
+    return call(k_cache, v_cache, src, dst)

@@ -3,6 +3,8 @@
 Each translation unit under csrc/ is compiled in parallel with nvcc for
 sm_103a only, then linked into ``tensor_attn_fwd_gb300/libattn.so`` (in-tree,
 git-ignored).  The build is skipped when the library is newer than every source.
+Beside it, ``_binding.so`` (csrc/binding.cpp, g++ against the installed PyTorch)
+marshals tensors for the calls that are too short for Python's own marshalling.
 
     python -m tensor_attn_fwd_gb300.build [--force] [--verbose]
 """
@@ -68,6 +70,56 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
 EXACT_REGISTERS = {"attn_fwd_kernel": 168}
 
 
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+
+
+def binding_up_to_date() -> bool:
+    import torch
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "attn.h"), os.path.abspath(__file__),
+            os.path.join(os.path.dirname(torch.__file__), "version.py")]
+    return (os.path.exists(BINDING_PATH)
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING_PATH) for d in deps))
+
+
+def _run(cmd, what: str, verbose: bool):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed")
+
+
+def compile_binding(verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against the installed PyTorch."""
+    import sysconfig
+
+    import torch
+    include = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda_home = os.path.dirname(os.path.dirname(_nvcc()))
+    obj = os.path.join(BUILD_DIR, "binding.cpp.o")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", sysconfig.get_paths()["include"], "-isystem", include,
+          "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(cuda_home, "include"), "-c", BINDING_SRC, "-o", obj],
+         "binding compilation", verbose)
+    return obj
+
+
+def link_binding(obj: str, verbose: bool = False) -> str:
+    """Link _binding.so to PyTorch and, by name, to the libattn.so beside it."""
+    import torch
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", obj, "-o", tmp,
+          "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+          "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10",
+          "-L", PKG_DIR, "-l:libattn.so", "-Wl,-rpath,$ORIGIN"], "binding link", verbose)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def check_register_counts(ptxas_log: str):
     """Parse `ptxas -v` output; raise if a kernel in EXACT_REGISTERS deviates."""
     current = None
@@ -94,6 +146,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug: b
     lib_path = DEBUG_LIB_PATH if debug else LIB_PATH
     build_dir = DEBUG_BUILD_DIR if debug else BUILD_DIR
     if not force and up_to_date(lib_path):
+        if not debug and not binding_up_to_date():
+            link_binding(compile_binding(verbose), verbose)
         return lib_path
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -105,7 +159,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug: b
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(compile_binding, verbose) if not debug else None
         results = list(ex.map(compile_one, sources()))
     failed = False
     seen = set()
@@ -130,6 +185,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug: b
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("libattn link failed")
     os.replace(tmp, lib_path)
+    if binding is not None:
+        link_binding(binding.result(), verbose)
     return lib_path
 
 
