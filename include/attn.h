@@ -354,6 +354,12 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const float *
  *   o [B,Hq,Sq,D] bf16 (each fp32 result rounded to nearest even once)
  *   lse [B,Hq,Sq] fp32
  *   window >= 1, sinks >= 0 (else ATTN_ERR_INVALID_ARG); both may exceed Sk.
+ *   num_splits: 1, or up to ceil(Sk / 128) (else ATTN_ERR_INVALID_ARG): the key tiles
+ *      that a query tile sees are shared out evenly over so many CTAs, for chunks with
+ *      too few rows to fill the GPU, and their fp32 partials are merged
+ *      (attn_combine's formula) by a second kernel
+ *   workspace: num_splits * B * Hq * Sq * (D + 1) floats, 16-byte aligned, contents
+ *      undefined; not touched, and NULL allowed, with one split
  *   D 64 or 128 (else ATTN_ERR_UNSUPPORTED).  Sizes, alignment, other errors and
  *   rows that see no key (O = 0, LSE = -inf) as attn_fwd.
  *   K and V have to be finite in every 128-key tile (keys [128n, 128n + 128)) that
@@ -362,8 +368,18 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const float *
  *   condition.)
  */
 ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
-                             int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
-                             float scale, void *stream);
+                             float *workspace, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                             int window, int sinks, int num_splits, float scale, void *stream);
+
+/*
+ * A split count for attn_window_fwd on the current device (a measured rule of this
+ * library): of the counts whose work items (per split, 128 rows of two query heads
+ * of a KV head, or 256 rows of one where their number is odd) run at the same time,
+ * the one with the least estimated time.  At most 32.  Host-only.
+ * ATTN_ERR_INVALID_ARG as attn_window_fwd.
+ */
+ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                                        int sinks, int *num_splits);
 
 /*
  * Gradients of sum(dO * O) for attn_window_fwd: attn_bwd's formulas under its mask.
@@ -399,7 +415,7 @@ ATTN_API int attn_window_bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, i
  *      each.  With num_splits = 1, o_part, lse_part and counters may be NULL and
  *      are not touched; otherwise they are as attn_decode_fused (partials
  *      [num_splits,B,Hq,D] and [num_splits,B,Hq], zeroed counters).
- *      attn_decode_num_splits(B, Hq, Hkv, min(Sk, window + sinks), D) is a good count.
+ *      attn_decode_window_num_splits gives a good count.
  *   window, sinks as attn_window_fwd; D in {64, 128, 256}; other arguments and
  *   errors as attn_decode_fused.  A sequence of length 0 gives O = 0, LSE = -inf.
  */
@@ -407,6 +423,13 @@ ATTN_API int attn_decode_window(const void *q, const void *k, const void *v, con
                                 void *o, float *lse, float *o_part, float *lse_part, int *counters,
                                 int B, int Hq, int Hkv, int Sk, int D, int window, int sinks,
                                 int num_splits, float scale, void *stream);
+
+/* A split count for attn_decode_window (paged: Sk = max_pages * page_size): that of
+ * attn_decode_num_splits for the keys within reach, min(Sk, window + sinks), or more
+ * where a few warps would walk them for long.  Host-only.  Errors as that function's,
+ * and ATTN_ERR_INVALID_ARG for a bad window or sinks. */
+ATTN_API int attn_decode_window_num_splits(int B, int Hq, int Hkv, int Sk, int D, int window,
+                                           int sinks, int *num_splits);
 
 /*
  * attn_decode_window over a paged cache (layout, block_table and seqlens as

@@ -88,9 +88,11 @@ _SIGNATURES = {
     "attn_decode_num_splits": ([_int, _int, _int, _int, _int, ctypes.POINTER(_int)], _int),
     "attn_qkv_rope": ([_vp] * 7 + [_int] * 8 + [_vp], _int),
     "attn_bwd": ([_vp] * 10 + [_int] * 7 + [_flt, _vp], _int),
-    "attn_window_fwd": ([_vp] * 5 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_window_fwd": ([_vp] * 6 + [_int] * 9 + [_flt, _vp], _int),
+    "attn_window_fwd_num_splits": ([_int] * 8 + [ctypes.POINTER(_int)], _int),
     "attn_window_bwd": ([_vp] * 10 + [_int] * 8 + [_flt, _vp], _int),
     "attn_window_bwd_workspace": ([_int] * 8 + [ctypes.POINTER(ctypes.c_longlong)], _int),
+    "attn_decode_window_num_splits": ([_int] * 7 + [ctypes.POINTER(_int)], _int),
     "attn_decode_window": ([_vp] * 9 + [_int] * 8 + [_flt, _vp], _int),
     "attn_decode_window_paged": ([_vp] * 10 + [_int] * 10 + [_flt, _vp], _int),
     "attn_pages_free": ([_vp] * 5 + [_int] * 7 + [_vp], _int),
@@ -727,16 +729,19 @@ def _on_stream(stream, call, first, *args):
 
 def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int,
                     sinks: int = 0, scale: float | None = None, o: torch.Tensor | None = None,
-                    lse: torch.Tensor | None = None, stream=None):
+                    lse: torch.Tensor | None = None, stream=None,
+                    num_splits: int | None = None):
     """Attention under a sliding window with sinks; returns (o bf16 [B,Hq,Sq,D], lse fp32).
 
     q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64 or 128.  Row i stands
     at p = i + Sk - Sq and sees key j when j <= p and (j > p - window or j < sinks).
+    ``num_splits`` > 1 cuts each row's keys into so many parts and merges them, for
+    chunks with too few rows to fill the GPU; None picks attn_window_fwd_num_splits.
     """
     call = (_fast or _native()).window_fwd
     if stream is not None:
-        return _on_stream(stream, call, q, k, v, window, sinks, scale, o, lse)
-    return call(q, k, v, window, sinks, scale, o, lse)
+        return _on_stream(stream, call, q, k, v, window, sinks, scale, o, lse, num_splits)
+    return call(q, k, v, window, sinks, scale, o, lse, num_splits)
 
 
 def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
@@ -769,8 +774,8 @@ def decode_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int
     q [B,Hq,1,D], k/v [B,Hkv,Sk,D] (bf16), D 64, 128 or 256.  The query stands at
     its sequence's last key (Sk keys, or its first seqlens[b]) and sees the last
     ``window`` keys and the first ``sinks``.  ``num_splits=None`` picks
-    attn_decode_num_splits for the keys seen; ``workspace`` and ``counters`` as
-    attn_decode_fused (not used with one split).  Without ``counters`` a call captured
+    attn_decode_window_num_splits; ``workspace`` and ``counters`` as attn_decode_fused
+    (not used with one split).  Without ``counters`` a call captured
     in a graph has its own.
     """
     call = (_fast or _native()).decode_window

@@ -227,21 +227,63 @@ int attn_fwd_splitkv(const void* q, const void* k, const void* v, float* o_part,
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B,
-                    int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
-                    void* stream) {
-  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                    float* workspace, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                    int sinks, int num_splits, float scale, void* stream) {
+  if (window < 1 || sinks < 0 || num_splits < 1) return ATTN_ERR_INVALID_ARG;
+  if (num_splits > 1 && !workspace) return ATTN_ERR_INVALID_ARG;
   const int chk = fwd_check_args(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, 1, scale);
   if (chk != ATTN_OK) return chk;
   if (D == 256) return ATTN_ERR_UNSUPPORTED;
+  if (num_splits > 1) {
+    // Every split of the longest row has a key tile; rows and items are counted with int.
+    if (num_splits > (Sk + 127) / 128) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * Hq * Sq > (1ll << 30) ||
+        window_items(B, Hq, Hkv, Sq) * num_splits > (1ll << 30) ||
+        static_cast<long long>(num_splits) * B * Hq * Sq * D > kMaxElems)
+      return ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
+  float* lse_part = workspace;
+  if (num_splits > 1) lse_part += static_cast<long long>(num_splits) * B * Hq * Sq * D;
   // A window or sinks past the last key mean all keys; clamped, the kernels' sums fit int.
   const cudaError_t e =
-      launch_attn_window_fwd(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
-                             sinks < Sk ? sinks : Sk, scale, static_cast<cudaStream_t>(stream),
-                             status);
+      launch_attn_window_fwd(q, k, v, o, lse, workspace,
+                             lse_part, B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
+                             sinks < Sk ? sinks : Sk, num_splits, scale,
+                             static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                               int sinks, int* num_splits) {
+  if (num_splits == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0 ||
+      Hq % Hkv != 0 || window < 1 || sinks < 0)
+    return ATTN_ERR_INVALID_ARG;
+  const long long n_sm = sm_count(), items = window_items(B, Hq, Hkv, Sq);
+  // Key tiles of an item at most: its rows' windows and the sinks, or all there are.
+  const long long all = (static_cast<long long>(Sk) + 127) / 128;
+  const long long seen = (static_cast<long long>(window) + 126) / 128 + 1 +
+                         (static_cast<long long>(sinks) + 127) / 128;
+  const long long tiles = seen < all ? seen : all;
+  // Estimated time of a count that still runs in one round, in ns: 1400 for a step of
+  // an item, 3500 around it, and for the merge 3500 and the partials' way to L2 and
+  // back at 5 bytes a ps.  Measured (us) against it, D = 128, 32/8 heads: Sq 512, 34
+  // tiles: 1 split 51.9 (est. 52), 2 37.2 (38); Sq 512, 10 tiles: 1 20.0 (17), 2 21.1
+  // (20); Sq 128, 34 tiles: 4 22.8 (23), 8 19.4 (20), 16 26.4 (more than one round).
+  const long long partial_ns = 2ll * B * Hq * Sq * D * 4 / 5000;  // of one split
+  long long best = 1, best_ns = tiles * 1400 + 3500;
+  for (long long ns = 2; ns <= tiles && ns <= 32 && ns * items <= n_sm; ++ns) {
+    const long long t = (tiles + ns - 1) / ns * 1400 + 7000 + ns * partial_ns;
+    if (t < best_ns) {
+      best = ns;
+      best_ns = t;
+    }
+  }
+  *num_splits = static_cast<int>(best);
+  return ATTN_OK;
 }
 
 int attn_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, int* num_splits) {
@@ -455,6 +497,27 @@ int attn_decode_window(const void* q, const void* k, const void* v, const int* s
                        void* stream) {
   return decode_window_common(q, k, v, seqlens, nullptr, o, lse, o_part, lse_part, counters, B,
                               Hq, Hkv, Sk, D, window, sinks, num_splits, scale, stream);
+}
+
+int attn_decode_window_num_splits(int B, int Hq, int Hkv, int Sk, int D, int window, int sinks,
+                                  int* num_splits) {
+  if (num_splits == nullptr || Sk <= 0 || window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  const long long reach = static_cast<long long>(window) + sinks;
+  const int keys = static_cast<int>(reach < Sk ? reach : Sk);
+  const int e = attn_decode_num_splits(B, Hq, Hkv, keys, D, num_splits);
+  if (e != ATTN_OK) return e;
+  // A short reach is bound by the latency of a warp's blocks one after the other (1.1
+  // us each; splitting costs 2.6 us).  From 16 blocks on at least as many splits as
+  // fit one round, of two blocks or more, up to 12: B1 Hkv8 D128, 1024 + 4 keys: 1
+  // split 13.5 us, 4 (the rule for long caches) 10.3, 12 9.0, 16 9.0; D64 2 10.2, 12
+  // 7.6; B4 4 10.4, 12 13.6; 128 + 4 keys: 1 split 5.8, 2 7.8.
+  const long long blocks = (static_cast<long long>(keys) + 31) / 32;
+  const long long base = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 15) / 16);
+  long long ns = sm_count() / base;
+  if (ns > blocks / 2) ns = blocks / 2;
+  if (ns > 12) ns = 12;
+  if (blocks >= 16 && ns > *num_splits) *num_splits = static_cast<int>(ns);
+  return ATTN_OK;
 }
 
 int attn_decode_window_paged(const void* q, const void* k_cache, const void* v_cache,

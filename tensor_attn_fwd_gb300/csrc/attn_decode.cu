@@ -28,6 +28,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -613,10 +614,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 // Splits are handled 32 at a time: lane s holds split s's LSE and weight, the
 // max and sum are warp reductions, and the O loads of all splits of a chunk are
 // independent (lane-parallel over D, unrolled over splits).
-template <int D>
+// TO: fp32, or bf16 (rounded once).
+template <int D, typename TO = float>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ o_part,
                                                       const float* __restrict__ lse_part,
-                                                      float* __restrict__ o,
+                                                      TO* __restrict__ o,
                                                       float* __restrict__ lse, int rows,
                                                       int num_splits) {
   constexpr int DPL = D / 32;
@@ -673,8 +675,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     for (int e = 0; e < DPL; ++e) out[e] *= inv;
     L = M + logf(W);
   }
-  float* dst = o + static_cast<size_t>(row) * D + lane * DPL;
-  if constexpr (DPL >= 4) {
+  TO* dst = o + static_cast<size_t>(row) * D + lane * DPL;
+  if constexpr (std::is_same_v<TO, __nv_bfloat16>) {
+#pragma unroll
+    for (int e = 0; e < DPL; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(out[e], out[e + 1]);
+  } else if constexpr (DPL >= 4) {
 #pragma unroll
     for (int e = 0; e < DPL; e += 4)
       *reinterpret_cast<float4*>(dst + e) = make_float4(out[e], out[e + 1], out[e + 2], out[e + 3]);
@@ -771,6 +777,13 @@ cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o,
     e = cudaLaunchKernelEx(&cfg, combine_kernel<64>, o_part, lse_part, o, lse, rows, num_splits);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+cudaError_t launch_combine_bf16(const float* o_part, const float* lse_part, void* o, float* lse,
+                                int rows, int D, int num_splits, cudaStream_t stream) {
+  auto kernel = D == 128 ? combine_kernel<128, __nv_bfloat16> : combine_kernel<64, __nv_bfloat16>;
+  return launch_programmatic(kernel, dim3((rows + 7) / 8), dim3(256), 0, stream, o_part, lse_part,
+                             static_cast<__nv_bfloat16*>(o), lse, rows, num_splits);
 }
 
 }  // namespace attn

@@ -143,28 +143,31 @@ __device__ __forceinline__ int next_tile(const Item& it, int j) {
 __device__ __forceinline__ Item get_window_item(const FwdParams& p, int idx) {
   const int group = p.Hq / p.Hkv;
   const int per_group = p.head_pairs ? group / 2 : group;
+  const int per_split = p.total_items / p.num_splits;
+  const int split = idx / per_split;
+  idx -= split * per_split;
   const int rest = idx / per_group;
   const int bg = rest / p.num_pairs;  // b * Hkv + KV head
   const int tile = p.num_pairs - 1 - rest % p.num_pairs;
   Item it;
-  it.split = 0;
+  it.split = split;
   it.bh = (bg / p.Hkv) * p.Hq + (bg % p.Hkv) * group +
           (idx % per_group) * (p.head_pairs ? 2 : 1);
   it.q_row0 = tile * (p.head_pairs ? 128 : kRowsPerItem);
   it.r[0] = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0);
   it.r[1] = p.head_pairs ? it.r[0]
                          : window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0 + 128);
+  if (p.num_splits > 1) {
+    // Split s of a query tile: its s-th equal run of steps.
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int chunk = (it.r[t].count() + p.num_splits - 1) / p.num_splits;
+      it.r[t] = it.r[t].steps(split * chunk, split * chunk + chunk);
+    }
+  }
   it.n[0] = it.r[0].e;
   it.n[1] = it.r[1].e;
-  // Tile 1's rows come later: its tiles start and end no earlier, unless it (or
-  // tile 0, whose rows may all stand before the first key) is empty.
-  it.u = it.r[1];
-  if (it.r[1].e == 0) {
-    it.u = it.r[0];
-  } else if (it.r[0].e > 0) {
-    it.u.w = it.r[0].w;
-    it.u.s = min(max(it.r[0].s, it.r[1].s), it.u.w);
-  }
+  it.u = tile_union(it.r[0], it.r[1]);
   it.j0 = it.u.first();
   return it;
 }
@@ -551,10 +554,10 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
       // No key of the split visible to any row of this tile (or the tile is
       // past Sq): O = 0, LSE = -inf (a split a combine weighs with 0).
       if (row_valid &&
-          store_in_bounds(WIN || p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
-                          D * (WIN || p.o_bf16 ? 2 : 4), p.o, p.o_bytes, p.status) &&
+          store_in_bounds(p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
+                          D * (p.o_bf16 ? 2 : 4), p.o, p.o_bytes, p.status) &&
           store_in_bounds(lse_ptr, 4, p.lse, p.lse_bytes, p.status)) {
-        if (WIN || p.o_bf16) {
+        if (p.o_bf16) {
 #pragma unroll 4
           for (int c = 0; c < D; c += 8)
             *reinterpret_cast<uint4*>(o_row16 + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -715,7 +718,7 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
     // 32, halving the L1 wavefronts that the per-row layout of TMEM costs.
     const int pb = lane & 1;
     const bool even_valid = row - pb < p.Sq, odd_valid = row - pb + 1 < p.Sq;
-    if (WIN || p.o_bf16) {
+    if (p.o_bf16) {
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t w[16];
@@ -880,12 +883,12 @@ cudaError_t launch_fwd_impl(const void* q, const void* k, const void* v, void* o
                              tmK, tmV, p);
 }
 
-// Windowed forward: one split, bf16 O (P is rounded to bf16 for the second
-// product, so an fp32 O would hold no more).
+// Windowed forward: bf16 O (P is rounded to bf16 for the second product, so an fp32
+// O would hold no more), or with several splits their fp32 partials.
 template <int D>
 cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void* o, float* lse,
                                int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks,
-                               float scale, cudaStream_t stream, int* status) {
+                               int num_splits, float scale, cudaStream_t stream, int* status) {
   using C = Cfg<D>;
   CUtensorMap tmQ, tmK, tmV;
   if (!encode_bf16_map(&tmQ, q, D, Sq, B * Hq, 128) || !encode_bf16_map(&tmK, k, D, Sk, B * Hkv, 128) ||
@@ -897,10 +900,12 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   if (e != cudaSuccess) return e;
   FwdParams p = {};
   p.o = o;
-  p.o_bf16 = 1;
+  p.o_bf16 = num_splits == 1;
   p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  p.o_bytes = static_cast<size_t>(B) * Hq * Sq * D * 2;
-  p.lse_bytes = static_cast<size_t>(B) * Hq * Sq * sizeof(float);
+  p.split_stride_lse = static_cast<size_t>(B) * Hq * Sq;
+  p.split_stride_o = p.split_stride_lse * D;
+  p.o_bytes = num_splits * p.split_stride_o * (p.o_bf16 ? 2 : 4);
+  p.lse_bytes = num_splits * p.split_stride_lse * sizeof(float);
   p.lse = lse;
   p.status = status;
   p.B = B;
@@ -910,13 +915,13 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   p.Sk = Sk;
   p.causal = 1;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.head_pairs = (Hq / Hkv) % 2 == 0;
+  p.head_pairs = window_head_pairs(Hq, Hkv);
   const int rows = p.head_pairs ? 128 : kRowsPerItem;
   p.num_pairs = (Sq + rows - 1) / rows;
-  p.num_splits = 1;
+  p.num_splits = num_splits;
   p.window = window;
   p.sinks = sinks;
-  p.total_items = (p.head_pairs ? B * Hq / 2 : B * Hq) * p.num_pairs;
+  p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq) * num_splits);
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,
                              tmK, tmV, p);
@@ -925,14 +930,19 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
 }  // namespace
 
 cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, void* o,
-                                   float* lse, int B, int Hq, int Hkv, int Sq, int Sk, int D,
-                                   int window, int sinks, float scale, cudaStream_t stream,
+                                   float* lse, float* o_part, float* lse_part, int B, int Hq,
+                                   int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                                   int num_splits, float scale, cudaStream_t stream,
                                    int* status) {
-  if (D == 128)
-    return launch_window_impl<128>(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, window, sinks, scale,
-                                   stream, status);
-  return launch_window_impl<64>(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, window, sinks, scale, stream,
-                                status);
+  void* o_to = num_splits > 1 ? o_part : o;
+  float* lse_to = num_splits > 1 ? lse_part : lse;
+  const cudaError_t e =
+      D == 128 ? launch_window_impl<128>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
+                                         num_splits, scale, stream, status)
+               : launch_window_impl<64>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
+                                        num_splits, scale, stream, status);
+  if (e != cudaSuccess || num_splits == 1) return e;
+  return launch_combine_bf16(o_part, lse_part, o, lse, B * Hq * Sq, D, num_splits, stream);
 }
 
 cudaError_t launch_attn_fwd(const void* q, const void* k, const void* v, void* o, int o_bf16,

@@ -203,9 +203,9 @@ PyObject* call(Py_ssize_t given, Py_ssize_t n, F body) {
 }
 
 // ------------------------------------------------------------------ attention
-// q, k, v, window, sinks, scale, o, lse
+// q, k, v, window, sinks, scale, o, lse, num_splits
 PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 8, [&] {
+  return call(n, 9, [&] {
     const Tensor& q = bf16(a[0], "q", 4);
     const Tensor &k = bf16(a[1], "k", 4, &q), &v = bf16(a[2], "v", 4, &q);
     const Sizes s = sizes_of(q, k, v);
@@ -214,9 +214,19 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(q.device());
     Tensor o = output_bf16(a[6], q.sizes(), q.device(), "o");
     Tensor lse = output_f32(a[7], {s.B, s.Hq, s.Sq}, q.device(), "lse");
+    int splits = 0;
+    if (a[8] == Py_None)
+      raise_if(attn_window_fwd_num_splits(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, &splits),
+               "attn_window_fwd_num_splits");
+    else
+      splits = integer(a[8], "num_splits", LLONG_MIN, INT_MAX);
+    Tensor ws;
+    if (splits > 1)
+      ws = at::empty({static_cast<int64_t>(splits) * s.B * s.Hq * s.Sq * (s.D + 1)},
+                     at::TensorOptions().dtype(at::kFloat).device(q.device()));
     raise_if(attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
-                             s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, scale,
-                             current_stream(q.device())),
+                             ws.defined() ? floats(ws) : nullptr, s.B, s.Hq, s.Hkv, s.Sq, s.Sk,
+                             s.D, window, sinks, splits, scale, current_stream(q.device())),
              "attn_window_fwd");
     return pack({o, lse});
   });
@@ -314,13 +324,11 @@ PyObject* decode(const Tensor& q, const Cache& c, PyObject* const* a, const char
   const c10::cuda::CUDAGuard guard(device);
   void* stream = current_stream(device);
   int splits = 0;
-  if (a[3] == Py_None) {
-    const long long keys = std::min<long long>(c.Sk, static_cast<long long>(window) + sinks);
-    raise_if(attn_decode_num_splits(B, Hq, c.Hkv, static_cast<int>(keys), D, &splits),
-             "attn_decode_num_splits");
-  } else {
+  if (a[3] == Py_None)
+    raise_if(attn_decode_window_num_splits(B, Hq, c.Hkv, c.Sk, D, window, sinks, &splits),
+             "attn_decode_window_num_splits");
+  else
     splits = integer(a[3], "num_splits", LLONG_MIN, INT_MAX);
-  }
   Tensor o = output_bf16(a[7], {B, Hq, D}, device, "o");
   Tensor lse = output_f32(a[8], {B, Hq}, device, "lse");
   Tensor part, lse_part, counters;

@@ -10,21 +10,35 @@
 
 namespace attn {
 
-// KV tiles [0, s) and [w, e) with s <= w < e, or none (e = 0).  The window part of
-// a tile's rows runs from its first row's window start to its last row's
-// position; sink tiles that meet it are counted to it (s = w: one run).
+// KV tiles [b, s) and [w, e) in that order, or none (e = 0).  Of a whole query tile
+// b = 0 and s <= w < e: [0, s) holds sinks and [w, e) runs from its first row's window
+// start to its last row's position (sink tiles that meet it are counted to it).  A
+// run of steps of such a list (steps()) has the same form; without tiles of one part
+// b = s = 0, or w = e = s.  e - 1 is always the last tile.
 struct TileRange {
-  int s, w, e;
-  __device__ __forceinline__ int first() const { return s > 0 ? 0 : w; }
+  int b, s, w, e;
+  __device__ __forceinline__ int first() const { return b < s ? b : w; }
   __device__ __forceinline__ int next(int j) const { return j + 1 == s ? w : j + 1; }
-  __device__ __forceinline__ bool has(int j) const { return j < s || (j >= w && j < e); }
-  __device__ __forceinline__ int count() const { return e > 0 ? s + e - w : 0; }
-  __device__ __forceinline__ int tile(int step) const { return step < s ? step : step - s + w; }
+  __device__ __forceinline__ bool has(int j) const {
+    return (j >= b && j < s) || (j >= w && j < e);
+  }
+  __device__ __forceinline__ int count() const { return s - b + e - w; }
+  __device__ __forceinline__ int tile(int step) const {  // of a whole list
+    return step < s ? step : step - s + w;
+  }
+  // Steps [x, y) of a whole list, y clamped to its end.
+  __device__ __forceinline__ TileRange steps(int x, int y) const {
+    y = min(y, count());
+    if (x >= y) return {0, 0, 0, 0};
+    if (x >= s) return {0, 0, w + x - s, w + y - s};
+    if (y <= s) return {x, y, y, y};
+    return {x, s, w, w + y - s};
+  }
 };
 
 __device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window, int sinks,
                                                      int row_first) {
-  TileRange r = {0, 0, 0};
+  TileRange r = {0, 0, 0, 0};
   const int row_last = min(row_first + 127, Sq - 1);
   const int hi = row_last + Sk - Sq + 1;  // keys [0, hi) up to the last row's position
   if (row_first >= Sq || hi <= 0) return r;
@@ -32,6 +46,27 @@ __device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window,
   r.w = max(row_first + Sk - Sq - window + 1, 0) / 128;
   r.s = min((min(sinks, hi) + 127) / 128, r.w);
   return r;
+}
+
+// The tiles of two neighbouring query tiles as one list (it may hold a tile that
+// neither needs).
+__device__ __forceinline__ TileRange tile_union(const TileRange& x, const TileRange& y) {
+  if (x.e == 0) return y;
+  if (y.e == 0) return x;
+  TileRange u;
+  const bool xs = x.b < x.s, ys = y.b < y.s;
+  u.b = xs && ys ? min(x.b, y.b) : (xs ? x.b : y.b);
+  u.s = max(x.s, y.s);
+  const bool xw = x.w < x.e, yw = y.w < y.e;
+  u.w = xw && yw ? min(x.w, y.w) : (xw ? x.w : y.w);
+  u.e = max(x.e, y.e);
+  if (!xw && !yw) {
+    u.w = u.e = u.s;
+  } else if (u.s >= u.w) {  // the parts meet: one run from the lower begin
+    if (u.b < u.s) u.w = min(u.w, u.b);
+    u.b = u.s = 0;
+  }
+  return u;
 }
 
 // Masks of 32 columns as bits: one test per column, where the comparisons of the

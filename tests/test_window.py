@@ -131,8 +131,24 @@ def test_a_window_over_everything_is_the_causal_forward(B, Hq, Hkv, Sq, Sk, D):
     q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, 5)
     want = attn.attn_fwd_bf16o(q, k, v, causal=True)
     for window, sinks in ((Sk, 0), (2 ** 31 + 5, 0), (1, Sk), (7, 2 ** 40)):
-        got = attn.attn_window_fwd(q, k, v, window, sinks)
+        got = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=1)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES + [(1, 4, 2, 40, 3000, 64, 1500, 300)])
+@pytest.mark.parametrize("splits", [2, 3, 7, None])
+def test_forward_in_splits(shape, splits):
+    # Also splits without a tile, splits of sinks alone, and row pairs whose tiles' runs differ.
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    if splits is not None and splits > -(-Sk // 128):
+        pytest.skip("more splits than key tiles")
+    q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, Sq + 3 * Sk)
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=splits)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    ref, tol = reference(q, k, v, window, sinks, 1.0 / math.sqrt(D))
+    check("o", o, ref["o"], tol["o"])
+    check("lse", lse, ref["lse"], tol["lse"])
 
 
 @pytest.mark.gpu
@@ -388,8 +404,9 @@ def _lib():
 
 
 def fwd(q=A, k=A, v=A, o=A, lse=A, B=1, Hq=2, Hkv=1, Sq=8, Sk=8, D=64, window=4, sinks=1,
-        scale=0.125):
-    return _lib().attn_window_fwd(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, window, sinks, scale, None)
+        scale=0.125, ws=None, ns=1):
+    return _lib().attn_window_fwd(q, k, v, o, lse, ws, B, Hq, Hkv, Sq, Sk, D, window, sinks, ns, scale,
+                                  None)
 
 
 def bwd(q=A, k=A, v=A, o=A, lse=A, do=A, dq=A, dk=A, dv=A, ws=A, B=1, Hq=2, Hkv=1, Sq=8, Sk=8, D=64,
@@ -416,10 +433,34 @@ COMMON = [
 
 
 @pytest.mark.parametrize("call,kw,code", [(f, kw, c) for f in (fwd, bwd) for kw, c in COMMON] + [
+    (fwd, dict(ns=0), attn.ATTN_ERR_INVALID_ARG),
+    (fwd, dict(ns=-3, ws=A), attn.ATTN_ERR_INVALID_ARG),
+    (fwd, dict(ns=2, Sk=300), attn.ATTN_ERR_INVALID_ARG),        # no workspace
+    (fwd, dict(ns=4, Sk=300, ws=A), attn.ATTN_ERR_INVALID_ARG),  # three key tiles
+    (fwd, dict(ns=2, Sk=300, ws=M), attn.ATTN_ERR_MISALIGNED),
+    (fwd, dict(ns=2, Sk=300, ws=A, Sq=1 << 30), attn.ATTN_ERR_UNSUPPORTED),
     (bwd, dict(ws=None), attn.ATTN_ERR_INVALID_ARG),
     (bwd, dict(dk=M), attn.ATTN_ERR_MISALIGNED)])
 def test_prefill_and_backward_reject(call, kw, code):
     assert call(**kw) == code
+
+
+def test_forward_split_rule():
+    n = ctypes.c_int(0)
+    rule = _lib().attn_window_fwd_num_splits
+    assert rule(1, 2, 1, 8, 8, 64, 4, 1, None) == attn.ATTN_ERR_INVALID_ARG
+    assert rule(1, 2, 1, 8, 8, 64, 0, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert rule(1, 2, 1, 8, 1 << 20, 64, 500, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 1
+
+
+def test_decode_split_rule():
+    n = ctypes.c_int(0)
+    rule = _lib().attn_decode_window_num_splits
+    assert rule(1, 2, 1, 100, 64, 4, 1, None) == attn.ATTN_ERR_INVALID_ARG
+    assert rule(1, 2, 1, 0, 64, 4, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert rule(1, 2, 1, 100, 64, 0, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert rule(1, 3, 2, 100, 64, 4, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert rule(1, 2, 1, 1 << 30, 64, 100, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 1
 
 
 def test_backward_workspace():
