@@ -471,8 +471,7 @@ ATTN_API int attn_decode_window_paged(const void *q, const void *k_cache, const 
  * count falls by one.  seqlens[b] < 0 marks a finished row: all its pages go.  A
  * window as long as the rows (INT_MAX) gives up only what lies behind them.
  *   block_table_out [B,max_pages], refs_out [num_pages]; each may be its input.
- *   window >= 1, sinks >= 0, room >= 0.  A page whose count is not positive sets
- *   ATTN_ERR_INVALID_ARG in the status word (and is counted down all the same).
+ *   window >= 1, sinks >= 0, room >= 0.
  */
 ATTN_API int attn_pages_free(const int *block_table, const int *refs, const int *seqlens,
                              int *block_table_out, int *refs_out, int B, int max_pages,

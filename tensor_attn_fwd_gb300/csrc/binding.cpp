@@ -114,9 +114,31 @@ Tensor output_f32(PyObject* given, at::IntArrayRef shape, at::Device device, con
 Tensor output_int32(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
   return output(given, shape, at::kInt, "int32", device, name);
 }
-Tensor new_int32(at::IntArrayRef shape, at::Device device) {
-  return at::empty(shape, at::TensorOptions().dtype(at::kInt).device(device));
+Tensor new_int32(int64_t n, at::Device device) {
+  return at::empty({n}, at::TensorOptions().dtype(at::kInt).device(device));
 }
+
+// Tensors that share one allocation of int32: an allocation and its tensor cost
+// over a microsecond each, a further tensor on its storage a tenth of that.
+class Carver {
+ public:
+  Carver(int64_t n, at::Device device) : all_(new_int32(n, device)) {}
+  Tensor take(at::IntArrayRef shape) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(all_.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), all_.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(at_);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    at_ += t.numel();
+    return t;
+  }
+
+  void skip_to(int64_t at) { at_ = at; }
+
+ private:
+  Tensor all_;
+  int64_t at_ = 0;
+};
+int64_t padded(int64_t n) { return (n + 3) / 4 * 4; }  // to 16 bytes of int32
 
 // An integer in [least, most]; larger ones (all keys, all room) become `most`.
 int integer(PyObject* obj, const char* name, long long least, long long most) {
@@ -424,8 +446,17 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int window = a[4] == Py_None ? static_cast<int>(kAll) : integer(a[4], "window", 1, kAll);
     const int sinks = integer(a[5], "sinks", 0, kAll), room = integer(a[6], "room", 0, kAll);
     const c10::cuda::CUDAGuard guard(p.device);
-    Tensor table = output_int32(a[7], {p.B, p.M}, p.device, "block_table_out");
-    Tensor refs = output_int32(a[8], {p.P}, p.device, "refs_out");
+    Tensor table, refs;
+    if (a[7] == Py_None && a[8] == Py_None) {
+      const int64_t entries = padded(static_cast<int64_t>(p.B) * p.M);
+      Carver results(entries + p.P, p.device);
+      table = results.take({p.B, p.M});
+      results.skip_to(entries);
+      refs = results.take({p.P});
+    } else {
+      table = output_int32(a[7], {p.B, p.M}, p.device, "block_table_out");
+      refs = output_int32(a[8], {p.P}, p.device, "refs_out");
+    }
     raise_if(attn_pages_free(ints(p.table), ints(p.refs), ints(lens), ints(table), ints(refs), p.B,
                              p.M, p.P, page, window, sinks, room, current_stream(p.device)),
              "attn_pages_free");
@@ -436,7 +467,7 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
 Tensor pages_workspace(const Pages& p, int rows) {
   long long n = 0;
   raise_if(attn_pages_workspace(p.P, rows, &n), "attn_pages_workspace");
-  return new_int32({n}, p.device);
+  return new_int32(n, p.device);
 }
 
 // block_table, refs, seqlens, parents, page_size, room
@@ -450,9 +481,10 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int room = integer(a[5], "room", 0, kAll);
     const c10::cuda::CUDAGuard guard(p.device);
     Tensor ws = pages_workspace(p, R);
-    Tensor table = new_int32({R, p.M}, p.device), refs = new_int32({p.P}, p.device);
-    Tensor lens_out = new_int32({R}, p.device), src = new_int32({R}, p.device);
-    Tensor dst = new_int32({R}, p.device), counts = new_int32({2}, p.device);
+    Carver results(static_cast<int64_t>(R) * p.M + p.P + 3ll * R + 2, p.device);
+    Tensor table = results.take({R, p.M}), refs = results.take({p.P});
+    Tensor lens_out = results.take({R}), src = results.take({R}), dst = results.take({R});
+    Tensor counts = results.take({2});
     raise_if(attn_pages_fork(ints(p.table), ints(p.refs), ints(lens), ints(parents), ints(table),
                              ints(refs), ints(lens_out), ints(src), ints(dst), ints(counts),
                              ints(ws), p.B, R, p.M, p.P, page, room, current_stream(p.device)),
@@ -467,9 +499,10 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Pages p = pages_of(a[0], a[1]);
     const c10::cuda::CUDAGuard guard(p.device);
     Tensor ws = pages_workspace(p, 0);
-    Tensor table = new_int32({p.B, p.M}, p.device), refs = new_int32({p.P}, p.device);
-    Tensor src = new_int32({p.P / 2}, p.device), dst = new_int32({p.P / 2}, p.device);
-    Tensor live = new_int32({1}, p.device);
+    Carver results(static_cast<int64_t>(p.B) * p.M + p.P + 2ll * (p.P / 2) + 1, p.device);
+    Tensor table = results.take({p.B, p.M}), refs = results.take({p.P});
+    Tensor src = results.take({p.P / 2}), dst = results.take({p.P / 2});
+    Tensor live = results.take({1});
     raise_if(attn_pages_compact(ints(p.table), ints(p.refs), ints(table), ints(refs), ints(src),
                                 ints(dst), ints(live), ints(ws), p.B, p.M, p.P,
                                 current_stream(p.device)),

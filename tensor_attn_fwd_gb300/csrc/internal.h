@@ -175,10 +175,8 @@ inline long long window_bwd_delta_floats(int B, int Hq, int Sq) {
 long long window_bwd_workspace_floats(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
                                       int sinks);
 
-// Page bookkeeping (pages.cu): P pages, a table of B rows x M slots.  Calls whose
-// largest array has at most kPagesClusterWork elements run as one cluster.
+// Page bookkeeping (pages.cu): P pages, a table of B rows x M slots.
 constexpr int kPagesMaxCtas = 512;
-constexpr long long kPagesClusterWork = 1 << 16;
 // int32 workspace of launch_pages_fork (R new rows) and launch_pages_compact (R = 0).
 inline long long pages_workspace(int P, int R) { return 2ll * P + R + 2 * kPagesMaxCtas; }
 cudaError_t launch_pages_free(const int* table, const int* refs, const int* seqlens,

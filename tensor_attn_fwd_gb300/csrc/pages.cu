@@ -8,18 +8,28 @@
 // their order changes nothing.  The host never reads back, so the calls can be
 // captured in a graph between decode steps.
 //
-// Each operation is a few phases with a barrier between them, which every CTA
-// enters:
+// Each operation is a few phases with a barrier between them:
 //   free     1 copy refs              2 give up the references
 //   fork     1 copy refs, count free  2 count holders, list free pages, copy the
 //            read-only slots          3 count the pages each row needs
 //            4 hand them out
 //   compact  1 count live             2 list holes and movers   3 renumber
-// Bound: the bytes of the tables for large ones, latency for the usual few
-// thousand entries.  A small call is one launch of one cluster of 8 CTAs, whose
-// barrier is the hardware's; a large one launches one grid per phase (phases()).
+// What a call costs beyond the tables' bytes is latency: round trips to L2 that follow
+// each other, and the barriers.  So the number of CTAs that take part grows with the
+// call (us for fork / compact / free, graph replays):
+//   one CTA, lists and counters in shared memory (run_small; fork and compact):
+//     8 x 48 slots, 600 pages 5.0 / 2.8; 32 x 64, 4000 6.8 / 5.3; 64 x 64, 6000 9.3 / 11.6
+//   one cluster of 16 CTAs and the hardware's barrier, up to 2^15 elements:
+//     64 x 64, 6000 - / 8.0 / 4.9; 128 x 128, 16000 11.1 / 8.2 / 5.0; 256 x 128, 30000
+//     13.5 / 10.0 / 5.0; 256 x 256, 60000 17.6 / 13.2 / 5.0 (clusters of 8: 24.9 / 18.9 / 7.7)
+//   a cooperative grid of 1024 elements a CTA, at most one CTA an SM: 128 x 128, 16000
+//     14.0 / 9.7 / 4.9; 256 x 128, 30000 14.3 / 10.2 / 5.0; 256 x 256, 60000 14.1 / 10.3
+//     / 5.0; 1024 x 2048, 2 M 44.5 / 35.6 / 11.0 (a launch per phase: 64.4 / 52.0 / 12.5).
+//     Bound there by the L2's rate of scattered 4-byte atomics.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -33,7 +43,11 @@ using namespace ptx;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kClusterCtas = 8;
+// The largest calls (elements of arrays) of one CTA, and of one cluster.
+constexpr long long kSmallForkEntries = 8192, kSmallForkPages = 6144, kSmallForkSlots = 8192;
+constexpr long long kSmallCompactEntries = 8192, kSmallCompactPages = 4096;
+constexpr long long kClusterWork = 1 << 15;
+constexpr int kClusterCtas = 16;  // past the portable 8: the kernels opt in
 
 __device__ __forceinline__ void record_status(int* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
@@ -89,6 +103,10 @@ __device__ __forceinline__ int sum_counts(const int* counts, int n, int* smem) {
   return block_sum(x, smem);
 }
 
+// Place of element i in a shared array that threads read in runs: a word of padding
+// every 32 keeps the runs of a warp in different banks.
+__host__ __device__ __forceinline__ constexpr int pad(int i) { return i + (i >> 5); }
+
 // A table entry: a page, or -1 (an entry that is neither is reported and read as -1).
 __device__ __forceinline__ int checked_entry(int e, int num_pages, int* status) {
   if (e >= num_pages || e < -1) {
@@ -98,17 +116,34 @@ __device__ __forceinline__ int checked_entry(int e, int num_pages, int* status) 
   return e;
 }
 
-// The phases [first, last) with the grid's barrier between them: in a cluster
-// launch all of them and the cluster's barrier, else one phase a launch.
-template <typename Op>
-__global__ void __launch_bounds__(kThreads, 1) pages_kernel(const Op op, int first, int last) {
+// Phases [first, last).  kCluster: one cluster and its barrier; else a cooperative
+// grid and its (every CTA is resident, and each enters every barrier).
+enum Span { kCluster, kGrid };
+template <typename Op, Span SPAN>
+__global__ void __launch_bounds__(kThreads, 1) pages_phases_kernel(const Op op) {
   __shared__ int smem[32];
+  if constexpr (SPAN == kCluster) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
+  for (int ph = 0; ph < Op::kPhases; ++ph) {
+    op.run(ph, smem);
+    if (ph + 1 == Op::kPhases) break;
+    if constexpr (SPAN == kCluster)
+      cluster_sync();
+    else
+      cooperative_groups::this_grid().sync();
+  }
+}
+
+// A small call: one CTA.
+template <typename Op>
+__global__ void __launch_bounds__(kThreads, 1) pages_small_kernel(const Op op) {
+  __shared__ int smem[32];
+  extern __shared__ int lists[];
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int ph = first; ph < last; ++ph) {
-    op.run(ph, smem);
-    if (ph + 1 < last) cluster_sync();
-  }
+  op.run_small(smem, lists);
 }
 
 // ------------------------------------------------------------------ free
@@ -117,28 +152,63 @@ struct FreeOp {
   const int *table, *refs, *seqlens;
   int *table_out, *refs_out;
   int B, M, P, page_size, window, sinks, room;
+  int refs_vec, table_vec;  // 16-byte accesses are aligned
   int* status;
 
+  // Slots s, s + 1, ... of a row of `len` keys, holding e: the pages kept, or -1 for
+  // those given up.
+  template <int N>
+  __device__ __forceinline__ void settle(int (&e)[N], int s, int len) const {
+    bool drop[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      e[i] = checked_entry(e[i], P, status);
+      // A slot is kept when the row goes on and the slot holds a key that the next
+      // decode reads (the window of seqlens, the sinks) or that is still to come.
+      const int lo = (s + i) * page_size;
+      const bool keep = len >= 0 && lo < static_cast<long long>(len) + room &&
+                        (lo + page_size > len - window || lo < sinks);
+      drop[i] = !keep && e[i] >= 0;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (drop[i]) {
+        atomicSub(refs_out + e[i], 1);  // (its result unused: a reduction in L2)
+        e[i] = -1;
+      }
+  }
+  __device__ __forceinline__ int length(int b) const { return min(seqlens[b], M * page_size); }
+
   __device__ void run(int ph, int*) const {
-    const int tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+    const unsigned tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+    // Four at a time where the arrays allow it: the whole of refs in 16-byte vectors,
+    // and the tables if their rows are multiples of four slots.
     if (ph == 0) {
-      if (refs != refs_out)
-        for (int p = tid; p < P; p += n_threads) refs_out[p] = refs[p];
+      if (refs == refs_out) return;
+      const unsigned vecs = refs_vec ? P / 4 : 0;
+      for (unsigned i = tid; i < vecs; i += n_threads)
+        reinterpret_cast<int4*>(refs_out)[i] = reinterpret_cast<const int4*>(refs)[i];
+      for (unsigned p = 4 * vecs + tid; p < static_cast<unsigned>(P); p += n_threads)
+        refs_out[p] = refs[p];
       return;
     }
     const unsigned entries = static_cast<unsigned>(B) * M;  // < 2^31: i cannot wrap
-    for (unsigned i = tid; i < entries; i += n_threads) {
-      const int b = i / static_cast<unsigned>(M), s = i - b * M;
-      const int e = checked_entry(table[i], P, status);
-      const int len = min(seqlens[b], M * page_size);
-      // A slot is kept when the row goes on and the slot holds a key that the next
-      // decode reads (the window of seqlens, the sinks) or that is still to come.
-      const int lo = s * page_size;
-      const bool keep = len >= 0 && lo < static_cast<long long>(len) + room &&
-                        (lo + page_size > len - window || lo < sinks);
-      if (!keep && e >= 0 && atomicSub(refs_out + e, 1) <= 0)
-        record_status(status, ATTN_ERR_INVALID_ARG);  // more holders than were counted
-      table_out[i] = keep ? e : -1;
+    if (table_vec) {
+      const unsigned row_vecs = M / 4;
+      for (unsigned i = tid; i < entries / 4; i += n_threads) {
+        const int b = i / row_vecs, s = 4 * (i - b * row_vecs), len = length(b);
+        const int4 x = reinterpret_cast<const int4*>(table)[i];
+        int e[4] = {x.x, x.y, x.z, x.w};
+        settle(e, s, len);
+        reinterpret_cast<int4*>(table_out)[i] = make_int4(e[0], e[1], e[2], e[3]);
+      }
+    } else {
+      for (unsigned i = tid; i < entries; i += n_threads) {
+        const int b = i / static_cast<unsigned>(M);
+        int e[1] = {table[i]};
+        settle(e, i - b * M, length(b));
+        table_out[i] = e[0];
+      }
     }
   }
 };
@@ -293,6 +363,114 @@ struct ForkOp {
       }
     }
   }
+
+  // One CTA, everything but the tables in shared memory.  The slots to be written are
+  // numbered r * W + j, j < W = room / page_size + 2, which is their order, so each
+  // thread takes a run of them and one prefix sum ranks the pages they need.
+  static int small_slots(int room, int page_size) { return room / page_size + 2; }
+  static size_t small_bytes(int P, int R) {
+    return (pad(P) + 2ll * P + 2ll * R) * sizeof(int);
+  }
+  __device__ void run_small(int* smem, int* lists) const {
+    int* held = lists;       // holders other than slots to be written; then refs_out
+    int* low = held + pad(P);     // lowest (r, slot) that would write the page
+    int* free_at = low + P;  // free pages, ascending
+    int* parent = free_at + P;
+    int* len = parent + R;
+    const int t = threadIdx.x;
+    const int per = (P + kThreads - 1) / kThreads;  // pages of a thread, in one run
+    const int p0 = min(t * per, P), p1 = min(p0 + per, P);
+    int n = 0;
+    for (int p = t; p < P; p += kThreads) {
+      held[pad(p)] = refs[p];
+      low[p] = INT_MAX;
+    }
+    for (int r = t; r < R; r += kThreads) {
+      const Row x = row(r);
+      parent[r] = x.parent;
+      len[r] = x.len;
+    }
+    __syncthreads();
+    for (int p = p0; p < p1; ++p) n += held[pad(p)] == 0;
+    int n_free;
+    int k = block_scan(n, smem, n_free);
+    for (int p = p0; p < p1; ++p)
+      if (held[pad(p)] == 0) free_at[k++] = p;
+    __syncthreads();
+    const unsigned entries = B * M, new_entries = R * M;
+    for (unsigned i = t; i < entries; i += kThreads) {
+      const int e = checked_entry(table[i], P, status);
+      if (e >= 0) atomicSub(held + pad(e), 1);
+    }
+    const auto slot_end = [&](int r) {
+      const long long end = (static_cast<long long>(len[r]) + room + page_size - 1) / page_size;
+      return parent[r] < 0 ? 0 : static_cast<int>(min(end, static_cast<long long>(M)));
+    };
+    for (unsigned i = t; i < new_entries; i += kThreads) {
+      const int r = i / static_cast<unsigned>(M), s = i - r * M;
+      const int lo = len[r] / page_size;
+      int e = -1;
+      if (s < lo || s < slot_end(r)) e = checked_entry(table[parent[r] * M + s], P, status);
+      if (s < lo) {
+        if (e >= 0) atomicAdd(held + pad(e), 1);
+      } else if (e >= 0) {
+        atomicMin(low + e, static_cast<int>(i));
+        e = -1;
+      }
+      table_out[i] = e;
+    }
+    __syncthreads();
+    const int W = room / page_size + 2, slots = R * W;
+    const int run = (slots + kThreads - 1) / kThreads;
+    const int f0 = min(t * run, slots), f1 = min(f0 + run, slots);
+    // Slot f's entry; -2 if it is past its row's end.  `stays`: its page is its own.
+    const auto entry = [&](int f, int& r, int& s, bool& stays) {
+      r = f / W;
+      s = len[r] / page_size + f - r * W;
+      stays = false;
+      if (s >= slot_end(r)) return -2;
+      const int e = checked_entry(table[parent[r] * M + s], P, nullptr);
+      stays = e >= 0 && low[e] == r * M + s && held[pad(e)] == 0;
+      return e;
+    };
+    n = 0;
+    int r, s;
+    bool stays;
+    for (int f = f0; f < f1; ++f) n += entry(f, r, s, stays) != -2 && !stays;
+    int needed;
+    k = block_scan(n, smem, needed);  // its barrier: nobody reads held as it was any more
+    // A row without slots to write has nothing to copy; the others set theirs below.
+    for (int f = f0; f < f1; ++f) {
+      int e = entry(f, r, s, stays);
+      // Only a row's first slot to write can hold keys already.
+      const bool first = f == r * W, holds_keys = first && e != -2 && s * page_size < len[r];
+      const int from = e;
+      int length = len[r];
+      bool copied = false;
+      if (e != -2) {
+        if (!stays) {
+          e = k < n_free ? free_at[k] : -1;
+          ++k;
+          copied = holds_keys && from >= 0 && e >= 0;
+          if (holds_keys && e < 0) length = s * page_size;  // no page left for the keys
+        }
+        table_out[r * M + s] = e;
+        if (e >= 0) low[e] = -1;  // taken: one more holder, and nobody's lowest
+      }
+      if (first) {
+        src[r] = copied ? from : -1;
+        dst[r] = copied ? e : -1;
+        seqlens_out[r] = length;
+      }
+    }
+    if (t == 0) {
+      counts[0] = needed;
+      counts[1] = n_free;
+      if (needed > n_free) record_status(status, ATTN_ERR_NO_PAGES);
+    }
+    __syncthreads();
+    for (int p = t; p < P; p += kThreads) refs_out[p] = low[p] == -1 ? 1 : held[pad(p)];
+  }
 };
 
 // ------------------------------------------------------------------ compact
@@ -366,6 +544,59 @@ struct CompactOp {
       }
     }
   }
+
+  // One CTA: the new id of every page in shared memory, a run of pages per thread.
+  static size_t small_bytes(int P) { return (pad(P) + P / 2) * sizeof(int); }
+  __device__ void run_small(int* smem, int* lists) const {
+    int* to = lists;       // the page's count, then its new id (-1: not live)
+    int* holes = to + pad(P);   // free ids below n_live, ascending
+    const int t = threadIdx.x;
+    const int per = (P + kThreads - 1) / kThreads;
+    const int p0 = min(t * per, P), p1 = min(p0 + per, P);
+    for (int p = t; p < P; p += kThreads) to[pad(p)] = refs[p];
+    __syncthreads();
+    int n = 0;
+    for (int p = p0; p < p1; ++p) n += to[pad(p)] > 0;
+    int n_live;
+    const int before = block_scan(n, smem, n_live);  // live pages below p0
+    n = 0;
+    for (int p = p0; p < min(p1, n_live); ++p) n += to[pad(p)] > 0;
+    const int stay = block_sum(n, smem), moves = n_live - stay;
+    int k = before;
+    for (int p = p0; p < p1; ++p) {
+      if (to[pad(p)] > 0)
+        ++k;
+      else if (p < n_live)
+        holes[p - k] = p;
+    }
+    __syncthreads();
+    k = before;
+    for (int p = p0; p < p1; ++p) {
+      const int c = to[pad(p)];
+      int id = -1;
+      if (c > 0) {
+        id = p < n_live ? p : holes[k - stay];
+        if (p >= n_live) {
+          src[k - stay] = p;
+          dst[k - stay] = id;
+        }
+        refs_out[id] = c;
+        ++k;
+      }
+      if (p >= n_live) refs_out[p] = 0;
+      to[pad(p)] = id;
+    }
+    for (int i = moves + t; i < P / 2; i += kThreads) src[i] = dst[i] = -1;
+    if (t == 0) *num_live = n_live;
+    __syncthreads();
+    const unsigned entries = B * M;
+    for (unsigned i = t; i < entries; i += kThreads) {
+      const int e = checked_entry(table[i], P, status);
+      const int id = e >= 0 ? to[pad(e)] : -1;
+      if (e >= 0 && id < 0) record_status(status, ATTN_ERR_INVALID_ARG);  // counts no holder
+      table_out[i] = id;
+    }
+  }
 };
 
 // ------------------------------------------------------------------ copies
@@ -407,44 +638,75 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 // ------------------------------------------------------------------ host side
 template <typename Op>
-cudaError_t launch(const Op& op, long long work, cudaStream_t stream) {
+cudaError_t launch_small(const Op& op, size_t smem, cudaStream_t stream) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(pages_small_kernel<Op>),
+                                           static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_programmatic(pages_small_kernel<Op>, dim3(1), dim3(kThreads), smem, stream, op);
+}
+
+// The opt-in to clusters of kClusterCtas, once per device.
+template <typename Op>
+cudaError_t allow_cluster() {
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (allowed.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(pages_phases_kernel<Op, kCluster>),
+                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// work: elements of the largest array.
+template <typename Op>
+cudaError_t launch_phases(const Op& op, long long work, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kClusterCtas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  if (work <= kPagesClusterWork) {
+  cudaError_t e;
+  if (work <= kClusterWork) {
+    if ((e = allow_cluster<Op>()) != cudaSuccess) return e;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kClusterCtas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(kClusterCtas, 1, 1);
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_kernel<Op>, op, 0, Op::kPhases);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, pages_phases_kernel<Op, kCluster>, op);
+  } else {
+    const long long ctas = (work + kThreads - 1) / kThreads;
+    const int most = sm_count() < kPagesMaxCtas ? sm_count() : kPagesMaxCtas;
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, pages_phases_kernel<Op, kGrid>, op);
   }
-  const long long ctas = (work + 4 * kThreads - 1) / (4 * kThreads);
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas < kPagesMaxCtas ? ctas : kPagesMaxCtas), 1, 1);
-  cfg.numAttrs = 1;
-  for (int ph = 0; ph < Op::kPhases; ++ph) {
-    cudaError_t e = cudaLaunchKernelEx(&cfg, pages_kernel<Op>, op, ph, ph + 1);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
 cudaError_t launch_pages_free(const int* table, const int* refs, const int* seqlens,
                               int* table_out, int* refs_out, int B, int M, int P, int page_size,
                               int window, int sinks, int room, cudaStream_t stream, int* status) {
-  const FreeOp op{table, refs, seqlens, table_out, refs_out, B,    M,
-                  P,     page_size, window, sinks, room, status};
+  FreeOp op{table, refs, seqlens, table_out, refs_out, B, M, P, page_size, window, sinks, room};
+  op.refs_vec = aligned16(refs) && aligned16(refs_out);
+  op.table_vec = M % 4 == 0 && aligned16(table) && aligned16(table_out);
+  op.status = status;
   const long long entries = static_cast<long long>(B) * M;
-  return launch(op, entries > P ? entries : P, stream);
+  return launch_phases(op, entries > P ? entries : P, stream);
 }
 
 cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seqlens,
@@ -465,7 +727,10 @@ cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seql
   op.room = room;
   op.status = status;
   const long long entries = static_cast<long long>(B > R ? B : R) * M;
-  return launch(op, entries > P ? entries : P, stream);
+  if (entries <= kSmallForkEntries && P <= kSmallForkPages &&
+      static_cast<long long>(R) * ForkOp::small_slots(room, page_size) <= kSmallForkSlots)
+    return launch_small(op, ForkOp::small_bytes(P, R), stream);
+  return launch_phases(op, entries > P ? entries : P, stream);
 }
 
 cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_out, int* refs_out,
@@ -479,7 +744,9 @@ cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_o
   op.P = P;
   op.status = status;
   const long long entries = static_cast<long long>(B) * M;
-  return launch(op, entries > P ? entries : P, stream);
+  if (entries <= kSmallCompactEntries && P <= kSmallCompactPages)
+    return launch_small(op, CompactOp::small_bytes(P), stream);
+  return launch_phases(op, entries > P ? entries : P, stream);
 }
 
 cudaError_t launch_pages_copy(void* k, void* v, const int* src, const int* dst, int n,
