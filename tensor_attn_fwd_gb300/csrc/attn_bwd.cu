@@ -58,6 +58,9 @@ constexpr int kBwdThreads = 320;
 constexpr int kBwdMmaWarp = 8;
 constexpr int kBwdLoadWarp = 9;
 constexpr int kGradThreads = 256;
+constexpr int kDqDeltaWarp = 10;  // windowed dQ: warps 10 and 11 compute Delta
+constexpr int kDqWinThreads = 384;
+constexpr uint32_t kDqDeltaBytes = 2 * 128 * sizeof(float);
 constexpr int kStages = 2;
 constexpr uint32_t kSub = 128 * 128;  // [128 rows x 64 bf16] 128B-swizzled sub-tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -78,7 +81,7 @@ struct BwdCfg {
   // dQ smem: Q and dO fixed, a K ring and a V ring, barriers.
   static constexpr size_t kSmemDq =
       1024 + kFixed + size_t(kKStages + kVStages) * kTile + kBarBytes;
-  static_assert(kSmem <= 232448 && kSmemDq <= 232448, "shared memory per CTA");
+  static_assert(kSmem <= 232448 && kSmemDq + kDqDeltaBytes <= 232448, "shared memory per CTA");
   static constexpr uint32_t kColS = 0, kColDP = 128, kColA0 = 256, kColA1 = 256 + D;
   static constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescTS = idesc_bf16_f32(128, D, false, true);
@@ -96,6 +99,8 @@ struct BwdBars {
   uint64_t mma_done;
   // persistent dQ kernel: Q/dO buffer reusable; dQ accumulator b complete / read out
   uint64_t q_empty, acc_full2[2], acc_free[2];
+  // windowed dQ: Delta of a tile is in shared memory / has been read (two buffers)
+  uint64_t delta_full[2], delta_free[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -112,6 +117,10 @@ struct BwdParams {
   // Windowed kernels: the visibility of window.cuh, and bf16 gradients (out0, out1
   // point at bf16).
   int window, sinks;
+  // Windowed dQ, which runs first: it computes Delta from O and dO for its tiles and
+  // leaves it in delta_out for dK/dV.
+  const __nv_bfloat16 *o, *dout;
+  float* delta_out;
   // Windowed dK/dV: the first split_tiles key tiles (those with sinks, which every
   // later row sees) are cut along their steps into `parts` CTAs each.  Part i of
   // such a tile writes fp32 partials, [part][tile][B * Hkv][128][D], dK's then dV's,
@@ -198,37 +207,50 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16* __r
   if (lane == 0) delta[row] = acc;
 }
 
-// Delta for a bf16 O: D / 8 lanes a row, each one 16-byte load of O and of dO for
-// four rows at a time (bound by the two reads).
-constexpr int kDeltaRows = 4;
+// Delta of 32 consecutive rows by one warp: lane l returns row row0 + l's.  D / 8 lanes
+// read a row's O and dO in 16-byte loads, 256 / D rows at a time; the lanes' partial
+// sums are reduced and spread by exchanging halves (each exchange halves the values
+// a lane carries).  Rows from `rows` on read the last row.
 template <int D>
-__global__ void __launch_bounds__(256)
-    window_delta_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ o,
-                        float* __restrict__ delta, int rows) {
-  constexpr int L = D / 8;  // lanes a row
-  const int lane = threadIdx.x % L;
-  const int row0 = blockIdx.x * (256 / L) * kDeltaRows + threadIdx.x / L;
-  uint4 a[kDeltaRows], b[kDeltaRows];
+__device__ __forceinline__ float warp_delta(const __nv_bfloat16* o, const __nv_bfloat16* dout,
+                                            long long row0, long long rows, int lane) {
+  constexpr int L = D / 8;        // lanes a row
+  constexpr int R = 32 / L;       // rows at a time
+  constexpr int N = 32 / R;       // values a lane starts with (= L)
+  float acc[N];
 #pragma unroll
-  for (int i = 0; i < kDeltaRows; ++i) {
-    const int row = min(row0 + i * (256 / L), rows - 1);
-    a[i] = __ldg(dout + static_cast<size_t>(row) * L + lane);
-    b[i] = __ldg(o + static_cast<size_t>(row) * L + lane);
-  }
+  for (int i0 = 0; i0 < N; i0 += 4) {
+    uint4 a[4], b[4];
 #pragma unroll
-  for (int i = 0; i < kDeltaRows; ++i) {
-    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-    float acc = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {  // a bf16 is the upper half of its float
-      acc = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), acc);
-      acc = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), acc);
+    for (int i = 0; i < 4; ++i) {
+      const long long row = min(row0 + (i0 + i) * R + lane / L, rows - 1);
+      a[i] = __ldg(reinterpret_cast<const uint4*>(o) + row * L + lane % L);
+      b[i] = __ldg(reinterpret_cast<const uint4*>(dout) + row * L + lane % L);
     }
 #pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    const int row = row0 + i * (256 / L);
-    if (lane == 0 && row < rows) delta[row] = acc;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // a bf16 is the upper half of its float
+        sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+        sum = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), sum);
+      }
+      acc[i0 + i] = sum;
+    }
   }
+  // Lane l ends with value l % L of its group of L lanes: row (l % L) * R + l / L.
+#pragma unroll
+  for (int m = L / 2; m > 0; m >>= 1) {
+    const bool upper = lane & m;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float give = upper ? acc[i] : acc[i + m];
+      const float keep = upper ? acc[i + m] : acc[i];
+      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+    }
+  }
+  return __shfl_sync(0xffffffffu, acc[0], (lane % R) * L + lane / R);
 }
 
 // ------------------------------------------------------------------ shared pieces
@@ -419,6 +441,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
+  if constexpr (WIN) {  // launched as a dependent of dQ, which leaves Delta
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
 
   if (warp == kBwdLoadWarp) {
     if (nsteps > 0) {
@@ -712,6 +738,8 @@ __global__ void __launch_bounds__(256)
     bwd_sum_parts_kernel(const float* __restrict__ partials, __nv_bfloat16* __restrict__ dk,
                          __nv_bfloat16* __restrict__ dv, int split_tiles, int parts, int BH,
                          int Sk) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const size_t plane = static_cast<size_t>(split_tiles) * BH * 128 * D;
   const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   const int row = static_cast<int>(at / D);  // (tile * BH + bg) * 128 + key of the tile
@@ -769,7 +797,7 @@ struct DqTiles {
 };
 
 template <int D, bool WIN = false>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ CUtensorMap tmDO, const BwdParams p) {
@@ -782,6 +810,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint8_t* sK = smem + C::kFixed;                // K ring: kKStages tiles
   uint8_t* sV = sK + kKStages * C::kTile;        // V ring: kVStages tiles
   BwdBars* bars = reinterpret_cast<BwdBars*>(sV + kVStages * C::kTile);
+  float* sDelta = reinterpret_cast<float*>(sV + kVStages * C::kTile + C::kBarBytes);  // [2][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // Work: query tile m of head (b, h), numbered m-major with the highest m first.
@@ -808,6 +837,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->acc_full2[b], 1);
       mbar_init(&bars->acc_free[b], kGradThreads / 32);
+      if constexpr (WIN) {
+        mbar_init(&bars->delta_full[b], 2);
+        mbar_init(&bars->delta_free[b], kGradThreads / 32);
+      }
     }
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -822,6 +855,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
+  if constexpr (WIN) {  // launched as a dependent of the kernel before (the forward)
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
 
   if (warp == kBwdLoadWarp) {
     uint32_t G = 0;   // first global step of the current tile
@@ -943,6 +980,37 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // Every MMA this warp issued completes before TMEM is released.
     tc_commit_w(&bars->mma_done);
     (void)mbar_wait(&bars->mma_done, 0);
+  } else if (WIN && warp >= kDqDeltaWarp) {
+    // Delta, a tile or two ahead of the gradient warps: 64 rows a warp, from global
+    // memory, to shared memory for them and to delta_out for dK/dV.  (By the gradient
+    // warps themselves, at a tile's start, the loads' latency cost more than a kernel
+    // of its own for Delta: 8192 rows, 32 heads, D = 128: 561 against 552 us a step.)
+    int kt = 0;
+    for (int rnd = 0; ok; ++rnd) {
+      const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
+      if (idx >= total) break;
+      const int m = mtiles - 1 - idx / BH, bh = idx % BH;
+      const int nsteps = DqTiles<WIN>(p, m).nsteps;
+      const int buf = kt & 1;
+      if (nsteps > 0 && kt >= 2) {
+        ok = __all_sync(0xffffffffu, bwd_wait(&bars->delta_free[buf], ((kt >> 1) - 1) & 1, bars));
+        if (!ok) break;
+      }
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int r = 64 * (warp - kDqDeltaWarp) + 32 * i;
+        const long long row0 = static_cast<long long>(bh) * p.Sq + 128 * m + r;
+        const float dlt =
+            warp_delta<D>(p.o, p.dout, row0, static_cast<long long>(BH) * p.Sq, lane);
+        if (128 * m + r + lane < p.Sq) p.delta_out[row0 + lane] = dlt;
+        if (nsteps > 0) sDelta[128 * buf + r + lane] = dlt;
+      }
+      if (nsteps > 0) {
+        mbar_arrive_warp(&bars->delta_full[buf]);
+        ++kt;
+      }
+    }
+    if (!ok) bwd_record(p.status);
   } else {
     // Gradient warps: thread r owns query row 128m + r (TMEM lane r); warpgroup
     // `half` handles keys [64*half, 64*half + 64) of each tile.
@@ -981,7 +1049,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       const float lse2 = row_valid ? __ldg(p.lse + static_cast<size_t>(bh) * p.Sq + row) * kLog2e
                                    : 0.f;
-      const float dlt = row_valid ? __ldg(p.delta + static_cast<size_t>(bh) * p.Sq + row) : 0.f;
+      float dlt = 0.f;
+      if constexpr (WIN) {
+        const int buf = kt & 1;
+        ok = __all_sync(0xffffffffu, bwd_wait(&bars->delta_full[buf], (kt >> 1) & 1, bars));
+        if (!ok) break;
+        dlt = row_valid ? sDelta[128 * buf + r] : 0.f;
+        mbar_arrive_warp(&bars->delta_free[buf]);
+      } else {
+        dlt = row_valid ? __ldg(p.delta + static_cast<size_t>(bh) * p.Sq + row) : 0.f;
+      }
       const uint64_t nl2 = f2_pack(-lse2, -lse2);
       const uint64_t ndl = f2_pack(-dlt, -dlt);
       const int key_hi = WIN || p.causal ? min(p.Sk - 1, row + p.Sk - p.Sq) : p.Sk - 1;
@@ -1113,17 +1190,13 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
                             float* delta, int B, int Hq, int Hkv, int Sq, int Sk, int causal,
                             int window, int sinks, float scale, cudaStream_t stream, int* status) {
   using C = BwdCfg<D>;
-  const int rows = B * Hq * Sq;
-  if constexpr (WIN) {
-    const int per_cta = 256 / (D / 8) * kDeltaRows;
-    window_delta_kernel<D><<<(rows + per_cta - 1) / per_cta, 256, 0, stream>>>(
-        static_cast<const uint4*>(dout), static_cast<const uint4*>(o), delta, rows);
-  } else {
+  cudaError_t e = cudaSuccess;
+  if constexpr (!WIN) {
+    const int rows = B * Hq * Sq;
     bwd_delta_kernel<D><<<(rows + 7) / 8, 256, 0, stream>>>(
         static_cast<const __nv_bfloat16*>(dout), static_cast<const float*>(o), delta, rows);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   CUtensorMap tmQ, tmK, tmV, tmDO;
   if (!encode_bf16_map(&tmQ, q, D, Sq, B * Hq, 128) ||
       !encode_bf16_map(&tmK, k, D, Sk, B * Hkv, 128) ||
@@ -1134,7 +1207,8 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
                             static_cast<int>(C::kSmem))) != cudaSuccess)
     return e;
   if ((e = ensure_smem_attr(reinterpret_cast<const void*>(bwd_dq_kernel<D, WIN>),
-                            static_cast<int>(C::kSmemDq))) != cudaSuccess)
+                            static_cast<int>(C::kSmemDq + (WIN ? kDqDeltaBytes : 0)))) !=
+      cudaSuccess)
     return e;
   BwdParams p;
   p.lse = lse;
@@ -1150,35 +1224,51 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
   p.scale_log2 = scale * kLog2e;
   p.window = window;
   p.sinks = sinks;
-  p.out0 = static_cast<float*>(dk);
-  p.out1 = static_cast<float*>(dv);
   p.split_tiles = 0;
   p.parts = 1;
   p.partials = nullptr;
+  p.o = static_cast<const __nv_bfloat16*>(WIN ? o : nullptr);
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.delta_out = delta;
+  const int q_tiles = B * Hq * ((Sq + 127) / 128);
+  const int q_ctas = q_tiles < sm_count() ? q_tiles : sm_count();
+  const int kv_tiles = (Sk + 127) / 128;
   if constexpr (WIN) {
+    // dQ first (it computes Delta), each kernel the programmatic dependent of the last.
     const SinkSplit split = sink_split(B, Hq, Hkv, Sq, Sk, window, sinks);
     p.split_tiles = split.tiles;
     p.parts = split.parts;
     p.partials = delta + window_bwd_delta_floats(B, Hq, Sq);
+    p.out0 = static_cast<float*>(dq);
+    p.out1 = nullptr;
+    if ((e = launch_programmatic(bwd_dq_kernel<D, true>, dim3(q_ctas), dim3(kDqWinThreads),
+                                 C::kSmemDq + kDqDeltaBytes, stream, tmQ, tmK, tmV, tmDO, p)) !=
+        cudaSuccess)
+      return e;
+    p.out0 = static_cast<float*>(dk);
+    p.out1 = static_cast<float*>(dv);
+    const int kv_ctas = B * Hkv * (kv_tiles + p.split_tiles * (p.parts - 1));
+    if ((e = launch_programmatic(bwd_dkdv_kernel<D, true>, dim3(kv_ctas), dim3(kBwdThreads),
+                                 C::kSmem, stream, tmQ, tmK, tmV, tmDO, p)) != cudaSuccess)
+      return e;
+    if (p.split_tiles == 0) return cudaSuccess;
+    const size_t vecs = static_cast<size_t>(p.split_tiles) * B * Hkv * 128 * (D / 4);
+    return launch_programmatic(bwd_sum_parts_kernel<D>,
+                               dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0,
+                               stream, p.partials, static_cast<__nv_bfloat16*>(dk),
+                               static_cast<__nv_bfloat16*>(dv), p.split_tiles, p.parts, B * Hkv,
+                               Sk);
+  } else {
+    p.out0 = static_cast<float*>(dk);
+    p.out1 = static_cast<float*>(dv);
+    bwd_dkdv_kernel<D><<<B * Hkv * kv_tiles, kBwdThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, tmDO,
+                                                                            p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    p.out0 = static_cast<float*>(dq);
+    p.out1 = nullptr;
+    bwd_dq_kernel<D><<<q_ctas, kBwdThreads, C::kSmemDq, stream>>>(tmQ, tmK, tmV, tmDO, p);
+    return cudaGetLastError();
   }
-  const int kv_ctas = B * Hkv * ((Sk + 127) / 128 + p.split_tiles * (p.parts - 1));
-  bwd_dkdv_kernel<D, WIN><<<kv_ctas, kBwdThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, tmDO, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if constexpr (WIN) {
-    if (p.split_tiles > 0) {
-      const size_t vecs = static_cast<size_t>(p.split_tiles) * B * Hkv * 128 * (D / 4);
-      bwd_sum_parts_kernel<D><<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(
-          p.partials, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
-          p.split_tiles, p.parts, B * Hkv, Sk);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-  }
-  p.out0 = static_cast<float*>(dq);
-  p.out1 = nullptr;
-  const int q_tiles = B * Hq * ((Sq + 127) / 128);
-  const int q_ctas = q_tiles < sm_count() ? q_tiles : sm_count();
-  bwd_dq_kernel<D, WIN><<<q_ctas, kBwdThreads, C::kSmemDq, stream>>>(tmQ, tmK, tmV, tmDO, p);
-  return cudaGetLastError();
 }
 
 }  // namespace
