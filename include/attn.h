@@ -362,10 +362,10 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const float *
  *      undefined; not touched, and NULL allowed, with one split
  *   D 64 or 128 (else ATTN_ERR_UNSUPPORTED).  Sizes, alignment, other errors and
  *   rows that see no key (O = 0, LSE = -inf) as attn_fwd.
- *   K and V have to be finite in every 128-key tile (keys [128n, 128n + 128)) that
- *   holds a key some row sees: a masked key has weight 0 in its tile, and 0 times
- *   a V that is not finite is NaN.  (As in attn_fwd; the decode form has no such
- *   condition.)
+ *   Keys that no row sees may hold anything (NaN, unwritten memory).  K and V have to
+ *   be finite at keys that some row sees: one that is not finite reaches, beside the
+ *   rows that see it, rows of their 128-row query tiles that do not (a weight of 0
+ *   times NaN is NaN; as in attn_fwd).
  */
 ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
                              float *workspace, int B, int Hq, int Hkv, int Sq, int Sk, int D,
@@ -390,7 +390,8 @@ ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, 
  *   workspace: attn_window_bwd_workspace floats, caller-owned, contents undefined
  *      (Delta, and partial sums of the key tiles that hold sinks: every later row
  *      sees those, so their work is split and added up in a fixed order)
- *   Same arguments and errors as attn_window_fwd; all pointers 16-byte aligned.
+ *   Same arguments, conditions and errors as attn_window_fwd (q, dout and o finite);
+ *   all pointers 16-byte aligned.
  */
 ATTN_API int attn_window_bwd(const void *q, const void *k, const void *v, const void *o,
                              const float *lse, const void *dout, void *dq, void *dk, void *dv,

@@ -30,7 +30,7 @@ struct AttrEntry {
   int bytes;
   uint64_t device_mask;
 };
-constexpr int kAttrSlots = 32;  // one per kernel instantiation that sets its shared memory size
+constexpr int kAttrSlots = 64;  // one per kernel instantiation that sets its shared memory size
 AttrEntry g_attr[kAttrSlots];
 int g_attr_n = 0;
 

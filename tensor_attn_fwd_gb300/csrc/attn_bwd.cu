@@ -366,7 +366,7 @@ __device__ __forceinline__ void store_acc_row16(uint32_t taddr, __nv_bfloat16* d
 }
 
 // ------------------------------------------------------------------ dK / dV
-template <int D, bool WIN = false>
+template <int D, Mask WIN = kNoWindow>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -477,6 +477,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == kBwdMmaWarp) {
     if (nsteps > 0) {
       ok = bwd_wait_w(&bars->fixed_full, 0, bars);
+      if constexpr (WIN == kUnseen) {
+        const int unseen = unseen_end(p.Sq, p.Sk, p.window);
+        zero_unseen_rows<D>(sK, 128 * n, p.sinks, unseen, lane);
+        zero_unseen_rows<D>(sV, 128 * n, p.sinks, unseen, lane);
+      }
       const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV);
       // S^T = K Q^T of step s (its Q/dO stage must have landed) and dP^T = V dO^T.
       auto issue_s = [&](int s) -> bool {  // this lane's wait outcome
@@ -776,7 +781,7 @@ __device__ __forceinline__ int dq_tile_index(int round, int cta, int grid) {
 }
 
 // The KV tiles of query tile m: step s reads tile kv_tile(s), s < nsteps.
-template <bool WIN>
+template <Mask WIN>
 struct DqTiles {
   int nsteps;
   TileRange r;
@@ -796,7 +801,7 @@ struct DqTiles {
   }
 };
 
-template <int D, bool WIN = false>
+template <int D, Mask WIN = kNoWindow>
 __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV,
@@ -917,16 +922,22 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
   } else if (warp == kBwdMmaWarp) {
     const uint32_t q_addr = smem_u32(sQ), do_addr = smem_u32(sDO);
     const uint32_t k_base = smem_u32(sK), v_base = smem_u32(sV);
-    auto issue_s = [&](uint32_t g) -> bool {  // S = Q K^T; this lane's wait outcome
+    const int unseen = WIN == kUnseen ? unseen_end(p.Sq, p.Sk, p.window) : 0;
+    // Step g's products; `tile` is its KV tile.
+    auto issue_s = [&](uint32_t g, int tile) -> bool {  // S = Q K^T; this lane's wait outcome
       const int sk = g % kKStages;
       const bool got = bwd_wait(&bars->full[sk], (g / kKStages) & 1, bars);
+      if constexpr (WIN == kUnseen)
+        zero_unseen_rows<D>(sK + sk * C::kTile, 128 * tile, p.sinks, unseen, lane);
       mma_ss_tile<D>(tmem, C::kColS, q_addr, k_base + sk * C::kTile);
       tc_commit_w(&bars->s_full);
       return got;
     };
-    auto issue_dp = [&](uint32_t g) -> bool {  // dP = dO V^T; V(g) is free afterwards
+    auto issue_dp = [&](uint32_t g, int tile) -> bool {  // dP = dO V^T; V(g) is free afterwards
       const int sv = g % kVStages;
       const bool got = bwd_wait(&bars->full_v[sv], (g / kVStages) & 1, bars);
+      if constexpr (WIN == kUnseen)
+        zero_unseen_rows<D>(sV + sv * C::kTile, 128 * tile, p.sinks, unseen, lane);
       mma_ss_tile<D>(tmem, C::kColDP, do_addr, v_base + sv * C::kTile);
       tc_commit_w(&bars->dp_full);
       tc_commit_w(&bars->empty_v[sv]);
@@ -938,7 +949,8 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
-      const int nsteps = DqTiles<WIN>(p, mtiles - 1 - idx / BH).nsteps;
+      const DqTiles<WIN> tiles(p, mtiles - 1 - idx / BH);
+      const int nsteps = tiles.nsteps;
       if (nsteps == 0) continue;
       const int buf = kt & 1;
       const uint32_t acc_col = buf ? C::kColA1 : C::kColA0;
@@ -948,8 +960,8 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
       // S(G) overwrites the S columns once the previous step's S has been read.
       if (G > 0) good &= bwd_wait(&bars->p_ready, (G - 1) & 1, bars);
       tc_fence_after();
-      good &= issue_s(G);
-      good &= issue_dp(G);
+      good &= issue_s(G, tiles.kv_tile(0));
+      good &= issue_dp(G, tiles.kv_tile(0));
       if (nsteps == 1) tc_commit_w(&bars->q_empty);  // last S and dP of the tile issued
       for (int s = 0; s < nsteps; ++s) {
         const uint32_t g = G + s;
@@ -957,7 +969,7 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         if (s + 1 < nsteps) {
           good &= bwd_wait(&bars->p_ready, g & 1, bars);
           tc_fence_after();
-          good &= issue_s(g + 1);
+          good &= issue_s(g + 1, tiles.kv_tile(s + 1));
         }
         // ... dQ += dS K once dS(g) is in TMEM (K MN-major: its rows are the K dim) ...
         good &= bwd_wait(&bars->ds_full, g & 1, bars);
@@ -967,7 +979,7 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         // ... then dP(g+1), which overwrites dS(g) after dQ has read it.  After
         // the tile's last dP, Q and dO may be replaced by the next tile's.
         if (s + 1 < nsteps) {
-          good &= issue_dp(g + 1);
+          good &= issue_dp(g + 1, tiles.kv_tile(s + 1));
           if (s + 2 == nsteps) tc_commit_w(&bars->q_empty);
         }
       }
@@ -1184,7 +1196,7 @@ SinkSplit sink_split(int B, int Hq, int Hkv, int Sq, int Sk, int window, int sin
 
 // o, dq, dk and dv are fp32, or bf16 in the windowed form (window > 0), whose
 // `delta` is followed by the partials of the split sink tiles.
-template <int D, bool WIN>
+template <int D, Mask WIN>
 cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const void* o,
                             const float* lse, const void* dout, void* dq, void* dk, void* dv,
                             float* delta, int B, int Hq, int Hkv, int Sq, int Sk, int causal,
@@ -1241,14 +1253,14 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
     p.partials = delta + window_bwd_delta_floats(B, Hq, Sq);
     p.out0 = static_cast<float*>(dq);
     p.out1 = nullptr;
-    if ((e = launch_programmatic(bwd_dq_kernel<D, true>, dim3(q_ctas), dim3(kDqWinThreads),
+    if ((e = launch_programmatic(bwd_dq_kernel<D, WIN>, dim3(q_ctas), dim3(kDqWinThreads),
                                  C::kSmemDq + kDqDeltaBytes, stream, tmQ, tmK, tmV, tmDO, p)) !=
         cudaSuccess)
       return e;
     p.out0 = static_cast<float*>(dk);
     p.out1 = static_cast<float*>(dv);
     const int kv_ctas = B * Hkv * (kv_tiles + p.split_tiles * (p.parts - 1));
-    if ((e = launch_programmatic(bwd_dkdv_kernel<D, true>, dim3(kv_ctas), dim3(kBwdThreads),
+    if ((e = launch_programmatic(bwd_dkdv_kernel<D, WIN>, dim3(kv_ctas), dim3(kBwdThreads),
                                  C::kSmem, stream, tmQ, tmK, tmV, tmDO, p)) != cudaSuccess)
       return e;
     if (p.split_tiles == 0) return cudaSuccess;
@@ -1278,9 +1290,9 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const f
                             float* delta, int B, int Hq, int Hkv, int Sq, int Sk, int D,
                             int causal, float scale, cudaStream_t stream, int* status) {
   if (D == 128)
-    return launch_bwd_impl<128, false>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq,
+    return launch_bwd_impl<128, kNoWindow>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq,
                                        Sk, causal, 0, 0, scale, stream, status);
-  return launch_bwd_impl<64, false>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
+  return launch_bwd_impl<64, kNoWindow>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
                                     causal, 0, 0, scale, stream, status);
 }
 
@@ -1296,11 +1308,11 @@ cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, 
                                    void* dv, float* delta, int B, int Hq, int Hkv, int Sq, int Sk,
                                    int D, int window, int sinks, float scale, cudaStream_t stream,
                                    int* status) {
-  if (D == 128)
-    return launch_bwd_impl<128, true>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq,
-                                      Sk, 1, window, sinks, scale, stream, status);
-  return launch_bwd_impl<64, true>(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk,
-                                   1, window, sinks, scale, stream, status);
+  const auto launch = has_unseen(Sq, Sk, window, sinks)
+                          ? (D == 128 ? launch_bwd_impl<128, kUnseen> : launch_bwd_impl<64, kUnseen>)
+                          : (D == 128 ? launch_bwd_impl<128, kWindow> : launch_bwd_impl<64, kWindow>);
+  return launch(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Sq, Sk, 1, window, sinks,
+                scale, stream, status);
 }
 
 }  // namespace attn

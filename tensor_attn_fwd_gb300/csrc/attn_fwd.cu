@@ -127,7 +127,7 @@ struct Item {
 };
 
 // The KV tile after j in an item's stream.
-template <bool WIN>
+template <Mask WIN>
 __device__ __forceinline__ int next_tile(const Item& it, int j) {
   if constexpr (WIN)
     return it.u.next(j);
@@ -215,7 +215,7 @@ __device__ __forceinline__ int tile_bh(const FwdParams& p, const Item& it, int t
 //            1.5-2.5 % slower.  Under the causal mask, chunking the KV heads so
 //            that the heads in flight stay in L2 (the D = 256 kernel's ORDER 2)
 //            measured -3 to +3 % here, so causal launches keep ORDER 0.
-template <int ORDER, bool WIN>
+template <int ORDER, Mask WIN>
 __device__ __forceinline__ Item get_item(const FwdParams& p, int idx) {
   if constexpr (WIN) return get_window_item(p, idx);
   const int BH = p.B * p.Hq;
@@ -282,7 +282,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* 
 // elect.sync, so the warp reconverges by itself.
 
 // ------------------------------------------------------------------ producer
-template <int D, int ORDER, bool WIN>
+template <int D, int ORDER, Mask WIN>
 __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
                           const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* bars) {
   using C = Cfg<D>;
@@ -379,7 +379,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
 }
 
 // ------------------------------------------------------------------ MMA issuer
-template <int D, int ORDER, bool WIN>
+template <int D, int ORDER, Mask WIN>
 __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* bars,
                          uint32_t tmem) {
   using C = Cfg<D>;
@@ -396,6 +396,7 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
   const uint32_t q_lo = kLoK + (smem_u32(sQ) >> 4);
   const uint32_t k_lo = kLoK + (smem_u32(sKV) >> 4);
   const uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
+  const int unseen = WIN == kUnseen ? unseen_end(p.Sq, p.Sk, p.window) : 0;
   uint32_t kv_ctr = 0, q_ctr = 0;
   uint32_t p_phase[2] = {0, 0};
   bool ok = true;
@@ -480,6 +481,8 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
         nkst = kv_ctr % C::kStages;
         ++kv_ctr;
       }
+      if constexpr (WIN == kUnseen)
+        zero_unseen_rows<D>(sKV + vst * C::kTileBytes, 128 * j, p.sinks, unseen, threadIdx.x & 31);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if constexpr (WIN) {
@@ -519,7 +522,7 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
 }
 
 // ------------------------------------------------------------------ softmax
-template <int D, int ORDER, bool WIN>
+template <int D, int ORDER, Mask WIN>
 __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int warp, int lane) {
   using C = Cfg<D>;
   const int t = warp >> 2;
@@ -764,7 +767,7 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, int ORDER, bool WIN = false>
+template <int D, int ORDER, Mask WIN = kNoWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -894,7 +897,8 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   if (!encode_bf16_map(&tmQ, q, D, Sq, B * Hq, 128) || !encode_bf16_map(&tmK, k, D, Sk, B * Hkv, 128) ||
       !encode_bf16_map(&tmV, v, D, Sk, B * Hkv, 128))
     return cudaErrorInvalidValue;
-  auto kernel = attn_fwd_kernel<D, 0, true>;
+  auto kernel = has_unseen(Sq, Sk, window, sinks) ? attn_fwd_kernel<D, 0, kUnseen>
+                                                  : attn_fwd_kernel<D, 0, kWindow>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel),
                                          static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;

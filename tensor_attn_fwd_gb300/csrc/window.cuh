@@ -8,6 +8,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace attn {
 
 // KV tiles [b, s) and [w, e) in that order, or none (e = 0).  Of a whole query tile
@@ -67,6 +69,38 @@ __device__ __forceinline__ TileRange tile_union(const TileRange& x, const TileRa
     u.b = u.s = 0;
   }
   return u;
+}
+
+// The kernels' masks.  kUnseen is kWindow for calls with keys that no row sees (a
+// chunk against a longer sequence), which have to be kept from the products; the work
+// for it in the MMA warp's loop costs a training step, which has none, 2.4 %.
+enum Mask { kNoWindow = 0, kWindow = 1, kUnseen = 2 };
+
+// Keys [sinks, unseen_end) are seen by no row: the first row's window starts at
+// unseen_end.
+__host__ __device__ __forceinline__ int unseen_end(int Sq, int Sk, int window) {
+  return Sk - Sq - window + 1 > 0 ? Sk - Sq - window + 1 : 0;
+}
+inline bool has_unseen(int Sq, int Sk, int window, int sinks) {
+  return sinks < unseen_end(Sq, Sk, window);
+}
+// Their rows of a K or V tile of keys [key0, key0 + 128) in shared memory (128-byte
+// swizzled sub-tiles of 64 dims) become zero: memory that no row sees may hold NaN, and
+// a weight of 0 times NaN is NaN.  A whole warp, which afterwards may issue MMAs on
+// the tile; nothing to do but for the two tiles at the ends of the range.
+template <int D>
+__device__ __forceinline__ void zero_unseen_rows(uint8_t* tile, int key0, int sinks, int end,
+                                                 int lane) {
+  const int r0 = max(sinks - key0, 0), r1 = min(end - key0, 128);
+  if (r0 >= r1) return;
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+  for (int i = lane; i < (r1 - r0) * kChunks; i += 32) {
+    const int r = r0 + i / kChunks, c = i % kChunks;
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // Masks of 32 columns as bits: one test per column, where the comparisons of the

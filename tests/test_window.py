@@ -203,18 +203,23 @@ def test_sink_tiles_whose_rows_are_split(shape):
 
 
 @pytest.mark.gpu
-def test_unseen_keys_may_be_anything_outside_the_tiles_in_use():
-    # Keys that the window has passed, in tiles that no row sees.
-    B, Hq, Hkv, Sq, Sk, D, window, sinks = 1, 4, 2, 70, 1024, 128, 100, 5
+@pytest.mark.parametrize("shape", [(1, 4, 2, 70, 1024, 128, 100, 5), (2, 2, 2, 300, 900, 64, 130, 128),
+                                   (1, 3, 1, 40, 700, 128, 1, 0), (1, 2, 1, 1, 300, 64, 37, 200),
+                                   (1, 2, 1, 129, 2000, 64, 500, 300)])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_keys_that_no_row_sees_may_be_anything(shape, splits):
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
     q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, 8, grad=True)
-    want = attn.attn_window_fwd(q, k, v, window, sinks)
+    want = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=splits)
     gwant = attn.attn_window_bwd(q, k, v, *want, do, window, sinks)
+    unseen = ~visible(Sq, Sk, window, sinks).any(0)
+    assert bool(unseen.any())
     k2, v2 = k.clone(), v.clone()
-    first = (Sk - Sq - window + 1) // 128 * 128
-    k2[:, :, 128:first] = float("nan")
-    v2[:, :, 128:first] = float("inf")
-    got = attn.attn_window_fwd(q, k2, v2, window, sinks)
+    k2[:, :, unseen.cuda()] = float("nan")
+    v2[:, :, unseen.cuda()] = float("-inf")
+    got = attn.attn_window_fwd(q, k2, v2, window, sinks, num_splits=splits)
     ggot = attn.attn_window_bwd(q, k2, v2, *got, do, window, sinks)
+    assert attn.attn_debug_status() == attn.ATTN_OK
     for a, b in zip(got + ggot, want + gwant):
         assert torch.equal(a, b)
 
