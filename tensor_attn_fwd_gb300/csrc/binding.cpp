@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -96,10 +96,16 @@ const Tensor& int32(PyObject* obj, const char* name, at::IntArrayRef shape, at::
   return t;
 }
 
+// An uninitialised tensor, straight from the CUDA allocator (at::empty's dispatch
+// costs as much again as the allocation).
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, at::Device device) {
+  return at::detail::empty_cuda(shape, type, device, std::nullopt);
+}
+
 // The output that the caller gave, or a new one.
 Tensor output(PyObject* given, at::IntArrayRef shape, at::ScalarType type, const char* type_name,
               at::Device device, const char* name) {
-  if (given == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+  if (given == Py_None) return fresh(shape, type, device);
   const Tensor& t = tensor(given, name);
   check(t, name, type, type_name, static_cast<int>(shape.size()), device);
   check_shape(t, name, shape);
@@ -115,7 +121,7 @@ Tensor output_int32(PyObject* given, at::IntArrayRef shape, at::Device device, c
   return output(given, shape, at::kInt, "int32", device, name);
 }
 Tensor new_int32(int64_t n, at::Device device) {
-  return at::empty({n}, at::TensorOptions().dtype(at::kInt).device(device));
+  return fresh({n}, at::kInt, device);
 }
 
 // Tensors that share one allocation of int32: an allocation and its tensor cost
@@ -244,8 +250,8 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       splits = integer(a[8], "num_splits", LLONG_MIN, INT_MAX);
     Tensor ws;
     if (splits > 1)
-      ws = at::empty({static_cast<int64_t>(splits) * s.B * s.Hq * s.Sq * (s.D + 1)},
-                     at::TensorOptions().dtype(at::kFloat).device(q.device()));
+      ws = fresh({static_cast<int64_t>(splits) * s.B * s.Hq * s.Sq * (s.D + 1)}, at::kFloat,
+                 q.device());
     raise_if(attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
                              ws.defined() ? floats(ws) : nullptr, s.B, s.Hq, s.Hkv, s.Sq, s.Sk,
                              s.D, window, sinks, splits, scale, current_stream(q.device())),
@@ -277,7 +283,7 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
              "attn_window_bwd_workspace");
     Tensor ws;
     if (a[12] == Py_None) {
-      ws = at::empty({need}, at::TensorOptions().dtype(at::kFloat).device(q.device()));
+      ws = fresh({need}, at::kFloat, q.device());
     } else {
       ws = tensor(a[12], "workspace");
       check(ws, "workspace", at::kFloat, "float32", static_cast<int>(ws.dim()), q.device());
@@ -357,8 +363,7 @@ PyObject* decode(const Tensor& q, const Cache& c, PyObject* const* a, const char
   if (splits > 1) {
     if (a[5] == Py_None) {
       // One allocation: the partials, then their LSEs.
-      part = at::empty({static_cast<int64_t>(splits) * B * Hq * (D + 1)},
-                       at::TensorOptions().dtype(at::kFloat).device(device));
+      part = fresh({static_cast<int64_t>(splits) * B * Hq * (D + 1)}, at::kFloat, device);
     } else {
       part = output_f32(a[5], {splits, B, Hq, D}, device, "o_part");
       lse_part = output_f32(a[6], {splits, B, Hq}, device, "lse_part");

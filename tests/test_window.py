@@ -398,6 +398,52 @@ def test_training_step_in_a_graph_repeats_its_bits():
             assert torch.equal(a, b)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 4, 2, 301, 301, 64, 100, 4), (1, 4, 1, 129, 777, 128, 300, 5),
+                                   (1, 3, 3, 300, 129, 64, 40, 200), (1, 2, 1, 1300, 1300, 128, 60, 5)])
+def test_debug_build_stores_in_bounds_and_matches(shape):
+    # Every output store checked against its buffer (a stray one is skipped and reported).
+    from tensor_attn_fwd_gb300 import build as attn_build
+    dbg = ctypes.CDLL(attn_build.build(debug=True))
+    for name in ("attn_window_fwd", "attn_window_bwd", "attn_decode_window", "attn_debug_status"):
+        fn, like = getattr(dbg, name), getattr(attn.load_library(), name)
+        fn.argtypes, fn.restype = like.argtypes, like.restype
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, 21, grad=True)
+    scale, stream = 1.0 / math.sqrt(D), torch.cuda.current_stream().cuda_stream
+    floats = 4 * B * Hq * Sq * (D + 1)
+    n = ctypes.c_longlong(0)
+    attn.load_library().attn_window_bwd_workspace(*shape, ctypes.byref(n))
+    ws = torch.empty(max(floats, n.value), device="cuda")
+    for splits in (1, 2):
+        want = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=splits)
+        o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        assert dbg.attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                   lse.data_ptr(), ws.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
+                                   sinks, splits, scale, stream) == attn.ATTN_OK
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    want = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+    got = [torch.empty_like(t) for t in want]
+    assert dbg.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                               do.data_ptr(), *(t.data_ptr() for t in got), ws.data_ptr(), *shape,
+                               scale, stream) == attn.ATTN_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    qd = q[:, :, -1:].contiguous()
+    for splits in (1, 2):
+        want = attn.decode_window(qd, k, v, window, sinks, num_splits=splits)
+        got = [torch.empty_like(t) for t in want]
+        counters = torch.zeros(B * Hq, dtype=torch.int32, device="cuda")
+        part = ws[: splits * B * Hq * D]
+        lse_part = torch.empty(splits * B * Hq, device="cuda")
+        assert dbg.attn_decode_window(qd.data_ptr(), k.data_ptr(), v.data_ptr(), None,
+                                      got[0].data_ptr(), got[1].data_ptr(), part.data_ptr(),
+                                      lse_part.data_ptr(), counters.data_ptr(), B, Hq, Hkv, Sk, D,
+                                      window, sinks, splits, scale, stream) == attn.ATTN_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert dbg.attn_debug_status(None) == attn.ATTN_OK
+
+
 # ------------------------------------------------------------------ refusals (no GPU)
 A, M = 0x10000000, 0x10000004
 
