@@ -412,23 +412,21 @@ ATTN_API int attn_window_bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, i
  *
  *   q [B,Hq,1,D], k, v [B,Hkv,Sk,D] bf16; seqlens device int32 [B] or NULL
  *   o [B,Hq,D] bf16 (rounded once from fp32), lse [B,Hq] fp32, 16-byte aligned
- *   num_splits: the seen blocks are shared out evenly, ceil(blocks / num_splits)
- *      each.  With num_splits = 1, o_part, lse_part and counters may be NULL and
- *      are not touched; otherwise they are as attn_decode_fused (partials
- *      [num_splits,B,Hq,D] and [num_splits,B,Hq], zeroed counters).
+ *   num_splits: 1 to 16 (else ATTN_ERR_INVALID_ARG).  The seen blocks are shared out
+ *      evenly, ceil(blocks / num_splits) each, over the CTAs of one thread-block
+ *      cluster, which merge their partial results in shared memory: no workspace.
  *      attn_decode_window_num_splits gives a good count.
  *   window, sinks as attn_window_fwd; D in {64, 128, 256}; other arguments and
- *   errors as attn_decode_fused.  A sequence of length 0 gives O = 0, LSE = -inf.
+ *   errors as attn_decode_splitkv.  A sequence of length 0 gives O = 0, LSE = -inf.
  */
 ATTN_API int attn_decode_window(const void *q, const void *k, const void *v, const int *seqlens,
-                                void *o, float *lse, float *o_part, float *lse_part, int *counters,
-                                int B, int Hq, int Hkv, int Sk, int D, int window, int sinks,
-                                int num_splits, float scale, void *stream);
+                                void *o, float *lse, int B, int Hq, int Hkv, int Sk, int D,
+                                int window, int sinks, int num_splits, float scale, void *stream);
 
-/* A split count for attn_decode_window (paged: Sk = max_pages * page_size): that of
- * attn_decode_num_splits for the keys within reach, min(Sk, window + sinks), or more
- * where a few warps would walk them for long.  Host-only.  Errors as that function's,
- * and ATTN_ERR_INVALID_ARG for a bad window or sinks. */
+/* A split count for attn_decode_window on the current device (paged: Sk = max_pages *
+ * page_size), a measured rule of this library on the number of CTAs and of keys within
+ * reach, min(Sk, window + sinks).  Host-only.  ATTN_ERR_INVALID_ARG for non-positive
+ * sizes, Hq % Hkv != 0 or a bad window or sinks. */
 ATTN_API int attn_decode_window_num_splits(int B, int Hq, int Hkv, int Sk, int D, int window,
                                            int sinks, int *num_splits);
 
@@ -439,10 +437,9 @@ ATTN_API int attn_decode_window_num_splits(int B, int Hq, int Hkv, int Sk, int D
  */
 ATTN_API int attn_decode_window_paged(const void *q, const void *k_cache, const void *v_cache,
                                       const int *block_table, const int *seqlens, void *o,
-                                      float *lse, float *o_part, float *lse_part, int *counters,
-                                      int B, int Hq, int Hkv, int num_pages, int page_size,
-                                      int max_pages, int D, int window, int sinks, int num_splits,
-                                      float scale, void *stream);
+                                      float *lse, int B, int Hq, int Hkv, int num_pages,
+                                      int page_size, int max_pages, int D, int window, int sinks,
+                                      int num_splits, float scale, void *stream);
 
 /*
  * Pages of a KV cache, kept on the device.  A paged cache (attn_decode_splitkv_paged)

@@ -93,8 +93,8 @@ _SIGNATURES = {
     "attn_window_bwd": ([_vp] * 10 + [_int] * 8 + [_flt, _vp], _int),
     "attn_window_bwd_workspace": ([_int] * 8 + [ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_decode_window_num_splits": ([_int] * 7 + [ctypes.POINTER(_int)], _int),
-    "attn_decode_window": ([_vp] * 9 + [_int] * 8 + [_flt, _vp], _int),
-    "attn_decode_window_paged": ([_vp] * 10 + [_int] * 10 + [_flt, _vp], _int),
+    "attn_decode_window": ([_vp] * 6 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_decode_window_paged": ([_vp] * 7 + [_int] * 10 + [_flt, _vp], _int),
     "attn_pages_free": ([_vp] * 5 + [_int] * 7 + [_vp], _int),
     "attn_pages_fork": ([_vp] * 11 + [_int] * 6 + [_vp], _int),
     "attn_pages_compact": ([_vp] * 8 + [_int] * 3 + [_vp], _int),
@@ -765,44 +765,35 @@ def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
 
 def decode_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
                   seqlens: torch.Tensor | None = None, num_splits: int | None = None,
-                  scale: float | None = None, workspace=None, o: torch.Tensor | None = None,
-                  lse: torch.Tensor | None = None, counters: torch.Tensor | None = None,
-                  stream=None):
+                  scale: float | None = None, o: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, stream=None):
     """Decode one token under a sliding window with sinks, in one launch; returns
     (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
 
     q [B,Hq,1,D], k/v [B,Hkv,Sk,D] (bf16), D 64, 128 or 256.  The query stands at
     its sequence's last key (Sk keys, or its first seqlens[b]) and sees the last
-    ``window`` keys and the first ``sinks``.  ``num_splits=None`` picks
-    attn_decode_window_num_splits; ``workspace`` and ``counters`` as attn_decode_fused
-    (not used with one split).  Without ``counters`` a call captured
-    in a graph has its own.
+    ``window`` keys and the first ``sinks``.  ``num_splits`` (1 to 16) is the CTAs that
+    share a KV head's keys; None picks attn_decode_window_num_splits.
     """
     call = (_fast or _native()).decode_window
-    part, lse_part = (None, None) if workspace is None else workspace
     if stream is not None:
-        return _on_stream(stream, call, q, k, v, seqlens, window, sinks, num_splits, scale, part,
-                          lse_part, o, lse, counters)
-    return call(q, k, v, seqlens, window, sinks, num_splits, scale, part, lse_part, o, lse,
-                counters)
+        return _on_stream(stream, call, q, k, v, seqlens, window, sinks, num_splits, scale, o, lse)
+    return call(q, k, v, seqlens, window, sinks, num_splits, scale, o, lse)
 
 
 def decode_window_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                         block_table: torch.Tensor, seqlens: torch.Tensor, window: int,
                         sinks: int = 0, num_splits: int | None = None, scale: float | None = None,
-                        workspace=None, o: torch.Tensor | None = None,
-                        lse: torch.Tensor | None = None, counters: torch.Tensor | None = None,
+                        o: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                         stream=None):
     """decode_window over a paged cache (k_cache/v_cache [num_pages,Hkv,page_size,D],
     block_table int32 [B,max_pages], seqlens int32 [B], as decode_paged).  Entries of
     pages that hold no seen key are not read (attn_pages_free makes them -1)."""
     call = (_fast or _native()).decode_window_paged
-    part, lse_part = (None, None) if workspace is None else workspace
     if stream is not None:
         return _on_stream(stream, call, q, k_cache, v_cache, block_table, seqlens, window, sinks,
-                          num_splits, scale, part, lse_part, o, lse, counters)
-    return call(q, k_cache, v_cache, block_table, seqlens, window, sinks, num_splits, scale, part,
-                lse_part, o, lse, counters)
+                          num_splits, scale, o, lse)
+    return call(q, k_cache, v_cache, block_table, seqlens, window, sinks, num_splits, scale, o, lse)
 
 
 def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,

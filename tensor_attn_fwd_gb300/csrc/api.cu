@@ -96,6 +96,20 @@ cudaError_t ensure_smem_attr(const void* kernel, int bytes) {
   return cudaSuccess;
 }
 
+cudaError_t allow_large_cluster(const void* kernel) {
+  static const void* seen[kMaxDevices][16] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  int i = 0;
+  while (i < 16 && seen[dev][i] != nullptr && seen[dev][i] != kernel) ++i;
+  if (i < 16 && seen[dev][i] == kernel) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && i < 16) seen[dev][i] = kernel;  // (table full: set again next time)
+  return e;
+}
+
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
@@ -466,73 +480,83 @@ namespace {
 
 // Sk: the cache's capacity; paged: its layout, or nullptr (contiguous, [B,Hkv,Sk,D]).
 int decode_window_common(const void* q, const void* k, const void* v, const int* seqlens,
-                         const PagedKV* paged, void* o, float* lse, float* o_part,
-                         float* lse_part, int* counters, int B, int Hq, int Hkv, int Sk, int D,
-                         int window, int sinks, int num_splits, float scale, void* stream) {
-  if (!o || !lse || window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
-  // One split writes the result itself: no partials, no counters.
-  if (num_splits != 1 && (!o_part || !lse_part || !counters)) return ATTN_ERR_INVALID_ARG;
-  const int chk =
-      decode_check_args(q, k, v, B, Hq, Hkv, Sk, D, num_splits, scale, paged != nullptr);
+                         const PagedKV* paged, void* o, float* lse, int B, int Hq, int Hkv, int Sk,
+                         int D, int window, int sinks, int num_splits, float scale,
+                         void* stream) {
+  if (!o || !lse || window < 1 || sinks < 0 || num_splits > kWindowDecodeSplits)
+    return ATTN_ERR_INVALID_ARG;
+  // (Splits without a block of their own are empty: there may be more splits than keys.)
+  const int chk = decode_check_args(q, k, v, B, Hq, Hkv, Sk, D,
+                                    num_splits < 1 ? num_splits : 1, scale, paged != nullptr);
   if (chk != ATTN_OK) return chk;
-  if (!aligned16(o_part) || !aligned16(lse_part) || !aligned16(o) || !aligned16(lse))
-    return ATTN_ERR_MISALIGNED;
-  if ((reinterpret_cast<uintptr_t>(counters) & 3u) != 0 ||
-      (reinterpret_cast<uintptr_t>(seqlens) & 3u) != 0)
-    return ATTN_ERR_MISALIGNED;
+  if (!aligned16(o) || !aligned16(lse)) return ATTN_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(seqlens) & 3u) != 0) return ATTN_ERR_MISALIGNED;
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
-  const FusedCombine out{o, lse, counters};
   const cudaError_t e = launch_decode_window(
-      q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk, D, window < Sk ? window : Sk,
-      sinks < Sk ? sinks : Sk, num_splits, scale, static_cast<cudaStream_t>(stream), status, out);
+      q, k, v, seqlens, paged, o, lse, B, Hq, Hkv, Sk, D, window < Sk ? window : Sk,
+      sinks < Sk ? sinks : Sk, num_splits, scale, static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
 
 int attn_decode_window(const void* q, const void* k, const void* v, const int* seqlens, void* o,
-                       float* lse, float* o_part, float* lse_part, int* counters, int B, int Hq,
-                       int Hkv, int Sk, int D, int window, int sinks, int num_splits, float scale,
-                       void* stream) {
-  return decode_window_common(q, k, v, seqlens, nullptr, o, lse, o_part, lse_part, counters, B,
-                              Hq, Hkv, Sk, D, window, sinks, num_splits, scale, stream);
+                       float* lse, int B, int Hq, int Hkv, int Sk, int D, int window, int sinks,
+                       int num_splits, float scale, void* stream) {
+  return decode_window_common(q, k, v, seqlens, nullptr, o, lse, B, Hq, Hkv, Sk, D, window, sinks,
+                              num_splits, scale, stream);
 }
 
 int attn_decode_window_num_splits(int B, int Hq, int Hkv, int Sk, int D, int window, int sinks,
                                   int* num_splits) {
-  if (num_splits == nullptr || Sk <= 0 || window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  if (num_splits == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sk <= 0 || D <= 0 ||
+      Hq % Hkv != 0 || window < 1 || sinks < 0)
+    return ATTN_ERR_INVALID_ARG;
+  const long long n_sm = sm_count();
+  if (n_sm <= 0) return ATTN_ERR_CUDA;
   const long long reach = static_cast<long long>(window) + sinks;
-  const int keys = static_cast<int>(reach < Sk ? reach : Sk);
-  const int e = attn_decode_num_splits(B, Hq, Hkv, keys, D, num_splits);
-  if (e != ATTN_OK) return e;
-  // A short reach is bound by the latency of a warp's blocks one after the other (1.1
-  // us each; splitting costs 2.6 us).  From 16 blocks on at least as many splits as
-  // fit one round, of two blocks or more, up to 12: B1 Hkv8 D128, 1024 + 4 keys: 1
-  // split 13.5 us, 4 (the rule for long caches) 10.3, 12 9.0, 16 9.0; D64 2 10.2, 12
-  // 7.6; B4 4 10.4, 12 13.6; 128 + 4 keys: 1 split 5.8, 2 7.8.
-  const long long blocks = (static_cast<long long>(keys) + 31) / 32;
+  const long long blocks = ((reach < Sk ? reach : Sk) + 31) / 32;
+  // CTAs of one split.  Measured (us; 32 query heads a KV head's group of 4, keys seen):
   const long long base = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 15) / 16);
-  long long ns = sm_count() / base;
+  long long ns;
+  if (D == 64) {
+    // Two CTAs an SM or more: base 128, 4100 keys: 1 split 32.1, 2 23.6, 4 30.4.
+    ns = 2 * n_sm / base;
+  } else if (D == 256) {
+    // One CTA an SM: base 64, 2052 keys: 1 split 34.3, 2 27.5, 3 37.0.
+    ns = n_sm / base;
+  } else if (base * 5 >= n_sm * 4) {
+    ns = 1;  // base 128, 4100 keys: 1 split 44.4, 2 44.9
+  } else if (base >= 16) {
+    // About one CTA an SM, to a power of two: base 64, 1028 keys: 2 splits 10.2, 4 9.9, 6
+    // 16.3; base 32: 2 10.0, 4 8.0, 8 8.7; base 96, 4100 keys: 1 40.8, 2 35.6, 4 42.3.
+    ns = 1ll << std::lround(std::log2(static_cast<double>((n_sm + base - 1) / base)));
+  } else {
+    ns = n_sm / base;
+  }
+  // A split keeps two blocks (base 8, 260 keys: 1 split 6.8, 4 5.4, 8 5.6), and clusters
+  // past 12 pay only for few and long walks (base 8, 1028 keys: 8 splits 6.7, 12 6.2, 16 7.8;
+  // base 1, 16388 keys: 12 16.9, 16 15.0).
+  const long long most = base <= 4 && blocks >= 256 ? kWindowDecodeSplits : 12;
+  if (ns > most) ns = most;
   if (ns > blocks / 2) ns = blocks / 2;
-  if (ns > 12) ns = 12;
-  if (blocks >= 16 && ns > *num_splits) *num_splits = static_cast<int>(ns);
+  *num_splits = ns > 1 ? static_cast<int>(ns) : 1;
   return ATTN_OK;
 }
 
 int attn_decode_window_paged(const void* q, const void* k_cache, const void* v_cache,
                              const int* block_table, const int* seqlens, void* o, float* lse,
-                             float* o_part, float* lse_part, int* counters, int B, int Hq,
-                             int Hkv, int num_pages, int page_size, int max_pages, int D,
-                             int window, int sinks, int num_splits, float scale, void* stream) {
+                             int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages,
+                             int D, int window, int sinks, int num_splits, float scale,
+                             void* stream) {
   PagedKV paged;
   int capacity = 0;
   const int pchk = paged_check_args(block_table, seqlens, Hkv, num_pages, page_size, max_pages,
                                     D, B, &paged, &capacity);
   if (pchk != ATTN_OK) return pchk;
-  return decode_window_common(q, k_cache, v_cache, seqlens, &paged, o, lse, o_part, lse_part,
-                              counters, B, Hq, Hkv, capacity, D, window, sinks, num_splits, scale,
-                              stream);
+  return decode_window_common(q, k_cache, v_cache, seqlens, &paged, o, lse, B, Hq, Hkv, capacity,
+                              D, window, sinks, num_splits, scale, stream);
 }
 
 int attn_decode_splitkv_paged(const void* q, const void* k_cache, const void* v_cache,

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   constexpr int KS = D / 16;  // k-steps of S = Q K^T
   constexpr int NT = D / 8;   // n-tiles of O += P V
   extern __shared__ uint8_t smem_raw[];
+  __shared__ float split_lse[kRows];  // windowed, merged in the cluster
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
@@ -447,21 +448,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       }
       const size_t row = (static_cast<size_t>(split) * B + b) * Hq + hq;
       const size_t rows = static_cast<size_t>(num_splits) * B * Hq;  // debug bounds checks
-      if (WIN && num_splits == 1) {
-        // The only split is the result: no partials.
-        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(o_final) + row * D + part * DPT;
-        if (store_in_bounds(dst16, DPT * 2, o_final, rows * D * 2, status)) {
+      if constexpr (WIN) {
+        if (num_splits > 1) {
+          // Over the CTA's own partial sums: only this thread has read this part of them.
+          float* mine = red_o + r * D + part * DPT;
 #pragma unroll
-          for (int e = 0; e < DPT; e += 8)
-            *reinterpret_cast<uint4*>(dst16 + e) =
-                make_uint4(pack_bf16x2(out[e], out[e + 1]), pack_bf16x2(out[e + 2], out[e + 3]),
-                           pack_bf16x2(out[e + 4], out[e + 5]), pack_bf16x2(out[e + 6], out[e + 7]));
+          for (int e = 0; e < DPT; e += 4)
+            *reinterpret_cast<float4*>(mine + e) =
+                make_float4(out[e], out[e + 1], out[e + 2], out[e + 3]);
+          if (part == 0) split_lse[r] = lse;
+        } else {
+          // The only split is the result.
+          __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(o_final) + row * D + part * DPT;
+          if (store_in_bounds(dst16, DPT * 2, o_final, rows * D * 2, status)) {
+#pragma unroll
+            for (int e = 0; e < DPT; e += 8)
+              *reinterpret_cast<uint4*>(dst16 + e) = make_uint4(
+                  pack_bf16x2(out[e], out[e + 1]), pack_bf16x2(out[e + 2], out[e + 3]),
+                  pack_bf16x2(out[e + 4], out[e + 5]), pack_bf16x2(out[e + 6], out[e + 7]));
+          }
+          if (part == 0 &&
+              store_in_bounds(lse_final + row, 4, lse_final, rows * sizeof(float), status))
+            lse_final[row] = lse;
         }
-        if (part == 0 &&
-            store_in_bounds(lse_final + row, 4, lse_final, rows * sizeof(float), status))
-          lse_final[row] = lse;
-        return;
-      }
+      } else {
       float* dst = o_part + row * D + part * DPT;
       if (store_in_bounds(dst, DPT * 4, o_part, rows * D * sizeof(float), status)) {
 #pragma unroll
@@ -470,7 +480,57 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       }
       if (part == 0 && store_in_bounds(lse_part + row, 4, lse_part, rows * sizeof(float), status))
         lse_part[row] = lse;
+      }
     }
+  }
+
+  // Windowed: a group's splits are the CTAs of one cluster and read each other's
+  // partials from shared memory (attn_combine's formula, splits in order): no
+  // workspace, and no round trips to L2 for counter and partials.  B1, 32/8 heads, 1024
+  // + 4 keys in 12 splits: 6.2 us, through L2 9.0.
+  if constexpr (WIN) {
+    if (num_splits > 1) {
+      constexpr float kLog2e = 1.4426950408889634f;
+      cluster_sync();
+      const int rows = min(kRows, G - slice * kRows);
+      const uint32_t o_addr = smem_u32(red_o), l_addr = smem_u32(split_lse);
+      for (int i = split * (kWarps * 32) + threadIdx.x; i < rows * (D / 4);
+           i += num_splits * (kWarps * 32)) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        float M = -INFINITY;
+        for (int s = 0; s < num_splits; ++s)
+          M = fmaxf(M, ld_cluster_f32(mapa_shared(l_addr + 4 * r, s)));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float W = 0.f;
+        if (M != -INFINITY) {
+#pragma unroll 4
+          for (int s = 0; s < num_splits; ++s) {
+            const float w = ex2((ld_cluster_f32(mapa_shared(l_addr + 4 * r, s)) - M) * kLog2e);
+            const float4 x = ld_cluster_f32x4(mapa_shared(o_addr + (r * D + 4 * c) * 4, s));
+            W += w;
+            acc.x = fmaf(w, x.x, acc.x);
+            acc.y = fmaf(w, x.y, acc.y);
+            acc.z = fmaf(w, x.z, acc.z);
+            acc.w = fmaf(w, x.w, acc.w);
+          }
+          const float inv = 1.f / W;
+          acc.x *= inv;
+          acc.y *= inv;
+          acc.z *= inv;
+          acc.w *= inv;
+        }
+        const size_t row = static_cast<size_t>(b) * Hq + g * G + slice * kRows + r;
+        const size_t all = static_cast<size_t>(B) * Hq;
+        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(o_final) + row * D + 4 * c;
+        if (store_in_bounds(dst16, 8, o_final, all * D * 2, status))
+          *reinterpret_cast<uint2*>(dst16) =
+              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (c == 0 && store_in_bounds(lse_final + row, 4, lse_final, all * sizeof(float), status))
+          lse_final[row] = M == -INFINITY ? M : M + logf(W);
+      }
+      cluster_sync();  // no CTA leaves while another reads its shared memory
+    }
+    return;
   }
 
   // Fused combine (counters != nullptr): the CTA that completes a (batch, KV
@@ -481,7 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // barrier), the acquire in the last CTA makes every other CTA's visible.
   // The merge is combine_kernel's, warp by warp over the rows (lanes over the
   // splits), so both paths give the same bits; it reads through L2 (ld.cg).
-  if (counters != nullptr && !(WIN && num_splits == 1)) {
+  if (counters != nullptr) {
     __shared__ int s_last;
     __syncthreads();
     int* counter = counters + blockIdx.z * gridDim.y + blockIdx.y;
@@ -567,25 +627,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
           for (int e = 0; e < DPL; ++e) out[i][e] *= inv;
           L = M[i] + logf(W[i]);
-        }
-        if constexpr (WIN) {
-          // bf16 O, rounded once (P is rounded to bf16 for the second product).
-          __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(o_final) + row0[i] * D + lane * DPL;
-          if (store_in_bounds(dst16, DPL * 2, o_final, split_rows * D * 2, status)) {
-            uint32_t pk[DPL / 2];
-#pragma unroll
-            for (int e = 0; e < DPL / 2; ++e) pk[e] = pack_bf16x2(out[i][2 * e], out[i][2 * e + 1]);
-            if constexpr (DPL == 8)
-              *reinterpret_cast<uint4*>(dst16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            else if constexpr (DPL == 4)
-              *reinterpret_cast<uint2*>(dst16) = make_uint2(pk[0], pk[1]);
-            else
-              *reinterpret_cast<uint32_t*>(dst16) = pk[0];
-          }
-          if (lane == 0 && store_in_bounds(lse_final + row0[i], 4, lse_final,
-                                           split_rows * sizeof(float), status))
-            lse_final[row0[i]] = L;
-          continue;
         }
         float* dst = static_cast<float*>(o_final) + row0[i] * D + lane * DPL;
         if (store_in_bounds(dst, DPL * 4, o_final, split_rows * D * sizeof(float), status)) {
@@ -712,8 +753,14 @@ cudaError_t launch_decode_impl(const void* q, const void* k, const void* v, cons
   if (e != cudaSuccess) return e;
   const dim3 grid(num_splits, Hkv * head_slices, B);
   const float scale_log2 = scale * 1.4426950408889634f;
-  return launch_programmatic(
-      decode_splitkv_kernel<D, WIN>, grid, dim3(kWarps * 32), C::kSmemBytes, stream, tmK, tmV,
+  // Windowed: the splits of a group are a cluster.
+  if (WIN && num_splits > 1 &&
+      (e = allow_large_cluster(reinterpret_cast<const void*>(decode_splitkv_kernel<D, WIN>))) !=
+          cudaSuccess)
+    return e;
+  return launch_programmatic_cluster(
+      decode_splitkv_kernel<D, WIN>, grid, dim3(kWarps * 32), C::kSmemBytes, stream,
+      WIN ? num_splits : 1, tmK, tmV,
       static_cast<const __nv_bfloat16*>(q), o_part, lse_part, seqlens,
       paged != nullptr ? paged->block_table : nullptr, paged != nullptr ? paged->page_size : 0,
       paged != nullptr ? paged->max_pages : 0, paged != nullptr ? paged->num_pages : 0, B, Hq, Hkv,
@@ -740,18 +787,15 @@ cudaError_t launch_decode_splitkv(const void* q, const void* k, const void* v, f
 }
 
 cudaError_t launch_decode_window(const void* q, const void* k, const void* v, const int* seqlens,
-                                 const PagedKV* paged, float* o_part, float* lse_part, int B,
-                                 int Hq, int Hkv, int Sk, int D, int window, int sinks,
-                                 int num_splits, float scale, cudaStream_t stream, int* status,
-                                 const FusedCombine& out) {
-  if (D == 256)
-    return launch_decode_impl<256, true>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
-                                         num_splits, scale, stream, status, &out, window, sinks);
-  if (D == 128)
-    return launch_decode_impl<128, true>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
-                                         num_splits, scale, stream, status, &out, window, sinks);
-  return launch_decode_impl<64, true>(q, k, v, seqlens, paged, o_part, lse_part, B, Hq, Hkv, Sk,
-                                      num_splits, scale, stream, status, &out, window, sinks);
+                                 const PagedKV* paged, void* o, float* lse, int B, int Hq, int Hkv,
+                                 int Sk, int D, int window, int sinks, int num_splits, float scale,
+                                 cudaStream_t stream, int* status) {
+  const FusedCombine out{o, lse, nullptr};
+  const auto launch = D == 256   ? launch_decode_impl<256, true>
+                      : D == 128 ? launch_decode_impl<128, true>
+                                 : launch_decode_impl<64, true>;
+  return launch(q, k, v, seqlens, paged, nullptr, nullptr, B, Hq, Hkv, Sk, num_splits, scale,
+                stream, status, &out, window, sinks);
 }
 
 cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o, float* lse,

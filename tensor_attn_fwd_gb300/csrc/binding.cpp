@@ -10,9 +10,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <ATen/ops/zeros.h>
-#include <c10/cuda/CUDAFunctions.h>
-#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -22,8 +19,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <list>
-#include <mutex>
 #include <string>
 
 #include "../../include/attn.h"
@@ -299,40 +294,6 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Zeroed split counters, one array per (device, stream): a call leaves its counters
-// zero, so the calls of one stream share an array and those of different streams,
-// which may overlap, never do.  The 256 most recently used streams are remembered; a
-// dropped array was allocated on its own stream, so the allocator reuses it after
-// that stream's work.  (The list lives as long as the process: its tensors must not be
-// freed after the CUDA context.)
-Tensor stream_counters(at::Device device, void* stream, int64_t n) {
-  struct Entry {
-    int device;
-    void* stream;
-    Tensor counters;
-  };
-  static std::mutex mutex;
-  static std::list<Entry>* const kept = new std::list<Entry>;
-  const auto zeros = [&] {
-    return at::zeros({std::max<int64_t>(n, 1024)},
-                     at::TensorOptions().dtype(at::kInt).device(device));
-  };
-  // A captured call zeroes counters of its own on every replay: graphs that run at
-  // the same time must not share the stream's array.
-  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
-    return zeros();
-  const std::lock_guard<std::mutex> lock(mutex);
-  for (auto it = kept->begin(); it != kept->end(); ++it) {
-    if (it->device != device.index() || it->stream != stream) continue;
-    if (it->counters.numel() < n) it->counters = zeros();
-    kept->splice(kept->begin(), *kept, it);
-    return kept->front().counters;
-  }
-  kept->push_front({device.index(), stream, zeros()});
-  if (kept->size() > 256) kept->pop_back();
-  return kept->front().counters;
-}
-
 // The cache of a decode: Sk its capacity in keys; table and page size when paged.
 struct Cache {
   const Tensor &k, &v;
@@ -340,7 +301,7 @@ struct Cache {
   int Hkv, Sk;
 };
 
-// a: seqlens, window, sinks, num_splits, scale, o_part, lse_part, o, lse, counters
+// a: seqlens, window, sinks, num_splits, scale, o, lse
 PyObject* decode(const Tensor& q, const Cache& c, PyObject* const* a, const char* what) {
   if (q.size(2) != 1) refuse("decode takes one query row per head (q.shape[2] == 1)");
   const int B = size_int(q.size(0), "q"), Hq = size_int(q.size(1), "q"),
@@ -350,58 +311,32 @@ PyObject* decode(const Tensor& q, const Cache& c, PyObject* const* a, const char
   const int window = integer(a[1], "window", 1, kAll), sinks = integer(a[2], "sinks", 0, kAll);
   const float scale = scale_of(a[4], D);
   const c10::cuda::CUDAGuard guard(device);
-  void* stream = current_stream(device);
   int splits = 0;
   if (a[3] == Py_None)
     raise_if(attn_decode_window_num_splits(B, Hq, c.Hkv, c.Sk, D, window, sinks, &splits),
              "attn_decode_window_num_splits");
   else
     splits = integer(a[3], "num_splits", LLONG_MIN, INT_MAX);
-  Tensor o = output_bf16(a[7], {B, Hq, D}, device, "o");
-  Tensor lse = output_f32(a[8], {B, Hq}, device, "lse");
-  Tensor part, lse_part, counters;
-  if (splits > 1) {
-    if (a[5] == Py_None) {
-      // One allocation: the partials, then their LSEs.
-      part = fresh({static_cast<int64_t>(splits) * B * Hq * (D + 1)}, at::kFloat, device);
-    } else {
-      part = output_f32(a[5], {splits, B, Hq, D}, device, "o_part");
-      lse_part = output_f32(a[6], {splits, B, Hq}, device, "lse_part");
-    }
-    int n = 0;
-    raise_if(attn_decode_fused_counters(B, Hq, c.Hkv, &n), "attn_decode_fused_counters");
-    if (a[9] == Py_None) {
-      counters = stream_counters(device, stream, n);
-    } else {
-      counters = tensor(a[9], "counters");
-      check(counters, "counters", at::kInt, "int32", static_cast<int>(counters.dim()), device);
-      if (counters.numel() < n)
-        refuse("counters must have at least " + std::to_string(n) + " entries");
-    }
-  }
-  float* po = part.defined() ? floats(part) : nullptr;
-  float* pl = lse_part.defined() ? floats(lse_part)
-              : part.defined()   ? po + static_cast<int64_t>(splits) * B * Hq * D
-                                 : nullptr;
-  int* pc = counters.defined() ? ints(counters) : nullptr;
+  Tensor o = output_bf16(a[5], {B, Hq, D}, device, "o");
+  Tensor lse = output_f32(a[6], {B, Hq}, device, "lse");
   if (c.table == nullptr)
     raise_if(attn_decode_window(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), seqlens, o.data_ptr(),
-                                floats(lse), po, pl, pc, B, Hq, c.Hkv, c.Sk, D, window, sinks,
-                                splits, scale, stream),
+                                floats(lse), B, Hq, c.Hkv, c.Sk, D, window, sinks, splits, scale,
+                                current_stream(device)),
              what);
   else
     raise_if(attn_decode_window_paged(
                  q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(*c.table), seqlens,
-                 o.data_ptr(), floats(lse), po, pl, pc, B, Hq, c.Hkv, size_int(c.k.size(0), "k_cache"),
+                 o.data_ptr(), floats(lse), B, Hq, c.Hkv, size_int(c.k.size(0), "k_cache"),
                  size_int(c.k.size(2), "k_cache"), size_int(c.table->size(1), "block_table"), D,
-                 window, sinks, splits, scale, stream),
+                 window, sinks, splits, scale, current_stream(device)),
              what);
   return pack({o, lse});
 }
 
 // q, k, v, then decode's
 PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 13, [&] {
+  return call(n, 10, [&] {
     const Tensor& q = bf16(a[0], "q", 4);
     const Tensor &k = bf16(a[1], "k", 4, &q), &v = bf16(a[2], "v", 4, &q);
     const Sizes s = sizes_of(q, k, v);
@@ -411,7 +346,7 @@ PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // q, k_cache, v_cache, block_table, then decode's
 PyObject* decode_window_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 14, [&] {
+  return call(n, 11, [&] {
     const Tensor& q = bf16(a[0], "q", 4);
     const Tensor &k = bf16(a[1], "k_cache", 4, &q), &v = bf16(a[2], "v_cache", 4, &q);
     if (k.size(3) != q.size(3) || v.sizes() != k.sizes()) refuse("q/cache shape mismatch");

@@ -49,6 +49,34 @@ cudaError_t launch_programmatic(void (*kernel)(KArgs...), dim3 grid, dim3 block,
   return cudaGetLastError();
 }
 
+// launch_programmatic with clusters of `cluster` CTAs along x (1: none).  More than 8
+// need allow_large_cluster(kernel) first.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_programmatic_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                        size_t smem, cudaStream_t stream, int cluster,
+                                        Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+// Let `kernel` be launched in clusters past the portable 8 CTAs, once per (kernel, device).
+cudaError_t allow_large_cluster(const void* kernel);
+
 // Kernel launchers; arguments are already validated.  Return cudaError_t of
 // the launch.
 // o: fp32 [B,Hq,Sq,D], or bf16 when o_bf16 != 0.
@@ -128,7 +156,7 @@ int decode_check_args(const void* q, const void* k, const void* v, int B, int Hq
 // 16-head slice) group last also combines the group's partials into o / lse
 // (counters: int32 [B * Hkv * ceil((Hq/Hkv)/16)], zero on entry, zero again after).
 struct FusedCombine {
-  void* o;  // fp32; bf16 for launch_decode_window
+  void* o;  // fp32
   float* lse;
   int* counters;
 };
@@ -138,14 +166,15 @@ cudaError_t launch_decode_splitkv(const void* q, const void* k, const void* v, f
                                   const int* seqlens = nullptr, const PagedKV* paged = nullptr,
                                   const FusedCombine* fused = nullptr);
 
-// The windowed form (always fused): sequence b's query stands at its last key and
-// sees the last `window` keys and the first `sinks` (1 <= window <= Sk, 0 <= sinks
-// <= Sk).  Splits share out the 32-key blocks that hold a visible key.
+// The windowed form: sequence b's query stands at its last key and sees the last
+// `window` keys and the first `sinks` (1 <= window <= Sk, 0 <= sinks <= Sk); o is bf16.
+// Splits share out the 32-key blocks that hold a visible key, and are merged inside
+// a cluster of at most kWindowDecodeSplits CTAs.
+constexpr int kWindowDecodeSplits = 16;
 cudaError_t launch_decode_window(const void* q, const void* k, const void* v, const int* seqlens,
-                                 const PagedKV* paged, float* o_part, float* lse_part, int B,
-                                 int Hq, int Hkv, int Sk, int D, int window, int sinks,
-                                 int num_splits, float scale, cudaStream_t stream, int* status,
-                                 const FusedCombine& out);
+                                 const PagedKV* paged, void* o, float* lse, int B, int Hq, int Hkv,
+                                 int Sk, int D, int window, int sinks, int num_splits, float scale,
+                                 cudaStream_t stream, int* status);
 
 // Sliding-window prefill and backward (bf16 O and gradients, D 64 or 128); window
 // and sinks clamped as above.

@@ -29,7 +29,6 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -647,50 +646,28 @@ cudaError_t launch_small(const Op& op, size_t smem, cudaStream_t stream) {
   return launch_programmatic(pages_small_kernel<Op>, dim3(1), dim3(kThreads), smem, stream, op);
 }
 
-// The opt-in to clusters of kClusterCtas, once per device.
-template <typename Op>
-cudaError_t allow_cluster() {
-  static std::atomic<uint64_t> allowed{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (allowed.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(pages_phases_kernel<Op, kCluster>),
-                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 // work: elements of the largest array.
 template <typename Op>
 cudaError_t launch_phases(const Op& op, long long work, cudaStream_t stream) {
+  if (work <= kClusterWork) {
+    const auto kernel = pages_phases_kernel<Op, kCluster>;
+    const cudaError_t e = allow_large_cluster(reinterpret_cast<const void*>(kernel));
+    if (e != cudaSuccess) return e;
+    return launch_programmatic_cluster(kernel, dim3(kClusterCtas), dim3(kThreads), 0, stream,
+                                       kClusterCtas, op);
+  }
+  const long long ctas = (work + kThreads - 1) / kThreads;
+  const int most = sm_count() < kPagesMaxCtas ? sm_count() : kPagesMaxCtas;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
-  cudaError_t e;
-  if (work <= kClusterWork) {
-    if ((e = allow_cluster<Op>()) != cudaSuccess) return e;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kClusterCtas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(kClusterCtas, 1, 1);
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, pages_phases_kernel<Op, kCluster>, op);
-  } else {
-    const long long ctas = (work + kThreads - 1) / kThreads;
-    const int most = sm_count() < kPagesMaxCtas ? sm_count() : kPagesMaxCtas;
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, pages_phases_kernel<Op, kGrid>, op);
-  }
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_phases_kernel<Op, kGrid>, op);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

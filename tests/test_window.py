@@ -291,12 +291,10 @@ DECODES = [
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("case", DECODES)
-@pytest.mark.parametrize("splits", [1, 3, None])
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 16, None])
 def test_decode_matches_the_formula(case, splits):
     Hq, Hkv, D, window, sinks, lens = case
     B, Sk = len(lens), max(lens)
-    if splits is not None and splits > Sk:
-        splits = Sk
     q, k, v = inputs(B, Hq, Hkv, 1, Sk, D, 17 * Hq + D) if B else None
     scale = 1.0 / math.sqrt(D)
     seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -351,20 +349,21 @@ def test_decode_reports_a_bad_page_it_reaches():
 
 
 @pytest.mark.gpu
-def test_streams_and_two_graphs_at_once():
+@pytest.mark.parametrize("splits", [1, 12])
+def test_streams_and_two_graphs_at_once(splits):
     Hq, Hkv, D, Sk, window, sinks = 8, 2, 128, 4096, 2000, 4
     sets = [inputs(1, Hq, Hkv, 1, Sk, D, s) for s in (1, 2)]
-    want = [attn.decode_window(*s, window, sinks, num_splits=8) for s in sets]
+    want = [attn.decode_window(*s, window, sinks, num_splits=splits) for s in sets]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    on_side = attn.decode_window(*sets[0], window, sinks, num_splits=8, stream=side)
+    on_side = attn.decode_window(*sets[0], window, sinks, num_splits=splits, stream=side)
     side.synchronize()
     assert torch.equal(on_side[0], want[0][0]) and torch.equal(on_side[1], want[0][1])
     graphs, outs = [], []
-    for s in sets:  # both captured on one stream, with no counters of the caller's
+    for s in sets:  # both captured on one stream
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=side):
-            outs.append(attn.decode_window(*s, window, sinks, num_splits=8))
+            outs.append(attn.decode_window(*s, window, sinks, num_splits=splits))
         graphs.append(g)
     streams = [torch.cuda.Stream() for _ in graphs]
     for _ in range(20):
@@ -430,15 +429,11 @@ def test_debug_build_stores_in_bounds_and_matches(shape):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     qd = q[:, :, -1:].contiguous()
-    for splits in (1, 2):
+    for splits in (1, 9):
         want = attn.decode_window(qd, k, v, window, sinks, num_splits=splits)
         got = [torch.empty_like(t) for t in want]
-        counters = torch.zeros(B * Hq, dtype=torch.int32, device="cuda")
-        part = ws[: splits * B * Hq * D]
-        lse_part = torch.empty(splits * B * Hq, device="cuda")
         assert dbg.attn_decode_window(qd.data_ptr(), k.data_ptr(), v.data_ptr(), None,
-                                      got[0].data_ptr(), got[1].data_ptr(), part.data_ptr(),
-                                      lse_part.data_ptr(), counters.data_ptr(), B, Hq, Hkv, Sk, D,
+                                      got[0].data_ptr(), got[1].data_ptr(), B, Hq, Hkv, Sk, D,
                                       window, sinks, splits, scale, stream) == attn.ATTN_OK
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert dbg.attn_debug_status(None) == attn.ATTN_OK
@@ -511,7 +506,9 @@ def test_decode_split_rule():
     assert rule(1, 2, 1, 0, 64, 4, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
     assert rule(1, 2, 1, 100, 64, 0, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
     assert rule(1, 3, 2, 100, 64, 4, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
-    assert rule(1, 2, 1, 1 << 30, 64, 100, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 1
+    assert rule(1, 2, 1, 1 << 30, 64, 20, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 1
+    assert rule(1, 2, 1, 1 << 30, 64, 1 << 30, 1 << 30, ctypes.byref(n)) == attn.ATTN_OK
+    assert 1 <= n.value <= 16
 
 
 def test_backward_workspace():
@@ -524,25 +521,24 @@ def test_backward_workspace():
     assert size(1, 2, 1, 9, 9, 64, 4, 0, ctypes.byref(n)) == attn.ATTN_OK and n.value >= 2 * 9
 
 
-def dec(q=A, k=A, v=A, sl=A, o=A, lse=A, op=A, lp=A, ct=A, B=1, Hq=4, Hkv=1, Sk=64, D=128, window=8,
-        sinks=1, ns=4, scale=0.1):
-    return _lib().attn_decode_window(q, k, v, sl, o, lse, op, lp, ct, B, Hq, Hkv, Sk, D, window,
-                                     sinks, ns, scale, None)
+def dec(q=A, k=A, v=A, sl=A, o=A, lse=A, B=1, Hq=4, Hkv=1, Sk=64, D=128, window=8, sinks=1, ns=4,
+        scale=0.1):
+    return _lib().attn_decode_window(q, k, v, sl, o, lse, B, Hq, Hkv, Sk, D, window, sinks, ns, scale,
+                                     None)
 
 
-def decp(q=A, k=A, v=A, sl=A, o=A, lse=A, op=A, lp=A, ct=A, B=1, Hq=4, Hkv=1, D=128, window=8,
-         sinks=1, ns=4, scale=0.1, bt=A, num_pages=8, page=64, max_pages=4):
-    return _lib().attn_decode_window_paged(q, k, v, bt, sl, o, lse, op, lp, ct, B, Hq, Hkv,
-                                           num_pages, page, max_pages, D, window, sinks, ns, scale,
-                                           None)
+def decp(q=A, k=A, v=A, sl=A, o=A, lse=A, B=1, Hq=4, Hkv=1, D=128, window=8, sinks=1, ns=4, scale=0.1,
+         bt=A, num_pages=8, page=64, max_pages=4):
+    return _lib().attn_decode_window_paged(q, k, v, bt, sl, o, lse, B, Hq, Hkv, num_pages, page,
+                                           max_pages, D, window, sinks, ns, scale, None)
 
 
 @pytest.mark.parametrize("call,kw,code", list(itertools.chain.from_iterable(
     [(f, kw, c) for kw, c in [
         (dict(o=None), attn.ATTN_ERR_INVALID_ARG),
         (dict(lse=None), attn.ATTN_ERR_INVALID_ARG),
-        (dict(op=None), attn.ATTN_ERR_INVALID_ARG),
-        (dict(ct=None), attn.ATTN_ERR_INVALID_ARG),
+        (dict(ns=17), attn.ATTN_ERR_INVALID_ARG),
+        (dict(ns=-1), attn.ATTN_ERR_INVALID_ARG),
         (dict(window=0), attn.ATTN_ERR_INVALID_ARG),
         (dict(sinks=-3), attn.ATTN_ERR_INVALID_ARG),
         (dict(ns=0), attn.ATTN_ERR_INVALID_ARG),
@@ -551,8 +547,7 @@ def decp(q=A, k=A, v=A, sl=A, o=A, lse=A, op=A, lp=A, ct=A, B=1, Hq=4, Hkv=1, D=
         (dict(B=70000), attn.ATTN_ERR_UNSUPPORTED),
         (dict(k=M), attn.ATTN_ERR_MISALIGNED),
         (dict(o=M), attn.ATTN_ERR_MISALIGNED),
-        (dict(op=M), attn.ATTN_ERR_MISALIGNED),
-        (dict(ct=A + 2), attn.ATTN_ERR_MISALIGNED),
+        (dict(lse=M), attn.ATTN_ERR_MISALIGNED),
         (dict(sl=A + 1), attn.ATTN_ERR_MISALIGNED),
     ]] for f in (dec, decp))) + [
         (decp, dict(sl=None), attn.ATTN_ERR_INVALID_ARG),
