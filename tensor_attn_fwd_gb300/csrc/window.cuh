@@ -91,6 +91,8 @@ inline bool has_unseen(int Sq, int Sk, int window, int sinks) {
 template <int D>
 __device__ __forceinline__ void zero_unseen_rows(uint8_t* tile, int key0, int sinks, int end,
                                                  int lane) {
+  // (Tiles wholly inside the range are read by nobody.)
+  if (key0 != (sinks & ~127) && key0 != (end & ~127)) return;
   const int r0 = max(sinks - key0, 0), r1 = min(end - key0, 128);
   if (r0 >= r1) return;
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
