@@ -60,7 +60,9 @@ constexpr int kBwdLoadWarp = 9;
 constexpr int kGradThreads = 256;
 constexpr int kDqDeltaWarp = 10;  // windowed dQ: warps 10 and 11 compute Delta
 constexpr int kDqWinThreads = 384;
-constexpr uint32_t kDqDeltaBytes = 2 * 128 * sizeof(float);
+// Query tiles of few key tiles compute Delta a second time (see the dQ kernel).
+constexpr int kExactDeltaSteps = 4;
+constexpr uint32_t kDqDeltaBytes = 3 * 128 * sizeof(float);  // two tiles' Delta, one's sums
 constexpr int kStages = 2;
 constexpr uint32_t kSub = 128 * 128;  // [128 rows x 64 bf16] 128B-swizzled sub-tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -101,6 +103,8 @@ struct BwdBars {
   uint64_t q_empty, acc_full2[2], acc_free[2];
   // windowed dQ: Delta of a tile is in shared memory / has been read (two buffers)
   uint64_t delta_full[2], delta_free[2];
+  // ... and the sums of P dP of warps 4-7 / those of warps 0-7 are in shared memory
+  uint64_t part_full, total_full;
   uint32_t tmem_base;
   int abort;
 };
@@ -816,6 +820,7 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
   uint8_t* sV = sK + kKStages * C::kTile;        // V ring: kVStages tiles
   BwdBars* bars = reinterpret_cast<BwdBars*>(sV + kVStages * C::kTile);
   float* sDelta = reinterpret_cast<float*>(sV + kVStages * C::kTile + C::kBarBytes);  // [2][128]
+  float* sPart = sDelta + 2 * 128;                                                        // [128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // Work: query tile m of head (b, h), numbered m-major with the highest m first.
@@ -845,6 +850,10 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
       if constexpr (WIN) {
         mbar_init(&bars->delta_full[b], 2);
         mbar_init(&bars->delta_free[b], kGradThreads / 32);
+        if (b == 0) {
+          mbar_init(&bars->part_full, kGradThreads / 64);
+          mbar_init(&bars->total_full, kGradThreads / 64);
+        }
       }
     }
     mbar_init(&bars->mma_done, 1);
@@ -1014,7 +1023,8 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         const long long row0 = static_cast<long long>(bh) * p.Sq + 128 * m + r;
         const float dlt =
             warp_delta<D>(p.o, p.dout, row0, static_cast<long long>(BH) * p.Sq, lane);
-        if (128 * m + r + lane < p.Sq) p.delta_out[row0 + lane] = dlt;
+        if ((nsteps == 0 || nsteps > kExactDeltaSteps) && 128 * m + r + lane < p.Sq)
+          p.delta_out[row0 + lane] = dlt;
         if (nsteps > 0) sDelta[128 * buf + r + lane] = dlt;
       }
       if (nsteps > 0) {
@@ -1035,6 +1045,7 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         static_cast<size_t>(p.B) * p.Hq * p.Sq * D * (WIN ? sizeof(__nv_bfloat16) : sizeof(float));
     uint32_t G = 0;  // first global step of the current tile
     int kt = 0;      // tiles with work so far
+    int exact_tiles = 0;  // windowed: those whose Delta was added up here
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
@@ -1072,7 +1083,15 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         dlt = row_valid ? __ldg(p.delta + static_cast<size_t>(bh) * p.Sq + row) : 0.f;
       }
       const uint64_t nl2 = f2_pack(-lse2, -lse2);
-      const uint64_t ndl = f2_pack(-dlt, -dlt);
+      uint64_t ndl = f2_pack(-dlt, -dlt);
+      // Delta from a bf16 O is off by O's rounding (and P's in it), which a row of few
+      // keys shows: at a window of 8 dQ and dK are 2.7e-3 off, 1.63 times what their own
+      // rounding alone would make, and still 1.5 times at 64.  So where a tile has few
+      // steps (and windows are that short) sum_j P dP, which is Delta, is added up on
+      // the way: the last step, which holds most of such a row's keys, and dK/dV use it.
+      // (2.4e-3 then, at each window.)
+      const bool exact = WIN && nsteps <= kExactDeltaSteps;
+      uint64_t p_dp = f2_pack(0.f, 0.f);
       const int key_hi = WIN || p.causal ? min(p.Sk - 1, row + p.Sk - p.Sq) : p.Sk - 1;
       const int win_lo = row + p.Sk - p.Sq - p.window + 1;  // windowed: the window's first key
       for (int s = 0; s < nsteps && ok; ++s) {
@@ -1121,6 +1140,41 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         ok = __all_sync(0xffffffffu, bwd_wait(&bars->dp_full, g & 1, bars));
         if (!ok) break;
         tc_fence_after();
+        if constexpr (WIN) {
+          if (exact) {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              uint32_t dr[32];
+              tmem_ld32(tmem + lane_addr + C::kColDP + 64 * half + 32 * cc, dr);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                p_dp = f2_fma(f2_pack(pv[32 * cc + e], pv[32 * cc + e + 1]),
+                              f2_pack(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])), p_dp);
+            }
+            if (s + 1 == nsteps) {
+              // The two warpgroups' halves of the sum: 4-7 to 0-3, the total back.
+              float a, b;
+              f2_unpack(p_dp, a, b);
+              dlt = a + b;
+              if (half == 1) {
+                sPart[r] = dlt;
+                mbar_arrive_warp(&bars->part_full);
+                ok = __all_sync(0xffffffffu, bwd_wait(&bars->total_full, exact_tiles & 1, bars));
+                if (!ok) break;
+                dlt = sPart[r];
+              } else {
+                ok = __all_sync(0xffffffffu, bwd_wait(&bars->part_full, exact_tiles & 1, bars));
+                if (!ok) break;
+                dlt += sPart[r];
+                sPart[r] = dlt;
+                mbar_arrive_warp(&bars->total_full);
+                if (row_valid) p.delta_out[static_cast<size_t>(bh) * p.Sq + row] = dlt;
+              }
+              ++exact_tiles;
+              ndl = f2_pack(-dlt, -dlt);
+            }
+          }
+        }
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t dr[32];
