@@ -746,7 +746,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
     bwd_sum_parts_kernel(const float* __restrict__ partials, __nv_bfloat16* __restrict__ dk,
                          __nv_bfloat16* __restrict__ dv, int split_tiles, int parts, int BH,
-                         int Sk) {
+                         int Sk, int* status) {
   grid_dependency_wait();
   grid_launch_dependents();
   const size_t plane = static_cast<size_t>(split_tiles) * BH * 128 * D;
@@ -767,8 +767,10 @@ __global__ void __launch_bounds__(256)
       x.z += y.z;
       x.w += y.w;
     }
-    *reinterpret_cast<uint2*>((i ? dv : dk) + to) =
-        make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    __nv_bfloat16* out = i ? dv : dk;
+    if (store_in_bounds(out + to, 8, out, static_cast<size_t>(BH) * Sk * D * 2, status))
+      *reinterpret_cast<uint2*>(out + to) =
+          make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   }
 }
 
@@ -1323,7 +1325,7 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
                                dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0,
                                stream, p.partials, static_cast<__nv_bfloat16*>(dk),
                                static_cast<__nv_bfloat16*>(dv), p.split_tiles, p.parts, B * Hkv,
-                               Sk);
+                               Sk, status);
   } else {
     p.out0 = static_cast<float*>(dk);
     p.out1 = static_cast<float*>(dv);

@@ -294,10 +294,11 @@ def test_bad_entries_are_reported_and_read_as_no_page():
 
 
 @pytest.mark.gpu
-def test_graph_and_stream():
+@pytest.mark.parametrize("B,P", [(12, 400), (300, 8000), (2000, 60000)])  # each launch form
+def test_graph_and_stream(B, P):
     rng = np.random.default_rng(3)
-    table, refs, lens = cache_tables(rng, 12, 20, 400, 32, 0.7, 0.5)
-    args = gpu(table, refs, lens, rng.integers(0, 12, 12))
+    table, refs, lens = cache_tables(rng, B, 20, P, 32, 0.7, 0.5)
+    args = gpu(table, refs, lens, rng.integers(0, B, B))
     want = attn.attn_pages_fork(*args, 32, 5)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -16,6 +16,7 @@ w = 2^-12 relative to the sum of magnitudes at these sizes):
 import ctypes
 import itertools
 import math
+import threading
 
 import pytest
 import torch
@@ -243,6 +244,33 @@ def test_outputs_rows_behind_the_tensor_stay():
         assert bool((buf[view.numel():] == 7.0).all())
 
 
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    # q, o, dout and dq of 2.2e9 elements: the last rows of the last head against the same
+    # rows computed as a chunk of their own (each within the bounds: twice them apart).
+    B, Hq, Hkv, S, D, window, sinks = 1, 32, 1, 530000, 128, 100, 4
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, do = (torch.randn(B, Hq, S, D, generator=g, device="cuda", dtype=torch.bfloat16)
+             for _ in range(2))
+    k, v = (torch.randn(B, Hkv, S, D, generator=g, device="cuda", dtype=torch.bfloat16)
+            for _ in range(2))
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks)
+    dq, dk, dv = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    n = 300  # rows; their keys: the sinks, and the last n + window
+    seen = torch.cat([torch.arange(sinks), torch.arange(S - n - window, S)]).cuda()
+    kt, vt = k[:, :, seen], v[:, :, seen]
+    rows = [t[:, -1:, -n:].contiguous() for t in (q, do)]
+    ref, tol = reference(rows[0], kt, vt, window, sinks, 1.0 / math.sqrt(D), rows[1])
+    check("o", o[:, -1:, -n:], ref["o"], tol["o"])
+    check("lse", lse[:, -1:, -n:], ref["lse"], tol["lse"])
+    check("dq", dq[:, -1:, -n:], ref["dq"], tol["dq"])
+    # The last key's gradients come from the last row of every head.
+    ref, tol = reference(q[:, :, -1:], kt, vt, window, sinks, 1.0 / math.sqrt(D), do[:, :, -1:])
+    check("dk", dk[:, :, -1], ref["dk"][:, :, -1], tol["dk"][:, :, -1])
+    check("dv", dv[:, :, -1], ref["dv"][:, :, -1], tol["dv"][:, :, -1])
+
+
 # ------------------------------------------------------------------ decode
 def paged(k, v, page, seed, spare=3):
     """A paged copy of contiguous caches: (k_cache, v_cache, table), pages shuffled."""
@@ -336,6 +364,27 @@ def test_decode_without_lengths_is_the_forward_of_the_last_row():
 
 
 @pytest.mark.gpu
+def test_decode_of_a_cache_past_32_bits():
+    P, Hkv, page, D, window, sinks = 33000, 8, 64, 128, 200, 3  # 2.2e9 elements a cache
+    kc = torch.empty(P, Hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    q, k, v = inputs(1, 16, Hkv, 1, 320, D, 12)
+    table = torch.tensor([[P - 1, 7, P - 2, 5, P - 3]], dtype=torch.int32, device="cuda")
+    for s, p in enumerate(table[0].tolist()):
+        kc[p], vc[p] = k[0, :, s * page:(s + 1) * page], v[0, :, s * page:(s + 1) * page]
+    seqlens = torch.tensor([311], dtype=torch.int32, device="cuda")
+    ref, tol = decode_reference(q, k, v, [311], window, sinks, 1.0 / math.sqrt(D))
+    o, lse = attn.decode_window_paged(q, kc, vc, table, seqlens, window, sinks)
+    check("o", o, ref["o"], tol["o"])
+    check("lse", lse, ref["lse"], tol["lse"])
+    src = torch.tensor([P - 1, 5], dtype=torch.int32, device="cuda")
+    dst = torch.tensor([9, P - 4], dtype=torch.int32, device="cuda")
+    attn.attn_pages_copy(kc, vc, src, dst)
+    for a, b in ((P - 1, 9), (5, P - 4)):
+        assert torch.equal(kc[a], kc[b]) and torch.equal(vc[a], vc[b])
+
+
+@pytest.mark.gpu
 def test_decode_reports_a_bad_page_it_reaches():
     q, k, v = inputs(1, 2, 1, 1, 128, 64, 2)
     kc, vc, table = paged(k, v, 32, 1, spare=0)
@@ -373,6 +422,37 @@ def test_streams_and_two_graphs_at_once(splits):
     torch.cuda.synchronize()
     for got, w in zip(outs, want):
         assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+
+
+@pytest.mark.gpu
+def test_threads_on_streams_of_their_own():
+    shapes = [(1, 4, 2, 300, 300, 64, 70, 4), (1, 2, 2, 40, 2000, 128, 900, 3),
+              (2, 6, 2, 500, 500, 64, 33, 130), (1, 8, 1, 700, 700, 128, 128, 0)]
+
+    def work(shape, out, stream):
+        B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+        with torch.cuda.stream(stream):
+            q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, Sq, grad=True)
+            for _ in range(5):
+                o, lse = attn.attn_window_fwd(q, k, v, window, sinks)
+                grads = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+                dec = attn.decode_window(q[:, :, -1:].contiguous(), k, v, window, sinks)
+            out.append((o, lse) + grads + dec)
+            stream.synchronize()
+
+    want = [[] for _ in shapes]
+    for shape, out in zip(shapes, want):
+        work(shape, out, torch.cuda.current_stream())
+    got = [[] for _ in shapes]
+    threads = [threading.Thread(target=work, args=(s, g, torch.cuda.Stream()))
+               for s, g in zip(shapes, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for w, g in zip(want, got):
+        for a, b in zip(w[0], g[0]):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
