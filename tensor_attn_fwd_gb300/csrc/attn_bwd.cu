@@ -445,10 +445,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
-  if constexpr (WIN) {  // launched as a dependent of dQ, which leaves Delta
-    grid_dependency_wait();
-    grid_launch_dependents();
-  }
+  // Windowed: a dependent of dQ, which leaves Delta.  Only the gradient warps, which read
+  // it, wait for dQ: the first products run beside dQ's end.  (The call's inputs are
+  // complete: dQ let its dependents start after its own wait for what came before.)
+  if constexpr (WIN) grid_launch_dependents();
 
   if (warp == kBwdLoadWarp) {
     if (nsteps > 0) {
@@ -559,6 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         pre_d[u] = ld_nc_f32(p.delta + base + row);
       }
     };
+    if constexpr (WIN) grid_dependency_wait();
     if (nsteps > 0) fetch(0);
     for (int s = 0; s < nsteps && ok; ++s) {
       const int m = m0 + (s_base + s) % per_head;
