@@ -22,6 +22,11 @@
 // Scores are kept in the log2 domain (scaled by scale * log2 e).  The running
 // maximum is moved lazily (only when it grows by more than 8) so the O
 // fragments are rarely rescaled; O and l always share one reference maximum.
+//
+// The windowed instantiations read only the 32-key blocks that hold a key within a
+// sliding window or a sink, write a bf16 O, and merge the splits of a group in a
+// thread-block cluster.  HBM-bound with many rows (64 rows, window 4096: 156 us, the
+// copy's rate), latency-bound with one (window 1024: 6.2 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
