@@ -115,7 +115,7 @@ __device__ __forceinline__ int checked_entry(int e, int num_pages, int* status) 
   return e;
 }
 
-// Phases [first, last).  kCluster: one cluster and its barrier; else a cooperative
+// All phases of a call.  kCluster: one cluster and its barrier; kGrid: a cooperative
 // grid and its (every CTA is resident, and each enters every barrier).
 enum Span { kCluster, kGrid };
 template <typename Op, Span SPAN>
