@@ -360,8 +360,8 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const float *
  *      (attn_combine's formula) by a second kernel
  *   workspace: num_splits * B * Hq * Sq * (D + 1) floats, 16-byte aligned, contents
  *      undefined; not touched, and NULL allowed, with one split
- *   D 64 or 128 (else ATTN_ERR_UNSUPPORTED).  Sizes, alignment, other errors and
- *   rows that see no key (O = 0, LSE = -inf) as attn_fwd.
+ *   D in {64, 128, 256} (else ATTN_ERR_UNSUPPORTED).  Sizes, alignment, other errors
+ *   and rows that see no key (O = 0, LSE = -inf) as attn_fwd.
  *   Keys that no row sees may hold anything (NaN, unwritten memory).  K and V have to
  *   be finite at keys that some row sees: one that is not finite reaches, beside the
  *   rows that see it, rows of their 128-row query tiles that do not (a weight of 0
@@ -390,8 +390,8 @@ ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, 
  *   workspace: attn_window_bwd_workspace floats, caller-owned, contents undefined
  *      (Delta, and partial sums of the key tiles that hold sinks: every later row
  *      sees those, so their work is split and added up in a fixed order)
- *   Same arguments, conditions and errors as attn_window_fwd (q, dout and o finite);
- *   all pointers 16-byte aligned.
+ *   Same arguments, conditions and errors as attn_window_fwd (q, dout and o finite),
+ *   but D 64 or 128; all pointers 16-byte aligned.
  */
 ATTN_API int attn_window_bwd(const void *q, const void *k, const void *v, const void *o,
                              const float *lse, const void *dout, void *dq, void *dk, void *dv,

@@ -733,7 +733,7 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
                     num_splits: int | None = None):
     """Attention under a sliding window with sinks; returns (o bf16 [B,Hq,Sq,D], lse fp32).
 
-    q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64 or 128.  Row i stands
+    q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64, 128 or 256.  Row i stands
     at p = i + Sk - Sq and sees key j when j <= p and (j > p - window or j < sinks).
     ``num_splits`` > 1 cuts each row's keys into so many parts and merges them, for
     chunks with too few rows to fill the GPU; None picks attn_window_fwd_num_splits.
@@ -752,7 +752,8 @@ def attn_window_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     """Gradients of sum(dout * O) for O = attn_window_fwd(q, k, v, window, sinks):
     returns (dq, dk, dv) bf16, summed in fp32 and rounded once.
 
-    o (bf16) and lse (fp32) are attn_window_fwd's results; dout is bf16 like q.
+    o (bf16) and lse (fp32) are attn_window_fwd's results; dout is bf16 like q.  D 64
+    or 128.
     ``workspace`` is an optional fp32 CUDA tensor of at least
     attn_window_bwd_workspace floats (include/attn.h).
     """

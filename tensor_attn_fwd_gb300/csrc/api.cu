@@ -248,12 +248,11 @@ int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float*
   if (num_splits > 1 && !workspace) return ATTN_ERR_INVALID_ARG;
   const int chk = fwd_check_args(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, 1, scale);
   if (chk != ATTN_OK) return chk;
-  if (D == 256) return ATTN_ERR_UNSUPPORTED;
   if (num_splits > 1) {
     // Every split of the longest row has a key tile; rows and items are counted with int.
     if (num_splits > (Sk + 127) / 128) return ATTN_ERR_INVALID_ARG;
     if (static_cast<long long>(B) * Hq * Sq > (1ll << 30) ||
-        window_items(B, Hq, Hkv, Sq) * num_splits > (1ll << 30) ||
+        window_items(B, Hq, Hkv, Sq, D) * num_splits > (1ll << 30) ||
         static_cast<long long>(num_splits) * B * Hq * Sq * D > kMaxElems)
       return ATTN_ERR_UNSUPPORTED;
     if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
@@ -276,7 +275,7 @@ int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, in
   if (num_splits == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0 ||
       Hq % Hkv != 0 || window < 1 || sinks < 0)
     return ATTN_ERR_INVALID_ARG;
-  const long long n_sm = sm_count(), items = window_items(B, Hq, Hkv, Sq);
+  const long long n_sm = sm_count(), items = window_items(B, Hq, Hkv, Sq, D);
   // Key tiles of an item at most: its rows' windows and the sinks, or all there are.
   const long long all = (static_cast<long long>(Sk) + 127) / 128;
   const long long seen = (static_cast<long long>(window) + 126) / 128 + 1 +

@@ -830,7 +830,9 @@ cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o,
 
 cudaError_t launch_combine_bf16(const float* o_part, const float* lse_part, void* o, float* lse,
                                 int rows, int D, int num_splits, cudaStream_t stream) {
-  auto kernel = D == 128 ? combine_kernel<128, __nv_bfloat16> : combine_kernel<64, __nv_bfloat16>;
+  auto kernel = D == 256   ? combine_kernel<256, __nv_bfloat16>
+                : D == 128 ? combine_kernel<128, __nv_bfloat16>
+                           : combine_kernel<64, __nv_bfloat16>;
   return launch_programmatic(kernel, dim3((rows + 7) / 8), dim3(256), 0, stream, o_part, lse_part,
                              static_cast<__nv_bfloat16*>(o), lse, rows, num_splits);
 }

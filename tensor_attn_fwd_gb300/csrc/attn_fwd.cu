@@ -932,7 +932,7 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   p.num_splits = num_splits;
   p.window = window;
   p.sinks = sinks;
-  p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq) * num_splits);
+  p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, D) * num_splits);
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,
                              tmK, tmV, p);
@@ -948,7 +948,9 @@ cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, 
   void* o_to = num_splits > 1 ? o_part : o;
   float* lse_to = num_splits > 1 ? lse_part : lse;
   const cudaError_t e =
-      D == 128 ? launch_window_impl<128>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
+      D == 256 ? launch_attn_window_fwd_d256(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window,
+                                             sinks, num_splits, scale, stream, status)
+      : D == 128 ? launch_window_impl<128>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
                                          num_splits, scale, stream, status)
                : launch_window_impl<64>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
                                         num_splits, scale, stream, status);

@@ -32,6 +32,12 @@
 // in the epilogue, for step g) is never more than one phase of that barrier
 // behind -- with a single barrier it could be two, and a parity wait would
 // pass early.  All waits are bounded.
+//
+// The windowed instantiations (Mask; window.cuh) walk the key tiles that a sliding
+// window with sinks leaves, or with several splits an equal run of them each.
+// B2 16/4 heads S8192, window 1024, 4 sinks: 242 us (2 x D = 128's 127; the whole
+// causal mask 664); a chunk of 512 rows against 16384 keys, window 4096: 56.0 us in one
+// pass, 36.9 in two splits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,6 +47,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace attn {
 namespace {
@@ -90,13 +97,28 @@ struct Params256 {
   int num_tiles;    // ceil(Sq / 128)
   int total_items;  // B * Hq * num_tiles
   int kv_chunk;     // ORDER 2: KV heads per chunk
+  // Windowed: the mask, and the splits of an item (fp32 partials, split s at
+  // o + s * split_stride_o and lse + s * split_stride_lse).
+  int window, sinks, num_splits;
+  size_t split_stride_o, split_stride_lse;
 };
 
 struct Item256 {
   int bh;
   int row0;  // first query row
   int n;     // KV tiles to visit (0: nothing visible)
+  TileRange r;  // windowed: those tiles
+  int split;
 };
+
+// The KV tile of an item's step j.
+template <Mask WIN>
+__device__ __forceinline__ int step_tile(const Item256& it, int j) {
+  if constexpr (WIN)
+    return it.r.tile(j);
+  else
+    return j;
+}
 
 __device__ __forceinline__ int kv_tiles(const Params256& p, int row_first) {
   if (row_first >= p.Sq) return 0;
@@ -135,10 +157,25 @@ __device__ __forceinline__ int item_idx(int round, int cta, int grid) {
 //            +29 %, B4 H16 S4096 +8 %, GQA B4 Hq32 Hkv8 S4096 +6.5 %).  At
 //            S = 8192 the chunks' longest-first lists no longer balance across
 //            the CTAs (multi-head D = 128 B4 H32 S8192: -5 to -8 %).
-template <int ORDER>
+// Windowed: KV head by KV head (its query heads, then its row tiles), split by split.
+template <int ORDER, Mask WIN>
 __device__ __forceinline__ Item256 item_at(const Params256& p, int idx) {
   const int BH = p.B * p.Hq;
   Item256 it;
+  if constexpr (WIN) {
+    const int per_split = p.total_items / p.num_splits, group = p.Hq / p.Hkv;
+    it.split = idx / per_split;
+    idx -= it.split * per_split;
+    const int rest = idx / group;
+    const int bg = rest / p.num_tiles;  // b * Hkv + KV head
+    it.bh = (bg / p.Hkv) * p.Hq + (bg % p.Hkv) * group + idx % group;
+    it.row0 = (p.num_tiles - 1 - rest % p.num_tiles) * 128;
+    it.r = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.row0);
+    const int chunk = (it.r.count() + p.num_splits - 1) / p.num_splits;
+    it.r = it.r.steps(it.split * chunk, it.split * chunk + chunk);
+    it.n = it.r.count();
+    return it;
+  }
   if (ORDER == 0) {
     it.bh = idx % BH;
     it.row0 = (p.num_tiles - 1 - idx / BH) * 128;
@@ -161,13 +198,13 @@ __device__ __forceinline__ Item256 item_at(const Params256& p, int idx) {
 }
 
 // Next item of this CTA with work, starting at round r (r is advanced past it).
-template <int ORDER>
+template <int ORDER, Mask WIN>
 __device__ __forceinline__ bool next_work(const Params256& p, int& r, Item256& it) {
   while (true) {
     const int idx = item_idx(r, blockIdx.x, gridDim.x);
     if (idx >= p.total_items) return false;
     ++r;
-    it = item_at<ORDER>(p, idx);
+    it = item_at<ORDER, WIN>(p, idx);
     if (it.n > 0) return true;
   }
 }
@@ -228,7 +265,7 @@ __device__ __forceinline__ bool load_half(const CUtensorMap* map, int half, int 
   return got;  // this lane's outcome
 }
 
-template <int ORDER>
+template <int ORDER, Mask WIN>
 __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
                              const CUtensorMap* tmV, const Params256& p, uint8_t* sQ,
                              uint8_t* sKV, Bars256* bars) {
@@ -238,7 +275,7 @@ __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   bool ok = true;
   int r = 0;
   Item256 it;
-  if (!next_work<ORDER>(p, r, it)) return;
+  if (!next_work<ORDER, WIN>(p, r, it)) return;
   auto load_q_k0 = [&](const Item256& x) -> bool {
     if (q_ctr > 0 && !wait_bar_w(&bars->q_empty, (q_ctr - 1) & 1, bars)) return false;
     if (elect_one()) {
@@ -250,8 +287,9 @@ __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
     __syncwarp();
     ++q_ctr;
     const int bkv = (x.bh / p.Hq) * p.Hkv + (x.bh % p.Hq) / group;
-    bool g = load_half(tmK, 0, 0, bkv, sKV, bars, ring);
-    g &= load_half(tmK, 1, 0, bkv, sKV, bars, ring);
+    const int key0 = WIN ? step_tile<WIN>(x, 0) * 128 : 0;
+    bool g = load_half(tmK, 0, key0, bkv, sKV, bars, ring);
+    g &= load_half(tmK, 1, key0, bkv, sKV, bars, ring);
     return __all_sync(0xffffffffu, g);
   };
   ok = load_q_k0(it);
@@ -262,14 +300,15 @@ __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
     for (int j = 0; j < it.n && ok; ++j) {
       bool g = true;
       if (j + 1 < it.n) {
-        g &= load_half(tmK, 0, (j + 1) * 128, bkv, sKV, bars, ring);
-        g &= load_half(tmK, 1, (j + 1) * 128, bkv, sKV, bars, ring);
+        const int next_key = step_tile<WIN>(it, j + 1) * 128;
+        g &= load_half(tmK, 0, next_key, bkv, sKV, bars, ring);
+        g &= load_half(tmK, 1, next_key, bkv, sKV, bars, ring);
       } else {
-        have_next = next_work<ORDER>(p, r, nxt);
+        have_next = next_work<ORDER, WIN>(p, r, nxt);
         if (have_next) g &= load_q_k0(nxt);
       }
-      g &= load_half(tmV, 0, j * 128, bkv, sKV, bars, ring);
-      g &= load_half(tmV, 1, j * 128, bkv, sKV, bars, ring);
+      g &= load_half(tmV, 0, step_tile<WIN>(it, j) * 128, bkv, sKV, bars, ring);
+      g &= load_half(tmV, 1, step_tile<WIN>(it, j) * 128, bkv, sKV, bars, ring);
       ok = __all_sync(0xffffffffu, g);
     }
     if (!ok || !have_next) break;
@@ -284,7 +323,7 @@ __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 }
 
 // ------------------------------------------------------------------ MMA issuer
-template <int ORDER>
+template <int ORDER, Mask WIN>
 __device__ void mma_role256(const Params256& p, uint8_t* sQ, uint8_t* sKV, Bars256* bars,
                             uint32_t tmem) {
   constexpr uint64_t kDescK = sdesc_sw128(0, 16, 1024);    // Q and K: K-major
@@ -299,6 +338,7 @@ __device__ void mma_role256(const Params256& p, uint8_t* sQ, uint8_t* sKV, Bars2
   const uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
   uint32_t kv_ctr = 0, q_ctr = 0;
   uint32_t g_s = 0, g_pv = 0;  // steps whose S / PV have been issued
+  const int unseen = WIN == kUnseen ? unseen_end(p.Sq, p.Sk, p.window) : 0;
   bool ok = true;
 
   // Per-lane outcomes (no vote); see the note above wait_bar_w.
@@ -336,7 +376,7 @@ __device__ void mma_role256(const Params256& p, uint8_t* sQ, uint8_t* sKV, Bars2
 
   int r = 0;
   Item256 it;
-  if (!next_work<ORDER>(p, r, it)) return;
+  if (!next_work<ORDER, WIN>(p, r, it)) return;
   if (!(ok = wait_bar_w(&bars->q_full, q_ctr & 1, bars))) goto done;
   ++q_ctr;
   if (!(ok = __all_sync(0xffffffffu, issue_s()))) goto done;
@@ -351,7 +391,7 @@ __device__ void mma_role256(const Params256& p, uint8_t* sQ, uint8_t* sKV, Bars2
         good &= issue_s();
         if (j + 2 == it.n) tc_commit_w(&bars->q_empty);  // the item's last S is issued
       } else {
-        have_next = next_work<ORDER>(p, r, nxt);
+        have_next = next_work<ORDER, WIN>(p, r, nxt);
         if (have_next) {
           if (!(ok = wait_bar_w(&bars->q_full, q_ctr & 1, bars))) goto done;
           ++q_ctr;
@@ -363,6 +403,11 @@ __device__ void mma_role256(const Params256& p, uint8_t* sQ, uint8_t* sKV, Bars2
       uint32_t v0, v1;
       good &= acquire(v0);
       good &= acquire(v1);
+      if constexpr (WIN == kUnseen) {  // a half tile is a D = 128 tile
+        const int key0 = 128 * step_tile<WIN>(it, j), lane = threadIdx.x & 31;
+        zero_unseen_rows<128>(sKV + v0 * kHalfBytes, key0, p.sinks, unseen, lane);
+        zero_unseen_rows<128>(sKV + v1 * kHalfBytes, key0, p.sinks, unseen, lane);
+      }
       const uint32_t buf = g_pv & 1;
       const uint32_t a = tmem + (buf ? kColS1 : kColS0);
       const uint32_t par = (g_pv >> 1) & 1;
@@ -416,7 +461,7 @@ done:
 }
 
 // ------------------------------------------------------------------ softmax + epilogue
-template <int ORDER>
+template <int ORDER, Mask WIN>
 __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem, int warp,
                                 int lane) {
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
@@ -428,13 +473,15 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
   for (int r = 0; ok; ++r) {
     const int idx = item_idx(r, blockIdx.x, gridDim.x);
     if (idx >= p.total_items) break;
-    const Item256 it = item_at<ORDER>(p, idx);
+    const Item256 it = item_at<ORDER, WIN>(p, idx);
     const int row = it.row0 + warp * 32 + lane;
     const bool row_valid = row < p.Sq;
-    const size_t o_off = (static_cast<size_t>(it.bh) * p.Sq + row) * kD;
+    const size_t o_off = (static_cast<size_t>(it.bh) * p.Sq + row) * kD +
+                         (WIN ? it.split * p.split_stride_o : 0);
     float* o_row = static_cast<float*>(p.o) + o_off;
     __nv_bfloat16* o_row16 = static_cast<__nv_bfloat16*>(p.o) + o_off;
-    float* lse_ptr = p.lse + static_cast<size_t>(it.bh) * p.Sq + row;
+    float* lse_ptr = p.lse + static_cast<size_t>(it.bh) * p.Sq + row +
+                     (WIN ? it.split * p.split_stride_lse : 0);
     if (it.n == 0) {
       if (row_valid &&
           store_in_bounds(p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
@@ -453,7 +500,9 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
       }
       continue;
     }
-    const int limit = p.causal ? min(row + p.Sk - p.Sq, p.Sk - 1) : p.Sk - 1;
+    const int limit = WIN || p.causal ? min(row + p.Sk - p.Sq, p.Sk - 1) : p.Sk - 1;
+    // Windowed: first key of the row's window; earlier keys are seen below `sinks`.
+    const int win_lo = row + p.Sk - p.Sq - p.window + 1;
     float m = -INFINITY;
     float l = 0.f;
 
@@ -466,12 +515,30 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
       uint32_t sa[64], sb[64];
       tmem_ld64(tS, sa);
       tmem_ld64_nowait(tS + 64, sb);
-      const int key0 = j * 128;
-      const bool need_mask = __any_sync(0xffffffffu, key0 + 127 > limit);
-      if (need_mask) {
+      const int key0 = step_tile<WIN>(it, j) * 128;
+      const bool need_mask = __any_sync(
+          0xffffffffu, key0 + 127 > limit || (WIN && key0 < win_lo && key0 + 127 >= p.sinks));
+      // Windowed: columns [64h, 64h + 64) of the step (as in the D <= 128 kernel).
+      auto mask_half = [&](uint32_t(&x)[64], int h) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (key0 + c > limit) sa[c] = __float_as_uint(-INFINITY);
+        for (int q = 0; q < 2; ++q) {
+          const int k0 = key0 + 64 * h + 32 * q;
+          const uint32_t bits = window_bits(win_lo - k0, limit + 1 - k0, p.sinks - k0);
+          if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(bits >> c & 1u)) x[32 * q + c] = __float_as_uint(-INFINITY);
+          }
+        }
+      };
+      if (need_mask) {
+        if constexpr (WIN) {
+          mask_half(sa, 0);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (key0 + c > limit) sa[c] = __float_as_uint(-INFINITY);
+        }
       }
       float ch[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -481,9 +548,13 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
           ch[e] = max3(ch[e], __uint_as_float(sa[c + e]), __uint_as_float(sa[c + 4 + e]));
       tmem_ld_wait64(sb);
       if (need_mask) {
+        if constexpr (WIN) {
+          mask_half(sb, 1);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (key0 + 64 + c > limit) sb[c] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < 64; ++c)
+            if (key0 + 64 + c > limit) sb[c] = __float_as_uint(-INFINITY);
+        }
       }
 #pragma unroll
       for (int c = 0; c < 64; c += 8)
@@ -622,7 +693,7 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
 }
 
 // ------------------------------------------------------------------ kernel
-template <int ORDER>
+template <int ORDER, Mask WIN = kNoWindow>
 __global__ void __launch_bounds__(kThreads256, 1)
     attn_fwd_d256_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -673,11 +744,11 @@ __global__ void __launch_bounds__(kThreads256, 1)
   grid_launch_dependents();
 
   if (warp < 4) {
-    softmax_role256<ORDER>(p, bars, tmem, warp, lane);
+    softmax_role256<ORDER, WIN>(p, bars, tmem, warp, lane);
   } else if (warp == kMmaWarp256) {
-    mma_role256<ORDER>(p, sQ, sKV, bars, tmem);
+    mma_role256<ORDER, WIN>(p, sQ, sKV, bars, tmem);
   } else if (warp == kLoadWarp256) {
-    load_role256<ORDER>(&tmQ, &tmK, &tmV, p, sQ, sKV, bars);
+    load_role256<ORDER, WIN>(&tmQ, &tmK, &tmV, p, sQ, sKV, bars);
   }
 
   tc_fence_before();
@@ -726,6 +797,47 @@ cudaError_t launch_attn_fwd_d256(const void* q, const void* k, const void* v, vo
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads256), kSmem256,
                              stream, tmQ, tmK, tmV, p);
+}
+
+cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void* v, void* o,
+                                        float* lse, int B, int Hq, int Hkv, int Sq, int Sk,
+                                        int window, int sinks, int num_splits, float scale,
+                                        cudaStream_t stream, int* status) {
+  CUtensorMap tmQ, tmK, tmV;
+  if (!encode_bf16_map(&tmQ, q, kD, Sq, B * Hq, 128) ||
+      !encode_bf16_map(&tmK, k, kD, Sk, B * Hkv, 128) ||
+      !encode_bf16_map(&tmV, v, kD, Sk, B * Hkv, 128))
+    return cudaErrorInvalidValue;
+  auto kernel = has_unseen(Sq, Sk, window, sinks) ? attn_fwd_d256_kernel<0, kUnseen>
+                                                  : attn_fwd_d256_kernel<0, kWindow>;
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(kernel), static_cast<int>(kSmem256));
+  if (e != cudaSuccess) return e;
+  Params256 p = {};
+  p.o = o;
+  p.o_bf16 = num_splits == 1;
+  p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  p.split_stride_lse = static_cast<size_t>(B) * Hq * Sq;
+  p.split_stride_o = p.split_stride_lse * kD;
+  p.o_bytes = num_splits * p.split_stride_o * (p.o_bf16 ? 2 : 4);
+  p.lse_bytes = num_splits * p.split_stride_lse * sizeof(float);
+  p.lse = lse;
+  p.status = status;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Sq = Sq;
+  p.Sk = Sk;
+  p.causal = 1;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.num_tiles = (Sq + 127) / 128;
+  p.window = window;
+  p.sinks = sinks;
+  p.num_splits = num_splits;
+  p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, kD) * num_splits);
+  const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
+  return launch_programmatic(kernel, dim3(grid), dim3(kThreads256), kSmem256, stream, tmQ, tmK,
+                             tmV, p);
 }
 
 }  // namespace attn

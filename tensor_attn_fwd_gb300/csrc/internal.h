@@ -176,15 +176,20 @@ cudaError_t launch_decode_window(const void* q, const void* k, const void* v, co
                                  int Sk, int D, int window, int sinks, int num_splits, float scale,
                                  cudaStream_t stream, int* status);
 
-// Sliding-window prefill and backward (bf16 O and gradients, D 64 or 128); window
-// and sinks clamped as above.
+// Sliding-window prefill (bf16 O; D 64, 128 or 256) and backward (bf16 gradients; D 64 or
+// 128); window and sinks clamped as above.
 // num_splits > 1: fp32 partials in o_part [ns,B,Hq,Sq,D] and lse_part [ns,B,Hq,Sq],
 // then their combine into o.
 inline int window_head_pairs(int Hq, int Hkv) { return (Hq / Hkv) % 2 == 0; }
-inline long long window_items(long long B, int Hq, int Hkv, int Sq) {  // per split
+inline long long window_items(long long B, int Hq, int Hkv, int Sq, int D) {  // per split
+  if (D == 256) return B * Hq * ((Sq + 127) / 128);  // one query tile a CTA
   return window_head_pairs(Hq, Hkv) ? B * Hq / 2 * ((Sq + 127) / 128)
                                     : B * Hq * ((Sq + 255) / 256);
 }
+cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void* v, void* o,
+                                        float* lse, int B, int Hq, int Hkv, int Sq, int Sk,
+                                        int window, int sinks, int num_splits, float scale,
+                                        cudaStream_t stream, int* status);
 cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, void* o,
                                    float* lse, float* o_part, float* lse_part, int B, int Hq,
                                    int Hkv, int Sq, int Sk, int D, int window, int sinks,
@@ -230,7 +235,7 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const f
 
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int* status, uint64_t* waited_ns,
                                  cudaStream_t stream);
-// bf16 o; D 64 or 128.
+// bf16 o.
 cudaError_t launch_combine_bf16(const float* o_part, const float* lse_part, void* o, float* lse,
                                 int rows, int D, int num_splits, cudaStream_t stream);
 cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o, float* lse,

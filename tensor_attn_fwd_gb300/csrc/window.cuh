@@ -25,8 +25,8 @@ struct TileRange {
     return (j >= b && j < s) || (j >= w && j < e);
   }
   __device__ __forceinline__ int count() const { return s - b + e - w; }
-  __device__ __forceinline__ int tile(int step) const {  // of a whole list
-    return step < s ? step : step - s + w;
+  __device__ __forceinline__ int tile(int step) const {
+    return step < s - b ? b + step : step - (s - b) + w;
   }
   // Steps [x, y) of a whole list, y clamped to its end.
   __device__ __forceinline__ TileRange steps(int x, int y) const {

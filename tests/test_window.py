@@ -125,9 +125,30 @@ def test_forward_and_backward_match_the_formula(shape):
         check(name, got, ref[name], tol[name])
 
 
+# The same shapes at the head dimension that has a kernel of its own (no backward).
+SHAPES_256 = [s[:5] + (256,) + s[6:] for s in SHAPES[:17]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES_256 + [(1, 2, 1, 40, 3000, 256, 1500, 300)])
+@pytest.mark.parametrize("splits", [1, 2, 5, None])
+def test_forward_of_head_dimension_256(shape, splits):
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    splits = splits if splits is None else min(splits, -(-Sk // 128))
+    q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, Sq + 5 * Sk)
+    want, tol = reference(q, k, v, window, sinks, 1.0 / math.sqrt(D))
+    unseen = ~visible(Sq, Sk, window, sinks).any(0)
+    k[:, :, unseen.cuda()] = float("nan")
+    v[:, :, unseen.cuda()] = float("inf")
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=splits)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    check("o", o, want["o"], tol["o"])
+    check("lse", lse, want["lse"], tol["lse"])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,D", [(2, 4, 2, 333, 333, 128), (1, 3, 3, 200, 700, 64),
-                                              (1, 2, 1, 300, 129, 64)])
+                                              (1, 2, 1, 300, 129, 64), (1, 4, 2, 300, 500, 256)])
 def test_a_window_over_everything_is_the_causal_forward(B, Hq, Hkv, Sq, Sk, D):
     q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, 5)
     want = attn.attn_fwd_bf16o(q, k, v, causal=True)
@@ -479,7 +500,8 @@ def test_training_step_in_a_graph_repeats_its_bits():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(2, 4, 2, 301, 301, 64, 100, 4), (1, 4, 1, 129, 777, 128, 300, 5),
-                                   (1, 3, 3, 300, 129, 64, 40, 200), (1, 2, 1, 1300, 1300, 128, 60, 5)])
+                                   (1, 3, 3, 300, 129, 64, 40, 200), (1, 2, 1, 1300, 1300, 128, 60, 5),
+                                   (1, 2, 1, 200, 640, 256, 300, 5)])
 def test_debug_build_stores_in_bounds_and_matches(shape):
     # Every output store checked against its buffer (a stray one is skipped and reported).
     from tensor_attn_fwd_gb300 import build as attn_build
@@ -492,7 +514,8 @@ def test_debug_build_stores_in_bounds_and_matches(shape):
     scale, stream = 1.0 / math.sqrt(D), torch.cuda.current_stream().cuda_stream
     floats = 4 * B * Hq * Sq * (D + 1)
     n = ctypes.c_longlong(0)
-    attn.load_library().attn_window_bwd_workspace(*shape, ctypes.byref(n))
+    if D < 256:
+        attn.load_library().attn_window_bwd_workspace(*shape, ctypes.byref(n))
     ws = torch.empty(max(floats, n.value), device="cuda")
     for splits in (1, 2):
         want = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=splits)
@@ -501,13 +524,14 @@ def test_debug_build_stores_in_bounds_and_matches(shape):
                                    lse.data_ptr(), ws.data_ptr(), B, Hq, Hkv, Sq, Sk, D, window,
                                    sinks, splits, scale, stream) == attn.ATTN_OK
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
-    want = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
-    got = [torch.empty_like(t) for t in want]
-    assert dbg.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                               do.data_ptr(), *(t.data_ptr() for t in got), ws.data_ptr(), *shape,
-                               scale, stream) == attn.ATTN_OK
-    for a, b in zip(got, want):
-        assert torch.equal(a, b)
+    if D < 256:
+        want = attn.attn_window_bwd(q, k, v, o, lse, do, window, sinks)
+        got = [torch.empty_like(t) for t in want]
+        assert dbg.attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                   lse.data_ptr(), do.data_ptr(), *(t.data_ptr() for t in got),
+                                   ws.data_ptr(), *shape, scale, stream) == attn.ATTN_OK
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
     qd = q[:, :, -1:].contiguous()
     for splits in (1, 9):
         want = attn.decode_window(qd, k, v, window, sinks, num_splits=splits)
@@ -550,7 +574,6 @@ COMMON = [
     (dict(Hq=3, Hkv=2), attn.ATTN_ERR_INVALID_ARG),
     (dict(Sq=0), attn.ATTN_ERR_INVALID_ARG),
     (dict(scale=float("inf")), attn.ATTN_ERR_INVALID_ARG),
-    (dict(D=256), attn.ATTN_ERR_UNSUPPORTED),
     (dict(D=96), attn.ATTN_ERR_UNSUPPORTED),
     (dict(Sk=(1 << 30) + 1), attn.ATTN_ERR_UNSUPPORTED),
     (dict(v=M), attn.ATTN_ERR_MISALIGNED),
@@ -565,6 +588,7 @@ COMMON = [
     (fwd, dict(ns=4, Sk=300, ws=A), attn.ATTN_ERR_INVALID_ARG),  # three key tiles
     (fwd, dict(ns=2, Sk=300, ws=M), attn.ATTN_ERR_MISALIGNED),
     (fwd, dict(ns=2, Sk=300, ws=A, Sq=1 << 30), attn.ATTN_ERR_UNSUPPORTED),
+    (bwd, dict(D=256), attn.ATTN_ERR_UNSUPPORTED),
     (bwd, dict(ws=None), attn.ATTN_ERR_INVALID_ARG),
     (bwd, dict(dk=M), attn.ATTN_ERR_MISALIGNED)])
 def test_prefill_and_backward_reject(call, kw, code):
