@@ -115,6 +115,7 @@ struct FwdParams {
   size_t split_stride_o, split_stride_lse;
   int total_items;   // B * Hq * num_pairs * num_splits (B * Hq / 2 * num_splits in pairs)
   int window, sinks;  // windowed kernels: row at position p sees (p - window, p] and [0, sinks)
+  int ramp;  // windowed kernels: window_ramp
 };
 
 // A work item is two 128-row query tiles that stream the same K/V: rows
@@ -142,8 +143,7 @@ __device__ __forceinline__ int next_tile(const Item& it, int j) {
     return j + 1;
 }
 
-// Windowed items, KV head by KV head (their query heads, then row tiles side by
-// side, so that the items in flight share K/V in L2).  With an even number of
+// Windowed items, in window_item's order.  With an even number of
 // query heads per KV head an item is one 128-row tile of two heads: both tiles
 // then need the same KV tiles.  Otherwise it is 256 rows of one head, whose tiles
 // differ by one KV tile at either end.
@@ -153,14 +153,11 @@ __device__ __forceinline__ Item get_window_item(const FwdParams& p, int idx) {
   const int per_split = p.total_items / p.num_splits;
   const int split = idx / per_split;
   idx -= split * per_split;
-  const int rest = idx / per_group;
-  const int bg = rest / p.num_pairs;  // b * Hkv + KV head
-  const int tile = p.num_pairs - 1 - rest % p.num_pairs;
+  const WindowItem w = window_item(idx, p.B * p.Hkv, per_group, p.num_pairs, p.ramp);
   Item it;
   it.split = split;
-  it.bh = (bg / p.Hkv) * p.Hq + (bg % p.Hkv) * group +
-          (idx % per_group) * (p.head_pairs ? 2 : 1);
-  it.q_row0 = tile * (p.head_pairs ? 128 : kRowsPerItem);
+  it.bh = w.bg * group + w.member * (p.head_pairs ? 2 : 1);
+  it.q_row0 = w.tile * (p.head_pairs ? 128 : kRowsPerItem);
   it.r[0] = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0);
   it.r[1] = p.head_pairs ? it.r[0]
                          : window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0 + 128);
@@ -932,6 +929,7 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   p.num_splits = num_splits;
   p.window = window;
   p.sinks = sinks;
+  p.ramp = window_ramp(Sq, Sk, window, rows, p.num_pairs);
   p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, D) * num_splits);
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,

@@ -99,7 +99,7 @@ struct Params256 {
   int kv_chunk;     // ORDER 2: KV heads per chunk
   // Windowed: the mask, and the splits of an item (fp32 partials, split s at
   // o + s * split_stride_o and lse + s * split_stride_lse).
-  int window, sinks, num_splits;
+  int window, sinks, num_splits, ramp;
   size_t split_stride_o, split_stride_lse;
 };
 
@@ -157,7 +157,7 @@ __device__ __forceinline__ int item_idx(int round, int cta, int grid) {
 //            +29 %, B4 H16 S4096 +8 %, GQA B4 Hq32 Hkv8 S4096 +6.5 %).  At
 //            S = 8192 the chunks' longest-first lists no longer balance across
 //            the CTAs (multi-head D = 128 B4 H32 S8192: -5 to -8 %).
-// Windowed: KV head by KV head (its query heads, then its row tiles), split by split.
+// Windowed: window_item's order, split by split.
 template <int ORDER, Mask WIN>
 __device__ __forceinline__ Item256 item_at(const Params256& p, int idx) {
   const int BH = p.B * p.Hq;
@@ -166,10 +166,9 @@ __device__ __forceinline__ Item256 item_at(const Params256& p, int idx) {
     const int per_split = p.total_items / p.num_splits, group = p.Hq / p.Hkv;
     it.split = idx / per_split;
     idx -= it.split * per_split;
-    const int rest = idx / group;
-    const int bg = rest / p.num_tiles;  // b * Hkv + KV head
-    it.bh = (bg / p.Hkv) * p.Hq + (bg % p.Hkv) * group + idx % group;
-    it.row0 = (p.num_tiles - 1 - rest % p.num_tiles) * 128;
+    const WindowItem w = window_item(idx, p.B * p.Hkv, group, p.num_tiles, p.ramp);
+    it.bh = w.bg * group + w.member;
+    it.row0 = w.tile * 128;
     it.r = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.row0);
     const int chunk = (it.r.count() + p.num_splits - 1) / p.num_splits;
     it.r = it.r.steps(it.split * chunk, it.split * chunk + chunk);
@@ -834,6 +833,7 @@ cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void
   p.window = window;
   p.sinks = sinks;
   p.num_splits = num_splits;
+  p.ramp = window_ramp(Sq, Sk, window, 128, p.num_tiles);
   p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, kD) * num_splits);
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads256), kSmem256, stream, tmQ, tmK,
