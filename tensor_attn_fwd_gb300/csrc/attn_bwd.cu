@@ -554,21 +554,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // keeps them ahead of that work's tcgen05 operations).  Rows past Sq load
     // row Sq - 1 (in bounds) and are zeroed when staged.
     float pre_l[2] = {0.f, 0.f}, pre_d[2] = {0.f, 0.f};
-    auto fetch = [&](int s) {
-      const int h = g * group + (s_base + s) / per_head;
-      const int m = m0 + (s_base + s) % per_head;
-      const size_t base = static_cast<size_t>(b * p.Hq + h) * p.Sq;
+    // The step being fetched: its query tile, and its head as b * Hq + h (counted, as a
+    // division a step costs 0.5 to 3 % of a windowed backward).
+    int pre_m = 0, next_m = m0, next_head = bg * group;
+    if (s_base > 0) {
+      next_m += s_base % per_head;
+      next_head += s_base / per_head;
+    }
+    auto fetch = [&]() {
+      const size_t base = static_cast<size_t>(next_head) * p.Sq;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int row = min(128 * m + 64 * half + 32 * u + lane, p.Sq - 1);
+        const int row = min(128 * next_m + 64 * half + 32 * u + lane, p.Sq - 1);
         pre_l[u] = ld_nc_f32(p.lse + base + row);
         pre_d[u] = ld_nc_f32(p.delta + base + row);
       }
+      pre_m = next_m;
+      if (++next_m == m0 + per_head) {
+        next_m = m0;
+        ++next_head;
+      }
     };
     if constexpr (WIN) grid_dependency_wait();
-    if (nsteps > 0) fetch(0);
+    if (nsteps > 0) fetch();
     for (int s = 0; s < nsteps && ok; ++s) {
-      const int m = m0 + (s_base + s) % per_head;
+      const int m = pre_m;
       // This step's -LSE (log2 domain) and -Delta for the warpgroup's 64
       // columns, in the warp's own buffer (no cross-warp barrier, so an
       // aborting warp cannot strand others); read back as broadcast float4.
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ndl[32 * u + lane] = rv ? -pre_d[u] : 0.f;
       }
       __syncwarp();
-      if (s + 1 < nsteps) fetch(s + 1);
+      if (s + 1 < nsteps) fetch();
       // Visible columns (query rows 128m + col) of this key: [c_lo, c_hi) --
       // row >= key - (Sk - Sq) under the causal mask, row < Sq.
       const int row_lo = WIN || p.causal ? key - (p.Sk - p.Sq) : -0x40000000;
