@@ -446,6 +446,49 @@ def test_streams_and_two_graphs_at_once(splits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_two_prefill_graphs_at_once(D, splits):
+    window, sinks = 500, 4
+    sets = [inputs(1, 4, 2, 200, 1500, D, s) for s in (1, 2)]
+    want = [attn.attn_window_fwd(*s, window, sinks, num_splits=splits) for s in sets]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    for s in sets:  # both captured on one stream
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(attn.attn_window_fwd(*s, window, sinks, num_splits=splits))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 6, 2, 2100, 2100, 64, 700, 4), (3, 8, 4, 1500, 2000, 128, 900, 130),
+                                   (2, 5, 5, 3000, 3000, 64, 4000, 0), (4, 4, 2, 1300, 1300, 256, 400, 3)])
+def test_heads_of_many_rounds_match_a_call_of_their_own(shape):
+    # More items than SMs, in every order of the schedule: a KV head's rows come out the
+    # same bits as when it is called alone.
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, 3)
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=1)
+    G = Hq // Hkv
+    for b in range(B):
+        for h in range(Hkv):
+            one = [t[b:b + 1, h * n:(h + 1) * n].contiguous() for t, n in ((q, G), (k, 1), (v, 1))]
+            o1, l1 = attn.attn_window_fwd(*one, window, sinks, num_splits=1)
+            assert torch.equal(o1, o[b:b + 1, h * G:(h + 1) * G])
+            assert torch.equal(l1, lse[b:b + 1, h * G:(h + 1) * G])
+
+
+@pytest.mark.gpu
 def test_threads_on_streams_of_their_own():
     shapes = [(1, 4, 2, 300, 300, 64, 70, 4), (1, 2, 2, 40, 2000, 128, 900, 3),
               (2, 6, 2, 500, 500, 64, 33, 130), (1, 8, 1, 700, 700, 128, 128, 0)]
