@@ -374,8 +374,9 @@ ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *
 /*
  * A split count for attn_window_fwd on the current device (a measured rule of this
  * library): of the counts whose work items (per split, 128 rows of two query heads
- * of a KV head, or 256 rows of one where their number is odd) run at the same time,
- * the one with the least estimated time.  At most 32.  Host-only.
+ * of a KV head, or 256 rows of one where their number is odd; D = 256: 128 rows of
+ * one) run at the same time, the one with the least estimated time.  At most 32.
+ * Host-only.
  * ATTN_ERR_INVALID_ARG as attn_window_fwd.
  */
 ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,

@@ -286,6 +286,9 @@ int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, in
   // back at 5 bytes a ps.  Measured (us) against it, D = 128, 32/8 heads: Sq 512, 34
   // tiles: 1 split 51.9 (est. 52), 2 37.2 (38); Sq 512, 10 tiles: 1 20.0 (17), 2 21.1
   // (20); Sq 128, 34 tiles: 4 22.8 (23), 8 19.4 (20), 16 26.4 (more than one round).
+  // D = 256, where an item is one tile of a head, measured alike: 16/4 heads, Sq 512, 34
+  // tiles: 1 56.0, 2 36.9, 3 50.0; Sq 128: 7 20.6, 8 22.3; 32 items of 4 tiles: 1 12.3,
+  // 2 13.6; 24 items of 34: 6 22.1, 7 30.7.
   const long long partial_ns = 2ll * B * Hq * Sq * D * 4 / 5000;  // of one split
   long long best = 1, best_ns = tiles * 1400 + 3500;
   for (long long ns = 2; ns <= tiles && ns <= 32 && ns * items <= n_sm; ++ns) {
