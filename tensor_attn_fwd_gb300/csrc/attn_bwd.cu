@@ -137,6 +137,9 @@ struct BwdParams {
   // to `partials`; bwd_sum_parts_kernel adds them in order.
   int split_tiles, parts;
   float* partials;
+  // Windowed: B * Hq, B * Hkv, Hq / Hkv, parts.  (As divisions they cost dQ's roles,
+  // which find their next tile between two, about as much as the forward's.)
+  FixedDiv by_q_planes, by_kv_planes, by_group, by_parts;
 };
 
 // Read-only global load issued where it stands in the program.
@@ -396,18 +399,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // Work: key tile n of KV head (b, g); CTAs are numbered n-major so the
   // largest work (low n under a causal mask) is scheduled first.
   const int BH = p.B * p.Hkv;
-  int n = blockIdx.x / BH;
-  const int bg = blockIdx.x % BH;
+  int n = WIN ? p.by_kv_planes.div(blockIdx.x) : blockIdx.x / BH;
+  const int bg = blockIdx.x - n * BH;
   int part = -1;  // windowed: this CTA's part of a split tile
   if constexpr (WIN) {
     if (n < p.split_tiles * p.parts) {
-      part = n % p.parts;
-      n /= p.parts;
+      const int tile = p.by_parts.div(n);
+      part = n - tile * p.parts;
+      n = tile;
     } else {
       n -= p.split_tiles * (p.parts - 1);
     }
   }
-  const int b = bg / p.Hkv, g = bg % p.Hkv;
   const int group = p.Hq / p.Hkv;
   const int mtiles = (p.Sq + 127) / 128;
   int m0 = min(first_q_tile(p, n), mtiles);
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int s_base = 0;  // first of the tile's steps that this CTA takes
   if constexpr (WIN) {
     if (part >= 0) {
-      const int chunk = (nsteps + p.parts - 1) / p.parts;
+      const int chunk = p.by_parts.div(nsteps + p.parts - 1);
       s_base = min(part * chunk, nsteps);
       nsteps = min(chunk, nsteps - s_base);
     }
@@ -468,13 +471,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int st = s % kStages;
         bool good = true;
         if (s >= kStages) good = bwd_wait(&bars->empty[st], ((s / kStages) - 1) & 1, bars);
-        const int h = g * group + (s_base + s) / per_head;
+        const int head = bg * group + (s_base + s) / per_head;  // b * Hq + h
         const int m = m0 + (s_base + s) % per_head;
         uint8_t* dst = sRing + st * 2 * C::kTile;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars->full[st], 2 * C::kTile);
-          load_tile<D>(dst, &tmQ, &bars->full[st], 128 * m, b * p.Hq + h);
-          load_tile<D>(dst + C::kTile, &tmDO, &bars->full[st], 128 * m, b * p.Hq + h);
+          load_tile<D>(dst, &tmQ, &bars->full[st], 128 * m, head);
+          load_tile<D>(dst + C::kTile, &tmDO, &bars->full[st], 128 * m, head);
         }
         __syncwarp();
         ok = __all_sync(0xffffffffu, good);
@@ -847,6 +850,12 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
   const int mtiles = (p.Sq + 127) / 128;
   const int total = BH * mtiles;
   const int group = p.Hq / p.Hkv;
+  // Query tile m of head bh (b * Hq + h) of item idx.
+  auto tile_of = [&](int idx, int& m, int& bh) {
+    const int rank = WIN ? p.by_q_planes.div(idx) : idx / BH;
+    m = mtiles - 1 - rank;
+    bh = WIN ? idx - rank * BH : idx % BH;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->fixed_full, 1);  // this tile's Q and dO have landed
@@ -900,11 +909,12 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
-      const int m = mtiles - 1 - idx / BH, bh = idx % BH;
+      int m, bh;
+      tile_of(idx, m, bh);
       const DqTiles<WIN> tiles(p, m);
       const int nsteps = tiles.nsteps;
       if (nsteps == 0) continue;
-      const int bkv = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / group;
+      const int bkv = WIN ? p.by_group.div(bh) : (bh / p.Hq) * p.Hkv + (bh % p.Hq) / group;
       // Q and dO of this tile once the previous tile's last S and dP are done.
       if (kt > 0 && !(ok = __all_sync(0xffffffffu, bwd_wait(&bars->q_empty, (kt - 1) & 1, bars))))
         break;
@@ -977,7 +987,9 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
-      const DqTiles<WIN> tiles(p, mtiles - 1 - idx / BH);
+      int m, bh;
+      tile_of(idx, m, bh);
+      const DqTiles<WIN> tiles(p, m);
       const int nsteps = tiles.nsteps;
       if (nsteps == 0) continue;
       const int buf = kt & 1;
@@ -1029,7 +1041,8 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
-      const int m = mtiles - 1 - idx / BH, bh = idx % BH;
+      int m, bh;
+      tile_of(idx, m, bh);
       const int nsteps = DqTiles<WIN>(p, m).nsteps;
       const int buf = kt & 1;
       if (nsteps > 0 && kt >= 2) {
@@ -1068,7 +1081,8 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     for (int rnd = 0; ok; ++rnd) {
       const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
       if (idx >= total) break;
-      const int m = mtiles - 1 - idx / BH, bh = idx % BH;
+      int m, bh;
+      tile_of(idx, m, bh);
       const DqTiles<WIN> tiles(p, m);
       const int nsteps = tiles.nsteps;
       const int row = 128 * m + r;
@@ -1295,7 +1309,7 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
                             static_cast<int>(C::kSmemDq + (WIN ? kDqDeltaBytes : 0)))) !=
       cudaSuccess)
     return e;
-  BwdParams p;
+  BwdParams p = {};
   p.lse = lse;
   p.delta = delta;
   p.status = status;
@@ -1324,6 +1338,10 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
     p.split_tiles = split.tiles;
     p.parts = split.parts;
     p.partials = delta + window_bwd_delta_floats(B, Hq, Sq);
+    p.by_q_planes = FixedDiv(B * Hq);
+    p.by_kv_planes = FixedDiv(B * Hkv);
+    p.by_group = FixedDiv(Hq / Hkv);
+    p.by_parts = FixedDiv(p.parts);
     p.out0 = static_cast<float*>(dq);
     p.out1 = nullptr;
     if ((e = launch_programmatic(bwd_dq_kernel<D, WIN>, dim3(q_ctas), dim3(kDqWinThreads),

@@ -115,7 +115,7 @@ struct FwdParams {
   size_t split_stride_o, split_stride_lse;
   int total_items;   // B * Hq * num_pairs * num_splits (B * Hq / 2 * num_splits in pairs)
   int window, sinks;  // windowed kernels: row at position p sees (p - window, p] and [0, sinks)
-  int ramp;  // windowed kernels: window_ramp
+  WindowOrder order;  // windowed kernels: the items
 };
 
 // A work item is two 128-row query tiles that stream the same K/V: rows
@@ -124,6 +124,7 @@ struct FwdParams {
 // query heads 2k and 2k+1 (the same KV head), so that both tiles have rows.
 struct Item {
   int bh;      // b * Hq + h of query tile 0; tile 1's is bh + head_pairs
+  int bg;      // windowed: b * Hkv + KV head
   int q_row0;  // first query row of tile 0; tile 1's is q_row0 + 128 (0 in head pairs)
   int split;   // KV split
   int j0;      // first KV tile of the split
@@ -143,32 +144,22 @@ __device__ __forceinline__ int next_tile(const Item& it, int j) {
     return j + 1;
 }
 
-// Windowed items, in window_item's order.  With an even number of
+// Windowed items, in WindowOrder's order.  With an even number of
 // query heads per KV head an item is one 128-row tile of two heads: both tiles
 // then need the same KV tiles.  Otherwise it is 256 rows of one head, whose tiles
 // differ by one KV tile at either end.
 __device__ __forceinline__ Item get_window_item(const FwdParams& p, int idx) {
-  const int group = p.Hq / p.Hkv;
-  const int per_group = p.head_pairs ? group / 2 : group;
-  const int per_split = p.total_items / p.num_splits;
-  const int split = idx / per_split;
-  idx -= split * per_split;
-  const WindowItem w = window_item(idx, p.B * p.Hkv, per_group, p.num_pairs, p.ramp);
+  const WindowItem w = p.order.item(idx);
   Item it;
-  it.split = split;
-  it.bh = w.bg * group + w.member * (p.head_pairs ? 2 : 1);
+  it.split = w.split;
+  it.bg = w.bg;
+  it.bh = (w.bg * p.order.per_group + w.member) << p.head_pairs;
   it.q_row0 = w.tile * (p.head_pairs ? 128 : kRowsPerItem);
   it.r[0] = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0);
   it.r[1] = p.head_pairs ? it.r[0]
                          : window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0 + 128);
-  if (p.num_splits > 1) {
-    // Split s of a query tile: its s-th equal run of steps.
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int chunk = (it.r[t].count() + p.num_splits - 1) / p.num_splits;
-      it.r[t] = it.r[t].steps(split * chunk, split * chunk + chunk);
-    }
-  }
+  it.r[0] = p.order.steps_of(it.r[0], w.split);
+  it.r[1] = p.order.steps_of(it.r[1], w.split);
   it.n[0] = it.r[0].e;
   it.n[1] = it.r[1].e;
   it.u = tile_union(it.r[0], it.r[1]);
@@ -305,7 +296,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
     const int n = max(it.n[0], it.n[1]);  // end of the item's KV tiles
     if (n <= it.j0) continue;
     const int b = it.bh / p.Hq, h = it.bh % p.Hq;  // both tiles' KV head
-    const int bkv = b * p.Hkv + h / group;
+    const int bkv = WIN ? it.bg : b * p.Hkv + h / group;
     if (q_ctr > 0 && !(ok = wait_warp(&bars->q_empty, (q_ctr - 1) & 1, bars))) break;
     if (elect_one()) {
       mbar_arrive_expect_tx(&bars->q_full, 2 * C::kTileBytes);
@@ -929,7 +920,7 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   p.num_splits = num_splits;
   p.window = window;
   p.sinks = sinks;
-  p.ramp = window_ramp(Sq, Sk, window, rows, p.num_pairs);
+  p.order = WindowOrder::make(Sq, Sk, window, rows, B * Hkv, (Hq / Hkv) >> p.head_pairs, num_splits);
   p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, D) * num_splits);
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,

@@ -99,7 +99,8 @@ struct Params256 {
   int kv_chunk;     // ORDER 2: KV heads per chunk
   // Windowed: the mask, and the splits of an item (fp32 partials, split s at
   // o + s * split_stride_o and lse + s * split_stride_lse).
-  int window, sinks, num_splits, ramp;
+  int window, sinks;
+  WindowOrder order;
   size_t split_stride_o, split_stride_lse;
 };
 
@@ -108,7 +109,7 @@ struct Item256 {
   int row0;  // first query row
   int n;     // KV tiles to visit (0: nothing visible)
   TileRange r;  // windowed: those tiles
-  int split;
+  int split, bg;  // windowed: key split; b * Hkv + KV head
 };
 
 // The KV tile of an item's step j.
@@ -157,21 +158,19 @@ __device__ __forceinline__ int item_idx(int round, int cta, int grid) {
 //            +29 %, B4 H16 S4096 +8 %, GQA B4 Hq32 Hkv8 S4096 +6.5 %).  At
 //            S = 8192 the chunks' longest-first lists no longer balance across
 //            the CTAs (multi-head D = 128 B4 H32 S8192: -5 to -8 %).
-// Windowed: window_item's order, split by split.
+// Windowed: WindowOrder's order.
 template <int ORDER, Mask WIN>
 __device__ __forceinline__ Item256 item_at(const Params256& p, int idx) {
   const int BH = p.B * p.Hq;
   Item256 it;
   if constexpr (WIN) {
-    const int per_split = p.total_items / p.num_splits, group = p.Hq / p.Hkv;
-    it.split = idx / per_split;
-    idx -= it.split * per_split;
-    const WindowItem w = window_item(idx, p.B * p.Hkv, group, p.num_tiles, p.ramp);
-    it.bh = w.bg * group + w.member;
+    const WindowItem w = p.order.item(idx);
+    it.split = w.split;
+    it.bg = w.bg;
+    it.bh = w.bg * p.order.per_group + w.member;
     it.row0 = w.tile * 128;
     it.r = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.row0);
-    const int chunk = (it.r.count() + p.num_splits - 1) / p.num_splits;
-    it.r = it.r.steps(it.split * chunk, it.split * chunk + chunk);
+    it.r = p.order.steps_of(it.r, w.split);
     it.n = it.r.count();
     return it;
   }
@@ -285,7 +284,7 @@ __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
     }
     __syncwarp();
     ++q_ctr;
-    const int bkv = (x.bh / p.Hq) * p.Hkv + (x.bh % p.Hq) / group;
+    const int bkv = WIN ? x.bg : (x.bh / p.Hq) * p.Hkv + (x.bh % p.Hq) / group;
     const int key0 = WIN ? step_tile<WIN>(x, 0) * 128 : 0;
     bool g = load_half(tmK, 0, key0, bkv, sKV, bars, ring);
     g &= load_half(tmK, 1, key0, bkv, sKV, bars, ring);
@@ -293,7 +292,7 @@ __device__ void load_role256(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   };
   ok = load_q_k0(it);
   while (ok) {
-    const int bkv = (it.bh / p.Hq) * p.Hkv + (it.bh % p.Hq) / group;
+    const int bkv = WIN ? it.bg : (it.bh / p.Hq) * p.Hkv + (it.bh % p.Hq) / group;
     Item256 nxt;
     bool have_next = false;
     for (int j = 0; j < it.n && ok; ++j) {
@@ -832,8 +831,7 @@ cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void
   p.num_tiles = (Sq + 127) / 128;
   p.window = window;
   p.sinks = sinks;
-  p.num_splits = num_splits;
-  p.ramp = window_ramp(Sq, Sk, window, 128, p.num_tiles);
+  p.order = WindowOrder::make(Sq, Sk, window, 128, B * Hkv, Hq / Hkv, num_splits);
   p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, kD) * num_splits);
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads256), kSmem256, stream, tmQ, tmK,

@@ -12,6 +12,21 @@
 
 namespace attn {
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 with one multiplication (Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication", 1994).
+struct FixedDiv {
+  uint32_t mul, shift;
+  FixedDiv() = default;
+  explicit FixedDiv(uint32_t d) : shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >>
+                            shift);
+  }
+};
+
 // KV tiles [b, s) and [w, e) in that order, or none (e = 0).  Of a whole query tile
 // b = 0 and s <= w < e: [0, s) holds sinks and [w, e) runs from its first row's window
 // start to its last row's position (sink tiles that meet it are counted to it).  A
@@ -53,32 +68,64 @@ __device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window,
 // Order of the forward's items (per_group of them at each tile of a KV head, n_bg KV
 // heads).  First the tiles whose rows all have their whole window, which take equally
 // long: KV head by KV head, so that the items in flight share K/V in L2.  Then the
-// `ramp` tiles below (window_ramp), longest first across the heads, which balances the
+// `ramp` tiles below, longest first across the heads, which balances the
 // CTAs: with all of them in the first order a window of all of S = 4096 keys (16/8
 // heads of 128) took 76.3 us instead of 51.5, and one of 512 keys at B2 S4096 32/8 heads
 // 80.1 instead of 71.1.
+//
+// Every role of a CTA works an item out for itself, between two items, so the divisions
+// are multiplications (as divisions they cost 0.7 us an item).
 struct WindowItem {
-  int bg, member, tile;
+  int split, bg, member, tile;
 };
-__device__ __forceinline__ WindowItem window_item(int idx, int n_bg, int per_group, int tiles,
-                                                  int ramp) {
-  const int whole = tiles - ramp;
-  const int rest = idx / per_group;
-  const int member = idx - rest * per_group;
-  if (rest < n_bg * whole) {
-    const int bg = rest / whole;
-    return {bg, member, tiles - 1 - (rest - bg * whole)};
+struct WindowOrder {
+  int tiles, n_bg, per_group, num_splits, per_split, ramp;
+  FixedDiv by_split, by_group, by_whole, by_bg, by_num_splits;
+
+  // rows: query rows of a tile.
+  static WindowOrder make(int Sq, int Sk, int window, int rows, int n_bg, int per_group,
+                          int num_splits) {
+    WindowOrder o;
+    o.tiles = (Sq + rows - 1) / rows;
+    o.n_bg = n_bg;
+    o.per_group = per_group;
+    o.num_splits = num_splits;
+    o.per_split = n_bg * per_group * o.tiles;
+    // Tiles that hold a row with less than its window before it.
+    const long long short_rows = static_cast<long long>(window) - 1 - (Sk - Sq);
+    const long long n = short_rows <= 0 ? 0 : (short_rows + rows - 1) / rows;
+    o.ramp = n < o.tiles ? static_cast<int>(n) : o.tiles;
+    o.by_split = FixedDiv(o.per_split);
+    o.by_group = FixedDiv(per_group);
+    o.by_whole = FixedDiv(o.tiles > o.ramp ? o.tiles - o.ramp : 1);
+    o.by_bg = FixedDiv(n_bg);
+    o.by_num_splits = FixedDiv(num_splits);
+    return o;
   }
-  const int t = (rest - n_bg * whole) / n_bg;
-  return {rest - n_bg * (whole + t), member, ramp - 1 - t};
-}
-// Tiles of `rows` query rows that hold a row with less than its window before it.
-inline int window_ramp(int Sq, int Sk, int window, int rows, int tiles) {
-  const long long short_rows = static_cast<long long>(window) - 1 - (Sk - Sq);
-  if (short_rows <= 0) return 0;
-  const long long n = (short_rows + rows - 1) / rows;
-  return n < tiles ? static_cast<int>(n) : tiles;
-}
+  __device__ __forceinline__ WindowItem item(int idx) const {
+    WindowItem x;
+    x.split = by_split.div(idx);
+    idx -= x.split * per_split;
+    const int rest = by_group.div(idx);
+    x.member = idx - rest * per_group;
+    const int whole = tiles - ramp;
+    if (rest < n_bg * whole) {
+      x.bg = by_whole.div(rest);
+      x.tile = tiles - 1 - (rest - x.bg * whole);
+    } else {
+      const int t = by_bg.div(rest - n_bg * whole);
+      x.bg = rest - n_bg * (whole + t);
+      x.tile = ramp - 1 - t;
+    }
+    return x;
+  }
+  // The steps of split `split` of a tile's list: its split-th equal run.
+  __device__ __forceinline__ TileRange steps_of(const TileRange& r, int split) const {
+    if (num_splits == 1) return r;
+    const int chunk = by_num_splits.div(r.count() + num_splits - 1);
+    return r.steps(split * chunk, split * chunk + chunk);
+  }
+};
 
 // The tiles of two neighbouring query tiles as one list (it may hold a tile that
 // neither needs).
