@@ -26,6 +26,10 @@
 //     14.0 / 9.7 / 4.9; 256 x 128, 30000 14.3 / 10.2 / 5.0; 256 x 256, 60000 14.1 / 10.3
 //     / 5.0; 1024 x 2048, 2 M 44.5 / 35.6 / 11.0 (a launch per phase: 64.4 / 52.0 / 12.5).
 //     Bound there by the L2's rate of scattered 4-byte atomics.
+// The forms were compared with divisions in fork.  As multiplications they save it 0.4 to
+// 1.5 us up to 2^20 slots (8 x 48 4.5, 32 x 64 5.8, 64 x 64 7.7, 256 x 128 12.4, 1024 x
+// 512 with 500000 pages 18.6); from 2^21 on it takes 8 % longer (48.0), the atomics
+// meeting in denser bursts.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +38,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace attn {
 namespace {
@@ -152,6 +157,7 @@ struct FreeOp {
   int *table_out, *refs_out;
   int B, M, P, page_size, window, sinks, room;
   int refs_vec, table_vec;  // 16-byte accesses are aligned
+  FixedDiv by_row;          // M, or M / 4 with table_vec
   int* status;
 
   // Slots s, s + 1, ... of a row of `len` keys, holding e: the pages kept, or -1 for
@@ -195,7 +201,7 @@ struct FreeOp {
     if (table_vec) {
       const unsigned row_vecs = M / 4;
       for (unsigned i = tid; i < entries / 4; i += n_threads) {
-        const int b = i / row_vecs, s = 4 * (i - b * row_vecs), len = length(b);
+        const int b = by_row.div(i), s = 4 * (i - b * row_vecs), len = length(b);
         const int4 x = reinterpret_cast<const int4*>(table)[i];
         int e[4] = {x.x, x.y, x.z, x.w};
         settle(e, s, len);
@@ -203,7 +209,7 @@ struct FreeOp {
       }
     } else {
       for (unsigned i = tid; i < entries; i += n_threads) {
-        const int b = i / static_cast<unsigned>(M);
+        const int b = by_row.div(i);
         int e[1] = {table[i]};
         settle(e, i - b * M, length(b));
         table_out[i] = e[0];
@@ -219,7 +225,15 @@ struct ForkOp {
   int *table_out, *refs_out, *seqlens_out, *src, *dst, *counts;
   int *lowest, *free_list, *need, *cta_free, *cta_need;  // workspace
   int B, R, M, P, page_size, room;
+  FixedDiv by_page, by_row, by_writable;  // page_size, M, small_slots
   int* status;
+
+  // Slots of a row that hold keys or shall: ceil((len + room) / page_size), at most M.
+  // (M * page_size <= 2^30 and the host clamps room to it.)
+  __device__ __forceinline__ int slots_for(int len) const {
+    const unsigned keys = min(static_cast<unsigned>(len) + room, static_cast<unsigned>(M) * page_size);
+    return by_page.div(static_cast<int>(keys + page_size - 1));
+  }
 
   // New row r: its parent (-1: an empty row), length, and slots to be written [lo, hi).
   struct Row {
@@ -233,9 +247,8 @@ struct ForkOp {
       x.parent = -1;
     }
     x.len = x.parent < 0 ? 0 : min(max(seqlens[x.parent], 0), M * page_size);
-    x.lo = x.len / page_size;
-    const long long end = (static_cast<long long>(x.len) + room + page_size - 1) / page_size;
-    x.hi = x.parent < 0 ? 0 : static_cast<int>(min(end, static_cast<long long>(M)));
+    x.lo = by_page.div(x.len);
+    x.hi = x.parent < 0 ? 0 : slots_for(x.len);
     return x;
   }
   // A page of a slot to be written stays with the lowest (row, slot) that has it
@@ -269,7 +282,7 @@ struct ForkOp {
       }
       // ... and the read-only slots of the new one.
       for (unsigned i = tid; i < new_entries; i += n_threads) {
-        const int r = i / static_cast<unsigned>(M), s = i - r * M;
+        const int r = by_row.div(i), s = i - r * M;
         const Row x = row(r);
         int e = -1;
         if (s < x.hi || s < x.lo) e = checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, status);
@@ -366,7 +379,7 @@ struct ForkOp {
   // One CTA, everything but the tables in shared memory.  The slots to be written are
   // numbered r * W + j, j < W = room / page_size + 2, which is their order, so each
   // thread takes a run of them and one prefix sum ranks the pages they need.
-  static int small_slots(int room, int page_size) { return room / page_size + 2; }
+  __host__ __device__ static int small_slots(int room, int page_size) { return room / page_size + 2; }
   static size_t small_bytes(int P, int R) {
     return (pad(P) + 2ll * P + 2ll * R) * sizeof(int);
   }
@@ -401,13 +414,10 @@ struct ForkOp {
       const int e = checked_entry(table[i], P, status);
       if (e >= 0) atomicSub(held + pad(e), 1);
     }
-    const auto slot_end = [&](int r) {
-      const long long end = (static_cast<long long>(len[r]) + room + page_size - 1) / page_size;
-      return parent[r] < 0 ? 0 : static_cast<int>(min(end, static_cast<long long>(M)));
-    };
+    const auto slot_end = [&](int r) { return parent[r] < 0 ? 0 : slots_for(len[r]); };
     for (unsigned i = t; i < new_entries; i += kThreads) {
-      const int r = i / static_cast<unsigned>(M), s = i - r * M;
-      const int lo = len[r] / page_size;
+      const int r = by_row.div(i), s = i - r * M;
+      const int lo = by_page.div(len[r]);
       int e = -1;
       if (s < lo || s < slot_end(r)) e = checked_entry(table[parent[r] * M + s], P, status);
       if (s < lo) {
@@ -419,13 +429,13 @@ struct ForkOp {
       table_out[i] = e;
     }
     __syncthreads();
-    const int W = room / page_size + 2, slots = R * W;
+    const int W = small_slots(room, page_size), slots = R * W;
     const int run = (slots + kThreads - 1) / kThreads;
     const int f0 = min(t * run, slots), f1 = min(f0 + run, slots);
     // Slot f's entry; -2 if it is past its row's end.  `stays`: its page is its own.
     const auto entry = [&](int f, int& r, int& s, bool& stays) {
-      r = f / W;
-      s = len[r] / page_size + f - r * W;
+      r = by_writable.div(f);
+      s = by_page.div(len[r]) + f - r * W;
       stays = false;
       if (s >= slot_end(r)) return -2;
       const int e = checked_entry(table[parent[r] * M + s], P, nullptr);
@@ -681,6 +691,7 @@ cudaError_t launch_pages_free(const int* table, const int* refs, const int* seql
   FreeOp op{table, refs, seqlens, table_out, refs_out, B, M, P, page_size, window, sinks, room};
   op.refs_vec = aligned16(refs) && aligned16(refs_out);
   op.table_vec = M % 4 == 0 && aligned16(table) && aligned16(table_out);
+  op.by_row = FixedDiv(op.table_vec ? M / 4 : M);
   op.status = status;
   const long long entries = static_cast<long long>(B) * M;
   return launch_phases(op, entries > P ? entries : P, stream);
@@ -701,11 +712,14 @@ cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seql
   op.M = M;
   op.P = P;
   op.page_size = page_size;
-  op.room = room;
+  op.room = room < M * page_size ? room : M * page_size;  // further keys have no slots
+  op.by_page = FixedDiv(page_size);
+  op.by_row = FixedDiv(M);
+  op.by_writable = FixedDiv(ForkOp::small_slots(op.room, page_size));
   op.status = status;
   const long long entries = static_cast<long long>(B > R ? B : R) * M;
   if (entries <= kSmallForkEntries && P <= kSmallForkPages &&
-      static_cast<long long>(R) * ForkOp::small_slots(room, page_size) <= kSmallForkSlots)
+      static_cast<long long>(R) * ForkOp::small_slots(op.room, page_size) <= kSmallForkSlots)
     return launch_small(op, ForkOp::small_bytes(P, R), stream);
   return launch_phases(op, entries > P ? entries : P, stream);
 }
