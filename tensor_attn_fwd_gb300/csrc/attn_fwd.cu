@@ -40,8 +40,8 @@
 // The windowed instantiations (Mask; window.cuh) are the same kernel on the key tiles
 // that a sliding window with sinks leaves: a query tile's steps walk a list of tiles
 // in place of a range, and rows mask the tiles they see in part.  Bound, like the
-// causal form, by the hand-off between the MMA warp and the softmax warps: 0.91 us a
-// 128 x 128 step at D = 128 (8192 rows, 32/8 heads, window 1024, sinks 4: 118 us, 1.46
+// causal form, by the hand-off between the MMA warp and the softmax warps: 0.89 us a
+// 128 x 128 step at D = 128 (8192 rows, 32/8 heads, window 1024, sinks 4: 115 us, 1.49
 // PFLOP/s executed), a fifth of it around an item's steps.
 #include <cuda.h>
 #include <cuda_bf16.h>
