@@ -354,12 +354,12 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const float *
  *   o [B,Hq,Sq,D] bf16 (each fp32 result rounded to nearest even once)
  *   lse [B,Hq,Sq] fp32
  *   window >= 1, sinks >= 0 (else ATTN_ERR_INVALID_ARG); both may exceed Sk.
- *   num_splits: 1, or up to ceil(Sk / 128) (else ATTN_ERR_INVALID_ARG): the key tiles
- *      that a query tile sees are shared out evenly over so many CTAs, for chunks with
- *      too few rows to fill the GPU, and their fp32 partials are merged
- *      (attn_combine's formula) by a second kernel
- *   workspace: num_splits * B * Hq * Sq * (D + 1) floats, 16-byte aligned, contents
- *      undefined; not touched, and NULL allowed, with one split
+ *   num_splits: 1, or up to ceil(Sk / 128) (else ATTN_ERR_INVALID_ARG): of the query
+ *      tiles that do not fill the GPU (all of a chunk with few rows, of more the last
+ *      round), the key tiles that each sees are shared out evenly over so many CTAs, and
+ *      their fp32 partials are merged (attn_combine's formula) by a second kernel
+ *   workspace: attn_window_fwd_workspace floats, 16-byte aligned, contents undefined;
+ *      not touched, and NULL allowed, with one split
  *   D in {64, 128, 256} (else ATTN_ERR_UNSUPPORTED).  Sizes, alignment, other errors
  *   and rows that see no key (O = 0, LSE = -inf) as attn_fwd.
  *   Keys that no row sees may hold anything (NaN, unwritten memory).  K and V have to
@@ -373,14 +373,19 @@ ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *
 
 /*
  * A split count for attn_window_fwd on the current device (a measured rule of this
- * library): of the counts whose work items (per split, 128 rows of two query heads
- * of a KV head, or 256 rows of one where their number is odd; D = 256: 128 rows of
- * one) run at the same time, the one with the least estimated time.  At most 32.
- * Host-only.
+ * library): of the counts whose work items in the last round (per split, 128 rows of
+ * two query heads of a KV head, or 256 rows of one where their number is odd; D = 256:
+ * 128 rows of one) run at the same time, the one with the least estimated time.  At
+ * most 32.  Host-only.
  * ATTN_ERR_INVALID_ARG as attn_window_fwd.
  */
 ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
                                         int sinks, int *num_splits);
+
+/* Floats of workspace for attn_window_fwd with num_splits on the current device (0 with
+ * one).  Host-only.  ATTN_ERR_INVALID_ARG and ATTN_ERR_UNSUPPORTED as attn_window_fwd. */
+ATTN_API int attn_window_fwd_workspace(int B, int Hq, int Hkv, int Sq, int D, int num_splits,
+                                       long long *floats);
 
 /*
  * Gradients of sum(dO * O) for attn_window_fwd: attn_bwd's formulas under its mask.

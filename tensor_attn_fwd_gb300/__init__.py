@@ -90,6 +90,7 @@ _SIGNATURES = {
     "attn_bwd": ([_vp] * 10 + [_int] * 7 + [_flt, _vp], _int),
     "attn_window_fwd": ([_vp] * 6 + [_int] * 9 + [_flt, _vp], _int),
     "attn_window_fwd_num_splits": ([_int] * 8 + [ctypes.POINTER(_int)], _int),
+    "attn_window_fwd_workspace": ([_int] * 6 + [ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_window_bwd": ([_vp] * 10 + [_int] * 8 + [_flt, _vp], _int),
     "attn_window_bwd_workspace": ([_int] * 8 + [ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_decode_window_num_splits": ([_int] * 7 + [ctypes.POINTER(_int)], _int),
@@ -735,8 +736,9 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
 
     q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] (bf16, contiguous), D 64, 128 or 256.  Row i stands
     at p = i + Sk - Sq and sees key j when j <= p and (j > p - window or j < sinks).
-    ``num_splits`` > 1 cuts each row's keys into so many parts and merges them, for
-    chunks with too few rows to fill the GPU; None picks attn_window_fwd_num_splits.
+    ``num_splits`` > 1 cuts the keys of the rows that do not fill the GPU (all of a chunk
+    with few rows, of more the last round) into so many parts and merges them; None
+    picks attn_window_fwd_num_splits.
     """
     call = (_fast or _native()).window_fwd
     if stream is not None:

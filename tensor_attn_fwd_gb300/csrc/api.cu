@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "window.cuh"
 
 namespace attn {
 namespace {
@@ -241,6 +242,20 @@ int attn_fwd_splitkv(const void* q, const void* k, const void* v, float* o_part,
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+namespace {
+// Items that splits cut (the last round's), at most: see WindowOrder.
+long long window_split_items(long long B, int Hq, int Hkv, int Sq, int D) {
+  const long long items = window_items(B, Hq, Hkv, Sq, D), n_sm = sm_count();
+  return items % n_sm;
+}
+bool window_splits_fit(int B, int Hq, int Hkv, int Sq, int D, int num_splits) {
+  const long long rem = window_split_items(B, Hq, Hkv, Sq, D);
+  return static_cast<long long>(B) * Hq * Sq <= (1ll << 30) &&
+         window_items(B, Hq, Hkv, Sq, D) + rem * num_splits <= (1ll << 30) &&
+         rem * num_splits * window_item_rows(D) * D <= kMaxElems;
+}
+}  // namespace
+
 int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                     float* workspace, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
                     int sinks, int num_splits, float scale, void* stream) {
@@ -251,22 +266,16 @@ int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float*
   if (num_splits > 1) {
     // Every split of the longest row has a key tile; rows and items are counted with int.
     if (num_splits > (Sk + 127) / 128) return ATTN_ERR_INVALID_ARG;
-    if (static_cast<long long>(B) * Hq * Sq > (1ll << 30) ||
-        window_items(B, Hq, Hkv, Sq, D) * num_splits > (1ll << 30) ||
-        static_cast<long long>(num_splits) * B * Hq * Sq * D > kMaxElems)
-      return ATTN_ERR_UNSUPPORTED;
+    if (!window_splits_fit(B, Hq, Hkv, Sq, D, num_splits)) return ATTN_ERR_UNSUPPORTED;
     if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
   }
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
-  float* lse_part = workspace;
-  if (num_splits > 1) lse_part += static_cast<long long>(num_splits) * B * Hq * Sq * D;
   // A window or sinks past the last key mean all keys; clamped, the kernels' sums fit int.
   const cudaError_t e =
-      launch_attn_window_fwd(q, k, v, o, lse, workspace,
-                             lse_part, B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
-                             sinks < Sk ? sinks : Sk, num_splits, scale,
-                             static_cast<cudaStream_t>(stream), status);
+      launch_attn_window_fwd(q, k, v, o, lse, workspace, B, Hq, Hkv, Sq, Sk, D,
+                             window < Sk ? window : Sk, sinks < Sk ? sinks : Sk, num_splits,
+                             scale, static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -275,30 +284,54 @@ int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, in
   if (num_splits == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0 ||
       Hq % Hkv != 0 || window < 1 || sinks < 0)
     return ATTN_ERR_INVALID_ARG;
-  const long long n_sm = sm_count(), items = window_items(B, Hq, Hkv, Sq, D);
-  // Key tiles of an item at most: its rows' windows and the sinks, or all there are.
-  const long long all = (static_cast<long long>(Sk) + 127) / 128;
-  const long long seen = (static_cast<long long>(window) + 126) / 128 + 1 +
-                         (static_cast<long long>(sinks) + 127) / 128;
-  const long long tiles = seen < all ? seen : all;
-  // Estimated time of a count that still runs in one round, in ns: 1400 for a step of
-  // an item, 3500 around it, and for the merge 3500 and the partials' way to L2 and
-  // back at 5 bytes a ps.  Measured (us) against it, D = 128, 32/8 heads: Sq 512, 34
-  // tiles: 1 split 51.9 (est. 52), 2 37.2 (38); Sq 512, 10 tiles: 1 20.0 (17), 2 21.1
-  // (20); Sq 128, 34 tiles: 4 22.8 (23), 8 19.4 (20), 16 26.4 (more than one round).
+  *num_splits = 1;
+  if (Sq > kMaxSeq || Sk > kMaxSeq || static_cast<long long>(B) * Hq > (1ll << 30) ||
+      !window_splits_fit(B, Hq, Hkv, Sq, D, 32))
+    return ATTN_OK;
+  const long long n_sm = sm_count();
+  window = window < Sk ? window : Sk;
+  sinks = sinks < Sk ? sinks : Sk;
+  const WindowOrder order = window_order(B, Hq, Hkv, Sq, Sk, D, window, 2);
+  if (order.rem == 0) return ATTN_OK;
+  // Key tiles of the last round's longest item, its first.
+  const int tile_rows = D == 256 || window_head_pairs(Hq, Hkv) ? 128 : 256;
+  const int row0 = order.item(order.unsplit).tile * tile_rows;
+  const TileRange r0 = window_kv_tiles(Sq, Sk, window, sinks, row0);
+  const TileRange r1 = window_kv_tiles(Sq, Sk, window, sinks, row0 + tile_rows - 128);
+  const long long tiles = r0.count() > r1.count() ? r0.count() : r1.count();
+  // Estimated time of the last round, in ns: 1400 for a step of an item, 3500 around it,
+  // and for the merge 3500 and the partials' way to L2 and back at 5 bytes a ps.
+  // Measured (us, all of one round) against it, D = 128, 32/8 heads: Sq 512, 34 tiles:
+  // 1 split 51.9 (est. 52), 2 37.2 (38); Sq 512, 10 tiles: 1 20.0 (17), 2 21.1 (20);
+  // Sq 128, 34 tiles: 4 22.8 (23), 8 19.4 (20), 16 26.4 (more than one round).
   // D = 256, where an item is one tile of a head, measured alike: 16/4 heads, Sq 512, 34
   // tiles: 1 56.0, 2 36.9, 3 50.0; Sq 128: 7 20.6, 8 22.3; 32 items of 4 tiles: 1 12.3,
   // 2 13.6; 24 items of 34: 6 22.1, 7 30.7.
-  const long long partial_ns = 2ll * B * Hq * Sq * D * 4 / 5000;  // of one split
-  long long best = 1, best_ns = tiles * 1400 + 3500;
-  for (long long ns = 2; ns <= tiles && ns <= 32 && ns * items <= n_sm; ++ns) {
+  const long long rows = 1ll * order.rem * window_item_rows(D), all = 1ll * B * Hq * Sq;
+  const long long partial_ns = 2 * (rows < all ? rows : all) * D * 4 / 5000;  // of one split
+  long long best_ns = tiles * 1400 + 3500;
+  for (long long ns = 2; ns <= tiles && ns <= 32 && ns * order.rem <= n_sm; ++ns) {
     const long long t = (tiles + ns - 1) / ns * 1400 + 7000 + ns * partial_ns;
     if (t < best_ns) {
-      best = ns;
+      *num_splits = static_cast<int>(ns);
       best_ns = t;
     }
   }
-  *num_splits = static_cast<int>(best);
+  return ATTN_OK;
+}
+
+int attn_window_fwd_workspace(int B, int Hq, int Hkv, int Sq, int D, int num_splits,
+                              long long* floats) {
+  if (floats == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || D <= 0 || num_splits < 1 ||
+      Hq % Hkv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
+  if (Sq > kMaxSeq || static_cast<long long>(B) * Hq > (1ll << 30) ||
+      (num_splits > 1 && !window_splits_fit(B, Hq, Hkv, Sq, D, num_splits)))
+    return ATTN_ERR_UNSUPPORTED;
+  *floats = num_splits == 1 ? 0
+                            : window_split_items(B, Hq, Hkv, Sq, D) * num_splits *
+                                  window_item_rows(D) * (D + 1);
   return ATTN_OK;
 }
 

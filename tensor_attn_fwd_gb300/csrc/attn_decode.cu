@@ -674,20 +674,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 // max and sum are warp reductions, and the O loads of all splits of a chunk are
 // independent (lane-parallel over D, unrolled over splits).
 // TO: fp32, or bf16 (rounded once).
-template <int D, typename TO = float>
+// Rows: the row of o and lse that a row of the partials is (-1: none).
+struct SameRow {
+  __device__ __forceinline__ int operator()(int row) const { return row; }
+};
+template <int D, typename TO = float, typename Rows = SameRow>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ o_part,
                                                       const float* __restrict__ lse_part,
                                                       TO* __restrict__ o,
                                                       float* __restrict__ lse, int rows,
-                                                      int num_splits) {
+                                                      int num_splits, const Rows rows_of) {
   constexpr int DPL = D / 32;
   constexpr float kLog2e = 1.4426950408889634f;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  const int to = row < rows ? rows_of(row) : -1;
   // Launched as a dependent of the split kernel: its partials are complete
   // and visible once this returns.
   grid_dependency_wait();
-  if (row >= rows) return;
+  if (to < 0) return;
   float M = -INFINITY;
   for (int s = lane; s < num_splits; s += 32)
     M = fmaxf(M, __ldg(lse_part + static_cast<size_t>(s) * rows + row));
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     for (int e = 0; e < DPL; ++e) out[e] *= inv;
     L = M + logf(W);
   }
-  TO* dst = o + static_cast<size_t>(row) * D + lane * DPL;
+  TO* dst = o + static_cast<size_t>(to) * D + lane * DPL;
   if constexpr (std::is_same_v<TO, __nv_bfloat16>) {
 #pragma unroll
     for (int e = 0; e < DPL; e += 2)
@@ -746,7 +751,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   } else {
     *reinterpret_cast<float2*>(dst) = make_float2(out[0], out[1]);
   }
-  if (lane == 0) lse[row] = L;
+  if (lane == 0) lse[to] = L;
 }
 
 template <int D, bool WIN>
@@ -832,22 +837,26 @@ cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o,
   cfg.numAttrs = 1;
   cudaError_t e;
   if (D == 256)
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<256>, o_part, lse_part, o, lse, rows, num_splits);
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<256>, o_part, lse_part, o, lse, rows, num_splits,
+                           SameRow{});
   else if (D == 128)
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<128>, o_part, lse_part, o, lse, rows, num_splits);
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<128>, o_part, lse_part, o, lse, rows, num_splits,
+                           SameRow{});
   else
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<64>, o_part, lse_part, o, lse, rows, num_splits);
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<64>, o_part, lse_part, o, lse, rows, num_splits,
+                           SameRow{});
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
-cudaError_t launch_combine_bf16(const float* o_part, const float* lse_part, void* o, float* lse,
-                                int rows, int D, int num_splits, cudaStream_t stream) {
-  auto kernel = D == 256   ? combine_kernel<256, __nv_bfloat16>
-                : D == 128 ? combine_kernel<128, __nv_bfloat16>
-                           : combine_kernel<64, __nv_bfloat16>;
+cudaError_t launch_combine_window(const float* o_part, const float* lse_part, void* o, float* lse,
+                                  int rows, const WindowRows& rows_of, int D, int num_splits,
+                                  cudaStream_t stream) {
+  auto kernel = D == 256   ? combine_kernel<256, __nv_bfloat16, WindowRows>
+                : D == 128 ? combine_kernel<128, __nv_bfloat16, WindowRows>
+                           : combine_kernel<64, __nv_bfloat16, WindowRows>;
   return launch_programmatic(kernel, dim3((rows + 7) / 8), dim3(256), 0, stream, o_part, lse_part,
-                             static_cast<__nv_bfloat16*>(o), lse, rows, num_splits);
+                             static_cast<__nv_bfloat16*>(o), lse, rows, num_splits, rows_of);
 }
 
 }  // namespace attn

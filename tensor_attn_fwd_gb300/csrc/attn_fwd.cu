@@ -116,6 +116,9 @@ struct FwdParams {
   int total_items;   // B * Hq * num_pairs * num_splits (B * Hq / 2 * num_splits in pairs)
   int window, sinks;  // windowed kernels: row at position p sees (p - window, p] and [0, sinks)
   WindowOrder order;  // windowed kernels: the items
+  float *part_o, *part_lse;  // ... and the fp32 partials of those that are split (WindowRows)
+  int part_v8;
+  size_t part_o_bytes, part_lse_bytes;
 };
 
 // A work item is two 128-row query tiles that stream the same K/V: rows
@@ -125,6 +128,7 @@ struct FwdParams {
 struct Item {
   int bh;      // b * Hq + h of query tile 0; tile 1's is bh + head_pairs
   int bg;      // windowed: b * Hkv + KV head
+  int slot;    // windowed: of a split item (WindowItem)
   int q_row0;  // first query row of tile 0; tile 1's is q_row0 + 128 (0 in head pairs)
   int split;   // KV split
   int j0;      // first KV tile of the split
@@ -152,14 +156,15 @@ __device__ __forceinline__ Item get_window_item(const FwdParams& p, int idx) {
   const WindowItem w = p.order.item(idx);
   Item it;
   it.split = w.split;
+  it.slot = w.slot;
   it.bg = w.bg;
   it.bh = (w.bg * p.order.per_group + w.member) << p.head_pairs;
   it.q_row0 = w.tile * (p.head_pairs ? 128 : kRowsPerItem);
   it.r[0] = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0);
   it.r[1] = p.head_pairs ? it.r[0]
                          : window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.q_row0 + 128);
-  it.r[0] = p.order.steps_of(it.r[0], w.split);
-  it.r[1] = p.order.steps_of(it.r[1], w.split);
+  it.r[0] = p.order.steps_of(it.r[0], w);
+  it.r[1] = p.order.steps_of(it.r[1], w);
   it.n[0] = it.r[0].e;
   it.n[1] = it.r[1].e;
   it.u = tile_union(it.r[0], it.r[1]);
@@ -542,20 +547,32 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
     const int bh = tile_bh(p, it, t);
     const int row = tile_row0(p, it, t) + quad * 32 + lane;
     const bool row_valid = row < p.Sq;
-    const size_t o_off = (static_cast<size_t>(bh) * p.Sq + row) * D +
-                         static_cast<size_t>(it.split) * p.split_stride_o;
-    float* o_row = static_cast<float*>(p.o) + o_off;
-    __nv_bfloat16* o_row16 = static_cast<__nv_bfloat16*>(p.o) + o_off;
-    float* lse_ptr = p.lse + static_cast<size_t>(bh) * p.Sq + row +
-                     static_cast<size_t>(it.split) * p.split_stride_lse;
+    // Windowed: a whole item's rows of O, or a split one's partials.
+    const bool part = WIN && it.slot >= 0;
+    const int o_bf16 = WIN ? !part : p.o_bf16;
+    void* const o_base = part ? p.part_o : p.o;
+    float* const lse_base = part ? p.part_lse : p.lse;
+    const size_t o_bytes = part ? p.part_o_bytes : p.o_bytes;
+    const size_t lse_bytes = part ? p.part_lse_bytes : p.lse_bytes;
+    const int o_v8 = part ? p.part_v8 : p.o_v8;
+    size_t at = static_cast<size_t>(bh) * p.Sq + row;
+    if (part)
+      at = (static_cast<size_t>(it.split) * p.order.rem + it.slot) * kRowsPerItem + 128 * t +
+           quad * 32 + lane;
+    const size_t o_off =
+        WIN ? at * D : at * D + static_cast<size_t>(it.split) * p.split_stride_o;
+    float* o_row = static_cast<float*>(o_base) + o_off;
+    __nv_bfloat16* o_row16 = static_cast<__nv_bfloat16*>(o_base) + o_off;
+    float* lse_ptr =
+        lse_base + at + (WIN ? 0 : static_cast<size_t>(it.split) * p.split_stride_lse);
     if (nt <= j_first) {
       // No key of the split visible to any row of this tile (or the tile is
       // past Sq): O = 0, LSE = -inf (a split a combine weighs with 0).
       if (row_valid &&
-          store_in_bounds(p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
-                          D * (p.o_bf16 ? 2 : 4), p.o, p.o_bytes, p.status) &&
-          store_in_bounds(lse_ptr, 4, p.lse, p.lse_bytes, p.status)) {
-        if (p.o_bf16) {
+          store_in_bounds(o_bf16 ? static_cast<const void*>(o_row16) : o_row,
+                          D * (o_bf16 ? 2 : 4), o_base, o_bytes, p.status) &&
+          store_in_bounds(lse_ptr, 4, lse_base, lse_bytes, p.status)) {
+        if (o_bf16) {
 #pragma unroll 4
           for (int c = 0; c < D; c += 8)
             *reinterpret_cast<uint4*>(o_row16 + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -716,7 +733,7 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
     // 32, halving the L1 wavefronts that the per-row layout of TMEM costs.
     const int pb = lane & 1;
     const bool even_valid = row - pb < p.Sq, odd_valid = row - pb + 1 < p.Sq;
-    if (p.o_bf16) {
+    if (o_bf16) {
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t w[16];
@@ -731,10 +748,10 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
         pair_transpose8(w, lane);
         __nv_bfloat16* e16 = o_row16 + (0 - pb) * D + c + 16 * pb;
         __nv_bfloat16* d16 = o_row16 + (1 - pb) * D + c + 16 * pb;
-        if (even_valid && store_in_bounds(e16, 32, p.o, p.o_bytes, p.status))
-          st_global_8w_hint(e16, &w[0], p.o_v8, pol_o);
-        if (odd_valid && store_in_bounds(d16, 32, p.o, p.o_bytes, p.status))
-          st_global_8w_hint(d16, &w[8], p.o_v8, pol_o);
+        if (even_valid && store_in_bounds(e16, 32, o_base, o_bytes, p.status))
+          st_global_8w_hint(e16, &w[0], o_v8, pol_o);
+        if (odd_valid && store_in_bounds(d16, 32, o_base, o_bytes, p.status))
+          st_global_8w_hint(d16, &w[8], o_v8, pol_o);
       }
     } else {
 #pragma unroll 1
@@ -748,14 +765,14 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
         for (int m = 0; m < 2; ++m) {
           float* e32 = o_row + (0 - pb) * D + c + 8 * (2 * m + pb);
           float* d32 = o_row + (1 - pb) * D + c + 8 * (2 * m + pb);
-          if (even_valid && store_in_bounds(e32, 32, p.o, p.o_bytes, p.status))
-            st_global_8w_hint(e32, &w[16 * m], p.o_v8, pol_o);
-          if (odd_valid && store_in_bounds(d32, 32, p.o, p.o_bytes, p.status))
-            st_global_8w_hint(d32, &w[16 * m + 8], p.o_v8, pol_o);
+          if (even_valid && store_in_bounds(e32, 32, o_base, o_bytes, p.status))
+            st_global_8w_hint(e32, &w[16 * m], o_v8, pol_o);
+          if (odd_valid && store_in_bounds(d32, 32, o_base, o_bytes, p.status))
+            st_global_8w_hint(d32, &w[16 * m + 8], o_v8, pol_o);
         }
       }
     }
-    if (row_valid && store_in_bounds(lse_ptr, 4, p.lse, p.lse_bytes, p.status))
+    if (row_valid && store_in_bounds(lse_ptr, 4, lse_base, lse_bytes, p.status))
       *lse_ptr = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
   if (!ok) record_status(p.status, ATTN_ERR_TIMEOUT);
@@ -885,8 +902,9 @@ cudaError_t launch_fwd_impl(const void* q, const void* k, const void* v, void* o
 // O would hold no more), or with several splits their fp32 partials.
 template <int D>
 cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void* o, float* lse,
-                               int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks,
-                               int num_splits, float scale, cudaStream_t stream, int* status) {
+                               float* part, const WindowOrder& order, int B, int Hq, int Hkv,
+                               int Sq, int Sk, int window, int sinks, float scale,
+                               cudaStream_t stream, int* status) {
   using C = Cfg<D>;
   CUtensorMap tmQ, tmK, tmV;
   if (!encode_bf16_map(&tmQ, q, D, Sq, B * Hq, 128) || !encode_bf16_map(&tmK, k, D, Sk, B * Hkv, 128) ||
@@ -899,12 +917,10 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   if (e != cudaSuccess) return e;
   FwdParams p = {};
   p.o = o;
-  p.o_bf16 = num_splits == 1;
+  p.o_bf16 = 1;
   p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  p.split_stride_lse = static_cast<size_t>(B) * Hq * Sq;
-  p.split_stride_o = p.split_stride_lse * D;
-  p.o_bytes = num_splits * p.split_stride_o * (p.o_bf16 ? 2 : 4);
-  p.lse_bytes = num_splits * p.split_stride_lse * sizeof(float);
+  p.lse_bytes = static_cast<size_t>(B) * Hq * Sq * sizeof(float);
+  p.o_bytes = static_cast<size_t>(B) * Hq * Sq * D * 2;
   p.lse = lse;
   p.status = status;
   p.B = B;
@@ -915,13 +931,17 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   p.causal = 1;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.head_pairs = window_head_pairs(Hq, Hkv);
-  const int rows = p.head_pairs ? 128 : kRowsPerItem;
-  p.num_pairs = (Sq + rows - 1) / rows;
-  p.num_splits = num_splits;
+  p.num_splits = order.num_splits;
   p.window = window;
   p.sinks = sinks;
-  p.order = WindowOrder::make(Sq, Sk, window, rows, B * Hkv, (Hq / Hkv) >> p.head_pairs, num_splits);
-  p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, D) * num_splits);
+  p.order = order;
+  const size_t part_rows = static_cast<size_t>(order.num_splits) * order.rem * kRowsPerItem;
+  p.part_o = part;
+  p.part_lse = part + part_rows * D;
+  p.part_v8 = (reinterpret_cast<uintptr_t>(part) & 31u) == 0;
+  p.part_o_bytes = part_rows * D * sizeof(float);
+  p.part_lse_bytes = part_rows * sizeof(float);
+  p.total_items = order.total();
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,
                              tmK, tmV, p);
@@ -929,22 +949,30 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
 
 }  // namespace
 
+WindowOrder window_order(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                         int num_splits) {
+  const int pairs = D != 256 && window_head_pairs(Hq, Hkv);
+  const int rows = D == 256 || pairs ? 128 : kRowsPerItem;
+  return WindowOrder::make(Sq, Sk, window, rows, B * Hkv, (Hq / Hkv) >> pairs, num_splits,
+                           sm_count());
+}
+
 cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, void* o,
-                                   float* lse, float* o_part, float* lse_part, int B, int Hq,
-                                   int Hkv, int Sq, int Sk, int D, int window, int sinks,
-                                   int num_splits, float scale, cudaStream_t stream,
-                                   int* status) {
-  void* o_to = num_splits > 1 ? o_part : o;
-  float* lse_to = num_splits > 1 ? lse_part : lse;
-  const cudaError_t e =
-      D == 256 ? launch_attn_window_fwd_d256(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window,
-                                             sinks, num_splits, scale, stream, status)
-      : D == 128 ? launch_window_impl<128>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
-                                         num_splits, scale, stream, status)
-               : launch_window_impl<64>(q, k, v, o_to, lse_to, B, Hq, Hkv, Sq, Sk, window, sinks,
-                                        num_splits, scale, stream, status);
-  if (e != cudaSuccess || num_splits == 1) return e;
-  return launch_combine_bf16(o_part, lse_part, o, lse, B * Hq * Sq, D, num_splits, stream);
+                                   float* lse, float* workspace, int B, int Hq, int Hkv, int Sq,
+                                   int Sk, int D, int window, int sinks, int num_splits,
+                                   float scale, cudaStream_t stream, int* status) {
+  const WindowOrder order = window_order(B, Hq, Hkv, Sq, Sk, D, window, num_splits);
+  const auto launch = D == 256   ? launch_attn_window_fwd_d256
+                      : D == 128 ? launch_window_impl<128>
+                                 : launch_window_impl<64>;
+  const cudaError_t e = launch(q, k, v, o, lse, workspace, order, B, Hq, Hkv, Sq, Sk, window,
+                               sinks, scale, stream, status);
+  if (e != cudaSuccess || order.num_splits == 1) return e;
+  const WindowRows rows{order, Sq, D != 256 && window_head_pairs(Hq, Hkv),
+                        window_item_rows(D)};
+  const int n = order.rem * rows.item_rows;
+  return launch_combine_window(workspace, workspace + static_cast<size_t>(order.num_splits) * n * D,
+                               o, lse, n, rows, D, order.num_splits, stream);
 }
 
 cudaError_t launch_attn_fwd(const void* q, const void* k, const void* v, void* o, int o_bf16,

@@ -97,11 +97,13 @@ struct Params256 {
   int num_tiles;    // ceil(Sq / 128)
   int total_items;  // B * Hq * num_tiles
   int kv_chunk;     // ORDER 2: KV heads per chunk
-  // Windowed: the mask, and the splits of an item (fp32 partials, split s at
-  // o + s * split_stride_o and lse + s * split_stride_lse).
+  // Windowed: the mask, the items, and the fp32 partials of those that are split
+  // (WindowRows).
   int window, sinks;
   WindowOrder order;
-  size_t split_stride_o, split_stride_lse;
+  float *part_o, *part_lse;
+  int part_v8;
+  size_t part_o_bytes, part_lse_bytes;
 };
 
 struct Item256 {
@@ -109,7 +111,7 @@ struct Item256 {
   int row0;  // first query row
   int n;     // KV tiles to visit (0: nothing visible)
   TileRange r;  // windowed: those tiles
-  int split, bg;  // windowed: key split; b * Hkv + KV head
+  int split, slot, bg;  // windowed: as WindowItem; b * Hkv + KV head
 };
 
 // The KV tile of an item's step j.
@@ -166,11 +168,12 @@ __device__ __forceinline__ Item256 item_at(const Params256& p, int idx) {
   if constexpr (WIN) {
     const WindowItem w = p.order.item(idx);
     it.split = w.split;
+    it.slot = w.slot;
     it.bg = w.bg;
     it.bh = w.bg * p.order.per_group + w.member;
     it.row0 = w.tile * 128;
     it.r = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, it.row0);
-    it.r = p.order.steps_of(it.r, w.split);
+    it.r = p.order.steps_of(it.r, w);
     it.n = it.r.count();
     return it;
   }
@@ -474,18 +477,26 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
     const Item256 it = item_at<ORDER, WIN>(p, idx);
     const int row = it.row0 + warp * 32 + lane;
     const bool row_valid = row < p.Sq;
-    const size_t o_off = (static_cast<size_t>(it.bh) * p.Sq + row) * kD +
-                         (WIN ? it.split * p.split_stride_o : 0);
-    float* o_row = static_cast<float*>(p.o) + o_off;
-    __nv_bfloat16* o_row16 = static_cast<__nv_bfloat16*>(p.o) + o_off;
-    float* lse_ptr = p.lse + static_cast<size_t>(it.bh) * p.Sq + row +
-                     (WIN ? it.split * p.split_stride_lse : 0);
+    // Windowed: a whole item's rows of O, or a split one's partials.
+    const bool part = WIN && it.slot >= 0;
+    const int o_bf16 = WIN ? !part : p.o_bf16;
+    void* const o_base = part ? p.part_o : p.o;
+    float* const lse_base = part ? p.part_lse : p.lse;
+    const size_t o_bytes = part ? p.part_o_bytes : p.o_bytes;
+    const size_t lse_bytes = part ? p.part_lse_bytes : p.lse_bytes;
+    const int o_v8 = part ? p.part_v8 : p.o_v8;
+    size_t at = static_cast<size_t>(it.bh) * p.Sq + row;
+    if (part)
+      at = (static_cast<size_t>(it.split) * p.order.rem + it.slot) * 128 + warp * 32 + lane;
+    float* o_row = static_cast<float*>(o_base) + at * kD;
+    __nv_bfloat16* o_row16 = static_cast<__nv_bfloat16*>(o_base) + at * kD;
+    float* lse_ptr = lse_base + at;
     if (it.n == 0) {
       if (row_valid &&
-          store_in_bounds(p.o_bf16 ? static_cast<const void*>(o_row16) : o_row,
-                          kD * (p.o_bf16 ? 2 : 4), p.o, p.o_bytes, p.status) &&
-          store_in_bounds(lse_ptr, 4, p.lse, p.lse_bytes, p.status)) {
-        if (p.o_bf16) {
+          store_in_bounds(o_bf16 ? static_cast<const void*>(o_row16) : o_row,
+                          kD * (o_bf16 ? 2 : 4), o_base, o_bytes, p.status) &&
+          store_in_bounds(lse_ptr, 4, lse_base, lse_bytes, p.status)) {
+        if (o_bf16) {
 #pragma unroll 4
           for (int c = 0; c < kD; c += 8)
             *reinterpret_cast<uint4*>(o_row16 + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -642,7 +653,7 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
     // contiguous bytes of a row (as in the D = 64/128 kernel's epilogue).
     const int pb = lane & 1;
     const bool even_valid = row - pb < p.Sq, odd_valid = row - pb + 1 < p.Sq;
-    if (p.o_bf16) {
+    if (o_bf16) {
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         uint32_t w[16];
@@ -657,10 +668,10 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
         pair_transpose8(w, lane);
         __nv_bfloat16* e16 = o_row16 + (0 - pb) * kD + c + 16 * pb;
         __nv_bfloat16* d16 = o_row16 + (1 - pb) * kD + c + 16 * pb;
-        if (even_valid && store_in_bounds(e16, 32, p.o, p.o_bytes, p.status))
-          st_global_8w(e16, &w[0], p.o_v8);
-        if (odd_valid && store_in_bounds(d16, 32, p.o, p.o_bytes, p.status))
-          st_global_8w(d16, &w[8], p.o_v8);
+        if (even_valid && store_in_bounds(e16, 32, o_base, o_bytes, p.status))
+          st_global_8w(e16, &w[0], o_v8);
+        if (odd_valid && store_in_bounds(d16, 32, o_base, o_bytes, p.status))
+          st_global_8w(d16, &w[8], o_v8);
       }
     } else {
 #pragma unroll 1
@@ -674,17 +685,17 @@ __device__ void softmax_role256(const Params256& p, Bars256* bars, uint32_t tmem
         for (int m = 0; m < 2; ++m) {
           float* e32 = o_row + (0 - pb) * kD + c + 8 * (2 * m + pb);
           float* d32 = o_row + (1 - pb) * kD + c + 8 * (2 * m + pb);
-          if (even_valid && store_in_bounds(e32, 32, p.o, p.o_bytes, p.status))
-            st_global_8w(e32, &w[16 * m], p.o_v8);
-          if (odd_valid && store_in_bounds(d32, 32, p.o, p.o_bytes, p.status))
-            st_global_8w(d32, &w[16 * m + 8], p.o_v8);
+          if (even_valid && store_in_bounds(e32, 32, o_base, o_bytes, p.status))
+            st_global_8w(e32, &w[16 * m], o_v8);
+          if (odd_valid && store_in_bounds(d32, 32, o_base, o_bytes, p.status))
+            st_global_8w(d32, &w[16 * m + 8], o_v8);
         }
       }
     }
     // The TMEM loads of O have completed (tcgen05.wait::ld inside tmem_ld32)
     // before the next item's first product may overwrite O: that product
     // waits for P of the next step, which these threads write after this.
-    if (row_valid && store_in_bounds(lse_ptr, 4, p.lse, p.lse_bytes, p.status))
+    if (row_valid && store_in_bounds(lse_ptr, 4, lse_base, lse_bytes, p.status))
       *lse_ptr = l > 0.f ? (m + log2f(l)) * kLn2f : -INFINITY;
   }
   if (!ok) note_status(p.status, ATTN_ERR_TIMEOUT);
@@ -798,9 +809,9 @@ cudaError_t launch_attn_fwd_d256(const void* q, const void* k, const void* v, vo
 }
 
 cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void* v, void* o,
-                                        float* lse, int B, int Hq, int Hkv, int Sq, int Sk,
-                                        int window, int sinks, int num_splits, float scale,
-                                        cudaStream_t stream, int* status) {
+                                        float* lse, float* part, const WindowOrder& order, int B,
+                                        int Hq, int Hkv, int Sq, int Sk, int window, int sinks,
+                                        float scale, cudaStream_t stream, int* status) {
   CUtensorMap tmQ, tmK, tmV;
   if (!encode_bf16_map(&tmQ, q, kD, Sq, B * Hq, 128) ||
       !encode_bf16_map(&tmK, k, kD, Sk, B * Hkv, 128) ||
@@ -813,12 +824,10 @@ cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void
   if (e != cudaSuccess) return e;
   Params256 p = {};
   p.o = o;
-  p.o_bf16 = num_splits == 1;
+  p.o_bf16 = 1;
   p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  p.split_stride_lse = static_cast<size_t>(B) * Hq * Sq;
-  p.split_stride_o = p.split_stride_lse * kD;
-  p.o_bytes = num_splits * p.split_stride_o * (p.o_bf16 ? 2 : 4);
-  p.lse_bytes = num_splits * p.split_stride_lse * sizeof(float);
+  p.lse_bytes = static_cast<size_t>(B) * Hq * Sq * sizeof(float);
+  p.o_bytes = static_cast<size_t>(B) * Hq * Sq * kD * 2;
   p.lse = lse;
   p.status = status;
   p.B = B;
@@ -831,8 +840,14 @@ cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void
   p.num_tiles = (Sq + 127) / 128;
   p.window = window;
   p.sinks = sinks;
-  p.order = WindowOrder::make(Sq, Sk, window, 128, B * Hkv, Hq / Hkv, num_splits);
-  p.total_items = static_cast<int>(window_items(B, Hq, Hkv, Sq, kD) * num_splits);
+  p.order = order;
+  const size_t part_rows = static_cast<size_t>(order.num_splits) * order.rem * 128;
+  p.part_o = part;
+  p.part_lse = part + part_rows * kD;
+  p.part_v8 = (reinterpret_cast<uintptr_t>(part) & 31u) == 0;
+  p.part_o_bytes = part_rows * kD * sizeof(float);
+  p.part_lse_bytes = part_rows * sizeof(float);
+  p.total_items = order.total();
   const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads256), kSmem256, stream, tmQ, tmK,
                              tmV, p);

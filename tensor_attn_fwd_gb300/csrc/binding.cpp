@@ -244,9 +244,12 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else
       splits = integer(a[8], "num_splits", LLONG_MIN, INT_MAX);
     Tensor ws;
-    if (splits > 1)
-      ws = fresh({static_cast<int64_t>(splits) * s.B * s.Hq * s.Sq * (s.D + 1)}, at::kFloat,
-                 q.device());
+    if (splits > 1) {
+      long long need = 0;
+      raise_if(attn_window_fwd_workspace(s.B, s.Hq, s.Hkv, s.Sq, s.D, splits, &need),
+               "attn_window_fwd");
+      ws = fresh({need}, at::kFloat, q.device());
+    }
     raise_if(attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
                              ws.defined() ? floats(ws) : nullptr, s.B, s.Hq, s.Hkv, s.Sq, s.Sk,
                              s.D, window, sinks, splits, scale, current_stream(q.device())),

@@ -178,23 +178,26 @@ cudaError_t launch_decode_window(const void* q, const void* k, const void* v, co
 
 // Sliding-window prefill (bf16 O; D 64, 128 or 256) and backward (bf16 gradients; D 64 or
 // 128); window and sinks clamped as above.
-// num_splits > 1: fp32 partials in o_part [ns,B,Hq,Sq,D] and lse_part [ns,B,Hq,Sq],
-// then their combine into o.
+// With splits: fp32 partials of the last round's items in workspace, then their combine
+// into o and lse.
+struct WindowOrder;
+struct WindowRows;
 inline int window_head_pairs(int Hq, int Hkv) { return (Hq / Hkv) % 2 == 0; }
-inline long long window_items(long long B, int Hq, int Hkv, int Sq, int D) {  // per split
-  if (D == 256) return B * Hq * ((Sq + 127) / 128);  // one query tile a CTA
+inline int window_item_rows(int D) { return D == 256 ? 128 : 256; }  // two tiles, or one
+inline long long window_items(long long B, int Hq, int Hkv, int Sq, int D) {  // unsplit
+  if (D == 256) return B * Hq * ((Sq + 127) / 128);
   return window_head_pairs(Hq, Hkv) ? B * Hq / 2 * ((Sq + 127) / 128)
                                     : B * Hq * ((Sq + 255) / 256);
 }
+WindowOrder window_order(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int num_splits);
 cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void* v, void* o,
-                                        float* lse, int B, int Hq, int Hkv, int Sq, int Sk,
-                                        int window, int sinks, int num_splits, float scale,
-                                        cudaStream_t stream, int* status);
+                                        float* lse, float* part, const WindowOrder& order, int B,
+                                        int Hq, int Hkv, int Sq, int Sk, int window, int sinks,
+                                        float scale, cudaStream_t stream, int* status);
 cudaError_t launch_attn_window_fwd(const void* q, const void* k, const void* v, void* o,
-                                   float* lse, float* o_part, float* lse_part, int B, int Hq,
-                                   int Hkv, int Sq, int Sk, int D, int window, int sinks,
-                                   int num_splits, float scale, cudaStream_t stream,
-                                   int* status);
+                                   float* lse, float* workspace, int B, int Hq, int Hkv, int Sq,
+                                   int Sk, int D, int window, int sinks, int num_splits,
+                                   float scale, cudaStream_t stream, int* status);
 cudaError_t launch_attn_window_bwd(const void* q, const void* k, const void* v, const void* o,
                                    const float* lse, const void* dout, void* dq, void* dk,
                                    void* dv, float* delta, int B, int Hq, int Hkv, int Sq, int Sk,
@@ -235,9 +238,9 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const f
 
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int* status, uint64_t* waited_ns,
                                  cudaStream_t stream);
-// bf16 o.
-cudaError_t launch_combine_bf16(const float* o_part, const float* lse_part, void* o, float* lse,
-                                int rows, int D, int num_splits, cudaStream_t stream);
+cudaError_t launch_combine_window(const float* o_part, const float* lse_part, void* o, float* lse,
+                                  int rows, const WindowRows& rows_of, int D, int num_splits,
+                                  cudaStream_t stream);
 cudaError_t launch_combine(const float* o_part, const float* lse_part, float* o, float* lse,
                            int rows, int D, int num_splits, cudaStream_t stream);
 

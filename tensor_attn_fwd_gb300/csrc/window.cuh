@@ -21,9 +21,9 @@ struct FixedDiv {
     while ((1ull << shift) < d) ++shift;
     mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
   }
-  __device__ __forceinline__ int div(int n) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >>
-                            shift);
+  __host__ __device__ __forceinline__ int div(int n) const {
+    const uint32_t x = static_cast<uint32_t>(n);
+    return static_cast<int>((static_cast<uint32_t>((static_cast<uint64_t>(x) * mul) >> 32) + x) >> shift);
   }
 };
 
@@ -39,7 +39,7 @@ struct TileRange {
   __device__ __forceinline__ bool has(int j) const {
     return (j >= b && j < s) || (j >= w && j < e);
   }
-  __device__ __forceinline__ int count() const { return s - b + e - w; }
+  __host__ __device__ __forceinline__ int count() const { return s - b + e - w; }
   __device__ __forceinline__ int tile(int step) const {
     return step < s - b ? b + step : step - (s - b) + w;
   }
@@ -53,7 +53,7 @@ struct TileRange {
   }
 };
 
-__device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window, int sinks,
+__host__ __device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window, int sinks,
                                                      int row_first) {
   TileRange r = {0, 0, 0, 0};
   const int row_last = min(row_first + 127, Sq - 1);
@@ -75,37 +75,51 @@ __device__ __forceinline__ TileRange window_kv_tiles(int Sq, int Sk, int window,
 //
 // Every role of a CTA works an item out for itself, between two items, so the divisions
 // are multiplications (as divisions they cost 0.7 us an item).
+//
+// With splits, the last round of items, which does not fill the CTAs, is cut along the
+// keys into num_splits parts each, so that it takes a part of the time: the first
+// `unsplit` items are left whole, a multiple of the CTAs, and the `rem` others are
+// counted split by split (slot: their number).
 struct WindowItem {
-  int split, bg, member, tile;
+  int split, slot;  // slot -1: whole
+  int bg, member, tile;
 };
 struct WindowOrder {
-  int tiles, n_bg, per_group, num_splits, per_split, ramp;
-  FixedDiv by_split, by_group, by_whole, by_bg, by_num_splits;
+  int tiles, n_bg, per_group, num_splits, unsplit, rem, ramp;
+  FixedDiv by_rem, by_group, by_whole, by_bg, by_num_splits;
 
-  // rows: query rows of a tile.
+  // rows: query rows of a tile; ctas: that run at once.
   static WindowOrder make(int Sq, int Sk, int window, int rows, int n_bg, int per_group,
-                          int num_splits) {
+                          int num_splits, int ctas) {
     WindowOrder o;
     o.tiles = (Sq + rows - 1) / rows;
     o.n_bg = n_bg;
     o.per_group = per_group;
-    o.num_splits = num_splits;
-    o.per_split = n_bg * per_group * o.tiles;
+    const int items = n_bg * per_group * o.tiles;
+    o.unsplit = num_splits == 1 ? items : items / ctas * ctas;
+    o.rem = items - o.unsplit;
+    o.num_splits = o.rem == 0 ? 1 : num_splits;
     // Tiles that hold a row with less than its window before it.
     const long long short_rows = static_cast<long long>(window) - 1 - (Sk - Sq);
     const long long n = short_rows <= 0 ? 0 : (short_rows + rows - 1) / rows;
     o.ramp = n < o.tiles ? static_cast<int>(n) : o.tiles;
-    o.by_split = FixedDiv(o.per_split);
+    o.by_rem = FixedDiv(o.rem > 0 ? o.rem : 1);
     o.by_group = FixedDiv(per_group);
     o.by_whole = FixedDiv(o.tiles > o.ramp ? o.tiles - o.ramp : 1);
     o.by_bg = FixedDiv(n_bg);
-    o.by_num_splits = FixedDiv(num_splits);
+    o.by_num_splits = FixedDiv(o.num_splits);
     return o;
   }
-  __device__ __forceinline__ WindowItem item(int idx) const {
+  int total() const { return unsplit + rem * num_splits; }
+  __host__ __device__ __forceinline__ WindowItem item(int idx) const {
     WindowItem x;
-    x.split = by_split.div(idx);
-    idx -= x.split * per_split;
+    x.split = 0;
+    x.slot = -1;
+    if (idx >= unsplit) {
+      x.split = by_rem.div(idx - unsplit);
+      x.slot = idx - unsplit - x.split * rem;
+      idx = unsplit + x.slot;
+    }
     const int rest = by_group.div(idx);
     x.member = idx - rest * per_group;
     const int whole = tiles - ramp;
@@ -119,11 +133,26 @@ struct WindowOrder {
     }
     return x;
   }
-  // The steps of split `split` of a tile's list: its split-th equal run.
-  __device__ __forceinline__ TileRange steps_of(const TileRange& r, int split) const {
-    if (num_splits == 1) return r;
+  // An item's part of a tile's list: its split-th equal run of steps.
+  __device__ __forceinline__ TileRange steps_of(const TileRange& r, const WindowItem& x) const {
+    if (x.slot < 0) return r;
     const int chunk = by_num_splits.div(r.count() + num_splits - 1);
-    return r.steps(split * chunk, split * chunk + chunk);
+    return r.steps(x.split * chunk, x.split * chunk + chunk);
+  }
+};
+
+// Where the rows of split items go: partials in [split][slot][item_rows], and the row
+// of O (b * Hq + h) * Sq + i, or -1, that row `row` of a split's [slot][item_rows] is.
+// An item of 256 rows is a tile of two heads (head_pairs), or two tiles of one.
+struct WindowRows {
+  WindowOrder order;
+  int Sq, head_pairs, item_rows;
+  __device__ __forceinline__ int operator()(int row) const {
+    const int slot = item_rows == 256 ? row >> 8 : row >> 7, r = row - slot * item_rows;
+    const WindowItem x = order.item(order.unsplit + slot);
+    const int head = ((x.bg * order.per_group + x.member) << head_pairs) + (head_pairs ? r >> 7 : 0);
+    const int i = head_pairs ? x.tile * 128 + (r & 127) : x.tile * item_rows + r;
+    return i < Sq ? head * Sq + i : -1;
   }
 };
 

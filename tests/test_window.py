@@ -489,6 +489,38 @@ def test_heads_of_many_rounds_match_a_call_of_their_own(shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 80, 40, 600, 900, 64, 200, 5), (2, 45, 45, 500, 500, 128, 130, 0),
+                                   (1, 90, 30, 250, 700, 256, 300, 140), (1, 88, 44, 500, 500, 128, 700, 0)])
+@pytest.mark.parametrize("splits", [2, 3, None])
+def test_splits_of_the_last_round(shape, splits):
+    # More items than SMs: those of the last round are cut, the others are not.
+    B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    q, k, v = inputs(B, Hq, Hkv, Sq, Sk, D, 9)
+    k, v = k.clone(), v.clone()
+    unseen = ~visible(Sq, Sk, window, sinks).any(0)
+    heads = [0, 1, Hkv // 2, Hkv - 1]
+    G = Hq // Hkv
+    of = [h * G + g for h in heads for g in range(G)]
+    want, tol = reference(q[:, of], k[:, heads], v[:, heads], window, sinks, 1.0 / math.sqrt(D))
+    k[:, :, unseen.cuda()] = float("nan")
+    v[:, :, unseen.cuda()] = float("nan")
+    whole, whole_lse = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=1)
+    o, lse = attn.attn_window_fwd(q, k, v, window, sinks, num_splits=splits)
+    assert attn.attn_debug_status() == attn.ATTN_OK
+    check("o", o[:, of], want["o"], tol["o"])
+    check("lse", lse[:, of], want["lse"], tol["lse"])
+    assert bool(torch.isfinite(o).all())
+    # The rest agree with one split: two results of that bound, and whole rounds alike.
+    n_sm = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 256 if D < 256 and G % 2 else 128
+    tiles = -(-Sq // rows)
+    items = B * Hkv * tiles * (G // 2 if rows == 128 and D < 256 else G)
+    differ = (lse != whole_lse).sum().item()
+    assert differ <= items % n_sm * (128 if D == 256 else 256)
+    assert (o.float() - whole.float()).abs().max().item() <= 2 * tol["o"].max().item()
+
+
+@pytest.mark.gpu
 def test_threads_on_streams_of_their_own():
     shapes = [(1, 4, 2, 300, 300, 64, 70, 4), (1, 2, 2, 40, 2000, 128, 900, 3),
               (2, 6, 2, 500, 500, 64, 33, 130), (1, 8, 1, 700, 700, 128, 128, 0)]
@@ -549,14 +581,16 @@ def test_debug_build_stores_in_bounds_and_matches(shape):
     # Every output store checked against its buffer (a stray one is skipped and reported).
     from tensor_attn_fwd_gb300 import build as attn_build
     dbg = ctypes.CDLL(attn_build.build(debug=True))
-    for name in ("attn_window_fwd", "attn_window_bwd", "attn_decode_window", "attn_debug_status"):
+    for name in ("attn_window_fwd", "attn_window_fwd_workspace", "attn_window_bwd", "attn_decode_window",
+                 "attn_debug_status"):
         fn, like = getattr(dbg, name), getattr(attn.load_library(), name)
         fn.argtypes, fn.restype = like.argtypes, like.restype
     B, Hq, Hkv, Sq, Sk, D, window, sinks = shape
     q, k, v, do = inputs(B, Hq, Hkv, Sq, Sk, D, 21, grad=True)
     scale, stream = 1.0 / math.sqrt(D), torch.cuda.current_stream().cuda_stream
-    floats = 4 * B * Hq * Sq * (D + 1)
     n = ctypes.c_longlong(0)
+    assert dbg.attn_window_fwd_workspace(B, Hq, Hkv, Sq, D, 2, ctypes.byref(n)) == attn.ATTN_OK
+    floats = n.value
     if D < 256:
         attn.load_library().attn_window_bwd_workspace(*shape, ctypes.byref(n))
     ws = torch.empty(max(floats, n.value), device="cuda")
@@ -643,7 +677,21 @@ def test_forward_split_rule():
     rule = _lib().attn_window_fwd_num_splits
     assert rule(1, 2, 1, 8, 8, 64, 4, 1, None) == attn.ATTN_ERR_INVALID_ARG
     assert rule(1, 2, 1, 8, 8, 64, 0, 1, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
-    assert rule(1, 2, 1, 8, 1 << 20, 64, 500, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 1
+    assert rule(1, 2, 1, 8, 1 << 20, 64, 500, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value >= 1
+    big = 2**31 - 1  # too large for attn_window_fwd: still a count
+    assert rule(big, big, 1, big, big, big, 5, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 1
+
+
+def test_forward_workspace():
+    n = ctypes.c_longlong(-1)
+    size = _lib().attn_window_fwd_workspace
+    assert size(1, 2, 1, 8, 64, 1, None) == attn.ATTN_ERR_INVALID_ARG
+    assert size(1, 2, 1, 8, 64, 0, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert size(1, 3, 2, 8, 64, 2, ctypes.byref(n)) == attn.ATTN_ERR_INVALID_ARG
+    assert size(1, 2, 1, 8, 96, 2, ctypes.byref(n)) == attn.ATTN_ERR_UNSUPPORTED
+    assert size(1, 4, 1, 1 << 30, 64, 2, ctypes.byref(n)) == attn.ATTN_ERR_UNSUPPORTED
+    assert size(1, 2, 1, 8, 64, 1, ctypes.byref(n)) == attn.ATTN_OK and n.value == 0
+    assert size(1, 2, 1, 8, 64, 3, ctypes.byref(n)) == attn.ATTN_OK and n.value >= 0
 
 
 def test_decode_split_rule():
