@@ -382,8 +382,9 @@ ATTN_API int attn_window_fwd(const void *q, const void *k, const void *v, void *
 ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
                                         int sinks, int *num_splits);
 
-/* Floats of workspace for attn_window_fwd with num_splits on the current device (0 with
- * one).  Host-only.  ATTN_ERR_INVALID_ARG and ATTN_ERR_UNSUPPORTED as attn_window_fwd. */
+/* Floats of workspace for attn_window_fwd with num_splits on the current device: 0 with
+ * one, or where every round is full (the pointer may not be NULL then either).
+ * Host-only.  ATTN_ERR_INVALID_ARG and ATTN_ERR_UNSUPPORTED as attn_window_fwd. */
 ATTN_API int attn_window_fwd_workspace(int B, int Hq, int Hkv, int Sq, int D, int num_splits,
                                        long long *floats);
 

@@ -285,6 +285,8 @@ int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, in
       Hq % Hkv != 0 || window < 1 || sinks < 0)
     return ATTN_ERR_INVALID_ARG;
   *num_splits = 1;
+  // (Up to three tiles, one split is always best by the estimate below.)
+  if (static_cast<long long>(window) + sinks <= 128 || Sk <= 384) return ATTN_OK;
   if (Sq > kMaxSeq || Sk > kMaxSeq || static_cast<long long>(B) * Hq > (1ll << 30) ||
       !window_splits_fit(B, Hq, Hkv, Sq, D, 32))
     return ATTN_OK;

@@ -942,8 +942,7 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   p.part_o_bytes = part_rows * D * sizeof(float);
   p.part_lse_bytes = part_rows * sizeof(float);
   p.total_items = order.total();
-  const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
-  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, tmQ,
+  return launch_programmatic(kernel, dim3(order.ctas), dim3(kThreads), C::kSmemBytes, stream, tmQ,
                              tmK, tmV, p);
 }
 

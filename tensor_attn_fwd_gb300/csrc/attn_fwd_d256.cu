@@ -848,8 +848,7 @@ cudaError_t launch_attn_window_fwd_d256(const void* q, const void* k, const void
   p.part_o_bytes = part_rows * kD * sizeof(float);
   p.part_lse_bytes = part_rows * sizeof(float);
   p.total_items = order.total();
-  const int grid = p.total_items < sm_count() ? p.total_items : sm_count();
-  return launch_programmatic(kernel, dim3(grid), dim3(kThreads256), kSmem256, stream, tmQ, tmK,
+  return launch_programmatic(kernel, dim3(order.ctas), dim3(kThreads256), kSmem256, stream, tmQ, tmK,
                              tmV, p);
 }
 

@@ -244,11 +244,11 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else
       splits = integer(a[8], "num_splits", LLONG_MIN, INT_MAX);
     Tensor ws;
-    if (splits > 1) {
+    if (splits > 1 && splits <= (static_cast<int64_t>(s.Sk) + 127) / 128) {  // (more are refused below)
       long long need = 0;
       raise_if(attn_window_fwd_workspace(s.B, s.Hq, s.Hkv, s.Sq, s.D, splits, &need),
                "attn_window_fwd");
-      ws = fresh({need}, at::kFloat, q.device());
+      ws = fresh({std::max(need, 1ll)}, at::kFloat, q.device());  // full rounds need none
     }
     raise_if(attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
                              ws.defined() ? floats(ws) : nullptr, s.B, s.Hq, s.Hkv, s.Sq, s.Sk,

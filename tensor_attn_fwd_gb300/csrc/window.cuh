@@ -17,8 +17,7 @@ namespace attn {
 struct FixedDiv {
   uint32_t mul, shift;
   FixedDiv() = default;
-  explicit FixedDiv(uint32_t d) : shift(0) {
-    while ((1ull << shift) < d) ++shift;
+  explicit FixedDiv(uint32_t d) : shift(d > 1 ? 32 - __builtin_clz(d - 1) : 0) {
     mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
   }
   __host__ __device__ __forceinline__ int div(int n) const {
@@ -85,7 +84,7 @@ struct WindowItem {
   int bg, member, tile;
 };
 struct WindowOrder {
-  int tiles, n_bg, per_group, num_splits, unsplit, rem, ramp;
+  int tiles, n_bg, per_group, num_splits, unsplit, rem, ramp, ctas;
   FixedDiv by_rem, by_group, by_whole, by_bg, by_num_splits;
 
   // rows: query rows of a tile; ctas: that run at once.
@@ -99,6 +98,7 @@ struct WindowOrder {
     o.unsplit = num_splits == 1 ? items : items / ctas * ctas;
     o.rem = items - o.unsplit;
     o.num_splits = o.rem == 0 ? 1 : num_splits;
+    o.ctas = o.total() < ctas ? o.total() : ctas;  // of the launch
     // Tiles that hold a row with less than its window before it.
     const long long short_rows = static_cast<long long>(window) - 1 - (Sk - Sq);
     const long long n = short_rows <= 0 ? 0 : (short_rows + rows - 1) / rows;

@@ -490,7 +490,8 @@ def test_heads_of_many_rounds_match_a_call_of_their_own(shape):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(1, 80, 40, 600, 900, 64, 200, 5), (2, 45, 45, 500, 500, 128, 130, 0),
-                                   (1, 90, 30, 250, 700, 256, 300, 140), (1, 88, 44, 500, 500, 128, 700, 0)])
+                                   (1, 90, 30, 250, 700, 256, 300, 140), (1, 88, 44, 500, 500, 128, 700, 0),
+                                   (1, 152, 76, 200, 400, 64, 100, 3)])  # full rounds on 152 SMs
 @pytest.mark.parametrize("splits", [2, 3, None])
 def test_splits_of_the_last_round(shape, splits):
     # More items than SMs: those of the last round are cut, the others are not.
@@ -770,6 +771,9 @@ def test_python_rejects_shapes_types_and_reach():
     for bad in (dict(window=0), dict(window=-2), dict(window=4, sinks=-1)):
         with pytest.raises(ValueError):
             attn.attn_window_fwd(q, k, v, **bad)
+    for splits in (0, 2, 2**30):  # one key tile
+        with pytest.raises((ValueError, RuntimeError)):
+            attn.attn_window_fwd(q, k, v, 4, num_splits=splits)
     with pytest.raises(ValueError):
         attn.attn_window_fwd(q.float(), k, v, 4)
     with pytest.raises(ValueError):
