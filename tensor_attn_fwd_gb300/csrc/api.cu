@@ -572,6 +572,16 @@ int attn_decode_window_num_splits(int B, int Hq, int Hkv, int Sk, int D, int win
   } else {
     ns = n_sm / base;
   }
+  // CTAs a little past one or two rounds of resident ones (3, 2 or 1 an SM) and long
+  // walks: with splits the last round is as short as its CTAs.  D 128, 4100 keys: base
+  // 312: 1 split 122.3, 2 110.8, 3 105.5; 384: 128.5, 119.5, 124.9; 416: 130.2, 129.8;
+  // 640: 206.8, 197.2, 195.1; 2052 keys: base 312: 68.1, 64.9, 64.3; 1028 keys: 38.2,
+  // 39.9.  D 64, 4100 keys: base 480: 101.9, 89.9, 86.1.  D 256: base 160: 144, 130, 122.
+  const long long slots = n_sm * (D == 64 ? 3 : D == 128 ? 2 : 1);
+  const long long rounds = base / slots, extra = base % slots;
+  if ((rounds == 1 || rounds == 2) && extra > 0 && extra * 20 <= slots * 7 &&
+      blocks >= 64 * rounds)
+    ns = extra * 20 <= slots * 3 ? 3 : 2;
   // A split keeps two blocks (base 8, 260 keys: 1 split 6.8, 4 5.4, 8 5.6), and clusters
   // past 12 pay only for few and long walks (base 8, 1028 keys: 8 splits 6.7, 12 6.2, 16 7.8;
   // base 1, 16388 keys: 12 16.9, 16 15.0).
