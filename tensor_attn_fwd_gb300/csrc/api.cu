@@ -12,12 +12,13 @@
 #include <mutex>
 
 #include "internal.h"
+#include "kernel_attrs.h"
 #include "window.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = SharedMemoryLimits::kMaxDevices;
 
 // Written by kernels whose bounded wait expired (ATTN_ERR_TIMEOUT).
 __device__ int g_status_word = 0;
@@ -26,14 +27,7 @@ std::mutex g_mutex;
 int g_sm_count[kMaxDevices] = {0};
 int* g_status_ptr[kMaxDevices] = {nullptr};
 
-struct AttrEntry {
-  const void* kernel;
-  int bytes;
-  uint64_t device_mask;
-};
-constexpr int kAttrSlots = 64;  // one per kernel instantiation that sets its shared memory size
-AttrEntry g_attr[kAttrSlots];
-int g_attr_n = 0;
+SharedMemoryLimits g_smem_limits;
 
 int current_device() {
   int dev = 0;
@@ -78,23 +72,9 @@ cudaError_t ensure_smem_attr(const void* kernel, int bytes) {
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_mutex);
-  AttrEntry* e = nullptr;
-  for (int i = 0; i < g_attr_n; ++i)
-    if (g_attr[i].kernel == kernel) e = &g_attr[i];
-  if (e != nullptr && e->bytes >= bytes && (e->device_mask >> dev & 1u)) return cudaSuccess;
-  const cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err != cudaSuccess) return err;
-  if (e == nullptr) {
-    if (g_attr_n >= kAttrSlots) return cudaSuccess;  // table full: set again next time
-    e = &g_attr[g_attr_n++];
-    e->kernel = kernel;
-    e->bytes = bytes;
-    e->device_mask = 0;
-  }
-  e->bytes = bytes;
-  e->device_mask |= uint64_t(1) << dev;
-  return cudaSuccess;
+  return g_smem_limits.allow(kernel, dev, bytes, [](const void* f, int n) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  });
 }
 
 cudaError_t allow_large_cluster(const void* kernel) {
