@@ -463,8 +463,8 @@ ATTN_API int attn_decode_window_paged(const void *q, const void *k_cache, const 
  * (free pages are taken lowest id first).  An entry that is neither a page nor -1
  * sets ATTN_ERR_INVALID_ARG in the device status word (attn_debug_status) and
  * counts as -1.  Limits: rows * max_pages < 2^31, max_pages * page_size <= 2^30,
- * num_pages <= 2^30 (else ATTN_ERR_UNSUPPORTED).  Outputs may not overlap inputs
- * unless said otherwise.
+ * num_pages <= 2^30, at most 2^30 rows of a fork (else ATTN_ERR_UNSUPPORTED).  Outputs
+ * may not overlap inputs unless said otherwise.
  */
 
 /*

@@ -820,7 +820,9 @@ int attn_pages_fork(const int* block_table, const int* refs, const int* seqlens,
   const int chk = pages_check_args(block_table, refs, block_table_out, refs_out, B, max_pages,
                                    num_pages, page_size);
   if (chk != ATTN_OK) return chk;
-  if (static_cast<long long>(R) * max_pages > (1ll << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+  // (A row's number and the rows in flight at once are added as ints.)
+  if (static_cast<long long>(R) * max_pages > (1ll << 31) - 1 || R > kMaxSeq)
+    return ATTN_ERR_UNSUPPORTED;
   // The phases read their inputs after other CTAs have written outputs.
   if (block_table_out == block_table || refs_out == refs || seqlens_out == seqlens ||
       seqlens_out == parents || src == parents || dst == parents || src == dst)
