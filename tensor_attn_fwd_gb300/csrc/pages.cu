@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kCopyThreads)
   grid_launch_dependents();
   const int pair = blockIdx.y;
   const int from = __ldg(src + pair), to = __ldg(dst + pair);
-  if (from < 0 && to < 0) return;
+  if (from == -1 && to == -1) return;
   if (from < 0 || to < 0 || from >= num_pages || to >= num_pages) {
     if (threadIdx.x == 0) record_status(status, ATTN_ERR_INVALID_ARG);
     return;

@@ -15,3 +15,16 @@ def test_fork_refuses_more_rows_than_its_loops_count(R):
     # One slot a row: R * max_pages is below 2^31, but a row number past 2^30 plus the
     # threads of a grid is not.
     assert c_fork(R=R, M=1) == UNS
+
+
+# ------------------------------------------------------------------ inconsistent input
+@pytest.mark.gpu
+@pytest.mark.parametrize("pair", [(-2, -5), (-1, -3), (-2, -1), (-(2 ** 31), -1)])
+def test_copy_reports_every_pair_that_is_no_page(pair):
+    # Only -1, -1 is an unused place of the list.
+    k = torch.arange(32, device="cuda").to(torch.bfloat16).view(4, 8)
+    v = k + 1
+    kw, vw = k.clone(), v.clone()
+    attn.attn_pages_copy(k, v, *gpu([pair[0], -1], [pair[1], -1]))
+    assert attn.attn_debug_status() == attn.ATTN_ERR_INVALID_ARG
+    assert torch.equal(k, kw) and torch.equal(v, vw)
