@@ -505,6 +505,8 @@ ATTN_API int attn_pages_free(const int *block_table, const int *refs, const int 
  *   and a row whose keys they were ends before them (seqlens_out[r] a multiple of
  *   page_size).
  *   workspace: attn_pages_workspace(num_pages, R) int32, contents undefined
+ *   An entry whose page has refs <= 0 sets ATTN_ERR_INVALID_ARG in the status word and
+ *   counts as -1 (as for attn_pages_compact).
  *   A parent outside [-1, B) sets ATTN_ERR_INVALID_ARG in the status word and makes
  *   an empty row.  seqlens are clamped to [0, max_pages * page_size].
  */

@@ -215,7 +215,9 @@ long long window_bwd_workspace_floats(int B, int Hq, int Hkv, int Sq, int Sk, in
 // Page bookkeeping (pages.cu): P pages, a table of B rows x M slots.
 constexpr int kPagesMaxCtas = 512;
 // int32 workspace of launch_pages_fork (R new rows) and launch_pages_compact (R = 0).
-inline long long pages_workspace(int P, int R) { return 2ll * P + R + 2 * kPagesMaxCtas; }
+inline long long pages_workspace(int P, int R) {
+  return 2ll * P + R + 2 * kPagesMaxCtas + (P + 31ll) / 32;
+}
 cudaError_t launch_pages_free(const int* table, const int* refs, const int* seqlens,
                               int* table_out, int* refs_out, int B, int M, int P, int page_size,
                               int window, int sinks, int room, cudaStream_t stream, int* status);

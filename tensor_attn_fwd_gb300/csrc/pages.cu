@@ -60,8 +60,9 @@ __device__ __forceinline__ void record_status(int* status, int code) {
 // This CTA's part [begin, end) of n things shared out over the grid.
 struct Part {
   int begin, end;
-  __device__ __forceinline__ explicit Part(int n) {
-    const int chunk = (n + gridDim.x - 1) / gridDim.x;
+  // The parts begin at multiples of `align` (a power of two).
+  __device__ __forceinline__ explicit Part(int n, int align = 1) {
+    const int chunk = ((n + gridDim.x - 1) / gridDim.x + align - 1) & ~(align - 1);
     begin = static_cast<int>(min(static_cast<long long>(blockIdx.x) * chunk, static_cast<long long>(n)));
     end = min(begin + chunk, n);
   }
@@ -224,9 +225,21 @@ struct ForkOp {
   const int *table, *refs, *seqlens, *parents;
   int *table_out, *refs_out, *seqlens_out, *src, *dst, *counts;
   int *lowest, *free_list, *need, *cta_free, *cta_need;  // workspace
+  unsigned* live;  // workspace: bit p of word p / 32: page p has holders
   int B, R, M, P, page_size, room;
   FixedDiv by_page, by_row, by_writable;  // page_size, M, small_slots
   int* status;
+
+  // An entry of the old table: a page, or -1.  One that is neither, or whose page counts
+  // no holder (it is in the free list), is reported and read as -1.  (From bits, which
+  // stay in L1: 1024 x 2048 slots of 2 M pages take 62 us, 53 without the look-up and 70
+  // with refs itself; 256 x 256 of 60000 13.3, 13.1 and 14.0.)
+  __device__ __forceinline__ int old_entry(size_t i, int* report) const {
+    const int e = checked_entry(table[i], P, report);
+    if (e < 0 || (live[e >> 5] >> (e & 31) & 1u)) return e;
+    record_status(report, ATTN_ERR_INVALID_ARG);
+    return -1;
+  }
 
   // Slots of a row that hold keys or shall: ceil((len + room) / page_size), at most M.
   // (M * page_size <= 2^30 and the host clamps room to it.)
@@ -261,14 +274,19 @@ struct ForkOp {
   __device__ void run(int ph, int* smem) const {
     const int tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Part pages(P), rows(R);
+    const Part pages(P, 32), rows(R);
     if (ph == 0) {
       int n = 0;
-      for (int p = pages.begin + threadIdx.x; p < pages.end; p += kThreads) {
-        const int c = refs[p];
+      for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads) {
+        const int p = p0 + threadIdx.x;
+        const int c = p < pages.end ? refs[p] : -1;
         n += c == 0;
-        refs_out[p] = c;
-        lowest[p] = INT_MAX;
+        const unsigned bits = __ballot_sync(0xffffffffu, c > 0);
+        if (p < pages.end) {
+          refs_out[p] = c;
+          lowest[p] = INT_MAX;
+          if (lane == 0) live[p >> 5] = bits;
+        }
       }
       n = block_sum(n, smem);
       if (threadIdx.x == 0) cta_free[blockIdx.x] = n;
@@ -277,7 +295,7 @@ struct ForkOp {
       // refs_out: the holders that are no slots of the old table ...
       const unsigned entries = static_cast<unsigned>(B) * M, new_entries = static_cast<unsigned>(R) * M;
       for (unsigned i = tid; i < entries; i += n_threads) {
-        const int e = checked_entry(table[i], P, status);
+        const int e = old_entry(i, status);
         if (e >= 0) atomicSub(refs_out + e, 1);
       }
       // ... and the read-only slots of the new one.
@@ -285,7 +303,7 @@ struct ForkOp {
         const int r = by_row.div(i), s = i - r * M;
         const Row x = row(r);
         int e = -1;
-        if (s < x.hi || s < x.lo) e = checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, status);
+        if (s < x.hi || s < x.lo) e = old_entry(static_cast<size_t>(x.parent) * M + s, nullptr);
         if (s < x.lo) {
           if (e >= 0) atomicAdd(refs_out + e, 1);
         } else if (e >= 0) {
@@ -309,7 +327,7 @@ struct ForkOp {
         const Row x = row(r);
         int n = 0;
         for (int s = x.lo + lane; s < x.hi; s += 32) {
-          const int e = checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, nullptr);
+          const int e = old_entry(static_cast<size_t>(x.parent) * M + s, nullptr);
           n += !keeps(e, r * M + s);
         }
         n = __reduce_add_sync(0xffffffffu, n);
@@ -346,7 +364,7 @@ struct ForkOp {
           const bool mine = s < x.hi;
           const int at = r * M + s;
           const int e =
-              mine ? checked_entry(table[static_cast<size_t>(x.parent) * M + s], P, nullptr) : -1;
+              mine ? old_entry(static_cast<size_t>(x.parent) * M + s, nullptr) : -1;
           const bool keep = mine && keeps(e, at);
           const unsigned fresh = __ballot_sync(0xffffffffu, mine && !keep);
           int page = e;
@@ -385,7 +403,10 @@ struct ForkOp {
   }
   __device__ void run_small(int* smem, int* lists) const {
     int* held = lists;       // holders other than slots to be written; then refs_out
-    int* low = held + pad(P);     // lowest (r, slot) that would write the page
+    // Lowest (r, slot) that would write the page; kFree: it has no holder.  Of the pages
+    // in slots to be written, at the end: kStays, or of those that had no holder kGiven.
+    int* low = held + pad(P);
+    constexpr int kFree = INT_MAX - 1, kStays = -1, kGiven = -2;
     int* free_at = low + P;  // free pages, ascending
     int* parent = free_at + P;
     int* len = parent + R;
@@ -394,8 +415,9 @@ struct ForkOp {
     const int p0 = min(t * per, P), p1 = min(p0 + per, P);
     int n = 0;
     for (int p = t; p < P; p += kThreads) {
-      held[pad(p)] = refs[p];
-      low[p] = INT_MAX;
+      const int c = refs[p];
+      held[pad(p)] = c;
+      low[p] = c > 0 ? INT_MAX : kFree;
     }
     for (int r = t; r < R; r += kThreads) {
       const Row x = row(r);
@@ -409,9 +431,17 @@ struct ForkOp {
     for (int p = p0; p < p1; ++p)
       if (held[pad(p)] == 0) free_at[k++] = p;
     __syncthreads();
+    const auto old_entry = [&](int i, int* report) {  // as in run
+      const int e = checked_entry(table[i], P, report);
+      if (e < 0) return e;
+      const int l = low[e];
+      if (l != kFree && l != kGiven) return e;
+      record_status(report, ATTN_ERR_INVALID_ARG);
+      return -1;
+    };
     const unsigned entries = B * M, new_entries = R * M;
     for (unsigned i = t; i < entries; i += kThreads) {
-      const int e = checked_entry(table[i], P, status);
+      const int e = old_entry(i, status);
       if (e >= 0) atomicSub(held + pad(e), 1);
     }
     const auto slot_end = [&](int r) { return parent[r] < 0 ? 0 : slots_for(len[r]); };
@@ -419,7 +449,7 @@ struct ForkOp {
       const int r = by_row.div(i), s = i - r * M;
       const int lo = by_page.div(len[r]);
       int e = -1;
-      if (s < lo || s < slot_end(r)) e = checked_entry(table[parent[r] * M + s], P, status);
+      if (s < lo || s < slot_end(r)) e = old_entry(parent[r] * M + s, nullptr);
       if (s < lo) {
         if (e >= 0) atomicAdd(held + pad(e), 1);
       } else if (e >= 0) {
@@ -438,7 +468,7 @@ struct ForkOp {
       s = by_page.div(len[r]) + f - r * W;
       stays = false;
       if (s >= slot_end(r)) return -2;
-      const int e = checked_entry(table[parent[r] * M + s], P, nullptr);
+      const int e = old_entry(parent[r] * M + s, nullptr);
       stays = e >= 0 && low[e] == r * M + s && held[pad(e)] == 0;
       return e;
     };
@@ -464,7 +494,7 @@ struct ForkOp {
           if (holds_keys && e < 0) length = s * page_size;  // no page left for the keys
         }
         table_out[r * M + s] = e;
-        if (e >= 0) low[e] = -1;  // taken: one more holder, and nobody's lowest
+        if (e >= 0) low[e] = stays ? kStays : kGiven;  // one holder, and nobody's lowest
       }
       if (first) {
         src[r] = copied ? from : -1;
@@ -478,7 +508,7 @@ struct ForkOp {
       if (needed > n_free) record_status(status, ATTN_ERR_NO_PAGES);
     }
     __syncthreads();
-    for (int p = t; p < P; p += kThreads) refs_out[p] = low[p] == -1 ? 1 : held[pad(p)];
+    for (int p = t; p < P; p += kThreads) refs_out[p] = low[p] < 0 ? 1 : held[pad(p)];
   }
 };
 
@@ -707,6 +737,7 @@ cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seql
   op.cta_free = op.free_list + P;
   op.cta_need = op.cta_free + kPagesMaxCtas;
   op.need = op.cta_need + kPagesMaxCtas;
+  op.live = reinterpret_cast<unsigned*>(op.need + R);
   op.B = B;
   op.R = R;
   op.M = M;
