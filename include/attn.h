@@ -471,10 +471,11 @@ ATTN_API int attn_decode_window_paged(const void *q, const void *k_cache, const 
  * Give up the pages that the next decode cannot read.  Slot s of row b keeps its
  * page iff seqlens[b] >= 0, s * page_size < seqlens[b] + room, and
  *     (s + 1) * page_size > seqlens[b] - window  or  s * page_size < sinks:
- * exactly the pages that attn_decode_window_paged reads at these lengths, and those
- * reserved for the next `room` keys.  Any other entry becomes -1 and its page's
- * count falls by one.  seqlens[b] < 0 marks a finished row: all its pages go.  A
- * window as long as the rows (INT_MAX) gives up only what lies behind them.
+ * exactly the pages that attn_decode_window_paged reads at these lengths (at most
+ * max_pages * page_size), and those reserved for the next `room` keys.  Any other entry
+ * becomes -1 and its page's count falls by one.  seqlens[b] < 0 marks a finished row:
+ * all its pages go.  A window as long as the rows (INT_MAX) gives up only what lies
+ * behind them.
  *   block_table_out [B,max_pages], refs_out [num_pages]; each may be its input.
  *   window >= 1, sinks >= 0, room >= 0.
  */
@@ -508,7 +509,9 @@ ATTN_API int attn_pages_free(const int *block_table, const int *refs, const int 
  *   An entry whose page has refs <= 0 sets ATTN_ERR_INVALID_ARG in the status word and
  *   counts as -1 (as for attn_pages_compact).
  *   A parent outside [-1, B) sets ATTN_ERR_INVALID_ARG in the status word and makes
- *   an empty row.  seqlens are clamped to [0, max_pages * page_size].
+ *   an empty row.  A parent with seqlens < 0, a finished row (attn_pages_free), makes a
+ *   row without pages whose seqlens_out is that number: it stays finished.  seqlens
+ *   past max_pages * page_size count as that many.
  */
 ATTN_API int attn_pages_fork(const int *block_table, const int *refs, const int *seqlens,
                              const int *parents, int *block_table_out, int *refs_out,

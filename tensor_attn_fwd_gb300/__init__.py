@@ -824,7 +824,8 @@ def attn_pages_fork(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     """New rows from old ones, with pages for keys [0, length + room); returns
     (block_table [R,max_pages], refs, seqlens [R], src [R], dst [R], counts [2]).
 
-    parents int32 [R]: the old row that each new row continues (-1: an empty row).
+    parents int32 [R]: the old row that each new row continues (-1: an empty row).  A
+    finished row (negative seqlens, as for attn_pages_free) stays one, without pages.
     Full pages are shared; a page still to be written stays with the lowest row that
     has it, if nobody else holds it, and the others get free pages, lowest id first.
     (src, dst) lists the pages to copy (attn_pages_copy, for every layer's cache)

@@ -248,7 +248,8 @@ struct ForkOp {
     return by_page.div(static_cast<int>(keys + page_size - 1));
   }
 
-  // New row r: its parent (-1: an empty row), length, and slots to be written [lo, hi).
+  // New row r: its parent (-1: a row without pages), length, and slots to be written
+  // [lo, hi).  A finished row's (length below 0) stays one.
   struct Row {
     int parent, len, lo, hi;
   };
@@ -259,8 +260,9 @@ struct ForkOp {
       record_status(status, ATTN_ERR_INVALID_ARG);
       x.parent = -1;
     }
-    x.len = x.parent < 0 ? 0 : min(max(seqlens[x.parent], 0), M * page_size);
-    x.lo = by_page.div(x.len);
+    x.len = x.parent < 0 ? 0 : min(seqlens[x.parent], M * page_size);
+    if (x.len < 0) x.parent = -1;
+    x.lo = x.parent < 0 ? 0 : by_page.div(x.len);
     x.hi = x.parent < 0 ? 0 : slots_for(x.len);
     return x;
   }
@@ -444,10 +446,11 @@ struct ForkOp {
       const int e = old_entry(i, status);
       if (e >= 0) atomicSub(held + pad(e), 1);
     }
+    const auto slot_begin = [&](int r) { return parent[r] < 0 ? 0 : by_page.div(len[r]); };
     const auto slot_end = [&](int r) { return parent[r] < 0 ? 0 : slots_for(len[r]); };
     for (unsigned i = t; i < new_entries; i += kThreads) {
       const int r = by_row.div(i), s = i - r * M;
-      const int lo = by_page.div(len[r]);
+      const int lo = slot_begin(r);
       int e = -1;
       if (s < lo || s < slot_end(r)) e = old_entry(parent[r] * M + s, nullptr);
       if (s < lo) {
@@ -465,7 +468,7 @@ struct ForkOp {
     // Slot f's entry; -2 if it is past its row's end.  `stays`: its page is its own.
     const auto entry = [&](int f, int& r, int& s, bool& stays) {
       r = by_writable.div(f);
-      s = by_page.div(len[r]) + f - r * W;
+      s = slot_begin(r) + f - r * W;
       stays = false;
       if (s >= slot_end(r)) return -2;
       const int e = old_entry(parent[r] * M + s, nullptr);

@@ -6,7 +6,7 @@ import torch
 
 import tensor_attn_fwd_gb300 as attn
 
-from test_pages import A, A2, A3, UNS, c_fork, cache_tables, gpu, plain_fork, same  # noqa: F401
+from test_pages import A, A2, A3, UNS, c_fork, cache_tables, gpu, plain_fork, plain_free, same  # noqa: F401
 
 
 # ------------------------------------------------------------------ limits (no GPU)
@@ -51,3 +51,34 @@ def test_fork_reports_entries_whose_page_counts_no_holder(B, P, room):
     got = attn.attn_pages_fork(*gpu(table, refs, lens, parents), 32, room)
     assert attn.attn_debug_status() == attn.ATTN_ERR_INVALID_ARG
     same(got, want, ("table", "refs", "seqlens", "src", "dst", "counts"))
+
+
+# ------------------------------------------------------------------ finished rows
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,P", FORMS)
+@pytest.mark.parametrize("kind", ["same", "beams"])
+def test_fork_keeps_finished_rows_finished(B, P, kind):
+    # free, fork with room, free: a finished row takes no pages and keeps its mark.
+    rng = np.random.default_rng(B)
+    page, room = 32, 40
+    table, refs, lens = cache_tables(rng, B, 20, P, page, 0.7, 0.5)
+    done = rng.random(B) < 0.3
+    done[0] = True
+    lens[done] = -rng.integers(1, 1000, done.sum())
+    parents = np.arange(B) if kind == "same" else rng.integers(-1, B, B)
+    for freed_first in (False, True):
+        t, r = (plain_free(table, refs, lens, page, 10 ** 9, 0) if freed_first else (table, refs))
+        live = np.where((parents >= 0) & (lens[parents] < 0), -1, parents)
+        want = list(plain_fork(t, r, lens, live, page, room))
+        want[2] = np.where((parents >= 0) & (lens[parents] < 0), lens[parents], want[2])
+        got = attn.attn_pages_fork(*gpu(t, r, lens, parents), page, room)
+        assert attn.attn_debug_status() == attn.ATTN_OK
+        same(got, want, ("table", "refs", "seqlens", "src", "dst", "counts"))
+        again = attn.attn_pages_free(got[0], got[1], got[2], page, room=room)
+        same(again, plain_free(want[0], want[1], want[2], page, 10 ** 9, 0, room), ("table", "refs"))
+        assert bool((again[0][torch.from_numpy(want[2] < 0).cuda()] == -1).all())
+    # A length as low as it gets.
+    args = gpu([[0, 1], [2, -1]], [1, 1, 1, 0, 0, 0], [-(2 ** 31), 3], [0, 1])
+    got = attn.attn_pages_fork(*args, 4, room=2)
+    same(got, ([[-1, -1], [2, 3]], [0, 0, 1, 1, 0, 0], [-(2 ** 31), 3], [-1, -1], [-1, -1], [1, 3]),
+         ("table", "refs", "seqlens", "src", "dst", "counts"))
