@@ -141,7 +141,9 @@ class Carver {
 };
 int64_t padded(int64_t n) { return (n + 3) / 4 * 4; }  // to 16 bytes of int32
 
-// An integer in [least, most]; larger ones (all keys, all room) become `most`.
+// An integer in [least, most]; larger ones (all keys, all room) become `most`.  Without
+// a least one the C ABI refuses what is too low: any number below int's is as low.
+constexpr long long kAny = LLONG_MIN;
 int integer(PyObject* obj, const char* name, long long least, long long most) {
   PyObject* index = PyNumber_Index(obj);
   if (index == nullptr) throw PythonError{};
@@ -150,7 +152,7 @@ int integer(PyObject* obj, const char* name, long long least, long long most) {
   Py_DECREF(index);
   if (overflow != 0) x = overflow > 0 ? LLONG_MAX : LLONG_MIN;
   if (x < least) refuse(std::string(name) + " must be at least " + std::to_string(least));
-  return static_cast<int>(std::min(x, most));
+  return static_cast<int>(std::max<long long>(std::min(x, most), INT_MIN));
 }
 
 constexpr long long kAll = 1ll << 30;  // beyond every sequence
@@ -242,7 +244,7 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       raise_if(attn_window_fwd_num_splits(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, &splits),
                "attn_window_fwd_num_splits");
     else
-      splits = integer(a[8], "num_splits", LLONG_MIN, INT_MAX);
+      splits = integer(a[8], "num_splits", kAny, INT_MAX);
     Tensor ws;
     if (splits > 1 && splits <= (static_cast<int64_t>(s.Sk) + 127) / 128) {  // (more are refused below)
       long long need = 0;
@@ -319,7 +321,7 @@ PyObject* decode(const Tensor& q, const Cache& c, PyObject* const* a, const char
     raise_if(attn_decode_window_num_splits(B, Hq, c.Hkv, c.Sk, D, window, sinks, &splits),
              "attn_decode_window_num_splits");
   else
-    splits = integer(a[3], "num_splits", LLONG_MIN, INT_MAX);
+    splits = integer(a[3], "num_splits", kAny, INT_MAX);
   Tensor o = output_bf16(a[5], {B, Hq, D}, device, "o");
   Tensor lse = output_f32(a[6], {B, Hq}, device, "lse");
   if (c.table == nullptr)
@@ -385,7 +387,7 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 9, [&] {
     const Pages p = pages_of(a[0], a[1]);
     const Tensor& lens = int32(a[2], "seqlens", {p.B}, p.device);
-    const int page = integer(a[3], "page_size", LLONG_MIN, INT_MAX);
+    const int page = integer(a[3], "page_size", kAny, INT_MAX);
     const int window = a[4] == Py_None ? static_cast<int>(kAll) : integer(a[4], "window", 1, kAll);
     const int sinks = integer(a[5], "sinks", 0, kAll), room = integer(a[6], "room", 0, kAll);
     const c10::cuda::CUDAGuard guard(p.device);
@@ -420,7 +422,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& lens = int32(a[2], "seqlens", {p.B}, p.device);
     const Tensor& parents = int32(a[3], "parents", {-1}, p.device);
     const int R = size_int(parents.size(0), "parents");
-    const int page = integer(a[4], "page_size", LLONG_MIN, INT_MAX);
+    const int page = integer(a[4], "page_size", kAny, INT_MAX);
     const int room = integer(a[5], "room", 0, kAll);
     const c10::cuda::CUDAGuard guard(p.device);
     Tensor ws = pages_workspace(p, R);
