@@ -8,6 +8,7 @@
 // functions document the calls and pass their arguments on.
 #include <Python.h>
 
+#include <ATen/core/DimVector.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -97,23 +98,34 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, at::Device device) {
   return at::detail::empty_cuda(shape, type, device, std::nullopt);
 }
 
-// The output that the caller gave, or a new one.
-Tensor output(PyObject* given, at::IntArrayRef shape, at::ScalarType type, const char* type_name,
-              at::Device device, const char* name) {
-  if (given == Py_None) return fresh(shape, type, device);
-  const Tensor& t = tensor(given, name);
-  check(t, name, type, type_name, static_cast<int>(shape.size()), device);
-  check_shape(t, name, shape);
-  return t;
+// The output that the caller gave, or a new one from get().
+class Output {
+ public:
+  Output(PyObject* given, at::IntArrayRef shape, at::ScalarType type, const char* type_name,
+         at::Device device, const char* name)
+      : shape_(shape.begin(), shape.end()), type_(type), device_(device) {
+    if (given == Py_None) return;
+    given_ = &tensor(given, name);
+    check(*given_, name, type, type_name, static_cast<int>(shape.size()), device);
+    check_shape(*given_, name, shape);
+  }
+  bool given() const { return given_ != nullptr; }
+  Tensor get() const { return given_ != nullptr ? *given_ : fresh(shape_, type_, device_); }
+
+ private:
+  const Tensor* given_ = nullptr;
+  at::DimVector shape_;
+  at::ScalarType type_;
+  at::Device device_;
+};
+Output output_bf16(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
+  return Output(given, shape, at::kBFloat16, "bfloat16", device, name);
 }
-Tensor output_bf16(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
-  return output(given, shape, at::kBFloat16, "bfloat16", device, name);
+Output output_f32(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
+  return Output(given, shape, at::kFloat, "float32", device, name);
 }
-Tensor output_f32(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
-  return output(given, shape, at::kFloat, "float32", device, name);
-}
-Tensor output_int32(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
-  return output(given, shape, at::kInt, "int32", device, name);
+Output output_int32(PyObject* given, at::IntArrayRef shape, at::Device device, const char* name) {
+  return Output(given, shape, at::kInt, "int32", device, name);
 }
 Tensor new_int32(int64_t n, at::Device device) {
   return fresh({n}, at::kInt, device);
@@ -187,6 +199,24 @@ void* current_stream(at::Device device) {
 int* ints(const Tensor& t) { return t.numel() > 0 ? static_cast<int*>(t.data_ptr()) : nullptr; }
 float* floats(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 
+// The GPU part of a call, without Python's lock: allocations and launches can wait for
+// the GPU (a full launch queue, a pool that has to grow), other threads go on meanwhile,
+// and a host function in a stream that takes the lock cannot be waited for by its holder.
+// No Python object is touched in it.
+class GpuPart {
+ public:
+  explicit GpuPart(at::Device device) : lock_(PyEval_SaveThread()), guard_(device) {}
+  GpuPart(const GpuPart&) = delete;
+
+ private:
+  struct Lock {
+    explicit Lock(PyThreadState* state) : state(state) {}
+    ~Lock() { PyEval_RestoreThread(state); }
+    PyThreadState* state;
+  } lock_;
+  c10::cuda::CUDAGuard guard_;
+};
+
 // ------------------------------------------------------------------ results
 PyObject* pack(std::initializer_list<Tensor> tensors) {
   PyObject* tuple = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
@@ -236,26 +266,30 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Sizes s = sizes_of(q, k, v);
     const int window = integer(a[3], "window", 1, kAll), sinks = integer(a[4], "sinks", 0, kAll);
     const float scale = scale_of(a[5], s.D);
-    const c10::cuda::CUDAGuard guard(q.device());
-    Tensor o = output_bf16(a[6], q.sizes(), q.device(), "o");
-    Tensor lse = output_f32(a[7], {s.B, s.Hq, s.Sq}, q.device(), "lse");
-    int splits = 0;
-    if (a[8] == Py_None)
-      raise_if(attn_window_fwd_num_splits(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, &splits),
-               "attn_window_fwd_num_splits");
-    else
-      splits = integer(a[8], "num_splits", kAny, INT_MAX);
-    Tensor ws;
-    if (splits > 1 && splits <= (static_cast<int64_t>(s.Sk) + 127) / 128) {  // (more are refused below)
-      long long need = 0;
-      raise_if(attn_window_fwd_workspace(s.B, s.Hq, s.Hkv, s.Sq, s.D, splits, &need),
+    const Output o_out = output_bf16(a[6], q.sizes(), q.device(), "o");
+    const Output lse_out = output_f32(a[7], {s.B, s.Hq, s.Sq}, q.device(), "lse");
+    const bool pick = a[8] == Py_None;
+    int splits = pick ? 0 : integer(a[8], "num_splits", kAny, INT_MAX);
+    Tensor o, lse;
+    {
+      const GpuPart gpu(q.device());
+      if (pick)
+        raise_if(attn_window_fwd_num_splits(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, &splits),
+                 "attn_window_fwd_num_splits");
+      o = o_out.get();
+      lse = lse_out.get();
+      Tensor ws;
+      if (splits > 1 && splits <= (static_cast<int64_t>(s.Sk) + 127) / 128) {  // (more are refused below)
+        long long need = 0;
+        raise_if(attn_window_fwd_workspace(s.B, s.Hq, s.Hkv, s.Sq, s.D, splits, &need),
+                 "attn_window_fwd");
+        ws = fresh({std::max(need, 1ll)}, at::kFloat, q.device());  // full rounds need none
+      }
+      raise_if(attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
+                               ws.defined() ? floats(ws) : nullptr, s.B, s.Hq, s.Hkv, s.Sq, s.Sk,
+                               s.D, window, sinks, splits, scale, current_stream(q.device())),
                "attn_window_fwd");
-      ws = fresh({std::max(need, 1ll)}, at::kFloat, q.device());  // full rounds need none
     }
-    raise_if(attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
-                             ws.defined() ? floats(ws) : nullptr, s.B, s.Hq, s.Hkv, s.Sq, s.Sk,
-                             s.D, window, sinks, splits, scale, current_stream(q.device())),
-             "attn_window_fwd");
     return pack({o, lse});
   });
 }
@@ -274,27 +308,32 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_shape(lse, "lse", {s.B, s.Hq, s.Sq});
     const int window = integer(a[6], "window", 1, kAll), sinks = integer(a[7], "sinks", 0, kAll);
     const float scale = scale_of(a[8], s.D);
-    const c10::cuda::CUDAGuard guard(q.device());
-    Tensor dq = output_bf16(a[9], q.sizes(), q.device(), "dq");
-    Tensor dk = output_bf16(a[10], k.sizes(), q.device(), "dk");
-    Tensor dv = output_bf16(a[11], k.sizes(), q.device(), "dv");
-    long long need = 0;
-    raise_if(attn_window_bwd_workspace(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, &need),
-             "attn_window_bwd_workspace");
+    const Output dq_out = output_bf16(a[9], q.sizes(), q.device(), "dq");
+    const Output dk_out = output_bf16(a[10], k.sizes(), q.device(), "dk");
+    const Output dv_out = output_bf16(a[11], k.sizes(), q.device(), "dv");
     Tensor ws;
-    if (a[12] == Py_None) {
-      ws = fresh({need}, at::kFloat, q.device());
-    } else {
+    if (a[12] != Py_None) {
       ws = tensor(a[12], "workspace");
       check(ws, "workspace", at::kFloat, "float32", static_cast<int>(ws.dim()), q.device());
-      if (ws.numel() < need)
-        refuse("workspace must have at least " + std::to_string(need) + " entries");
     }
-    raise_if(attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
-                             dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                             floats(ws), s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, scale,
-                             current_stream(q.device())),
-             "attn_window_bwd");
+    Tensor dq, dk, dv;
+    {
+      const GpuPart gpu(q.device());
+      long long need = 0;
+      raise_if(attn_window_bwd_workspace(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, &need),
+               "attn_window_bwd_workspace");
+      if (ws.defined() && ws.numel() < need)
+        refuse("workspace must have at least " + std::to_string(need) + " entries");
+      dq = dq_out.get();
+      dk = dk_out.get();
+      dv = dv_out.get();
+      if (!ws.defined()) ws = fresh({need}, at::kFloat, q.device());
+      raise_if(attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), floats(lse),
+                               dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                               floats(ws), s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, window, sinks, scale,
+                               current_stream(q.device())),
+               "attn_window_bwd");
+    }
     return pack({dq, dk, dv});
   });
 }
@@ -315,27 +354,31 @@ PyObject* decode(const Tensor& q, const Cache& c, PyObject* const* a, const char
   const int* seqlens = a[0] == Py_None ? nullptr : ints(int32(a[0], "seqlens", {B}, device));
   const int window = integer(a[1], "window", 1, kAll), sinks = integer(a[2], "sinks", 0, kAll);
   const float scale = scale_of(a[4], D);
-  const c10::cuda::CUDAGuard guard(device);
-  int splits = 0;
-  if (a[3] == Py_None)
-    raise_if(attn_decode_window_num_splits(B, Hq, c.Hkv, c.Sk, D, window, sinks, &splits),
-             "attn_decode_window_num_splits");
-  else
-    splits = integer(a[3], "num_splits", kAny, INT_MAX);
-  Tensor o = output_bf16(a[5], {B, Hq, D}, device, "o");
-  Tensor lse = output_f32(a[6], {B, Hq}, device, "lse");
-  if (c.table == nullptr)
-    raise_if(attn_decode_window(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), seqlens, o.data_ptr(),
-                                floats(lse), B, Hq, c.Hkv, c.Sk, D, window, sinks, splits, scale,
-                                current_stream(device)),
-             what);
-  else
-    raise_if(attn_decode_window_paged(
-                 q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(*c.table), seqlens,
-                 o.data_ptr(), floats(lse), B, Hq, c.Hkv, size_int(c.k.size(0), "k_cache"),
-                 size_int(c.k.size(2), "k_cache"), size_int(c.table->size(1), "block_table"), D,
-                 window, sinks, splits, scale, current_stream(device)),
-             what);
+  const bool pick = a[3] == Py_None;
+  int splits = pick ? 0 : integer(a[3], "num_splits", kAny, INT_MAX);
+  const Output o_out = output_bf16(a[5], {B, Hq, D}, device, "o");
+  const Output lse_out = output_f32(a[6], {B, Hq}, device, "lse");
+  Tensor o, lse;
+  {
+    const GpuPart gpu(device);
+    if (pick)
+      raise_if(attn_decode_window_num_splits(B, Hq, c.Hkv, c.Sk, D, window, sinks, &splits),
+               "attn_decode_window_num_splits");
+    o = o_out.get();
+    lse = lse_out.get();
+    if (c.table == nullptr)
+      raise_if(attn_decode_window(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), seqlens,
+                                  o.data_ptr(), floats(lse), B, Hq, c.Hkv, c.Sk, D, window, sinks,
+                                  splits, scale, current_stream(device)),
+               what);
+    else
+      raise_if(attn_decode_window_paged(
+                   q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(*c.table), seqlens,
+                   o.data_ptr(), floats(lse), B, Hq, c.Hkv, size_int(c.k.size(0), "k_cache"),
+                   size_int(c.k.size(2), "k_cache"), size_int(c.table->size(1), "block_table"), D,
+                   window, sinks, splits, scale, current_stream(device)),
+               what);
+  }
   return pack({o, lse});
 }
 
@@ -390,21 +433,25 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int page = integer(a[3], "page_size", kAny, INT_MAX);
     const int window = a[4] == Py_None ? static_cast<int>(kAll) : integer(a[4], "window", 1, kAll);
     const int sinks = integer(a[5], "sinks", 0, kAll), room = integer(a[6], "room", 0, kAll);
-    const c10::cuda::CUDAGuard guard(p.device);
+    const Output table_out = output_int32(a[7], {p.B, p.M}, p.device, "block_table_out");
+    const Output refs_out = output_int32(a[8], {p.P}, p.device, "refs_out");
     Tensor table, refs;
-    if (a[7] == Py_None && a[8] == Py_None) {
-      const int64_t entries = padded(static_cast<int64_t>(p.B) * p.M);
-      Carver results(entries + p.P, p.device);
-      table = results.take({p.B, p.M});
-      results.skip_to(entries);
-      refs = results.take({p.P});
-    } else {
-      table = output_int32(a[7], {p.B, p.M}, p.device, "block_table_out");
-      refs = output_int32(a[8], {p.P}, p.device, "refs_out");
+    {
+      const GpuPart gpu(p.device);
+      if (!table_out.given() && !refs_out.given()) {
+        const int64_t entries = padded(static_cast<int64_t>(p.B) * p.M);
+        Carver results(entries + p.P, p.device);
+        table = results.take({p.B, p.M});
+        results.skip_to(entries);
+        refs = results.take({p.P});
+      } else {
+        table = table_out.get();
+        refs = refs_out.get();
+      }
+      raise_if(attn_pages_free(ints(p.table), ints(p.refs), ints(lens), ints(table), ints(refs), p.B,
+                               p.M, p.P, page, window, sinks, room, current_stream(p.device)),
+               "attn_pages_free");
     }
-    raise_if(attn_pages_free(ints(p.table), ints(p.refs), ints(lens), ints(table), ints(refs), p.B,
-                             p.M, p.P, page, window, sinks, room, current_stream(p.device)),
-             "attn_pages_free");
     return pack({table, refs});
   });
 }
@@ -424,16 +471,22 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int R = size_int(parents.size(0), "parents");
     const int page = integer(a[4], "page_size", kAny, INT_MAX);
     const int room = integer(a[5], "room", 0, kAll);
-    const c10::cuda::CUDAGuard guard(p.device);
-    Tensor ws = pages_workspace(p, R);
-    Carver results(static_cast<int64_t>(R) * p.M + p.P + 3ll * R + 2, p.device);
-    Tensor table = results.take({R, p.M}), refs = results.take({p.P});
-    Tensor lens_out = results.take({R}), src = results.take({R}), dst = results.take({R});
-    Tensor counts = results.take({2});
-    raise_if(attn_pages_fork(ints(p.table), ints(p.refs), ints(lens), ints(parents), ints(table),
-                             ints(refs), ints(lens_out), ints(src), ints(dst), ints(counts),
-                             ints(ws), p.B, R, p.M, p.P, page, room, current_stream(p.device)),
-             "attn_pages_fork");
+    Tensor table, refs, lens_out, src, dst, counts;
+    {
+      const GpuPart gpu(p.device);
+      Tensor ws = pages_workspace(p, R);
+      Carver results(static_cast<int64_t>(R) * p.M + p.P + 3ll * R + 2, p.device);
+      table = results.take({R, p.M});
+      refs = results.take({p.P});
+      lens_out = results.take({R});
+      src = results.take({R});
+      dst = results.take({R});
+      counts = results.take({2});
+      raise_if(attn_pages_fork(ints(p.table), ints(p.refs), ints(lens), ints(parents), ints(table),
+                               ints(refs), ints(lens_out), ints(src), ints(dst), ints(counts),
+                               ints(ws), p.B, R, p.M, p.P, page, room, current_stream(p.device)),
+               "attn_pages_fork");
+    }
     return pack({table, refs, lens_out, src, dst, counts});
   });
 }
@@ -442,16 +495,21 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 2, [&] {
     const Pages p = pages_of(a[0], a[1]);
-    const c10::cuda::CUDAGuard guard(p.device);
-    Tensor ws = pages_workspace(p, 0);
-    Carver results(static_cast<int64_t>(p.B) * p.M + p.P + 2ll * (p.P / 2) + 1, p.device);
-    Tensor table = results.take({p.B, p.M}), refs = results.take({p.P});
-    Tensor src = results.take({p.P / 2}), dst = results.take({p.P / 2});
-    Tensor live = results.take({1});
-    raise_if(attn_pages_compact(ints(p.table), ints(p.refs), ints(table), ints(refs), ints(src),
-                                ints(dst), ints(live), ints(ws), p.B, p.M, p.P,
-                                current_stream(p.device)),
-             "attn_pages_compact");
+    Tensor table, refs, src, dst, live;
+    {
+      const GpuPart gpu(p.device);
+      Tensor ws = pages_workspace(p, 0);
+      Carver results(static_cast<int64_t>(p.B) * p.M + p.P + 2ll * (p.P / 2) + 1, p.device);
+      table = results.take({p.B, p.M});
+      refs = results.take({p.P});
+      src = results.take({p.P / 2});
+      dst = results.take({p.P / 2});
+      live = results.take({1});
+      raise_if(attn_pages_compact(ints(p.table), ints(p.refs), ints(table), ints(refs), ints(src),
+                                  ints(dst), ints(live), ints(ws), p.B, p.M, p.P,
+                                  current_stream(p.device)),
+               "attn_pages_compact");
+    }
     return pack({table, refs, src, dst, live});
   });
 }
@@ -467,12 +525,14 @@ PyObject* pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("the caches must have one shape, type and device");
     const Tensor& src = int32(a[2], "src", {-1}, k.device());
     const Tensor& dst = int32(a[3], "dst", {src.size(0)}, k.device());
-    const c10::cuda::CUDAGuard guard(k.device());
     const long long page_bytes = k.numel() / k.size(0) * k.element_size();
-    raise_if(attn_pages_copy(k.data_ptr(), v.data_ptr(), ints(src), ints(dst),
-                             size_int(src.size(0), "src"), size_int(k.size(0), "k_cache"),
-                             page_bytes, current_stream(k.device())),
-             "attn_pages_copy");
+    {
+      const GpuPart gpu(k.device());
+      raise_if(attn_pages_copy(k.data_ptr(), v.data_ptr(), ints(src), ints(dst),
+                               size_int(src.size(0), "src"), size_int(k.size(0), "k_cache"),
+                               page_bytes, current_stream(k.device())),
+               "attn_pages_copy");
+    }
     Py_RETURN_NONE;
   });
 }

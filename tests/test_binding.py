@@ -1,8 +1,15 @@
 """The compiled binding (csrc/binding.cpp) of the windowed and page calls."""
+import os
+import subprocess
+import sys
+import sysconfig
+
 import pytest
 import torch
 
 import tensor_attn_fwd_gb300 as attn
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _tensors():
@@ -28,3 +35,46 @@ def test_no_negative_number_passes_for_a_positive_one(n):
                  lambda: attn.attn_pages_fork(table, refs, lens, parents, n)):
         with pytest.raises(attn.AttnError, match="INVALID_ARG"):
             call()
+
+
+# A stand-in for the library's launches, which says whether its caller held Python's lock.
+STAND_IN = r"""
+#include <Python.h>
+#define F(name) int name() { return PyGILState_Check() ? 4 : 0; }
+F(attn_window_fwd) F(attn_window_bwd) F(attn_decode_window) F(attn_decode_window_paged)
+F(attn_pages_free) F(attn_pages_fork) F(attn_pages_compact) F(attn_pages_copy)
+"""
+CALLS = r"""
+import ctypes, sys
+ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)  # found before libattn.so's own
+sys.path[:0] = [sys.argv[2], sys.argv[2] + "/tests"]
+import torch
+import tensor_attn_fwd_gb300 as attn
+from test_binding import _tensors
+q, k, cache, table, refs, lens, parents = _tensors()
+q1 = q[:, :, :1].contiguous()
+o, lse = attn.attn_window_fwd(q, k, k, 100, num_splits=1)
+for call in (lambda: attn.attn_window_fwd(q, k, k, 100),
+             lambda: attn.attn_window_fwd(q, k, k, 100, num_splits=2, o=o, lse=lse),
+             lambda: attn.attn_window_bwd(q, k, k, o, lse, q, 100),
+             lambda: attn.decode_window(q1, k, k, 100),
+             lambda: attn.decode_window_paged(q1, cache, cache, table, lens, 100),
+             lambda: attn.attn_pages_free(table, refs, lens, 64, 100),
+             lambda: attn.attn_pages_fork(table, refs, lens, parents, 64),
+             lambda: attn.attn_pages_compact(table, refs),
+             lambda: attn.attn_pages_copy(cache, cache, table[0], table[0])):
+    call()
+"""
+
+
+@pytest.mark.gpu
+def test_launches_do_not_hold_the_interpreters_lock(tmp_path):
+    # A launch can wait for the GPU; the other threads, and host functions in a stream that
+    # need the lock, have to go on meanwhile.
+    src, lib = tmp_path / "stand_in.c", tmp_path / "stand_in.so"
+    src.write_text(STAND_IN)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], str(src),
+                    "-o", str(lib)], check=True)
+    r = subprocess.run([sys.executable, "-c", CALLS, str(lib), ROOT], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
