@@ -809,7 +809,8 @@ def attn_pages_free(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     each page), seqlens int32 [B] (negative: a finished row).  Kept are the pages that
     decode_window_paged reads at these lengths with this window and sinks
     (``window=None``: every key), and those reserved for the next ``room`` keys.
-    ``block_table_out`` and ``refs_out`` may be the inputs.
+    ``block_table_out`` and ``refs_out`` may be the inputs; without both the results
+    share one allocation.
     """
     call = (_fast or _native()).pages_free
     if stream is not None:
@@ -830,7 +831,8 @@ def attn_pages_fork(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torc
     has it, if nobody else holds it, and the others get free pages, lowest id first.
     (src, dst) lists the pages to copy (attn_pages_copy, for every layer's cache)
     before the new rows are used.  counts holds the pages needed and the pages free;
-    if they do not suffice, attn_debug_status reports ATTN_ERR_NO_PAGES.
+    if they do not suffice, attn_debug_status reports ATTN_ERR_NO_PAGES.  The results
+    share one allocation: clone what is to be kept longer than the rest.
     """
     call = (_fast or _native()).pages_fork
     if stream is not None:
@@ -844,7 +846,7 @@ def attn_pages_compact(block_table: torch.Tensor, refs: torch.Tensor, stream=Non
 
     Pages below num_live stay, the others move to the lowest free ids; (src, dst)
     lists the moves (then -1) for attn_pages_copy, for every layer's cache, before
-    the new table is used.
+    the new table is used.  The results share one allocation, as attn_pages_fork's.
     """
     call = (_fast or _native()).pages_compact
     if stream is not None:

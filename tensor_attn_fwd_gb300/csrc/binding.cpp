@@ -131,8 +131,11 @@ Tensor new_int32(int64_t n, at::Device device) {
   return fresh({n}, at::kInt, device);
 }
 
+int64_t padded(int64_t n) { return (n + 3) / 4 * 4; }  // to 16 bytes of int32
+
 // Tensors that share one allocation of int32: an allocation and its tensor cost
-// over a microsecond each, a further tensor on its storage a tenth of that.
+// over a microsecond each, a further tensor on its storage a tenth of that.  Each begins
+// at a multiple of 16 bytes, for the vector accesses of the calls that take it next.
 class Carver {
  public:
   Carver(int64_t n, at::Device device) : all_(new_int32(n, device)) {}
@@ -141,17 +144,14 @@ class Carver {
         c10::Storage(all_.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), all_.dtype());
     t.unsafeGetTensorImpl()->set_storage_offset(at_);
     t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    at_ += t.numel();
+    at_ += padded(t.numel());
     return t;
   }
-
-  void skip_to(int64_t at) { at_ = at; }
 
  private:
   Tensor all_;
   int64_t at_ = 0;
 };
-int64_t padded(int64_t n) { return (n + 3) / 4 * 4; }  // to 16 bytes of int32
 
 // An integer in [least, most]; larger ones (all keys, all room) become `most`.  Without
 // a least one the C ABI refuses what is too low: any number below int's is as low.
@@ -439,10 +439,8 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
       const GpuPart gpu(p.device);
       if (!table_out.given() && !refs_out.given()) {
-        const int64_t entries = padded(static_cast<int64_t>(p.B) * p.M);
-        Carver results(entries + p.P, p.device);
+        Carver results(padded(static_cast<int64_t>(p.B) * p.M) + p.P, p.device);
         table = results.take({p.B, p.M});
-        results.skip_to(entries);
         refs = results.take({p.P});
       } else {
         table = table_out.get();
@@ -475,7 +473,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
       const GpuPart gpu(p.device);
       Tensor ws = pages_workspace(p, R);
-      Carver results(static_cast<int64_t>(R) * p.M + p.P + 3ll * R + 2, p.device);
+      Carver results(padded(static_cast<int64_t>(R) * p.M) + padded(p.P) + 3 * padded(R) + 2, p.device);
       table = results.take({R, p.M});
       refs = results.take({p.P});
       lens_out = results.take({R});
@@ -499,7 +497,8 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
       const GpuPart gpu(p.device);
       Tensor ws = pages_workspace(p, 0);
-      Carver results(static_cast<int64_t>(p.B) * p.M + p.P + 2ll * (p.P / 2) + 1, p.device);
+      Carver results(padded(static_cast<int64_t>(p.B) * p.M) + padded(p.P) + 2 * padded(p.P / 2) + 1,
+                     p.device);
       table = results.take({p.B, p.M});
       refs = results.take({p.P});
       src = results.take({p.P / 2});

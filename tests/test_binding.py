@@ -78,3 +78,22 @@ def test_launches_do_not_hold_the_interpreters_lock(tmp_path):
     r = subprocess.run([sys.executable, "-c", CALLS, str(lib), ROOT], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,M,P", [(1, 1, 1), (3, 5, 21), (7, 9, 130), (50, 33, 5001), (300, 5, 9999)])
+def test_page_results_begin_at_16_bytes_and_do_not_overlap(B, M, P):
+    # One allocation, from which the next calls read and write in vectors.
+    table = torch.full((B, M), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    parents = torch.arange(B, dtype=torch.int32, device="cuda")
+    for results in (attn.attn_pages_free(table, refs, lens, 4),
+                    attn.attn_pages_fork(table, refs, lens, parents, 4),
+                    attn.attn_pages_compact(table, refs)):
+        spans = []
+        for t in results:
+            assert t.data_ptr() % 16 == 0
+            spans.append((t.storage_offset(), t.storage_offset() + t.numel()))
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        assert spans[-1][1] * 4 <= results[0].untyped_storage().nbytes()
