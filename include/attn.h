@@ -384,7 +384,8 @@ ATTN_API int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, 
 
 /* Floats of workspace for attn_window_fwd with num_splits on the current device: 0 with
  * one, or where every round is full (the pointer may not be NULL then either).
- * Host-only.  ATTN_ERR_INVALID_ARG and ATTN_ERR_UNSUPPORTED as attn_window_fwd. */
+ * Host-only.  ATTN_ERR_INVALID_ARG and ATTN_ERR_UNSUPPORTED as attn_window_fwd (but for
+ * Sk, which the size does not depend on). */
 ATTN_API int attn_window_fwd_workspace(int B, int Hq, int Hkv, int Sq, int D, int num_splits,
                                        long long *floats);
 

@@ -309,6 +309,8 @@ int attn_window_fwd_workspace(int B, int Hq, int Hkv, int Sq, int D, int num_spl
     return ATTN_ERR_INVALID_ARG;
   if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
   if (Sq > kMaxSeq || static_cast<long long>(B) * Hq > (1ll << 30) ||
+      static_cast<long long>(B) * Hq * Sq > kMaxElems / D ||
+      static_cast<long long>(B) * Hq * ((Sq + 127) / 128) > (1ll << 30) ||
       (num_splits > 1 && !window_splits_fit(B, Hq, Hkv, Sq, D, num_splits)))
     return ATTN_ERR_UNSUPPORTED;
   *floats = num_splits == 1 ? 0
@@ -604,6 +606,21 @@ int attn_decode_splitkv_paged(const void* q, const void* k_cache, const void* v_
 
 namespace {
 
+// The backward's sizes (positive ones) are within its limits.
+bool bwd_sizes_fit(int B, int Hq, int Hkv, int Sq, int Sk, int D) {
+  if (Sq > kMaxSeq || Sk > kMaxSeq) return false;
+  if (static_cast<long long>(B) * Hq > (1ll << 30)) return false;  // (no product below overflows)
+  if (static_cast<long long>(B) * Hq * Sq > kMaxElems / D ||
+      static_cast<long long>(B) * Hkv * Sk > kMaxElems / D)
+    return false;
+  if (static_cast<long long>(B) * Hq * ((Sq + 127) / 128) > (1ll << 30) ||
+      static_cast<long long>(B) * Hkv * ((Sk + 127) / 128) > (1ll << 30))
+    return false;
+  // Delta rows are indexed with int.
+  if (static_cast<long long>(B) * Hq * Sq > (1ll << 30)) return false;
+  return D == 64 || D == 128;
+}
+
 // The argument checks of the backward entry points; ATTN_OK or the status to return.
 int bwd_check_args(const void* q, const void* k, const void* v, const void* o, const float* lse,
                    const void* dout, const void* dq, const void* dk, const void* dv,
@@ -615,16 +632,7 @@ int bwd_check_args(const void* q, const void* k, const void* v, const void* o, c
   if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  if (Sq > kMaxSeq || Sk > kMaxSeq) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hq * Sq * D > kMaxElems ||
-      static_cast<long long>(B) * Hkv * Sk * D > kMaxElems)
-    return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hq * ((Sq + 127) / 128) > (1ll << 30) ||
-      static_cast<long long>(B) * Hkv * ((Sk + 127) / 128) > (1ll << 30))
-    return ATTN_ERR_UNSUPPORTED;
-  // Delta rows are indexed with int.
-  if (static_cast<long long>(B) * Hq * Sq > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
-  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!bwd_sizes_fit(B, Hq, Hkv, Sq, Sk, D)) return ATTN_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
       !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
       !aligned16(delta_ws))
@@ -670,9 +678,7 @@ int attn_window_bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int
   if (floats == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || D <= 0 ||
       window < 1 || sinks < 0 || Hq % Hkv != 0)
     return ATTN_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
-  if (Sq > kMaxSeq || Sk > kMaxSeq || static_cast<long long>(B) * Hq > (1ll << 30))
-    return ATTN_ERR_UNSUPPORTED;
+  if (!bwd_sizes_fit(B, Hq, Hkv, Sq, Sk, D)) return ATTN_ERR_UNSUPPORTED;
   *floats = window_bwd_workspace_floats(B, Hq, Hkv, Sq, Sk, D, window < Sk ? window : Sk,
                                         sinks < Sk ? sinks : Sk);
   return ATTN_OK;

@@ -48,3 +48,29 @@ def test_forward_workspace_holds_the_partials_of_the_last_round():
     n_sm = torch.cuda.get_device_properties(0).multi_processor_count
     check_workspaces(n_sm)
     assert any(workspace_floats(*case, 2, n_sm) for case in WORKSPACES)
+
+
+# B, Hq, Hkv, Sq, D: too many elements; too many 128-row tiles; too many heads
+@pytest.mark.parametrize("case", [(1, 1 << 10, 1, 1 << 30, 128), (1 << 20, 1 << 10, 1, 129, 64),
+                                  (1 << 21, 1 << 10, 1, 8, 64), (1, 2, 1, (1 << 30) + 1, 64),
+                                  (2 ** 31 - 1, 2 ** 31 - 1, 1, 2 ** 31 - 1, 128)])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_forward_workspace_refuses_the_sizes_that_the_call_refuses(case, splits):
+    n = ctypes.c_longlong(-1)
+    assert _lib().attn_window_fwd_workspace(*case, splits, ctypes.byref(n)) == UNS
+    A = 0x10000000
+    B, Hq, Hkv, Sq, D = case
+    assert _lib().attn_window_fwd(A, A, A, A, A, A, B, Hq, Hkv, Sq, 1000, D, 10, 1, splits, 0.1, None) == UNS
+
+
+# B, Hq, Hkv, Sq, Sk, D
+@pytest.mark.parametrize("case", [(1, 1 << 10, 1, 1 << 30, 8, 128), (1, 1 << 10, 1 << 10, 8, 1 << 30, 128),
+                                  (1, 1 << 10, 1, 1 << 21, 8, 64), (1 << 20, 1 << 10, 1 << 10, 1, 200, 64),
+                                  (1 << 21, 1 << 10, 1, 1, 8, 64), (1, 2, 1, 8, (1 << 30) + 1, 64),
+                                  (2 ** 31 - 1, 2 ** 31 - 1, 1, 2 ** 31 - 1, 2 ** 31 - 1, 128),
+                                  (1, 2, 1, 8, 8, 256)])
+def test_backward_workspace_refuses_the_sizes_that_the_call_refuses(case):
+    n = ctypes.c_longlong(-1)
+    assert _lib().attn_window_bwd_workspace(*case, 10, 1, ctypes.byref(n)) == UNS
+    A = 0x10000000
+    assert _lib().attn_window_bwd(*[A] * 10, *case, 10, 1, 0.1, None) == UNS
