@@ -157,8 +157,10 @@ int fwd_check_args(const void* q, const void* k, const void* v, const void* o, c
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (Sq > kMaxSeq || Sk > kMaxSeq) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hq * Sq * D > kMaxElems ||
-      static_cast<long long>(B) * Hkv * Sk * D > kMaxElems)
+  // (Then no product below overflows.)
+  if (static_cast<long long>(B) * Hq > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hq * Sq > kMaxElems / D ||
+      static_cast<long long>(B) * Hkv * Sk > kMaxElems / D)
     return ATTN_ERR_UNSUPPORTED;
   // Work items (B*Hq*ceil(Sq/256), or ceil(Sq/128) at D = 256) are indexed with int.
   if (static_cast<long long>(B) * Hq * ((Sq + 127) / 128) > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;

@@ -74,3 +74,16 @@ def test_backward_workspace_refuses_the_sizes_that_the_call_refuses(case):
     assert _lib().attn_window_bwd_workspace(*case, 10, 1, ctypes.byref(n)) == UNS
     A = 0x10000000
     assert _lib().attn_window_bwd(*[A] * 10, *case, 10, 1, 0.1, None) == UNS
+
+
+# ------------------------------------------------------------------ products past 64 bits
+@pytest.mark.parametrize("call", ["attn_fwd", "attn_window_fwd"])
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk", [(1 << 30, 1 << 30, 1, 1 << 30, 8), (1 << 30, 1 << 30, 1, 1 << 28, 8),
+                                            (1 << 29, 1 << 30, 1 << 30, 1 << 30, 1 << 30)])
+def test_sizes_whose_product_wraps_are_refused(call, B, Hq, Hkv, Sq, Sk):
+    A = 0x10000000
+    if call == "attn_fwd":
+        status = _lib().attn_fwd(A, A, A, A, A, B, Hq, Hkv, Sq, Sk, 64, 1, 0.1, None)
+    else:
+        status = _lib().attn_window_fwd(A, A, A, A, A, None, B, Hq, Hkv, Sq, Sk, 64, 10, 1, 1, 0.1, None)
+    assert status == UNS
