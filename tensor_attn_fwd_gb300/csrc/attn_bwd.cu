@@ -124,10 +124,14 @@ struct BwdParams {
   int* status;
   int B, Hq, Hkv, Sq, Sk, causal;
   float scale, scale_log2;
-  // Windowed kernels: the visibility of window.cuh, and bf16 gradients (out0, out1
-  // point at bf16).
+  // Named by code that the plain dQ kernel does not reach (BwdWindowParams has its own).
+  static constexpr int window = 0, sinks = 0;
+};
+// The windowed kernels': the visibility of window.cuh, and bf16 gradients (out0, out1 point
+// at bf16).
+struct BwdWindowParams : BwdParams {
   int window, sinks;
-  // Windowed dQ, which runs first: it computes Delta from O and dO for its tiles and
+  // dQ, which runs first: it computes Delta from O and dO for its tiles and
   // leaves it in delta_out for dK/dV.
   const __nv_bfloat16 *o, *dout;
   float* delta_out;
@@ -141,6 +145,10 @@ struct BwdParams {
   // which find their next tile between two, about as much as the forward's.)
   FixedDiv by_q_planes, by_kv_planes, by_group, by_parts;
 };
+// dQ's parameters.  (dK/dV takes the windowed ones in either form: as it is compiled, the
+// plain kernel is 0.6 to 1 % slower with the others.)
+template <Mask WIN>
+using DqArgs = ParamsOf<WIN, BwdParams, BwdWindowParams>;
 
 // Read-only global load issued where it stands in the program.
 __device__ __forceinline__ float ld_nc_f32(const float* ptr) {
@@ -384,7 +392,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmDO, const BwdParams p) {
+                    const __grid_constant__ CUtensorMap tmDO, const BwdWindowParams p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -399,7 +407,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // Work: key tile n of KV head (b, g); CTAs are numbered n-major so the
   // largest work (low n under a causal mask) is scheduled first.
   const int BH = p.B * p.Hkv;
-  int n = WIN ? p.by_kv_planes.div(blockIdx.x) : blockIdx.x / BH;
+  int n;
+  if constexpr (WIN)
+    n = p.by_kv_planes.div(blockIdx.x);
+  else
+    n = blockIdx.x / BH;
   const int bg = blockIdx.x - n * BH;
   int part = -1;  // windowed: this CTA's part of a split tile
   if constexpr (WIN) {
@@ -811,7 +823,7 @@ template <Mask WIN>
 struct DqTiles {
   int nsteps;
   TileRange r;
-  __device__ __forceinline__ DqTiles(const BwdParams& p, int m) {
+  __device__ __forceinline__ DqTiles(const DqArgs<WIN>& p, int m) {
     if constexpr (WIN) {
       r = window_kv_tiles(p.Sq, p.Sk, p.window, p.sinks, 128 * m);
       nsteps = r.count();
@@ -831,7 +843,7 @@ template <int D, Mask WIN = kNoWindow>
 __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV,
-                  const __grid_constant__ CUtensorMap tmDO, const BwdParams p) {
+                  const __grid_constant__ CUtensorMap tmDO, const DqArgs<WIN> p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -852,9 +864,14 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
   const int group = p.Hq / p.Hkv;
   // Query tile m of head bh (b * Hq + h) of item idx.
   auto tile_of = [&](int idx, int& m, int& bh) {
-    const int rank = WIN ? p.by_q_planes.div(idx) : idx / BH;
-    m = mtiles - 1 - rank;
-    bh = WIN ? idx - rank * BH : idx % BH;
+    if constexpr (WIN) {
+      const int rank = p.by_q_planes.div(idx);
+      m = mtiles - 1 - rank;
+      bh = idx - rank * BH;
+    } else {
+      m = mtiles - 1 - idx / BH;
+      bh = idx % BH;
+    }
   };
 
   if (threadIdx.x == 0) {
@@ -914,7 +931,11 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
       const DqTiles<WIN> tiles(p, m);
       const int nsteps = tiles.nsteps;
       if (nsteps == 0) continue;
-      const int bkv = WIN ? p.by_group.div(bh) : (bh / p.Hq) * p.Hkv + (bh % p.Hq) / group;
+      int bkv;  // b * Hkv + KV head
+      if constexpr (WIN)
+        bkv = p.by_group.div(bh);
+      else
+        bkv = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / group;
       // Q and dO of this tile once the previous tile's last S and dP are done.
       if (kt > 0 && !(ok = __all_sync(0xffffffffu, bwd_wait(&bars->q_empty, (kt - 1) & 1, bars))))
         break;
@@ -1033,35 +1054,37 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
     tc_commit_w(&bars->mma_done);
     (void)mbar_wait(&bars->mma_done, 0);
   } else if (WIN && warp >= kDqDeltaWarp) {
-    // Delta, a tile or two ahead of the gradient warps: 64 rows a warp, from global
-    // memory, to shared memory for them and to delta_out for dK/dV.  (By the gradient
-    // warps themselves, at a tile's start, the loads' latency cost more than a kernel
-    // of its own for Delta: 8192 rows, 32 heads, D = 128: 561 against 552 us a step.)
-    int kt = 0;
-    for (int rnd = 0; ok; ++rnd) {
-      const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
-      if (idx >= total) break;
-      int m, bh;
-      tile_of(idx, m, bh);
-      const int nsteps = DqTiles<WIN>(p, m).nsteps;
-      const int buf = kt & 1;
-      if (nsteps > 0 && kt >= 2) {
-        ok = __all_sync(0xffffffffu, bwd_wait(&bars->delta_free[buf], ((kt >> 1) - 1) & 1, bars));
-        if (!ok) break;
-      }
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const int r = 64 * (warp - kDqDeltaWarp) + 32 * i;
-        const long long row0 = static_cast<long long>(bh) * p.Sq + 128 * m + r;
-        const float dlt =
-            warp_delta<D>(p.o, p.dout, row0, static_cast<long long>(BH) * p.Sq, lane);
-        if ((nsteps == 0 || nsteps > kExactDeltaSteps) && 128 * m + r + lane < p.Sq)
-          p.delta_out[row0 + lane] = dlt;
-        if (nsteps > 0) sDelta[128 * buf + r + lane] = dlt;
-      }
-      if (nsteps > 0) {
-        mbar_arrive_warp(&bars->delta_full[buf]);
-        ++kt;
+    if constexpr (WIN) {
+      // Delta, a tile or two ahead of the gradient warps: 64 rows a warp, from global
+      // memory, to shared memory for them and to delta_out for dK/dV.  (By the gradient
+      // warps themselves, at a tile's start, the loads' latency cost more than a kernel
+      // of its own for Delta: 8192 rows, 32 heads, D = 128: 561 against 552 us a step.)
+      int kt = 0;
+      for (int rnd = 0; ok; ++rnd) {
+        const int idx = dq_tile_index(rnd, blockIdx.x, gridDim.x);
+        if (idx >= total) break;
+        int m, bh;
+        tile_of(idx, m, bh);
+        const int nsteps = DqTiles<WIN>(p, m).nsteps;
+        const int buf = kt & 1;
+        if (nsteps > 0 && kt >= 2) {
+          ok = __all_sync(0xffffffffu, bwd_wait(&bars->delta_free[buf], ((kt >> 1) - 1) & 1, bars));
+          if (!ok) break;
+        }
+  #pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int r = 64 * (warp - kDqDeltaWarp) + 32 * i;
+          const long long row0 = static_cast<long long>(bh) * p.Sq + 128 * m + r;
+          const float dlt =
+              warp_delta<D>(p.o, p.dout, row0, static_cast<long long>(BH) * p.Sq, lane);
+          if ((nsteps == 0 || nsteps > kExactDeltaSteps) && 128 * m + r + lane < p.Sq)
+            p.delta_out[row0 + lane] = dlt;
+          if (nsteps > 0) sDelta[128 * buf + r + lane] = dlt;
+        }
+        if (nsteps > 0) {
+          mbar_arrive_warp(&bars->delta_full[buf]);
+          ++kt;
+        }
       }
     }
     if (!ok) bwd_record(p.status);
@@ -1141,7 +1164,11 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
         mbar_arrive_warp(&bars->p_ready);
         // Keys 128s + 64*half + e are visible for e < n_vis (causal limit, Sk).
         const int key0 = 128 * tiles.kv_tile(s) + 64 * half;
-        const int n_vis = row_valid ? min(max(key_hi - key0 + 1, 0), 64) : 0;
+        int n_vis;  // (Written as in each form it measured best.)
+        if constexpr (WIN)
+          n_vis = row_valid ? min(max(key_hi - key0 + 1, 0), 64) : 0;
+        else
+          n_vis = row_valid ? min(max(key_hi - (128 * s + 64 * half) + 1, 0), 64) : 0;
         // Windowed: of those, only e < n_sink or e >= n_skip.
         const int n_sink = p.sinks - key0, n_skip = win_lo - key0;
         const bool need_mask =
@@ -1259,7 +1286,7 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
   }
 }
 
-// The sink tiles' parts (see BwdParams).  A key tile with sinks is seen by every
+// The sink tiles' parts (see BwdWindowParams).  A key tile with sinks is seen by every
 // later row, group * ceil(Sq/128) steps, where the others take about group *
 // (window/128 + 2): on one CTA it outlasts all of them (8192 rows, window 1024, 32/8
 // heads: 432 us for dK/dV, of which 0.4 of the CTAs' time was idle).  It is cut into
@@ -1309,7 +1336,7 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
                             static_cast<int>(C::kSmemDq + (WIN ? kDqDeltaBytes : 0)))) !=
       cudaSuccess)
     return e;
-  BwdParams p = {};
+  BwdWindowParams p = {};
   p.lse = lse;
   p.delta = delta;
   p.status = status;
@@ -1321,20 +1348,17 @@ cudaError_t launch_bwd_impl(const void* q, const void* k, const void* v, const v
   p.causal = causal;
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
-  p.window = window;
-  p.sinks = sinks;
-  p.split_tiles = 0;
-  p.parts = 1;
-  p.partials = nullptr;
-  p.o = static_cast<const __nv_bfloat16*>(WIN ? o : nullptr);
-  p.dout = static_cast<const __nv_bfloat16*>(dout);
-  p.delta_out = delta;
   const int q_tiles = B * Hq * ((Sq + 127) / 128);
   const int q_ctas = q_tiles < sm_count() ? q_tiles : sm_count();
   const int kv_tiles = (Sk + 127) / 128;
   if constexpr (WIN) {
     // dQ first (it computes Delta), each kernel the programmatic dependent of the last.
     const SinkSplit split = sink_split(B, Hq, Hkv, Sq, Sk, window, sinks);
+    p.window = window;
+    p.sinks = sinks;
+    p.o = static_cast<const __nv_bfloat16*>(o);
+    p.dout = static_cast<const __nv_bfloat16*>(dout);
+    p.delta_out = delta;
     p.split_tiles = split.tiles;
     p.parts = split.parts;
     p.partials = delta + window_bwd_delta_floats(B, Hq, Sq);

@@ -158,12 +158,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int grp = lane >> 2;  // MMA group: rows grp and grp + 8
   const int tq = lane & 3;    // thread in group
   uint64_t* my_full = full + warp * kSlots;
-  if (lane == 0) {
+  auto init_barriers = [&] {
+    if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) mbar_init(&my_full[s], 1);
-    fence_mbar_init();
-  }
+      for (int s = 0; s < kSlots; ++s) mbar_init(&my_full[s], 1);
+      fence_mbar_init();
+    }
+  };
   if constexpr (WIN) {
+    init_barriers();
     if (threadIdx.x == 0) {
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
@@ -194,6 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
   uint8_t* my_ring = ring + size_t(warp) * kSlots * C::kSlotBytes;
   int* my_pids = pids + warp * kPidBlocks;
+  if constexpr (!WIN) init_barriers();  // (beside the load of the length)
   // Page id of a block (key0 is a multiple of 32 and page_size of 32: the
   // block lies inside one page); a bad table entry is reported and page 0 read.
   auto slot_of = [&](int key0) { return WIN ? by_page.div(key0) : key0 / page_size; };

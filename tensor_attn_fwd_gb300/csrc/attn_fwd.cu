@@ -114,12 +114,20 @@ struct FwdParams {
   int split_tiles;   // KV tiles per split
   size_t split_stride_o, split_stride_lse;
   int total_items;   // B * Hq * num_pairs * num_splits (B * Hq / 2 * num_splits in pairs)
-  int window, sinks;  // windowed kernels: row at position p sees (p - window, p] and [0, sinks)
-  WindowOrder order;  // windowed kernels: the items
+  // Named by code that the plain kernels do not reach (FwdWindowParams has its own).
+  static constexpr int window = 0, sinks = 0, part_v8 = 0;
+  static constexpr float *part_o = nullptr, *part_lse = nullptr;
+  static constexpr size_t part_o_bytes = 0, part_lse_bytes = 0;
+};
+struct FwdWindowParams : FwdParams {
+  int window, sinks;  // row at position p sees (p - window, p] and [0, sinks)
+  WindowOrder order;  // the items
   float *part_o, *part_lse;  // ... and the fp32 partials of those that are split (WindowRows)
   int part_v8;
   size_t part_o_bytes, part_lse_bytes;
 };
+template <Mask WIN>
+using FwdArgs = ParamsOf<WIN, FwdParams, FwdWindowParams>;
 
 // A work item is two 128-row query tiles that stream the same K/V: rows
 // [256i, 256i+128) and [256i+128, 256i+256) of one query head, or, when
@@ -152,7 +160,7 @@ __device__ __forceinline__ int next_tile(const Item& it, int j) {
 // query heads per KV head an item is one 128-row tile of two heads: both tiles
 // then need the same KV tiles.  Otherwise it is 256 rows of one head, whose tiles
 // differ by one KV tile at either end.
-__device__ __forceinline__ Item get_window_item(const FwdParams& p, int idx) {
+__device__ __forceinline__ Item get_window_item(const FwdWindowParams& p, int idx) {
   const WindowItem w = p.order.item(idx);
   Item it;
   it.split = w.split;
@@ -216,7 +224,7 @@ __device__ __forceinline__ int tile_bh(const FwdParams& p, const Item& it, int t
 //            that the heads in flight stay in L2 (the D = 256 kernel's ORDER 2)
 //            measured -3 to +3 % here, so causal launches keep ORDER 0.
 template <int ORDER, Mask WIN>
-__device__ __forceinline__ Item get_item(const FwdParams& p, int idx) {
+__device__ __forceinline__ Item get_item(const FwdArgs<WIN>& p, int idx) {
   if constexpr (WIN) return get_window_item(p, idx);
   const int BH = p.B * p.Hq;
   Item it;
@@ -284,7 +292,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* 
 // ------------------------------------------------------------------ producer
 template <int D, int ORDER, Mask WIN>
 __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                          const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* bars) {
+                          const FwdArgs<WIN>& p, uint8_t* sQ, uint8_t* sKV, Bars* bars) {
   using C = Cfg<D>;
   const int group = p.Hq / p.Hkv;
   uint32_t kv_ctr = 0, q_ctr = 0;
@@ -380,7 +388,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
 
 // ------------------------------------------------------------------ MMA issuer
 template <int D, int ORDER, Mask WIN>
-__device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* bars,
+__device__ void mma_role(const FwdArgs<WIN>& p, uint8_t* sQ, uint8_t* sKV, Bars* bars,
                          uint32_t tmem) {
   using C = Cfg<D>;
   // Descriptor words: the high word is fixed per operand kind, the low word is
@@ -523,7 +531,8 @@ __device__ void mma_role(const FwdParams& p, uint8_t* sQ, uint8_t* sKV, Bars* ba
 
 // ------------------------------------------------------------------ softmax
 template <int D, int ORDER, Mask WIN>
-__device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int warp, int lane) {
+__device__ void softmax_role(const FwdArgs<WIN>& p, Bars* bars, uint32_t tmem, int warp,
+                             int lane) {
   using C = Cfg<D>;
   const int t = warp >> 2;
   const int quad = warp & 3;
@@ -556,9 +565,11 @@ __device__ void softmax_role(const FwdParams& p, Bars* bars, uint32_t tmem, int 
     const size_t lse_bytes = part ? p.part_lse_bytes : p.lse_bytes;
     const int o_v8 = part ? p.part_v8 : p.o_v8;
     size_t at = static_cast<size_t>(bh) * p.Sq + row;
-    if (part)
-      at = (static_cast<size_t>(it.split) * p.order.rem + it.slot) * kRowsPerItem + 128 * t +
-           quad * 32 + lane;
+    if constexpr (WIN) {
+      if (part)
+        at = (static_cast<size_t>(it.split) * p.order.rem + it.slot) * kRowsPerItem + 128 * t +
+             quad * 32 + lane;
+    }
     const size_t o_off =
         WIN ? at * D : at * D + static_cast<size_t>(it.split) * p.split_stride_o;
     float* o_row = static_cast<float*>(o_base) + o_off;
@@ -783,7 +794,7 @@ template <int D, int ORDER, Mask WIN = kNoWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
+                    const __grid_constant__ CUtensorMap tmV, const FwdArgs<WIN> p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -915,7 +926,7 @@ cudaError_t launch_window_impl(const void* q, const void* k, const void* v, void
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel),
                                          static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;
-  FwdParams p = {};
+  FwdWindowParams p = {};
   p.o = o;
   p.o_bf16 = 1;
   p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;

@@ -7,6 +7,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -181,6 +182,12 @@ __device__ __forceinline__ TileRange tile_union(const TileRange& x, const TileRa
 // chunk against a longer sequence), which have to be kept from the products; the work
 // for it in the MMA warp's loop costs a training step, which has none, 2.4 %.
 enum Mask { kNoWindow = 0, kWindow = 1, kUnseen = 2 };
+// A kernel's parameters: the windowed kernels' have members more.  The plain ones read none
+// of them, but a longer parameter block alone changes what the compiler makes of a kernel:
+// where it cost something (the plain dQ kernel 2 to 4 %, with 134 registers for 140; the
+// forward of D <= 128 0.3 to 1 %) the plain form is not given them.
+template <Mask WIN, typename Plain, typename Windowed>
+using ParamsOf = std::conditional_t<WIN == kNoWindow, Plain, Windowed>;
 
 // Keys [sinks, unseen_end) are seen by no row: the first row's window starts at
 // unseen_end.
