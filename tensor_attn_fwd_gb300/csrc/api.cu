@@ -291,6 +291,9 @@ int attn_window_fwd_num_splits(int B, int Hq, int Hkv, int Sq, int Sk, int D, in
   // D = 256, where an item is one tile of a head, measured alike: 16/4 heads, Sq 512, 34
   // tiles: 1 56.0, 2 36.9, 3 50.0; Sq 128: 7 20.6, 8 22.3; 32 items of 4 tiles: 1 12.3,
   // 2 13.6; 24 items of 34: 6 22.1, 7 30.7.
+  // D = 64, whose step takes about 1200, 32/8 heads: Sq 512, 34 tiles: 1 45.9, 2 31.7, 3
+  // 40.6; Sq 512, 10 tiles: 1 17.5, 2 17.3; Sq 128, 34 tiles: 6 16.9, 8 16.2, 12 20.6; Sq 1280:
+  // 2 72.6, 8 60.2, 12 58.9, 16 60.0.  The rule takes 2, 2, 9 and 17: the same estimate serves.
   const long long rows = 1ll * order.rem * window_item_rows(D), all = 1ll * B * Hq * Sq;
   const long long partial_ns = 2 * (rows < all ? rows : all) * D * 4 / 5000;  // of one split
   long long best_ns = tiles * 1400 + 3500;

@@ -1144,8 +1144,9 @@ __global__ void __launch_bounds__(WIN ? kDqWinThreads : kBwdThreads, 1)
       // keys shows: at a window of 8 dQ and dK are 2.7e-3 off, 1.63 times what their own
       // rounding alone would make, and still 1.5 times at 64.  So where a tile has few
       // steps (and windows are that short) sum_j P dP, which is Delta, is added up on
-      // the way: the last step, which holds most of such a row's keys, and dK/dV use it.
-      // (2.4e-3 then, at each window.)
+      // the way: dK/dV uses it, and here the last step, which holds most keys of the
+      // tile's later rows.  (2.4e-3 then, at each window.)  The steps before it, which
+      // hold most keys of its first rows, keep the Delta from O.
       const bool exact = WIN && nsteps <= kExactDeltaSteps;
       uint64_t p_dp = f2_pack(0.f, 0.f);
       const int key_hi = WIN || p.causal ? min(p.Sk - 1, row + p.Sk - p.Sq) : p.Sk - 1;

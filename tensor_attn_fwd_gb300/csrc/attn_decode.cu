@@ -26,7 +26,8 @@
 // The windowed instantiations read only the 32-key blocks that hold a key within a
 // sliding window or a sink, write a bf16 O, and merge the splits of a group in a
 // thread-block cluster.  HBM-bound with many rows (64 rows, window 4096: 156 us, the
-// copy's rate), latency-bound with one (window 1024: 6.2 us).
+// copy's rate), latency-bound with one (window 1024: 6.2 us, 6.5 over pages).  At D = 256
+// this form spills 16 bytes of its 255 registers (the plain one 4).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // the sequence lengths, the partials a previous combine may still read) is
   // touched before the previous kernel in the stream has completed.
   // (Windowed: the set-up below, which touches none, comes first; 6.8 -> 6.6 us for one
-  // row of 1028 keys, with the divisions below as multiplications.  An early start of
+  // row of 1028 keys over pages, with the divisions below as multiplications.  An early start of
   // the next kernel measured 6.3 there, but up to 6 % slower with 100 to 300 CTAs.)
   if constexpr (!WIN) grid_dependency_wait();
 
@@ -366,9 +367,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       consumed = li + 1;
       const uint32_t vb = smem_u32(my_ring + slot * C::kSlotBytes);
       if (partial) {
-        // Rows outside the window, and rows past the block's last key are real keys of another split, zero
-        // fill past Sk, or (with per-sequence lengths) unwritten cache memory
-        // that may hold NaN/Inf: zero them so that p = 0 contributes nothing.
+        // Rows past the block's last key (real keys of another split, zero fill past Sk
+        // or, with per-sequence lengths, unwritten cache memory) and rows outside the
+        // window may hold NaN/Inf: zero them so that p = 0 contributes nothing.
         uint8_t* vrow = my_ring + slot * C::kSlotBytes;
         const int r0 = WIN ? 0 : nvalid;
         for (int idx = lane; idx < (kBlk - r0) * 8 * C::kSub; idx += 32) {
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // Windowed: a group's splits are the CTAs of one cluster and read each other's
   // partials from shared memory (attn_combine's formula, splits in order): no
   // workspace, and no round trips to L2 for counter and partials.  B1, 32/8 heads, 1024
-  // + 4 keys in 12 splits: 6.2 us, through L2 9.0.
+  // + 4 keys of a contiguous cache in 12 splits: 6.2 us, through L2 9.0.
   if constexpr (WIN) {
     if (num_splits > 1) {
       constexpr float kLog2e = 1.4426950408889634f;

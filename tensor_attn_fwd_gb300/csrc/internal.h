@@ -156,7 +156,7 @@ int decode_check_args(const void* q, const void* k, const void* v, int B, int Hq
 // 16-head slice) group last also combines the group's partials into o / lse
 // (counters: int32 [B * Hkv * ceil((Hq/Hkv)/16)], zero on entry, zero again after).
 struct FusedCombine {
-  void* o;  // fp32
+  void* o;  // fp32 (bf16 from the windowed kernel, which has no counters)
   float* lse;
   int* counters;
 };

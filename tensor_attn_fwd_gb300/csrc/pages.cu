@@ -25,11 +25,17 @@
 //   a cooperative grid of 1024 elements a CTA, at most one CTA an SM: 128 x 128, 16000
 //     14.0 / 9.7 / 4.9; 256 x 128, 30000 14.3 / 10.2 / 5.0; 256 x 256, 60000 14.1 / 10.3
 //     / 5.0; 1024 x 2048, 2 M 44.5 / 35.6 / 11.0 (a launch per phase: 64.4 / 52.0 / 12.5).
-//     Bound there by the L2's rate of scattered 4-byte atomics.
+//     Bound there by the L2's rate of scattered 4-byte atomics.  (Free grows with what is
+//     given up: of 2 M entries none 8.2, half 11.7, 1.4 M 14.5, nearly all 15.9, and 16 to
+//     18 with inputs that are not in L2.)
 // The forms were compared with divisions in fork.  As multiplications they save it 0.4 to
 // 1.5 us up to 2^20 slots (8 x 48 4.5, 32 x 64 5.8, 64 x 64 7.7, 256 x 128 12.4, 1024 x
 // 512 with 500000 pages 18.6); from 2^21 on it takes 8 % longer (48.0), the atomics
 // meeting in denser bursts.
+// All of the above before fork looked up whether each entry's page has holders
+// (old_entry): with that, on inputs of its own, 8 x 48 4.5, 32 x 64 6.0, 64 x 64 8.1, 128 x
+// 128 10.9, 256 x 128 13.2, 256 x 256 13.4, 1024 x 512 25, 1024 x 2048 56 to 62; without
+// it 4.5, 6.0, 8.0, 10.8, 13.0, 13.2, 23, 53.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
