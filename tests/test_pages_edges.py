@@ -6,7 +6,7 @@ import torch
 
 import tensor_attn_fwd_gb300 as attn
 
-from test_pages import A, A2, A3, UNS, c_fork, cache_tables, gpu, plain_fork, plain_free, same  # noqa: F401
+from test_pages import UNS, c_fork, cache_tables, gpu, plain_fork, plain_free, same
 
 
 # ------------------------------------------------------------------ limits (no GPU)
