@@ -49,7 +49,8 @@ typedef enum {
     ATTN_ERR_TIMEOUT = 5,      /* a kernel's bounded wait expired (device status) */
     ATTN_ERR_BOUNDS = 6,       /* debug builds (-DATTN_DEBUG_BOUNDS): a kernel skipped a
                                   store outside its output buffer (device status) */
-    ATTN_ERR_NO_PAGES = 7      /* attn_pages_fork ran out of free pages (device status) */
+    ATTN_ERR_NO_PAGES = 7      /* attn_pages_fork or attn_pages_append ran out of free pages
+                                  (device status) */
 } attn_status;
 
 /*
@@ -553,6 +554,164 @@ ATTN_API int attn_pages_workspace(int num_pages, int R, long long *entries);
  */
 ATTN_API int attn_pages_copy(void *k_cache, void *v_cache, const int *src, const int *dst, int n,
                              int num_pages, long long page_bytes, void *stream);
+
+/*
+ * A serving step over a paged cache: a batch of requests with some new tokens each (a
+ * chunk of a prompt, or one generated token), packed request after request.  The calls
+ * of a step, in order, none of which reads anything back to the host:
+ *   attn_pages_append   pages for the new tokens; each token's position and cache slot
+ *   attn_chunk_plan     how the GPU shares out the attention (one plan for all layers)
+ *   per layer: a projection of the caller's, then
+ *     attn_rope_append  rotary positions on its queries and keys; keys and values to
+ *                       their slots
+ *     attn_chunk_paged  the new tokens' attention over the pages
+ * The pages that the other entry points cite print none of this; the rules are stated here
+ * in full.
+ */
+
+/*
+ * Pages, positions and slots for a step's new tokens.  Row b (block_table, refs, seqlens as
+ * attn_pages_fork) has seqlens[b] keys and gets new_lens[b] more.  Its slots of the table
+ * that hold new keys and name no page get free pages (refs = 0), lowest id first in the
+ * order of (row, slot), which count one holder then; entries that are there (reserved by
+ * attn_pages_fork) are kept as they are: rows that share a page to be written have to be
+ * forked first.
+ *   A row takes all its tokens or none.  Rows take none when the pages needed up to and
+ *   with theirs exceed the free ones (ATTN_ERR_NO_PAGES in the status word), when their
+ *   keys would exceed max_pages * page_size or their tokens T (ATTN_ERR_INVALID_ARG in the
+ *   status word), and finished rows (seqlens < 0).  They keep their length and entries, and
+ *   their tokens have slot -1.  A negative new_lens sets ATTN_ERR_INVALID_ARG in the status
+ *   word and counts as 0.
+ *
+ *   new_lens [B]; T: tokens of the step, at least the sum of new_lens
+ *   block_table_out [B,max_pages], refs_out [num_pages], seqlens_out [B] (the lengths
+ *     with the tokens taken); each may be its input
+ *   cu_tokens [B+1]: row b's tokens are cu_tokens[b] to cu_tokens[b+1] of the packed
+ *     ones, whether it takes them or not (at most T)
+ *   positions [T], slots [T]: token i of row b stands at p = seqlens[b] + i, in slot
+ *     block_table_out[b][p / page_size] * page_size + p % page_size of the cache.  Tokens
+ *     that are not taken, and those behind the last row's, have position 0 and slot -1.
+ *   counts [2]: pages needed and pages free
+ *   workspace: attn_pages_append_workspace(num_pages, B) int32, contents undefined
+ *   Entries, alignment and limits as the other page calls; num_pages * page_size < 2^31.
+ */
+ATTN_API int attn_pages_append(const int *block_table, const int *refs, const int *seqlens,
+                               const int *new_lens, int *block_table_out, int *refs_out,
+                               int *seqlens_out, int *cu_tokens, int *positions, int *slots,
+                               int *counts, int *workspace, int B, int T, int max_pages,
+                               int num_pages, int page_size, void *stream);
+
+/* int32 entries of workspace for attn_pages_append.  Host-only.  ATTN_ERR_INVALID_ARG for
+ * num_pages < 1, B < 1 or a NULL result. */
+ATTN_API int attn_pages_append_workspace(int num_pages, int B, long long *entries);
+
+/*
+ * Rotary-embedding table whose frequencies are scaled for contexts longer than those a
+ * model was trained on, and for rotating the first R dims of a head.
+ *   theta_i = base^(-2i/R), 0 <= i < R/2, is multiplied by k_i + (1 - k_i) / factor:
+ *     original_pos = 0: k_i = 0, every frequency divided by factor (positions interpolated)
+ *     original_pos > 0: k_i = (r_i - low) / (high - low) clamped to [0, 1], where r_i =
+ *       original_pos * theta_i / (2 pi) is the turns that dim makes in the original
+ *       context (interpolated by parts: fast dims keep their frequency)
+ *   table [max_pos, R/2, 2] fp32 as attn_rope_table's: amplitude * (cos, sin) of p times the
+ *     scaled frequency, computed in double precision and rounded once
+ *   factor = 1, amplitude = 1 is attn_rope_table(max_pos, R, base).  factor > 0, amplitude >
+ *   0, 0 <= low < high, R even, base > 1, all finite.
+ */
+ATTN_API int attn_rope_table_scaled(float *table, int max_pos, int R, float base, float factor,
+                                    float low, float high, int original_pos, float amplitude,
+                                    void *stream);
+
+/*
+ * Rotary positions between a projection and the attention layout, for projections that
+ * attn_qkv_rope does not compute (with a bias, adapters, quantised weights), rotating the
+ * first R dims of each query and key head.
+ *   qkv row t = b*S + s begins at qkv + t * ld elements: Hq query heads, Hkv key heads, Hkv
+ *     value heads of D dims, bf16; ld >= (Hq + 2*Hkv)*D, a multiple of 8
+ *   rope_table [max_pos, R/2, 2]; positions [B*S] or NULL, style 0 or 1: as attn_qkv_rope,
+ *     of pairs (2i, 2i+1) or (i, i + R/2) of the first R dims
+ *   q [B,Hq,S,D], k, v [B,Hkv,S,D] bf16, rounded to nearest even once; dims from R on, and
+ *     values, are copied
+ *   D in {64, 128, 256}; R a multiple of 16 (else ATTN_ERR_UNSUPPORTED), R <= D.  Pointers
+ *   16-byte aligned (positions 4-byte).  Outputs may not overlap inputs.
+ */
+ATTN_API int attn_rope_split(const void *qkv, long long ld, const float *rope_table,
+                             const int *positions, void *q, void *k, void *v, int B, int S, int Hq,
+                             int Hkv, int D, int R, int max_pos, int style, void *stream);
+
+/*
+ * The gradient of attn_rope_split: dqkv (bf16, rows of ld elements; those behind the
+ * heads are not written) from dq [B,Hq,S,D], dk, dv [B,Hkv,S,D], bf16 (as attn_window_bwd
+ * writes them) or with fp32 = 1 fp32 (as attn_bwd).  Pairs are turned back (the transposed
+ * map: a table with an amplitude multiplies by it again).
+ */
+ATTN_API int attn_rope_split_bwd(const void *dq, const void *dk, const void *dv, int fp32,
+                                 const float *rope_table, const int *positions, void *dqkv,
+                                 long long ld, int B, int S, int Hq, int Hkv, int D, int R,
+                                 int max_pos, int style, void *stream);
+
+/*
+ * attn_rope_split's rotation for the packed tokens of a step, whose keys and values go to
+ * their slots of a paged cache.
+ *   qkv [T] rows of ld elements; positions, slots device int32 [T] (attn_pages_append)
+ *   q [T,Hq,D] bf16
+ *   k_cache, v_cache [num_pages,Hkv,page_size,D] bf16: token t's are written to row slots[t] %
+ *     page_size of page slots[t] / page_size; slot -1: nowhere.  No slot may appear twice (its
+ *     contents would be either token's).  Any other slot outside the cache is skipped and
+ *     sets ATTN_ERR_INVALID_ARG in the status word.
+ *   Other arguments, conditions and errors as attn_rope_split; num_pages * page_size < 2^31.
+ */
+ATTN_API int attn_rope_append(const void *qkv, long long ld, const float *rope_table,
+                              const int *positions, const int *slots, void *q, void *k_cache,
+                              void *v_cache, int T, int Hq, int Hkv, int D, int R, int max_pos,
+                              int num_pages, int page_size, int style, void *stream);
+
+/*
+ * Plan of a step's attention (attn_chunk_paged), from the requests' lengths on the device.
+ *   cu_tokens [B+1], seqlens [B] device int32: request b's new tokens are cu_tokens[b] to
+ *     cu_tokens[b+1] of the T packed ones, and it has seqlens[b] keys, theirs included
+ *     (both as attn_pages_append writes them; seqlens are clamped to [0, max_keys])
+ *   Token i of request b, of n_b, stands at p = seqlens[b] - n_b + i and sees key j iff
+ *     j <= p  and  (j > p - window  or  j < sinks)      (window >= max_keys: all up to p)
+ *   max_keys: max_pages * page_size of the table that the plan is used with
+ *   plan: attn_chunk_plan_size int32, 16-byte aligned; contents undefined before, and of
+ *     this library's own form after.  It is for calls with these B, T, Hq, Hkv, D and
+ *     max_keys on this kind of device, and holds the lengths' values.
+ *   Bounds that do not ascend within [0, T] set ATTN_ERR_INVALID_ARG in the status word; such
+ *     a request has no tokens (or, where requests overlap too often, none has).
+ *   D in {64, 128}; at most 2^31 - 1 rows T * Hq (else ATTN_ERR_UNSUPPORTED).
+ */
+ATTN_API int attn_chunk_plan(const int *cu_tokens, const int *seqlens, int *plan, int B, int T,
+                             int Hq, int Hkv, int D, int max_keys, int window, int sinks,
+                             void *stream);
+
+/* int32 entries of a plan on the current device.  Host-only.  Errors as attn_chunk_plan. */
+ATTN_API int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long long *entries);
+
+/*
+ * Attention of a step's new tokens over a paged cache, as its plan says.
+ *   q [T,Hq,D] bf16 (attn_rope_append); k_cache, v_cache, block_table as
+ *     attn_decode_splitkv_paged.  The new tokens' keys and values have to be in the cache.
+ *   o [T,Hq,D] bf16 (rounded once from fp32), lse [T,Hq] fp32.  A token that sees no key (p <
+ *     0: more new tokens than keys) gets O = 0 and LSE = -inf.  Tokens behind the last
+ *     request's are left as they were.
+ *   workspace: attn_chunk_workspace floats, caller-owned, contents undefined
+ *   Table entries of pages that hold no seen key are not read and may be anything.  Keys
+ *     that no token sees may hold anything; K and V have to be finite at keys that some
+ *     token sees (attn_window_fwd).  A bad entry that is read sets ATTN_ERR_INVALID_ARG in
+ *     the status word and reads page 0.
+ *   A plan of other sizes sets ATTN_ERR_INVALID_ARG in the status word and writes nothing.
+ *   num_pages * Hkv * page_size < 2^31 - 256 (else ATTN_ERR_UNSUPPORTED).  All pointers
+ *   16-byte aligned (block_table 4-byte); other conditions as attn_decode_splitkv_paged.
+ */
+ATTN_API int attn_chunk_paged(const void *q, const void *k_cache, const void *v_cache,
+                              const int *block_table, const int *plan, void *o, float *lse,
+                              float *workspace, int B, int T, int Hq, int Hkv, int num_pages,
+                              int page_size, int max_pages, int D, float scale, void *stream);
+
+/* Floats of workspace for attn_chunk_paged on the current device.  Host-only.
+ * ATTN_ERR_INVALID_ARG for a NULL result, ATTN_ERR_UNSUPPORTED for other D. */
+ATTN_API int attn_chunk_workspace(int D, long long *floats);
 
 /* Human-readable name of a status code (static string, never NULL). */
 ATTN_API const char *attn_status_string(int status);

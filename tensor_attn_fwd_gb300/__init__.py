@@ -28,6 +28,14 @@ Names follow the C ABI:
                             -> (block_table, refs, seqlens, src, dst, counts)
     attn_pages_compact(block_table, refs) -> (block_table, refs, src, dst, num_live)
     attn_pages_copy(k_cache, v_cache, src, dst)
+    attn_pages_append(block_table, refs, seqlens, new_lens, tokens, page_size)
+                            -> (block_table, refs, seqlens, cu_tokens, positions, slots, counts)
+    attn_rope_table_scaled(max_pos, R, base, factor, ...) -> (cos, sin) table
+    attn_rope_split(qkv, table, Hq, Hkv)        -> (q, k, v) bf16, RoPE applied
+    attn_rope_split_bwd(dq, dk, dv, table)      -> dqkv bf16
+    attn_rope_append(qkv, table, positions, slots, k_cache, v_cache, Hq) -> q bf16
+    attn_chunk_plan(cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks) -> plan
+    attn_chunk_paged(q, k_cache, v_cache, block_table, plan) -> (o bf16, lse)
 Layouts: Q [B,Hq,Sq,D], K/V [B,Hkv,Sk,D] bf16; O [B,Hq,Sq,D], LSE [B,Hq,Sq] fp32.
 """
 from __future__ import annotations
@@ -47,6 +55,8 @@ __all__ = ["AttnError", "attn_fwd", "attn_fwd_bf16o", "attn_decode_splitkv", "at
            "ATTN_ERR_CUDA", "ATTN_ERR_TIMEOUT", "ATTN_ERR_BOUNDS", "attn_wait_selftest", "attn_fwd_splitkv", "attn_fwd_num_splits",
            "attn_window_fwd", "attn_window_bwd", "decode_window", "decode_window_paged",
            "attn_pages_free", "attn_pages_fork", "attn_pages_compact", "attn_pages_copy",
+           "attn_pages_append", "attn_rope_table_scaled", "attn_rope_split", "attn_rope_split_bwd",
+           "attn_rope_append", "attn_chunk_plan", "attn_chunk_paged",
            "ATTN_ERR_NO_PAGES"]
 
 ATTN_OK = 0
@@ -101,6 +111,17 @@ _SIGNATURES = {
     "attn_pages_compact": ([_vp] * 8 + [_int] * 3 + [_vp], _int),
     "attn_pages_workspace": ([_int, _int, ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_pages_copy": ([_vp] * 4 + [_int, _int, ctypes.c_longlong, _vp], _int),
+    "attn_pages_append": ([_vp] * 12 + [_int] * 5 + [_vp], _int),
+    "attn_pages_append_workspace": ([_int, _int, ctypes.POINTER(ctypes.c_longlong)], _int),
+    "attn_rope_table_scaled": ([_vp, _int, _int, _flt, _flt, _flt, _flt, _int, _flt, _vp], _int),
+    "attn_rope_split": ([_vp, ctypes.c_longlong] + [_vp] * 5 + [_int] * 8 + [_vp], _int),
+    "attn_rope_split_bwd": ([_vp] * 3 + [_int] + [_vp] * 3 + [ctypes.c_longlong] + [_int] * 8 + [_vp],
+                            _int),
+    "attn_rope_append": ([_vp, ctypes.c_longlong] + [_vp] * 6 + [_int] * 9 + [_vp], _int),
+    "attn_chunk_plan": ([_vp] * 3 + [_int] * 8 + [_vp], _int),
+    "attn_chunk_plan_size": ([_int] * 5 + [ctypes.POINTER(ctypes.c_longlong)], _int),
+    "attn_chunk_paged": ([_vp] * 8 + [_int] * 8 + [_flt, _vp], _int),
+    "attn_chunk_workspace": ([_int, ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_status_string": ([_int], ctypes.c_char_p),
     "attn_debug_status": ([_vp], _int),
     "attn_wait_selftest": ([ctypes.c_ulonglong, _vp, _vp], _int),
@@ -864,3 +885,129 @@ def attn_pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Ten
     if stream is not None:
         return _on_stream(stream, call, k_cache, v_cache, src, dst)
     return call(k_cache, v_cache, src, dst)
+
+
+# ---------------------------------------------------------------- a serving step
+def attn_pages_append(block_table: torch.Tensor, refs: torch.Tensor, seqlens: torch.Tensor,
+                      new_lens: torch.Tensor, tokens: int, page_size: int,
+                      block_table_out: torch.Tensor | None = None,
+                      refs_out: torch.Tensor | None = None,
+                      seqlens_out: torch.Tensor | None = None, stream=None):
+    """Pages, positions and slots for a step's new tokens; returns (block_table, refs,
+    seqlens, cu_tokens [B+1], positions [tokens], slots [tokens], counts [2]).
+
+    Row b, of seqlens[b] keys, gets new_lens[b] (int32 [B]) more; its slots that hold them and
+    have no page get free pages, lowest id first.  ``tokens`` is the length of the packed
+    token arrays, at least the sum of new_lens (the rest: position 0, slot -1).  A row
+    takes all its tokens or none: without enough free pages (attn_debug_status then
+    reports ATTN_ERR_NO_PAGES; counts holds the pages needed and free) or finished
+    (negative seqlens) it keeps its length, and its tokens have slot -1.  A token's slot is
+    page * page_size + its place in the page.  The ``..._out`` tensors may be the
+    inputs; the other results share one allocation.
+    """
+    call = (_fast or _native()).pages_append
+    args = (block_table, refs, seqlens, new_lens, tokens, page_size, block_table_out, refs_out,
+            seqlens_out)
+    return call(*args) if stream is None else _on_stream(stream, call, *args)
+
+
+def attn_rope_table_scaled(max_pos: int, R: int, base: float = 10000.0, factor: float = 1.0,
+                           low: float = 0.0, high: float = 1.0, original_pos: int = 0,
+                           amplitude: float = 1.0, device=None,
+                           out: torch.Tensor | None = None, stream=None):
+    """(cos, sin) table [max_pos, R/2, 2] fp32 for the first R dims of a head, its
+    frequencies scaled for long contexts.
+
+    theta_i = base^(-2i/R) is divided by ``factor``, or with ``original_pos`` multiplied by
+    k + (1 - k) / factor, k = clamp((r - low) / (high - low), 0, 1), where r is the turns
+    that the dim makes in the original context: fast dims keep their frequency.
+    ``amplitude`` multiplies the entries.
+    """
+    if out is None:
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        out = torch.empty((int(max_pos), int(R) // 2, 2), dtype=torch.float32, device=dev)
+    _check(out.is_cuda and out.dtype == torch.float32 and out.is_contiguous()
+           and tuple(out.shape) == (int(max_pos), int(R) // 2, 2),
+           "out must be a contiguous float32 CUDA tensor [max_pos, R/2, 2]")
+    lib = load_library()
+    with torch.cuda.device(out.device):
+        st = lib.attn_rope_table_scaled(out.data_ptr(), int(max_pos), int(R), float(base),
+                                        float(factor), float(low), float(high), int(original_pos),
+                                        float(amplitude), _stream_handle(stream))
+    _raise_if(st, "attn_rope_table_scaled")
+    return out
+
+
+def attn_rope_split(qkv: torch.Tensor, rope_table: torch.Tensor, Hq: int, Hkv: int,
+                    positions: torch.Tensor | None = None, style: int = 0,
+                    q: torch.Tensor | None = None, k: torch.Tensor | None = None,
+                    v: torch.Tensor | None = None, stream=None):
+    """Projected rows to attention inputs, rotary positions applied; returns bf16
+    q [B,Hq,S,D], k and v [B,Hkv,S,D].
+
+    qkv [B,S,(Hq+2*Hkv)*D] bf16 (its rows may be parts of longer ones); rope_table
+    [max_pos, R/2, 2] rotates the first R dims of the query and key heads; positions int32
+    with B*S entries (default: s); style as attn_qkv_rope.
+    """
+    call = (_fast or _native()).rope_split
+    args = (qkv, rope_table, Hq, Hkv, positions, style, q, k, v)
+    return call(*args) if stream is None else _on_stream(stream, call, *args)
+
+
+def attn_rope_split_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
+                        rope_table: torch.Tensor, positions: torch.Tensor | None = None,
+                        style: int = 0, dqkv: torch.Tensor | None = None, stream=None):
+    """Gradient of attn_rope_split: dqkv [B,S,(Hq+2*Hkv)*D] bf16 from dq [B,Hq,S,D], dk and dv
+    [B,Hkv,S,D], all bf16 (attn_window_bwd) or all fp32 (attn_bwd)."""
+    call = (_fast or _native()).rope_split_bwd
+    args = (dq, dk, dv, rope_table, positions, style, dqkv)
+    return call(*args) if stream is None else _on_stream(stream, call, *args)
+
+
+def attn_rope_append(qkv: torch.Tensor, rope_table: torch.Tensor, positions: torch.Tensor,
+                     slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, Hq: int,
+                     style: int = 0, q: torch.Tensor | None = None, stream=None):
+    """Rotary positions on a step's projected tokens, whose keys and values go to their
+    slots of the caches; returns q [T,Hq,D] bf16.
+
+    qkv [T,(Hq+2*Hkv)*D] bf16 (its rows may be parts of longer ones); positions and slots
+    int32 [T] (attn_pages_append; slot -1: nowhere); caches [num_pages,Hkv,page_size,D].
+    """
+    call = (_fast or _native()).rope_append
+    args = (qkv, rope_table, positions, slots, k_cache, v_cache, Hq, style, q)
+    return call(*args) if stream is None else _on_stream(stream, call, *args)
+
+
+def attn_chunk_plan(cu_tokens: torch.Tensor, seqlens: torch.Tensor, tokens: int, Hq: int, Hkv: int,
+                    D: int, max_keys: int, window: int | None = None, sinks: int = 0,
+                    plan: torch.Tensor | None = None, stream=None):
+    """Plan of a step's attention for attn_chunk_paged, one for all its layers; an int32
+    tensor of the library's own form.
+
+    Request b's new tokens are cu_tokens[b] to cu_tokens[b+1] of the ``tokens`` packed ones,
+    its last keys of seqlens[b] (attn_pages_append's results).  Each sees the keys up to its own,
+    of them the last ``window`` and the first ``sinks`` (``window=None``: all).  ``max_keys``
+    is max_pages * page_size of the block table.  D is 64 or 128.
+    """
+    call = (_fast or _native()).chunk_plan
+    args = (tokens, Hq, Hkv, D, max_keys, window, sinks, plan)
+    if stream is None:
+        return call(cu_tokens, seqlens, *args)
+    return _on_stream(stream, call, cu_tokens, seqlens, *args)
+
+
+def attn_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_table: torch.Tensor, plan: torch.Tensor, scale: float | None = None,
+                     o: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """Attention of a step's new tokens over a paged cache; returns (o bf16 [T,Hq,D],
+    lse fp32 [T,Hq]).
+
+    q [T,Hq,D] bf16; caches [num_pages,Hkv,page_size,D] that hold the new tokens' keys and
+    values too (attn_rope_append); block_table int32 [B,max_pages]; plan from attn_chunk_plan.
+    Tokens behind the last request's are left as they were.  ``workspace`` is an optional
+    fp32 CUDA tensor of attn_chunk_workspace floats (include/attn.h).
+    """
+    call = (_fast or _native()).chunk_paged
+    args = (q, k_cache, v_cache, block_table, plan, scale, o, lse, workspace)
+    return call(*args) if stream is None else _on_stream(stream, call, *args)

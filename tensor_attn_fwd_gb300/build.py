@@ -67,7 +67,7 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
 # Kernels that rebalance registers with setmaxnreg must be compiled with exactly
 # the per-thread count their split assumes (threads x count = the pool that
 # setmaxnreg.inc draws from); a smaller count would make .inc wait forever.
-EXACT_REGISTERS = {"attn_fwd_kernel": 168}
+EXACT_REGISTERS = {"attn_fwd_kernel": 168, "attn_chunk_kernel": 168}
 
 
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")

@@ -110,12 +110,12 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 }  // namespace
 
 bool encode_bf16_map(CUtensorMap* map, const void* base, int D, int rows, int planes,
-                     int box_rows) {
+                     int box_rows, int box_planes) {
   auto fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(rows), cuuint64_t(planes)};
   const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(D) * 2 * cuuint64_t(rows)};
-  const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(box_planes)};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -890,6 +890,206 @@ int attn_pages_copy(void* k_cache, void* v_cache, const int* src, const int* dst
   if (status == nullptr) return ATTN_ERR_CUDA;
   const cudaError_t e = launch_pages_copy(k_cache, v_cache, src, dst, n, num_pages, page_bytes,
                                           static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- a serving step
+namespace {
+
+// The checks that the rotary entry points share; ATTN_OK or the status to return.
+int rope_check_args(const void* qkv, long long ld, const float* table, const int* positions,
+                    const void* q, const void* k, const void* v, long long tokens, int Hq, int Hkv,
+                    int D, int R, int max_pos, int style) {
+  if (!qkv || !table || !q || !k || !v) return ATTN_ERR_INVALID_ARG;
+  if (tokens <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || R <= 0 || max_pos <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0 || R > D || (style != 0 && style != 1)) return ATTN_ERR_INVALID_ARG;
+  const long long N = (Hq + 2ll * Hkv) * D;
+  if (ld < N) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
+  if (R % 16 != 0) return ATTN_ERR_UNSUPPORTED;  // a thread's vectors hold whole pairs
+  if (ld % 8 != 0) return ATTN_ERR_UNSUPPORTED;  // rows begin at 16 bytes
+  if (tokens > (1ll << 30) || N > (1ll << 30) || ld > kMaxElems / tokens ||
+      static_cast<long long>(max_pos) * R > kMaxElems)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(qkv) || !aligned16(table) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned4(positions))
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+// The sizes of a chunk call are valid and supported; ATTN_OK or the status to return.
+int chunk_check_sizes(int B, int T, int Hq, int Hkv, int D) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (B > kMaxSeq || T > kMaxSeq || static_cast<long long>(T) * Hq > (1ll << 31) - 1)
+    return ATTN_ERR_UNSUPPORTED;
+  // Items of the plan, counted with int.
+  if (ChunkTiling(Hq, Hkv).max_items(B, T, Hkv) > (1ll << 26)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int attn_pages_append_workspace(int num_pages, int B, long long* entries) {
+  if (entries == nullptr || num_pages < 1 || B < 1) return ATTN_ERR_INVALID_ARG;
+  *entries = pages_append_workspace(num_pages, B);
+  return ATTN_OK;
+}
+
+int attn_pages_append(const int* block_table, const int* refs, const int* seqlens,
+                      const int* new_lens, int* block_table_out, int* refs_out, int* seqlens_out,
+                      int* cu_tokens, int* positions, int* slots, int* counts, int* workspace,
+                      int B, int T, int max_pages, int num_pages, int page_size, void* stream) {
+  if (!seqlens || !new_lens || !seqlens_out || !cu_tokens || !positions || !slots || !counts ||
+      !workspace || T <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  const int chk = pages_check_args(block_table, refs, block_table_out, refs_out, B, max_pages,
+                                   num_pages, page_size);
+  if (chk != ATTN_OK) return chk;
+  // Slots are numbered, and rows and tokens counted, with int.
+  if (static_cast<long long>(num_pages) * page_size > (1ll << 31) - 1 || T > kMaxSeq || B > kMaxSeq)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(seqlens) || !aligned4(new_lens) || !aligned4(seqlens_out) || !aligned4(cu_tokens) ||
+      !aligned4(positions) || !aligned4(slots) || !aligned4(counts) || !aligned4(workspace))
+    return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e = launch_pages_append(
+      block_table, refs, seqlens, new_lens, block_table_out, refs_out, seqlens_out, cu_tokens,
+      positions, slots, counts, workspace, B, T, max_pages, num_pages, page_size,
+      static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_rope_table_scaled(float* table, int max_pos, int R, float base, float factor, float low,
+                           float high, int original_pos, float amplitude, void* stream) {
+  if (!table) return ATTN_ERR_INVALID_ARG;
+  if (max_pos <= 0 || R <= 0 || R % 2 != 0 || original_pos < 0) return ATTN_ERR_INVALID_ARG;
+  if (!(base > 1.f) || !std::isfinite(base) || !(factor > 0.f) || !std::isfinite(factor) ||
+      !(amplitude > 0.f) || !std::isfinite(amplitude))
+    return ATTN_ERR_INVALID_ARG;
+  if (original_pos > 0 && (!(low >= 0.f) || !(high > low) || !std::isfinite(high)))
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pos) * R > kMaxElems) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(table)) return ATTN_ERR_MISALIGNED;
+  const RopeScaling scaling{factor, low, high, amplitude, original_pos};
+  const cudaError_t e = launch_rope_table_scaled(table, max_pos, R, static_cast<double>(base), scaling,
+                                                 static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_rope_split(const void* qkv, long long ld, const float* rope_table, const int* positions,
+                    void* q, void* k, void* v, int B, int S, int Hq, int Hkv, int D, int R,
+                    int max_pos, int style, void* stream) {
+  if (B <= 0 || S <= 0) return ATTN_ERR_INVALID_ARG;
+  const int chk = rope_check_args(qkv, ld, rope_table, positions, q, k, v,
+                                  static_cast<long long>(B) * S, Hq, Hkv, D, R, max_pos, style);
+  if (chk != ATTN_OK) return chk;
+  if (positions == nullptr && max_pos < S) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e =
+      launch_rope_split(qkv, ld, rope_table, positions, q, k, v, B, S, Hq, Hkv, D, R, max_pos, style,
+                        static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_rope_split_bwd(const void* dq, const void* dk, const void* dv, int fp32,
+                        const float* rope_table, const int* positions, void* dqkv, long long ld,
+                        int B, int S, int Hq, int Hkv, int D, int R, int max_pos, int style,
+                        void* stream) {
+  if (B <= 0 || S <= 0 || (fp32 != 0 && fp32 != 1)) return ATTN_ERR_INVALID_ARG;
+  const int chk = rope_check_args(dqkv, ld, rope_table, positions, dq, dk, dv,
+                                  static_cast<long long>(B) * S, Hq, Hkv, D, R, max_pos, style);
+  if (chk != ATTN_OK) return chk;
+  if (positions == nullptr && max_pos < S) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e =
+      launch_rope_split_bwd(dq, dk, dv, fp32, rope_table, positions, dqkv, ld, B, S, Hq, Hkv, D, R,
+                            max_pos, style, static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_rope_append(const void* qkv, long long ld, const float* rope_table, const int* positions,
+                     const int* slots, void* q, void* k_cache, void* v_cache, int T, int Hq,
+                     int Hkv, int D, int R, int max_pos, int num_pages, int page_size, int style,
+                     void* stream) {
+  if (!positions || !slots || num_pages <= 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+  const int chk = rope_check_args(qkv, ld, rope_table, positions, q, k_cache, v_cache, T, Hq, Hkv, D,
+                                  R, max_pos, style);
+  if (chk != ATTN_OK) return chk;
+  if (static_cast<long long>(num_pages) * page_size > (1ll << 31) - 1 ||
+      static_cast<long long>(num_pages) * page_size > kMaxElems / D / Hkv)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(slots)) return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e =
+      launch_rope_append(qkv, ld, rope_table, positions, slots, q, k_cache, v_cache, T, Hq, Hkv, D, R,
+                         max_pos, num_pages, page_size, style, static_cast<cudaStream_t>(stream),
+                         status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long long* entries) {
+  if (entries == nullptr) return ATTN_ERR_INVALID_ARG;
+  const int chk = chunk_check_sizes(B, T, Hq, Hkv, D);
+  if (chk != ATTN_OK) return chk;
+  *entries = ChunkLayout(B, ChunkTiling(Hq, Hkv).max_items(B, T, Hkv), sm_count()).total;
+  return ATTN_OK;
+}
+
+int attn_chunk_workspace(int D, long long* floats) {
+  if (floats == nullptr || D <= 0) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  *floats = chunk_workspace_floats(sm_count(), D);
+  return ATTN_OK;
+}
+
+int attn_chunk_plan(const int* cu_tokens, const int* seqlens, int* plan, int B, int T, int Hq,
+                    int Hkv, int D, int max_keys, int window, int sinks, void* stream) {
+  if (!cu_tokens || !seqlens || !plan || max_keys <= 0 || window < 1 || sinks < 0)
+    return ATTN_ERR_INVALID_ARG;
+  const int chk = chunk_check_sizes(B, T, Hq, Hkv, D);
+  if (chk != ATTN_OK) return chk;
+  if (max_keys > kMaxSeq) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(cu_tokens) || !aligned4(seqlens) || !aligned16(plan)) return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  // A window or sinks past the last key mean all keys; clamped, the kernels' sums fit int.
+  const cudaError_t e = launch_chunk_plan(
+      cu_tokens, seqlens, plan, B, T, Hq, Hkv, D, max_keys, window < max_keys ? window : max_keys,
+      sinks < max_keys ? sinks : max_keys, static_cast<cudaStream_t>(stream), status);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_chunk_paged(const void* q, const void* k_cache, const void* v_cache,
+                     const int* block_table, const int* plan, void* o, float* lse,
+                     float* workspace, int B, int T, int Hq, int Hkv, int num_pages, int page_size,
+                     int max_pages, int D, float scale, void* stream) {
+  if (!q || !k_cache || !v_cache || !plan || !o || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  const int chk = chunk_check_sizes(B, T, Hq, Hkv, D);
+  if (chk != ATTN_OK) return chk;
+  PagedKV paged;
+  int capacity = 0;
+  const int pchk = paged_check_args(block_table, plan, Hkv, num_pages, page_size, max_pages, D, B,
+                                    &paged, &capacity);
+  if (pchk != ATTN_OK) return pchk;
+  // Rows of the caches are coordinates of a tensor map; the one behind the last, too.
+  if (static_cast<long long>(num_pages) * Hkv > ((1ll << 31) - 256) / page_size)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(plan) ||
+      !aligned16(o) || !aligned16(lse) || !aligned16(workspace))
+    return ATTN_ERR_MISALIGNED;
+  int* status = status_word_device_ptr();
+  if (status == nullptr) return ATTN_ERR_CUDA;
+  const cudaError_t e =
+      launch_attn_chunk(q, k_cache, v_cache, plan, paged, o, lse, workspace, B, T, Hq, Hkv, D, scale,
+                        static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

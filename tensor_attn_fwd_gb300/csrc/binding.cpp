@@ -1,4 +1,4 @@
-// binding.cpp -- marshals the windowed-attention and page calls between PyTorch
+// binding.cpp -- marshals the windowed-attention, page and serving-step calls between PyTorch
 // tensors and the C ABI of libattn.so (include/attn.h): checks, outputs and
 // workspaces, the current stream, and errors.  Nothing is computed here.
 //
@@ -231,6 +231,12 @@ PyObject* pack(std::initializer_list<Tensor> tensors) {
     PyTuple_SET_ITEM(tuple, i++, obj);
   }
   return tuple;
+}
+
+PyObject* pack_one(const Tensor& t) {
+  PyObject* obj = THPVariable_Wrap(t);
+  if (obj == nullptr) throw PythonError{};
+  return obj;
 }
 
 // One call: `n` positional arguments, exceptions turned into Python's.
@@ -536,6 +542,280 @@ PyObject* pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ a serving step
+// block_table, refs, seqlens, new_lens, tokens, page_size, block_table_out, refs_out,
+// seqlens_out
+PyObject* pages_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const Pages p = pages_of(a[0], a[1]);
+    const Tensor& lens = int32(a[2], "seqlens", {p.B}, p.device);
+    const Tensor& news = int32(a[3], "new_lens", {p.B}, p.device);
+    const int T = integer(a[4], "tokens", 1, INT_MAX);
+    const int page = integer(a[5], "page_size", kAny, INT_MAX);
+    const Output table_out = output_int32(a[6], {p.B, p.M}, p.device, "block_table_out");
+    const Output refs_out = output_int32(a[7], {p.P}, p.device, "refs_out");
+    const Output lens_out = output_int32(a[8], {p.B}, p.device, "seqlens_out");
+    if (T > kAll) throw Failed{ATTN_ERR_UNSUPPORTED, "attn_pages_append"};
+    Tensor table, refs, lens_new, cu, positions, slots, counts;
+    {
+      const GpuPart gpu(p.device);
+      long long need = 0;
+      raise_if(attn_pages_append_workspace(p.P, p.B, &need), "attn_pages_append");
+      const Tensor ws = new_int32(need, p.device);
+      Carver results((table_out.given() ? 0 : padded(static_cast<int64_t>(p.B) * p.M)) +
+                         (refs_out.given() ? 0 : padded(p.P)) + (lens_out.given() ? 0 : padded(p.B)) +
+                         padded(static_cast<int64_t>(p.B) + 1) + 2 * padded(T) + 2,
+                     p.device);
+      table = table_out.given() ? table_out.get() : results.take({p.B, p.M});
+      refs = refs_out.given() ? refs_out.get() : results.take({p.P});
+      lens_new = lens_out.given() ? lens_out.get() : results.take({p.B});
+      cu = results.take({static_cast<int64_t>(p.B) + 1});
+      positions = results.take({T});
+      slots = results.take({T});
+      counts = results.take({2});
+      raise_if(attn_pages_append(ints(p.table), ints(p.refs), ints(lens), ints(news), ints(table),
+                                 ints(refs), ints(lens_new), ints(cu), ints(positions), ints(slots),
+                                 ints(counts), ints(ws), p.B, T, p.M, p.P, page,
+                                 current_stream(p.device)),
+               "attn_pages_append");
+    }
+    return pack({table, refs, lens_new, cu, positions, slots, counts});
+  });
+}
+
+// Rows of bf16 heads: [..., N] whose last dim is contiguous and whose others are one run of
+// rows, `ld` elements apart.
+struct Rows {
+  const Tensor& t;
+  int64_t count, width;
+  long long ld;
+};
+Rows rows_of(PyObject* obj, const char* name, int ndim, const Tensor* like = nullptr) {
+  const Tensor& t = tensor(obj, name);
+  if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+  if (t.scalar_type() != at::kBFloat16)
+    refuse(std::string(name) + " must be bfloat16, got " + c10::toString(t.scalar_type()));
+  if (t.dim() != ndim)
+    refuse(std::string(name) + " must have " + std::to_string(ndim) + " dims, got " +
+           std::to_string(t.dim()));
+  if (like != nullptr && t.device() != like->device())
+    refuse(std::string(name) + " must be on " + like->device().str());
+  const int64_t width = t.size(ndim - 1);
+  int64_t count = 1;
+  for (int i = 0; i + 1 < ndim; ++i) count *= t.size(i);
+  // (The stride of a dim of size 1 means nothing.)
+  long long ld = width;
+  bool regular = t.numel() > 0 && (width == 1 || t.stride(ndim - 1) == 1);
+  int64_t step = -1, above = 1;
+  for (int i = ndim - 2; i >= 0 && regular; --i) {
+    if (t.size(i) == 1) continue;
+    if (step < 0) {
+      step = t.stride(i) / above;
+      regular = t.stride(i) % above == 0;
+    }
+    regular = regular && t.stride(i) == step * above;
+    above *= t.size(i);
+  }
+  if (step >= 0) ld = step;
+  if (!regular) refuse(std::string(name) + " must be rows of contiguous elements, equally far apart");
+  return {t, count, width, ld};
+}
+
+// The table of attn_rope_table: [max_pos, R/2, 2].
+struct RopeTable {
+  const float* data;
+  int max_pos, R;
+};
+RopeTable rope_table_of(PyObject* obj, at::Device device) {
+  const Tensor& t = tensor(obj, "rope_table");
+  check(t, "rope_table", at::kFloat, "float32", 3, device);
+  if (t.size(2) != 2) refuse("rope_table must come from attn_rope_table");
+  return {static_cast<const float*>(t.data_ptr()), size_int(t.size(0), "rope_table"),
+          size_int(2 * t.size(1), "rope_table")};
+}
+const int* positions_of(PyObject* obj, int64_t count, at::Device device) {
+  if (obj == Py_None) return nullptr;
+  const Tensor& t = tensor(obj, "positions");
+  check(t, "positions", at::kInt, "int32", static_cast<int>(t.dim()), device);
+  if (t.numel() != count) refuse("positions must have " + std::to_string(count) + " entries");
+  return static_cast<const int*>(t.data_ptr());
+}
+
+// qkv, rope_table, Hq, Hkv, positions, style, q, k, v
+PyObject* rope_split(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const Rows x = rows_of(a[0], "qkv", 3);
+    const at::Device device = x.t.device();
+    const RopeTable table = rope_table_of(a[1], device);
+    const int Hq = integer(a[2], "Hq", 1, INT_MAX), Hkv = integer(a[3], "Hkv", 1, INT_MAX);
+    const int* positions = positions_of(a[4], x.count, device);
+    const int style = integer(a[5], "style", kAny, INT_MAX);
+    const int64_t heads = static_cast<int64_t>(Hq) + 2ll * Hkv;
+    if (x.width % heads != 0) refuse("qkv must have (Hq + 2 * Hkv) * D columns");
+    const int64_t B = x.t.size(0), S = x.t.size(1), D = x.width / heads;
+    const Output q_out = output_bf16(a[6], {B, Hq, S, D}, device, "q");
+    const Output k_out = output_bf16(a[7], {B, Hkv, S, D}, device, "k");
+    const Output v_out = output_bf16(a[8], {B, Hkv, S, D}, device, "v");
+    Tensor q, k, v;
+    {
+      const GpuPart gpu(device);
+      q = q_out.get();
+      k = k_out.get();
+      v = v_out.get();
+      raise_if(attn_rope_split(x.t.data_ptr(), x.ld, table.data, positions, q.data_ptr(),
+                               k.data_ptr(), v.data_ptr(), size_int(B, "qkv"), size_int(S, "qkv"),
+                               Hq, Hkv, size_int(D, "qkv"), table.R, table.max_pos, style,
+                               current_stream(device)),
+               "attn_rope_split");
+    }
+    return pack({q, k, v});
+  });
+}
+
+// dq, dk, dv, rope_table, positions, style, dqkv
+PyObject* rope_split_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 7, [&] {
+    const Tensor& dq = tensor(a[0], "dq");
+    const at::Device device = dq.device();
+    const bool fp32 = dq.scalar_type() == at::kFloat;
+    const auto type = fp32 ? at::kFloat : at::kBFloat16;
+    const char* type_name = fp32 ? "float32" : "bfloat16";
+    check(dq, "dq", type, type_name, 4, device);
+    const Tensor &dk = tensor(a[1], "dk"), &dv = tensor(a[2], "dv");
+    check(dk, "dk", type, type_name, 4, device);
+    check(dv, "dv", type, type_name, 4, device);
+    if (dk.sizes() != dv.sizes() || dk.size(0) != dq.size(0) || dk.size(2) != dq.size(2) ||
+        dk.size(3) != dq.size(3))
+      refuse("dq/dk/dv shape mismatch");
+    const RopeTable table = rope_table_of(a[3], device);
+    const int64_t B = dq.size(0), Hq = dq.size(1), S = dq.size(2), D = dq.size(3), Hkv = dk.size(1);
+    const int* positions = positions_of(a[4], B * S, device);
+    const int style = integer(a[5], "style", kAny, INT_MAX);
+    const int64_t N = (Hq + 2 * Hkv) * D;
+    Tensor dqkv;
+    long long ld = N;
+    if (a[6] != Py_None) {
+      const Rows y = rows_of(a[6], "dqkv", 3, &dq);
+      check_shape(y.t, "dqkv", {B, S, N});
+      dqkv = y.t;
+      ld = y.ld;
+    }
+    {
+      const GpuPart gpu(device);
+      if (!dqkv.defined()) dqkv = fresh({B, S, N}, at::kBFloat16, device);
+      raise_if(attn_rope_split_bwd(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), fp32, table.data,
+                                   positions, dqkv.data_ptr(), ld, size_int(B, "dq"),
+                                   size_int(S, "dq"), size_int(Hq, "dq"), size_int(Hkv, "dk"),
+                                   size_int(D, "dq"), table.R, table.max_pos, style,
+                                   current_stream(device)),
+               "attn_rope_split_bwd");
+    }
+    return pack_one(dqkv);
+  });
+}
+
+// qkv, rope_table, positions, slots, k_cache, v_cache, Hq, style, q
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const Rows x = rows_of(a[0], "qkv", 2);
+    const at::Device device = x.t.device();
+    const RopeTable table = rope_table_of(a[1], device);
+    const Tensor& positions = int32(a[2], "positions", {x.count}, device);
+    const Tensor& slots = int32(a[3], "slots", {x.count}, device);
+    const Tensor &k = bf16(a[4], "k_cache", 4, &x.t), &v = bf16(a[5], "v_cache", 4, &x.t);
+    if (k.sizes() != v.sizes()) refuse("the caches must have one shape");
+    const int Hq = integer(a[6], "Hq", 1, INT_MAX), style = integer(a[7], "style", kAny, INT_MAX);
+    const int64_t Hkv = k.size(1), D = k.size(3);
+    if (x.width != (Hq + 2 * Hkv) * D) refuse("qkv must have (Hq + 2 * Hkv) * D columns");
+    const Output q_out = output_bf16(a[8], {x.count, Hq, D}, device, "q");
+    Tensor q;
+    {
+      const GpuPart gpu(device);
+      q = q_out.get();
+      raise_if(attn_rope_append(x.t.data_ptr(), x.ld, table.data, ints(positions), ints(slots),
+                                q.data_ptr(), k.data_ptr(), v.data_ptr(), size_int(x.count, "qkv"),
+                                Hq, size_int(Hkv, "k_cache"), size_int(D, "k_cache"), table.R,
+                                table.max_pos, size_int(k.size(0), "k_cache"),
+                                size_int(k.size(2), "k_cache"), style, current_stream(device)),
+               "attn_rope_append");
+    }
+    return pack_one(q);
+  });
+}
+
+// cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, plan
+PyObject* chunk_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&] {
+    const Tensor& lens = tensor(a[1], "seqlens");
+    check(lens, "seqlens", at::kInt, "int32", 1, lens.device());
+    const at::Device device = lens.device();
+    const int B = size_int(lens.size(0), "seqlens");
+    const Tensor& cu = int32(a[0], "cu_tokens", {static_cast<int64_t>(B) + 1}, device);
+    const int T = integer(a[2], "tokens", kAny, INT_MAX), Hq = integer(a[3], "Hq", kAny, INT_MAX);
+    const int Hkv = integer(a[4], "Hkv", kAny, INT_MAX), D = integer(a[5], "D", kAny, INT_MAX);
+    const int max_keys = integer(a[6], "max_keys", kAny, INT_MAX);
+    const int window = a[7] == Py_None ? static_cast<int>(kAll) : integer(a[7], "window", 1, kAll);
+    const int sinks = integer(a[8], "sinks", 0, kAll);
+    Tensor plan;
+    if (a[9] != Py_None) plan = int32(a[9], "plan", {-1}, device);
+    {
+      const GpuPart gpu(device);
+      long long need = 0;
+      raise_if(attn_chunk_plan_size(B, T, Hq, Hkv, D, &need), "attn_chunk_plan");
+      if (plan.defined() && plan.numel() < need)
+        refuse("plan must have at least " + std::to_string(need) + " entries");
+      if (!plan.defined()) plan = new_int32(need, device);
+      raise_if(attn_chunk_plan(ints(cu), ints(lens), ints(plan), B, T, Hq, Hkv, D, max_keys, window,
+                               sinks, current_stream(device)),
+               "attn_chunk_plan");
+    }
+    return pack_one(plan);
+  });
+}
+
+// q, k_cache, v_cache, block_table, plan, scale, o, lse, workspace
+PyObject* chunk_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const Tensor& q = bf16(a[0], "q", 3);
+    const Tensor &k = bf16(a[1], "k_cache", 4, &q), &v = bf16(a[2], "v_cache", 4, &q);
+    if (k.size(3) != q.size(2) || v.sizes() != k.sizes()) refuse("q/cache shape mismatch");
+    const at::Device device = q.device();
+    const Tensor& table = int32(a[3], "block_table", {-1, -1}, device);
+    const Tensor& plan = int32(a[4], "plan", {-1}, device);
+    const int B = size_int(table.size(0), "block_table"), T = size_int(q.size(0), "q"),
+              Hq = size_int(q.size(1), "q"), Hkv = size_int(k.size(1), "k_cache"),
+              D = size_int(q.size(2), "q");
+    const float scale = scale_of(a[5], D);
+    const Output o_out = output_bf16(a[6], q.sizes(), device, "o");
+    const Output lse_out = output_f32(a[7], {T, Hq}, device, "lse");
+    Tensor ws;
+    if (a[8] != Py_None) {
+      ws = tensor(a[8], "workspace");
+      check(ws, "workspace", at::kFloat, "float32", static_cast<int>(ws.dim()), device);
+    }
+    Tensor o, lse;
+    {
+      const GpuPart gpu(device);
+      long long need = 0, entries = 0;
+      raise_if(attn_chunk_plan_size(B, T, Hq, Hkv, D, &entries), "attn_chunk_paged");
+      if (plan.numel() < entries) refuse("plan must come from attn_chunk_plan for these sizes");
+      raise_if(attn_chunk_workspace(D, &need), "attn_chunk_paged");
+      if (ws.defined() && ws.numel() < need)
+        refuse("workspace must have at least " + std::to_string(need) + " entries");
+      o = o_out.get();
+      lse = lse_out.get();
+      if (!ws.defined()) ws = fresh({need}, at::kFloat, device);
+      raise_if(attn_chunk_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), ints(table), ints(plan),
+                                o.data_ptr(), floats(lse), floats(ws), B, T, Hq, Hkv,
+                                size_int(k.size(0), "k_cache"), size_int(k.size(2), "k_cache"),
+                                size_int(table.size(1), "block_table"), D, scale,
+                                current_stream(device)),
+               "attn_chunk_paged");
+    }
+    return pack({o, lse});
+  });
+}
+
 // attn_error: the exception class of failed calls, called with (status, what)
 PyObject* setup(PyObject*, PyObject* attn_error) {
   Py_INCREF(attn_error);
@@ -553,6 +833,12 @@ PyMethodDef kMethods[] = {{"setup", setup, METH_O, nullptr},
                           FAST(pages_fork),
                           FAST(pages_compact),
                           FAST(pages_copy),
+                          FAST(pages_append),
+                          FAST(rope_split),
+                          FAST(rope_split_bwd),
+                          FAST(rope_append),
+                          FAST(chunk_plan),
+                          FAST(chunk_paged),
                           {nullptr, nullptr, 0, nullptr}};
 #undef FAST
 

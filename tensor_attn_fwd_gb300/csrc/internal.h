@@ -22,10 +22,10 @@ int sm_count();
 cudaError_t ensure_smem_attr(const void* kernel, int bytes);
 
 // Tiled TMA map of a contiguous [planes, rows, D] bf16 tensor with boxes of
-// [1, box_rows, 64] elements and 128-byte swizzle (rows past `rows` read as
+// [box_planes, box_rows, 64] elements and 128-byte swizzle (rows past `rows` read as
 // zero).  False if the driver entry point is unavailable or rejects the map.
 bool encode_bf16_map(CUtensorMap* map, const void* base, int D, int rows, int planes,
-                     int box_rows);
+                     int box_rows, int box_planes = 1);
 
 // Launch `kernel` on `stream` as a programmatic dependent of the previous
 // kernel in the stream: its CTAs may start (and run their set-up) while that
@@ -144,6 +144,29 @@ cudaError_t launch_qkv_rope(const void* x, const void* w, const float* rope, con
                             void* q, void* k, void* v, int B, int S, int hidden, int Hq, int Hkv,
                             int D, int max_pos, int style, cudaStream_t stream, int* status);
 
+
+// Rotary positions on projected rows (rope.cu): in training, and into the pages of a cache.
+// The frequencies' scaling for contexts longer than the trained one (include/attn.h).
+struct RopeScaling {
+  double factor, low, high, amplitude;
+  int original;
+};
+cudaError_t launch_rope_table_scaled(float* table, int max_pos, int R, double base,
+                                     const RopeScaling& scaling, cudaStream_t stream);
+cudaError_t launch_rope_split(const void* qkv, long long ld, const float* table,
+                              const int* positions, void* q, void* k, void* v, int B, int S, int Hq,
+                              int Hkv, int D, int R, int max_pos, int style, cudaStream_t stream,
+                              int* status);
+cudaError_t launch_rope_split_bwd(const void* dq, const void* dk, const void* dv, int fp32,
+                                  const float* table, const int* positions, void* dqkv,
+                                  long long ld, int B, int S, int Hq, int Hkv, int D, int R,
+                                  int max_pos, int style, cudaStream_t stream, int* status);
+cudaError_t launch_rope_append(const void* qkv, long long ld, const float* table,
+                               const int* positions, const int* slots, void* q, void* k_cache,
+                               void* v_cache, int T, int Hq, int Hkv, int D, int R, int max_pos,
+                               int num_pages, int page_size, int style, cudaStream_t stream,
+                               int* status);
+
 // The argument checks every split-KV decode entry point shares (inputs, sizes,
 // split count, scale, head dimension, input alignment); `paged` skips the
 // contiguous-cache size limit.  ATTN_OK or the status to return.
@@ -225,12 +248,58 @@ cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seql
                               const int* parents, int* table_out, int* refs_out, int* seqlens_out,
                               int* src, int* dst, int* counts, int* workspace, int B, int R, int M,
                               int P, int page_size, int room, cudaStream_t stream, int* status);
+// int32 workspace of launch_pages_append (B rows).
+inline long long pages_append_workspace(int P, int B) { return P + 3ll * B + 3 * kPagesMaxCtas; }
+cudaError_t launch_pages_append(const int* table, const int* refs, const int* seqlens,
+                                const int* new_lens, int* table_out, int* refs_out,
+                                int* seqlens_out, int* cu, int* positions, int* slots, int* counts,
+                                int* workspace, int B, int T, int M, int P, int page_size,
+                                cudaStream_t stream, int* status);
 cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_out, int* refs_out,
                                  int* src, int* dst, int* num_live, int* workspace, int B, int M,
                                  int P, cudaStream_t stream, int* status);
 cudaError_t launch_pages_copy(void* k, void* v, const int* src, const int* dst, int n,
                               int num_pages, long long page_bytes, cudaStream_t stream,
                               int* status);
+
+// Attention of a step's new tokens over a paged cache (attn_chunk.cu).  A query tile holds
+// the tokens of up to 128 rows of one KV head's query heads: tile_tokens of them with
+// slice_heads heads each (more than 128 heads a KV head: in `slices` slices).
+struct ChunkTiling {
+  int group, slices, slice_heads, tile_tokens;
+  ChunkTiling(int Hq, int Hkv)
+      : group(Hq / Hkv),
+        slices((group + 127) / 128),
+        slice_heads((group + slices - 1) / slices),
+        tile_tokens(128 / slice_heads) {}
+  // Items of two query tiles (the last of a request may be one), at most.
+  long long max_items(int B, int T, int Hkv) const {
+    return (static_cast<long long>(T) / (2 * tile_tokens) + B) * Hkv * slices;
+  }
+};
+// Layout of a plan in int32: header, CTAs' pieces, cut items, the requests' item counts,
+// pieces.
+constexpr int kChunkHeader = 16, kChunkRecord = 8;
+struct ChunkLayout {
+  long long begins, cuts, tiles, pieces, total;
+  static __host__ __device__ long long align(long long n) { return (n + 7) / 8 * 8; }
+  __host__ __device__ ChunkLayout(int B, long long max_items, int ctas) {
+    begins = kChunkHeader;
+    cuts = align(begins + ctas + 1);
+    tiles = cuts + static_cast<long long>(kChunkRecord) * ctas;
+    pieces = align(tiles + B + 1);
+    total = pieces + kChunkRecord * (max_items + ctas);
+  }
+};
+// Partial results: two of 256 rows for each CTA.
+inline long long chunk_workspace_floats(int ctas, int D) { return 2ll * ctas * 256 * (D + 1); }
+cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
+                              int Hkv, int D, int max_keys, int window, int sinks,
+                              cudaStream_t stream, int* status);
+cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_cache,
+                              const int* plan, const PagedKV& paged, void* o, float* lse,
+                              float* workspace, int B, int T, int Hq, int Hkv, int D, float scale,
+                              cudaStream_t stream, int* status);
 
 // Backward: Delta into `delta` ([B,Hq,Sq]), then dK/dV and dQ kernels.
 cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const float* o,

@@ -56,6 +56,7 @@ constexpr int kWarps = kThreads / 32;
 // The largest calls (elements of arrays) of one CTA, and of one cluster.
 constexpr long long kSmallForkEntries = 8192, kSmallForkPages = 6144, kSmallForkSlots = 8192;
 constexpr long long kSmallCompactEntries = 8192, kSmallCompactPages = 4096;
+constexpr long long kBlockWork = 4096;  // append
 constexpr long long kClusterWork = 1 << 15;
 constexpr int kClusterCtas = 16;  // past the portable 8: the kernels opt in
 
@@ -127,20 +128,22 @@ __device__ __forceinline__ int checked_entry(int e, int num_pages, int* status) 
   return e;
 }
 
-// All phases of a call.  kCluster: one cluster and its barrier; kGrid: a cooperative
-// grid and its (every CTA is resident, and each enters every barrier).
-enum Span { kCluster, kGrid };
+// All phases of a call.  kBlock: one CTA and its barrier; kCluster: one cluster and its;
+// kGrid: a cooperative grid and its (every CTA is resident, and each enters every barrier).
+enum Span { kBlock, kCluster, kGrid };
 template <typename Op, Span SPAN>
 __global__ void __launch_bounds__(kThreads, 1) pages_phases_kernel(const Op op) {
   __shared__ int smem[32];
-  if constexpr (SPAN == kCluster) {
+  if constexpr (SPAN != kGrid) {
     grid_dependency_wait();
     grid_launch_dependents();
   }
   for (int ph = 0; ph < Op::kPhases; ++ph) {
     op.run(ph, smem);
     if (ph + 1 == Op::kPhases) break;
-    if constexpr (SPAN == kCluster)
+    if constexpr (SPAN == kBlock)
+      __syncthreads();
+    else if constexpr (SPAN == kCluster)
       cluster_sync();
     else
       cooperative_groups::this_grid().sync();
@@ -647,6 +650,217 @@ struct CompactOp {
   }
 };
 
+// ------------------------------------------------------------------ append
+// Pages, positions and slots for a step's new tokens.  Token sums are clamped to T + 1
+// (a sum that saturates stays associative), so that no row count overflows them.
+struct AppendOp {
+  static constexpr int kPhases = 4;
+  const int *table, *refs, *seqlens, *new_lens;
+  int *table_out, *refs_out, *seqlens_out, *cu, *positions, *slots, *counts;
+  // Workspace: the free pages, ascending; each CTA's free pages, needed pages and tokens; per
+  // row those before it (in its CTA's rows, then of all rows, or -1 for a row that
+  // takes no tokens), its first token, and its length before.
+  int *free_list, *cta_free, *cta_need, *cta_tokens, *need, *first, *len;
+  int B, M, P, T, page_size;
+  FixedDiv by_page;
+  int table_vec;  // 16-byte accesses are aligned
+  int* status;
+
+  struct Row {
+    int len, n;
+    int lo, hi;  // slots of the new tokens
+  };
+  __device__ __forceinline__ Row row(int r, int* report) const {
+    Row x;
+    x.len = seqlens[r];
+    x.n = new_lens[r];
+    x.lo = x.hi = 0;
+    if (x.n < 0) {
+      record_status(report, ATTN_ERR_INVALID_ARG);
+      x.n = 0;
+    }
+    const long long end = static_cast<long long>(x.len) + x.n;
+    if (x.n == 0 || x.len < 0) return x;
+    if (end > static_cast<long long>(M) * page_size) {
+      record_status(report, ATTN_ERR_INVALID_ARG);
+      return x;
+    }
+    x.lo = by_page.div(x.len);
+    x.hi = by_page.div(static_cast<int>(end) - 1) + 1;
+    return x;
+  }
+  __device__ __forceinline__ int tokens(int n) const { return min(n, T + 1); }
+  __device__ __forceinline__ int add_tokens(int a, int b) const {
+    return static_cast<int>(min(static_cast<unsigned>(a) + b, static_cast<unsigned>(T) + 1));
+  }
+  // Exclusive prefix of the token counts over the CTA, as block_scan.
+  __device__ __forceinline__ int token_scan(int x, int* smem, int& total) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl = add_tokens(incl, y);
+    }
+    const int excl = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 31) smem[warp] = incl;
+    __syncthreads();
+    int wincl = smem[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, wincl, off);
+      if (lane >= off) wincl = add_tokens(wincl, y);
+    }
+    total = __shfl_sync(0xffffffffu, wincl, 31);
+    const int before = __shfl_sync(0xffffffffu, wincl, max(warp - 1, 0));
+    __syncthreads();
+    return add_tokens(warp > 0 ? before : 0, lane > 0 ? excl : 0);
+  }
+
+  __device__ void run(int ph, int* smem) const {
+    const unsigned tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Part pages(P), rows(B);
+    if (ph == 0) {
+      int n = 0;
+      for (int p = pages.begin + threadIdx.x; p < pages.end; p += kThreads) {
+        const int c = refs[p];
+        n += c == 0;
+        if (refs_out != refs) refs_out[p] = c;
+      }
+      n = block_sum(n, smem);
+      if (threadIdx.x == 0) cta_free[blockIdx.x] = n;
+      // A warp per row: the pages it lacks.
+      for (int r = rows.begin + warp; r < rows.end; r += kWarps) {
+        const Row x = row(r, nullptr);
+        int lacks = 0;
+        for (int s = x.lo + lane; s < x.hi; s += 32)
+          lacks += checked_entry(table[static_cast<size_t>(r) * M + s], P, nullptr) < 0;
+        lacks = __reduce_add_sync(0xffffffffu, lacks);
+        if (lane == 0) need[r] = lacks;
+      }
+      __syncthreads();
+      int at = 0, tok = 0;
+      for (int r0 = rows.begin; r0 < rows.end; r0 += kThreads) {
+        const int r = r0 + threadIdx.x;
+        int total, tok_total;
+        const int k = at + block_scan(r < rows.end ? need[r] : 0, smem, total);
+        const int t = add_tokens(
+            tok, token_scan(r < rows.end ? tokens(row(r, nullptr).n) : 0, smem, tok_total));
+        if (r < rows.end) {
+          need[r] = k;
+          first[r] = t;
+        }
+        at += total;
+        tok = add_tokens(tok, tok_total);
+      }
+      if (threadIdx.x == 0) {
+        cta_need[blockIdx.x] = at;
+        cta_tokens[blockIdx.x] = tok;
+      }
+    } else if (ph == 1) {
+      // The free pages of this CTA's part, and the table as it is.
+      int at = sum_counts(cta_free, blockIdx.x, smem);
+      for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads) {
+        const int p = p0 + threadIdx.x;
+        const int is_free = p < pages.end && refs[p] == 0;
+        int total;
+        const int k = at + block_scan(is_free, smem, total);
+        if (is_free) free_list[k] = p;
+        at += total;
+      }
+      const unsigned entries = static_cast<unsigned>(B) * M;
+      if (table_vec) {
+        for (unsigned i = tid; i < entries / 4; i += n_threads) {
+          int4 e = reinterpret_cast<const int4*>(table)[i];
+          e.x = checked_entry(e.x, P, status);
+          e.y = checked_entry(e.y, P, status);
+          e.z = checked_entry(e.z, P, status);
+          e.w = checked_entry(e.w, P, status);
+          reinterpret_cast<int4*>(table_out)[i] = e;
+        }
+      } else {
+        for (unsigned i = tid; i < entries; i += n_threads)
+          table_out[i] = checked_entry(table[i], P, status);
+      }
+      // Which rows take their tokens: those whose pages and whose places in the step's T
+      // suffice.  (Each row's lengths are read for the last time here, by the thread that
+      // writes the new one: the two arrays may be one.)
+      const int n_free = sum_counts(cta_free, gridDim.x, smem);
+      const int base = sum_counts(cta_need, blockIdx.x, smem);
+      const int all_need = sum_counts(cta_need, gridDim.x, smem);
+      int tok_base = 0;
+      {
+        int x = 0;
+        for (int i = threadIdx.x; i < static_cast<int>(blockIdx.x); i += kThreads)
+          x = add_tokens(x, cta_tokens[i]);
+        token_scan(x, smem, tok_base);
+      }
+      for (int r = rows.begin + threadIdx.x; r < rows.end; r += kThreads) {
+        const Row x = row(r, status);
+        const int before = base + need[r];
+        const int after = r + 1 < rows.end ? base + need[r + 1] : base + cta_need[blockIdx.x];
+        const int t = add_tokens(tok_base, first[r]), end = add_tokens(t, tokens(x.n));
+        bool takes = x.lo < x.hi;
+        if (end > T) {
+          record_status(status, ATTN_ERR_INVALID_ARG);
+          takes = false;
+        }
+        takes = takes && after <= n_free;
+        cu[r + 1] = min(end, T);
+        len[r] = takes ? x.len : -1;
+        seqlens_out[r] = takes ? x.len + x.n : x.len;
+      }
+      if (tid == 0) {
+        cu[0] = 0;
+        counts[0] = all_need;
+        counts[1] = n_free;
+        if (all_need > n_free) record_status(status, ATTN_ERR_NO_PAGES);
+      }
+    } else if (ph == 2) {
+      const int base = sum_counts(cta_need, blockIdx.x, smem);
+      for (int r = rows.begin + warp; r < rows.end; r += kWarps) {
+        const int from = len[r];
+        if (from < 0) continue;
+        const int lo = by_page.div(from), hi = by_page.div(seqlens_out[r] - 1) + 1;
+        int k = base + need[r];
+        for (int s0 = lo; s0 < hi; s0 += 32) {
+          const int s = s0 + lane;
+          int* const entry = table_out + static_cast<size_t>(r) * M + s;
+          const bool lacks = s < hi && *entry < 0;
+          const unsigned votes = __ballot_sync(0xffffffffu, lacks);
+          if (lacks) {
+            const int page = free_list[k + __popc(votes & ((1u << lane) - 1u))];
+            *entry = page;
+            refs_out[page] = 1;
+          }
+          k += __popc(votes);
+        }
+      }
+    } else {
+      for (unsigned t = tid; t < static_cast<unsigned>(T); t += n_threads) {
+        // The row whose tokens begin last at or before t.
+        int lo = 0, hi = B;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (cu[mid + 1] <= static_cast<int>(t))
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        int pos = 0, slot = -1;
+        if (lo < B && len[lo] >= 0) {
+          pos = len[lo] + static_cast<int>(t) - cu[lo];
+          const int s = by_page.div(pos);
+          slot = table_out[static_cast<size_t>(lo) * M + s] * page_size + pos - s * page_size;
+        }
+        positions[t] = pos;
+        slots[t] = slot;
+      }
+    }
+  }
+};
+
 // ------------------------------------------------------------------ copies
 // A CTA per 32 KB of a page, every load in flight before the first store, both marked
 // as used once (evict-first).  Bound by HBM: 4000 pages of 2 x 64 KB in 161.7 us, 6484
@@ -762,6 +976,37 @@ cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seql
       static_cast<long long>(R) * ForkOp::small_slots(op.room, page_size) <= kSmallForkSlots)
     return launch_small(op, ForkOp::small_bytes(P, R), stream);
   return launch_phases(op, entries > P ? entries : P, stream);
+}
+
+cudaError_t launch_pages_append(const int* table, const int* refs, const int* seqlens,
+                                const int* new_lens, int* table_out, int* refs_out,
+                                int* seqlens_out, int* cu, int* positions, int* slots, int* counts,
+                                int* workspace, int B, int T, int M, int P, int page_size,
+                                cudaStream_t stream, int* status) {
+  AppendOp op{table, refs, seqlens, new_lens, table_out, refs_out, seqlens_out,
+              cu, positions, slots, counts};
+  op.free_list = workspace;
+  op.cta_free = op.free_list + P;
+  op.cta_need = op.cta_free + kPagesMaxCtas;
+  op.cta_tokens = op.cta_need + kPagesMaxCtas;
+  op.need = op.cta_tokens + kPagesMaxCtas;
+  op.first = op.need + B;
+  op.len = op.first + B;
+  op.B = B;
+  op.M = M;
+  op.P = P;
+  op.T = T;
+  op.page_size = page_size;
+  op.by_page = FixedDiv(page_size);
+  op.table_vec = static_cast<long long>(B) * M % 4 == 0 && aligned16(table) && aligned16(table_out);
+  op.status = status;
+  const long long entries = static_cast<long long>(B) * M;
+  long long work = entries > P ? entries : P;
+  if (T > work) work = T;
+  if (work <= kBlockWork)
+    return launch_programmatic(pages_phases_kernel<AppendOp, kBlock>, dim3(1), dim3(kThreads), 0,
+                               stream, op);
+  return launch_phases(op, work, stream);
 }
 
 cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_out, int* refs_out,

@@ -1,0 +1,301 @@
+// rope.cu -- rotary positions on projected rows, beside the projection that has them in
+// its epilogue (qkv_rope.cu): between a projection of any kind and the attention's layout,
+// in training (split and its gradient), and into the pages of a cache in serving (append).
+//
+// A row of qkv holds Hq query heads, Hkv key heads and Hkv value heads of D dims.  The
+// first R dims of a query or key head at position p are R/2 pairs (a, b), dims (2i, 2i+1)
+// (style 0) or (i, i + R/2) (style 1), turned by the angle p * theta_i:
+//   a' = a cos - b sin,   b' = a sin + b cos,
+// from a table of (cos, sin) rows; dims from R on, and value heads, are copied.  The map
+// is linear, so the gradient is its transpose: the same with sin negated, and the
+// scatter of the heads turned round.
+//
+// Bound by memory: each element is read and written once.  A thread owns a unit of 16
+// dims of a head, two 16-byte vectors that hold whole pairs in either style, at the same
+// place of every U-th head of its token, so that it reads its eight (cos, sin) once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "window.cuh"
+
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void record_status(int* status, int code) {
+  if (status != nullptr) atomicCAS(status, 0, code);
+}
+
+enum Form { kSplit, kAppend, kGrad };
+
+struct RopeParams {
+  // Rows of Hq + 2 Hkv heads: read (split, append: qkv), or written (gradient: dqkv).
+  __nv_bfloat16* rows;
+  long long ld;  // elements from one row to the next
+  const float* table;    // [max_pos, R/2, 2]
+  const int* positions;  // [tokens], or null: s
+  const int* slots;      // append: [tokens]
+  // Split: [B,H,S,D]; append: q [tokens,Hq,D] and the caches; gradient: dq, dk, dv.
+  void *q, *k, *v;
+  int tokens, S, Hq, Hkv, D, R, max_pos;
+  int page_size;
+  long long num_slots;  // append: num_pages * page_size
+  FixedDiv by_seq, by_page;
+  int* status;
+};
+
+// Eight elements as floats.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+// Rounded once, to nearest even.
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// One CTA per token.  TG: the type of dq, dk and dv.
+template <Form FORM, int STYLE, typename TG>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = blockIdx.x;
+  const int units = p.D / 16, turned = p.R / 16;
+  const int u = threadIdx.x & (units - 1);  // (D is a power of two)
+  const int heads = p.Hq + 2 * p.Hkv;
+  const int step = kThreads / units;
+  int b = 0, s = t;
+  if (FORM != kAppend) {
+    b = p.by_seq.div(t);
+    s = t - b * p.S;
+  }
+  // This unit's two vectors of a rotated head, and of one that is copied.
+  const bool turns = u < turned;
+  const int o0 = STYLE == 1 && turns ? 8 * u : 16 * u;
+  const int o1 = STYLE == 1 && turns ? p.R / 2 + 8 * u : 16 * u + 8;
+  float cs[8], sn[8];
+  if (turns) {
+    int pos = p.positions != nullptr ? __ldg(p.positions + t) : s;
+    if (pos < 0 || pos >= p.max_pos) {
+      record_status(p.status, ATTN_ERR_INVALID_ARG);
+      pos = min(max(pos, 0), p.max_pos - 1);
+    }
+    const float4* row =
+        reinterpret_cast<const float4*>(p.table + static_cast<size_t>(pos) * p.R + 16 * u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 w = __ldg(row + i);
+      cs[2 * i] = w.x, sn[2 * i] = w.y, cs[2 * i + 1] = w.z, sn[2 * i + 1] = w.w;
+    }
+    if (FORM == kGrad)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+  }
+  long long page = -1;
+  int at = 0;
+  if (FORM == kAppend) {
+    const int slot = __ldg(p.slots + t);
+    if (slot >= 0 && slot < p.num_slots) {
+      page = p.by_page.div(slot);
+      at = slot - static_cast<int>(page) * p.page_size;
+    } else if (slot != -1) {
+      record_status(p.status, ATTN_ERR_INVALID_ARG);
+    }
+  }
+  __nv_bfloat16* const row = p.rows + t * p.ld;
+#pragma unroll 2
+  for (int h = threadIdx.x / units; h < heads; h += step) {
+    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+    const int g = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+    void* const base = is_q ? p.q : is_v ? p.v : p.k;
+    const int H = is_q ? p.Hq : p.Hkv;
+    size_t other;  // of the head's first dim in base
+    if (FORM == kAppend && !is_q) {
+      if (page < 0) continue;
+      other = ((page * H + g) * p.page_size + at) * p.D;
+    } else if (FORM == kAppend) {
+      other = (static_cast<size_t>(t) * H + g) * p.D;
+    } else {
+      other = ((static_cast<size_t>(b) * H + g) * p.S + s) * p.D;
+    }
+    __nv_bfloat16* const mine = row + static_cast<size_t>(h) * p.D;
+    // A value head's vectors lie side by side.
+    const int a0 = is_v ? 16 * u : o0, a1 = is_v ? 16 * u + 8 : o1;
+    float x[8], y[8];
+    if constexpr (FORM == kGrad) {
+      const TG* from = static_cast<const TG*>(base) + other;
+      load8(from + a0, x);
+      load8(from + a1, y);
+    } else {
+      load8(mine + a0, x);
+      load8(mine + a1, y);
+    }
+    if (turns && !is_v) {
+      if constexpr (STYLE == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[i], c = y[i];
+          x[i] = a * cs[i] - c * sn[i];
+          y[i] = a * sn[i] + c * cs[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[2 * i], c = x[2 * i + 1];
+          x[2 * i] = a * cs[i] - c * sn[i];
+          x[2 * i + 1] = a * sn[i] + c * cs[i];
+          const float d = y[2 * i], e = y[2 * i + 1];
+          y[2 * i] = d * cs[4 + i] - e * sn[4 + i];
+          y[2 * i + 1] = d * sn[4 + i] + e * cs[4 + i];
+        }
+      }
+    }
+    if constexpr (FORM == kGrad) {
+      store8(mine + a0, x);
+      store8(mine + a1, y);
+    } else {
+      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(base) + other;
+      store8(to + a0, x);
+      store8(to + a1, y);
+    }
+  }
+}
+
+template <Form FORM, typename TG = float>
+cudaError_t launch_rope(const RopeParams& p, int style, cudaStream_t stream) {
+  return launch_programmatic(style == 0 ? rope_kernel<FORM, 0, TG> : rope_kernel<FORM, 1, TG>,
+                             dim3(p.tokens), dim3(kThreads), 0, stream, p);
+}
+
+// The frequencies' scaling, as internal.h's RopeScaling; one thread per table entry.  In
+// 64 bits: the angle of a far position needs more than 32.
+__global__ void rope_table_scaled_kernel(float* table, int max_pos, int R, double log_base,
+                                         const RopeScaling sc) {
+  const long long n = static_cast<long long>(max_pos) * (R / 2);
+  for (long long idx = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; idx < n;
+       idx += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int i = static_cast<int>(idx % (R / 2));
+    const long long pos = idx / (R / 2);
+    double theta = exp(-2.0 * i / R * log_base);
+    // Turns over the original context decide how far the frequency is lowered.
+    double keep = 0.0;
+    if (sc.original > 0) {
+      const double turns = sc.original * theta * 0.15915494309189535;  // 1 / (2 pi)
+      keep = fmin(fmax((turns - sc.low) / (sc.high - sc.low), 0.0), 1.0);
+    }
+    theta *= keep + (1.0 - keep) / sc.factor;
+    double sn, cs;
+    sincos(static_cast<double>(pos) * theta, &sn, &cs);
+    table[2 * idx] = static_cast<float>(cs * sc.amplitude);
+    table[2 * idx + 1] = static_cast<float>(sn * sc.amplitude);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table_scaled(float* table, int max_pos, int R, double base,
+                                     const RopeScaling& scaling, cudaStream_t stream) {
+  const long long n = static_cast<long long>(max_pos) * (R / 2);
+  const int blocks = static_cast<int>(n / 256 + 1 < 4096 ? n / 256 + 1 : 4096);
+  rope_table_scaled_kernel<<<blocks, 256, 0, stream>>>(table, max_pos, R, std::log(base), scaling);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_split(const void* qkv, long long ld, const float* table,
+                              const int* positions, void* q, void* k, void* v, int B, int S, int Hq,
+                              int Hkv, int D, int R, int max_pos, int style, cudaStream_t stream,
+                              int* status) {
+  RopeParams p = {};
+  p.rows = static_cast<__nv_bfloat16*>(const_cast<void*>(qkv));
+  p.ld = ld;
+  p.table = table;
+  p.positions = positions;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.tokens = B * S;
+  p.S = S;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.R = R;
+  p.max_pos = max_pos;
+  p.by_seq = FixedDiv(S);
+  p.status = status;
+  return launch_rope<kSplit>(p, style, stream);
+}
+
+cudaError_t launch_rope_split_bwd(const void* dq, const void* dk, const void* dv, int fp32,
+                                  const float* table, const int* positions, void* dqkv,
+                                  long long ld, int B, int S, int Hq, int Hkv, int D, int R,
+                                  int max_pos, int style, cudaStream_t stream, int* status) {
+  RopeParams p = {};
+  p.rows = static_cast<__nv_bfloat16*>(dqkv);
+  p.ld = ld;
+  p.table = table;
+  p.positions = positions;
+  p.q = const_cast<void*>(dq);
+  p.k = const_cast<void*>(dk);
+  p.v = const_cast<void*>(dv);
+  p.tokens = B * S;
+  p.S = S;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.R = R;
+  p.max_pos = max_pos;
+  p.by_seq = FixedDiv(S);
+  p.status = status;
+  return fp32 ? launch_rope<kGrad, float>(p, style, stream)
+              : launch_rope<kGrad, __nv_bfloat16>(p, style, stream);
+}
+
+cudaError_t launch_rope_append(const void* qkv, long long ld, const float* table,
+                               const int* positions, const int* slots, void* q, void* k_cache,
+                               void* v_cache, int T, int Hq, int Hkv, int D, int R, int max_pos,
+                               int num_pages, int page_size, int style, cudaStream_t stream,
+                               int* status) {
+  RopeParams p = {};
+  p.rows = static_cast<__nv_bfloat16*>(const_cast<void*>(qkv));
+  p.ld = ld;
+  p.table = table;
+  p.positions = positions;
+  p.slots = slots;
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.tokens = T;
+  p.S = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.R = R;
+  p.max_pos = max_pos;
+  p.page_size = page_size;
+  p.num_slots = static_cast<long long>(num_pages) * page_size;
+  p.by_page = FixedDiv(page_size);
+  p.status = status;
+  return launch_rope<kAppend>(p, style, stream);
+}
+
+}  // namespace attn
