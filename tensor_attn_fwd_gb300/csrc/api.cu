@@ -1038,14 +1038,14 @@ int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long long* entrie
   if (entries == nullptr) return ATTN_ERR_INVALID_ARG;
   const int chk = chunk_check_sizes(B, T, Hq, Hkv, D);
   if (chk != ATTN_OK) return chk;
-  *entries = ChunkLayout(B, ChunkTiling(Hq, Hkv).max_items(B, T, Hkv), sm_count()).total;
+  *entries = ChunkLayout(B, ChunkTiling(Hq, Hkv).max_items(B, T, Hkv), chunk_ctas()).total;
   return ATTN_OK;
 }
 
 int attn_chunk_workspace(int D, long long* floats) {
   if (floats == nullptr || D <= 0) return ATTN_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
-  *floats = chunk_workspace_floats(sm_count(), D);
+  *floats = chunk_workspace_floats(chunk_ctas(), D);
   return ATTN_OK;
 }
 

@@ -19,8 +19,9 @@
 //
 // Plan.  Requests differ in their numbers of tokens and keys, so the items' K/V tiles are
 // put in one line and cut into equal parts, one for each CTA; an item that is cut leaves
-// partial results, which a second kernel merges by their LSE (attn_combine's formula).
-// The plan depends on the lengths alone: one serves all layers of a step.
+// partial results, which are merged by their LSE (attn_combine's formula) by whoever
+// finishes its piece last (see Parts).  The plan depends on the lengths alone: one serves
+// all layers of a step.
 //
 // Pages.  A K/V tile is loaded as boxes of 32, 64 or 128 keys (what divides the page), each
 // found through the block table; boxes that no row sees are filled with zeros by a load
@@ -31,8 +32,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -45,12 +49,13 @@ using namespace ptx;
 
 constexpr int kMagic = 0x43484b31;
 constexpr int kMaxKeys = 1 << 30;  // of a request
-// A piece's cost around its K/V tiles, in tiles.
-constexpr int kOverhead = 1;
+// Costs of an item in the line: per K/V tile with one query tile and with two, and around its
+// tiles.
+constexpr int kCostOne = 2, kCostTwo = 3, kOverhead = 5;
 // An item is cut no closer than this to its ends (in tiles): a cut costs partial results.
 constexpr int kSnap = 2;
 // Cost that is worth a CTA of its own.
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 8;
 
 __device__ __forceinline__ void record_status(int* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
@@ -59,27 +64,32 @@ __device__ __forceinline__ void record_status(int* status, int code) {
 // The plan's header.
 struct PlanHeader {
   int magic, B, T, Hq, Hkv, D, max_keys, window, sinks, ctas;
-  int n_pieces, n_cuts;
-  int pad[kChunkHeader - 12];
+  int n_pieces;
+  int pad[kChunkHeader - 11];
 };
 static_assert(sizeof(PlanHeader) == kChunkHeader * sizeof(int), "header size");
 
 // A run of K/V tiles of an item.
+enum : uint16_t {
+  kRagged = 1,  // the item's last K/V tile reaches past the request's keys
+  kShared = 2,  // the request's K/V is read by several items
+};
 struct alignas(16) Piece {
-  int token, tokens;  // first packed token, their number (1 to 2 tiles' worth)
+  int token;          // first packed token
+  uint16_t tokens;    // their number (1 to 2 tiles' worth)
+  uint16_t flags;     // kRagged, kShared
   int pos;            // the first one's position
   int row;            // request
   int head;           // KV head * slices + slice
   int begin, end;     // K/V tiles, in the order of the item's list
-  int part;           // slot of its partial result; -1: it is the whole item
+  int part;           // slots of its item's partial results (part_word); -1: it is the whole item
 };
 static_assert(sizeof(Piece) == kChunkRecord * sizeof(int), "record size");
-// An item in pieces: partial results [part, part + parts).
-struct alignas(16) Cut {
-  int token, tokens, head, part, parts;
-  int pad[3];
-};
-static_assert(sizeof(Cut) == kChunkRecord * sizeof(int), "record size");
+// The item's slots are [first, first + count), this piece's is `own`.
+__device__ __forceinline__ int part_word(int own, int first, int count) {
+  return own | first << 10 | count << 20;
+}
+static_assert(2 * kChunkMaxCtas <= 1024, "slots of ten bits");
 
 // The K/V tiles that `tokens` tokens from position `pos` on see: sink tiles [0, s), then
 // [w, e); e = 0: none.
@@ -130,7 +140,7 @@ struct PlanParams {
   const int *cu, *seqlens;
   int* plan;
   int B, T, Hq, Hkv, D, max_keys, window, sinks, ctas;
-  int heads, item_tokens;  // KV heads x slices; tokens of an item
+  int heads, item_tokens;  // KV heads x slices; tokens of an item (two tiles)
   long long max_items;
   int* status;
 };
@@ -142,7 +152,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
   const ChunkLayout at(p.B, p.max_items, p.ctas);
   PlanHeader* const header = reinterpret_cast<PlanHeader*>(p.plan);
   int* const begins = p.plan + at.begins;
-  Cut* const cuts = reinterpret_cast<Cut*>(p.plan + at.cuts);
   int* const tiles = p.plan + at.tiles;  // a KV head's items of the requests before
   Piece* const pieces = reinterpret_cast<Piece*>(p.plan + at.pieces);
   const int tid = threadIdx.x;
@@ -189,17 +198,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     x.head = rest / n;
     const int from = (rest - x.head * n) * p.item_tokens;
     x.token = t0 + from;
-    x.tokens = min(p.item_tokens, n_tok - from);
+    x.tokens = static_cast<uint16_t>(min(p.item_tokens, n_tok - from));
     x.pos = len - n_tok + from;
+    x.flags = ((len & 127) != 0 && (x.pos + x.tokens + 127) / 128 == (len + 127) / 128 ? kRagged : 0) |
+              (n > 1 ? kShared : 0);
     x.begin = 0;
     x.end = KvTiles(x.pos, x.tokens, p.window, p.sinks).count();
     x.part = -1;
+  };
+  const auto cost_of = [&](const Piece& x) {
+    return x.end * (2 * x.tokens > p.item_tokens ? kCostTwo : kCostOne) + kOverhead;
   };
   long long cost = 0;
   for (int i = tid; i < items; i += kPlanThreads) {
     Piece x;
     item(i, x);
-    cost += x.end + kOverhead;
+    cost += cost_of(x);
   }
   long long all;
   scan(cost, smem, all);
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     int w = 0;
     if (i < items) {
       item(i, x);
-      w = x.end + kOverhead;
+      w = cost_of(x);
     }
     long long total;
     const long long from = line + scan(static_cast<long long>(w), smem, total);
@@ -249,18 +263,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     before_items += static_cast<int>(sums >> 32);
     if (w > 0) {
       int piece = i + cuts_before;
-      int part = n_cuts > 0 ? cuts_before + items_before : -1;
-      if (n_cuts > 0) {
-        Cut cut = {x.token, x.tokens, x.head, part, n_cuts + 1, {0, 0, 0}};
-        cuts[items_before] = cut;
-      }
+      const int first = cuts_before + items_before;  // cut items have a slot more than cuts
+      int own = first;
       int last = 0;
       for (int c = c0; c < n && all * c / n < from + w; ++c) {
         const int k = cut_at(c);
         if (k > last && k < steps) {
           x.begin = last;
           x.end = k;
-          x.part = part++;
+          x.part = part_word(own++, first, n_cuts + 1);
           pieces[piece++] = x;
           last = k;
         }
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
       }
       x.begin = last;
       x.end = steps;
-      x.part = part;
+      x.part = n_cuts > 0 ? part_word(own, first, n_cuts + 1) : -1;
       pieces[piece] = x;
     }
   }
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
   }
   if (tid == 0) {
     PlanHeader h = {kMagic, p.B, p.T, p.Hq, p.Hkv, p.D, p.max_keys, p.window, p.sinks, p.ctas,
-                    n_pieces, before_items, {0, 0, 0, 0}};
+                    n_pieces, {0, 0, 0, 0, 0}};
     *header = h;
   }
 }
@@ -288,12 +299,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
 // ------------------------------------------------------------------ attention
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 9;
+constexpr int kLoadKWarp = 9, kLoadVWarp = 10;
 constexpr uint32_t kSubBytes = 128 * 128;  // one [128 rows x 64 bf16] swizzled sub-tile
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kLaunchRegs = 168;  // 65536 / 384, rounded down to a multiple of 8
-constexpr uint32_t kRegsSoftmax = 200;
-constexpr uint32_t kRegsOther = 104;
+constexpr uint32_t kRegsSoftmax = 192;
+constexpr uint32_t kRegsOther = 120;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kLaunchRegs,
               "register split must use exactly the launch allocation");
 constexpr float kLn2 = 0.69314718055994531f;
@@ -335,14 +346,15 @@ struct ChunkParams {
   const int* block_table;
   __nv_bfloat16* o;
   float *lse, *part_o, *part_lse;
+  unsigned long long *flags, token;  // see Parts
   size_t o_bytes, lse_bytes, part_o_bytes, part_lse_bytes;  // bounds checks of debug builds
-  int o_v8, part_v8;  // 32-byte stores
+  int o_v8;  // 32-byte stores
   int* status;
   int B, T, Hq, Hkv, D, num_pages, page_size, max_pages;
   int group, slices, slice_heads, tile_tokens;
   int box_keys, page_rows;  // keys of a K/V box; rows of the caches (num_pages * Hkv * page_size)
   int ctas;
-  long long begins, cuts, pieces;  // the plan's layout
+  long long begins, pieces;  // the plan's layout
   FixedDiv by_page, by_heads, by_slices;
   float scale_log2;  // scale * log2(e)
 };
@@ -354,17 +366,47 @@ __device__ __forceinline__ bool plan_fits(const ChunkParams& p) {
          h->D == p.D && h->max_keys == p.max_pages * p.page_size && h->ctas == p.ctas;
 }
 
-// What all roles know of the plan: this CTA's pieces.
+// What a role knows of the plan: this CTA's pieces.  (Read by each for itself: held in common,
+// it costs the softmax warps registers that they do not have.)
 struct Work {
   const Piece* pieces;
   int begin, end;
   int window, sinks;
 };
+__device__ __forceinline__ int load_int(const int* x) {
+  int y;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(y) : "l"(x));
+  return y;
+}
+__device__ __forceinline__ Work load_work(const ChunkParams& p, bool fits) {
+  const PlanHeader* h = reinterpret_cast<const PlanHeader*>(p.plan);
+  Work work;
+  work.pieces = reinterpret_cast<const Piece*>(p.plan + p.pieces);
+  work.begin = fits ? load_int(p.plan + p.begins + blockIdx.x) : 0;
+  work.end = fits ? load_int(p.plan + p.begins + blockIdx.x + 1) : 0;
+  work.window = load_int(&h->window);
+  work.sinks = load_int(&h->sinks);
+  return work;
+}
 
 __device__ __forceinline__ Piece load_piece(const Piece* x) {
   const int4 a = __ldg(reinterpret_cast<const int4*>(x));
   const int4 b = __ldg(reinterpret_cast<const int4*>(x) + 1);
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return {a.x, static_cast<uint16_t>(a.y), static_cast<uint16_t>(a.y >> 16), a.z, a.w,
+          b.x, b.y, b.z, b.w};
+}
+
+// The fields that the softmax warps need only after a piece's tiles, read once more (from L1):
+// kept, they would not fit the registers.
+struct PieceEnd {
+  int token, head, part;
+};
+__device__ __forceinline__ PieceEnd load_piece_end(const Piece* x) {
+  PieceEnd y;
+  asm volatile("ld.global.nc.b32 %0, [%3];\n\tld.global.nc.b32 %1, [%3+16];\n\t"
+               "ld.global.nc.b32 %2, [%3+28];"
+               : "=r"(y.token), "=r"(y.head), "=r"(y.part) : "l"(x));
+  return y;
 }
 
 // Bounded wait that also gives up as soon as another role has aborted.
@@ -388,126 +430,136 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* 
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, bars));
 }
 
-// ------------------------------------------------------------------ producer
-// K tiles run ahead of V tiles by one step (two in items of one tile, whose slots take
-// them by turns): K_0 (K_1), then pairs V_k, K_k+1 (K_k+2) that complete on V_k's barrier,
-// which the MMA warp waits for once.
+// ------------------------------------------------------------------ producers
+// Two warps share a ring of stages, one for Q and K, one for V.  K tiles run ahead of V tiles by
+// one step, or two in items of one tile, whose slots take them by turns: K_0 (K_1), then V_k,
+// K_k+1 (K_k+2), which is the order in which the MMA warp needs them and in which they take
+// the stages.  (What bounds them is the issue of the copies, four a tile of 64-key pages at D =
+// 128: one warp for both needed TODO us a step.)
 template <int D>
-__device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                          const ChunkParams& p, const Work& work, uint8_t* sQ, uint8_t* sKV,
-                          Bars* bars, int lane) {
+__device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const ChunkParams& p,
+                          const Work& work, uint8_t* sQ, uint8_t* sKV, Bars* bars, int lane,
+                          bool loads_v) {
   using C = Cfg<D>;
-  uint32_t kv_ctr = 0, q_ctr = 0;
+  uint32_t before = 0, q_ctr = 0;  // tiles of the pieces before; pieces with tiles
   bool ok = true;
   const uint64_t pol_q = policy_evict_first();
-  const uint64_t pol_kv = policy_evict_last();
+  // K and V that several items read are kept in L2; those that one reads are let go, or a
+  // batch of single tokens would push the others out.
+  const uint64_t pol_keep = policy_evict_last();
   const int boxes = 128 / p.box_keys;      // of a K/V tile
   const int batch = 32 / boxes;            // tiles whose boxes the lanes look up at once
   const int my_tile = lane / boxes, my_box = lane % boxes;
   const uint32_t box_bytes = p.box_keys * 128;
   const uint32_t q_bytes = p.slice_heads * p.tile_tokens * 128 * C::kSub;
   bool bad_page = false;
-  for (int i = work.begin; i < work.end && ok; ++i) {
-    const Piece x = load_piece(work.pieces + i);
-    const int n = x.end - x.begin;
-    if (n <= 0) continue;
-    const bool dual = x.tokens <= p.tile_tokens;
+  // A piece, and the rows of the caches where this lane's boxes of two batches of its tiles
+  // begin.  The next one's are on their way while a piece is loaded.
+  struct Ahead {
+    Piece x;
+    int g, cur, nxt;
+  };
+  // Row of the caches where this lane's box of tiles [k0, k0 + batch) begins; past their end
+  // where no row sees a key of it.
+  const auto look_up = [&](const Piece& x, int g, int k0) {
+    const int k = x.begin + k0 + my_tile;
+    if (k >= x.end) return p.page_rows;
     const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
-    const int g = p.by_slices.div(x.head);
-    const int h0 = g * p.group + (x.head - g * p.slices) * p.slice_heads;
-    const int* table = p.block_table + static_cast<size_t>(x.row) * p.max_pages;
-    // Row of the caches where this lane's box of tiles [k0, k0 + batch) begins; past their
-    // end where no row sees a key of it.
-    const auto look_up = [&](int k0) {
-      const int k = x.begin + k0 + my_tile;
-      if (k >= x.end) return p.page_rows;
-      const int key = kv.tile(k) * 128 + my_box * p.box_keys;
-      if (key >= kv.hi || (key + p.box_keys <= kv.lo && key >= work.sinks)) return p.page_rows;
-      const int slot = p.by_page.div(key);
-      int page = __ldg(table + slot);
-      if (page < 0 || page >= p.num_pages) {
-        bad_page = true;
-        page = 0;
-      }
-      return (page * p.Hkv + g) * p.page_size + key - slot * p.page_size;
-    };
-    int cur = look_up(0), nxt = look_up(batch), cur0 = 0;
-    if (q_ctr > 0 && !(ok = wait_warp(&bars->q_empty, (q_ctr - 1) & 1, bars))) break;
-    if (elect_one()) {
-      mbar_arrive_expect_tx(&bars->q_full, dual ? q_bytes : 2 * q_bytes);
-      for (int t = 0; t < (dual ? 1 : 2); ++t)
-#pragma unroll
-        for (int s = 0; s < C::kSub; ++s)
-          tma_load_3d_hint(sQ + t * C::kTileBytes + s * kSubBytes, tmQ, &bars->q_full, s * 64, h0,
-                           x.token + t * p.tile_tokens, pol_q);
+    const int key = kv.tile(k) * 128 + my_box * p.box_keys;
+    if (key >= kv.hi || (key + p.box_keys <= kv.lo && key >= work.sinks)) return p.page_rows;
+    const int slot = p.by_page.div(key);
+    int page = __ldg(p.block_table + static_cast<size_t>(x.row) * p.max_pages + slot);
+    if (page < 0 || page >= p.num_pages) {
+      bad_page = true;
+      page = 0;
     }
-    __syncwarp();
-    ++q_ctr;
-    auto take_stage = [&](uint32_t& st) -> bool {
-      st = kv_ctr % C::kStages;
-      bool g = true;
-      if (kv_ctr >= uint32_t(C::kStages))
-        g = wait_or_abort(&bars->kv_empty[st], ((kv_ctr / C::kStages) - 1) & 1, bars);
-      ++kv_ctr;
-      return g;
-    };
-    // Tile k of the piece (all lanes call it; k is in the current batch or the next).
-    auto load_tile = [&](const CUtensorMap* tm, uint32_t st, uint64_t* bar, int k) {
-      for (int b = 0; b < boxes; ++b) {
-        const int at = k - cur0;
-        const int row = at < batch ? __shfl_sync(0xffffffffu, cur, at * boxes + b)
-                                   : __shfl_sync(0xffffffffu, nxt, (at - batch) * boxes + b);
-        if (elect_one()) {
-#pragma unroll
-          for (int s = 0; s < C::kSub; ++s)
-            tma_load_3d_hint(sKV + st * C::kTileBytes + s * kSubBytes + b * box_bytes, tm, bar,
-                             s * 64, row, 0, pol_kv);
-        }
-        __syncwarp();
-      }
-    };
-    auto expect = [&](uint64_t* bar, uint32_t bytes) {
-      if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
-      __syncwarp();
-    };
-    const int ahead = dual ? 2 : 1;
-    for (int k = 0; k < min(ahead, n) && ok; ++k) {
-      uint32_t st;
-      const bool g = take_stage(st);
-      expect(&bars->kv_full[st], C::kTileBytes);
-      load_tile(tmK, st, &bars->kv_full[st], k);
-      ok = __all_sync(0xffffffffu, g);
+    return (page * p.Hkv + g) * p.page_size + key - slot * p.page_size;
+  };
+  const auto look_ahead = [&](int i) {
+    Ahead a = {};
+    if (i >= work.end) return a;
+    a.x = load_piece(work.pieces + i);
+    a.g = p.by_slices.div(a.x.head);
+    a.cur = look_up(a.x, a.g, 0);
+    a.nxt = look_up(a.x, a.g, batch);
+    return a;
+  };
+  Ahead ahead_of = look_ahead(work.begin);
+  uint32_t last = 0;  // this warp's last tile, as a count of all
+  for (int i = work.begin; i < work.end && ok; ++i) {
+    const Piece x = ahead_of.x;
+    const int g = ahead_of.g;
+    int cur = ahead_of.cur, nxt = ahead_of.nxt, cur0 = 0;
+    const int n = x.end - x.begin;
+    if (n <= 0) {
+      ahead_of = look_ahead(i + 1);
+      continue;
     }
-    for (int k = 0; k < n && ok; ++k) {
-      // V_k and K_k+ahead lie in this batch or the next.
+    const bool dual = x.tokens <= p.tile_tokens;
+    const uint64_t pol_kv = x.flags & kShared ? pol_keep : pol_q;
+    const int ahead = min(dual ? 2 : 1, n);
+    // Tile k of this warp's kind into its stage.
+    auto load = [&](int k) {
+      // V_k lies in the batch of tile k or the one before.
       if (k == cur0 + batch) {
         cur0 = k;
         cur = nxt;
-        nxt = look_up(k + batch);
+        nxt = look_up(x, g, k + batch);
       }
-      uint32_t sv, sk = 0;
-      const bool pair = k + ahead < n;
-      bool good = take_stage(sv);
-      if (pair) good &= take_stage(sk);
-      expect(&bars->kv_full[sv], pair ? 2 * C::kTileBytes : C::kTileBytes);
-      load_tile(tmV, sv, &bars->kv_full[sv], k);
-      if (pair) {
-        load_tile(tmK, sk, &bars->kv_full[sv], k + ahead);
-        if (elect_one()) mbar_arrive(&bars->kv_full[sk]);
-        __syncwarp();
+      const uint32_t at = before + (loads_v      ? ahead + k + min(k, n - ahead)
+                                    : k < ahead ? k
+                                                : 2 * k - ahead + 1);
+      const uint32_t st = at % C::kStages;
+      bool got = true;
+      if (at >= uint32_t(C::kStages))
+        got = wait_or_abort(&bars->kv_empty[st], (at / C::kStages - 1) & 1, bars);
+      int row[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        row[b] = __shfl_sync(0xffffffffu, cur, (k - cur0) * boxes + b);
+      if (elect_one()) {
+        uint64_t* bar = &bars->kv_full[st];
+        uint8_t* to = sKV + st * C::kTileBytes;
+        mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (b < boxes) {
+#pragma unroll
+            for (int s = 0; s < C::kSub; ++s)
+              tma_load_3d_hint(to + s * kSubBytes + b * box_bytes, tm, bar, s * 64, row[b], 0,
+                               pol_kv);
+          }
       }
-      ok = __all_sync(0xffffffffu, good);
+      last = at + 1;
+      ok = __all_sync(0xffffffffu, got);
+    };
+    if (!loads_v) {
+      for (int k = 0; k < ahead && ok; ++k) load(k);
+      if (!ok || (q_ctr > 0 && !(ok = wait_warp(&bars->q_empty, (q_ctr - 1) & 1, bars)))) break;
+      if (elect_one()) {
+        const int h0 = g * p.group + (x.head - g * p.slices) * p.slice_heads;
+        mbar_arrive_expect_tx(&bars->q_full, dual ? q_bytes : 2 * q_bytes);
+        for (int t = 0; t < (dual ? 1 : 2); ++t)
+#pragma unroll
+          for (int s = 0; s < C::kSub; ++s)
+            tma_load_3d_hint(sQ + t * C::kTileBytes + s * kSubBytes, tmQ, &bars->q_full, s * 64, h0,
+                             x.token + t * p.tile_tokens, pol_q);
+      }
+      __syncwarp();
     }
+    ++q_ctr;
+    ahead_of = look_ahead(i + 1);
+    for (int k = loads_v ? 0 : ahead; k < n && ok; ++k) load(k);
+    before += 2 * n;
   }
   if (bad_page) record_status(p.status, ATTN_ERR_INVALID_ARG);
   if (!ok) record_status(p.status, ATTN_ERR_TIMEOUT);
-  // Let every copy that this thread issued land before the CTA can exit.  Those of stages
-  // reused since have landed (the MMA warp released them after it saw them, and with a V
-  // the K that counts on its barrier).
-  const uint32_t last = kv_ctr;
-  for (uint32_t c = (last > uint32_t(C::kStages) ? last - C::kStages : 0); c < last; ++c)
+  // Let every copy land before the CTA can exit: each stage's last one, whichever warp's (the MMA
+  // warp released those before it after it saw them).
+  const uint32_t all = ok ? before : last;
+  for (uint32_t c = all > uint32_t(C::kStages) ? all - C::kStages : 0; c < all; ++c)
     (void)mbar_wait(&bars->kv_full[c % C::kStages], (c / C::kStages) & 1);
-  if (q_ctr > 0) (void)mbar_wait(&bars->q_full, (q_ctr - 1) & 1);
+  if (!loads_v && q_ctr > 0) (void)mbar_wait(&bars->q_full, (q_ctr - 1) & 1);
 }
 
 // ------------------------------------------------------------------ MMA issuer
@@ -533,10 +585,10 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   constexpr uint32_t kLoK = static_cast<uint32_t>(kDescK);
   constexpr uint32_t kLoV = static_cast<uint32_t>(kDescV);
   constexpr uint32_t kTile16 = C::kTileBytes >> 4;
-  const uint32_t q_lo = kLoK + (smem_u32(sQ) >> 4);
-  const uint32_t k_lo = kLoK + (smem_u32(sKV) >> 4);
-  const uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
-  uint32_t kv_ctr = 0, q_ctr = 0;
+  uint32_t q_lo = kLoK + (smem_u32(sQ) >> 4);
+  uint32_t k_lo = kLoK + (smem_u32(sKV) >> 4);
+  uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
+  uint32_t q_ctr = 0;
   uint32_t p_phase = 0;  // bit t: slot t's
   bool ok = true;
 
@@ -581,16 +633,13 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
     return good;
   };
   // Per-lane outcome (no vote: one vote per piece makes the decision to stop uniform).
+  uint32_t stage = 0, stage_phase = 0;
   auto acquire_kv = [&](uint32_t& st) -> bool {
-    st = kv_ctr % C::kStages;
-    const bool got = wait_or_abort(&bars->kv_full[st], (kv_ctr / C::kStages) & 1, bars);
-    ++kv_ctr;
+    const bool got = wait_or_abort(&bars->kv_full[stage], stage_phase, bars);
+    st = stage;
+    stage = st + 1 == C::kStages ? 0 : st + 1;
+    if (stage == 0) stage_phase ^= 1;
     return got;
-  };
-  auto next_stage = [&] {  // landed with a V: counted on its barrier
-    const uint32_t st = kv_ctr % C::kStages;
-    ++kv_ctr;
-    return st;
   };
 
   for (int i = work.begin; i < work.end && ok; ++i) {
@@ -599,77 +648,85 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
     if (n <= 0) continue;
     const bool dual = x.tokens <= p.tile_tokens;
     const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
-    // Keys that no row sees may hold anything, and a weight of 0 times NaN is NaN: their
-    // rows of V become zero (those of whole boxes are loaded as zeros).
+    // Keys that no token sees may hold anything, and a weight of 0 times NaN is NaN: their
+    // rows of V become zero (those of whole boxes are loaded as zeros).  Keys behind an item's
+    // last position, but not the request's, are later tokens'.  Of the item's tiles these are the
+    // last, where the window begins and where the sinks end: `clear` is the next of them.
+    const int last_tile = x.flags & kRagged ? kv.count() - 1 : kMaxKeys;
+    const auto next_clear = [&](int k) {
+      if (k <= kv.s - 1 && (work.sinks & 127) != 0) return kv.s - 1;
+      if (k <= kv.s && (kv.lo & 127) != 0) return kv.s;
+      return last_tile;
+    };
+    int clear = next_clear(x.begin);
     auto clear_unseen = [&](uint32_t vst, int k) {
-      const int j = kv.tile(x.begin + k), key0 = 128 * j;
-      if (j != kv.e - 1 && j != kv.w && j != kv.s - 1) return;
+      const int key0 = 128 * kv.tile(k);
       uint8_t* tile = sKV + vst * C::kTileBytes;
       const int lo = max(work.sinks - key0, 0), hi = min(kv.lo - key0, 128);
       if (lo < hi) zero_rows<D>(tile, lo, hi, lane);
-      if (kv.hi < key0 + 128) zero_rows<D>(tile, kv.hi - key0, 128, lane);
+      if (k == last_tile) zero_rows<D>(tile, kv.hi - key0, 128, lane);
       fence_proxy_async_smem();
       __syncwarp();
+      clear = k < last_tile ? next_clear(k + 1) : kMaxKeys;
     };
     if (!(ok = wait_warp(&bars->q_full, q_ctr & 1, bars))) break;
     ++q_ctr;
     bool good = true;
-    if (dual) {
-      // Slot k & 1 takes tile k.
-      for (int k = 0; k < min(2, n); ++k) {
-        uint32_t kst;
-        good &= acquire_kv(kst);
-        tc_fence_after();
-        issue_s(k, 0, kst);
-        tc_commit_w(&bars->kv_empty[kst]);
-      }
-      if (n <= 2) tc_commit_w(&bars->q_empty);
-      for (int k = 0; k < n; ++k) {
-        uint32_t vst, nst = 0;
-        const int t = k & 1;
-        const bool more = k + 2 < n;
-        good &= acquire_kv(vst);
-        if (more) nst = next_stage();
-        clear_unseen(vst, k);
-        good &= issue_pv(t, vst, k < 2);
-        if (more) {
-          issue_s(t, 0, nst);
-          tc_commit_w(&bars->kv_empty[nst]);
-          if (k + 3 == n) tc_commit_w(&bars->q_empty);
-        } else {
-          tc_commit_w(&bars->o_full[t]);
-        }
-        tc_commit_w(&bars->kv_empty[vst]);
-      }
-    } else {
-      uint32_t kst;
+    int k = x.begin;  // the tile whose V comes next
+    // Turn t of a round: slot t adds P V of a tile and scores its next one.  With two query
+    // tiles both slots take each K/V tile, with one (DUAL) every second tile is a slot's.  (Two
+    // instances: the time between the MMAs' issues is lost to the tensor core, and with one
+    // for both a step of two tiles took 7 % longer.)
+    const auto run = [&](auto dual_constant) {
+      constexpr bool DUAL = decltype(dual_constant)::value;
+      // (What the operands' addresses make is worked out here: kept for both instances, it
+      // would not fit the registers.)
+      asm volatile("" : "+r"(q_lo), "+r"(k_lo), "+r"(v_lo), "+r"(tmem));
+      uint32_t vst = 0, kst = 0;
       good &= acquire_kv(kst);
       tc_fence_after();
       issue_s(0, 0, kst);
-      issue_s(1, 1, kst);
+      if (DUAL && n > 1) {
+        tc_commit_w(&bars->kv_empty[kst]);
+        good &= acquire_kv(kst);
+        tc_fence_after();
+      }
+      if (!DUAL || n > 1) issue_s(1, DUAL ? 0 : 1, kst);
       tc_commit_w(&bars->kv_empty[kst]);
-      if (n == 1) tc_commit_w(&bars->q_empty);
-      for (int k = 0; k < n; ++k) {
-        uint32_t vst, nst = 0;
-        const bool more = k + 1 < n;
-        good &= acquire_kv(vst);
-        if (more) nst = next_stage();
-        clear_unseen(vst, k);
+      if (n <= (DUAL ? 2 : 1)) tc_commit_w(&bars->q_empty);
+      for (int left = n; left > 0;) {  // tiles whose P V is to come
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          good &= issue_pv(t, vst, k == 0);
-          if (more)
-            issue_s(t, t, nst);
-          else
+          const bool more = left > (DUAL ? 2 : 1);
+          if (DUAL || t == 0) {
+            good &= acquire_kv(vst);
+            if (k == clear) clear_unseen(vst, k);
+          }
+          good &= issue_pv(t, vst, k < x.begin + (DUAL ? 2 : 1));
+          if (more) {
+            if (DUAL || t == 0) {
+              good &= acquire_kv(kst);
+              tc_fence_after();
+            }
+            issue_s(t, DUAL ? 0 : t, kst);
+          } else {
             tc_commit_w(&bars->o_full[t]);
-        }
-        tc_commit_w(&bars->kv_empty[vst]);
-        if (more) {
-          tc_commit_w(&bars->kv_empty[nst]);
-          if (k + 2 == n) tc_commit_w(&bars->q_empty);
+          }
+          if (DUAL || t == 1) {
+            tc_commit_w(&bars->kv_empty[vst]);
+            if (more) tc_commit_w(&bars->kv_empty[kst]);
+            if (left == (DUAL ? 3 : 2)) tc_commit_w(&bars->q_empty);  // after the last scores
+            ++k;
+            --left;
+            if (DUAL && left == 0) break;
+          }
         }
       }
-    }
+    };
+    if (dual)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
     ok = __all_sync(0xffffffffu, good);
   }
   if (!ok) record_status(p.status, ATTN_ERR_TIMEOUT);
@@ -678,7 +735,124 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   (void)mbar_wait(&bars->mma_done, 0);
 }
 
+// ------------------------------------------------------------------ merging
+// The pieces of an item run in different CTAs.  Each softmax warp has 32 rows of one (in items of one
+// tile, half their columns), and meets the warps of the same number in the item's other
+// pieces: one that finds their partial results there merges its own with them and writes
+// the rows; one that does not leaves its own for them, sets its flag, and looks once more (of
+// two that finish together at least one then sees both flags).  Nobody waits.  Sums run in the
+// order of the pieces whoever adds them, so that results do not depend on who was last.
+//
+// A flag holds the call's token.  Tokens differ from call to call, so that the workspace need
+// not be cleared; whoever merges clears the flags, for calls in a captured graph, which
+// come again with the same token.
+//
+// (A second kernel that merged took 11 to 12 us a call: its partial results, written and read by
+// all pieces, and its launch.)
+template <int D>
+struct Parts {
+  const ChunkParams& p;
+  int own, first, count;  // of the item's slots
+  int tile, tile_row, unit, lane;
+  float top, scale;  // of the weights 2^(lse - top) * scale
+
+  __device__ __forceinline__ Parts(const ChunkParams& p, int word, int tile, int tile_row, int unit,
+                                   int lane)
+      : p(p), tile(tile), tile_row(tile_row), unit(unit), lane(lane) {
+    first = word >> 10 & 1023;
+    own = (word & 1023) - first;
+    count = word >> 20;
+  }
+  __device__ __forceinline__ unsigned long long* flag(int s) const {
+    return p.flags + (first + s) * 8 + unit;
+  }
+  __device__ __forceinline__ float* lse(int s) const {
+    return p.part_lse + ((first + s) * 8 + unit) * 32 + lane;
+  }
+  // Columns c to c + 3 of the row (the lanes' lie side by side).
+  __device__ __forceinline__ float4* columns(int s, int c) const {
+    return reinterpret_cast<float4*>(p.part_o) +
+           (static_cast<size_t>(2 * (first + s) + tile) * (D / 4) + c / 4) * 128 + tile_row;
+  }
+
+  __device__ __forceinline__ bool others_done() const {
+    bool done = true;
+    for (int s = lane; s < count; s += 32) {
+      if (s == own) continue;
+      unsigned long long x;
+      asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(x) : "l"(flag(s)) : "memory");
+      done = done && x == p.token;
+    }
+    done = __all_sync(0xffffffffu, done);
+    __syncwarp();
+    return done;
+  }
+  template <int N>
+  __device__ __forceinline__ void store(int c, const uint32_t (&w)[N]) const {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      float4* to = columns(own, c + 4 * q);
+      if (store_in_bounds(to, 16, p.part_o, p.part_o_bytes, p.status))
+        *to = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
+                          __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
+    }
+  }
+  __device__ __forceinline__ void announce(float lse2) const {
+    *lse(own) = lse2;
+    __syncwarp();
+    __threadfence();
+    if (lane == 0)
+      asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(flag(own)), "l"(p.token) : "memory");
+    __syncwarp();
+    __threadfence();  // the flag is set before the others' are read
+  }
+  // The row's weights, and its LSE (log2 domain) of all pieces.
+  __device__ __forceinline__ float weigh(float lse2) {
+    top = lse2;
+    for (int s = 0; s < count; ++s)
+      if (s != own) top = fmaxf(top, *lse(s));
+    if (top == -INFINITY) {
+      top = scale = 0.f;
+      return -INFINITY;
+    }
+    float sum = 0.f;
+    for (int s = 0; s < count; ++s) sum += ex2((s == own ? lse2 : *lse(s)) - top);
+    scale = 1.f / sum;
+    return top + log2f(sum);
+  }
+  // Columns [c, c + N) of all pieces; own_columns(w): of this one, whose LSE is lse2.
+  template <int N, typename Own>
+  __device__ __forceinline__ void merge(int c, float lse2, uint32_t (&w)[N], Own own_columns) const {
+    float sum[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = 0.f;
+    for (int s = 0; s < count; ++s) {
+      const float weight = ex2((s == own ? lse2 : *lse(s)) - top) * scale;
+      if (s == own) {
+        own_columns(w);
+      } else {
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) {
+          const float4 x = *columns(s, c + 4 * q);
+          w[4 * q] = __float_as_uint(x.x), w[4 * q + 1] = __float_as_uint(x.y);
+          w[4 * q + 2] = __float_as_uint(x.z), w[4 * q + 3] = __float_as_uint(x.w);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] = fmaf(weight, __uint_as_float(w[e]), sum[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = __float_as_uint(sum[e]);
+  }
+  __device__ __forceinline__ void reset() const {
+    for (int s = lane; s < count; s += 32) *flag(s) = 0;
+  }
+};
+
 // ------------------------------------------------------------------ softmax
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&w)[32]) { tmem_ld32(at, w); }
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&w)[64]) { tmem_ld64(at, w); }
+
 template <int D>
 __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars, float2* stats,
                              uint32_t tmem, int warp, int lane) {
@@ -699,33 +873,32 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
 
   for (int i = work.begin; i < work.end && ok; ++i) {
     const Piece x = load_piece(work.pieces + i);
-    const int n = x.end - x.begin;
     const bool dual = x.tokens <= p.tile_tokens;
-    const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
-    const int g = p.by_slices.div(x.head);
-    const int slice_head = (x.head - g * p.slices) * p.slice_heads + row_head;
+    const int kv_head = p.by_slices.div(x.head);
+    const int slice_head = (x.head - kv_head * p.slices) * p.slice_heads + row_head;
     const int token = row_token + (dual ? 0 : t * p.tile_tokens);  // of the item's
     const bool row_valid =
         row_token < p.tile_tokens && token < x.tokens && slice_head < p.group;
     const bool warp_valid = __any_sync(0xffffffffu, row_valid);
+    const int first_token = __shfl_sync(0xffffffffu, token, 0);
+    // Last key that the row sees (nobody's rows take their warp's first one's: no masks more),
+    // and the first of its window.
+    const int limit = x.pos + (row_valid ? token : first_token);
+    const int win_lo = limit - work.window + 1;
     // This slot's tiles of the piece: all, or every second one.
-    const int k0 = dual ? t : 0, dk = dual ? 2 : 1;
-    // Last key that the row sees, and first of its window (rows that are nobody's: all keys,
-    // which spares their warp the masks).
-    const int limit = row_valid ? x.pos + token : kMaxKeys;
-    const int win_lo = row_valid ? limit - work.window + 1 : -kMaxKeys;
-
-    // Where the row's results go.
-    const bool part = x.part >= 0;
-    const int row_at = dual ? tile_row : t * 128 + tile_row;  // in the partial result
-    const size_t at = part ? static_cast<size_t>(x.part) * 256 + row_at
-                           : static_cast<size_t>(x.token + token) * p.Hq + g * p.group + slice_head;
-    float* const lse_ptr = (part ? p.part_lse : p.lse) + at;
-    const size_t lse_bytes = part ? p.part_lse_bytes : p.lse_bytes;
+    const int k_first = x.begin + (dual ? t : 0), dk = dual ? 2 : 1;
+    int k = k_first;
+    int sink_tiles, skip;  // tiles from sink_tiles on lie `skip` further on
+    {
+      const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
+      sink_tiles = kv.s;
+      skip = kv.w - kv.s;
+    }
 
     float m = -INFINITY;  // reference maximum (log2 domain)
     float l = 0.f;
-    for (int k = k0; k < n; k += dk) {
+    bool first = true;
+    for (; k < x.end; k += dk) {
       ok = wait_warp(&bars->s_full[t], s_phase, bars);
       if (!ok) break;
       s_phase ^= 1;
@@ -743,7 +916,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
       uint32_t sa[64], sb[64];
       tmem_ld64(tS, sa);
       tmem_ld64_nowait(tS + 64, sb);
-      const int key0 = kv.tile(x.begin + k) * 128;
+      const int key0 = (k < sink_tiles ? k : k + skip) * 128;
       const bool need_mask = __any_sync(
           0xffffffffu, key0 + 127 > limit || (key0 < win_lo && key0 + 127 >= work.sinks));
       auto mask_half = [&](uint32_t(&y)[64], int h) {
@@ -777,7 +950,8 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
 
       bool rescale = false;
       float alpha = 1.f;
-      if (k == k0) {
+      if (first) {
+        first = false;
         m = m_tile;
       } else if (row_valid && m_tile - m > kRescaleThreshold) {  // false when both are -inf
         alpha = ex2(m - m_tile);
@@ -844,7 +1018,8 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     }
     if (!ok) break;
 
-    const bool has_own = n > k0;  // (one tile in all: slot 1 of a dual item has none)
+    const bool has_own = k != k_first;  // (one tile in all: slot 1 of a dual item has none)
+    const int n = x.end - x.begin;
     if (has_own) {
       ok = wait_warp(&bars->o_full[t], o_phase, bars);
       if (!ok) break;
@@ -872,60 +1047,121 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     w_own *= inv_l;
     w_other *= inv_l;
+    const float own_lse = l > 0.f ? m + log2f(l) : -INFINITY;  // log2 domain
+    const PieceEnd to = load_piece_end(work.pieces + i);
+    const auto row_of = [&] {  // of O and LSE
+      const int kv_head = p.by_slices.div(to.head);
+      return static_cast<size_t>(to.token + row_token + (dual ? 0 : t * p.tile_tokens)) * p.Hq +
+             kv_head * p.group + (to.head - kv_head * p.slices) * p.slice_heads + row_head;
+    };
     // Lane pairs swap half their segments (pair_transpose8), so that each store writes 64
-    // contiguous bytes of a row.  A merged row's halves are each written by one slot.
+    // contiguous bytes of a row.
     const int pb = lane & 1;
-    const int c_begin = dual ? t * (D / 2) : 0, c_end = dual ? (t + 1) * (D / 2) : D;
     const unsigned valid = __ballot_sync(0xffffffffu, row_valid);
     const bool even_valid = valid >> (lane & ~1) & 1u, odd_valid = valid >> (lane | 1) & 1u;
-    const size_t other_at = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(at), 1);
-    const size_t even_at = pb ? other_at : at, odd_at = pb ? at : other_at;
-#pragma unroll 1
-    for (int c = c_begin; c < c_end; c += 32) {
-      uint32_t w[32];
-      if (has_own) {
-        tmem_ld32(tO + c, w);
+    const auto store_columns = [&](int c, uint32_t* w, __nv_bfloat16* even, __nv_bfloat16* odd) {
+      uint32_t v[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * w_own);
+      for (int e = 0; e < 16; ++e)
+        v[e] = pack_bf16x2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+      pair_transpose8(v, lane);
+      if (even_valid && store_in_bounds(even + c, 32, p.o, p.o_bytes, p.status))
+        st_global_8w_hint(even + c, &v[0], p.o_v8, pol_o);
+      if (odd_valid && store_in_bounds(odd + c, 32, p.o, p.o_bytes, p.status))
+        st_global_8w_hint(odd + c, &v[8], p.o_v8, pol_o);
+    };
+    const auto pair_rows = [&](size_t at, __nv_bfloat16*& even, __nv_bfloat16*& odd) {
+      const size_t other = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(at), 1);
+      even = p.o + (pb ? other : at) * D + 16 * pb;
+      odd = p.o + (pb ? at : other) * D + 16 * pb;
+    };
+    if (!dual && to.part < 0 && n > 0) {
+      // A whole item of two tiles: 64 columns of O at a time, the next ones on their way.  (The
+      // time of an item around its tiles is that of this.)
+      uint32_t wa[64], wb[64];
+      tmem_ld64(tO, wa);
+      if constexpr (D == 128) tmem_ld64_nowait(tO + 64, wb);
+      const size_t at = row_of();
+      __nv_bfloat16 *even, *odd;
+      pair_rows(at, even, odd);
+      const auto scaled = [&](uint32_t(&w)[64], int c) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * w_own);
+        store_columns(c, &w[0], even, odd);
+        store_columns(c + 32, &w[32], even, odd);
+      };
+      scaled(wa, 0);
+      if constexpr (D == 128) {
+        tmem_ld_wait64(wb);
+        scaled(wb, 64);
+      }
+      if (row_valid && store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
+        p.lse[at] = own_lse * kLn2;
+      continue;
+    }
+    // Columns [c, c + N) of the row's result of this piece.
+    const auto own_columns = [&](int c, auto& w) {
+      constexpr int N = sizeof(w) / sizeof(w[0]);
+      if (has_own) {
+        load_columns(tO + c, w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * w_own);
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = 0u;
+        for (int e = 0; e < N; ++e) w[e] = 0u;
       }
-      if (has_other) {
-        uint32_t y[32];
-        tmem_ld32(tOther + c, y);
+      if (N == 32 && has_other) {
+        uint32_t y[N];
+        load_columns(tOther + c, y);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
+        for (int e = 0; e < N; ++e)
           w[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w_other, __uint_as_float(w[e])));
       }
-      if (part) {
-        pair_transpose8(w, lane);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float* e32 = p.part_o + even_at * D + c + 8 * (2 * q + pb);
-          float* d32 = p.part_o + odd_at * D + c + 8 * (2 * q + pb);
-          if (even_valid && store_in_bounds(e32, 32, p.part_o, p.part_o_bytes, p.status))
-            st_global_8w(e32, &w[16 * q], p.part_v8);
-          if (odd_valid && store_in_bounds(d32, 32, p.part_o, p.part_o_bytes, p.status))
-            st_global_8w(d32, &w[16 * q + 8], p.part_v8);
+    };
+    Parts<D> parts(p, to.part, dual ? 0 : t, tile_row, warp, lane);
+    // The columns that this warp writes (of an item of one tile, whose slots are merged, each
+    // slot writes half), N at a time.
+    const auto finish = [&](auto n_constant, int c_begin, int c_end) {
+      constexpr int N = decltype(n_constant)::value;
+      bool write = true;
+      float lse2 = own_lse;
+      if (to.part >= 0) {
+        write = parts.others_done();
+        if (!write) {
+#pragma unroll 1
+          for (int c = c_begin; c < c_end; c += N) {
+            uint32_t w[N];
+            own_columns(c, w);
+            parts.store(c, w);
+          }
+          parts.announce(own_lse);
+          write = parts.others_done();
         }
-      } else {
-        uint32_t v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          v[e] = pack_bf16x2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
-        pair_transpose8(v, lane);
-        __nv_bfloat16* e16 = p.o + even_at * D + c + 16 * pb;
-        __nv_bfloat16* d16 = p.o + odd_at * D + c + 16 * pb;
-        if (even_valid && store_in_bounds(e16, 32, p.o, p.o_bytes, p.status))
-          st_global_8w_hint(e16, &v[0], p.o_v8, pol_o);
-        if (odd_valid && store_in_bounds(d16, 32, p.o, p.o_bytes, p.status))
-          st_global_8w_hint(d16, &v[8], p.o_v8, pol_o);
+        if (write) lse2 = parts.weigh(own_lse);
       }
-    }
-    if (row_valid && (!dual || t == 0) &&
-        store_in_bounds(lse_ptr, 4, part ? p.part_lse : p.lse, lse_bytes, p.status))
-      *lse_ptr = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (!write) return;
+      const size_t at = row_of();
+      __nv_bfloat16 *even, *odd;
+      pair_rows(at, even, odd);
+#pragma unroll 1
+      for (int c = c_begin; c < c_end; c += N) {
+        uint32_t w[N];
+        if (to.part >= 0)
+          parts.merge(c, own_lse, w, [&](auto& y) { own_columns(c, y); });
+        else
+          own_columns(c, w);
+#pragma unroll
+        for (int e = 0; e < N; e += 32) store_columns(c + e, &w[e], even, odd);
+      }
+      if (row_valid && (!dual || t == 0) &&
+          store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
+        p.lse[at] = lse2 * kLn2;
+      if (to.part >= 0) parts.reset();
+    };
+    if (dual)
+      finish(std::integral_constant<int, 32>{}, t * (D / 2), (t + 1) * (D / 2));
+    else
+      finish(std::integral_constant<int, 64>{}, 0, D);
     if (dual && n > 0) {
       // The other slot has read this one's O before it is written again.
       tc_fence_before();
@@ -981,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == kLoadKWarp && lane == 0) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -996,23 +1232,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const bool fits = plan_fits(p);
   if (!fits && threadIdx.x == 0) record_status(p.status, ATTN_ERR_INVALID_ARG);
-  const PlanHeader* header = reinterpret_cast<const PlanHeader*>(p.plan);
-  Work work;
-  work.pieces = reinterpret_cast<const Piece*>(p.plan + p.pieces);
-  work.begin = fits ? p.plan[p.begins + blockIdx.x] : 0;
-  work.end = fits ? p.plan[p.begins + blockIdx.x + 1] : 0;
-  work.window = header->window;
-  work.sinks = header->sinks;
-
   if (warp < 8) {
     setmaxnreg_inc<kRegsSoftmax>();
-    softmax_role<D>(p, work, bars, stats, tmem, warp, lane);
+    softmax_role<D>(p, load_work(p, fits), bars, stats, tmem, warp, lane);
   } else {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kMmaWarp) {
-      mma_role<D>(p, work, sQ, sKV, bars, tmem, lane);
-    } else if (warp == kLoadWarp) {
-      load_role<D>(&tmQ, &tmK, &tmV, p, work, sQ, sKV, bars, lane);
+      mma_role<D>(p, load_work(p, fits), sQ, sKV, bars, tmem, lane);
+    } else if (warp == kLoadKWarp || warp == kLoadVWarp) {
+      const bool loads_v = warp == kLoadVWarp;
+      load_role<D>(&tmQ, loads_v ? &tmV : &tmK, p, load_work(p, fits), sQ, sKV, bars, lane, loads_v);
     }
   }
 
@@ -1022,66 +1251,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
-  }
-}
-
-// ------------------------------------------------------------------ merge
-// A CTA column per cut item (grid x), its rows shared out over the warps of grid y: rows'
-// partial results weighted by their LSE, in the order of the keys.
-constexpr int kMergeWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int DPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  grid_dependency_wait();
-  if (!plan_fits(p)) return;
-  const PlanHeader* header = reinterpret_cast<const PlanHeader*>(p.plan);
-  if (static_cast<int>(blockIdx.x) >= header->n_cuts) return;
-  const Cut cut = reinterpret_cast<const Cut*>(p.plan + p.cuts)[blockIdx.x];
-  const bool dual = cut.tokens <= p.tile_tokens;
-  const int g = p.by_slices.div(cut.head);
-  for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < (dual ? 128 : 256);
-       row += gridDim.y * kMergeWarps) {
-    const int t = row >> 7, tile_row = row & 127;
-    const int row_token = p.by_heads.div(tile_row);
-    const int head = (cut.head - g * p.slices) * p.slice_heads + tile_row - row_token * p.slice_heads;
-    const int token = row_token + t * p.tile_tokens;
-    if (row_token >= p.tile_tokens || token >= cut.tokens || head >= p.group) continue;
-    const size_t to = static_cast<size_t>(cut.token + token) * p.Hq + g * p.group + head;
-    const float* lse = p.part_lse + static_cast<size_t>(cut.part) * 256 + row;
-    const float* o = p.part_o + (static_cast<size_t>(cut.part) * 256 + row) * D + lane * DPL;
-    float M = -INFINITY;
-    for (int s = lane; s < cut.parts; s += 32) M = fmaxf(M, lse[s * 256]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float out[DPL];
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) out[e] = 0.f;
-    float total = 0.f;
-    if (M != -INFINITY) {
-      for (int s = 0; s < cut.parts; ++s) {
-        const float w = ex2((lse[s * 256] - M) * kLog2e);
-        total += w;
-        const float* src = o + static_cast<size_t>(s) * 256 * D;
-#pragma unroll
-        for (int e = 0; e < DPL; e += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(src + e);
-          out[e] = fmaf(w, y.x, out[e]);
-          out[e + 1] = fmaf(w, y.y, out[e + 1]);
-        }
-      }
-      const float inv = 1.f / total;
-#pragma unroll
-      for (int e = 0; e < DPL; ++e) out[e] *= inv;
-    }
-    __nv_bfloat16* dst = p.o + to * D + lane * DPL;
-    if (store_in_bounds(dst, 2 * DPL, p.o, p.o_bytes, p.status)) {
-#pragma unroll
-      for (int e = 0; e < DPL; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(out[e], out[e + 1]);
-    }
-    if (lane == 0 && store_in_bounds(p.lse + to, 4, p.lse, p.lse_bytes, p.status))
-      p.lse[to] = M == -INFINITY ? -INFINITY : M + logf(total);
   }
 }
 
@@ -1097,20 +1266,33 @@ cudaError_t launch_impl(const void* q, const void* k, const void* v, const Chunk
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attn_chunk_kernel<D>),
                                    static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;
-  e = launch_programmatic(attn_chunk_kernel<D>, dim3(p.ctas), dim3(kThreads), C::kSmemBytes, stream,
-                          tmQ, tmK, tmV, p);
-  if (e != cudaSuccess) return e;
-  return launch_programmatic(chunk_merge_kernel<D>, dim3(p.ctas, 8), dim3(32 * kMergeWarps), 0,
-                             stream, p);
+  return launch_programmatic(attn_chunk_kernel<D>, dim3(p.ctas), dim3(kThreads), C::kSmemBytes, stream,
+                             tmQ, tmK, tmV, p);
 }
 
+}  // namespace
+
+int chunk_ctas() { return sm_count() < kChunkMaxCtas ? sm_count() : kChunkMaxCtas; }
+
+namespace {
+// A number that no other call has (a counter's, mixed: nothing that a workspace holds by
+// chance), never 0.
+unsigned long long next_token() {
+  static std::atomic<unsigned long long> calls{
+      static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count())};
+  unsigned long long x = calls.fetch_add(1) * 0x9e3779b97f4a7c15ull;
+  x ^= x >> 32;
+  x *= 0xd6e8feb86659fd93ull;
+  x ^= x >> 32;
+  return x != 0 ? x : 1;
+}
 }  // namespace
 
 cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
                               int Hkv, int D, int max_keys, int window, int sinks,
                               cudaStream_t stream, int* status) {
   const ChunkTiling tiling(Hq, Hkv);
-  PlanParams p = {cu, seqlens, plan, B, T, Hq, Hkv, D, max_keys, window, sinks, sm_count()};
+  PlanParams p = {cu, seqlens, plan, B, T, Hq, Hkv, D, max_keys, window, sinks, chunk_ctas()};
   p.heads = Hkv * tiling.slices;
   p.item_tokens = 2 * tiling.tile_tokens;
   p.max_items = tiling.max_items(B, T, Hkv);
@@ -1128,16 +1310,17 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   p.block_table = paged.block_table;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.ctas = sm_count();
+  p.ctas = chunk_ctas();
   const size_t part_rows = 2ull * p.ctas * 256;
   p.part_o = workspace;
   p.part_lse = workspace + part_rows * D;
+  p.flags = reinterpret_cast<unsigned long long*>(p.part_lse + part_rows);
+  p.token = next_token();
   p.o_bytes = static_cast<size_t>(T) * Hq * D * 2;
   p.lse_bytes = static_cast<size_t>(T) * Hq * sizeof(float);
   p.part_o_bytes = part_rows * D * sizeof(float);
   p.part_lse_bytes = part_rows * sizeof(float);
   p.o_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  p.part_v8 = (reinterpret_cast<uintptr_t>(workspace) & 31u) == 0;
   p.status = status;
   p.B = B;
   p.T = T;
@@ -1155,7 +1338,6 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   p.page_rows = paged.num_pages * Hkv * paged.page_size;
   const ChunkLayout layout(B, tiling.max_items(B, T, Hkv), p.ctas);
   p.begins = layout.begins;
-  p.cuts = layout.cuts;
   p.pieces = layout.pieces;
   p.by_page = FixedDiv(paged.page_size);
   p.by_heads = FixedDiv(tiling.slice_heads);

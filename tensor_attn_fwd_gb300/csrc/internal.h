@@ -277,22 +277,25 @@ struct ChunkTiling {
     return (static_cast<long long>(T) / (2 * tile_tokens) + B) * Hkv * slices;
   }
 };
-// Layout of a plan in int32: header, CTAs' pieces, cut items, the requests' item counts,
-// pieces.
+// CTAs that share the work on the current device: one an SM.
+constexpr int kChunkMaxCtas = 512;
+int chunk_ctas();
+// Layout of a plan in int32: header, CTAs' pieces, the requests' item counts, pieces.
 constexpr int kChunkHeader = 16, kChunkRecord = 8;
 struct ChunkLayout {
-  long long begins, cuts, tiles, pieces, total;
+  long long begins, tiles, pieces, total;
   static __host__ __device__ long long align(long long n) { return (n + 7) / 8 * 8; }
   __host__ __device__ ChunkLayout(int B, long long max_items, int ctas) {
     begins = kChunkHeader;
-    cuts = align(begins + ctas + 1);
-    tiles = cuts + static_cast<long long>(kChunkRecord) * ctas;
+    tiles = begins + ctas + 1;
     pieces = align(tiles + B + 1);
     total = pieces + kChunkRecord * (max_items + ctas);
   }
 };
-// Partial results: two of 256 rows for each CTA.
-inline long long chunk_workspace_floats(int ctas, int D) { return 2ll * ctas * 256 * (D + 1); }
+// Partial results, two for each CTA, of 256 rows with their LSE and eight flags of 64 bits.
+inline long long chunk_workspace_floats(int ctas, int D) {
+  return 2ll * ctas * (256 * (D + 1) + 16);
+}
 cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
                               int Hkv, int D, int max_keys, int window, int sinks,
                               cudaStream_t stream, int* status);
