@@ -19,9 +19,8 @@
 //
 // Plan.  Requests differ in their numbers of tokens and keys, so the items' K/V tiles are
 // put in one line and cut into equal parts, one for each CTA; an item that is cut leaves
-// partial results, which are merged by their LSE (attn_combine's formula) by whoever
-// finishes its piece last (see Parts).  The plan depends on the lengths alone: one serves
-// all layers of a step.
+// partial results, which a second kernel merges by their LSE (attn_combine's formula).
+// The plan depends on the lengths alone: one serves all layers of a step.
 //
 // Pages.  A K/V tile is loaded as boxes of 32, 64 or 128 keys (what divides the page), each
 // found through the block table; boxes that no row sees are filled with zeros by a load
@@ -32,8 +31,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -53,7 +50,9 @@ constexpr int kMaxKeys = 1 << 30;  // of a request
 // tiles.
 constexpr int kCostOne = 2, kCostTwo = 3, kOverhead = 5;
 // An item is cut no closer than this to its ends (in tiles): a cut costs partial results.
-constexpr int kSnap = 2;
+constexpr int kSnap = 4;
+// What cuts cost the CTAs that have them: whole items are dealt out if that is as good.
+constexpr int kCutCost = 12;
 // Cost that is worth a CTA of its own.
 constexpr int kMinShare = 8;
 
@@ -82,14 +81,15 @@ struct alignas(16) Piece {
   int row;            // request
   int head;           // KV head * slices + slice
   int begin, end;     // K/V tiles, in the order of the item's list
-  int part;           // slots of its item's partial results (part_word); -1: it is the whole item
+  int part;           // slot of its partial result; -1: it is the whole item
 };
 static_assert(sizeof(Piece) == kChunkRecord * sizeof(int), "record size");
-// The item's slots are [first, first + count), this piece's is `own`.
-__device__ __forceinline__ int part_word(int own, int first, int count) {
-  return own | first << 10 | count << 20;
-}
-static_assert(2 * kChunkMaxCtas <= 1024, "slots of ten bits");
+// An item in pieces: its partial results are those of slots [part, part + parts).
+struct alignas(16) Cut {
+  int token, tokens, head, part, parts;  // parts = 0: an unused record
+  int pad[3];
+};
+static_assert(sizeof(Cut) == kChunkRecord * sizeof(int), "record size");
 
 // The K/V tiles that `tokens` tokens from position `pos` on see: sink tiles [0, s), then
 // [w, e); e = 0: none.
@@ -109,6 +109,7 @@ struct KvTiles {
 
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
+constexpr int kCostLevels = 2048;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Exclusive prefix sum of one value per thread over the CTA; total: their sum.
@@ -152,6 +153,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
   const ChunkLayout at(p.B, p.max_items, p.ctas);
   PlanHeader* const header = reinterpret_cast<PlanHeader*>(p.plan);
   int* const begins = p.plan + at.begins;
+  Piece* const firsts = reinterpret_cast<Piece*>(p.plan + at.firsts);
+  Cut* const cuts = reinterpret_cast<Cut*>(p.plan + at.cuts);
   int* const tiles = p.plan + at.tiles;  // a KV head's items of the requests before
   Piece* const pieces = reinterpret_cast<Piece*>(p.plan + at.pieces);
   const int tid = threadIdx.x;
@@ -206,6 +209,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     x.end = KvTiles(x.pos, x.tokens, p.window, p.sinks).count();
     x.part = -1;
   };
+  __shared__ int counts[kCostLevels];  // items of each cost, then ranks
+  __shared__ int loads[kChunkMaxCtas];
+  for (int i = tid; i < kCostLevels; i += kPlanThreads) counts[i] = 0;
+  for (int i = tid; i < kChunkMaxCtas; i += kPlanThreads) loads[i] = 0;
+  __syncthreads();
   const auto cost_of = [&](const Piece& x) {
     return x.end * (2 * x.tokens > p.item_tokens ? kCostTwo : kCostOne) + kOverhead;
   };
@@ -214,16 +222,63 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     Piece x;
     item(i, x);
     cost += cost_of(x);
+    if (items >= 2 * p.ctas) atomicAdd(counts + min(cost_of(x), kCostLevels - 1), 1);
   }
   long long all;
   scan(cost, smem, all);
   const long long want = (all + kMinShare - 1) / kMinShare;
   const int n = want < p.ctas ? static_cast<int>(max(want, 1ll)) : p.ctas;
 
+  // Many items: whole ones, longest first, dealt out forth and back over the CTAs.  (Equal items
+  // in any order: it changes no result.)
+  bool dealt = false;
+  if (items >= 2 * p.ctas && n == p.ctas) {
+    __syncthreads();
+    static_assert(kCostLevels == 2 * kPlanThreads, "two levels a thread");
+    const int high = kCostLevels - 1 - 2 * tid;
+    const long long here = counts[high] + counts[high - 1];
+    long long total;
+    const int before = static_cast<int>(scan(here, smem, total));
+    const int of_high = counts[high];
+    __syncthreads();
+    counts[high] = before;
+    counts[high - 1] = before + of_high;
+    __syncthreads();
+    const int rounds = items / n, extra = items - rounds * n;  // the last round may be short
+    const auto begin_of = [&](int c) {
+      return c * rounds + (rounds & 1 ? max(c - (n - extra), 0) : min(c, extra));
+    };
+    for (int i = tid; i < items; i += kPlanThreads) {
+      Piece x;
+      item(i, x);
+      const int rank = atomicAdd(counts + min(cost_of(x), kCostLevels - 1), 1);
+      const int round = rank / n, j = rank - round * n;
+      const int c = round & 1 ? n - 1 - j : j;
+      pieces[begin_of(c) + round] = x;
+      atomicAdd(loads + c, cost_of(x));
+    }
+    __syncthreads();
+    // Taken if no CTA has much more than its share; otherwise the line is cut.
+    long long most = tid < n ? loads[tid] : 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if ((tid & 31) == 0) smem[tid >> 5] = most;
+    __syncthreads();
+    most = smem[tid & 31];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    __syncthreads();
+    dealt = most <= all / n + kCutCost;
+    if (dealt)
+      for (int c = tid; c < n; c += kPlanThreads) begins[c] = begin_of(c);
+  }
+
   // Part c of the line begins at all * c / n.
   long long line = 0;
   int before_cuts = 0, before_items = 0;  // so far: cuts, and items that are cut
-  for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
+  for (int i0 = 0; i0 < items && !dealt; i0 += kPlanThreads) {
     const int i = i0 + tid;
     Piece x = {};
     int w = 0;
@@ -263,15 +318,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     before_items += static_cast<int>(sums >> 32);
     if (w > 0) {
       int piece = i + cuts_before;
-      const int first = cuts_before + items_before;  // cut items have a slot more than cuts
-      int own = first;
+      int part = n_cuts > 0 ? cuts_before + items_before : -1;  // cut items have a slot more than cuts
+      if (n_cuts > 0) cuts[items_before] = {x.token, x.tokens, x.head, part, n_cuts + 1, {0, 0, 0}};
       int last = 0;
       for (int c = c0; c < n && all * c / n < from + w; ++c) {
         const int k = cut_at(c);
         if (k > last && k < steps) {
           x.begin = last;
           x.end = k;
-          x.part = part_word(own++, first, n_cuts + 1);
+          x.part = part++;
           pieces[piece++] = x;
           last = k;
         }
@@ -280,14 +335,21 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
       }
       x.begin = last;
       x.end = steps;
-      x.part = n_cuts > 0 ? part_word(own, first, n_cuts + 1) : -1;
+      x.part = part;
       pieces[piece] = x;
     }
   }
   const int n_pieces = items + before_cuts;
+  __syncthreads();
   for (int c = tid; c <= p.ctas; c += kPlanThreads) {
-    if (c == 0) begins[c] = 0;
+    if (c == 0 && !dealt) begins[c] = 0;
     if (c >= n || items == 0) begins[c] = c == 0 ? 0 : n_pieces;
+    if (c >= before_items && c < p.ctas) cuts[c] = {};
+    // The parts' first pieces once more, where they can be read without their numbers.
+    if (c < p.ctas) {
+      const int i = c < n && items > 0 ? begins[c] : n_pieces;
+      if (i < n_pieces) firsts[c] = pieces[i];
+    }
   }
   if (tid == 0) {
     PlanHeader h = {kMagic, p.B, p.T, p.Hq, p.Hkv, p.D, p.max_keys, p.window, p.sinks, p.ctas,
@@ -330,7 +392,7 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];  // of each Q tile
   uint64_t kv_full[10], kv_empty[10];
   uint64_t s_full[2], p_full[2][2], o_full[2];
   // Items of one tile: the two states of a warp's 32 rows are there to be merged; merged.
@@ -346,7 +408,6 @@ struct ChunkParams {
   const int* block_table;
   __nv_bfloat16* o;
   float *lse, *part_o, *part_lse;
-  unsigned long long *flags, token;  // see Parts
   size_t o_bytes, lse_bytes, part_o_bytes, part_lse_bytes;  // bounds checks of debug builds
   int o_v8;  // 32-byte stores
   int* status;
@@ -354,7 +415,7 @@ struct ChunkParams {
   int group, slices, slice_heads, tile_tokens;
   int box_keys, page_rows;  // keys of a K/V box; rows of the caches (num_pages * Hkv * page_size)
   int ctas;
-  long long begins, pieces;  // the plan's layout
+  long long begins, firsts, cuts, pieces;  // the plan's layout
   FixedDiv by_page, by_heads, by_slices;
   float scale_log2;  // scale * log2(e)
 };
@@ -378,22 +439,23 @@ __device__ __forceinline__ int load_int(const int* x) {
   asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(y) : "l"(x));
   return y;
 }
-__device__ __forceinline__ Work load_work(const ChunkParams& p, bool fits) {
-  const PlanHeader* h = reinterpret_cast<const PlanHeader*>(p.plan);
-  Work work;
-  work.pieces = reinterpret_cast<const Piece*>(p.plan + p.pieces);
-  work.begin = fits ? load_int(p.plan + p.begins + blockIdx.x) : 0;
-  work.end = fits ? load_int(p.plan + p.begins + blockIdx.x + 1) : 0;
-  work.window = load_int(&h->window);
-  work.sinks = load_int(&h->sinks);
-  return work;
-}
-
 __device__ __forceinline__ Piece load_piece(const Piece* x) {
   const int4 a = __ldg(reinterpret_cast<const int4*>(x));
   const int4 b = __ldg(reinterpret_cast<const int4*>(x) + 1);
   return {a.x, static_cast<uint16_t>(a.y), static_cast<uint16_t>(a.y >> 16), a.z, a.w,
           b.x, b.y, b.z, b.w};
+}
+// (All loads at once: one after the other they held up the first K tile by a microsecond.)
+__device__ __forceinline__ Work load_work(const ChunkParams& p) {
+  const PlanHeader* h = reinterpret_cast<const PlanHeader*>(p.plan);
+  Work work;
+  work.pieces = reinterpret_cast<const Piece*>(p.plan + p.pieces);
+  work.begin = load_int(p.plan + p.begins + blockIdx.x);
+  work.end = load_int(p.plan + p.begins + blockIdx.x + 1);
+  work.window = load_int(&h->window);
+  work.sinks = load_int(&h->sinks);
+  if (!plan_fits(p)) work.end = work.begin;
+  return work;
 }
 
 // The fields that the softmax warps need only after a piece's tiles, read once more (from L1):
@@ -438,10 +500,13 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* 
 // 128: one warp for both needed TODO us a step.)
 template <int D>
 __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const ChunkParams& p,
-                          const Work& work, uint8_t* sQ, uint8_t* sKV, Bars* bars, int lane,
-                          bool loads_v) {
+                          const Work& work, const Piece& first, uint8_t* sQ, uint8_t* sKV,
+                          Bars* bars, int lane, bool loads_v) {
   using C = Cfg<D>;
-  uint32_t before = 0, q_ctr = 0;  // tiles of the pieces before; pieces with tiles
+  uint32_t before = 0;         // tiles of the pieces before
+  uint32_t q_uses[2] = {0, 0};  // of each Q tile, so far
+  int q_tile = 1;              // items of one tile take the Q tiles by turns: one is loaded while
+                               // the other is in use
   bool ok = true;
   const uint64_t pol_q = policy_evict_first();
   // K and V that several items read are kept in L2; those that one reads are let go, or a
@@ -475,10 +540,11 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
     }
     return (page * p.Hkv + g) * p.page_size + key - slot * p.page_size;
   };
+  // (Read before what says whether there is one: the first K tile waits for it.)
   const auto look_ahead = [&](int i) {
     Ahead a = {};
     if (i >= work.end) return a;
-    a.x = load_piece(work.pieces + i);
+    a.x = i == work.begin ? first : load_piece(work.pieces + i);
     a.g = p.by_slices.div(a.x.head);
     a.cur = look_up(a.x, a.g, 0);
     a.nxt = look_up(a.x, a.g, batch);
@@ -533,21 +599,33 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
       last = at + 1;
       ok = __all_sync(0xffffffffu, got);
     };
-    if (!loads_v) {
-      for (int k = 0; k < ahead && ok; ++k) load(k);
-      if (!ok || (q_ctr > 0 && !(ok = wait_warp(&bars->q_empty, (q_ctr - 1) & 1, bars)))) break;
+    if (dual) q_tile ^= 1;
+    auto load_q = [&](int t, int token) {
+      if (q_uses[t] > 0) ok = wait_warp(&bars->q_empty[t], (q_uses[t] - 1) & 1, bars);
+      if (!ok) return;
       if (elect_one()) {
         const int h0 = g * p.group + (x.head - g * p.slices) * p.slice_heads;
-        mbar_arrive_expect_tx(&bars->q_full, dual ? q_bytes : 2 * q_bytes);
-        for (int t = 0; t < (dual ? 1 : 2); ++t)
+        mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
 #pragma unroll
-          for (int s = 0; s < C::kSub; ++s)
-            tma_load_3d_hint(sQ + t * C::kTileBytes + s * kSubBytes, tmQ, &bars->q_full, s * 64, h0,
-                             x.token + t * p.tile_tokens, pol_q);
+        for (int s = 0; s < C::kSub; ++s)
+          tma_load_3d_hint(sQ + t * C::kTileBytes + s * kSubBytes, tmQ, &bars->q_full[t], s * 64, h0,
+                           token, pol_q);
       }
       __syncwarp();
+      ++q_uses[t];
+    };
+    if (!loads_v) {
+      if (dual) {
+        if (q_tile == 0)
+          load_q(0, x.token);
+        else
+          load_q(1, x.token);
+      }
+      for (int k = 0; k < ahead && ok; ++k) load(k);
+      if (!dual && ok) load_q(0, x.token);
+      if (!dual && ok) load_q(1, x.token + p.tile_tokens);
+      if (!ok) break;
     }
-    ++q_ctr;
     ahead_of = look_ahead(i + 1);
     for (int k = loads_v ? 0 : ahead; k < n && ok; ++k) load(k);
     before += 2 * n;
@@ -559,7 +637,9 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
   const uint32_t all = ok ? before : last;
   for (uint32_t c = all > uint32_t(C::kStages) ? all - C::kStages : 0; c < all; ++c)
     (void)mbar_wait(&bars->kv_full[c % C::kStages], (c / C::kStages) & 1);
-  if (!loads_v && q_ctr > 0) (void)mbar_wait(&bars->q_full, (q_ctr - 1) & 1);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    if (q_uses[t] > 0) (void)mbar_wait(&bars->q_full[t], (q_uses[t] - 1) & 1);
 }
 
 // ------------------------------------------------------------------ MMA issuer
@@ -588,7 +668,8 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   uint32_t q_lo = kLoK + (smem_u32(sQ) >> 4);
   uint32_t k_lo = kLoK + (smem_u32(sKV) >> 4);
   uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
-  uint32_t q_ctr = 0;
+  uint32_t q_phase = 0;  // bit t: Q tile t's
+  int q_tile = 1;        // of items of one tile (see load_role)
   uint32_t p_phase = 0;  // bit t: slot t's
   bool ok = true;
 
@@ -669,8 +750,12 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
       __syncwarp();
       clear = k < last_tile ? next_clear(k + 1) : kMaxKeys;
     };
-    if (!(ok = wait_warp(&bars->q_full, q_ctr & 1, bars))) break;
-    ++q_ctr;
+    if (dual) q_tile ^= 1;
+    const uint32_t q_mine = dual ? 1u << q_tile : 3u;
+    for (int t = 0; t < 2 && ok; ++t)
+      if (q_mine >> t & 1) ok = wait_warp(&bars->q_full[t], q_phase >> t & 1, bars);
+    if (!ok) break;
+    q_phase ^= q_mine;
     bool good = true;
     int k = x.begin;  // the tile whose V comes next
     // Turn t of a round: slot t adds P V of a tile and scores its next one.  With two query
@@ -679,21 +764,25 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
     // for both a step of two tiles took 7 % longer.)
     const auto run = [&](auto dual_constant) {
       constexpr bool DUAL = decltype(dual_constant)::value;
+      const auto release_q = [&] {  // after the last scores
+        if (!DUAL) tc_commit_w(&bars->q_empty[0]);
+        tc_commit_w(&bars->q_empty[DUAL ? q_tile : 1]);
+      };
       // (What the operands' addresses make is worked out here: kept for both instances, it
       // would not fit the registers.)
       asm volatile("" : "+r"(q_lo), "+r"(k_lo), "+r"(v_lo), "+r"(tmem));
       uint32_t vst = 0, kst = 0;
       good &= acquire_kv(kst);
       tc_fence_after();
-      issue_s(0, 0, kst);
+      issue_s(0, DUAL ? q_tile : 0, kst);
       if (DUAL && n > 1) {
         tc_commit_w(&bars->kv_empty[kst]);
         good &= acquire_kv(kst);
         tc_fence_after();
       }
-      if (!DUAL || n > 1) issue_s(1, DUAL ? 0 : 1, kst);
+      if (!DUAL || n > 1) issue_s(1, DUAL ? q_tile : 1, kst);
       tc_commit_w(&bars->kv_empty[kst]);
-      if (n <= (DUAL ? 2 : 1)) tc_commit_w(&bars->q_empty);
+      if (n <= (DUAL ? 2 : 1)) release_q();
       for (int left = n; left > 0;) {  // tiles whose P V is to come
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -708,14 +797,14 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
               good &= acquire_kv(kst);
               tc_fence_after();
             }
-            issue_s(t, DUAL ? 0 : t, kst);
+            issue_s(t, DUAL ? q_tile : t, kst);
           } else {
             tc_commit_w(&bars->o_full[t]);
           }
           if (DUAL || t == 1) {
             tc_commit_w(&bars->kv_empty[vst]);
             if (more) tc_commit_w(&bars->kv_empty[kst]);
-            if (left == (DUAL ? 3 : 2)) tc_commit_w(&bars->q_empty);  // after the last scores
+            if (left == (DUAL ? 3 : 2)) release_q();
             ++k;
             --left;
             if (DUAL && left == 0) break;
@@ -735,119 +824,14 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   (void)mbar_wait(&bars->mma_done, 0);
 }
 
-// ------------------------------------------------------------------ merging
-// The pieces of an item run in different CTAs.  Each softmax warp has 32 rows of one (in items of one
-// tile, half their columns), and meets the warps of the same number in the item's other
-// pieces: one that finds their partial results there merges its own with them and writes
-// the rows; one that does not leaves its own for them, sets its flag, and looks once more (of
-// two that finish together at least one then sees both flags).  Nobody waits.  Sums run in the
-// order of the pieces whoever adds them, so that results do not depend on who was last.
-//
-// A flag holds the call's token.  Tokens differ from call to call, so that the workspace need
-// not be cleared; whoever merges clears the flags, for calls in a captured graph, which
-// come again with the same token.
-//
-// (A second kernel that merged took 11 to 12 us a call: its partial results, written and read by
-// all pieces, and its launch.)
-template <int D>
-struct Parts {
-  const ChunkParams& p;
-  int own, first, count;  // of the item's slots
-  int tile, tile_row, unit, lane;
-  float top, scale;  // of the weights 2^(lse - top) * scale
-
-  __device__ __forceinline__ Parts(const ChunkParams& p, int word, int tile, int tile_row, int unit,
-                                   int lane)
-      : p(p), tile(tile), tile_row(tile_row), unit(unit), lane(lane) {
-    first = word >> 10 & 1023;
-    own = (word & 1023) - first;
-    count = word >> 20;
-  }
-  __device__ __forceinline__ unsigned long long* flag(int s) const {
-    return p.flags + (first + s) * 8 + unit;
-  }
-  __device__ __forceinline__ float* lse(int s) const {
-    return p.part_lse + ((first + s) * 8 + unit) * 32 + lane;
-  }
-  // Columns c to c + 3 of the row (the lanes' lie side by side).
-  __device__ __forceinline__ float4* columns(int s, int c) const {
-    return reinterpret_cast<float4*>(p.part_o) +
-           (static_cast<size_t>(2 * (first + s) + tile) * (D / 4) + c / 4) * 128 + tile_row;
-  }
-
-  __device__ __forceinline__ bool others_done() const {
-    bool done = true;
-    for (int s = lane; s < count; s += 32) {
-      if (s == own) continue;
-      unsigned long long x;
-      asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(x) : "l"(flag(s)) : "memory");
-      done = done && x == p.token;
-    }
-    done = __all_sync(0xffffffffu, done);
-    __syncwarp();
-    return done;
-  }
-  template <int N>
-  __device__ __forceinline__ void store(int c, const uint32_t (&w)[N]) const {
-#pragma unroll
-    for (int q = 0; q < N / 4; ++q) {
-      float4* to = columns(own, c + 4 * q);
-      if (store_in_bounds(to, 16, p.part_o, p.part_o_bytes, p.status))
-        *to = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
-                          __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
-    }
-  }
-  __device__ __forceinline__ void announce(float lse2) const {
-    *lse(own) = lse2;
-    __syncwarp();
-    __threadfence();
-    if (lane == 0)
-      asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(flag(own)), "l"(p.token) : "memory");
-    __syncwarp();
-    __threadfence();  // the flag is set before the others' are read
-  }
-  // The row's weights, and its LSE (log2 domain) of all pieces.
-  __device__ __forceinline__ float weigh(float lse2) {
-    top = lse2;
-    for (int s = 0; s < count; ++s)
-      if (s != own) top = fmaxf(top, *lse(s));
-    if (top == -INFINITY) {
-      top = scale = 0.f;
-      return -INFINITY;
-    }
-    float sum = 0.f;
-    for (int s = 0; s < count; ++s) sum += ex2((s == own ? lse2 : *lse(s)) - top);
-    scale = 1.f / sum;
-    return top + log2f(sum);
-  }
-  // Columns [c, c + N) of all pieces; own_columns(w): of this one, whose LSE is lse2.
-  template <int N, typename Own>
-  __device__ __forceinline__ void merge(int c, float lse2, uint32_t (&w)[N], Own own_columns) const {
-    float sum[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum[e] = 0.f;
-    for (int s = 0; s < count; ++s) {
-      const float weight = ex2((s == own ? lse2 : *lse(s)) - top) * scale;
-      if (s == own) {
-        own_columns(w);
-      } else {
-#pragma unroll
-        for (int q = 0; q < N / 4; ++q) {
-          const float4 x = *columns(s, c + 4 * q);
-          w[4 * q] = __float_as_uint(x.x), w[4 * q + 1] = __float_as_uint(x.y);
-          w[4 * q + 2] = __float_as_uint(x.z), w[4 * q + 3] = __float_as_uint(x.w);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < N; ++e) sum[e] = fmaf(weight, __uint_as_float(w[e]), sum[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = __float_as_uint(sum[e]);
-  }
-  __device__ __forceinline__ void reset() const {
-    for (int s = lane; s < count; s += 32) *flag(s) = 0;
-  }
-};
+// A partial result: the rows' O (by their own sum) in fp32, four columns of all 128 rows of a
+// query tile beside each other, so that a warp's 32 rows are stored and read in whole lines.
+__device__ __forceinline__ size_t part_at(int part, int tile, int D, int column, int tile_row) {
+  return ((static_cast<size_t>(2 * part + tile) * (D / 4) + column / 4) * 128 + tile_row) * 4;
+}
+__device__ __forceinline__ int part_lse_at(int part, int tile, int tile_row) {
+  return (2 * part + tile) * 128 + tile_row;
+}
 
 // ------------------------------------------------------------------ softmax
 __device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&w)[32]) { tmem_ld32(at, w); }
@@ -1118,45 +1102,40 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
           w[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w_other, __uint_as_float(w[e])));
       }
     };
-    Parts<D> parts(p, to.part, dual ? 0 : t, tile_row, warp, lane);
     // The columns that this warp writes (of an item of one tile, whose slots are merged, each
     // slot writes half), N at a time.
     const auto finish = [&](auto n_constant, int c_begin, int c_end) {
       constexpr int N = decltype(n_constant)::value;
-      bool write = true;
-      float lse2 = own_lse;
+      const int tile = dual ? 0 : t;
+      const bool writes_lse = row_valid && (!dual || t == 0);
       if (to.part >= 0) {
-        write = parts.others_done();
-        if (!write) {
 #pragma unroll 1
-          for (int c = c_begin; c < c_end; c += N) {
-            uint32_t w[N];
-            own_columns(c, w);
-            parts.store(c, w);
+        for (int c = c_begin; c < c_end; c += N) {
+          uint32_t w[N];
+          own_columns(c, w);
+#pragma unroll
+          for (int e = 0; e < N; e += 4) {
+            float* y = p.part_o + part_at(to.part, tile, D, c + e, tile_row);
+            if (store_in_bounds(y, 16, p.part_o, p.part_o_bytes, p.status))
+              *reinterpret_cast<uint4*>(y) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
           }
-          parts.announce(own_lse);
-          write = parts.others_done();
         }
-        if (write) lse2 = parts.weigh(own_lse);
+        float* y = p.part_lse + part_lse_at(to.part, tile, tile_row);
+        if (writes_lse && store_in_bounds(y, 4, p.part_lse, p.part_lse_bytes, p.status)) *y = own_lse;
+        return;
       }
-      if (!write) return;
       const size_t at = row_of();
       __nv_bfloat16 *even, *odd;
       pair_rows(at, even, odd);
 #pragma unroll 1
       for (int c = c_begin; c < c_end; c += N) {
         uint32_t w[N];
-        if (to.part >= 0)
-          parts.merge(c, own_lse, w, [&](auto& y) { own_columns(c, y); });
-        else
-          own_columns(c, w);
+        own_columns(c, w);
 #pragma unroll
         for (int e = 0; e < N; e += 32) store_columns(c + e, &w[e], even, odd);
       }
-      if (row_valid && (!dual || t == 0) &&
-          store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
-        p.lse[at] = lse2 * kLn2;
-      if (to.part >= 0) parts.reset();
+      if (writes_lse && store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
+        p.lse[at] = own_lse * kLn2;
     };
     if (dual)
       finish(std::integral_constant<int, 32>{}, t * (D / 2), (t + 1) * (D / 2));
@@ -1193,8 +1172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], 1);
+    }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bars->kv_full[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
@@ -1230,18 +1211,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const bool fits = plan_fits(p);
-  if (!fits && threadIdx.x == 0) record_status(p.status, ATTN_ERR_INVALID_ARG);
+  if (threadIdx.x == 0 && !plan_fits(p)) record_status(p.status, ATTN_ERR_INVALID_ARG);
   if (warp < 8) {
     setmaxnreg_inc<kRegsSoftmax>();
-    softmax_role<D>(p, load_work(p, fits), bars, stats, tmem, warp, lane);
+    softmax_role<D>(p, load_work(p), bars, stats, tmem, warp, lane);
   } else {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kMmaWarp) {
-      mma_role<D>(p, load_work(p, fits), sQ, sKV, bars, tmem, lane);
+      mma_role<D>(p, load_work(p), sQ, sKV, bars, tmem, lane);
     } else if (warp == kLoadKWarp || warp == kLoadVWarp) {
       const bool loads_v = warp == kLoadVWarp;
-      load_role<D>(&tmQ, loads_v ? &tmV : &tmK, p, load_work(p, fits), sQ, sKV, bars, lane, loads_v);
+      const Piece first = load_piece(reinterpret_cast<const Piece*>(p.plan + p.firsts) + blockIdx.x);
+      load_role<D>(&tmQ, loads_v ? &tmV : &tmK, p, load_work(p), first, sQ, sKV, bars, lane, loads_v);
     }
   }
 
@@ -1252,6 +1233,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+}
+
+// ------------------------------------------------------------------ merge
+// A cut item (grid x, or none), 16 columns (y) of a query tile (z), a row to a thread: the
+// partial results weighted by their LSE, summed in the order of the keys.  A thread's loads of
+// up to four pieces are on their way at once, so that it takes few trips to L2.
+//
+// The plan is older than the attention kernel, which has waited for it, so it is read ahead of the
+// wait for that kernel, and CTAs without an item leave.  (Not the first: the kernel has to end
+// after the one before, on which the next kernel in the stream relies.)
+constexpr int kMergeColumns = 16;
+template <int D>
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
+  const Cut cut = reinterpret_cast<const Cut*>(p.plan + p.cuts)[blockIdx.x];
+  const int tile = blockIdx.z, tile_row = threadIdx.x, c = blockIdx.y * kMergeColumns;
+  const bool mine = plan_fits(p) && cut.parts > 0 && tile * p.tile_tokens < cut.tokens;
+  if (!mine && (blockIdx.x | blockIdx.y | blockIdx.z) != 0) return;
+  const int g = p.by_slices.div(cut.head);
+  const int row_token = p.by_heads.div(tile_row);
+  const int head = (cut.head - g * p.slices) * p.slice_heads + tile_row - row_token * p.slice_heads;
+  const int token = row_token + tile * p.tile_tokens;
+  grid_dependency_wait();
+  if (!mine || row_token >= p.tile_tokens || token >= cut.tokens || head >= p.group) return;
+  float top = -INFINITY, total = 0.f;  // of the weights 2^(lse - top), their sum
+  float sum[kMergeColumns];
+#pragma unroll
+  for (int e = 0; e < kMergeColumns; ++e) sum[e] = 0.f;
+  for (int s0 = 0; s0 < cut.parts; s0 += 4) {
+    const int n = min(4, cut.parts - s0);
+    float lse[4];
+    float4 x[4][kMergeColumns / 4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int part = cut.part + s0 + min(s, n - 1);
+      lse[s] = s < n ? p.part_lse[part_lse_at(part, tile, tile_row)] : -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kMergeColumns / 4; ++q)
+        x[s][q] = *reinterpret_cast<const float4*>(
+            p.part_o + part_at(part, tile, D, c + 4 * q, tile_row));
+    }
+    const float higher = fmaxf(fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])), top);
+    if (higher == -INFINITY) continue;
+    const float scale = ex2(top - higher);
+    top = higher;
+    total *= scale;
+#pragma unroll
+    for (int e = 0; e < kMergeColumns; ++e) sum[e] *= scale;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float w = ex2(lse[s] - top);
+      total += w;
+#pragma unroll
+      for (int q = 0; q < kMergeColumns / 4; ++q) {
+        sum[4 * q] = fmaf(w, x[s][q].x, sum[4 * q]);
+        sum[4 * q + 1] = fmaf(w, x[s][q].y, sum[4 * q + 1]);
+        sum[4 * q + 2] = fmaf(w, x[s][q].z, sum[4 * q + 2]);
+        sum[4 * q + 3] = fmaf(w, x[s][q].w, sum[4 * q + 3]);
+      }
+    }
+  }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  uint32_t y[kMergeColumns / 2];
+#pragma unroll
+  for (int e = 0; e < kMergeColumns / 2; ++e)
+    y[e] = pack_bf16x2(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+  const size_t at = static_cast<size_t>(cut.token + token) * p.Hq + g * p.group + head;
+  if (store_in_bounds(p.o + at * D + c, 2 * kMergeColumns, p.o, p.o_bytes, p.status))
+    st_global_8w(p.o + at * D + c, y, p.o_v8);
+  if (c == 0 && store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
+    p.lse[at] = total > 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
 template <int D>
@@ -1266,27 +1317,17 @@ cudaError_t launch_impl(const void* q, const void* k, const void* v, const Chunk
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attn_chunk_kernel<D>),
                                    static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;
-  return launch_programmatic(attn_chunk_kernel<D>, dim3(p.ctas), dim3(kThreads), C::kSmemBytes, stream,
-                             tmQ, tmK, tmV, p);
+  e = launch_programmatic(attn_chunk_kernel<D>, dim3(p.ctas), dim3(kThreads), C::kSmemBytes, stream,
+                          tmQ, tmK, tmV, p);
+  // (Items of so few tiles are never cut.)
+  if (e != cudaSuccess || p.max_pages * p.page_size <= (2 * kSnap - 1) * 128) return e;
+  return launch_programmatic(chunk_merge_kernel<D>, dim3(p.ctas, D / kMergeColumns, 2), dim3(128), 0,
+                             stream, p);
 }
 
 }  // namespace
 
 int chunk_ctas() { return sm_count() < kChunkMaxCtas ? sm_count() : kChunkMaxCtas; }
-
-namespace {
-// A number that no other call has (a counter's, mixed: nothing that a workspace holds by
-// chance), never 0.
-unsigned long long next_token() {
-  static std::atomic<unsigned long long> calls{
-      static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count())};
-  unsigned long long x = calls.fetch_add(1) * 0x9e3779b97f4a7c15ull;
-  x ^= x >> 32;
-  x *= 0xd6e8feb86659fd93ull;
-  x ^= x >> 32;
-  return x != 0 ? x : 1;
-}
-}  // namespace
 
 cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
                               int Hkv, int D, int max_keys, int window, int sinks,
@@ -1314,8 +1355,6 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   const size_t part_rows = 2ull * p.ctas * 256;
   p.part_o = workspace;
   p.part_lse = workspace + part_rows * D;
-  p.flags = reinterpret_cast<unsigned long long*>(p.part_lse + part_rows);
-  p.token = next_token();
   p.o_bytes = static_cast<size_t>(T) * Hq * D * 2;
   p.lse_bytes = static_cast<size_t>(T) * Hq * sizeof(float);
   p.part_o_bytes = part_rows * D * sizeof(float);
@@ -1338,6 +1377,8 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   p.page_rows = paged.num_pages * Hkv * paged.page_size;
   const ChunkLayout layout(B, tiling.max_items(B, T, Hkv), p.ctas);
   p.begins = layout.begins;
+  p.firsts = layout.firsts;
+  p.cuts = layout.cuts;
   p.pieces = layout.pieces;
   p.by_page = FixedDiv(paged.page_size);
   p.by_heads = FixedDiv(tiling.slice_heads);

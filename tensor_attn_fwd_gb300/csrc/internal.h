@@ -280,22 +280,23 @@ struct ChunkTiling {
 // CTAs that share the work on the current device: one an SM.
 constexpr int kChunkMaxCtas = 512;
 int chunk_ctas();
-// Layout of a plan in int32: header, CTAs' pieces, the requests' item counts, pieces.
+// Layout of a plan in int32: header, CTAs' pieces and the first of each, cut items, the
+// requests' item counts, pieces.
 constexpr int kChunkHeader = 16, kChunkRecord = 8;
 struct ChunkLayout {
-  long long begins, tiles, pieces, total;
+  long long begins, firsts, cuts, tiles, pieces, total;
   static __host__ __device__ long long align(long long n) { return (n + 7) / 8 * 8; }
   __host__ __device__ ChunkLayout(int B, long long max_items, int ctas) {
     begins = kChunkHeader;
-    tiles = begins + ctas + 1;
+    firsts = align(begins + ctas + 1);
+    cuts = firsts + static_cast<long long>(kChunkRecord) * ctas;
+    tiles = cuts + static_cast<long long>(kChunkRecord) * ctas;
     pieces = align(tiles + B + 1);
     total = pieces + kChunkRecord * (max_items + ctas);
   }
 };
-// Partial results, two for each CTA, of 256 rows with their LSE and eight flags of 64 bits.
-inline long long chunk_workspace_floats(int ctas, int D) {
-  return 2ll * ctas * (256 * (D + 1) + 16);
-}
+// Partial results, two for each CTA, of 256 rows with their LSE.
+inline long long chunk_workspace_floats(int ctas, int D) { return 2ll * ctas * 256 * (D + 1); }
 cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
                               int Hkv, int D, int max_keys, int window, int sinks,
                               cudaStream_t stream, int* status);
