@@ -906,9 +906,11 @@ def attn_pages_append(block_table: torch.Tensor, refs: torch.Tensor, seqlens: to
     inputs; the other results share one allocation.
     """
     call = (_fast or _native()).pages_append
-    args = (block_table, refs, seqlens, new_lens, tokens, page_size, block_table_out, refs_out,
-            seqlens_out)
-    return call(*args) if stream is None else _on_stream(stream, call, *args)
+    if stream is not None:
+        return _on_stream(stream, call, block_table, refs, seqlens, new_lens, tokens, page_size,
+                          block_table_out, refs_out, seqlens_out)
+    return call(block_table, refs, seqlens, new_lens, tokens, page_size, block_table_out, refs_out,
+                seqlens_out)
 
 
 def attn_rope_table_scaled(max_pos: int, R: int, base: float = 10000.0, factor: float = 1.0,
@@ -950,8 +952,9 @@ def attn_rope_split(qkv: torch.Tensor, rope_table: torch.Tensor, Hq: int, Hkv: i
     with B*S entries (default: s); style as attn_qkv_rope.
     """
     call = (_fast or _native()).rope_split
-    args = (qkv, rope_table, Hq, Hkv, positions, style, q, k, v)
-    return call(*args) if stream is None else _on_stream(stream, call, *args)
+    if stream is not None:
+        return _on_stream(stream, call, qkv, rope_table, Hq, Hkv, positions, style, q, k, v)
+    return call(qkv, rope_table, Hq, Hkv, positions, style, q, k, v)
 
 
 def attn_rope_split_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
@@ -960,8 +963,9 @@ def attn_rope_split_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
     """Gradient of attn_rope_split: dqkv [B,S,(Hq+2*Hkv)*D] bf16 from dq [B,Hq,S,D], dk and dv
     [B,Hkv,S,D], all bf16 (attn_window_bwd) or all fp32 (attn_bwd)."""
     call = (_fast or _native()).rope_split_bwd
-    args = (dq, dk, dv, rope_table, positions, style, dqkv)
-    return call(*args) if stream is None else _on_stream(stream, call, *args)
+    if stream is not None:
+        return _on_stream(stream, call, dq, dk, dv, rope_table, positions, style, dqkv)
+    return call(dq, dk, dv, rope_table, positions, style, dqkv)
 
 
 def attn_rope_append(qkv: torch.Tensor, rope_table: torch.Tensor, positions: torch.Tensor,
@@ -974,8 +978,10 @@ def attn_rope_append(qkv: torch.Tensor, rope_table: torch.Tensor, positions: tor
     int32 [T] (attn_pages_append; slot -1: nowhere); caches [num_pages,Hkv,page_size,D].
     """
     call = (_fast or _native()).rope_append
-    args = (qkv, rope_table, positions, slots, k_cache, v_cache, Hq, style, q)
-    return call(*args) if stream is None else _on_stream(stream, call, *args)
+    if stream is not None:
+        return _on_stream(stream, call, qkv, rope_table, positions, slots, k_cache, v_cache, Hq,
+                          style, q)
+    return call(qkv, rope_table, positions, slots, k_cache, v_cache, Hq, style, q)
 
 
 def attn_chunk_plan(cu_tokens: torch.Tensor, seqlens: torch.Tensor, tokens: int, Hq: int, Hkv: int,
@@ -990,10 +996,10 @@ def attn_chunk_plan(cu_tokens: torch.Tensor, seqlens: torch.Tensor, tokens: int,
     is max_pages * page_size of the block table.  D is 64 or 128.
     """
     call = (_fast or _native()).chunk_plan
-    args = (tokens, Hq, Hkv, D, max_keys, window, sinks, plan)
-    if stream is None:
-        return call(cu_tokens, seqlens, *args)
-    return _on_stream(stream, call, cu_tokens, seqlens, *args)
+    if stream is not None:
+        return _on_stream(stream, call, cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window,
+                          sinks, plan)
+    return call(cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, plan)
 
 
 def attn_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -1009,5 +1015,7 @@ def attn_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     fp32 CUDA tensor of attn_chunk_workspace floats (include/attn.h).
     """
     call = (_fast or _native()).chunk_paged
-    args = (q, k_cache, v_cache, block_table, plan, scale, o, lse, workspace)
-    return call(*args) if stream is None else _on_stream(stream, call, *args)
+    if stream is not None:
+        return _on_stream(stream, call, q, k_cache, v_cache, block_table, plan, scale, o, lse,
+                          workspace)
+    return call(q, k_cache, v_cache, block_table, plan, scale, o, lse, workspace)

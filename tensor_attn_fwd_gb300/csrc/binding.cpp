@@ -561,10 +561,11 @@ PyObject* pages_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const GpuPart gpu(p.device);
       long long need = 0;
       raise_if(attn_pages_append_workspace(p.P, p.B, &need), "attn_pages_append");
-      const Tensor ws = new_int32(need, p.device);
+      // (The workspace too is of the results' allocation: one allocation is what the call costs
+      // the host.)
       Carver results((table_out.given() ? 0 : padded(static_cast<int64_t>(p.B) * p.M)) +
                          (refs_out.given() ? 0 : padded(p.P)) + (lens_out.given() ? 0 : padded(p.B)) +
-                         padded(static_cast<int64_t>(p.B) + 1) + 2 * padded(T) + 2,
+                         padded(static_cast<int64_t>(p.B) + 1) + 2 * padded(T) + 4 + need,
                      p.device);
       table = table_out.given() ? table_out.get() : results.take({p.B, p.M});
       refs = refs_out.given() ? refs_out.get() : results.take({p.P});
@@ -573,6 +574,7 @@ PyObject* pages_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       positions = results.take({T});
       slots = results.take({T});
       counts = results.take({2});
+      const Tensor ws = results.take({need});
       raise_if(attn_pages_append(ints(p.table), ints(p.refs), ints(lens), ints(news), ints(table),
                                  ints(refs), ints(lens_new), ints(cu), ints(positions), ints(slots),
                                  ints(counts), ints(ws), p.B, T, p.M, p.P, page,

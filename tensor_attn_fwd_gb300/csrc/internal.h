@@ -249,7 +249,7 @@ cudaError_t launch_pages_fork(const int* table, const int* refs, const int* seql
                               int* src, int* dst, int* counts, int* workspace, int B, int R, int M,
                               int P, int page_size, int room, cudaStream_t stream, int* status);
 // int32 workspace of launch_pages_append (B rows).
-inline long long pages_append_workspace(int P, int B) { return P + 3ll * B + 3 * kPagesMaxCtas; }
+inline long long pages_append_workspace(int P, int B) { return P + 3ll * B + 16 * (32 + 3); }
 cudaError_t launch_pages_append(const int* table, const int* refs, const int* seqlens,
                                 const int* new_lens, int* table_out, int* refs_out,
                                 int* seqlens_out, int* cu, int* positions, int* slots, int* counts,

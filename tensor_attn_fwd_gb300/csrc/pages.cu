@@ -56,9 +56,10 @@ constexpr int kWarps = kThreads / 32;
 // The largest calls (elements of arrays) of one CTA, and of one cluster.
 constexpr long long kSmallForkEntries = 8192, kSmallForkPages = 6144, kSmallForkSlots = 8192;
 constexpr long long kSmallCompactEntries = 8192, kSmallCompactPages = 4096;
-constexpr long long kBlockWork = 4096;  // append
+constexpr long long kSmallAppendEntries = 8192, kSmallAppendPages = 8192, kSmallAppendTokens = 16384;
 constexpr long long kClusterWork = 1 << 15;
 constexpr int kClusterCtas = 16;  // past the portable 8: the kernels opt in
+constexpr int kMaxCopiers = 6;    // append: clusters that copy the table
 
 __device__ __forceinline__ void record_status(int* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
@@ -128,22 +129,20 @@ __device__ __forceinline__ int checked_entry(int e, int num_pages, int* status) 
   return e;
 }
 
-// All phases of a call.  kBlock: one CTA and its barrier; kCluster: one cluster and its;
-// kGrid: a cooperative grid and its (every CTA is resident, and each enters every barrier).
-enum Span { kBlock, kCluster, kGrid };
+// All phases of a call.  kCluster: one cluster and its barrier; kGrid: a cooperative
+// grid and its (every CTA is resident, and each enters every barrier).
+enum Span { kCluster, kGrid };
 template <typename Op, Span SPAN>
 __global__ void __launch_bounds__(kThreads, 1) pages_phases_kernel(const Op op) {
   __shared__ int smem[32];
-  if constexpr (SPAN != kGrid) {
+  if constexpr (SPAN == kCluster) {
     grid_dependency_wait();
     grid_launch_dependents();
   }
   for (int ph = 0; ph < Op::kPhases; ++ph) {
     op.run(ph, smem);
     if (ph + 1 == Op::kPhases) break;
-    if constexpr (SPAN == kBlock)
-      __syncthreads();
-    else if constexpr (SPAN == kCluster)
+    if constexpr (SPAN == kCluster)
       cluster_sync();
     else
       cooperative_groups::this_grid().sync();
@@ -651,19 +650,27 @@ struct CompactOp {
 };
 
 // ------------------------------------------------------------------ append
-// Pages, positions and slots for a step's new tokens.  Token sums are clamped to T + 1
-// (a sum that saturates stays associative), so that no row count overflows them.
+// Pages, positions and slots for a step's new tokens.  The workers, a cluster of CTAs, take
+// equal parts of the pages and of the rows:
+//   1 count the free pages; count the pages that each row lacks, its tokens
+//   2 list the free pages that are needed; decide which rows take their tokens
+//   3 hand the pages out  4 positions and slots of the tokens
+// and further CTAs copy refs and the table meanwhile, but for the pages and entries that are
+// the workers'.
+// Token sums are clamped to T + 1 (a sum that saturates stays associative).
+//
+// Latency, again: each phase is a few dependent trips to L2 (us TODO).
 struct AppendOp {
-  static constexpr int kPhases = 4;
   const int *table, *refs, *seqlens, *new_lens;
   int *table_out, *refs_out, *seqlens_out, *cu, *positions, *slots, *counts;
-  // Workspace: the free pages, ascending; each CTA's free pages, needed pages and tokens; per
-  // row those before it (in its CTA's rows, then of all rows, or -1 for a row that
-  // takes no tokens), its first token, and its length before.
-  int *free_list, *cta_free, *cta_need, *cta_tokens, *need, *first, *len;
-  int B, M, P, T, page_size;
-  FixedDiv by_page;
-  int table_vec;  // 16-byte accesses are aligned
+  // Workspace: the free pages that are needed, ascending; of each worker's warps the free
+  // pages, and of each worker the free and needed pages and the tokens; per row the needed
+  // pages before it, its first token (both in its worker's rows), and its length before (-1:
+  // it takes no tokens).
+  int *free_list, *warp_free, *cta_free, *cta_need, *cta_tokens, *need, *first, *len;
+  int B, M, P, T, page_size, workers;
+  FixedDiv by_page, by_row;  // page_size; M, or M / 4 with table_vec
+  int refs_vec, table_vec;   // 16-byte accesses are aligned
   int* status;
 
   struct Row {
@@ -671,10 +678,10 @@ struct AppendOp {
     int lo, hi;  // slots of the new tokens
   };
   __device__ __forceinline__ Row row(int r, int* report) const {
-    Row x;
-    x.len = seqlens[r];
-    x.n = new_lens[r];
-    x.lo = x.hi = 0;
+    return row(seqlens[r], new_lens[r], report);
+  }
+  __device__ __forceinline__ Row row(int length, int n, int* report) const {
+    Row x = {length, n, 0, 0};
     if (x.n < 0) {
       record_status(report, ATTN_ERR_INVALID_ARG);
       x.n = 0;
@@ -717,37 +724,200 @@ struct AppendOp {
     return add_tokens(warp > 0 ? before : 0, lane > 0 ? excl : 0);
   }
 
-  __device__ void run(int ph, int* smem) const {
-    const unsigned tid = blockIdx.x * kThreads + threadIdx.x, n_threads = gridDim.x * kThreads;
+  // Entries [i, i + N) of row b's slots from s on, copied (checked); entries that lack a
+  // page of the row's new tokens are a worker's.
+  template <int N>
+  __device__ __forceinline__ void copy(int b, int s, const int (&e)[N], int* to) const {
+    const Row x = row(b, nullptr);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int page = checked_entry(e[i], P, status);
+      if (page >= 0 || s + i < x.lo || s + i >= x.hi) to[i] = page;
+    }
+  }
+  // The table, by CTA `part` of `parts`.
+  __device__ void copy_table(int part, int parts) const {
+    const unsigned tid = part * kThreads + threadIdx.x, n_threads = parts * kThreads;
+    const unsigned entries = static_cast<unsigned>(B) * M;
+    if (table_vec) {
+      for (unsigned i = tid; i < entries / 4; i += n_threads) {
+        const int4 x = reinterpret_cast<const int4*>(table)[i];
+        const int e[4] = {x.x, x.y, x.z, x.w};
+        const int b = by_row.div(i), s = 4 * (i - b * (M / 4));
+        const Row r = row(b, nullptr);
+        if (s + 4 <= r.lo || s >= r.hi) {
+          reinterpret_cast<int4*>(table_out)[i] =
+              make_int4(checked_entry(x.x, P, status), checked_entry(x.y, P, status),
+                        checked_entry(x.z, P, status), checked_entry(x.w, P, status));
+        } else {
+          copy(b, s, e, table_out + 4 * static_cast<size_t>(i));
+        }
+      }
+    } else {
+      for (unsigned i = tid; i < entries; i += n_threads) {
+        const int e[1] = {table[i]};
+        const int b = by_row.div(i);
+        copy(b, i - b * M, e, table_out + i);
+      }
+    }
+  }
+
+  // Pages [begin, end) of one of the workers' warps, numbered over all of them.
+  __device__ __forceinline__ void warp_pages(int w, int& begin, int& end) const {
+    const int warps = workers * kWarps;
+    const int chunk = ((P + warps - 1) / warps + 127) & ~127;
+    begin = static_cast<int>(min(static_cast<long long>(w) * chunk, static_cast<long long>(P)));
+    end = static_cast<int>(min(static_cast<long long>(begin) + chunk, static_cast<long long>(P)));
+  }
+  // The free pages among this warp's [begin, end), 128 at a time, four to a lane as bits:
+  // f(round, bits), with several rounds' loads on their way at once.
+  template <typename F>
+  __device__ __forceinline__ void each_free(int begin, int end, F f) const {
+    constexpr int kAtOnce = 8;
+    const int lane = threadIdx.x & 31;
+    for (int i0 = 0; begin + 128 * i0 < end; i0 += kAtOnce) {
+      int4 c[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int p = begin + 128 * (i0 + i) + 4 * lane;
+        c[i] = make_int4(1, 1, 1, 1);
+        if (refs_vec && p + 4 <= end) {
+          c[i] = *reinterpret_cast<const int4*>(refs + p);
+        } else if (p < end) {
+          c[i].x = refs[p];
+          if (p + 1 < end) c[i].y = refs[p + 1];
+          if (p + 2 < end) c[i].z = refs[p + 2];
+          if (p + 3 < end) c[i].w = refs[p + 3];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (begin + 128 * (i0 + i) < end)
+          f(i0 + i, (c[i].x == 0) | (c[i].y == 0) << 1 | (c[i].z == 0) << 2 | (c[i].w == 0) << 3);
+    }
+  }
+  // The counts of pages that have holders (free pages are the workers'), by CTA `part` of `parts`.
+  __device__ void copy_refs(int part, int parts) const {
+    if (refs_out == refs) return;
+    const unsigned tid = part * kThreads + threadIdx.x, n_threads = parts * kThreads;
+    const unsigned vecs = refs_vec ? P / 4 : 0;
+    for (unsigned i = tid; i < vecs; i += n_threads) {
+      const int4 c = reinterpret_cast<const int4*>(refs)[i];
+      if (c.x != 0 && c.y != 0 && c.z != 0 && c.w != 0) {
+        reinterpret_cast<int4*>(refs_out)[i] = c;
+      } else {
+        const int e[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e[j] != 0) refs_out[4 * i + j] = e[j];
+      }
+    }
+    for (unsigned p = 4 * vecs + tid; p < static_cast<unsigned>(P); p += n_threads) {
+      const int c = refs[p];
+      if (c != 0) refs_out[p] = c;
+    }
+  }
+  static constexpr int kKept = 16;  // rounds of each_free whose bits a warp keeps
+
+  // What a worker's CTA shares between its threads.
+  struct Shared {
+    int sums[32];
+    // Of rows: their slots, how many of them lack a page (later the number of their first page,
+    // or -1), and which, as far as a word says it.
+    int lo[kThreads], hi[kThreads], lacking[kThreads];
+    unsigned mask[kThreads];
+    int starts[kThreads];
+    uint8_t free_bits[kWarps][kKept * 32];  // four pages each
+  };
+  // What a thread keeps from phase to phase where the worker's rows are no more than its
+  // threads: its row.
+  struct Mine {
+    Row x;
+    int lacking, k, t;
+  };
+  // The slots of the row at place i of `lo` and `hi`, eight lanes to a row, or all to a row
+  // of more slots: f(place, slot, lanes) with `lanes` the mask of those that share the row, in
+  // turns of eight or 32 slots; slots from hi on are nobody's (-1).
+  template <typename F>
+  __device__ __forceinline__ void each_slot(const Shared& sh, int i, F f) const {
+    const int lane = threadIdx.x & 31;
+    const int lo = sh.lo[i], hi = sh.hi[i];
+    if (hi - lo <= 8) {
+      if (lo < hi) f(i, lo + (lane & 7) < hi ? lo + (lane & 7) : -1, 0xffu << (lane & 24));
+    }
+    __syncwarp();
+    for (unsigned left = __ballot_sync(0xffffffffu, hi - lo > 8 && (lane & 7) == 0); left != 0;
+         left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const int ii = __shfl_sync(0xffffffffu, i, l), end = sh.hi[ii];
+      for (int s = sh.lo[ii] + lane; s - lane < end; s += 32) f(ii, s < end ? s : -1, 0xffffffffu);
+    }
+  }
+  static constexpr int kRowsAtOnce = kThreads / 8;
+  __device__ __forceinline__ bool lacks(int r, int s) const {
+    return checked_entry(table[static_cast<size_t>(r) * M + s], P, nullptr) < 0;
+  }
+
+  // Worker w of the pages and rows.
+  __device__ void run(int ph, int w, Mine& my, Shared& sh) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Part pages(P), rows(B);
+    const int per = (B + workers - 1) / workers;
+    const int r_begin = min(w * per, B), r_end = min(r_begin + per, B);
+    const bool one = r_end - r_begin <= kThreads;  // a row a thread
+    int p_begin, p_end;
+    warp_pages(w * kWarps + warp, p_begin, p_end);
     if (ph == 0) {
+      // The first rows' lengths, on their way with the pages' counts.
+      int length = 0, more = 0;
+      if (r_begin + static_cast<int>(threadIdx.x) < r_end) {
+        length = seqlens[r_begin + threadIdx.x];
+        more = new_lens[r_begin + threadIdx.x];
+      }
       int n = 0;
-      for (int p = pages.begin + threadIdx.x; p < pages.end; p += kThreads) {
-        const int c = refs[p];
-        n += c == 0;
-        if (refs_out != refs) refs_out[p] = c;
-      }
-      n = block_sum(n, smem);
-      if (threadIdx.x == 0) cta_free[blockIdx.x] = n;
-      // A warp per row: the pages it lacks.
-      for (int r = rows.begin + warp; r < rows.end; r += kWarps) {
-        const Row x = row(r, nullptr);
-        int lacks = 0;
-        for (int s = x.lo + lane; s < x.hi; s += 32)
-          lacks += checked_entry(table[static_cast<size_t>(r) * M + s], P, nullptr) < 0;
-        lacks = __reduce_add_sync(0xffffffffu, lacks);
-        if (lane == 0) need[r] = lacks;
-      }
+      each_free(p_begin, p_end, [&](int i, unsigned bits) {
+        if (bits != 0 && refs_out != refs) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (bits >> j & 1u) refs_out[p_begin + 128 * i + 4 * lane + j] = 0;
+        }
+        if (i < kKept) sh.free_bits[warp][32 * i + lane] = static_cast<uint8_t>(bits);
+        n += __popc(bits);
+      });
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) warp_free[w * kWarps + warp] = sh.sums[warp] = n;
       __syncthreads();
+      if (warp == 0) {
+        const int all = __reduce_add_sync(0xffffffffu, sh.sums[lane]);
+        if (lane == 0) cta_free[w] = all;
+      }
       int at = 0, tok = 0;
-      for (int r0 = rows.begin; r0 < rows.end; r0 += kThreads) {
+      for (int r0 = r_begin; r0 < r_end; r0 += kThreads) {
         const int r = r0 + threadIdx.x;
+        Row x = {0, 0, 0, 0};
+        if (r < r_end) x = r0 == r_begin ? row(length, more, nullptr) : row(r, nullptr);
+        sh.lo[threadIdx.x] = x.lo;
+        sh.hi[threadIdx.x] = x.hi;
+        sh.lacking[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i0 = 0; i0 < min(kThreads, r_end - r0); i0 += kRowsAtOnce)
+          each_slot(sh, i0 + (threadIdx.x >> 3), [&](int i, int s, unsigned lanes) {
+            const unsigned votes = __ballot_sync(lanes, s >= 0 && lacks(r0 + i, s));
+            if (lane == __ffs(lanes) - 1) {
+              sh.lacking[i] += __popc(votes);
+              sh.mask[i] = votes >> (__ffs(lanes) - 1);  // (of one turn; see `word`)
+            }
+          });
+        __syncthreads();
         int total, tok_total;
-        const int k = at + block_scan(r < rows.end ? need[r] : 0, smem, total);
-        const int t = add_tokens(
-            tok, token_scan(r < rows.end ? tokens(row(r, nullptr).n) : 0, smem, tok_total));
-        if (r < rows.end) {
+        const int lacking = sh.lacking[threadIdx.x];
+        const int k = at + block_scan(lacking, sh.sums, total);
+        const int t = add_tokens(tok, token_scan(tokens(x.n), sh.sums, tok_total));
+        if (one) {
+          my.x = x;
+          my.lacking = lacking;
+          my.k = k;
+          my.t = t;
+        } else if (r < r_end) {
           need[r] = k;
           first[r] = t;
         }
@@ -755,111 +925,308 @@ struct AppendOp {
         tok = add_tokens(tok, tok_total);
       }
       if (threadIdx.x == 0) {
-        cta_need[blockIdx.x] = at;
-        cta_tokens[blockIdx.x] = tok;
+        cta_need[w] = at;
+        cta_tokens[w] = tok;
       }
-    } else if (ph == 1) {
-      // The free pages of this CTA's part, and the table as it is.
-      int at = sum_counts(cta_free, blockIdx.x, smem);
-      for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads) {
-        const int p = p0 + threadIdx.x;
-        const int is_free = p < pages.end && refs[p] == 0;
-        int total;
-        const int k = at + block_scan(is_free, smem, total);
-        if (is_free) free_list[k] = p;
-        at += total;
-      }
-      const unsigned entries = static_cast<unsigned>(B) * M;
-      if (table_vec) {
-        for (unsigned i = tid; i < entries / 4; i += n_threads) {
-          int4 e = reinterpret_cast<const int4*>(table)[i];
-          e.x = checked_entry(e.x, P, status);
-          e.y = checked_entry(e.y, P, status);
-          e.z = checked_entry(e.z, P, status);
-          e.w = checked_entry(e.w, P, status);
-          reinterpret_cast<int4*>(table_out)[i] = e;
+      return;
+    }
+    // What the workers before this one have, and all of them (at most 32 workers).
+    int free_before = 0, free_all = 0, need_before = 0, need_all = 0, first_token = 0;
+    const int warp_has = ph == 1 ? warp_free[w * kWarps + lane] : 0;
+    if (ph == 1 || !one) {
+      const int f = lane < workers ? cta_free[lane] : 0, q = lane < workers ? cta_need[lane] : 0;
+      int t = lane < w ? cta_tokens[lane] : 0;
+      free_all = __reduce_add_sync(0xffffffffu, f);
+      need_all = __reduce_add_sync(0xffffffffu, q);
+      free_before = __reduce_add_sync(0xffffffffu, lane < w ? f : 0);
+      need_before = __reduce_add_sync(0xffffffffu, lane < w ? q : 0);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) t = add_tokens(t, __shfl_xor_sync(0xffffffffu, t, off));
+      first_token = t;
+    }
+    if (ph == 1) {
+      const int wanted = min(need_all, free_all);
+      int at = free_before + __reduce_add_sync(0xffffffffu, lane < warp ? warp_has : 0);
+      const int rounds = (p_end - p_begin + 127) / 128;
+      if (at < wanted && rounds <= kKept) {
+        // A run of each lane's own, so that one prefix sum ranks them.
+        const uint8_t* mine = sh.free_bits[warp] + lane * rounds;
+        int n = 0;
+        for (int i = 0; i < rounds; ++i) n += __popc(mine[i]);
+        int k = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, k, off);
+          if (lane >= off) k += y;
         }
-      } else {
-        for (unsigned i = tid; i < entries; i += n_threads)
-          table_out[i] = checked_entry(table[i], P, status);
+        k += at - n;
+        for (int i = 0; i < rounds; ++i)
+          for (unsigned bits = mine[i]; bits != 0; bits &= bits - 1) {
+            if (k < wanted) free_list[k] = p_begin + 4 * (lane * rounds + i) + __ffs(bits) - 1;
+            ++k;
+          }
+      } else if (at < wanted) {
+        each_free(p_begin, p_end, [&](int i, unsigned bits) {
+          if (at >= wanted || !__any_sync(0xffffffffu, bits != 0)) return;
+          const unsigned below = (1u << lane) - 1u;
+          int k = at;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const unsigned votes = __ballot_sync(0xffffffffu, bits >> j & 1u);
+            k += __popc(votes & below);
+            at += __popc(votes);
+          }
+          for (; bits != 0; bits &= bits - 1) {
+            if (k < wanted) free_list[k] = p_begin + 128 * i + 4 * lane + __ffs(bits) - 1;
+            ++k;
+          }
+        });
       }
       // Which rows take their tokens: those whose pages and whose places in the step's T
       // suffice.  (Each row's lengths are read for the last time here, by the thread that
       // writes the new one: the two arrays may be one.)
-      const int n_free = sum_counts(cta_free, gridDim.x, smem);
-      const int base = sum_counts(cta_need, blockIdx.x, smem);
-      const int all_need = sum_counts(cta_need, gridDim.x, smem);
-      int tok_base = 0;
-      {
-        int x = 0;
-        for (int i = threadIdx.x; i < static_cast<int>(blockIdx.x); i += kThreads)
-          x = add_tokens(x, cta_tokens[i]);
-        token_scan(x, smem, tok_base);
-      }
-      for (int r = rows.begin + threadIdx.x; r < rows.end; r += kThreads) {
-        const Row x = row(r, status);
-        const int before = base + need[r];
-        const int after = r + 1 < rows.end ? base + need[r + 1] : base + cta_need[blockIdx.x];
-        const int t = add_tokens(tok_base, first[r]), end = add_tokens(t, tokens(x.n));
+      for (int r = r_begin + threadIdx.x; r < r_end; r += kThreads) {
+        const Row x = one ? row(my.x.len, new_lens[r], status) : row(r, status);
+        const int after = need_before + (one             ? my.k + my.lacking
+                                         : r + 1 < r_end ? need[r + 1]
+                                                         : cta_need[w]);
+        const int t = add_tokens(first_token, one ? my.t : first[r]);
+        const int end = add_tokens(t, tokens(x.n));
         bool takes = x.lo < x.hi;
         if (end > T) {
           record_status(status, ATTN_ERR_INVALID_ARG);
           takes = false;
         }
-        takes = takes && after <= n_free;
+        takes = takes && after <= free_all;
         cu[r + 1] = min(end, T);
         len[r] = takes ? x.len : -1;
-        seqlens_out[r] = takes ? x.len + x.n : x.len;
+        if (one) {
+          sh.lacking[threadIdx.x] = takes ? need_before + my.k : -1;
+          seqlens_out[r] = takes ? x.len + x.n : x.len;
+        }
       }
-      if (tid == 0) {
+      if (w == 0 && threadIdx.x == 0) {
         cu[0] = 0;
-        counts[0] = all_need;
-        counts[1] = n_free;
-        if (all_need > n_free) record_status(status, ATTN_ERR_NO_PAGES);
+        counts[0] = need_all;
+        counts[1] = free_all;
+        if (need_all > free_all) record_status(status, ATTN_ERR_NO_PAGES);
       }
-    } else if (ph == 2) {
-      const int base = sum_counts(cta_need, blockIdx.x, smem);
-      for (int r = rows.begin + warp; r < rows.end; r += kWarps) {
-        const int from = len[r];
-        if (from < 0) continue;
-        const int lo = by_page.div(from), hi = by_page.div(seqlens_out[r] - 1) + 1;
-        int k = base + need[r];
-        for (int s0 = lo; s0 < hi; s0 += 32) {
-          const int s = s0 + lane;
-          int* const entry = table_out + static_cast<size_t>(r) * M + s;
-          const bool lacks = s < hi && *entry < 0;
-          const unsigned votes = __ballot_sync(0xffffffffu, lacks);
-          if (lacks) {
-            const int page = free_list[k + __popc(votes & ((1u << lane) - 1u))];
-            *entry = page;
-            refs_out[page] = 1;
+      return;
+    }
+    // Pages for the rows' slots that lack one (-1 for those of rows that take none).
+    for (int r0 = r_begin; r0 < r_end; r0 += kThreads) {
+      const int r = r0 + threadIdx.x;
+      if (!one) {
+        Row x = {0, 0, 0, 0};
+        int k0 = -1;
+        if (r < r_end) {
+          x = row(r, nullptr);
+          if (len[r] >= 0) k0 = need_before + need[r];
+        }
+        __syncthreads();
+        sh.lo[threadIdx.x] = x.lo;
+        sh.hi[threadIdx.x] = x.hi;
+        sh.lacking[threadIdx.x] = k0;
+        __syncthreads();
+      }
+      for (int i0 = 0; i0 < min(kThreads, r_end - r0); i0 += kRowsAtOnce)
+        each_slot(sh, i0 + (threadIdx.x >> 3), [&](int i, int s, unsigned lanes) {
+          const int leader = __ffs(lanes) - 1;
+          // One turn's slots are known from phase 1.
+          const bool word = one && sh.hi[i] - sh.lo[i] <= __popc(lanes);
+          const bool lacking =
+              word ? sh.mask[i] >> (lane - leader) & 1u : s >= 0 && lacks(r0 + i, s);
+          const unsigned votes = __ballot_sync(lanes, lacking);
+          const int k = sh.lacking[i];
+          __syncwarp(lanes);
+          if (lane == leader && k >= 0) sh.lacking[i] = k + __popc(votes);
+          __syncwarp(lanes);
+          if (lacking) {
+            const int page = k >= 0 ? free_list[k + __popc(votes & ((1u << lane) - 1u))] : -1;
+            table_out[static_cast<size_t>(r0 + i) * M + s] = page;
+            if (page >= 0) refs_out[page] = 1;
           }
-          k += __popc(votes);
-        }
+        });
+    }
+    if (one) return;
+    __syncthreads();
+    for (int r = r_begin + threadIdx.x; r < r_end; r += kThreads) {
+      const int x = seqlens[r];
+      seqlens_out[r] = len[r] >= 0 ? x + new_lens[r] : x;
+    }
+  }
+  // Positions and slots of the tokens, shared out over the workers.
+  __device__ void run_tokens(int w, Shared& sh) const {
+    int* const starts = sh.starts;
+    // Every step-th row's first token, for a search that seldom leaves the CTA.
+    const int step = (B + kStarts - 1) / kStarts, n = (B + step - 1) / step;
+    for (int i = threadIdx.x; i < n; i += kThreads) starts[i] = cu[i * step];
+    __syncthreads();
+    for (int t = w * kThreads + threadIdx.x; t < T; t += workers * kThreads) {
+      // The last row whose tokens begin at or before t (rows before it may have none).
+      int lo = 0, hi = n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (starts[mid] <= t)
+          lo = mid;
+        else
+          hi = mid;
       }
-    } else {
-      for (unsigned t = tid; t < static_cast<unsigned>(T); t += n_threads) {
-        // The row whose tokens begin last at or before t.
-        int lo = 0, hi = B;
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if (cu[mid + 1] <= static_cast<int>(t))
-            lo = mid + 1;
-          else
-            hi = mid;
-        }
-        int pos = 0, slot = -1;
-        if (lo < B && len[lo] >= 0) {
-          pos = len[lo] + static_cast<int>(t) - cu[lo];
-          const int s = by_page.div(pos);
-          slot = table_out[static_cast<size_t>(lo) * M + s] * page_size + pos - s * page_size;
-        }
-        positions[t] = pos;
-        slots[t] = slot;
+      lo *= step;
+      hi = min(lo + step, B);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cu[mid] <= t)
+          lo = mid;
+        else
+          hi = mid;
       }
+      int pos = 0, slot = -1;
+      const int from = len[lo], t0 = cu[lo], t1 = cu[lo + 1];
+      if (t < t1 && from >= 0) {
+        pos = from + t - t0;
+        const int s = by_page.div(pos);
+        slot = table_out[static_cast<size_t>(lo) * M + s] * page_size + pos - s * page_size;
+      }
+      positions[t] = pos;
+      slots[t] = slot;
+    }
+  }
+  static constexpr int kStarts = kThreads;
+
+  // One CTA, everything in shared memory between one trip for the inputs and the stores: a thread
+  // per row, and one prefix sum for its tokens, its lacking pages and a run of free pages.
+  static size_t small_bytes(long long entries, int P, int B) {
+    return (entries + pad(P) + P + 2ll * B + 1) * sizeof(int);
+  }
+  __device__ void run_small(unsigned long long* sums, int* lists) const {
+    const int t = threadIdx.x, entries = B * M;
+    int* const page_of = lists;           // the table
+    int* const held = page_of + entries;  // refs
+    int* const free_at = held + pad(P);   // free pages, ascending
+    int* const begin = free_at + P;       // rows' first tokens (B + 1)
+    int* const taken = begin + B + 1;     // rows' lengths before, or -1
+    const int length = t < B ? seqlens[t] : 0, more = t < B ? new_lens[t] : 0;
+    for (int i = t; i < entries; i += kThreads) page_of[i] = checked_entry(table[i], P, status);
+    for (int p = t; p < P; p += kThreads) held[pad(p)] = refs[p];
+    const Row x = row(length, more, status);
+    __syncthreads();
+    const int per = (P + kThreads - 1) / kThreads;  // pages of a thread, in one run
+    const int p0 = min(t * per, P), p1 = min(p0 + per, P);
+    int n_free = 0, lacking = 0;
+    for (int p = p0; p < p1; ++p) n_free += held[pad(p)] == 0;
+    for (int s = x.lo; s < x.hi; ++s) lacking += page_of[t * M + s] < 0;
+    // (Fields of 30, 17 and 17 bits: rows <= 2^10, tokens clamped to T + 1 <= 2^14, entries and
+    // pages <= 2^13.)
+    const unsigned long long mine = static_cast<unsigned long long>(tokens(x.n)) |
+                                    static_cast<unsigned long long>(lacking) << 30 |
+                                    static_cast<unsigned long long>(n_free) << 47;
+    unsigned long long incl = mine;
+    const int lane = t & 31, warp = t >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    unsigned long long warps = sums[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, warps, off);
+      if (lane >= off) warps += y;
+    }
+    const unsigned long long all = __shfl_sync(0xffffffffu, warps, 31);
+    unsigned long long before = __shfl_sync(0xffffffffu, warps, max(warp - 1, 0));
+    before = (warp > 0 ? before : 0) + incl - mine;
+    const auto token_field = [&](unsigned long long v) {
+      return min(static_cast<int>(v & ((1u << 30) - 1)), T + 1);
+    };
+    const auto field = [](unsigned long long v, int at) {
+      return static_cast<int>(v >> at & 0x1ffff);
+    };
+    int f = field(before, 47);
+    for (int p = p0; p < p1; ++p)
+      if (held[pad(p)] == 0) free_at[f++] = p;
+    const int free_all = field(all, 47), need_all = field(all, 30);
+    int k = field(before, 30);
+    const int t0 = token_field(before), t1 = token_field(before + mine);
+    if (t < B && t1 > T) record_status(status, ATTN_ERR_INVALID_ARG);
+    const bool takes = t < B && x.lo < x.hi && t1 <= T && k + lacking <= free_all;
+    if (t < B) {
+      begin[t] = min(t0, T);
+      taken[t] = takes ? x.len : -1;
+      cu[t] = min(t0, T);
+      seqlens_out[t] = takes ? x.len + x.n : length;
+    }
+    if (t == B - 1) begin[B] = cu[B] = min(t1, T);
+    if (t == 0) {
+      counts[0] = need_all;
+      counts[1] = free_all;
+      if (need_all > free_all) record_status(status, ATTN_ERR_NO_PAGES);
+    }
+    __syncthreads();
+    if (takes)
+      for (int s = x.lo; s < x.hi; ++s)
+        if (page_of[t * M + s] < 0) {
+          const int page = free_at[k++];
+          page_of[t * M + s] = page;
+          held[pad(page)] = 1;
+        }
+    __syncthreads();
+    for (int i = t; i < entries; i += kThreads) table_out[i] = page_of[i];
+    for (int p = t; p < P; p += kThreads) refs_out[p] = held[pad(p)];
+    for (int i = t; i < T; i += kThreads) {
+      int lo = 0, hi = B;  // the last row whose tokens begin at or before i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (begin[mid] <= i)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      int pos = 0, slot = -1;
+      if (i < begin[lo + 1] && taken[lo] >= 0) {
+        pos = taken[lo] + i - begin[lo];
+        const int s = by_page.div(pos);
+        slot = page_of[lo * M + s] * page_size + pos - s * page_size;
+      }
+      positions[i] = pos;
+      slots[i] = slot;
     }
   }
 };
+
+__global__ void __launch_bounds__(kThreads, 1) pages_append_small_kernel(const AppendOp op) {
+  __shared__ unsigned long long sums[32];
+  extern __shared__ int lists[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  op.run_small(sums, lists);
+}
+
+// A cluster of workers and further CTAs that copy (without those the workers do).
+__global__ void __launch_bounds__(kThreads, 1) pages_append_kernel(const AppendOp op) {
+  __shared__ AppendOp::Shared sh;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int w = blockIdx.x;
+  if (w >= op.workers) {
+    op.copy_refs(w - op.workers, gridDim.x - op.workers);
+    op.copy_table(w - op.workers, gridDim.x - op.workers);
+    return;
+  }
+  if (static_cast<int>(gridDim.x) == op.workers) {
+    op.copy_refs(w, op.workers);
+    op.copy_table(w, op.workers);
+  }
+  AppendOp::Mine my = {};
+  for (int ph = 0; ph < 3; ++ph) {
+    op.run(ph, w, my, sh);
+    cluster_sync();
+  }
+  op.run_tokens(w, sh);
+}
 
 // ------------------------------------------------------------------ copies
 // A CTA per 32 KB of a page, every load in flight before the first store, both marked
@@ -986,10 +1353,11 @@ cudaError_t launch_pages_append(const int* table, const int* refs, const int* se
   AppendOp op{table, refs, seqlens, new_lens, table_out, refs_out, seqlens_out,
               cu, positions, slots, counts};
   op.free_list = workspace;
-  op.cta_free = op.free_list + P;
-  op.cta_need = op.cta_free + kPagesMaxCtas;
-  op.cta_tokens = op.cta_need + kPagesMaxCtas;
-  op.need = op.cta_tokens + kPagesMaxCtas;
+  op.warp_free = op.free_list + P;
+  op.cta_free = op.warp_free + kClusterCtas * kWarps;
+  op.cta_need = op.cta_free + kClusterCtas;
+  op.cta_tokens = op.cta_need + kClusterCtas;
+  op.need = op.cta_tokens + kClusterCtas;
   op.first = op.need + B;
   op.len = op.first + B;
   op.B = B;
@@ -998,15 +1366,31 @@ cudaError_t launch_pages_append(const int* table, const int* refs, const int* se
   op.T = T;
   op.page_size = page_size;
   op.by_page = FixedDiv(page_size);
-  op.table_vec = static_cast<long long>(B) * M % 4 == 0 && aligned16(table) && aligned16(table_out);
+  op.refs_vec = aligned16(refs) && aligned16(refs_out);
+  op.table_vec = M % 4 == 0 && aligned16(table) && aligned16(table_out);
+  op.by_row = FixedDiv(op.table_vec ? M / 4 : M);
   op.status = status;
   const long long entries = static_cast<long long>(B) * M;
-  long long work = entries > P ? entries : P;
-  if (T > work) work = T;
-  if (work <= kBlockWork)
-    return launch_programmatic(pages_phases_kernel<AppendOp, kBlock>, dim3(1), dim3(kThreads), 0,
-                               stream, op);
-  return launch_phases(op, work, stream);
+  if (entries <= kSmallAppendEntries && P <= kSmallAppendPages && B <= kThreads &&
+      T < kSmallAppendTokens) {
+    const size_t smem = AppendOp::small_bytes(entries, P, B);
+    const auto small = pages_append_small_kernel;
+    const cudaError_t e =
+        ensure_smem_attr(reinterpret_cast<const void*>(small), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_programmatic(small, dim3(1), dim3(kThreads), smem, stream, op);
+  }
+  op.workers = kClusterCtas;
+  const auto kernel = pages_append_kernel;
+  const cudaError_t e = allow_large_cluster(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  // Eight entries or pages a thread for clusters that copy.  They read the rows' lengths whenever they
+  // run, so that lengths updated in place leave the copy to the workers.
+  long long copiers = (entries > P ? entries : P) / (8ll * kThreads * kClusterCtas);
+  if (copiers > kMaxCopiers) copiers = kMaxCopiers;
+  if (seqlens_out == seqlens) copiers = 0;
+  return launch_programmatic_cluster(kernel, dim3(static_cast<unsigned>((1 + copiers) * kClusterCtas)),
+                                     dim3(kThreads), 0, stream, kClusterCtas, op);
 }
 
 cudaError_t launch_pages_compact(const int* table, const int* refs, int* table_out, int* refs_out,

@@ -12,12 +12,18 @@
 //
 // Bound by memory: each element is read and written once.  A thread owns a unit of 16
 // dims of a head, two 16-byte vectors that hold whole pairs in either style, at the same
-// place of every U-th head of its token, so that it reads its eight (cos, sin) once.
+// place of several heads of its token, so that it reads its eight (cos, sin) once.  What
+// counts is loads on their way: six units of a thread at once, issued ahead of the position and
+// the angles that depend on it, in CTAs of 128 threads; and stores that are let go first
+// (8192 tokens, 32/8 heads of 128: split 31.6 us, 6.4 TB/s, its gradient 33.9, append 33.3; with a
+// CTA of 256 threads a token, two units at once, behind the angles, 51.2, 53.0 and 51.0;
+// four units at once 34.9, 33.8 and 35.1; without the streaming stores 36.2, 36.6, 38.1).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -28,7 +34,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kPerThread = 4;  // a thread's units, at least (where a token has so many)
 
 __device__ __forceinline__ void record_status(int* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
@@ -46,44 +53,71 @@ struct RopeParams {
   // Split: [B,H,S,D]; append: q [tokens,Hq,D] and the caches; gradient: dq, dk, dv.
   void *q, *k, *v;
   int tokens, S, Hq, Hkv, D, R, max_pos;
+  int group;  // threads of a token
   int page_size;
   long long num_slots;  // append: num_pages * page_size
   FixedDiv by_seq, by_page;
   int* status;
 };
 
-// Eight elements as floats.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// A unit's two vectors as they are in memory, and as floats.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    a = __ldcs(reinterpret_cast<const uint4*>(p));
+    b = __ldcs(reinterpret_cast<const uint4*>(q));
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+  static __device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8], float (&y)[8]) const {
+    widen(a, x);
+    widen(b, y);
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b, c, d;
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    c = __ldcs(reinterpret_cast<const float4*>(q));
+    d = __ldcs(reinterpret_cast<const float4*>(q) + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8], float (&y)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    y[0] = c.x, y[1] = c.y, y[2] = c.z, y[3] = c.w, y[4] = d.x, y[5] = d.y, y[6] = d.z, y[7] = d.w;
+  }
+};
 // Rounded once, to nearest even.
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  const uint4 w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  __stcs(reinterpret_cast<uint4*>(p), w);
 }
 
-// One CTA per token.  TG: the type of dq, dk and dv.
+// p.group threads to a token.  TG: the type of dq, dk and dv.
 template <Form FORM, int STYLE, typename TG>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  using TIn = std::conditional_t<FORM == kGrad, TG, __nv_bfloat16>;
+  constexpr int N = sizeof(TIn) == 2 ? 6 : 3;  // units on their way at once
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = blockIdx.x;
+  const int me = threadIdx.x & (p.group - 1);
+  const int t = blockIdx.x * (kThreads / p.group) + threadIdx.x / p.group;
+  if (t >= p.tokens) return;
   const int units = p.D / 16, turned = p.R / 16;
-  const int u = threadIdx.x & (units - 1);  // (D is a power of two)
+  const int u = me & (units - 1);  // (D is a power of two)
   const int heads = p.Hq + 2 * p.Hkv;
-  const int step = kThreads / units;
+  const int step = p.group / units;
   int b = 0, s = t;
   if (FORM != kAppend) {
     b = p.by_seq.div(t);
@@ -93,88 +127,96 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   const bool turns = u < turned;
   const int o0 = STYLE == 1 && turns ? 8 * u : 16 * u;
   const int o1 = STYLE == 1 && turns ? p.R / 2 + 8 * u : 16 * u + 8;
-  float cs[8], sn[8];
-  if (turns) {
-    int pos = p.positions != nullptr ? __ldg(p.positions + t) : s;
-    if (pos < 0 || pos >= p.max_pos) {
-      record_status(p.status, ATTN_ERR_INVALID_ARG);
-      pos = min(max(pos, 0), p.max_pos - 1);
-    }
-    const float4* row =
-        reinterpret_cast<const float4*>(p.table + static_cast<size_t>(pos) * p.R + 16 * u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 w = __ldg(row + i);
-      cs[2 * i] = w.x, sn[2 * i] = w.y, cs[2 * i + 1] = w.z, sn[2 * i + 1] = w.w;
-    }
-    if (FORM == kGrad)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
-  }
+  int slot = -1;
+  if (FORM == kAppend) slot = __ldg(p.slots + t);
+  int pos = s;
+  if (p.positions != nullptr) pos = __ldg(p.positions + t);
   long long page = -1;
   int at = 0;
-  if (FORM == kAppend) {
-    const int slot = __ldg(p.slots + t);
-    if (slot >= 0 && slot < p.num_slots) {
-      page = p.by_page.div(slot);
-      at = slot - static_cast<int>(page) * p.page_size;
-    } else if (slot != -1) {
-      record_status(p.status, ATTN_ERR_INVALID_ARG);
-    }
-  }
-  __nv_bfloat16* const row = p.rows + t * p.ld;
-#pragma unroll 2
-  for (int h = threadIdx.x / units; h < heads; h += step) {
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    const int g = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-    void* const base = is_q ? p.q : is_v ? p.v : p.k;
+  float cs[8], sn[8];
+
+  // Where head h begins on the other side than the projected row.
+  const auto other = [&](int h) -> size_t {
+    const bool is_q = h < p.Hq;
+    const int g = is_q ? h : h >= p.Hq + p.Hkv ? h - p.Hq - p.Hkv : h - p.Hq;
     const int H = is_q ? p.Hq : p.Hkv;
-    size_t other;  // of the head's first dim in base
-    if (FORM == kAppend && !is_q) {
-      if (page < 0) continue;
-      other = ((page * H + g) * p.page_size + at) * p.D;
-    } else if (FORM == kAppend) {
-      other = (static_cast<size_t>(t) * H + g) * p.D;
-    } else {
-      other = ((static_cast<size_t>(b) * H + g) * p.S + s) * p.D;
-    }
-    __nv_bfloat16* const mine = row + static_cast<size_t>(h) * p.D;
-    // A value head's vectors lie side by side.
-    const int a0 = is_v ? 16 * u : o0, a1 = is_v ? 16 * u + 8 : o1;
-    float x[8], y[8];
-    if constexpr (FORM == kGrad) {
-      const TG* from = static_cast<const TG*>(base) + other;
-      load8(from + a0, x);
-      load8(from + a1, y);
-    } else {
-      load8(mine + a0, x);
-      load8(mine + a1, y);
-    }
-    if (turns && !is_v) {
-      if constexpr (STYLE == 1) {
+    if (FORM == kAppend && !is_q) return ((page * H + g) * p.page_size + at) * p.D;
+    if (FORM == kAppend) return (static_cast<size_t>(t) * H + g) * p.D;
+    return ((static_cast<size_t>(b) * H + g) * p.S + s) * p.D;
+  };
+  const auto base = [&](int h) { return h < p.Hq ? p.q : h >= p.Hq + p.Hkv ? p.v : p.k; };
+  __nv_bfloat16* const row = p.rows + t * p.ld;
+  const int h_first = me / units;
+  for (int h0 = h_first; h0 < heads; h0 += N * step) {
+    Raw<TIn> raw[N];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], c = y[i];
-          x[i] = a * cs[i] - c * sn[i];
-          y[i] = a * sn[i] + c * cs[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], c = x[2 * i + 1];
-          x[2 * i] = a * cs[i] - c * sn[i];
-          x[2 * i + 1] = a * sn[i] + c * cs[i];
-          const float d = y[2 * i], e = y[2 * i + 1];
-          y[2 * i] = d * cs[4 + i] - e * sn[4 + i];
-          y[2 * i + 1] = d * sn[4 + i] + e * cs[4 + i];
-        }
+    for (int i = 0; i < N; ++i) {
+      const int h = h0 + i * step;
+      if (h < heads) {
+        const bool is_v = h >= p.Hq + p.Hkv;
+        // A value head's vectors lie side by side.
+        const int a0 = is_v ? 16 * u : o0, a1 = is_v ? 16 * u + 8 : o1;
+        const TIn* from = FORM == kGrad ? static_cast<const TIn*>(base(h)) + other(h)
+                                        : reinterpret_cast<const TIn*>(row) + h * p.D;
+        raw[i].load(from + a0, from + a1);
       }
     }
-    if constexpr (FORM == kGrad) {
-      store8(mine + a0, x);
-      store8(mine + a1, y);
-    } else {
-      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(base) + other;
+    if (h0 == h_first) {  // behind the first loads, which need neither
+      if (FORM == kAppend) {
+        if (slot >= 0 && slot < p.num_slots) {
+          page = p.by_page.div(slot);
+          at = slot - static_cast<int>(page) * p.page_size;
+        } else if (slot != -1) {
+          record_status(p.status, ATTN_ERR_INVALID_ARG);
+        }
+      }
+      if (turns) {
+        if (pos < 0 || pos >= p.max_pos) {
+          record_status(p.status, ATTN_ERR_INVALID_ARG);
+          pos = min(max(pos, 0), p.max_pos - 1);
+        }
+        const float4* angles =
+            reinterpret_cast<const float4*>(p.table + static_cast<size_t>(pos) * p.R + 16 * u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 w = __ldg(angles + i);
+          cs[2 * i] = w.x, sn[2 * i] = w.y, cs[2 * i + 1] = w.z, sn[2 * i + 1] = w.w;
+        }
+        if (FORM == kGrad)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int h = h0 + i * step;
+      const bool is_v = h >= p.Hq + p.Hkv;
+      if (h >= heads || (FORM == kAppend && h >= p.Hq && page < 0)) continue;
+      float x[8], y[8];
+      raw[i].get(x, y);
+      if (turns && !is_v) {
+        if constexpr (STYLE == 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = x[e], c = y[e];
+            x[e] = a * cs[e] - c * sn[e];
+            y[e] = a * sn[e] + c * cs[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = x[2 * e], c = x[2 * e + 1];
+            x[2 * e] = a * cs[e] - c * sn[e];
+            x[2 * e + 1] = a * sn[e] + c * cs[e];
+            const float d = y[2 * e], f = y[2 * e + 1];
+            y[2 * e] = d * cs[4 + e] - f * sn[4 + e];
+            y[2 * e + 1] = d * sn[4 + e] + f * cs[4 + e];
+          }
+        }
+      }
+      const int a0 = is_v ? 16 * u : o0, a1 = is_v ? 16 * u + 8 : o1;
+      __nv_bfloat16* to = FORM == kGrad ? row + h * p.D
+                                        : static_cast<__nv_bfloat16*>(base(h)) + other(h);
       store8(to + a0, x);
       store8(to + a1, y);
     }
@@ -182,9 +224,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
 }
 
 template <Form FORM, typename TG = float>
-cudaError_t launch_rope(const RopeParams& p, int style, cudaStream_t stream) {
+cudaError_t launch_rope(RopeParams p, int style, cudaStream_t stream) {
+  const long long units = (p.Hq + 2ll * p.Hkv) * (p.D / 16);
+  p.group = 32;
+  while (p.group < kThreads && 2 * kPerThread * p.group <= units) p.group *= 2;
+  const int tokens = kThreads / p.group;  // of a CTA
   return launch_programmatic(style == 0 ? rope_kernel<FORM, 0, TG> : rope_kernel<FORM, 1, TG>,
-                             dim3(p.tokens), dim3(kThreads), 0, stream, p);
+                             dim3((p.tokens + tokens - 1) / tokens), dim3(kThreads), 0, stream, p);
 }
 
 // The frequencies' scaling, as internal.h's RopeScaling; one thread per table entry.  In
