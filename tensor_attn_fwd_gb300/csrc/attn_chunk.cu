@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     x.part = -1;
   };
   __shared__ int counts[kCostLevels];  // items of each cost, then ranks
-  __shared__ int loads[kChunkMaxCtas];
+  __shared__ unsigned long long loads[kChunkMaxCtas];
   for (int i = tid; i < kCostLevels; i += kPlanThreads) counts[i] = 0;
   for (int i = tid; i < kChunkMaxCtas; i += kPlanThreads) loads[i] = 0;
   __syncthreads();
@@ -255,11 +255,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
       const int round = rank / n, j = rank - round * n;
       const int c = round & 1 ? n - 1 - j : j;
       pieces[begin_of(c) + round] = x;
-      atomicAdd(loads + c, cost_of(x));
+      atomicAdd(loads + c, static_cast<unsigned long long>(cost_of(x)));
     }
     __syncthreads();
     // Taken if no CTA has much more than its share; otherwise the line is cut.
-    long long most = tid < n ? loads[tid] : 0;
+    long long most = tid < n ? static_cast<long long>(loads[tid]) : 0;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
       most = max(most, __shfl_xor_sync(0xffffffffu, most, off));

@@ -104,6 +104,14 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   __stcs(reinterpret_cast<uint4*>(p), w);
 }
 
+// A pair turned, every product and sum rounded by itself (not fused): the bits that the formula
+// gives in 32-bit arithmetic, whoever computes it.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+  a = x;
+}
+
 // p.group threads to a token.  TG: the type of dq, dk and dv.
 template <Form FORM, int STYLE, typename TG>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
@@ -197,20 +205,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
       if (turns && !is_v) {
         if constexpr (STYLE == 1) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a = x[e], c = y[e];
-            x[e] = a * cs[e] - c * sn[e];
-            y[e] = a * sn[e] + c * cs[e];
-          }
+          for (int e = 0; e < 8; ++e) turn(x[e], y[e], cs[e], sn[e]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float a = x[2 * e], c = x[2 * e + 1];
-            x[2 * e] = a * cs[e] - c * sn[e];
-            x[2 * e + 1] = a * sn[e] + c * cs[e];
-            const float d = y[2 * e], f = y[2 * e + 1];
-            y[2 * e] = d * cs[4 + e] - f * sn[4 + e];
-            y[2 * e + 1] = d * sn[4 + e] + f * cs[4 + e];
+            turn(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
+            turn(y[2 * e], y[2 * e + 1], cs[4 + e], sn[4 + e]);
           }
         }
       }
