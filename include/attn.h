@@ -679,7 +679,7 @@ ATTN_API int attn_rope_append(const void *qkv, long long ld, const float *rope_t
  *     max_keys on this kind of device, and holds the lengths' values.
  *   Bounds that do not ascend within [0, T] set ATTN_ERR_INVALID_ARG in the status word; such
  *     a request has no tokens (or, where requests overlap too often, none has).
- *   D in {64, 128}; at most 2^31 - 1 rows T * Hq (else ATTN_ERR_UNSUPPORTED).
+ *   D in {64, 128, 256}; at most 2^31 - 1 rows T * Hq (else ATTN_ERR_UNSUPPORTED).
  */
 ATTN_API int attn_chunk_plan(const int *cu_tokens, const int *seqlens, int *plan, int B, int T,
                              int Hq, int Hkv, int D, int max_keys, int window, int sinks,

@@ -993,7 +993,7 @@ def attn_chunk_plan(cu_tokens: torch.Tensor, seqlens: torch.Tensor, tokens: int,
     Request b's new tokens are cu_tokens[b] to cu_tokens[b+1] of the ``tokens`` packed ones,
     its last keys of seqlens[b] (attn_pages_append's results).  Each sees the keys up to its own,
     of them the last ``window`` and the first ``sinks`` (``window=None``: all).  ``max_keys``
-    is max_pages * page_size of the block table.  D is 64 or 128.
+    is max_pages * page_size of the block table.  D is 64, 128 or 256.
     """
     call = (_fast or _native()).chunk_plan
     if stream is not None:

@@ -922,11 +922,11 @@ int rope_check_args(const void* qkv, long long ld, const float* table, const int
 int chunk_check_sizes(int B, int T, int Hq, int Hkv, int D) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0)
     return ATTN_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
   if (B > kMaxSeq || T > kMaxSeq || static_cast<long long>(T) * Hq > (1ll << 31) - 1)
     return ATTN_ERR_UNSUPPORTED;
   // Items of the plan, counted with int.
-  if (ChunkTiling(Hq, Hkv).max_items(B, T, Hkv) > (1ll << 26)) return ATTN_ERR_UNSUPPORTED;
+  if (ChunkTiling(Hq, Hkv).max_items(B, T, Hkv, D) > (1ll << 26)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -1038,13 +1038,13 @@ int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long long* entrie
   if (entries == nullptr) return ATTN_ERR_INVALID_ARG;
   const int chk = chunk_check_sizes(B, T, Hq, Hkv, D);
   if (chk != ATTN_OK) return chk;
-  *entries = ChunkLayout(B, ChunkTiling(Hq, Hkv).max_items(B, T, Hkv), chunk_ctas()).total;
+  *entries = ChunkLayout(B, ChunkTiling(Hq, Hkv).max_items(B, T, Hkv, D), chunk_ctas()).total;
   return ATTN_OK;
 }
 
 int attn_chunk_workspace(int D, long long* floats) {
   if (floats == nullptr || D <= 0) return ATTN_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
   *floats = chunk_workspace_floats(chunk_ctas(), D);
   return ATTN_OK;
 }

@@ -17,6 +17,9 @@
 // An item whose tokens fit one tile takes both tile slots for it, which share out its K/V
 // tiles by turns (two softmax states, merged at the end), for the same overlap.
 //
+// At D = 256 tensor memory holds one tile's O, and an item is one tile: both slots take its
+// rows and score them, and each adds up half of O's dims.  K/V tiles are 64 keys.
+//
 // Plan.  Requests differ in their numbers of tokens and keys, so the items' K/V tiles are
 // put in one line and cut into equal parts, one for each CTA; an item that is cut leaves
 // partial results, which a second kernel merges by their LSE (attn_combine's formula).
@@ -96,12 +99,13 @@ static_assert(sizeof(Cut) == kChunkRecord * sizeof(int), "record size");
 struct KvTiles {
   int s, w, e;
   int lo, hi;  // keys: some row sees [lo, hi) and [0, sinks)
-  __device__ __forceinline__ KvTiles(int pos, int tokens, int window, int sinks) {
+  __device__ __forceinline__ KvTiles(int pos, int tokens, int window, int sinks, int tile_keys) {
+    const int shift = tile_keys == 128 ? 7 : 6;
     hi = max(pos + tokens, 0);
     lo = max(pos - window + 1, 0);
-    e = (hi + 127) / 128;
-    w = min(lo / 128, e);
-    s = min((min(sinks, hi) + 127) / 128, w);
+    e = (hi + tile_keys - 1) >> shift;
+    w = min(lo >> shift, e);
+    s = min((min(sinks, hi) + tile_keys - 1) >> shift, w);
   }
   __device__ __forceinline__ int count() const { return s + e - w; }
   __device__ __forceinline__ int tile(int k) const { return k < s ? k : k - s + w; }
@@ -141,7 +145,8 @@ struct PlanParams {
   const int *cu, *seqlens;
   int* plan;
   int B, T, Hq, Hkv, D, max_keys, window, sinks, ctas;
-  int heads, item_tokens;  // KV heads x slices; tokens of an item (two tiles)
+  int heads, tile_tokens, item_tokens;  // KV heads x slices; tokens of a query tile, of an item
+  int tile_keys;
   long long max_items;
   int* status;
 };
@@ -203,10 +208,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     x.token = t0 + from;
     x.tokens = static_cast<uint16_t>(min(p.item_tokens, n_tok - from));
     x.pos = len - n_tok + from;
-    x.flags = ((len & 127) != 0 && (x.pos + x.tokens + 127) / 128 == (len + 127) / 128 ? kRagged : 0) |
-              (n > 1 ? kShared : 0);
+    const bool ragged = len % p.tile_keys != 0 &&
+                        (x.pos + x.tokens - 1) / p.tile_keys == (len - 1) / p.tile_keys;
+    x.flags = (ragged ? kRagged : 0) | (n > 1 ? kShared : 0);
     x.begin = 0;
-    x.end = KvTiles(x.pos, x.tokens, p.window, p.sinks).count();
+    x.end = KvTiles(x.pos, x.tokens, p.window, p.sinks, p.tile_keys).count();
     x.part = -1;
   };
   __shared__ int counts[kCostLevels];  // items of each cost, then ranks
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
   for (int i = tid; i < kChunkMaxCtas; i += kPlanThreads) loads[i] = 0;
   __syncthreads();
   const auto cost_of = [&](const Piece& x) {
-    return x.end * (2 * x.tokens > p.item_tokens ? kCostTwo : kCostOne) + kOverhead;
+    return x.end * (x.tokens > p.tile_tokens ? kCostTwo : kCostOne) + kOverhead;
   };
   long long cost = 0;
   for (int i = tid; i < items; i += kPlanThreads) {
@@ -362,7 +368,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadKWarp = 9, kLoadVWarp = 10;
-constexpr uint32_t kSubBytes = 128 * 128;  // one [128 rows x 64 bf16] swizzled sub-tile
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kLaunchRegs = 168;  // 65536 / 384, rounded down to a multiple of 8
 constexpr uint32_t kRegsSoftmax = 192;
@@ -374,21 +379,28 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
-  static constexpr int kSub = D / 64;
-  static constexpr uint32_t kTileBytes = kSub * kSubBytes;  // 128 x D bf16
-  static constexpr int kStages = (D == 128) ? 5 : 9;
+  static constexpr bool kBoth = D == 256;  // both slots take the item's one query tile
+  static constexpr int kSub = D / 64;      // swizzled sub-tiles of 64 dims
+  static constexpr int kKeys = kBoth ? 64 : 128;  // of a K/V tile
+  static constexpr uint32_t kQSubBytes = 128 * 128, kSubBytes = kKeys * 128;
+  static constexpr uint32_t kQTileBytes = kSub * kQSubBytes;
+  static constexpr int kQTiles = kBoth ? 1 : 2;
+  static constexpr uint32_t kTileBytes = kSub * kSubBytes;  // K or V
+  static constexpr int kStages = (D == 64) ? 9 : 5;
+  static constexpr int kCols = kBoth ? 128 : D;  // of a slot's O
   static constexpr uint32_t kColS0 = 0, kColS1 = 128;
-  static constexpr uint32_t kColO0 = 256, kColO1 = 256 + D;
+  static constexpr uint32_t kColO0 = 256, kColO1 = 256 + kCols;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kBarBytes = 512;
   static constexpr uint32_t kStatBytes = 2 * 128 * 2 * sizeof(float);
   // No room is left to align the tiles: the kernel has no static shared memory, so that the
   // dynamic one begins at a multiple of 1024 (and it looks).
-  static constexpr size_t kSmemBytes =
-      2 * size_t(kTileBytes) + size_t(kStages) * kTileBytes + kBarBytes + kStatBytes;
+  static constexpr size_t kKvOffset = size_t(kQTiles) * kQTileBytes;
+  static constexpr size_t kBarOffset = kKvOffset + size_t(kStages) * kTileBytes;
+  static constexpr size_t kSmemBytes = kBarOffset + kBarBytes + kStatBytes;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
-  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, false, false);
-  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKeys, false, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, kCols, false, true);
 };
 
 struct Bars {
@@ -512,7 +524,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
   // K and V that several items read are kept in L2; those that one reads are let go, or a
   // batch of single tokens would push the others out.
   const uint64_t pol_keep = policy_evict_last();
-  const int boxes = 128 / p.box_keys;      // of a K/V tile
+  const int boxes = C::kKeys / p.box_keys;  // of a K/V tile
   const int batch = 32 / boxes;            // tiles whose boxes the lanes look up at once
   const int my_tile = lane / boxes, my_box = lane % boxes;
   const uint32_t box_bytes = p.box_keys * 128;
@@ -529,8 +541,8 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
   const auto look_up = [&](const Piece& x, int g, int k0) {
     const int k = x.begin + k0 + my_tile;
     if (k >= x.end) return p.page_rows;
-    const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
-    const int key = kv.tile(k) * 128 + my_box * p.box_keys;
+    const KvTiles kv(x.pos, x.tokens, work.window, work.sinks, C::kKeys);
+    const int key = kv.tile(k) * C::kKeys + my_box * p.box_keys;
     if (key >= kv.hi || (key + p.box_keys <= kv.lo && key >= work.sinks)) return p.page_rows;
     const int slot = p.by_page.div(key);
     int page = __ldg(p.block_table + static_cast<size_t>(x.row) * p.max_pages + slot);
@@ -561,7 +573,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
       ahead_of = look_ahead(i + 1);
       continue;
     }
-    const bool dual = x.tokens <= p.tile_tokens;
+    const bool dual = !C::kBoth && x.tokens <= p.tile_tokens;
     const uint64_t pol_kv = x.flags & kShared ? pol_keep : pol_q;
     const int ahead = min(dual ? 2 : 1, n);
     // Tile k of this warp's kind into its stage.
@@ -592,7 +604,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
           if (b < boxes) {
 #pragma unroll
             for (int s = 0; s < C::kSub; ++s)
-              tma_load_3d_hint(to + s * kSubBytes + b * box_bytes, tm, bar, s * 64, row[b], 0,
+              tma_load_3d_hint(to + s * C::kSubBytes + b * box_bytes, tm, bar, s * 64, row[b], 0,
                                pol_kv);
           }
       }
@@ -608,7 +620,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
         mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
 #pragma unroll
         for (int s = 0; s < C::kSub; ++s)
-          tma_load_3d_hint(sQ + t * C::kTileBytes + s * kSubBytes, tmQ, &bars->q_full[t], s * 64, h0,
+          tma_load_3d_hint(sQ + t * C::kQTileBytes + s * C::kQSubBytes, tmQ, &bars->q_full[t], s * 64, h0,
                            token, pol_q);
       }
       __syncwarp();
@@ -623,7 +635,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
       }
       for (int k = 0; k < ahead && ok; ++k) load(k);
       if (!dual && ok) load_q(0, x.token);
-      if (!dual && ok) load_q(1, x.token + p.tile_tokens);
+      if (!C::kBoth && !dual && ok) load_q(1, x.token + p.tile_tokens);
       if (!ok) break;
     }
     ahead_of = look_ahead(i + 1);
@@ -649,7 +661,7 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lan
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   for (int i = lane; i < (r1 - r0) * kChunks; i += 32) {
     const int r = r0 + i / kChunks, c = i % kChunks;
-    *reinterpret_cast<uint4*>(tile + (c >> 3) * kSubBytes + r * 128 + (c & 7) * 16) =
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * Cfg<D>::kSubBytes + r * 128 + (c & 7) * 16) =
         make_uint4(0u, 0u, 0u, 0u);
   }
 }
@@ -659,12 +671,12 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
                          Bars* bars, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr uint64_t kDescK = sdesc_sw128(0, 16, 1024);         // Q and K: K-major
-  constexpr uint64_t kDescV = sdesc_sw128(0, kSubBytes, 1024);  // V: MN-major
+  constexpr uint64_t kDescV = sdesc_sw128(0, C::kSubBytes, 1024);  // V: MN-major
   constexpr uint32_t kHi = static_cast<uint32_t>(kDescK >> 32);
   static_assert(static_cast<uint32_t>(kDescV >> 32) == kHi, "same SBO/swizzle words");
   constexpr uint32_t kLoK = static_cast<uint32_t>(kDescK);
   constexpr uint32_t kLoV = static_cast<uint32_t>(kDescV);
-  constexpr uint32_t kTile16 = C::kTileBytes >> 4;
+  constexpr uint32_t kQTile16 = C::kQTileBytes >> 4, kTile16 = C::kTileBytes >> 4;
   uint32_t q_lo = kLoK + (smem_u32(sQ) >> 4);
   uint32_t k_lo = kLoK + (smem_u32(sKV) >> 4);
   uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
@@ -675,14 +687,15 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
 
   // S_t = Q_q K^T over D in steps of 16 (K-major operands, 128B swizzle).
   auto issue_s = [&](int t, int q, uint32_t kst) {
-    const uint32_t a0 = q_lo + q * kTile16;
+    const uint32_t a0 = q_lo + q * kQTile16;
     const uint32_t b0 = k_lo + kst * kTile16;
     const uint32_t d = tmem + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t off = ((kk >> 2) * kSubBytes + (kk & 3) * 32) >> 4;
-      const uint64_t a = desc_from_words(a0 + off, kHi);
-      const uint64_t b = desc_from_words(b0 + off, kHi);
+      const uint64_t a =
+          desc_from_words(a0 + (((kk >> 2) * C::kQSubBytes + (kk & 3) * 32) >> 4), kHi);
+      const uint64_t b =
+          desc_from_words(b0 + (((kk >> 2) * C::kSubBytes + (kk & 3) * 32) >> 4), kHi);
       if (kk == 0)
         mma_ss_w<0>(d, a, b, C::kIdescQK);
       else
@@ -692,7 +705,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   };
   // O_t (+)= P_t V (P from TMEM, V MN-major), as the halves of P arrive.
   auto issue_pv = [&](int t, uint32_t vst, bool first) -> bool {
-    const uint32_t b0 = v_lo + vst * kTile16;
+    const uint32_t b0 = v_lo + vst * kTile16 + (C::kBoth ? t * (2 * C::kSubBytes >> 4) : 0);
     const uint32_t d = tmem + (t ? C::kColO1 : C::kColO0);
     const uint32_t a = tmem + (t ? C::kColS1 : C::kColS0);
     bool good = true;
@@ -701,8 +714,8 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
       good &= wait_or_abort(&bars->p_full[t][half], p_phase >> t & 1, bars);
       tc_fence_after();
 #pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4) {
-        const int kk = half * 4 + k4;
+      for (int k4 = 0; k4 < C::kKeys / 32; ++k4) {
+        const int kk = half * (C::kKeys / 32) + k4;
         const uint64_t bd = desc_from_words(b0 + kk * (2048 >> 4), kHi);
         if (first && kk == 0)
           mma_ts_w<0>(d, a + kk * 8, bd, C::kIdescPV);
@@ -727,31 +740,31 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
     const Piece x = load_piece(work.pieces + i);
     const int n = x.end - x.begin;
     if (n <= 0) continue;
-    const bool dual = x.tokens <= p.tile_tokens;
-    const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
+    const bool dual = !C::kBoth && x.tokens <= p.tile_tokens;
+    const KvTiles kv(x.pos, x.tokens, work.window, work.sinks, C::kKeys);
     // Keys that no token sees may hold anything, and a weight of 0 times NaN is NaN: their
     // rows of V become zero (those of whole boxes are loaded as zeros).  Keys behind an item's
     // last position, but not the request's, are later tokens'.  Of the item's tiles these are the
     // last, where the window begins and where the sinks end: `clear` is the next of them.
     const int last_tile = x.flags & kRagged ? kv.count() - 1 : kMaxKeys;
     const auto next_clear = [&](int k) {
-      if (k <= kv.s - 1 && (work.sinks & 127) != 0) return kv.s - 1;
-      if (k <= kv.s && (kv.lo & 127) != 0) return kv.s;
+      if (k <= kv.s - 1 && work.sinks % C::kKeys != 0) return kv.s - 1;
+      if (k <= kv.s && kv.lo % C::kKeys != 0) return kv.s;
       return last_tile;
     };
     int clear = next_clear(x.begin);
     auto clear_unseen = [&](uint32_t vst, int k) {
-      const int key0 = 128 * kv.tile(k);
+      const int key0 = C::kKeys * kv.tile(k);
       uint8_t* tile = sKV + vst * C::kTileBytes;
-      const int lo = max(work.sinks - key0, 0), hi = min(kv.lo - key0, 128);
+      const int lo = max(work.sinks - key0, 0), hi = min(kv.lo - key0, C::kKeys);
       if (lo < hi) zero_rows<D>(tile, lo, hi, lane);
-      if (k == last_tile) zero_rows<D>(tile, kv.hi - key0, 128, lane);
+      if (k == last_tile) zero_rows<D>(tile, kv.hi - key0, C::kKeys, lane);
       fence_proxy_async_smem();
       __syncwarp();
       clear = k < last_tile ? next_clear(k + 1) : kMaxKeys;
     };
     if (dual) q_tile ^= 1;
-    const uint32_t q_mine = dual ? 1u << q_tile : 3u;
+    const uint32_t q_mine = dual ? 1u << q_tile : C::kBoth ? 1u : 3u;
     for (int t = 0; t < 2 && ok; ++t)
       if (q_mine >> t & 1) ok = wait_warp(&bars->q_full[t], q_phase >> t & 1, bars);
     if (!ok) break;
@@ -766,7 +779,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
       constexpr bool DUAL = decltype(dual_constant)::value;
       const auto release_q = [&] {  // after the last scores
         if (!DUAL) tc_commit_w(&bars->q_empty[0]);
-        tc_commit_w(&bars->q_empty[DUAL ? q_tile : 1]);
+        if (DUAL || !C::kBoth) tc_commit_w(&bars->q_empty[DUAL ? q_tile : 1]);
       };
       // (What the operands' addresses make is worked out here: kept for both instances, it
       // would not fit the registers.)
@@ -780,7 +793,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
         good &= acquire_kv(kst);
         tc_fence_after();
       }
-      if (!DUAL || n > 1) issue_s(1, DUAL ? q_tile : 1, kst);
+      if (!DUAL || n > 1) issue_s(1, DUAL ? q_tile : C::kBoth ? 0 : 1, kst);
       tc_commit_w(&bars->kv_empty[kst]);
       if (n <= (DUAL ? 2 : 1)) release_q();
       for (int left = n; left > 0;) {  // tiles whose P V is to come
@@ -797,7 +810,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
               good &= acquire_kv(kst);
               tc_fence_after();
             }
-            issue_s(t, DUAL ? q_tile : t, kst);
+            issue_s(t, DUAL ? q_tile : C::kBoth ? 0 : t, kst);
           } else {
             tc_commit_w(&bars->o_full[t]);
           }
@@ -812,10 +825,14 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
         }
       }
     };
-    if (dual)
-      run(std::true_type{});
-    else
+    if constexpr (C::kBoth) {
       run(std::false_type{});
+    } else {
+      if (dual)
+        run(std::true_type{});
+      else
+        run(std::false_type{});
+    }
     ok = __all_sync(0xffffffffu, good);
   }
   if (!ok) record_status(p.status, ATTN_ERR_TIMEOUT);
@@ -826,11 +843,14 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
 
 // A partial result: the rows' O (by their own sum) in fp32, four columns of all 128 rows of a
 // query tile beside each other, so that a warp's 32 rows are stored and read in whole lines.
-__device__ __forceinline__ size_t part_at(int part, int tile, int D, int column, int tile_row) {
-  return ((static_cast<size_t>(2 * part + tile) * (D / 4) + column / 4) * 128 + tile_row) * 4;
+template <int D>
+__device__ __forceinline__ size_t part_at(int part, int tile, int column, int tile_row) {
+  return ((static_cast<size_t>(Cfg<D>::kQTiles * part + tile) * (D / 4) + column / 4) * 128 +
+          tile_row) * 4;
 }
+template <int D>
 __device__ __forceinline__ int part_lse_at(int part, int tile, int tile_row) {
-  return (2 * part + tile) * 128 + tile_row;
+  return (Cfg<D>::kQTiles * part + tile) * 128 + tile_row;
 }
 
 // ------------------------------------------------------------------ softmax
@@ -857,10 +877,10 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
 
   for (int i = work.begin; i < work.end && ok; ++i) {
     const Piece x = load_piece(work.pieces + i);
-    const bool dual = x.tokens <= p.tile_tokens;
+    const bool dual = !C::kBoth && x.tokens <= p.tile_tokens;
     const int kv_head = p.by_slices.div(x.head);
     const int slice_head = (x.head - kv_head * p.slices) * p.slice_heads + row_head;
-    const int token = row_token + (dual ? 0 : t * p.tile_tokens);  // of the item's
+    const int token = row_token + (C::kBoth || dual ? 0 : t * p.tile_tokens);  // of the item's
     const bool row_valid =
         row_token < p.tile_tokens && token < x.tokens && slice_head < p.group;
     const bool warp_valid = __any_sync(0xffffffffu, row_valid);
@@ -874,7 +894,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     int k = k_first;
     int sink_tiles, skip;  // tiles from sink_tiles on lie `skip` further on
     {
-      const KvTiles kv(x.pos, x.tokens, work.window, work.sinks);
+      const KvTiles kv(x.pos, x.tokens, work.window, work.sinks, C::kKeys);
       sink_tiles = kv.s;
       skip = kv.w - kv.s;
     }
@@ -899,10 +919,10 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
       // flight while the first half is masked and reduced.
       uint32_t sa[64], sb[64];
       tmem_ld64(tS, sa);
-      tmem_ld64_nowait(tS + 64, sb);
-      const int key0 = (k < sink_tiles ? k : k + skip) * 128;
+      if constexpr (C::kKeys == 128) tmem_ld64_nowait(tS + 64, sb);
+      const int key0 = (k < sink_tiles ? k : k + skip) * C::kKeys;
       const bool need_mask = __any_sync(
-          0xffffffffu, key0 + 127 > limit || (key0 < win_lo && key0 + 127 >= work.sinks));
+          0xffffffffu, key0 + C::kKeys > limit + 1 || (key0 < win_lo && key0 + C::kKeys > work.sinks));
       auto mask_half = [&](uint32_t(&y)[64], int h) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -923,13 +943,15 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           ch[e] = max3(ch[e], __uint_as_float(sa[c + e]), __uint_as_float(sa[c + 4 + e]));
-      tmem_ld_wait64(sb);
-      if (need_mask) mask_half(sb, 1);
+      if constexpr (C::kKeys == 128) {
+        tmem_ld_wait64(sb);
+        if (need_mask) mask_half(sb, 1);
 #pragma unroll
-      for (int c = 0; c < 64; c += 8)
+        for (int c = 0; c < 64; c += 8)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          ch[e] = max3(ch[e], __uint_as_float(sb[c + e]), __uint_as_float(sb[c + 4 + e]));
+          for (int e = 0; e < 4; ++e)
+            ch[e] = max3(ch[e], __uint_as_float(sb[c + e]), __uint_as_float(sb[c + 4 + e]));
+      }
       const float m_tile = max3(ch[0], ch[1], fmaxf(ch[2], ch[3])) * sl2;
 
       bool rescale = false;
@@ -947,7 +969,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
         // The slot's last P V is complete: S was committed after it.
         const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < C::kCols; c += 32) {
           uint32_t orow[32];
           tmem_ld32(tO + c, orow);
 #pragma unroll
@@ -969,7 +991,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc2[e] = f2_pack(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < C::kKeys / 32; ++c) {
         const uint32_t* src = c < 2 ? &sa[32 * c] : &sb[32 * (c - 2)];
         uint32_t pk[16];
 #pragma unroll
@@ -984,11 +1006,12 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
           pk[e] = pack_bf16x2(p0, p1);
         }
         tmem_st16(tS + 16 * c, pk);
-        if (c & 1) {
-          // Keys [64*(c/2), 64*(c/2)+64) of P (and any O rescale) are in TMEM.
+        constexpr int kHalf = C::kKeys / 64;
+        if (c % kHalf == kHalf - 1) {
+          // Half of P's keys (and any O rescale) are in TMEM.
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive_warp(&bars->p_full[t][c >> 1]);
+          mbar_arrive_warp(&bars->p_full[t][c / kHalf]);
         }
       }
       float rsum = 0.f;
@@ -1035,9 +1058,12 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     const PieceEnd to = load_piece_end(work.pieces + i);
     const auto row_of = [&] {  // of O and LSE
       const int kv_head = p.by_slices.div(to.head);
-      return static_cast<size_t>(to.token + row_token + (dual ? 0 : t * p.tile_tokens)) * p.Hq +
+      return static_cast<size_t>(to.token + row_token +
+                                 (C::kBoth || dual ? 0 : t * p.tile_tokens)) * p.Hq +
              kv_head * p.group + (to.head - kv_head * p.slices) * p.slice_heads + row_head;
     };
+    const int c_off = C::kBoth ? t * C::kCols : 0;  // dim of the slot's first column
+    const bool writes_lse = row_valid && (!(C::kBoth || dual) || t == 0);
     // Lane pairs swap half their segments (pair_transpose8), so that each store writes 64
     // contiguous bytes of a row.
     const int pb = lane & 1;
@@ -1056,15 +1082,15 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     };
     const auto pair_rows = [&](size_t at, __nv_bfloat16*& even, __nv_bfloat16*& odd) {
       const size_t other = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(at), 1);
-      even = p.o + (pb ? other : at) * D + 16 * pb;
-      odd = p.o + (pb ? at : other) * D + 16 * pb;
+      even = p.o + (pb ? other : at) * D + c_off + 16 * pb;
+      odd = p.o + (pb ? at : other) * D + c_off + 16 * pb;
     };
     if (!dual && to.part < 0 && n > 0) {
       // A whole item of two tiles: 64 columns of O at a time, the next ones on their way.  (The
       // time of an item around its tiles is that of this.)
       uint32_t wa[64], wb[64];
       tmem_ld64(tO, wa);
-      if constexpr (D == 128) tmem_ld64_nowait(tO + 64, wb);
+      if constexpr (C::kCols == 128) tmem_ld64_nowait(tO + 64, wb);
       const size_t at = row_of();
       __nv_bfloat16 *even, *odd;
       pair_rows(at, even, odd);
@@ -1075,11 +1101,11 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
         store_columns(c + 32, &w[32], even, odd);
       };
       scaled(wa, 0);
-      if constexpr (D == 128) {
+      if constexpr (C::kCols == 128) {
         tmem_ld_wait64(wb);
         scaled(wb, 64);
       }
-      if (row_valid && store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
+      if (writes_lse && store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
         p.lse[at] = own_lse * kLn2;
       continue;
     }
@@ -1106,8 +1132,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     // slot writes half), N at a time.
     const auto finish = [&](auto n_constant, int c_begin, int c_end) {
       constexpr int N = decltype(n_constant)::value;
-      const int tile = dual ? 0 : t;
-      const bool writes_lse = row_valid && (!dual || t == 0);
+      const int tile = C::kBoth || dual ? 0 : t;
       if (to.part >= 0) {
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += N) {
@@ -1115,12 +1140,12 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
           own_columns(c, w);
 #pragma unroll
           for (int e = 0; e < N; e += 4) {
-            float* y = p.part_o + part_at(to.part, tile, D, c + e, tile_row);
+            float* y = p.part_o + part_at<D>(to.part, tile, c_off + c + e, tile_row);
             if (store_in_bounds(y, 16, p.part_o, p.part_o_bytes, p.status))
               *reinterpret_cast<uint4*>(y) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
           }
         }
-        float* y = p.part_lse + part_lse_at(to.part, tile, tile_row);
+        float* y = p.part_lse + part_lse_at<D>(to.part, tile, tile_row);
         if (writes_lse && store_in_bounds(y, 4, p.part_lse, p.part_lse_bytes, p.status)) *y = own_lse;
         return;
       }
@@ -1140,7 +1165,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     if (dual)
       finish(std::integral_constant<int, 32>{}, t * (D / 2), (t + 1) * (D / 2));
     else
-      finish(std::integral_constant<int, 64>{}, 0, D);
+      finish(std::integral_constant<int, 64>{}, 0, C::kCols);
     if (dual && n > 0) {
       // The other slot has read this one's O before it is written again.
       tc_fence_before();
@@ -1165,9 +1190,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * C::kTileBytes;
-  Bars* bars = reinterpret_cast<Bars*>(sKV + C::kStages * C::kTileBytes);
-  float2* stats = reinterpret_cast<float2*>(sKV + C::kStages * C::kTileBytes + C::kBarBytes);
+  uint8_t* sKV = smem + C::kKvOffset;
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOffset);
+  float2* stats = reinterpret_cast<float2*>(smem + C::kBarOffset + C::kBarBytes);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -1267,11 +1292,11 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int part = cut.part + s0 + min(s, n - 1);
-      lse[s] = s < n ? p.part_lse[part_lse_at(part, tile, tile_row)] : -INFINITY;
+      lse[s] = s < n ? p.part_lse[part_lse_at<D>(part, tile, tile_row)] : -INFINITY;
 #pragma unroll
       for (int q = 0; q < kMergeColumns / 4; ++q)
         x[s][q] = *reinterpret_cast<const float4*>(
-            p.part_o + part_at(part, tile, D, c + 4 * q, tile_row));
+            p.part_o + part_at<D>(part, tile, c + 4 * q, tile_row));
     }
     const float higher = fmaxf(fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])), top);
     if (higher == -INFINITY) continue;
@@ -1320,9 +1345,9 @@ cudaError_t launch_impl(const void* q, const void* k, const void* v, const Chunk
   e = launch_programmatic(attn_chunk_kernel<D>, dim3(p.ctas), dim3(kThreads), C::kSmemBytes, stream,
                           tmQ, tmK, tmV, p);
   // (Items of so few tiles are never cut.)
-  if (e != cudaSuccess || p.max_pages * p.page_size <= (2 * kSnap - 1) * 128) return e;
-  return launch_programmatic(chunk_merge_kernel<D>, dim3(p.ctas, D / kMergeColumns, 2), dim3(128), 0,
-                             stream, p);
+  if (e != cudaSuccess || p.max_pages * p.page_size <= (2 * kSnap - 1) * C::kKeys) return e;
+  return launch_programmatic(chunk_merge_kernel<D>, dim3(p.ctas, D / kMergeColumns, C::kQTiles),
+                             dim3(128), 0, stream, p);
 }
 
 }  // namespace
@@ -1335,8 +1360,10 @@ cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int 
   const ChunkTiling tiling(Hq, Hkv);
   PlanParams p = {cu, seqlens, plan, B, T, Hq, Hkv, D, max_keys, window, sinks, chunk_ctas()};
   p.heads = Hkv * tiling.slices;
-  p.item_tokens = 2 * tiling.tile_tokens;
-  p.max_items = tiling.max_items(B, T, Hkv);
+  p.tile_tokens = tiling.tile_tokens;
+  p.item_tokens = tiling.item_tokens(D);
+  p.tile_keys = chunk_tile_keys(D);
+  p.max_items = tiling.max_items(B, T, Hkv, D);
   p.status = status;
   return launch_programmatic(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
 }
@@ -1352,7 +1379,7 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.ctas = chunk_ctas();
-  const size_t part_rows = 2ull * p.ctas * 256;
+  const size_t part_rows = 2ull * p.ctas * chunk_part_rows(D);
   p.part_o = workspace;
   p.part_lse = workspace + part_rows * D;
   p.o_bytes = static_cast<size_t>(T) * Hq * D * 2;
@@ -1374,8 +1401,9 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   p.slice_heads = tiling.slice_heads;
   p.tile_tokens = tiling.tile_tokens;
   p.box_keys = paged.page_size % 128 == 0 ? 128 : paged.page_size % 64 == 0 ? 64 : 32;
+  if (p.box_keys > chunk_tile_keys(D)) p.box_keys = chunk_tile_keys(D);
   p.page_rows = paged.num_pages * Hkv * paged.page_size;
-  const ChunkLayout layout(B, tiling.max_items(B, T, Hkv), p.ctas);
+  const ChunkLayout layout(B, tiling.max_items(B, T, Hkv, D), p.ctas);
   p.begins = layout.begins;
   p.firsts = layout.firsts;
   p.cuts = layout.cuts;
@@ -1384,8 +1412,8 @@ cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_
   p.by_heads = FixedDiv(tiling.slice_heads);
   p.by_slices = FixedDiv(tiling.slices);
   p.scale_log2 = scale * 1.4426950408889634f;
-  return D == 128 ? launch_impl<128>(q, k_cache, v_cache, p, stream)
-                  : launch_impl<64>(q, k_cache, v_cache, p, stream);
+  const auto launch = D == 256 ? launch_impl<256> : D == 128 ? launch_impl<128> : launch_impl<64>;
+  return launch(q, k_cache, v_cache, p, stream);
 }
 
 }  // namespace attn

@@ -272,11 +272,14 @@ struct ChunkTiling {
         slices((group + 127) / 128),
         slice_heads((group + slices - 1) / slices),
         tile_tokens(128 / slice_heads) {}
-  // Items of two query tiles (the last of a request may be one), at most.
-  long long max_items(int B, int T, int Hkv) const {
-    return (static_cast<long long>(T) / (2 * tile_tokens) + B) * Hkv * slices;
+  // Items are two query tiles (the last of a request may be one), or one at D = 256.
+  int item_tokens(int D) const { return D == 256 ? tile_tokens : 2 * tile_tokens; }
+  long long max_items(int B, int T, int Hkv, int D) const {
+    return (static_cast<long long>(T) / item_tokens(D) + B) * Hkv * slices;
   }
 };
+inline int chunk_tile_keys(int D) { return D == 256 ? 64 : 128; }   // of a K/V tile
+inline int chunk_part_rows(int D) { return D == 256 ? 128 : 256; }  // of an item
 // CTAs that share the work on the current device: one an SM.
 constexpr int kChunkMaxCtas = 512;
 int chunk_ctas();
@@ -295,8 +298,10 @@ struct ChunkLayout {
     total = pieces + kChunkRecord * (max_items + ctas);
   }
 };
-// Partial results, two for each CTA, of 256 rows with their LSE.
-inline long long chunk_workspace_floats(int ctas, int D) { return 2ll * ctas * 256 * (D + 1); }
+// Partial results, two for each CTA, with their LSE.
+inline long long chunk_workspace_floats(int ctas, int D) {
+  return 2ll * ctas * chunk_part_rows(D) * (D + 1);
+}
 cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
                               int Hkv, int D, int max_keys, int window, int sinks,
                               cudaStream_t stream, int* status);
