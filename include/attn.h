@@ -585,7 +585,8 @@ ATTN_API int attn_pages_copy(void *k_cache, void *v_cache, const int *src, const
  *
  *   new_lens [B]; T: tokens of the step, at least the sum of new_lens
  *   block_table_out [B,max_pages], refs_out [num_pages], seqlens_out [B] (the lengths
- *     with the tokens taken); each may be its input
+ *     with the tokens taken); each may be its input (seqlens_out not new_lens:
+ *     ATTN_ERR_INVALID_ARG)
  *   cu_tokens [B+1]: row b's tokens are cu_tokens[b] to cu_tokens[b+1] of the packed
  *     ones, whether it takes them or not (at most T)
  *   positions [T], slots [T]: token i of row b stands at p = seqlens[b] + i, in slot
@@ -593,7 +594,9 @@ ATTN_API int attn_pages_copy(void *k_cache, void *v_cache, const int *src, const
  *     that are not taken, and those behind the last row's, have position 0 and slot -1.
  *   counts [2]: pages needed and pages free
  *   workspace: attn_pages_append_workspace(num_pages, B) int32, contents undefined
- *   Entries, alignment and limits as the other page calls; num_pages * page_size < 2^31.
+ *   An entry outside [-1, num_pages) sets ATTN_ERR_INVALID_ARG in the status word and counts
+ *   as -1; that entries name pages with holders is not checked.  Alignment and limits as the
+ *   other page calls; num_pages * page_size < 2^31.
  */
 ATTN_API int attn_pages_append(const int *block_table, const int *refs, const int *seqlens,
                                const int *new_lens, int *block_table_out, int *refs_out,

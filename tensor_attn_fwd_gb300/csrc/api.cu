@@ -948,6 +948,8 @@ int attn_pages_append(const int* block_table, const int* refs, const int* seqlen
   const int chk = pages_check_args(block_table, refs, block_table_out, refs_out, B, max_pages,
                                    num_pages, page_size);
   if (chk != ATTN_OK) return chk;
+  // (Rows' new tokens are read after the lengths are written.)
+  if (seqlens_out == new_lens) return ATTN_ERR_INVALID_ARG;
   // Slots are numbered, and rows and tokens counted, with int.
   if (static_cast<long long>(num_pages) * page_size > (1ll << 31) - 1 || T > kMaxSeq || B > kMaxSeq)
     return ATTN_ERR_UNSUPPORTED;

@@ -14,6 +14,7 @@
 //            read-only slots          3 count the pages each row needs
 //            4 hand them out
 //   compact  1 count live             2 list holes and movers   3 renumber
+//   append   at its struct
 // What a call costs beyond the tables' bytes is latency: round trips to L2 that follow
 // each other, and the barriers.  So the number of CTAs that take part grows with the
 // call (us for fork / compact / free, graph replays):
@@ -56,7 +57,8 @@ constexpr int kWarps = kThreads / 32;
 // The largest calls (elements of arrays) of one CTA, and of one cluster.
 constexpr long long kSmallForkEntries = 8192, kSmallForkPages = 6144, kSmallForkSlots = 8192;
 constexpr long long kSmallCompactEntries = 8192, kSmallCompactPages = 4096;
-constexpr long long kSmallAppendEntries = 8192, kSmallAppendPages = 8192, kSmallAppendTokens = 16384;
+constexpr long long kSmallAppendEntries = 8192, kSmallAppendPages = 8192, kSmallAppendTokens = 4096;
+constexpr long long kSmallAppendSlots = 128;  // of a row's new tokens
 constexpr long long kClusterWork = 1 << 15;
 constexpr int kClusterCtas = 16;  // past the portable 8: the kernels opt in
 constexpr int kMaxCopiers = 6;    // append: clusters that copy the table
@@ -659,7 +661,11 @@ struct CompactOp {
 // the workers'.
 // Token sums are clamped to T + 1 (a sum that saturates stays associative).
 //
-// Latency, again: each phase is a few dependent trips to L2 (us TODO).
+// Latency, again: each phase is a few dependent trips to L2.  1024 rows of 1024 slots, 560,000
+// pages and 9192 tokens take 15.0 us, with the workers alone 22.6.  Where all fits one CTA's shared
+// memory (run_small), there are no phases: 8 rows 3.7 us instead of 10.2, 64 rows of 128 slots
+// with 2048 tokens 8.1 instead of 12.0.  But its tokens take turns, and a row's slots one thread:
+// 15360 tokens took 19.2 us instead of 12.7, one row of 500 new slots 30.4 instead of 19.1.
 struct AppendOp {
   const int *table, *refs, *seqlens, *new_lens;
   int *table_out, *refs_out, *seqlens_out, *cu, *positions, *slots, *counts;
@@ -1116,7 +1122,7 @@ struct AppendOp {
     int n_free = 0, lacking = 0;
     for (int p = p0; p < p1; ++p) n_free += held[pad(p)] == 0;
     for (int s = x.lo; s < x.hi; ++s) lacking += page_of[t * M + s] < 0;
-    // (Fields of 30, 17 and 17 bits: rows <= 2^10, tokens clamped to T + 1 <= 2^14, entries and
+    // (Fields of 30, 17 and 17 bits: rows <= 2^10, tokens clamped to T + 1 < 2^13, entries and
     // pages <= 2^13.)
     const unsigned long long mine = static_cast<unsigned long long>(tokens(x.n)) |
                                     static_cast<unsigned long long>(lacking) << 30 |
@@ -1372,7 +1378,7 @@ cudaError_t launch_pages_append(const int* table, const int* refs, const int* se
   op.status = status;
   const long long entries = static_cast<long long>(B) * M;
   if (entries <= kSmallAppendEntries && P <= kSmallAppendPages && B <= kThreads &&
-      T < kSmallAppendTokens) {
+      T <= kSmallAppendTokens && T <= kSmallAppendSlots * page_size) {
     const size_t smem = AppendOp::small_bytes(entries, P, B);
     const auto small = pages_append_small_kernel;
     const cudaError_t e =

@@ -34,7 +34,7 @@ M4 = 0x10000004      # 4-byte aligned
 M2 = 0x10000002
 
 
-def c_append(lib, bt=A, refs=A, sl=A, nl=A, bto=A, ro=A, slo=A, cu=A, pos=A, slots=A, cnt=A, ws=A,
+def c_append(lib, bt=A, refs=A, sl=A, nl=A + 256, bto=A, ro=A, slo=A, cu=A, pos=A, slots=A, cnt=A, ws=A,
              B=2, T=8, M=4, P=16, ps=32):
     return lib.attn_pages_append(bt, refs, sl, nl, bto, ro, slo, cu, pos, slots, cnt, ws, B, T, M, P,
                                  ps, None)
@@ -55,6 +55,10 @@ def c_append(lib, bt=A, refs=A, sl=A, nl=A, bto=A, ro=A, slo=A, cu=A, pos=A, slo
 ])
 def test_append_rejects(lib, kw, code):
     assert c_append(lib, **kw) == code
+
+
+def test_append_rejects_lengths_over_new_ones(lib):
+    assert c_append(lib, nl=A + 64, slo=A + 64) == INV
 
 
 def test_append_workspace_rejects(lib):
@@ -255,7 +259,8 @@ def append_case(rng, B, M, P, ps, most_new, reserved=0.0):
 # many slots; many pages a warp; more rows than threads
 APPEND = [(1, 1, 1, 32, 32), (1, 5, 40, 32, 1), (7, 9, 100, 64, 70), (64, 16, 1000, 96, 300),
           (300, 33, 6000, 32, 9), (900, 100, 20000, 128, 500), (2500, 20, 60000, 32, 200),
-          (12, 300, 3000, 32, 4000), (40, 20, 1200001, 32, 100), (20000, 3, 70001, 32, 40)]
+          (12, 300, 3000, 32, 4000), (40, 20, 1200001, 32, 100), (20000, 3, 70001, 32, 40),
+          (2, 129, 700, 32, 4000), (60, 128, 8192, 64, 130), (1000, 8, 8192, 64, 4)]
 
 
 @pytest.mark.gpu
