@@ -17,8 +17,10 @@
 // An item whose tokens fit one tile takes both tile slots for it, which share out its K/V
 // tiles by turns (two softmax states, merged at the end), for the same overlap.
 //
-// At D = 256 tensor memory holds one tile's O, and an item is one tile: both slots take its
-// rows and score them, and each adds up half of O's dims.  K/V tiles are 64 keys.
+// At D = 256 tensor memory holds one tile's O, and an item is one tile, whose K/V tiles of 64
+// keys the slots take by turns.  Both add to the one O, so they share each row's reference
+// maximum: it goes from slot to slot with the tiles.  (Scored by both slots, each adding up half
+// of O's dims, four prompts of 2048 tokens took 183 us instead of 125, 16/4 heads.)
 //
 // Plan.  Requests differ in their numbers of tokens and keys, so the items' K/V tiles are
 // put in one line and cut into equal parts, one for each CTA; an item that is cut leaves
@@ -119,7 +121,6 @@ struct KvTiles {
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
 constexpr int kCostLevels = 2048;
-constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Exclusive prefix sum of one value per thread over the CTA; total: their sum.
 template <typename X>
@@ -381,11 +382,10 @@ constexpr uint32_t kRegsOther = 120;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kLaunchRegs,
               "register split must use exactly the launch allocation");
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
-  static constexpr bool kBoth = D == 256;  // both slots take the item's one query tile
+  static constexpr bool kBoth = D == 256;  // one query tile, whose one O both slots add to
   static constexpr int kSub = D / 64;      // swizzled sub-tiles of 64 dims
   static constexpr int kKeys = kBoth ? 64 : 128;  // of a K/V tile
   static constexpr uint32_t kQSubBytes = 128 * 128, kSubBytes = kKeys * 128;
@@ -393,7 +393,7 @@ struct Cfg {
   static constexpr int kQTiles = kBoth ? 1 : 2;
   static constexpr uint32_t kTileBytes = kSub * kSubBytes;  // K or V
   static constexpr int kStages = (D == 64) ? 9 : 5;
-  static constexpr int kCols = kBoth ? 128 : D;  // of a slot's O
+  static constexpr int kCols = kBoth ? 128 : D;  // of O that a slot writes
   static constexpr uint32_t kColS0 = 0, kColS1 = 128;
   static constexpr uint32_t kColO0 = 256, kColO1 = 256 + kCols;
   static constexpr uint32_t kTmemCols = 512;
@@ -406,7 +406,7 @@ struct Cfg {
   static constexpr size_t kSmemBytes = kBarOffset + kBarBytes + kStatBytes;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKeys, false, false);
-  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, kCols, false, true);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
 };
 
 struct Bars {
@@ -415,6 +415,7 @@ struct Bars {
   uint64_t s_full[2], p_full[2][2], o_full[2];
   // Items of one tile: the two states of a warp's 32 rows are there to be merged; merged.
   uint64_t merge_ready[4], merge_done[4];
+  uint64_t max_ready[2][4];  // one O: the rows' reference maxima, of each slot's last tile
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
@@ -582,7 +583,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tm, const C
     }
     const bool dual = !C::kBoth && x.tokens <= p.tile_tokens;
     const uint64_t pol_kv = x.flags & kShared ? pol_keep : pol_q;
-    const int ahead = min(dual ? 2 : 1, n);
+    const int ahead = min(C::kBoth || dual ? 2 : 1, n);
     // Tile k of this warp's kind into its stage.
     auto load = [&](int k) {
       // V_k lies in the batch of tile k or the one before.
@@ -688,7 +689,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   uint32_t k_lo = kLoK + (smem_u32(sKV) >> 4);
   uint32_t v_lo = kLoV + (smem_u32(sKV) >> 4);
   uint32_t q_phase = 0;  // bit t: Q tile t's
-  int q_tile = 1;        // of items of one tile (see load_role)
+  int q_tile = C::kBoth ? 0 : 1;  // of items of one tile (see load_role)
   uint32_t p_phase = 0;  // bit t: slot t's
   bool ok = true;
 
@@ -712,8 +713,8 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
   };
   // O_t (+)= P_t V (P from TMEM, V MN-major), as the halves of P arrive.
   auto issue_pv = [&](int t, uint32_t vst, bool first) -> bool {
-    const uint32_t b0 = v_lo + vst * kTile16 + (C::kBoth ? t * (2 * C::kSubBytes >> 4) : 0);
-    const uint32_t d = tmem + (t ? C::kColO1 : C::kColO0);
+    const uint32_t b0 = v_lo + vst * kTile16;
+    const uint32_t d = tmem + (t && !C::kBoth ? C::kColO1 : C::kColO0);
     const uint32_t a = tmem + (t ? C::kColS1 : C::kColS0);
     bool good = true;
 #pragma unroll
@@ -786,7 +787,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
       constexpr bool DUAL = decltype(dual_constant)::value;
       const auto release_q = [&] {  // after the last scores
         if (!DUAL) tc_commit_w(&bars->q_empty[0]);
-        if (DUAL || !C::kBoth) tc_commit_w(&bars->q_empty[DUAL ? q_tile : 1]);
+        tc_commit_w(&bars->q_empty[DUAL ? q_tile : 1]);
       };
       // (What the operands' addresses make is worked out here: kept for both instances, it
       // would not fit the registers.)
@@ -800,7 +801,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
         good &= acquire_kv(kst);
         tc_fence_after();
       }
-      if (!DUAL || n > 1) issue_s(1, DUAL ? q_tile : C::kBoth ? 0 : 1, kst);
+      if (!DUAL || n > 1) issue_s(1, DUAL ? q_tile : 1, kst);
       tc_commit_w(&bars->kv_empty[kst]);
       if (n <= (DUAL ? 2 : 1)) release_q();
       for (int left = n; left > 0;) {  // tiles whose P V is to come
@@ -811,14 +812,15 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
             good &= acquire_kv(vst);
             if (k == clear) clear_unseen(vst, k);
           }
-          good &= issue_pv(t, vst, k < x.begin + (DUAL ? 2 : 1));
+          good &= issue_pv(t, vst, k < x.begin + (DUAL && !C::kBoth ? 2 : 1));
+          if (C::kBoth) tc_commit_w(&bars->o_full[t]);
           if (more) {
             if (DUAL || t == 0) {
               good &= acquire_kv(kst);
               tc_fence_after();
             }
-            issue_s(t, DUAL ? q_tile : C::kBoth ? 0 : t, kst);
-          } else {
+            issue_s(t, DUAL ? q_tile : t, kst);
+          } else if (!C::kBoth) {
             tc_commit_w(&bars->o_full[t]);
           }
           if (DUAL || t == 1) {
@@ -833,7 +835,7 @@ __device__ void mma_role(const ChunkParams& p, const Work& work, uint8_t* sQ, ui
       }
     };
     if constexpr (C::kBoth) {
-      run(std::false_type{});
+      run(std::true_type{});
     } else {
       if (dual)
         run(std::true_type{});
@@ -880,6 +882,9 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
   const int row_token = p.by_heads.div(tile_row);  // of the tile's
   const int row_head = tile_row - row_token * p.slice_heads;
   uint32_t s_phase = 0, o_phase = 0, merge_phase = 0;
+  // One O: the tiles of the pieces before, this slot's and the other's, and those of the other
+  // whose maxima this warp could wait for.
+  uint32_t own_pv = 0, other_pv = 0, other_max = 0;
   bool ok = true;
 
   for (int i = work.begin; i < work.end && ok; ++i) {
@@ -897,7 +902,8 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     const int limit = x.pos + (row_valid ? token : first_token);
     const int win_lo = limit - work.window + 1;
     // This slot's tiles of the piece: all, or every second one.
-    const int k_first = x.begin + (dual ? t : 0), dk = dual ? 2 : 1;
+    const bool turns = C::kBoth || dual;
+    const int k_first = x.begin + (turns ? t : 0), dk = turns ? 2 : 1;
     int k = k_first;
     int sink_tiles, skip;  // tiles from sink_tiles on lie `skip` further on
     {
@@ -963,7 +969,28 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
 
       bool rescale = false;
       float alpha = 1.f;
-      if (first) {
+      if constexpr (C::kBoth) {
+        // One O has one reference: that of the tile before, from the other slot, or this tile's
+        // maximum.  It goes on to the other slot ahead of the exponentials.
+        const int j = k - x.begin;
+        if (j > 1) ok = wait_warp(&bars->o_full[t], (own_pv + (j >> 1) - 1) & 1, bars);
+        if (!ok) break;
+        float m_row = m_tile;
+        if (j > 0) {
+          ok = wait_warp(&bars->max_ready[1 - t][quad], (other_max + ((j - 1) >> 1)) & 1, bars);
+          if (!ok) break;
+          m_row = stats[(1 - t) * 128 + tile_row].x;
+          if (row_valid && m_tile - m_row > kRescaleThreshold) {
+            alpha = ex2(m_row - m_tile);
+            m_row = m_tile;
+            rescale = true;
+          }
+        }
+        if (m_row != m) l *= ex2(m - m_row);
+        m = m_row;
+        stats[t * 128 + tile_row].x = m;
+        mbar_arrive_warp(&bars->max_ready[t][quad]);
+      } else if (first) {
         first = false;
         m = m_tile;
       } else if (row_valid && m_tile - m > kRescaleThreshold) {  // false when both are -inf
@@ -973,12 +1000,20 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
         rescale = true;
       }
       if (__any_sync(0xffffffffu, rescale)) {
-        // The slot's last P V is complete: S was committed after it.
+        // The slot's last P V is complete: S was committed after it.  That of the other slot,
+        // in one O, is waited for.  (The one before it is complete: the other slot
+        // waited for it before it handed its maxima on.)
+        if constexpr (C::kBoth) {
+          ok = wait_warp(&bars->o_full[1 - t], (other_pv + ((k - x.begin - 1) >> 1)) & 1, bars);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t tAll = C::kBoth ? tmem + lane_addr + C::kColO0 : tO;
         const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
-        for (int c = 0; c < C::kCols; c += 32) {
+        for (int c = 0; c < D; c += 32) {
           uint32_t orow[32];
-          tmem_ld32(tO + c, orow);
+          tmem_ld32(tAll + c, orow);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float x0, x1;
@@ -987,7 +1022,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
             orow[e] = __float_as_uint(x0);
             orow[e + 1] = __float_as_uint(x1);
           }
-          tmem_st32(tO + c, orow);
+          tmem_st32(tAll + c, orow);
         }
       }
       // p = 2^(s * scale * log2 e - m), two columns per paired FMA/ADD.
@@ -1032,31 +1067,43 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
     }
     if (!ok) break;
 
-    const bool has_own = k != k_first;  // (one tile in all: slot 1 of a dual item has none)
     const int n = x.end - x.begin;
-    if (has_own) {
+    const bool has_own = C::kBoth ? n > 0 : k != k_first;  // (one tile in all: slot 1 has none)
+    if (!C::kBoth && has_own) {
       ok = wait_warp(&bars->o_full[t], o_phase, bars);
       if (!ok) break;
       o_phase ^= 1;
     }
+    const int own_n = (n + 1 - t) >> 1, other_n = (n + t) >> 1;  // tiles taken by turns
+    own_pv += own_n;
+    other_pv += other_n;
     if (!warp_valid) continue;
+    other_max += other_n;
     tc_fence_after();
     // Weights of the slot's O (and of the other's): O = (w O_t + w' O_t') / l.
     float w_own = 1.f, w_other = 0.f;
     bool has_other = false;
-    if (dual && n > 0) {
+    if (turns && n > 0) {
       stats[t * 128 + tile_row] = make_float2(m, l);
       mbar_arrive_warp(&bars->merge_ready[quad]);
       ok = wait_warp(&bars->merge_ready[quad], merge_phase, bars);
       if (!ok) break;
-      tc_fence_after();
       const float2 y = stats[(1 - t) * 128 + tile_row];
       const float both = fmaxf(m, y.x);
       w_own = m == -INFINITY ? 0.f : ex2(m - both);
       w_other = y.x == -INFINITY ? 0.f : ex2(y.x - both);
       l = l * w_own + y.y * w_other;
       m = both;
-      has_other = n > 1 - t;
+      if constexpr (C::kBoth) {
+        // O is relative to the last tile's reference, which is the highest.
+        const bool own_last = ((n - 1) & 1) == t;
+        ok = wait_warp(&bars->o_full[(n - 1) & 1], ((own_last ? own_pv : other_pv) - 1) & 1, bars);
+        if (!ok) break;
+        w_own = 1.f;
+        w_other = 0.f;
+      }
+      tc_fence_after();
+      has_other = !C::kBoth && n > 1 - t;
     }
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     w_own *= inv_l;
@@ -1092,7 +1139,14 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
       even = p.o + (pb ? other : at) * D + c_off + 16 * pb;
       odd = p.o + (pb ? at : other) * D + c_off + 16 * pb;
     };
-    if (!dual && to.part < 0 && n > 0) {
+    // The other slot has read O, or its part of it, before it is written again.
+    const auto release_o = [&] {
+      tc_fence_before();
+      mbar_arrive_warp(&bars->merge_done[quad]);
+      ok = wait_warp(&bars->merge_done[quad], merge_phase, bars);
+      merge_phase ^= 1;
+    };
+    if (!dual && to.part < 0 && n > 0) {  // (or of one, which the slots share out by columns)
       // A whole item of two tiles: 64 columns of O at a time, the next ones on their way.  (The
       // time of an item around its tiles is that of this.)
       uint32_t wa[64], wb[64];
@@ -1114,6 +1168,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
       }
       if (writes_lse && store_in_bounds(p.lse + at, 4, p.lse, p.lse_bytes, p.status))
         p.lse[at] = own_lse * kLn2;
+      if (C::kBoth) release_o();
       continue;
     }
     // Columns [c, c + N) of the row's result of this piece.
@@ -1173,13 +1228,7 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
       finish(std::integral_constant<int, 32>{}, t * (D / 2), (t + 1) * (D / 2));
     else
       finish(std::integral_constant<int, 64>{}, 0, C::kCols);
-    if (dual && n > 0) {
-      // The other slot has read this one's O before it is written again.
-      tc_fence_before();
-      mbar_arrive_warp(&bars->merge_done[quad]);
-      ok = wait_warp(&bars->merge_done[quad], merge_phase, bars);
-      merge_phase ^= 1;
-    }
+    if (turns && n > 0) release_o();
   }
   if (!ok) record_status(p.status, ATTN_ERR_TIMEOUT);
 }
@@ -1221,6 +1270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < 4; ++q) {
       mbar_init(&bars->merge_ready[q], 2);  // one per slot
       mbar_init(&bars->merge_done[q], 2);
+      mbar_init(&bars->max_ready[0][q], 1);
+      mbar_init(&bars->max_ready[1][q], 1);
     }
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;

@@ -628,14 +628,15 @@ def reference(q, ctxs, news, table, kc, vc, window, sinks, scale):
     return o, lse, size
 
 
-def check(got, ref, rows):
+def check(got, ref, rows, off=None):
     """P is rounded to bf16 (half a step, 2^-8 of each weight) and O once more; scores are
     sums of D products in 32 bits, off by up to D * 2^-23 of the terms' sum, about 0.64 sqrt(D):
     2^-13 at D = 128 and 2^-11.6 at D = 256, which moves the LSE by as much and the weights by
     twice that (they are divided by their sum)."""
     (o, lse), (ro, rl, size) = got, ref
     assert o.dtype == BF and lse.dtype == torch.float32
-    off = 2.0 ** -12 if o.shape[-1] <= 128 else 2.0 ** -11
+    if off is None:
+        off = 2.0 ** -12 if o.shape[-1] <= 128 else 2.0 ** -11
     o, lse, ro, rl, size = o[:rows].double(), lse[:rows].double(), ro[:rows], rl[:rows], size[:rows]
     err = (o - ro).abs() - 2.0 ** -8 * ro.abs() - (2.0 ** -8 + 2 * off) * size
     assert bool((err <= 0).all()), float(err.max())
@@ -784,6 +785,31 @@ def test_chunk_extreme_scores():
     assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse).all())
     assert float(((lse.double() - ref[1]) / ref[1].abs()).abs().max()) <= 2.0 ** -15
     status_ok()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("climb", [True, False])
+def test_chunk_moving_maximum(D, climb):
+    # Scores that climb with the keys, or jump, by more than 8 in base 2 from tile to tile, at
+    # other places in each row.  (Their terms add up to 155, the noise's to less than 25: off by
+    # D * 2^-23 of that.)
+    ctxs, news = [1000, 700, 2000], [60, 1, 13]
+    table, lens, kc, vc = pool(ctxs, news, 64, 2, D)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    u = torch.sign(torch.randn(D, generator=g, device="cuda"))
+    steps = torch.arange(64, device="cuda") * 5.0 if climb else \
+        torch.rand(64, generator=g, device="cuda") * 150
+    for b, (c, n) in enumerate(zip(ctxs, news)):
+        for slot in range(-(-(c + n) // 64)):
+            page = int(table[b, slot])
+            kc[page] = (kc[page].float() * 0.1 + steps[slot] / D * u).to(BF)
+    gain = torch.rand(sum(news), 8, 1, generator=g, device="cuda")
+    q = (gain * u + 0.1 * torch.randn(sum(news), 8, D, generator=g, device="cuda")).to(BF)
+    got = run_chunk(q, news, lens, table, kc, vc, scale=1.0)
+    status_ok()
+    check(got, reference(q, ctxs, news, table, kc, vc, 1 << 30, 0, 1.0), sum(news),
+          off=D * 2.0 ** -23 * 180)
 
 
 @pytest.mark.gpu
