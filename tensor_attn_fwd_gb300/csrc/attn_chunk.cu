@@ -241,12 +241,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
   const long long want = (all + kMinShare - 1) / kMinShare;
   const int n = want < p.ctas ? static_cast<int>(max(want, 1ll)) : p.ctas;
 
-  // Many items: whole ones, longest first, dealt out forth and back over the CTAs.  (Equal items
-  // in any order: it changes no result.)
+  // Many items: whole ones, longest first, dealt out forth and back over the CTAs.  (Items of
+  // equal cost in any order, which changes no CTA's load and no result.  The costs past the
+  // last level are not told apart: with one of them nothing is dealt.)
   bool dealt = false;
   if (items >= 2 * p.ctas && n == p.ctas) {
     __syncthreads();
     static_assert(kCostLevels == 2 * kPlanThreads, "two levels a thread");
+    const bool exact = counts[kCostLevels - 1] == 0;
     const int high = kCostLevels - 1 - 2 * tid;
     const long long here = counts[high] + counts[high - 1];
     long long total;
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     for (int off = 16; off > 0; off >>= 1)
       most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
     __syncthreads();
-    dealt = most <= all / n + kCutCost;
+    dealt = exact && most <= all / n + kCutCost;
     if (dealt)
       for (int c = tid; c < n; c += kPlanThreads) begins[c] = begin_of(c);
   }

@@ -889,6 +889,27 @@ def test_chunk_same_bits_each_time():
 
 
 @pytest.mark.gpu
+def test_chunk_same_bits_of_long_items():
+    # Twice as many items as CTAs, of more than 2^10 K/V tiles, a few of them four tiles longer:
+    # whether two of those meet in a CTA may not decide how the work is cut.
+    B, ps = 2 * torch.cuda.get_device_properties(0).multi_processor_count, 128
+    M = 1100
+    kc, vc = (torch.randn(M, 1, ps, 64, device="cuda", dtype=BF) for _ in range(2))
+    table = gpu(np.tile(np.arange(M), (B, 1)))  # one cache for all
+    lens = np.full(B, 1040 * ps)
+    lens[np.random.default_rng(0).permutation(B)[:18]] += 4 * ps
+    q = torch.randn(B, 1, 64, device="cuda", dtype=BF)
+    cu, lens = gpu(np.arange(B + 1), lens)
+    first = None
+    for _ in range(12):
+        plan = attn.attn_chunk_plan(cu, lens, B, 1, 1, 64, M * ps)
+        got = attn.attn_chunk_paged(q, kc, vc, table, plan)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    status_ok()
+
+
+@pytest.mark.gpu
 def test_chunk_two_streams_and_shared_plan():
     # One plan, two layers at once on streams of their own.
     ctxs, news = [3000, 700], [50, 1]
@@ -937,7 +958,7 @@ def test_chunk_offsets_past_32_bits():
 # ================================================================== together
 @pytest.mark.gpu
 @pytest.mark.parametrize("window,sinks", [(None, 0), (150, 4)])
-@pytest.mark.parametrize("D,R,style", [(64, 32, 0), (128, 128, 1)])
+@pytest.mark.parametrize("D,R,style", [(64, 32, 0), (128, 128, 1), (256, 64, 1)])
 def test_serving_steps(window, sinks, D, R, style):
     """Prompts in chunks and generated tokens side by side, two layers, over pages that the
     window gives up: each step's attention against the whole history in 64 bits."""
