@@ -878,6 +878,23 @@ def test_chunk_refuses_a_plan_of_other_sizes():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunk_output_off_32_bytes(D):
+    # Whole and cut items, to an output that is aligned to 16 bytes alone.
+    ctxs, news = [9000, 12, 900, 40], [60, 100, 1, 1]
+    table, lens, kc, vc = pool(ctxs, news, 64, 2, D)
+    q = torch.randn(sum(news), 6, D, device="cuda", dtype=BF)
+    want = run_chunk(q, news, lens, table, kc, vc)
+    buf = torch.full((q.numel() + 16,), 7.0, dtype=BF, device="cuda")
+    assert buf.data_ptr() % 32 == 0
+    o = buf[8:8 + q.numel()].view_as(q)
+    got = run_chunk(q, news, lens, table, kc, vc, o=o)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((buf[:8] == 7).all()) and bool((buf[-8:] == 7).all())
+    status_ok()
+
+
+@pytest.mark.gpu
 def test_chunk_same_bits_each_time():
     ctxs, news = [5000, 12, 900], [60, 100, 1]
     table, lens, kc, vc = pool(ctxs, news, 64, 2, 128)
