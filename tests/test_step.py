@@ -1039,6 +1039,45 @@ def test_serving_steps(window, sinks, D, R, style):
 
 
 @pytest.mark.gpu
+def test_steps_of_forked_rows():
+    """Three samples of one prompt: forked with its pages shared, then tokens of their own, with
+    and without pages that the fork reserved."""
+    Hq, Hkv, D, ps, M, P, n = 4, 2, 64, 32, 8, 40, 70
+    rope = attn.attn_rope_table(M * ps, D)
+    kc, vc = (torch.full((P, Hkv, ps, D), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def step(table, refs, lens, news):
+        T = sum(news)
+        qkv = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g, device="cuda", dtype=BF)
+        length = lens.tolist()
+        table, refs, lens, cu, pos, slots, _ = attn.attn_pages_append(
+            table, refs, lens, gpu(np.array(news)), T, ps)
+        plan = attn.attn_chunk_plan(cu, lens, T, Hq, Hkv, D, M * ps)
+        q = attn.attn_rope_append(qkv, rope, pos, slots, kc, vc, Hq)
+        got = attn.attn_chunk_paged(q, kc, vc, table, plan)
+        status_ok()
+        tab = table.cpu().numpy().astype(np.int64)
+        check(got, reference(q, length, news, tab, kc, vc, 1 << 30, 0, 0.125), T)
+        return table, refs, lens
+
+    table, refs, lens = step(*gpu(np.full((1, M), -1), np.zeros(P), np.zeros(1)), [n])
+    kept = kc[table[0, :2].long()].clone()
+    for room in (0, 40):
+        t, r, ln, src, dst, _ = attn.attn_pages_fork(table, refs, lens, gpu(np.zeros(3)), ps, room=room)
+        attn.attn_pages_copy(kc, vc, src, dst)
+        for news in ([1, 1, 1], [5, 0, 60], [1, 90, 1]):
+            t, r, ln = step(t, r, ln, news)
+        tab = t.cpu().numpy()
+        assert (tab[:, :2] == tab[0, 0:2]).all()  # full pages of the prompt: shared
+        own = tab[:, 2:][tab[:, 2:] >= 0]
+        assert len(set(own.tolist())) == own.size
+        np.testing.assert_array_equal(
+            r.cpu().numpy(), np.bincount(tab[tab >= 0], minlength=P))
+    assert torch.equal(kc[table[0, :2].long()], kept)
+
+
+@pytest.mark.gpu
 def test_step_in_a_graph():
     """A whole step captured once and replayed with other lengths."""
     Hq, Hkv, D, ps, B, M, P, T = 8, 2, 64, 32, 3, 20, 64, 40
