@@ -658,7 +658,9 @@ struct CompactOp {
 //   2 list the free pages that are needed; decide which rows take their tokens
 //   3 hand the pages out  4 positions and slots of the tokens
 // and further CTAs copy refs and the table meanwhile, but for the pages and entries that are
-// the workers'.
+// the workers'.  Nothing orders their stores before the workers' loads, so the workers take
+// entries that named a page before the call from `table`, and from `table_out` only those that
+// they wrote.
 // Token sums are clamped to T + 1 (a sum that saturates stays associative).
 //
 // Latency, again: each phase is a few dependent trips to L2.  1024 rows of 1024 slots, 560,000
@@ -1092,7 +1094,10 @@ struct AppendOp {
       if (t < t1 && from >= 0) {
         pos = from + t - t0;
         const int s = by_page.div(pos);
-        slot = table_out[static_cast<size_t>(lo) * M + s] * page_size + pos - s * page_size;
+        const size_t at = static_cast<size_t>(lo) * M + s;
+        int page = checked_entry(table[at], P, nullptr);
+        if (page < 0) page = table_out[at];  // a worker's (in place: already read)
+        slot = page * page_size + pos - s * page_size;
       }
       positions[t] = pos;
       slots[t] = slot;

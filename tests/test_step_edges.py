@@ -1,0 +1,59 @@
+"""A serving step at the edges of what the documentation allows: large tables that are copied
+beside the call's own work, rows that are refused, large scores, the bounds-checked build."""
+import numpy as np
+import pytest
+import torch
+
+import tensor_attn_fwd_gb300 as attn
+
+from test_step import INV, append_case, gpu, plain_append, same, status_ok
+
+
+# ------------------------------------------------------------------ large tables
+def busy(stream):
+    """A few milliseconds of matrix products on another stream."""
+    a = torch.ones(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(20):
+            torch.mm(a, a)
+    a.record_stream(stream)
+
+
+# Rows, slots, pages, page size, new tokens: tables and counts that CTAs of their own copy while
+# the others hand out pages (131072 entries or pages and more).
+LARGE = [(1024, 1024, 40000, 32, 40), (300, 700, 30000, 64, 200), (131, 1001, 150001, 32, 9),
+         (2000, 130, 200000, 96, 3)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,M,P,ps,most", LARGE)
+@pytest.mark.parametrize("reserved", [0.0, 0.01])
+def test_append_of_large_tables(B, M, P, ps, most, reserved):
+    # Slots of tokens in pages that rows had before (partly filled, or reserved) do not depend
+    # on when the copies are made: the results' memory holds other pages that look right.
+    rng = np.random.default_rng(B + M)
+    table, refs, lens, new = append_case(rng, B, M, P, ps, most, reserved)
+    T = int(new.sum()) + 5
+    want = plain_append(table, refs, lens, new, T, ps)
+    assert want[6][0] <= want[6][1]
+    inputs = gpu(table, refs, lens, new)
+    wrong = gpu((np.arange(B * M) * 7 % P).reshape(B, M), np.full(P, 5), np.full(B, 11))
+    other = torch.cuda.Stream()
+    for i in range(12):
+        out = [x.clone() for x in wrong]
+        if i % 3 == 1:
+            busy(other)
+        same(attn.attn_pages_append(*inputs, T, ps, block_table_out=out[0], refs_out=out[1],
+                                    seqlens_out=out[2]), want)
+        # Table and counts in place, lengths not.
+        here, out = [x.clone() for x in inputs], wrong[2].clone()
+        if i % 3 == 2:
+            busy(other)
+        same(attn.attn_pages_append(*here, T, ps, block_table_out=here[0], refs_out=here[1],
+                                    seqlens_out=out), want)
+        assert torch.equal(here[2], inputs[2])
+    # Everything in place.
+    same(attn.attn_pages_append(*inputs, T, ps, block_table_out=inputs[0], refs_out=inputs[1],
+                                seqlens_out=inputs[2]), want)
+    status_ok()
