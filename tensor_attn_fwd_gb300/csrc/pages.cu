@@ -862,8 +862,8 @@ struct AppendOp {
     }
   }
   static constexpr int kRowsAtOnce = kThreads / 8;
-  __device__ __forceinline__ bool lacks(int r, int s) const {
-    return checked_entry(table[static_cast<size_t>(r) * M + s], P, nullptr) < 0;
+  __device__ __forceinline__ bool lacks(int r, int s, int* report) const {
+    return checked_entry(table[static_cast<size_t>(r) * M + s], P, report) < 0;
   }
 
   // Worker w of the pages and rows.
@@ -909,7 +909,9 @@ struct AppendOp {
         __syncthreads();
         for (int i0 = 0; i0 < min(kThreads, r_end - r0); i0 += kRowsAtOnce)
           each_slot(sh, i0 + (threadIdx.x >> 3), [&](int i, int s, unsigned lanes) {
-            const unsigned votes = __ballot_sync(lanes, s >= 0 && lacks(r0 + i, s));
+            // (Bad entries are reported here: in place, a page may be in one's stead by the time
+            // that a CTA that copies looks.)
+            const unsigned votes = __ballot_sync(lanes, s >= 0 && lacks(r0 + i, s, status));
             if (lane == __ffs(lanes) - 1) {
               sh.lacking[i] += __popc(votes);
               sh.mask[i] = votes >> (__ffs(lanes) - 1);  // (of one turn; see `word`)
@@ -1043,7 +1045,7 @@ struct AppendOp {
           // One turn's slots are known from phase 1.
           const bool word = one && sh.hi[i] - sh.lo[i] <= __popc(lanes);
           const bool lacking =
-              word ? sh.mask[i] >> (lane - leader) & 1u : s >= 0 && lacks(r0 + i, s);
+              word ? sh.mask[i] >> (lane - leader) & 1u : s >= 0 && lacks(r0 + i, s, nullptr);
           const unsigned votes = __ballot_sync(lanes, lacking);
           const int k = sh.lacking[i];
           __syncwarp(lanes);

@@ -57,3 +57,26 @@ def test_append_of_large_tables(B, M, P, ps, most, reserved):
     same(attn.attn_pages_append(*inputs, T, ps, block_table_out=inputs[0], refs_out=inputs[1],
                                 seqlens_out=inputs[2]), want)
     status_ok()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,M,P,ps,most", LARGE)
+@pytest.mark.parametrize("bad", [-2, "P"])
+def test_append_reports_a_bad_entry_that_it_replaces(B, M, P, ps, most, bad):
+    # An entry that is no page, where a row's new tokens come: read as -1, and reported also where
+    # the page that takes its place is written to the same memory.
+    rng = np.random.default_rng(B)
+    table, refs, lens, new = append_case(rng, B, M, P, ps, most)
+    rows = [b for b in range(B) if new[b] > 0 and table[b, (lens[b] + new[b] - 1) // ps] < 0]
+    b = rows[len(rows) // 2]
+    table[b, (lens[b] + new[b] - 1) // ps] = P if bad == "P" else bad
+    T = int(new.sum())
+    want = plain_append(table, refs, lens, new, T, ps)
+    inputs = gpu(table, refs, lens, new)
+    for _ in range(8):
+        here, out = [x.clone() for x in inputs], torch.zeros_like(inputs[2])
+        same(attn.attn_pages_append(*here, T, ps, block_table_out=here[0], refs_out=here[1],
+                                    seqlens_out=out), want)
+        assert attn.attn_debug_status() == INV
+    same(attn.attn_pages_append(*inputs, T, ps), want)
+    assert attn.attn_debug_status() == INV
