@@ -574,14 +574,15 @@ ATTN_API int attn_pages_copy(void *k_cache, void *v_cache, const int *src, const
  * attn_pages_fork) has seqlens[b] keys and gets new_lens[b] more.  Its slots of the table
  * that hold new keys and name no page get free pages (refs = 0), lowest id first in the
  * order of (row, slot), which count one holder then; entries that are there (reserved by
- * attn_pages_fork) are kept as they are: rows that share a page to be written have to be
- * forked first.
+ * attn_pages_fork) are kept as they are.  A page that new keys go to has to be the row's
+ * alone: rows that share one are forked first.
  *   A row takes all its tokens or none.  Rows take none when the pages needed up to and
  *   with theirs exceed the free ones (ATTN_ERR_NO_PAGES in the status word), when their
- *   keys would exceed max_pages * page_size or their tokens T (ATTN_ERR_INVALID_ARG in the
- *   status word), and finished rows (seqlens < 0).  They keep their length and entries, and
- *   their tokens have slot -1.  A negative new_lens sets ATTN_ERR_INVALID_ARG in the status
- *   word and counts as 0.
+ *   tokens would exceed T, when their keys would exceed max_pages * page_size or go to a page
+ *   with refs > 1 (these three: ATTN_ERR_INVALID_ARG in the status word), and finished rows
+ *   (seqlens < 0).  They keep their length and entries, and their tokens have slot -1; those
+ *   over max_pages * page_size, of shared pages and finished need no pages.  A negative
+ *   new_lens sets ATTN_ERR_INVALID_ARG in the status word and counts as 0.
  *
  *   new_lens [B]; T: tokens of the step, at least the sum of new_lens
  *   block_table_out [B,max_pages], refs_out [num_pages], seqlens_out [B] (the lengths

@@ -900,9 +900,10 @@ def attn_pages_append(block_table: torch.Tensor, refs: torch.Tensor, seqlens: to
     have no page get free pages, lowest id first.  ``tokens`` is the length of the packed
     token arrays, at least the sum of new_lens (the rest: position 0, slot -1).  A row
     takes all its tokens or none: without enough free pages (attn_debug_status then
-    reports ATTN_ERR_NO_PAGES; counts holds the pages needed and free) or finished
-    (negative seqlens) it keeps its length, and its tokens have slot -1.  A token's slot is
-    page * page_size + its place in the page.  The ``..._out`` tensors may be the
+    reports ATTN_ERR_NO_PAGES; counts holds the pages needed and free), where it would write
+    past its slots or into a page of several holders (ATTN_ERR_INVALID_ARG: fork it first), or
+    finished (negative seqlens) it keeps its length, and its tokens have slot -1.  A token's
+    slot is page * page_size + its place in the page.  The ``..._out`` tensors may be the
     inputs; the other results share one allocation.
     """
     call = (_fast or _native()).pages_append

@@ -654,7 +654,8 @@ struct CompactOp {
 // ------------------------------------------------------------------ append
 // Pages, positions and slots for a step's new tokens.  The workers, a cluster of CTAs, take
 // equal parts of the pages and of the rows:
-//   1 count the free pages; count the pages that each row lacks, its tokens
+//   1 count the free pages; count the pages that each row lacks, its tokens; look for rows that
+//     would write into a page of several holders
 //   2 list the free pages that are needed; decide which rows take their tokens
 //   3 hand the pages out  4 positions and slots of the tokens
 // and further CTAs copy refs and the table meanwhile, but for the pages and entries that are
@@ -834,6 +835,7 @@ struct AppendOp {
     // or -1), and which, as far as a word says it.
     int lo[kThreads], hi[kThreads], lacking[kThreads];
     unsigned mask[kThreads];
+    uint8_t shares[kThreads];  // would write into a page of several holders
     int starts[kThreads];
     uint8_t free_bits[kWarps][kKept * 32];  // four pages each
   };
@@ -842,6 +844,7 @@ struct AppendOp {
   struct Mine {
     Row x;
     int lacking, k, t;
+    bool shares;
   };
   // The slots of the row at place i of `lo` and `hi`, eight lanes to a row, or all to a row
   // of more slots: f(place, slot, lanes) with `lanes` the mask of those that share the row, in
@@ -862,8 +865,8 @@ struct AppendOp {
     }
   }
   static constexpr int kRowsAtOnce = kThreads / 8;
-  __device__ __forceinline__ bool lacks(int r, int s, int* report) const {
-    return checked_entry(table[static_cast<size_t>(r) * M + s], P, report) < 0;
+  __device__ __forceinline__ int entry(int r, int s, int* report) const {
+    return checked_entry(table[static_cast<size_t>(r) * M + s], P, report);
   }
 
   // Worker w of the pages and rows.
@@ -906,12 +909,15 @@ struct AppendOp {
         sh.lo[threadIdx.x] = x.lo;
         sh.hi[threadIdx.x] = x.hi;
         sh.lacking[threadIdx.x] = 0;
+        sh.shares[threadIdx.x] = 0;
         __syncthreads();
         for (int i0 = 0; i0 < min(kThreads, r_end - r0); i0 += kRowsAtOnce)
           each_slot(sh, i0 + (threadIdx.x >> 3), [&](int i, int s, unsigned lanes) {
             // (Bad entries are reported here: in place, a page may be in one's stead by the time
             // that a CTA that copies looks.)
-            const unsigned votes = __ballot_sync(lanes, s >= 0 && lacks(r0 + i, s, status));
+            const int page = s >= 0 ? entry(r0 + i, s, status) : 0;
+            const unsigned votes = __ballot_sync(lanes, page < 0);
+            if (s >= 0 && page >= 0 && refs[page] > 1) sh.shares[i] = 1;
             if (lane == __ffs(lanes) - 1) {
               sh.lacking[i] += __popc(votes);
               sh.mask[i] = votes >> (__ffs(lanes) - 1);  // (of one turn; see `word`)
@@ -919,7 +925,8 @@ struct AppendOp {
           });
         __syncthreads();
         int total, tok_total;
-        const int lacking = sh.lacking[threadIdx.x];
+        const bool shares = sh.shares[threadIdx.x] != 0;
+        const int lacking = shares ? 0 : sh.lacking[threadIdx.x];
         const int k = at + block_scan(lacking, sh.sums, total);
         const int t = add_tokens(tok, token_scan(tokens(x.n), sh.sums, tok_total));
         if (one) {
@@ -927,9 +934,11 @@ struct AppendOp {
           my.lacking = lacking;
           my.k = k;
           my.t = t;
+          my.shares = shares;
         } else if (r < r_end) {
           need[r] = k;
           first[r] = t;
+          len[r] = shares ? -1 : 0;  // (for the next phase)
         }
         at += total;
         tok = add_tokens(tok, tok_total);
@@ -1002,8 +1011,9 @@ struct AppendOp {
                                                          : cta_need[w]);
         const int t = add_tokens(first_token, one ? my.t : first[r]);
         const int end = add_tokens(t, tokens(x.n));
-        bool takes = x.lo < x.hi;
-        if (end > T) {
+        const bool shares = one ? my.shares : len[r] < 0;
+        bool takes = x.lo < x.hi && !shares;
+        if (end > T || shares) {
           record_status(status, ATTN_ERR_INVALID_ARG);
           takes = false;
         }
@@ -1045,7 +1055,7 @@ struct AppendOp {
           // One turn's slots are known from phase 1.
           const bool word = one && sh.hi[i] - sh.lo[i] <= __popc(lanes);
           const bool lacking =
-              word ? sh.mask[i] >> (lane - leader) & 1u : s >= 0 && lacks(r0 + i, s, nullptr);
+              word ? sh.mask[i] >> (lane - leader) & 1u : s >= 0 && entry(r0 + i, s, nullptr) < 0;
           const unsigned votes = __ballot_sync(lanes, lacking);
           const int k = sh.lacking[i];
           __syncwarp(lanes);
@@ -1128,7 +1138,13 @@ struct AppendOp {
     const int p0 = min(t * per, P), p1 = min(p0 + per, P);
     int n_free = 0, lacking = 0;
     for (int p = p0; p < p1; ++p) n_free += held[pad(p)] == 0;
-    for (int s = x.lo; s < x.hi; ++s) lacking += page_of[t * M + s] < 0;
+    bool shares = false;
+    for (int s = x.lo; s < x.hi; ++s) {
+      const int page = page_of[t * M + s];
+      lacking += page < 0;
+      shares |= page >= 0 && held[pad(page)] > 1;
+    }
+    if (shares) lacking = 0;
     // (Fields of 30, 17 and 17 bits: rows <= 2^10, tokens clamped to T + 1 < 2^13, entries and
     // pages <= 2^13.)
     const unsigned long long mine = static_cast<unsigned long long>(tokens(x.n)) |
@@ -1164,8 +1180,9 @@ struct AppendOp {
     const int free_all = field(all, 47), need_all = field(all, 30);
     int k = field(before, 30);
     const int t0 = token_field(before), t1 = token_field(before + mine);
-    if (t < B && t1 > T) record_status(status, ATTN_ERR_INVALID_ARG);
-    const bool takes = t < B && x.lo < x.hi && t1 <= T && k + lacking <= free_all;
+    if (t < B && (t1 > T || shares)) record_status(status, ATTN_ERR_INVALID_ARG);
+    const bool takes =
+        t < B && x.lo < x.hi && !shares && t1 <= T && k + lacking <= free_all;
     if (t < B) {
       begin[t] = min(t0, T);
       taken[t] = takes ? x.len : -1;

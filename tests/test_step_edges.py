@@ -6,7 +6,7 @@ import torch
 
 import tensor_attn_fwd_gb300 as attn
 
-from test_step import INV, append_case, gpu, plain_append, same, status_ok
+from test_step import APPEND, INV, append_case, gpu, plain_append, same, status_ok
 
 
 # ------------------------------------------------------------------ large tables
@@ -80,3 +80,52 @@ def test_append_reports_a_bad_entry_that_it_replaces(B, M, P, ps, most, bad):
         assert attn.attn_debug_status() == INV
     same(attn.attn_pages_append(*inputs, T, ps), want)
     assert attn.attn_debug_status() == INV
+
+
+# ------------------------------------------------------------------ shared pages
+def append_of_sharing_rows(table, refs, lens, new, T, ps):
+    """plain_append, where rows whose new keys would go to a page of several holders take none
+    of their tokens and need no pages, as finished rows; and which rows those are."""
+    B, M = table.shape
+    shares = np.zeros(B, dtype=bool)
+    for b in range(B):
+        x, n = int(lens[b]), int(new[b])
+        if n > 0 and x >= 0 and x + n <= M * ps:
+            e = table[b, x // ps:(x + n - 1) // ps + 1]
+            shares[b] = bool((refs[e[e >= 0]] > 1).any())
+    out = list(plain_append(table, refs, np.where(shares, -1, lens), new, T, ps))
+    out[2] = np.where(shares, lens, out[2])
+    return out, shares
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,M,P,ps,most", APPEND[2:] + LARGE[:2])
+@pytest.mark.parametrize("reserved", [0.0, 0.3])
+def test_append_refuses_rows_that_share_a_page_to_be_written(B, M, P, ps, most, reserved):
+    rng = np.random.default_rng(B + 3)
+    table, refs, lens, new = append_case(rng, B, M, P, ps, most, reserved)
+    # Second holders of some pages: of those that are written, and of full ones.
+    held = np.nonzero(refs == 1)[0]
+    refs[held[rng.random(held.size) < 0.5 / (most // ps + 2)]] = 2
+    b = int(np.argmax((new > 0) & (lens % ps != 0)))
+    refs[table[b, lens[b] // ps]] = 3
+    T = int(new.sum())
+    want, shares = append_of_sharing_rows(table, refs, lens, new, T, ps)
+    assert shares[b] and (new[~shares] > 0).any()
+    inputs = gpu(table, refs, lens, new)
+    same(attn.attn_pages_append(*inputs, T, ps), want)
+    assert attn.attn_debug_status() == INV
+    same(attn.attn_pages_append(*inputs, T, ps, block_table_out=inputs[0], refs_out=inputs[1],
+                                seqlens_out=inputs[2]), want)
+    assert attn.attn_debug_status() == INV
+
+
+@pytest.mark.gpu
+def test_append_of_rows_that_share_full_pages():
+    # Samples of one prompt: full pages of several holders are no obstacle.
+    table = np.array([[0, 1, 2, -1], [0, 1, 3, -1], [0, 1, -1, -1]])
+    refs, lens, new = np.array([3, 3, 1, 1, 0, 0, 0]), np.array([70, 71, 64]), np.array([1, 40, 32])
+    want = plain_append(table, refs, lens, new, 73, 32)
+    assert (want[2] == lens + new).all()
+    same(attn.attn_pages_append(*gpu(table, refs, lens, new), 73, 32), want)
+    status_ok()
