@@ -560,7 +560,8 @@ ATTN_API int attn_pages_copy(void *k_cache, void *v_cache, const int *src, const
  * chunk of a prompt, or one generated token), packed request after request.  The calls
  * of a step, in order, none of which reads anything back to the host:
  *   attn_pages_append   pages for the new tokens; each token's position and cache slot
- *   attn_chunk_plan     how the GPU shares out the attention (one plan for all layers)
+ *   attn_chunk_plan_slots  how the GPU shares out the attention (one plan for all layers;
+ *                       attn_chunk_plan where every request has taken its tokens)
  *   per layer: a projection of the caller's, then
  *     attn_rope_append  rotary positions on its queries and keys; keys and values to
  *                       their slots
@@ -689,6 +690,18 @@ ATTN_API int attn_chunk_plan(const int *cu_tokens, const int *seqlens, int *plan
                              int Hq, int Hkv, int D, int max_keys, int window, int sinks,
                              void *stream);
 
+/*
+ * The same, for steps in which some request may not have taken its tokens.  attn_pages_append
+ * leaves those in cu_tokens, and seqlens[b] without them, so that attn_chunk_plan places
+ * them at the request's last keys: their results mean nothing, and under a window they may
+ * reach table entries that attn_pages_free has emptied (ATTN_ERR_INVALID_ARG).
+ *   slots [T] device int32 (attn_pages_append): the tokens of a request whose first one has a
+ *     negative slot see no key and get O = 0 and LSE = -inf.  NULL: ATTN_ERR_INVALID_ARG.
+ */
+ATTN_API int attn_chunk_plan_slots(const int *cu_tokens, const int *seqlens, const int *slots,
+                                   int *plan, int B, int T, int Hq, int Hkv, int D, int max_keys,
+                                   int window, int sinks, void *stream);
+
 /* int32 entries of a plan on the current device.  Host-only.  Errors as attn_chunk_plan. */
 ATTN_API int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long long *entries);
 
@@ -697,7 +710,8 @@ ATTN_API int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long lon
  *   q [T,Hq,D] bf16 (attn_rope_append); k_cache, v_cache, block_table as
  *     attn_decode_splitkv_paged.  The new tokens' keys and values have to be in the cache.
  *   o [T,Hq,D] bf16 (rounded once from fp32), lse [T,Hq] fp32.  A token that sees no key (p <
- *     0: more new tokens than keys) gets O = 0 and LSE = -inf.  Tokens behind the last
+ *     0: more new tokens than keys, or a finished row; or one not taken, by a plan of
+ *     attn_chunk_plan_slots) gets O = 0 and LSE = -inf.  Tokens behind the last
  *     request's are left as they were.
  *   workspace: attn_chunk_workspace floats, caller-owned, contents undefined
  *   Table entries of pages that hold no seen key are not read and may be anything.  Keys

@@ -34,7 +34,8 @@ Names follow the C ABI:
     attn_rope_split(qkv, table, Hq, Hkv)        -> (q, k, v) bf16, RoPE applied
     attn_rope_split_bwd(dq, dk, dv, table)      -> dqkv bf16
     attn_rope_append(qkv, table, positions, slots, k_cache, v_cache, Hq) -> q bf16
-    attn_chunk_plan(cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks) -> plan
+    attn_chunk_plan(cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, slots=slots)
+                            -> plan
     attn_chunk_paged(q, k_cache, v_cache, block_table, plan) -> (o bf16, lse)
 Layouts: Q [B,Hq,Sq,D], K/V [B,Hkv,Sk,D] bf16; O [B,Hq,Sq,D], LSE [B,Hq,Sq] fp32.
 """
@@ -119,6 +120,7 @@ _SIGNATURES = {
                             _int),
     "attn_rope_append": ([_vp, ctypes.c_longlong] + [_vp] * 6 + [_int] * 9 + [_vp], _int),
     "attn_chunk_plan": ([_vp] * 3 + [_int] * 8 + [_vp], _int),
+    "attn_chunk_plan_slots": ([_vp] * 4 + [_int] * 8 + [_vp], _int),
     "attn_chunk_plan_size": ([_int] * 5 + [ctypes.POINTER(ctypes.c_longlong)], _int),
     "attn_chunk_paged": ([_vp] * 8 + [_int] * 8 + [_flt, _vp], _int),
     "attn_chunk_workspace": ([_int, ctypes.POINTER(ctypes.c_longlong)], _int),
@@ -987,7 +989,8 @@ def attn_rope_append(qkv: torch.Tensor, rope_table: torch.Tensor, positions: tor
 
 def attn_chunk_plan(cu_tokens: torch.Tensor, seqlens: torch.Tensor, tokens: int, Hq: int, Hkv: int,
                     D: int, max_keys: int, window: int | None = None, sinks: int = 0,
-                    plan: torch.Tensor | None = None, stream=None):
+                    plan: torch.Tensor | None = None, stream=None, *,
+                    slots: torch.Tensor | None = None):
     """Plan of a step's attention for attn_chunk_paged, one for all its layers; an int32
     tensor of the library's own form.
 
@@ -995,12 +998,15 @@ def attn_chunk_plan(cu_tokens: torch.Tensor, seqlens: torch.Tensor, tokens: int,
     its last keys of seqlens[b] (attn_pages_append's results).  Each sees the keys up to its own,
     of them the last ``window`` and the first ``sinks`` (``window=None``: all).  ``max_keys``
     is max_pages * page_size of the block table.  D is 64, 128 or 256.
+    ``slots`` (int32 [tokens], attn_pages_append's) tells the requests that took their tokens:
+    those of the others (slot -1) see no key, and get O = 0 and LSE = -inf.  Without it such
+    tokens are placed at older ones' positions, and their results mean nothing.
     """
     call = (_fast or _native()).chunk_plan
     if stream is not None:
         return _on_stream(stream, call, cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window,
-                          sinks, plan)
-    return call(cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, plan)
+                          sinks, plan, slots)
+    return call(cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, plan, slots)
 
 
 def attn_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

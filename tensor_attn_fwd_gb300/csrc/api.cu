@@ -1051,21 +1051,43 @@ int attn_chunk_workspace(int D, long long* floats) {
   return ATTN_OK;
 }
 
-int attn_chunk_plan(const int* cu_tokens, const int* seqlens, int* plan, int B, int T, int Hq,
-                    int Hkv, int D, int max_keys, int window, int sinks, void* stream) {
+namespace {
+
+// slots: of the tokens, or nullptr.
+int chunk_plan_common(const int* cu_tokens, const int* seqlens, const int* slots, int* plan, int B,
+                      int T, int Hq, int Hkv, int D, int max_keys, int window, int sinks,
+                      void* stream) {
   if (!cu_tokens || !seqlens || !plan || max_keys <= 0 || window < 1 || sinks < 0)
     return ATTN_ERR_INVALID_ARG;
   const int chk = chunk_check_sizes(B, T, Hq, Hkv, D);
   if (chk != ATTN_OK) return chk;
   if (max_keys > kMaxSeq) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned4(cu_tokens) || !aligned4(seqlens) || !aligned16(plan)) return ATTN_ERR_MISALIGNED;
+  if (!aligned4(cu_tokens) || !aligned4(seqlens) || !aligned4(slots) || !aligned16(plan))
+    return ATTN_ERR_MISALIGNED;
   int* status = status_word_device_ptr();
   if (status == nullptr) return ATTN_ERR_CUDA;
   // A window or sinks past the last key mean all keys; clamped, the kernels' sums fit int.
   const cudaError_t e = launch_chunk_plan(
-      cu_tokens, seqlens, plan, B, T, Hq, Hkv, D, max_keys, window < max_keys ? window : max_keys,
-      sinks < max_keys ? sinks : max_keys, static_cast<cudaStream_t>(stream), status);
+      cu_tokens, seqlens, slots, plan, B, T, Hq, Hkv, D, max_keys,
+      window < max_keys ? window : max_keys, sinks < max_keys ? sinks : max_keys,
+      static_cast<cudaStream_t>(stream), status);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int attn_chunk_plan(const int* cu_tokens, const int* seqlens, int* plan, int B, int T, int Hq,
+                    int Hkv, int D, int max_keys, int window, int sinks, void* stream) {
+  return chunk_plan_common(cu_tokens, seqlens, nullptr, plan, B, T, Hq, Hkv, D, max_keys, window,
+                           sinks, stream);
+}
+
+int attn_chunk_plan_slots(const int* cu_tokens, const int* seqlens, const int* slots, int* plan,
+                          int B, int T, int Hq, int Hkv, int D, int max_keys, int window, int sinks,
+                          void* stream) {
+  if (!slots) return ATTN_ERR_INVALID_ARG;
+  return chunk_plan_common(cu_tokens, seqlens, slots, plan, B, T, Hq, Hkv, D, max_keys, window,
+                           sinks, stream);
 }
 
 int attn_chunk_paged(const void* q, const void* k_cache, const void* v_cache,

@@ -149,6 +149,7 @@ __device__ __forceinline__ X scan(X x, X* smem, X& total) {
 
 struct PlanParams {
   const int *cu, *seqlens;
+  const int* slots;  // of the tokens, or null: every request has taken its own
   int* plan;
   int B, T, Hq, Hkv, D, max_keys, window, sinks, ctas;
   int heads, tile_tokens, item_tokens;  // KV heads x slices; tokens of a query tile, of an item
@@ -207,7 +208,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const PlanP
     const int first = tiles[lo], n = tiles[lo + 1] - first;
     const int rest = i - first * p.heads;
     const int t0 = p.cu[lo], n_tok = p.cu[lo + 1] - t0;
-    const int len = min(max(p.seqlens[lo], 0), p.max_keys);
+    // (A request that has not taken its tokens has keys, but none that they see.)
+    const bool taken = p.slots == nullptr || p.slots[t0] >= 0;
+    const int len = taken ? min(max(p.seqlens[lo], 0), p.max_keys) : 0;
     x.row = lo;
     x.head = rest / n;
     const int from = (rest - x.head * n) * p.item_tokens;
@@ -1414,11 +1417,11 @@ cudaError_t launch_impl(const void* q, const void* k, const void* v, const Chunk
 
 int chunk_ctas() { return sm_count() < kChunkMaxCtas ? sm_count() : kChunkMaxCtas; }
 
-cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
-                              int Hkv, int D, int max_keys, int window, int sinks,
+cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, const int* slots, int* plan, int B,
+                              int T, int Hq, int Hkv, int D, int max_keys, int window, int sinks,
                               cudaStream_t stream, int* status) {
   const ChunkTiling tiling(Hq, Hkv);
-  PlanParams p = {cu, seqlens, plan, B, T, Hq, Hkv, D, max_keys, window, sinks, chunk_ctas()};
+  PlanParams p = {cu, seqlens, slots, plan, B, T, Hq, Hkv, D, max_keys, window, sinks, chunk_ctas()};
   p.heads = Hkv * tiling.slices;
   p.tile_tokens = tiling.tile_tokens;
   p.item_tokens = tiling.item_tokens(D);

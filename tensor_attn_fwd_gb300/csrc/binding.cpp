@@ -745,9 +745,9 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, plan
+// cu_tokens, seqlens, tokens, Hq, Hkv, D, max_keys, window, sinks, plan, slots
 PyObject* chunk_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 10, [&] {
+  return call(n, 11, [&] {
     const Tensor& lens = tensor(a[1], "seqlens");
     check(lens, "seqlens", at::kInt, "int32", 1, lens.device());
     const at::Device device = lens.device();
@@ -760,6 +760,8 @@ PyObject* chunk_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int sinks = integer(a[8], "sinks", 0, kAll);
     Tensor plan;
     if (a[9] != Py_None) plan = int32(a[9], "plan", {-1}, device);
+    const bool has_slots = a[10] != Py_None;
+    const int* slots = has_slots ? ints(int32(a[10], "slots", {T}, device)) : nullptr;
     {
       const GpuPart gpu(device);
       long long need = 0;
@@ -767,8 +769,11 @@ PyObject* chunk_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (plan.defined() && plan.numel() < need)
         refuse("plan must have at least " + std::to_string(need) + " entries");
       if (!plan.defined()) plan = new_int32(need, device);
-      raise_if(attn_chunk_plan(ints(cu), ints(lens), ints(plan), B, T, Hq, Hkv, D, max_keys, window,
-                               sinks, current_stream(device)),
+      raise_if(has_slots ? attn_chunk_plan_slots(ints(cu), ints(lens), slots, ints(plan), B, T, Hq,
+                                                 Hkv, D, max_keys, window, sinks,
+                                                 current_stream(device))
+                         : attn_chunk_plan(ints(cu), ints(lens), ints(plan), B, T, Hq, Hkv, D,
+                                           max_keys, window, sinks, current_stream(device)),
                "attn_chunk_plan");
     }
     return pack_one(plan);

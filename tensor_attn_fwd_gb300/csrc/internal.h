@@ -302,8 +302,8 @@ struct ChunkLayout {
 inline long long chunk_workspace_floats(int ctas, int D) {
   return 2ll * ctas * chunk_part_rows(D) * (D + 1);
 }
-cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, int* plan, int B, int T, int Hq,
-                              int Hkv, int D, int max_keys, int window, int sinks,
+cudaError_t launch_chunk_plan(const int* cu, const int* seqlens, const int* slots, int* plan, int B,
+                              int T, int Hq, int Hkv, int D, int max_keys, int window, int sinks,
                               cudaStream_t stream, int* status);
 cudaError_t launch_attn_chunk(const void* q, const void* k_cache, const void* v_cache,
                               const int* plan, const PagedKV& paged, void* o, float* lse,

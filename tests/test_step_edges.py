@@ -1,12 +1,33 @@
 """A serving step at the edges of what the documentation allows: large tables that are copied
 beside the call's own work, rows that are refused, large scores, the bounds-checked build."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import tensor_attn_fwd_gb300 as attn
 
-from test_step import APPEND, INV, append_case, gpu, plain_append, same, status_ok
+from test_step import (A, APPEND, BF, INV, M2, M4, MIS, append_case, check, gpu, plain_append,
+                       pool, reference, same, status_ok)
+
+
+# ------------------------------------------------------------------ refusals (no GPU)
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, INV) for n in ("cu", "sl", "slots", "plan")],
+    *[({n: M2}, MIS) for n in ("cu", "sl", "slots")], (dict(plan=M4), MIS),
+    *[({n: 0}, INV) for n in ("B", "T", "Hq", "Hkv", "D", "mk", "window")], (dict(sinks=-1), INV),
+])
+def test_plan_with_slots_rejects(kw, code):
+    d = dict(cu=A, sl=A, slots=A, plan=A, B=2, T=8, Hq=4, Hkv=2, D=64, mk=128, window=9, sinks=0)
+    d.update(kw)
+    assert attn.load_library().attn_chunk_plan_slots(*d.values(), None) == code
+
+
+def test_plan_with_slots_refuses_cpu_tensors():
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        attn.attn_chunk_plan(i, i[:3], 4, 4, 2, 64, 128, slots=i)
 
 
 # ------------------------------------------------------------------ large tables
@@ -129,3 +150,112 @@ def test_append_of_rows_that_share_full_pages():
     assert (want[2] == lens + new).all()
     same(attn.attn_pages_append(*gpu(table, refs, lens, new), 73, 32), want)
     status_ok()
+
+
+# ------------------------------------------------------------------ steps with refused requests
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (100, 4)])
+def test_step_with_refused_requests(D, window, sinks):
+    """Requests without pages for their tokens, past their slots, finished, and with an empty
+    table: none of their tokens sees a key, nothing is reported for them, and the others
+    are as without them."""
+    Hq, Hkv, ps, M, T = 8, 2, 32, 24, 420
+    rng = np.random.default_rng(D)
+    ctxs, new = [500, 300, 740, 90, 400, 0, 8, 333], [1, 200, 40, 60, 1, 70, 33, 1]
+    lens = np.array(ctxs)
+    lens[3] = -5  # finished
+    pages = -(-np.maximum(lens, 0) // ps)
+    table, at = np.full((8, M), -1), 0
+    ids = rng.permutation(200)
+    for b in range(8):
+        table[b, :pages[b]] = ids[at:at + pages[b]]
+        at += pages[b]
+    refs = np.bincount(table[table >= 0], minlength=200)
+    refs[np.nonzero(refs == 0)[0][8:]] = 1  # eight free pages: a part of the rows' needs
+    kc, vc = (torch.randn(200, Hkv, ps, D, device="cuda").to(BF) for _ in range(2))
+    tab, ref_counts, ln, nw = gpu(table, refs, lens, new)
+    if window:  # pages that the window has passed are gone
+        tab, ref_counts = attn.attn_pages_free(tab, ref_counts, ln, ps, window, sinks)
+        ref_counts.copy_(torch.from_numpy(refs).cuda())
+    rope = attn.attn_rope_table(M * ps, D)
+    qkv = torch.randn(T, (Hq + 2 * Hkv) * D, device="cuda").to(BF)
+    tab, ref_counts, ln, cu, pos, slots, counts = attn.attn_pages_append(tab, ref_counts, ln, nw, T, ps)
+    assert attn.attn_debug_status() != attn.ATTN_OK  # no pages, or past its slots: either first
+    taken = (ln.cpu().numpy() > lens) & (lens >= 0)
+    assert taken.tolist() == [True, True, False, False, True, False, False, False]
+    plan = attn.attn_chunk_plan(cu, ln, T, Hq, Hkv, D, M * ps, window, sinks, slots=slots)
+    q = attn.attn_rope_append(qkv, rope, pos, slots, kc, vc, Hq)
+    o = torch.full((T, Hq, D), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((T, Hq), 7.0, device="cuda")
+    attn.attn_chunk_paged(q, kc, vc, tab, plan, o=o, lse=lse)
+    status_ok()
+    seen = tab.cpu().numpy().astype(np.int64)
+    seen[seen < 0] = 0  # (of keys that the window has passed)
+    ref = reference(q, [c if t else -n for c, t, n in zip(ctxs, taken, new)], new, seen, kc, vc,
+                    window or 1 << 30, sinks, 1 / math.sqrt(D))
+    check((o, lse), ref, sum(new))
+    first = np.cumsum([0] + new)
+    for b in range(8):
+        rows = slice(first[b], first[b + 1])
+        assert bool((ref[1][rows] == -math.inf).all()) == (not taken[b])
+    assert bool((o[sum(new):] == 7).all()) and bool((lse[sum(new):] == 7).all())
+    # Where all are taken the slots change nothing.
+    cu1, ln1 = gpu(np.array([0, 1, 201]), np.array([501, 500]))
+    with_slots = attn.attn_chunk_plan(cu1, ln1, 201, Hq, Hkv, D, M * ps, window, sinks,
+                                      slots=slots[:201])
+    without = attn.attn_chunk_plan(cu1, ln1, 201, Hq, Hkv, D, M * ps, window, sinks)
+    a, b = (attn.attn_chunk_paged(q[:201], kc, vc, tab[:2].contiguous(), p) for p in (with_slots, without))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    status_ok()
+    for bad in (slots[:-1], slots.long(), slots.cpu()):
+        with pytest.raises(ValueError):
+            attn.attn_chunk_plan(cu, ln, T, Hq, Hkv, D, M * ps, slots=bad)
+
+
+@pytest.mark.gpu
+def test_refused_requests_in_a_graph():
+    """A captured step: a request waits for pages, sees nothing meanwhile, and goes on when
+    another's are free."""
+    Hq, Hkv, D, ps, B, M, P, T = 4, 2, 64, 32, 2, 8, 7, 100
+    rope = attn.attn_rope_table(M * ps, D)
+    table, refs, lens, new = gpu(np.full((B, M), -1), np.zeros(P), np.zeros(B), np.zeros(B))
+    qkv = torch.randn(T, (Hq + 2 * Hkv) * D, device="cuda").to(BF)
+    kc, vc = (torch.zeros(P, Hkv, ps, D, dtype=BF, device="cuda") for _ in range(2))
+    o, lse = torch.zeros(T, Hq, D, dtype=BF, device="cuda"), torch.zeros(T, Hq, device="cuda")
+
+    def step():
+        _, _, _, cu, pos, slots, _ = attn.attn_pages_append(
+            table, refs, lens, new, T, ps, block_table_out=table, refs_out=refs, seqlens_out=lens)
+        plan = attn.attn_chunk_plan(cu, lens, T, Hq, Hkv, D, M * ps, slots=slots)
+        q = attn.attn_rope_append(qkv, rope, pos, slots, kc, vc, Hq)
+        attn.attn_chunk_paged(q, kc, vc, table, plan, o=o, lse=lse)
+        return q
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            q = step()
+    torch.cuda.synchronize()
+    length = [0, 0]
+    for news, takes in (([60, 40], [1, 1]), ([70, 30], [1, 0]), ([1, 30], [1, 0]), (None, None),
+                        ([0, 30], [0, 1])):
+        if news is None:  # the first request ends; its pages are free
+            lens[0] = -1000
+            attn.attn_pages_free(table, refs, lens, ps, 1 << 30, 0, block_table_out=table,
+                                 refs_out=refs)
+            length[0] = 0
+            continue
+        qkv.normal_()
+        new.copy_(gpu(np.array(news)))
+        g.replay()
+        torch.cuda.synchronize()
+        assert attn.attn_debug_status() == (
+            attn.ATTN_OK if all(t or not n for t, n in zip(takes, news)) else attn.ATTN_ERR_NO_PAGES)
+        ref = reference(q, [x if t else -n for x, t, n in zip(length, takes, news)], news,
+                        np.maximum(table.cpu().numpy(), 0).astype(np.int64), kc, vc, 1 << 30, 0, 0.125)
+        check((o, lse), ref, sum(news))
+        length = [x + n * t for x, t, n in zip(length, takes, news)]
+        assert lens.tolist()[1] == length[1]
