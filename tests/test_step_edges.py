@@ -8,8 +8,8 @@ import torch
 
 import tensor_attn_fwd_gb300 as attn
 
-from test_step import (A, APPEND, BF, INV, M2, M4, MIS, append_case, check, gpu, plain_append,
-                       pool, reference, same, status_ok)
+from test_step import (A, APPEND, BF, INV, M2, M4, MIS, append_case, check, dense, gpu, plain_append,
+                       pool, reference, run_chunk, same, status_ok)
 
 
 # ------------------------------------------------------------------ refusals (no GPU)
@@ -259,3 +259,47 @@ def test_refused_requests_in_a_graph():
         check((o, lse), ref, sum(news))
         length = [x + n * t for x, t, n in zip(length, takes, news)]
         assert lens.tolist()[1] == length[1]
+
+
+# ------------------------------------------------------------------ large scores
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(1 << 30, 0), (300, 5)])
+def test_chunk_large_scores_choose_one_key(D, window, sinks):
+    """Scores of thousands, whose maximum moves far from tile to tile: the result is the best
+    key's V where that key is clearly the best.
+
+    A score is a sum of D products in 32 bits, off by at most E = (D + 16) 2^-23 of the sum of
+    its terms' sizes, scale and LSE's roundings included; the LSE of a row moves by no
+    more than its scores.  Where the best score leads by 2 E + 25, the others' weights are e^-25
+    of the best's each, 6000 of them 1e-7 in all.  The best's own is rounded to bf16 once
+    (2^-8; its 32-bit value is what the sum holds), and so is the result."""
+    ctxs, news, Hkv, G = [600, 130, 5500, 0], [1, 70, 33, 9], 2, 4
+    table, lens, kc, vc = pool(ctxs, news, 32, Hkv, D)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q = torch.randn(sum(news), Hkv * G, D, generator=g, device="cuda").to(BF) * 30
+    kc *= 20
+    o, lse = run_chunk(q, news, lens, table, kc, vc, window, sinks, scale=1.0)
+    status_ok()
+    ref = reference(q, ctxs, news, table, kc, vc, window, sinks, 1.0)
+    t0 = clear = rows = 0
+    for b, (c, n) in enumerate(zip(ctxs, news)):
+        k, v = (x.double() for x in dense(table[b], kc, vc, c + n))
+        x = q[t0:t0 + n].double().view(n, Hkv, G, D)
+        p, j = torch.arange(c, c + n, device="cuda")[:, None], torch.arange(c + n, device="cuda")
+        seen = (j <= p) & ((j > p - window) | (j < sinks))
+        s = torch.einsum("nhgd,khd->nhgk", x, k).masked_fill(~seen[:, None, None], -math.inf)
+        terms = torch.einsum("nhgd,khd->nhgk", x.abs(), k.abs())
+        off = (D + 16) * 2.0 ** -23 * terms.masked_fill(~seen[:, None, None], 0).amax(-1)
+        assert bool(((lse[t0:t0 + n].double() - ref[1][t0:t0 + n]).abs()
+                     <= off.view(n, -1)).all())
+        top = s.topk(min(2, c + n), -1)
+        lead = top.values[..., 0] - (top.values[..., 1] if c + n > 1 else -math.inf)
+        best = top.indices[..., 0]  # [n, Hkv, G]
+        want = v[best, torch.arange(Hkv, device="cuda")[None, :, None]]
+        pick = lead > 2 * off + 25
+        err = (o[t0:t0 + n].double().view(n, Hkv, G, D) - want).abs() - 2.0 ** -6.99 * want.abs() - 1e-6
+        assert float(err[pick].max()) <= 0
+        assert bool(torch.isfinite(o[t0:t0 + n]).all())
+        clear, rows, t0 = clear + int(pick.sum()), rows + pick.numel(), t0 + n
+    assert clear >= 0.9 * rows
