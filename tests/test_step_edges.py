@@ -1,5 +1,6 @@
 """A serving step at the edges of what the documentation allows: large tables that are copied
 beside the call's own work, rows that are refused, large scores, the bounds-checked build."""
+import ctypes
 import math
 
 import numpy as np
@@ -7,6 +8,7 @@ import pytest
 import torch
 
 import tensor_attn_fwd_gb300 as attn
+from tensor_attn_fwd_gb300 import build as attn_build
 
 from test_step import (A, APPEND, BF, INV, M2, M4, MIS, append_case, check, dense, gpu, plain_append,
                        pool, reference, run_chunk, same, status_ok)
@@ -303,3 +305,52 @@ def test_chunk_large_scores_choose_one_key(D, window, sinks):
         assert bool(torch.isfinite(o[t0:t0 + n]).all())
         clear, rows, t0 = clear + int(pick.sum()), rows + pick.numel(), t0 + n
     assert clear >= 0.9 * rows
+
+
+# ------------------------------------------------------------------ the bounds-checked build
+@pytest.fixture(scope="module")
+def dbg():
+    lib = ctypes.CDLL(attn_build.build(debug=True))
+    i, p = ctypes.c_int, ctypes.c_void_p
+    lib.attn_chunk_plan_slots.argtypes = [p] * 4 + [i] * 8 + [p]
+    lib.attn_chunk_paged.argtypes = [p] * 8 + [i] * 8 + [ctypes.c_float, p]
+    lib.attn_debug_status.argtypes = [p]
+    return lib
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ctxs,news,G,window,sinks,offset", [
+    ([9000, 12, 900, 40], [60, 100, 1, 1], 3, 1 << 30, 0, 8),   # cut and whole items
+    ([5, 300, 0, 2000, 77], [300, 257, 1, 129, 0], 4, 200, 7, 0),
+    ([30, 0, 500], [1, 1, 1], 1, 1 << 30, 0, 0),
+    ([100, 900], [9, 140], 130, 1 << 30, 0, 8),                 # more heads than a tile's rows
+])
+def test_debug_build_chunk_matches_release(dbg, ctxs, news, G, D, window, sinks, offset):
+    """Every store of the attention of new tokens checked against its buffer: none outside, and
+    the release library's bits; rows behind the last request left as they were."""
+    Hkv, ps, spare = 2, 64, 3
+    table, lens, kc, vc = pool(ctxs, news, ps, Hkv, D)
+    T, Hq, B = sum(news) + spare, Hkv * G, len(news)
+    q = torch.randn(T, Hq, D, device="cuda").to(BF)
+    want = [torch.full(s, 7.0, dtype=t, device="cuda") for s, t in (((T, Hq, D), BF), ((T, Hq), torch.float32))]
+    run_chunk(q, news, lens, table, kc, vc, window, sinks, o=want[0], lse=want[1])
+    status_ok()
+    n, size = ctypes.c_longlong(), ctypes.c_longlong()
+    lib = attn.load_library()
+    assert lib.attn_chunk_plan_size(B, T, Hq, Hkv, D, ctypes.byref(n)) == 0
+    assert lib.attn_chunk_workspace(D, ctypes.byref(size)) == 0
+    plan = torch.empty(n.value, dtype=torch.int32, device="cuda")
+    ws = torch.empty(size.value, device="cuda")
+    cu, ln, tab, slots = gpu(np.concatenate([[0], np.cumsum(news)]), lens, table, np.zeros(T))
+    buf = torch.full((q.numel() + offset,), 7.0, dtype=BF, device="cuda")
+    o, lse = buf[offset:].view_as(q), torch.full((T, Hq), 7.0, device="cuda")
+    stream, M = torch.cuda.current_stream().cuda_stream, table.shape[1]
+    assert dbg.attn_chunk_plan_slots(cu.data_ptr(), ln.data_ptr(), slots.data_ptr(), plan.data_ptr(), B, T,
+                                     Hq, Hkv, D, M * ps, window, sinks, stream) == 0
+    assert dbg.attn_chunk_paged(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), tab.data_ptr(),
+                                plan.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), B, T, Hq,
+                                Hkv, kc.shape[0], ps, M, D, 1 / math.sqrt(D), stream) == 0
+    assert dbg.attn_debug_status(None) == attn.ATTN_OK
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert bool((o[T - spare:] == 7).all())
