@@ -709,10 +709,12 @@ ATTN_API int attn_chunk_plan_size(int B, int T, int Hq, int Hkv, int D, long lon
  * Attention of a step's new tokens over a paged cache, as its plan says.
  *   q [T,Hq,D] bf16 (attn_rope_append); k_cache, v_cache, block_table as
  *     attn_decode_splitkv_paged.  The new tokens' keys and values have to be in the cache.
- *   o [T,Hq,D] bf16 (rounded once from fp32), lse [T,Hq] fp32.  A token that sees no key (p <
- *     0: more new tokens than keys, or a finished row; or one not taken, by a plan of
- *     attn_chunk_plan_slots) gets O = 0 and LSE = -inf.  Tokens behind the last
- *     request's are left as they were.
+ *   o [T,Hq,D] bf16, lse [T,Hq] fp32.  As in the other attention calls the weights exp(S - max)
+ *     are rounded to bf16 for their product with V; sums, the LSE and the partial results of
+ *     requests that are cut are fp32, and o is rounded once more at the end.
+ *     A token that sees no key gets O = 0 and LSE = -inf: p < 0 (more new tokens than keys, or
+ *     a finished row), or one not taken, by a plan of attn_chunk_plan_slots.  Tokens behind
+ *     the last request's are left as they were.
  *   workspace: attn_chunk_workspace floats, caller-owned, contents undefined
  *   Table entries of pages that hold no seen key are not read and may be anything.  Keys
  *     that no token sees may hold anything; K and V have to be finite at keys that some

@@ -54,7 +54,10 @@ constexpr int kMaxKeys = 1 << 30;  // of a request
 // Costs of an item in the line: per K/V tile with one query tile and with two, and around its
 // tiles (its start and its epilogue).  Alike for one tile and two: 64 requests with 8 prompts
 // among them 447 us instead of 347; 1 around them: 64 single tokens of up to 16384 keys, D 64,
-// 187 instead of 177.
+// 187 instead of 177.  (Measured with one cache for all requests, so that K and V come from L2,
+// us for a tile and around an item: two query tiles 1.43 and 3.7 at D = 128, 1.25 and 2.6 at 64;
+// one 0.81 and 3.0, 0.68 and 2.7; at D = 256, one tile by 64 keys, 0.91 and 3.0, which is near
+// enough to the others' ratios to share the constants.)
 constexpr int kCostOne = 2, kCostTwo = 3, kOverhead = 5;
 // An item is cut no closer than this to its ends (in tiles), since a cut costs partial results:
 // 100 tokens of 1000 19.0 us, with 4 22.6; one of 300 8.0, with 1 10.3.
@@ -1030,7 +1033,10 @@ __device__ void softmax_role(const ChunkParams& p, const Work& work, Bars* bars,
           tmem_st32(tAll + c, orow);
         }
       }
-      // p = 2^(s * scale * log2 e - m), two columns per paired FMA/ADD.
+      // p = 2^(s * scale * log2 e - m), two columns per paired FMA/ADD.  P is rounded to bf16, the
+      // type that its product with a bf16 V takes (twice the time in tf32, and twice the room in
+      // tensor memory); its sum is of the values in 32 bits.  That makes the error of O 2.0e-3 to
+      // 2.3e-3 (2-norm, relative) where one rounding of O alone has 1.6e-3.
       const float base = (m == -INFINITY) ? 0.f : m;
       const uint64_t sc2 = f2_pack(sl2, sl2);
       const uint64_t nb2 = f2_pack(-base, -base);

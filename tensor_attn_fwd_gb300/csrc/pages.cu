@@ -665,10 +665,11 @@ struct CompactOp {
 // Token sums are clamped to T + 1 (a sum that saturates stays associative).
 //
 // Latency, again: each phase is a few dependent trips to L2.  1024 rows of 1024 slots, 560,000
-// pages and 9192 tokens take 15.0 us, with the workers alone 22.6.  Where all fits one CTA's shared
-// memory (run_small), there are no phases: 8 rows 3.7 us instead of 10.2, 64 rows of 128 slots
-// with 2048 tokens 8.1 instead of 12.0.  But its tokens take turns, and a row's slots one thread:
-// 15360 tokens took 19.2 us instead of 12.7, one row of 500 new slots 30.4 instead of 19.1.
+// pages and 9152 tokens take 16.0 us; with lengths updated in place, where the workers copy
+// the table themselves before they begin, 21.5.  Where all fits one CTA's shared
+// memory (run_small), there are no phases: 8 rows 3.5 us instead of 10.2, 64 rows of 128 slots
+// with 2048 tokens 7.9 instead of 12.0.  But its tokens take turns, and a row's slots one thread:
+// 15360 tokens took 19.2 us instead of 12.7, one row of 500 new slots 30.4 instead of 19.6.
 struct AppendOp {
   const int *table, *refs, *seqlens, *new_lens;
   int *table_out, *refs_out, *seqlens_out, *cu, *positions, *slots, *counts;
